@@ -13,7 +13,13 @@ Entry points (same names as the C ABI, without the ``fa_`` prefix):
   decode_splitkv_gqa  the same with grouped key/value heads (query heads of a group packed)
   decode_splitkv_fused  the same with the combine done by each row's last split (one launch)
   merge_states     log-sum-exp combine of partial states
-  decode_default_splits, decode_gqa_default_splits, decode_workspace_size, get_device_error,
+  qk_norm_rope     query/key norm, position rotation and head-major layout of a layer's projections
+  qk_norm_rope_bwd     its gradient
+  qk_norm_rope_append  the same for new tokens, keys and values written into a cache
+  decode_tree      decode for a tree of drafted tokens over a cache
+  cache_compact    the accepted path of a tree moved up behind the cached tokens
+  decode_default_splits, decode_gqa_default_splits, decode_workspace_size,
+  decode_tree_workspace_size, qk_norm_rope_bwd_workspace_size, get_device_error,
   set_wait_timeout_ns, status_string
 """
 from __future__ import annotations
@@ -77,6 +83,21 @@ def _load():
     lib.fa_decode_splitkv_gqa.restype = i
     lib.fa_merge_states.argtypes = [vp, vp, i, i, i, vp, vp, i, vp]
     lib.fa_merge_states.restype = i
+    ll = ctypes.c_longlong
+    lib.fa_qk_norm_rope.argtypes = [vp] * 11 + [ll] * 3 + [i] * 9 + [f, i, vp]
+    lib.fa_qk_norm_rope.restype = i
+    lib.fa_qk_norm_rope_bwd_workspace_size.argtypes = [i]
+    lib.fa_qk_norm_rope_bwd_workspace_size.restype = sz
+    lib.fa_qk_norm_rope_bwd.argtypes = [vp] * 16 + [sz] + [ll] * 5 + [i] * 9 + [f, i, i, i, vp]
+    lib.fa_qk_norm_rope_bwd.restype = i
+    lib.fa_qk_norm_rope_append.argtypes = [vp] * 13 + [ll] * 3 + [i] * 9 + [f, i, vp]
+    lib.fa_qk_norm_rope_append.restype = i
+    lib.fa_decode_tree_workspace_size.argtypes = [i] * 5
+    lib.fa_decode_tree_workspace_size.restype = sz
+    lib.fa_decode_tree.argtypes = [vp] * 9 + [sz] + [i] * 7 + [f, i, vp]
+    lib.fa_decode_tree.restype = i
+    lib.fa_cache_compact.argtypes = [vp] * 6 + [i] * 7 + [vp]
+    lib.fa_cache_compact.restype = i
     lib.fa_get_device_error.argtypes = [vp]
     lib.fa_get_device_error.restype = i
     lib.fa_set_wait_timeout_ns.argtypes = [ull]
@@ -446,6 +467,266 @@ def merge_states(o_parts, lse_parts, out_dtype=torch.float32, out=None, lse=None
                                  _odt(out.dtype), _stream(dev))
     _check(st, "fa_merge_states")
     return out, lse
+
+
+def _token_stride(t, name, device=None, dtype=torch.bfloat16):
+    """Checks a projection [B, N, heads, d] whose tokens are evenly spaced; returns (device index, stride)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    di = t.get_device()
+    if di < 0:
+        raise ValueError(f"{name} must be on a CUDA device")
+    if device is not None and di != device:
+        raise ValueError(f"{name} is on cuda:{di}, expected cuda:{device}")
+    if t.dim() != 4:
+        raise ValueError(f"{name} must be [B, N, heads, head_dim]")
+    B, N, H, d = t.shape
+    sb, sn, sh, sd = t.stride()
+    tok = sn if N > 1 else sb if B > 1 else H * d
+    if (d > 1 and sd != 1) or (H > 1 and sh != d) or (B > 1 and sb != N * tok):
+        raise ValueError(f"{name} must have its heads contiguous and its tokens evenly spaced")
+    return di, tok
+
+
+def _rope_args(q, k, q_weight, k_weight, cos, sin):
+    """The checks that the norm's forms share; returns (device index, token strides, sizes, weight dtype)."""
+    di, qs = _token_stride(q, "q")
+    _, ks = _token_stride(k, "k", di)
+    B, N, Hq, d = q.shape
+    Hkv = k.shape[2]
+    if tuple(k.shape) != (B, N, Hkv, d):
+        raise ValueError("shape mismatch between q and k")
+    wt = q_weight.dtype if isinstance(q_weight, torch.Tensor) else None
+    _need(q_weight, "q_weight", wt, di)
+    _need(k_weight, "k_weight", wt, di)
+    if wt != torch.bfloat16 and wt != torch.float32:
+        raise ValueError("weights must be bfloat16 or float32")
+    _need(cos, "cos", torch.float32, di)
+    _need(sin, "sin", torch.float32, di)
+    if tuple(q_weight.shape) != (d,) or tuple(k_weight.shape) != (d,):
+        raise ValueError("weights must be [head_dim]")
+    if cos.dim() != 2 or cos.shape != sin.shape:
+        raise ValueError("cos and sin must be [max_pos, rot / 2]")
+    return di, qs, ks, B, N, Hq, Hkv, d, 2 * cos.shape[1], cos.shape[0], _odt(wt)
+
+
+def _need_shape(t, name, dtype, di, shape):
+    _need(t, name, dtype, di)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
+
+
+def qk_norm_rope(q, k, v, q_weight, k_weight, cos, sin, positions=None, eps=1e-6, interleaved=False, expand=False,
+                 q_out=None, k_out=None, v_out=None):
+    """Operands of ``fwd`` from a layer's projections: each query and key head normed (root mean square,
+    weights [d] bf16 or fp32), rotated by its token's angles and laid out head-major; values copied.
+
+    q [B,N,Hq,d], k and v [B,N,Hkv,d] bf16 with evenly spaced tokens (slices of one projection will do;
+    v may be None); cos, sin fp32 [max_pos, rot/2]; positions int32 [B,N] (None: 0 .. N-1).  Pairs are
+    (i, i + rot/2), or (2i, 2i+1) with ``interleaved``.  With ``expand`` key/value heads are repeated for
+    their query heads.  Returns (q [B,Hq,N,d], k, v [B,Hkv or Hq,N,d] or None), bf16.
+    """
+    lib = _load()
+    di, qs, ks, B, N, Hq, Hkv, d, rot, max_pos, wdt = _rope_args(q, k, q_weight, k_weight, cos, sin)
+    vs = 0
+    if v is not None:
+        _, vs = _token_stride(v, "v", di)
+        if tuple(v.shape) != (B, N, Hkv, d):
+            raise ValueError("shape mismatch between k and v")
+    elif v_out is not None:
+        raise ValueError("v_out without v")
+    if positions is not None:
+        _need_shape(positions, "positions", torch.int32, di, (B, N))
+    Ho = Hq if expand else Hkv
+    if q_out is None:
+        q_out = torch.empty((B, Hq, N, d), dtype=torch.bfloat16, device=q.device)
+    if k_out is None:
+        k_out = torch.empty((B, Ho, N, d), dtype=torch.bfloat16, device=q.device)
+    if v is not None and v_out is None:
+        v_out = torch.empty((B, Ho, N, d), dtype=torch.bfloat16, device=q.device)
+    _need_shape(q_out, "q_out", torch.bfloat16, di, (B, Hq, N, d))
+    _need_shape(k_out, "k_out", torch.bfloat16, di, (B, Ho, N, d))
+    if v is not None:
+        _need_shape(v_out, "v_out", torch.bfloat16, di, (B, Ho, N, d))
+    with _on_device(di):
+        st = lib.fa_qk_norm_rope(_ptr(q), _ptr(k), _ptr(v), _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin),
+                                 _ptr(positions), _ptr(q_out), _ptr(k_out), _ptr(v_out), qs, ks, vs, B, N, Hq, Hkv, d,
+                                 rot, max_pos, int(bool(interleaved)), int(bool(expand)), float(eps), wdt, _stream(di))
+    _check(st, "fa_qk_norm_rope")
+    return q_out, k_out, v_out
+
+
+def qk_norm_rope_bwd_workspace_size(d):
+    return int(_load().fa_qk_norm_rope_bwd_workspace_size(d))
+
+
+def qk_norm_rope_bwd(dq, dk, dv, q, k, q_weight, k_weight, cos, sin, positions=None, eps=1e-6, interleaved=False,
+                     expand=False, out_dtype=torch.bfloat16, grads=None, workspace=None):
+    """Gradient of ``qk_norm_rope`` for the gradients (dq, dk, dv) of its outputs (bf16 or fp32, as ``bwd``
+    returns them; dv may be None) and the forward's other arguments.
+
+    ``grads`` is an optional (grad_q, grad_k, grad_v) triple of ``out_dtype`` [B,N,heads,d] tensors with
+    evenly spaced tokens to write into (slices of one buffer will do).  Returns (grad_q, grad_k, grad_v
+    or None, grad_q_weight fp32 [d], grad_k_weight fp32 [d]); the same from run to run.
+    """
+    lib = _load()
+    di, qs, ks, B, N, Hq, Hkv, d, rot, max_pos, wdt = _rope_args(q, k, q_weight, k_weight, cos, sin)
+    if positions is not None:
+        _need_shape(positions, "positions", torch.int32, di, (B, N))
+    Ho = Hq if expand else Hkv
+    gt = dq.dtype if isinstance(dq, torch.Tensor) else None
+    _need_shape(dq, "dq", gt, di, (B, Hq, N, d))
+    _need_shape(dk, "dk", gt, di, (B, Ho, N, d))
+    if dv is not None:
+        _need_shape(dv, "dv", gt, di, (B, Ho, N, d))
+    gdt, odt = _odt(gt), _odt(out_dtype)
+    if grads is None:
+        grads = (torch.empty((B, N, Hq, d), dtype=out_dtype, device=q.device),
+                 torch.empty((B, N, Hkv, d), dtype=out_dtype, device=q.device),
+                 torch.empty((B, N, Hkv, d), dtype=out_dtype, device=q.device) if dv is not None else None)
+    gq, gk, gv = grads
+    _, gqs = _token_stride(gq, "grad_q", di, out_dtype)
+    _, gks = _token_stride(gk, "grad_k", di, out_dtype)
+    gvs = 0
+    if (gv is None) != (dv is None):
+        raise ValueError("grad_v goes with dv")
+    if gv is not None:
+        _, gvs = _token_stride(gv, "grad_v", di, out_dtype)
+    if (tuple(gq.shape) != (B, N, Hq, d) or tuple(gk.shape) != (B, N, Hkv, d)
+            or (gv is not None and tuple(gv.shape) != (B, N, Hkv, d))):
+        raise ValueError("gradient buffers have the wrong shape")
+    gwq = torch.empty((d,), dtype=torch.float32, device=q.device)
+    gwk = torch.empty((d,), dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = torch.empty(qk_norm_rope_bwd_workspace_size(d), dtype=torch.uint8, device=q.device)
+    _need(workspace, "workspace", torch.uint8, di)
+    with _on_device(di):
+        st = lib.fa_qk_norm_rope_bwd(_ptr(dq), _ptr(dk), _ptr(dv), _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight),
+                                     _ptr(cos), _ptr(sin), _ptr(positions), _ptr(gq), _ptr(gk), _ptr(gv), _ptr(gwq),
+                                     _ptr(gwk), _ptr(workspace), workspace.numel(), qs, ks, gqs, gks, gvs, B, N, Hq, Hkv,
+                                     d, rot, max_pos, int(bool(interleaved)), int(bool(expand)), float(eps), wdt, gdt, odt,
+                                     _stream(di))
+    _check(st, "fa_qk_norm_rope_bwd")
+    return gq, gk, gv, gwq, gwk
+
+
+def _tree_args(di, B, T, parents, n_nodes):
+    if parents is not None:
+        _need_shape(parents, "parents", torch.int32, di, (B, T))
+    if n_nodes is not None:
+        _need_shape(n_nodes, "n_nodes", torch.int32, di, (B,))
+
+
+def qk_norm_rope_append(q, k, v, q_weight, k_weight, cos, sin, k_cache, v_cache, seqlens, parents=None, n_nodes=None,
+                        eps=1e-6, interleaved=False, q_out=None):
+    """``qk_norm_rope`` for up to T = 128 new tokens of each sequence, keys and values written into the caches.
+
+    q [B,T,Hq,d], k and v [B,T,Hkv,d] bf16 with evenly spaced tokens; caches [B,Hkv,Nk_max,d] bf16; seqlens
+    int32 [B] the cached tokens.  The new tokens form a tree: parents int32 [B,T], an earlier node or -1 for
+    the last cached token (None: each token follows the one before it); n_nodes int32 [B] how many of the T
+    there are (None: all).  Token t goes to cache row seqlens + t, at position seqlens + the number of its
+    ancestors.  ``seqlens`` stays as it is.  Returns q [B,Hq,T,d] bf16 (0 for tokens that are not there).
+    """
+    lib = _load()
+    di, qs, ks, B, T, Hq, Hkv, d, rot, max_pos, wdt = _rope_args(q, k, q_weight, k_weight, cos, sin)
+    _, vs = _token_stride(v, "v", di)
+    if tuple(v.shape) != (B, T, Hkv, d):
+        raise ValueError("shape mismatch between k and v")
+    _need(k_cache, "k_cache", torch.bfloat16, di)
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [B, Hkv, Nk_max, head_dim]")
+    Nk_max = k_cache.shape[2]
+    _need_shape(k_cache, "k_cache", torch.bfloat16, di, (B, Hkv, Nk_max, d))
+    _need_shape(v_cache, "v_cache", torch.bfloat16, di, (B, Hkv, Nk_max, d))
+    _need_shape(seqlens, "seqlens", torch.int32, di, (B,))
+    _tree_args(di, B, T, parents, n_nodes)
+    if q_out is None:
+        q_out = torch.empty((B, Hq, T, d), dtype=torch.bfloat16, device=q.device)
+    _need_shape(q_out, "q_out", torch.bfloat16, di, (B, Hq, T, d))
+    with _on_device(di):
+        st = lib.fa_qk_norm_rope_append(_ptr(q), _ptr(k), _ptr(v), _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin),
+                                        _ptr(seqlens), _ptr(parents), _ptr(n_nodes), _ptr(q_out), _ptr(k_cache),
+                                        _ptr(v_cache), qs, ks, vs, B, T, Hq, Hkv, Nk_max, d, rot, max_pos,
+                                        int(bool(interleaved)), float(eps), wdt, _stream(di))
+    _check(st, "fa_qk_norm_rope_append")
+    return q_out
+
+
+def decode_tree_workspace_size(Hq, Hkv, T, d, num_sms):
+    return int(_load().fa_decode_tree_workspace_size(Hq, Hkv, T, d, num_sms))
+
+
+def decode_tree(q, k_cache, v_cache, seqlens, parents=None, n_nodes=None, scale=None, out_dtype=torch.bfloat16, out=None,
+                lse=None, workspace=None, return_lse=True):
+    """Decode attention for a tree of up to T = 128 drafted tokens of each sequence, whose keys and values are in
+    cache rows seqlens .. seqlens + n_nodes - 1: each sees the cached tokens, itself and its ancestors.
+
+    q [B,Hq,T,d] bf16, caches [B,Hkv,Nk_max,d] bf16 with Hkv dividing Hq, seqlens int32 [B] (without the tree),
+    parents and n_nodes as for ``qk_norm_rope_append``.  ``workspace`` is a uint8 CUDA tensor of at least
+    ``decode_tree_workspace_size`` bytes (allocated here when omitted).  Returns (O [B,Hq,T,d], LSE fp32
+    [B,Hq,T] or None); O = 0 and LSE = -inf for tokens that are not there.
+    """
+    lib = _load()
+    di = _need(q, "q", torch.bfloat16)
+    _need(k_cache, "k_cache", torch.bfloat16, di)
+    if q.dim() != 4 or k_cache.dim() != 4:
+        raise ValueError("q and the caches must be [B, heads, rows, head_dim]")
+    B, Hq, T, d = q.shape
+    Hkv, Nk_max = k_cache.shape[1], k_cache.shape[2]
+    if tuple(k_cache.shape) != (B, Hkv, Nk_max, d):
+        raise ValueError("shape mismatch between q and k_cache")
+    _need_shape(v_cache, "v_cache", torch.bfloat16, di, (B, Hkv, Nk_max, d))
+    _need_shape(seqlens, "seqlens", torch.int32, di, (B,))
+    _tree_args(di, B, T, parents, n_nodes)
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    if workspace is None:
+        workspace = torch.empty(max(decode_tree_workspace_size(Hq, Hkv, T, d, num_sms(q.device)), 256), dtype=torch.uint8,
+                                device=q.device)
+    _need(workspace, "workspace", torch.uint8, di)
+    if out is None:
+        out = torch.empty((B, Hq, T, d), dtype=out_dtype, device=q.device)
+    _need_shape(out, "out", out.dtype, di, (B, Hq, T, d))
+    if lse is None and return_lse:
+        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device)
+    if lse is not None:
+        _need_shape(lse, "lse", torch.float32, di, (B, Hq, T))
+    with _on_device(di):
+        st = lib.fa_decode_tree(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(seqlens), _ptr(parents), _ptr(n_nodes),
+                                _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), B, Hq, Hkv, T, Nk_max, d, d,
+                                scale, _odt(out.dtype), _stream(di))
+    _check(st, "fa_decode_tree")
+    return out, lse
+
+
+def cache_compact(k_cache, v_cache, seqlens, accepted, n_accepted, seqlens_out=None):
+    """Moves cache rows seqlens + accepted[b, i] to seqlens + i for i < n_accepted[b], in place, for every head
+    (rows are read before any is written: any order will do).
+
+    caches [B,Hkv,Nk_max,d] or [L,B,Hkv,Nk_max,d] bf16, seqlens and n_accepted int32 [B], accepted int32 [B,T]
+    with T <= 128.  Returns seqlens + n_accepted, in ``seqlens_out`` (which must not overlap seqlens).
+    """
+    lib = _load()
+    di = _need(k_cache, "k_cache", torch.bfloat16)
+    if k_cache.dim() not in (4, 5):
+        raise ValueError("caches must be [B, Hkv, Nk_max, head_dim], with or without layers before")
+    _need_shape(v_cache, "v_cache", torch.bfloat16, di, tuple(k_cache.shape))
+    B, Hkv, Nk_max, d = k_cache.shape[-4:]
+    L = k_cache.shape[0] if k_cache.dim() == 5 else 1
+    _need(accepted, "accepted", torch.int32, di)
+    if accepted.dim() != 2 or accepted.shape[0] != B:
+        raise ValueError("accepted must be [B, T]")
+    _need_shape(seqlens, "seqlens", torch.int32, di, (B,))
+    _need_shape(n_accepted, "n_accepted", torch.int32, di, (B,))
+    if seqlens_out is None:
+        seqlens_out = torch.empty((B,), dtype=torch.int32, device=k_cache.device)
+    _need_shape(seqlens_out, "seqlens_out", torch.int32, di, (B,))
+    with _on_device(di):
+        st = lib.fa_cache_compact(_ptr(k_cache), _ptr(v_cache), _ptr(seqlens), _ptr(accepted), _ptr(n_accepted),
+                                  _ptr(seqlens_out), L, B, Hkv, Nk_max, d, d, accepted.shape[1], _stream(di))
+    _check(st, "fa_cache_compact")
+    return seqlens_out
 
 
 def get_device_error(device=None):

@@ -254,6 +254,13 @@ size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 }  // namespace
 
+namespace fa {
+cudaError_t device_status_word(int** out) { return status_word(out); }
+cudaError_t device_sm_count(int* out) { return sm_count(out); }
+unsigned long long wait_limit_ns() { return g_wait_ns.load(); }
+bool bf16_tile_map(CUtensorMap* m, const void* ptr, int BH, int rows, int d) { return make_map(m, ptr, BH, rows, d); }
+}  // namespace fa
+
 extern "C" {
 
 const char* fa_status_string(fa_status s)

@@ -168,6 +168,91 @@ struct MergeParams {
 
 cudaError_t launch_merge(const MergeParams& p, fa_dtype o_dtype, cudaStream_t st);
 
+// Tree decode (fa_tree_kernel.cuh).  A group is a (sequence, key/value head) with its
+// rows = (Hq / Hkv) * T query rows, row = head within the group * T + node; a unit is a block of
+// part_rows of them.
+struct TreeParams {
+    CUtensorMap tm_q;    // bf16 [B*Hkv][rows][d], box {min(d,64), 128, 1}
+    CUtensorMap tm_k;    // bf16 [B*Hkv][Nk_max][d]
+    CUtensorMap tm_v;    // bf16 [B*Hkv][Nk_max][d]
+    const int* seqlens;  // int32 [B]: cached tokens, without the tree
+    const int* parents;  // int32 [B][T] or nullptr (a chain)
+    const int* n_nodes;  // int32 [B] or nullptr (T everywhere)
+    void* o;             // [B*Hkv][rows][d]
+    float* lse;          // [B*Hkv][rows] or nullptr
+    float* o_part;       // fp32 [2 * num_ctas][part_rows][d]
+    float* lse_part;     // fp32 [2 * num_ctas][part_rows]
+    int* status;
+    int B, Hkv, rows, T, Nk_max;
+    int part_rows;       // min(rows, 128), or 256 for more than 128 rows (PAIR form)
+    int n_qp;            // units per group: ceil(rows / part_rows)
+    int num_ctas;        // one per SM
+    float scale_log2;
+    fa_dtype o_dtype;
+    unsigned long long wait_limit_ns;
+};
+
+cudaError_t launch_tree_32(const TreeParams& p, cudaStream_t st);
+cudaError_t launch_tree_64(const TreeParams& p, cudaStream_t st);
+cudaError_t launch_tree_128(const TreeParams& p, cudaStream_t st);
+
+// Query/key norm with rotation (fa_qk_rope.cu).  A row is one head of one token, d elements.
+struct RopeParams {
+    const void *q, *k, *v;                       // bf16 [B*N tokens][heads][d]; v may be nullptr
+    long long q_stride, k_stride, v_stride;      // elements between tokens
+    const void *wq, *wk;                         // [d], bf16 or fp32
+    const float *cos_t, *sin_t;                  // fp32 [max_pos][rot / 2]
+    const int* positions;                        // int32 [B*N] or nullptr (token index in its sequence)
+    void *q_out, *k_out, *v_out;                 // bf16 [B][heads][N][d], or the caches [B][Hkv][Nk_max][d]
+    const int *seqlens, *parents, *n_nodes;      // append: as TreeParams
+    int* status;
+    int B, N, Hq, Hkv, rot, max_pos, Nk_max;
+    int copies;                                  // times each key/value head is written (Hq / Hkv expanded, else 1)
+    float eps;
+    fa_dtype w_dtype;
+};
+
+struct RopeBwdParams {
+    const void *dq, *dk, *dv;                    // [B][heads][N][d] of g_dtype; dv may be nullptr
+    const void *q, *k;                           // as RopeParams
+    long long q_stride, k_stride;
+    const void *wq, *wk;
+    const float *cos_t, *sin_t;
+    const int* positions;
+    void *gq, *gk, *gv;                          // [B*N][heads][d] of out_dtype
+    long long gq_stride, gk_stride, gv_stride;
+    float *gwq, *gwk;                            // fp32 [d]
+    float* part;                                 // fp32 [CTAs][2][d]
+    int* status;
+    int B, N, Hq, Hkv, rot, max_pos, copies;
+    float eps;
+    fa_dtype w_dtype, g_dtype, out_dtype;
+};
+
+// CTAs of the backward kernel, and so partial rows of the weights' gradients, at most.
+constexpr int kRopeBwdCtas = 1024;
+
+cudaError_t launch_qk_rope(const RopeParams& p, int d, bool interleaved, bool append, int sms, cudaStream_t st);
+cudaError_t launch_qk_rope_bwd(const RopeBwdParams& p, int d, bool interleaved, int sms, cudaStream_t st);
+
+// Cache compaction (fa_cache.cu).
+struct CompactParams {
+    void *k, *v;                                 // bf16 [L][B][Hkv][Nk_max][d]
+    const int *seqlens, *accepted, *n_accepted;  // int32 [B], [B][T], [B]
+    int* seqlens_out;                            // int32 [B] or nullptr
+    int* status;
+    int L, B, Hkv, Nk_max, d, T;
+};
+
+cudaError_t launch_cache_compact(const CompactParams& p, cudaStream_t st);
+
+// Host helpers of the C ABI files (fa_api.cu).
+cudaError_t device_status_word(int** out);  // the current device's status word
+cudaError_t device_sm_count(int* out);
+unsigned long long wait_limit_ns();
+// Tensor map of a bf16 tensor [BH][rows][d] with 128-row boxes, from the thread's cache when possible.
+bool bf16_tile_map(CUtensorMap* m, const void* ptr, int BH, int rows, int d);
+
 // Status word helpers (device side records the first failure only).
 enum : int { kStatusOk = 0 };
 

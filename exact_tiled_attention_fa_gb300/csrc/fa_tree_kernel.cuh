@@ -1,0 +1,935 @@
+// fa_tree_kernel.cuh -- decode attention for a tree of drafted tokens over a cache, for sm_103a.
+//
+// Mathematics.  Sequence b has p cached tokens (cache rows 0 .. p - 1) and n <= T drafted tokens
+// whose keys and values were written to cache rows p .. p + n - 1.  parents[t] < t is the node that
+// node t continues (-1: the last cached token).  With A(t) the set of t and its ancestors, query
+// row (h, t) attends to
+//   { rows j < p }  and  { rows p + a, a in A(t) },
+// O = softmax(scale q K^T) V over those rows.  The Hq / Hkv query heads of a key/value head and
+// their T nodes are the rows of one group ("flash_lab.py -- FlashAttention, flash-decoding and
+// megakernel in numpy", section 4 `split_kv_decode`: a group's query heads are packed as the rows
+// of q), the walk over 128-key tiles keeps the running max and sum of section 1 `softmax_online`,
+// and key ranges are joined by section 4's log-sum-exp combine.
+//
+// Work division.  A unit is a group's block of up to 128 query rows (256 in PAIR form); it has
+// ceil((p + n) / 128) key tiles.  The tiles of all units, in order, are cut into as many equal
+// shares as there are CTAs (one per SM), from lengths that only the device knows: each CTA scans
+// the lengths once.  A share crosses unit borders, and the rings of K and V tiles run on across
+// them, so a CTA pays its start-up once, however short the caches are.  A unit that lies in one
+// CTA's share is finished there; the parts of the others go to at most two slots per CTA (the
+// share's first and last unit) and fa_tree_merge_kernel joins them.  The slots are thus bounded by
+// the number of CTAs, not by the number of units.
+//
+// Roles of a CTA (12 warps):
+//   warps 0-3 / 4-7  softmax warpgroups 0 / 1: thread t owns row t of a 128-row tile (TMEM lane t).
+//   warp 8           TMA producer: query tiles, K and V tiles into rings of their own.
+//   warps 9, 10      tcgen05 issuers of warpgroup 0 / 1: S = Q K^T, O += P V (P from tensor memory).
+// ALT form (groups of at most 128 rows): both warpgroups hold the same 128 query rows and take the
+// key tiles in turn (tile k of the CTA's share goes to warpgroup k mod 2), each with its own running
+// max, sum and O accumulator, so one warpgroup's exponentials run under the other's products
+// although there is a single query tile.  At the end of a unit the two exchange max and sum through
+// shared memory and each reads half of the columns of both accumulators out of tensor memory (warps
+// w and w + 4 reach the same lanes).
+// PAIR form (more than 128 rows): warpgroup i takes query rows 128 i .. 128 i + 127 of the unit and
+// both walk every key tile, so that K and V are read once for 256 rows.
+//
+// Masks.  Only the tiles that hold drafted rows are masked, by four 32-bit words per query row (its
+// ancestors), shifted to the tile; hidden scores become -inf by selection, so a non-finite key
+// never reaches a row that does not see it.  V rows past the tree are zeroed in shared memory (0
+// times NaN would be NaN).
+//
+// Tensor memory, P's aliasing of S at d = 128, the bounded waits and the drain after a failure are
+// those of fa_fwd_kernel.cuh.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cstdint>
+
+#include "fa_internal.h"
+#include "fa_kernel_common.cuh"
+#include "ptx.cuh"
+
+namespace fa {
+
+constexpr int kTrThreads = 384;  // 12 warps = 3 warpgroups
+constexpr int kTrWarpProducer = 8;
+constexpr int kTrWarpMma = 9;  // and 10
+// Registers after the split of fa_fwd_kernel.cuh's kernels without a correction warpgroup:
+// 256 * softmax + 128 * control = 64512 = 384 * 168, checked by the launcher.
+template <int D>
+constexpr int kTrSoftmaxRegs = D == 128 ? 224 : 216;
+template <int D>
+constexpr int kTrControlRegs = D == 128 ? 56 : 72;
+
+enum : int {
+    kTbQFull = 0,     // + query buffer
+    kTbQEmpty = 2,    // + query buffer: both issuers are done with it
+    kTbSFull = 4,     // + warpgroup
+    kTbSFree = 6,     // + warpgroup: S_i has been read out of TMEM
+    kTbPFull = 8,     // + warpgroup
+    kTbPVDone = 10,   // + warpgroup
+    kTbOReady = 12,   // + warpgroup: the last product of a unit has completed
+    kTbOFree = 14,    // + warpgroup: O_i has been read out of TMEM
+    kTbMLFull = 16,   // ALT: both warpgroups' max and sum are in shared memory
+    kTbDrain = 17,    // + warpgroup
+    kTbKFull = 20,    // + K stage (up to 4)
+    kTbKEmpty = 24,
+    kTbVFull = 28,    // + V stage (up to 4)
+    kTbVEmpty = 32,
+    kTbCount = 36
+};
+
+template <int D>
+struct TrCfg {
+    static_assert(D == 32 || D == 64 || D == 128, "head size");
+    static constexpr int kCB = D < 64 ? D : 64;
+    static constexpr int kNumCB = D / kCB;
+    static constexpr int kRowBytes = kCB * 2;
+    static constexpr uint32_t kLayout = kRowBytes == 128 ? kSwizzle128B : kSwizzle64B;
+    static constexpr int kAtomBytes = 8 * kRowBytes;
+    static constexpr int kBlkBytes = kBlockM * kRowBytes;
+    static constexpr int kTileBytes = kNumCB * kBlkBytes;  // 128 x D bf16
+    // Stages of each ring.  Even, so that in ALT form a stage always serves the same warpgroup: a
+    // stage's previous tile was then consumed by the very thread that waits for its next one,
+    // which the phase parity of the wait relies on.
+    static constexpr int kStages = D == 128 ? 2 : 4;
+    static_assert(kStages % 2 == 0 && kStages <= 4, "ring stages");
+    static constexpr int kOffQ = 0;  // two query tiles: two units' (ALT) or a unit's two (PAIR)
+    static constexpr int kOffK = 2 * kTileBytes;
+    static constexpr int kOffV = kOffK + kStages * kTileBytes;
+    static constexpr int kOffML = kOffV + kStages * kTileBytes;  // [2 warpgroups][128] (max, sum)
+    static constexpr int kOffBar = kOffML + 2 * kBlockM * 8;
+    static constexpr int kOffStart = kOffBar + kTbCount * 8;
+    static constexpr int kUsedBytes = kOffStart + 48;
+    // At least 120 KB, so that no second CTA (which would wait for the 512 TMEM columns) shares the SM.
+    static constexpr int kSmemBytes = kUsedBytes + 1024 > 120 * 1024 ? kUsedBytes + 1024 : 120 * 1024;
+    static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
+    static constexpr int kTmemCols = 512;
+    static constexpr bool kAliasP = D == 128;
+    __host__ __device__ static constexpr uint32_t col_s(int i) { return 128u * i; }
+    __host__ __device__ static constexpr uint32_t col_o(int i) { return 256u + static_cast<uint32_t>(D) * i; }
+    __host__ __device__ static constexpr uint32_t col_p(int i)
+    {
+        return kAliasP ? col_s(i) : 256u + 2u * D + 64u * i;
+    }
+    static constexpr uint32_t kIdescS = idesc_bf16(kBlockM, kBlockN, false);
+    static constexpr uint32_t kIdescO = idesc_bf16(kBlockM, D, true);
+};
+
+// ---- work division -----------------------------------------------------------------------------
+
+// Cached tokens and drafted nodes of sequence b, clamped into the cache.
+struct TreeLen {
+    int prefix, nodes;
+    __device__ __forceinline__ int tiles() const
+    {
+        const int n = (prefix + nodes + kBlockN - 1) / kBlockN;
+        return n > 0 ? n : 1;  // a sequence without keys still has its rows written (O = 0)
+    }
+};
+
+__device__ __forceinline__ TreeLen tree_len(const int* seqlens, const int* n_nodes, int b, int T, int Nk_max, int* status)
+{
+    TreeLen x;
+    x.prefix = seqlens[b];
+    x.nodes = n_nodes != nullptr ? n_nodes[b] : T;
+    const bool bad = x.prefix < 0 || x.prefix > Nk_max || x.nodes < 0 || x.nodes > T || x.prefix > Nk_max - x.nodes;
+    if (bad) {
+        atomicCAS(status, 0, FA_ERR_INVALID_ARG);
+        x.prefix = min(max(x.prefix, 0), Nk_max);
+        x.nodes = min(min(max(x.nodes, 0), T), Nk_max - x.prefix);
+    }
+    return x;
+}
+
+// The share of CTA c: tiles [w0, w1) of all units in order, and the unit and tile it starts in.
+struct TreeStart {
+    long long w0, w1;
+    int b, unit, tile;  // sequence, unit within the sequence, tile within the unit
+};
+
+__device__ __forceinline__ long long share_begin(long long c, long long total, long long ctas) { return c * total / ctas; }
+
+// Sum of the sequences' tile counts by one warp.
+__device__ __forceinline__ long long tree_total(const TreeParams& p, int lane)
+{
+    long long sum = 0;
+    for (int b = lane; b < p.B; b += 32) sum += tree_len(p.seqlens, p.n_nodes, b, p.T, p.Nk_max, p.status).tiles();
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return sum;
+}
+
+// By one warp; every lane returns the same.  Empty (w0 = w1) for CTAs past the number of tiles.
+__device__ __forceinline__ TreeStart tree_locate(const TreeParams& p, int c, int lane)
+{
+    const long long upb = static_cast<long long>(p.Hkv) * p.n_qp;
+    const long long total = tree_total(p, lane) * upb;
+    const long long ctas = p.num_ctas < total ? p.num_ctas : total;
+    TreeStart s{0, 0, 0, 0, 0};
+    if (c >= ctas) return s;
+    s.w0 = share_begin(c, total, ctas);
+    s.w1 = share_begin(c + 1, total, ctas);
+    long long base = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+        const int b = b0 + lane;
+        const int tiles = b < p.B ? tree_len(p.seqlens, p.n_nodes, b, p.T, p.Nk_max, p.status).tiles() : 0;
+        long long incl = tiles * upb;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += x;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, base + incl > s.w0);
+        if (past != 0u) {
+            const int j = __ffs(past) - 1;  // the first sequence that ends after w0
+            const int tj = __shfl_sync(0xffffffffu, tiles, j);
+            const long long at = s.w0 - (base + __shfl_sync(0xffffffffu, incl, j) - tj * upb);
+            s.b = b0 + j;
+            s.unit = static_cast<int>(at / tj);
+            s.tile = static_cast<int>(at - static_cast<long long>(s.unit) * tj);
+            return s;
+        }
+        base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    s.w1 = s.w0;
+    return s;
+}
+
+// A CTA's share, segment by segment: a segment is a run of tiles of one unit.
+struct TreeWalk {
+    int left;            // tiles of the share not walked yet, this segment's included
+    int b, kvh, qp;      // sequence, key/value head, query block
+    int tile, tiles, n;  // first tile of the segment, tiles of the unit, tiles of the segment
+    TreeLen len;
+    bool first;          // the share's first segment
+    __device__ __forceinline__ void load(const TreeParams& p) { len = tree_len(p.seqlens, p.n_nodes, b, p.T, p.Nk_max, p.status); }
+    __device__ __forceinline__ void begin(const TreeParams& p, const TreeStart& s)
+    {
+        left = static_cast<int>(s.w1 - s.w0);
+        first = true;
+        if (left == 0) return;
+        b = s.b;
+        kvh = s.unit / p.n_qp;
+        qp = s.unit - kvh * p.n_qp;
+        tile = s.tile;
+        load(p);
+        tiles = len.tiles();
+        n = min(tiles - tile, left);
+    }
+    __device__ __forceinline__ bool live() const { return left > 0; }
+    __device__ __forceinline__ void next(const TreeParams& p)
+    {
+        left -= n;
+        first = false;
+        if (left == 0) return;
+        tile = 0;
+        if (++qp == p.n_qp) {
+            qp = 0;
+            if (++kvh == p.Hkv) {
+                kvh = 0;
+                ++b;
+                load(p);
+                tiles = len.tiles();
+            }
+        }
+        n = min(tiles, left);
+    }
+    __device__ __forceinline__ int group(const TreeParams& p) const { return b * p.Hkv + kvh; }
+    __device__ __forceinline__ bool whole() const { return n == tiles; }
+};
+
+// The slot of a part: a CTA's share holds at most two units that it does not finish alone, the one
+// that it starts in (slot 2c) and the one that it ends in (2c + 1, or 2c when they are the same).
+__device__ __forceinline__ int part_slot(int cta, bool first) { return 2 * cta + (first ? 0 : 1); }
+
+// Ancestors of node t (and t) as 128 bits.
+__device__ __forceinline__ void tree_ancestors(const int* parents, int t, int* status, uint32_t (&vis)[4])
+{
+#pragma unroll
+    for (int w = 0; w < 4; ++w) vis[w] = 0u;
+    if (parents == nullptr) {  // a chain: node t sees nodes 0 .. t
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const int bits = min(max(t + 1 - 32 * w, 0), 32);
+            vis[w] = bits == 32 ? 0xffffffffu : (1u << bits) - 1u;
+        }
+        return;
+    }
+    int cur = t;
+    while (cur >= 0) {  // strictly decreasing: at most T steps
+#pragma unroll
+        for (int w = 0; w < 4; ++w) vis[w] |= (cur >> 5) == w ? 1u << (cur & 31) : 0u;
+        int up = __ldg(parents + cur);
+        if (up >= cur || up < -1) {  // not a node before it: taken as a child of the last cached token
+            atomicCAS(status, 0, FA_ERR_INVALID_ARG);
+            up = -1;
+        }
+        cur = up;
+    }
+}
+
+// ---- kernel ------------------------------------------------------------------------------------
+
+// Converts and stores D / 2 consecutive fp32 values (D for a whole row) at element `at` of a row.
+template <int W>
+__device__ __forceinline__ void tree_store(const TreeParams& p, bool part, float* orow_part, void* o, size_t at, const float (&v)[W])
+{
+    static_assert(W == 16 || W == 32, "16 or 32 values");
+    if (part) {
+        if constexpr (W == 32) store_row32<float>(orow_part, v);
+        else store_row16<float>(orow_part, v);
+    } else if (p.o_dtype == FA_F32) {
+        if constexpr (W == 32) store_row32<float>(reinterpret_cast<float*>(o) + at, v);
+        else store_row16<float>(reinterpret_cast<float*>(o) + at, v);
+    } else {
+        if constexpr (W == 32) store_row32<__nv_bfloat16>(reinterpret_cast<__nv_bfloat16*>(o) + at, v);
+        else store_row16<__nv_bfloat16>(reinterpret_cast<__nv_bfloat16*>(o) + at, v);
+    }
+}
+
+template <int D, bool PAIR>
+__global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_constant__ TreeParams p)
+{
+    using C = TrCfg<D>;
+    constexpr int S = C::kStages;
+    extern __shared__ uint8_t tr_smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(tr_smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t bar0 = sbase + C::kOffBar;
+    auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
+    TreeStart* start_slot = reinterpret_cast<TreeStart*>(smem + C::kOffStart);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffStart + 32);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    static_assert(sizeof(TreeStart) <= 32, "start record");
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const unsigned long long limit = p.wait_limit_ns;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(kTbQFull + i), 1);
+            mbar_init(bar(kTbQEmpty + i), 2);
+            mbar_init(bar(kTbSFull + i), 1);
+            mbar_init(bar(kTbSFree + i), kBlockM);
+            mbar_init(bar(kTbPFull + i), kBlockM);
+            mbar_init(bar(kTbPVDone + i), 1);
+            mbar_init(bar(kTbOReady + i), 1);
+            mbar_init(bar(kTbOFree + i), PAIR ? kBlockM : 2 * kBlockM);
+            mbar_init(bar(kTbDrain + i), 1);
+        }
+        mbar_init(bar(kTbMLFull), 2 * kBlockM);
+        for (int s = 0; s < S; ++s) {
+            mbar_init(bar(kTbKFull + s), 1);
+            mbar_init(bar(kTbKEmpty + s), PAIR ? 2 : 1);
+            mbar_init(bar(kTbVFull + s), 1);
+            mbar_init(bar(kTbVEmpty + s), PAIR ? 2 : 1);
+        }
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == kTrWarpMma) {
+        tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
+        tmem_relinquish();
+    }
+    grid_dependency_wait();    // launched as a programmatic dependent of the previous kernel
+    grid_launch_dependents();  // the merge may begin launching (it waits for this grid)
+    if (warp == 0) {
+        const TreeStart s = tree_locate(p, blockIdx.x, lane);
+        if (lane == 0) *start_slot = s;
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    const TreeStart start = *start_slot;
+    const int total = static_cast<int>(start.w1 - start.w0);
+
+    if (warp >= kTrWarpProducer) {
+        regs_decrease<kTrControlRegs<D>>();
+        if (warp == kTrWarpProducer) {
+            // ======================================================== producer
+            if (lane == 0 && total > 0) {
+                prefetch_tensormap(&p.tm_q);
+                prefetch_tensormap(&p.tm_k);
+                prefetch_tensormap(&p.tm_v);
+                // K and V are read again only by a group's further query blocks
+                const uint64_t pol_kv = p.n_qp > 1 ? policy_evict_last() : policy_evict_first();
+                const uint64_t pol_q = policy_evict_first();
+                TreeWalk kw, vw;  // K runs one tile ahead of V
+                kw.begin(p, start);
+                vw.begin(p, start);
+                int kj = 0, vj = 0;  // tile within the segment
+                int segs = 0;        // query loads issued
+                int k_issued = 0, v_issued = 0;
+                auto load_k = [&]() -> bool {
+                    const int g = kw.group(p);
+                    if (kj == 0) {  // the segment's query rows
+                        const int buf = PAIR ? 0 : segs & 1;
+                        const int use = PAIR ? segs : segs >> 1;
+                        if (use > 0 && !mbar_wait(bar(kTbQEmpty + buf), static_cast<uint32_t>(use - 1) & 1, limit, abort_flag))
+                            return false;
+                        const int row0 = kw.qp * (PAIR ? 2 : 1) * kBlockM;
+                        const int q_tiles = PAIR && p.rows - row0 > kBlockM ? 2 : 1;
+                        mbar_arrive_expect_tx(bar(kTbQFull + buf), q_tiles * C::kTileBytes);
+                        for (int i = 0; i < q_tiles; ++i)
+                            for (int cb = 0; cb < C::kNumCB; ++cb)
+                                tma_load_3d(sbase + C::kOffQ + (buf + i) * C::kTileBytes + cb * C::kBlkBytes, &p.tm_q,
+                                            bar(kTbQFull + buf), cb * C::kCB, row0 + i * kBlockM, g, pol_q);
+                        ++segs;
+                    }
+                    const int s = k_issued % S;
+                    if (k_issued >= S &&
+                        !mbar_wait(bar(kTbKEmpty + s), static_cast<uint32_t>(k_issued / S - 1) & 1, limit, abort_flag))
+                        return false;
+                    mbar_arrive_expect_tx(bar(kTbKFull + s), C::kTileBytes);
+                    for (int cb = 0; cb < C::kNumCB; ++cb)
+                        tma_load_3d(sbase + C::kOffK + s * C::kTileBytes + cb * C::kBlkBytes, &p.tm_k, bar(kTbKFull + s),
+                                    cb * C::kCB, (kw.tile + kj) * kBlockN, g, pol_kv);
+                    ++k_issued;
+                    if (++kj == kw.n) {
+                        kj = 0;
+                        kw.next(p);
+                    }
+                    return true;
+                };
+                auto load_v = [&]() -> bool {
+                    const int s = v_issued % S;
+                    if (v_issued >= S &&
+                        !mbar_wait(bar(kTbVEmpty + s), static_cast<uint32_t>(v_issued / S - 1) & 1, limit, abort_flag))
+                        return false;
+                    mbar_arrive_expect_tx(bar(kTbVFull + s), C::kTileBytes);
+                    for (int cb = 0; cb < C::kNumCB; ++cb)
+                        tma_load_3d(sbase + C::kOffV + s * C::kTileBytes + cb * C::kBlkBytes, &p.tm_v, bar(kTbVFull + s),
+                                    cb * C::kCB, (vw.tile + vj) * kBlockN, vw.group(p), pol_kv);
+                    ++v_issued;
+                    if (++vj == vw.n) {
+                        vj = 0;
+                        vw.next(p);
+                    }
+                    return true;
+                };
+                bool ok = load_k();
+                for (int t = 0; ok && t < total; ++t) ok = (t + 1 >= total || load_k()) && load_v();
+                if (!ok && !*abort_flag) record_failure(p.status, abort_flag, FA_ERR_TIMEOUT);
+                // Every issued copy must land before the CTA may exit (its last phase per barrier).
+                const int q_bufs = PAIR ? 1 : 2;
+                for (int t = segs - q_bufs < 0 ? 0 : segs - q_bufs; t < segs; ++t)
+                    mbar_wait(bar(kTbQFull + t % q_bufs), static_cast<uint32_t>(t / q_bufs) & 1, kDrainLimitNs, nullptr);
+                for (int t = k_issued - S < 0 ? 0 : k_issued - S; t < k_issued; ++t)
+                    mbar_wait(bar(kTbKFull + t % S), static_cast<uint32_t>(t / S) & 1, kDrainLimitNs, nullptr);
+                for (int t = v_issued - S < 0 ? 0 : v_issued - S; t < v_issued; ++t)
+                    mbar_wait(bar(kTbVFull + t % S), static_cast<uint32_t>(t / S) & 1, kDrainLimitNs, nullptr);
+            }
+        } else if (warp == kTrWarpMma || warp == kTrWarpMma + 1) {
+            // ======================================================== MMA issuers
+            if (lane == 0 && total > 0) {
+                const int i = warp - kTrWarpMma;  // warpgroup of this issuer
+                const uint32_t d_s = tmem + C::col_s(i);
+                const uint32_t d_o = tmem + C::col_o(i);
+                const uint32_t a_p = tmem + C::col_p(i);
+                int tiles = 0;   // products issued by this issuer
+                int s_done = 0;  // score tiles issued
+                int k = 0;       // tile of the CTA's share
+                int segs = 0, o_uses = 0;  // segments walked; OFree phases that precede the next first product
+                bool ok = true;
+                auto issue_s = [&](int q_tile, int stage) {
+                    const uint64_t a0 = smem_desc(sbase + C::kOffQ + q_tile * C::kTileBytes, 16, C::kAtomBytes, C::kLayout);
+                    const uint64_t b0 = smem_desc(sbase + C::kOffK + stage * C::kTileBytes, 16, C::kAtomBytes, C::kLayout);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = ((kk * 16) / C::kCB * C::kBlkBytes + ((kk * 16) % C::kCB) * 2) >> 4;
+                        umma_ss(d_s, a0 + off, b0 + off, C::kIdescS, kk > 0 ? 1u : 0u);
+                    }
+                };
+                auto issue_pv = [&](int stage, bool accumulate) {
+                    const uint64_t b0 = smem_desc(sbase + C::kOffV + stage * C::kTileBytes, C::kBlkBytes, C::kAtomBytes,
+                                                  C::kLayout);
+#pragma unroll
+                    for (int kk = 0; kk < kBlockN / 16; ++kk)
+                        umma_ts(d_o, a_p + 8u * kk, b0 + ((kk * 16 * C::kRowBytes) >> 4), C::kIdescO,
+                                (accumulate || kk > 0) ? 1u : 0u);
+                };
+                // S_i of share tile kk.  Its columns must have been read (and, where P overwrites
+                // them, the product that reads P must have completed).
+                auto do_s = [&](int q_tile, int q_buf, int kk, bool last) -> bool {
+                    const int s = kk % S;
+                    if (!mbar_wait(bar(kTbKFull + s), static_cast<uint32_t>(kk / S) & 1, limit, abort_flag)) return false;
+                    if (s_done > 0 && !mbar_wait(bar((C::kAliasP ? kTbPVDone : kTbSFree) + i),
+                                                 static_cast<uint32_t>(s_done - 1) & 1, limit, abort_flag))
+                        return false;
+                    ++s_done;
+                    tc_fence_after_sync();
+                    issue_s(q_tile, s);
+                    umma_commit(bar(kTbSFull + i));
+                    umma_commit(bar(kTbKEmpty + s));
+                    if (last) umma_commit(bar(kTbQEmpty + q_buf));
+                    return true;
+                };
+                TreeWalk w;
+                for (w.begin(p, start); ok && w.live(); w.next(p)) {
+                    const int q_buf = PAIR ? 0 : segs & 1;
+                    const int q_use = PAIR ? segs : segs >> 1;
+                    const int q_tile = PAIR ? i : q_buf;
+                    const bool mine = !PAIR || i == 0 || p.rows - w.qp * 2 * kBlockM > kBlockM;
+                    const int step = PAIR ? 1 : 2;
+                    const int j0 = PAIR ? 0 : (k + i) & 1;  // first tile of the segment for this warpgroup
+                    // Also without tiles of its own in the segment: an issuer that skipped a phase of the
+                    // query barrier could take the phase before it for the one it needs.
+                    ok = mbar_wait(bar(kTbQFull + q_buf), static_cast<uint32_t>(q_use) & 1, limit, abort_flag);
+                    if (!ok) break;
+                    if (!mine || j0 >= w.n) {
+                        // (before the loop: the producer may be waiting to load the next unit's queries
+                        // ahead of this unit's last V)
+                        mbar_arrive(bar(kTbQEmpty + q_buf));
+                        if (PAIR) {  // no rows: pass every tile on
+                            for (int j = 0; ok && j < w.n; ++j) {
+                                const int s = (k + j) % S;
+                                const uint32_t ph = static_cast<uint32_t>((k + j) / S) & 1;
+                                ok = mbar_wait(bar(kTbKFull + s), ph, limit, abort_flag) &&
+                                     mbar_wait(bar(kTbVFull + s), ph, limit, abort_flag);
+                                if (!ok) break;
+                                mbar_arrive(bar(kTbKEmpty + s));
+                                mbar_arrive(bar(kTbVEmpty + s));
+                            }
+                        }
+                    } else {
+                        const int j_last = j0 + (w.n - 1 - j0) / step * step;
+                        ok = do_s(q_tile, q_buf, k + j0, j0 == j_last);
+                        for (int j = j0; ok && j < w.n; j += step) {
+                            const int kk = k + j;
+                            const int s = kk % S;
+                            // Without aliasing the next scores need only the current ones read: they run
+                            // while this tile is still being exponentiated.
+                            if (!C::kAliasP && j + step < w.n) ok = do_s(q_tile, q_buf, kk + step, j + step == j_last);
+                            ok = ok && mbar_wait(bar(kTbPFull + i), static_cast<uint32_t>(tiles) & 1, limit, abort_flag) &&
+                                 mbar_wait(bar(kTbVFull + s), static_cast<uint32_t>(kk / S) & 1, limit, abort_flag);
+                            // The first product of a segment overwrites O_i: the previous segment's must have
+                            // been read.  Waited for after P: this warpgroup has then been through every
+                            // earlier segment's exchange, so the barrier is at most one phase behind.
+                            if (ok && j == j0 && o_uses > 0)
+                                ok = mbar_wait(bar(kTbOFree + i), static_cast<uint32_t>(o_uses - 1) & 1, limit, abort_flag);
+                            if (!ok) break;
+                            tc_fence_after_sync();
+                            issue_pv(s, j > j0);
+                            umma_commit(bar(kTbPVDone + i));
+                            if (j == j_last) umma_commit(bar(kTbOReady + i));
+                            umma_commit(bar(kTbVEmpty + s));
+                            ++tiles;
+                            if (C::kAliasP && j + step < w.n) ok = do_s(q_tile, q_buf, kk + step, j + step == j_last);
+                        }
+                    }
+                    if (!PAIR || mine) ++o_uses;
+                    k += w.n;
+                    ++segs;
+                }
+                if (!ok && !*abort_flag) record_failure(p.status, abort_flag, FA_ERR_TIMEOUT);
+                umma_commit(bar(kTbDrain + i));
+                mbar_wait(bar(kTbDrain + i), 0, kDrainLimitNs, nullptr);
+            }
+        }
+    } else {
+        regs_increase<kTrSoftmaxRegs<D>>();
+        // ============================================================ softmax + epilogue
+        const int wg = warp >> 2;
+        const int r = threadIdx.x & 127;  // row of the tile == TMEM lane
+        const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t t_s = tmem + lane_base + C::col_s(wg);
+        const uint32_t t_o = tmem + lane_base + C::col_o(wg);
+        const uint32_t t_p = tmem + lane_base + C::col_p(wg);
+        float2* ml = reinterpret_cast<float2*>(smem + C::kOffML);
+        const float sl2 = p.scale_log2;
+        int tiles = 0;                 // key tiles processed by this warpgroup
+        int ready[2] = {0, 0};         // segments with tiles so far, per warpgroup
+        int segs = 0, k = 0;
+        bool ok = true;
+        TreeWalk w;
+        for (w.begin(p, start); ok && w.live(); w.next(p)) {
+            const int row0 = PAIR ? w.qp * 2 * kBlockM + wg * kBlockM : 0;
+            const int rows = min(p.rows - row0, kBlockM);  // rows of this warpgroup's tile (<= 0: none)
+            if (PAIR && rows <= 0) {
+                k += w.n;
+                ++segs;
+                continue;
+            }
+            const int row = row0 + r;
+            const int node = row % p.T;
+            const bool valid = r < rows;
+            const bool warp_live = 32 * (warp & 3) < rows;
+            const int step = PAIR ? 1 : 2;
+            const int j0 = PAIR ? 0 : (k + wg) & 1;
+            const int end = w.len.prefix + w.len.nodes;  // keys of the sequence
+            uint32_t vis[4] = {0u, 0u, 0u, 0u};
+            if ((w.tile + w.n) * kBlockN > w.len.prefix && valid && node < w.len.nodes)
+                tree_ancestors(p.parents != nullptr ? p.parents + static_cast<size_t>(w.b) * p.T : nullptr, node, p.status, vis);
+            float m_run = -INFINITY;  // running max of scale * log2(e) * S over visible keys
+            float l = 0.f;
+            for (int j = j0; j < w.n; j += step) {
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(kTbSFull + wg), tiles & 1, limit, abort_flag));
+                if (!ok) break;
+                tc_fence_after_sync();
+                const int k0 = (w.tile + j) * kBlockN;
+                const int stage = (k + j) % S;
+                if (warp_live) {
+                    uint32_t u[kBlockN];
+                    float mrow;
+                    if constexpr (D == 128) {
+                        float mh[2];
+                        tmem_ld64_max(t_s + 0, *reinterpret_cast<uint32_t(*)[64]>(&u[0]), mh[0]);
+                        tmem_ld64_max(t_s + 64, *reinterpret_cast<uint32_t(*)[64]>(&u[64]), mh[1]);
+                        tmem_ld_wait();
+                        mrow = fmaxf(mh[0], mh[1]);
+                    } else {
+                        float mq[4];
+                        tmem_ld32_max(t_s + 0, *reinterpret_cast<uint32_t(*)[32]>(&u[0]), mq[0]);
+                        tmem_ld32_max(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(&u[32]), mq[1]);
+                        tmem_ld32_max(t_s + 64, *reinterpret_cast<uint32_t(*)[32]>(&u[64]), mq[2]);
+                        tmem_ld32_max(t_s + 96, *reinterpret_cast<uint32_t(*)[32]>(&u[96]), mq[3]);
+                        tmem_ld_wait();
+                        mrow = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
+                    }
+                    if constexpr (!C::kAliasP) {
+                        tc_fence_before_sync();
+                        mbar_arrive(bar(kTbSFree + wg));
+                    }
+                    float s[kBlockN];
+#pragma unroll
+                    for (int c = 0; c < kBlockN; ++c) s[c] = __uint_as_float(u[c]);
+                    if (k0 + kBlockN > w.len.prefix) {  // the tile holds drafted rows, or rows past them
+                        const int shift = k0 - w.len.prefix;  // node index of the tile's first key
+                        auto word = [&](int q) -> uint32_t {
+                            return q == 0 ? vis[0] : q == 1 ? vis[1] : q == 2 ? vis[2] : q == 3 ? vis[3] : 0u;
+                        };
+                        float a[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int bit = shift + 32 * q;
+                            const int cached = min(max(-bit, 0), 32);  // columns that are cached tokens
+                            const uint32_t seen = __funnelshift_r(word(bit >> 5), word((bit >> 5) + 1), bit & 31) |
+                                                  (cached == 32 ? 0xffffffffu : (1u << cached) - 1u);
+                            a[q] = -INFINITY;
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) {
+                                s[32 * q + c] = (seen >> c) & 1u ? s[32 * q + c] : -INFINITY;
+                                a[q] = fmaxf(a[q], s[32 * q + c]);
+                            }
+                        }
+                        mrow = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
+                    }
+                    const float mt = mrow * sl2;
+                    const bool grow = mt > m_run;
+                    float alpha = 1.f;
+                    if (grow) {
+                        alpha = ex2(m_run - mt);  // 0 when m_run = -inf
+                        m_run = mt;
+                    }
+                    const float m_use = m_run == -INFINITY ? 0.f : m_run;
+                    const float2 sl2x2 = make_float2(sl2, sl2), negm = make_float2(-m_use, -m_use);
+                    float2 rs[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                                    make_float2(0.f, 0.f)};
+                    uint32_t pk[kBlockN / 2];
+#pragma unroll
+                    for (int c = 0; c < kBlockN; c += 8) {
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            const float2 x = __ffma2_rn(make_float2(s[c + 2 * h], s[c + 2 * h + 1]), sl2x2, negm);
+                            const float2 e = make_float2(ex2(x.x), ex2(x.y));
+                            rs[h] = __fadd2_rn(rs[h], e);
+                            // the weights are rounded to bf16 for the product (half a step, 2^-8 of each
+                            // weight); the sum l keeps the fp32 ones
+                            pk[c / 2 + h] = pack_bf16x2(e.x, e.y);
+                        }
+                    }
+                    // O_i and P_i are free once the previous product has completed (with P aliased into
+                    // S_i the arrival of S_i implies it)
+                    if (!C::kAliasP && j > j0) {
+                        ok = __all_sync(0xffffffffu, mbar_wait(bar(kTbPVDone + wg), (tiles - 1) & 1, limit, abort_flag));
+                        if (!ok) break;
+                        tc_fence_after_sync();
+                    }
+                    if (j > j0 && __any_sync(0xffffffffu, grow)) {
+                        constexpr int kRescale = D <= 64 ? D : 32;
+                        const float2 a2 = make_float2(alpha, alpha);
+#pragma unroll
+                        for (int c0 = 0; c0 < D; c0 += kRescale) {
+                            uint32_t oc[kRescale];
+#pragma unroll
+                            for (int c = 0; c < kRescale; c += 32)
+                                tmem_ld32(t_o + static_cast<uint32_t>(c0 + c), *reinterpret_cast<uint32_t(*)[32]>(&oc[c]));
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < kRescale; e += 2) {
+                                const float2 x = __fmul2_rn(make_float2(__uint_as_float(oc[e]), __uint_as_float(oc[e + 1])), a2);
+                                oc[e] = __float_as_uint(x.x);
+                                oc[e + 1] = __float_as_uint(x.y);
+                            }
+#pragma unroll
+                            for (int c = 0; c < kRescale; c += 32)
+                                tmem_st32(t_o + static_cast<uint32_t>(c0 + c), *reinterpret_cast<uint32_t(*)[32]>(&oc[c]));
+                        }
+                    }
+                    tmem_st32(t_p + 0, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
+                    tmem_st32(t_p + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
+                    tmem_st_wait();
+                    l = l * alpha + (((rs[0].x + rs[0].y) + (rs[1].x + rs[1].y)) + ((rs[2].x + rs[2].y) + (rs[3].x + rs[3].y)));
+                } else if (!C::kAliasP) {
+                    mbar_arrive(bar(kTbSFree + wg));
+                    // A warp without rows waits for the previous product too: with the next scores
+                    // already there, it could otherwise arrive twice in one phase of PFull.
+                    if (j > j0) {
+                        ok = __all_sync(0xffffffffu, mbar_wait(bar(kTbPVDone + wg), (tiles - 1) & 1, limit, abort_flag));
+                        if (!ok) break;
+                    }
+                }
+                if (k0 + kBlockN > end) {
+                    // V rows past the tree may hold anything: zero them before the product reads them.
+                    // (The stage's previous tile has been consumed: see kStages.)
+                    ok = __all_sync(0xffffffffu, mbar_wait(bar(kTbVFull + stage), static_cast<uint32_t>((k + j) / S) & 1,
+                                                           limit, abort_flag));
+                    if (!ok) break;
+                    if (k0 + r >= end) {
+                        const uint32_t vrow = sbase + C::kOffV + stage * C::kTileBytes + r * C::kRowBytes;
+#pragma unroll
+                        for (int cb = 0; cb < C::kNumCB; ++cb)
+#pragma unroll
+                            for (int c16 = 0; c16 < C::kRowBytes; c16 += 16)
+                                st_shared_v4(vrow + cb * C::kBlkBytes + c16, 0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_shared();
+                }
+                tc_fence_before_sync();
+                mbar_arrive(bar(kTbPFull + wg));
+                ++tiles;
+            }
+            if (!ok) break;
+            // ---- end of the segment: its rows' output and log-sum-exp, final or to a slot
+            const bool part = !w.whole();
+            const int slot = part_slot(blockIdx.x, w.first);
+            const bool shown = node < w.len.nodes;  // rows of nodes past the tree: O = 0, LSE = -inf
+            const size_t out_row = static_cast<size_t>(w.group(p)) * p.rows + row;
+            const size_t part_row = static_cast<size_t>(slot) * p.part_rows + (PAIR ? wg * kBlockM : 0) + r;
+            if constexpr (PAIR) {
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(kTbOReady + wg), ready[0] & 1, limit, abort_flag));
+                if (!ok) break;
+                ++ready[0];
+                tc_fence_after_sync();
+                if (warp_live) {
+                    const float inv = (l == 0.f || !shown) ? 0.f : 1.f / l;
+#pragma unroll
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        float x[32];
+                        tmem_ld32(t_o + static_cast<uint32_t>(c), o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) x[e] = shown ? __uint_as_float(o[e]) * inv : 0.f;
+                        if (valid) tree_store<32>(p, part, p.o_part + part_row * D + c, p.o, out_row * D + c, x);
+                    }
+                    const float lse = (l == 0.f || !shown) ? -INFINITY : (m_run + lg2_approx(l)) * 0.69314718055994531f;
+                    if (valid) {
+                        if (part) p.lse_part[part_row] = lse;
+                        else if (p.lse != nullptr) p.lse[out_row] = lse;
+                    }
+                }
+                tc_fence_before_sync();
+                mbar_arrive(bar(kTbOFree + wg));
+            } else {
+                const int jw[2] = {k & 1, (k + 1) & 1};  // first tile of the segment for warpgroups 0 and 1
+                const bool has0 = jw[0] < w.n, has1 = jw[1] < w.n;
+                // the other warpgroup must have read the previous segment's max and sum
+                if (segs > 0) ok = mbar_wait(bar(kTbOFree + wg), static_cast<uint32_t>(segs - 1) & 1, limit, abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                ml[wg * kBlockM + r] = make_float2(m_run, l);
+                mbar_arrive(bar(kTbMLFull));
+                ok = mbar_wait(bar(kTbMLFull), static_cast<uint32_t>(segs) & 1, limit, abort_flag);
+                if (ok && has0) ok = mbar_wait(bar(kTbOReady + 0), ready[0] & 1, limit, abort_flag);
+                if (ok && has1) ok = mbar_wait(bar(kTbOReady + 1), ready[1] & 1, limit, abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                ready[0] += has0 ? 1 : 0;
+                ready[1] += has1 ? 1 : 0;
+                tc_fence_after_sync();
+                if (warp_live) {
+                    const float2 x0 = ml[r], x1 = ml[kBlockM + r];
+                    const float M = fmaxf(x0.x, x1.x);
+                    const float f0 = x0.x == -INFINITY ? 0.f : ex2(x0.x - M);
+                    const float f1 = x1.x == -INFINITY ? 0.f : ex2(x1.x - M);
+                    const float L = x0.y * f0 + x1.y * f1;
+                    const bool none = L == 0.f || !shown;
+                    const float inv = none ? 0.f : 1.f / L;
+                    const float g0 = f0 * inv, g1 = f1 * inv;
+                    constexpr int W = D / 2 < 32 ? D / 2 : 32;  // this warpgroup's half of the columns, W at a time
+#pragma unroll
+                    for (int c = 0; c < D / 2; c += W) {
+                        const uint32_t col = static_cast<uint32_t>(wg * (D / 2) + c);
+                        uint32_t a[W], b[W];
+                        float x[W];
+                        if constexpr (W == 32) {
+                            if (has0) tmem_ld32(tmem + lane_base + C::col_o(0) + col, a);
+                            if (has1) tmem_ld32(tmem + lane_base + C::col_o(1) + col, b);
+                        } else {
+                            if (has0) tmem_ld16(tmem + lane_base + C::col_o(0) + col, a);
+                            if (has1) tmem_ld16(tmem + lane_base + C::col_o(1) + col, b);
+                        }
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < W; ++e) {
+                            const float y0 = has0 ? __uint_as_float(a[e]) * g0 : 0.f;
+                            x[e] = none ? 0.f : has1 ? fmaf(__uint_as_float(b[e]), g1, y0) : y0;
+                        }
+                        if (valid) tree_store<W>(p, part, p.o_part + part_row * D + col, p.o, out_row * D + col, x);
+                    }
+                    if (valid && wg == 0) {
+                        const float lse = none ? -INFINITY : (M + lg2_approx(L)) * 0.69314718055994531f;
+                        if (part) p.lse_part[part_row] = lse;
+                        else if (p.lse != nullptr) p.lse[out_row] = lse;
+                    }
+                }
+                tc_fence_before_sync();
+                mbar_arrive(bar(kTbOFree + 0));
+                mbar_arrive(bar(kTbOFree + 1));
+            }
+            k += w.n;
+            ++segs;
+        }
+        if (!ok && !*abort_flag) record_failure(p.status, abort_flag, FA_ERR_TIMEOUT);
+    }
+
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == kTrWarpMma) {
+        __syncwarp();
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, C::kTmemCols);
+    }
+}
+
+// Joins the parts of the units that several CTAs share: lse = log sum_s exp(lse_s),
+// o = sum_s exp(lse_s - lse) o_s ("flash_lab.py" section 4).  Block (u, y) serves unit u, rows
+// 32 y .. 32 y + 31, a warp four rows.  The part of the unit's first CTA is that CTA's last
+// segment unless its share begins with the unit; the parts of the others are their first segments.
+template <int D>
+__global__ void __launch_bounds__(256) fa_tree_merge_kernel(const __grid_constant__ TreeParams p)
+{
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int upb = p.Hkv * p.n_qp;
+    const int b = static_cast<int>(blockIdx.x / upb);
+    const int unit = static_cast<int>(blockIdx.x - static_cast<unsigned>(b) * upb);
+    const int kvh = unit / p.n_qp;
+    const int row_base = (unit - kvh * p.n_qp) * p.part_rows;  // first row of the unit within its group
+    const int rows = min(p.part_rows, p.rows - row_base);
+    grid_dependency_wait();
+    grid_launch_dependents();
+    long long before = 0, all = 0;  // tiles per unit of the sequences before b, and of all
+    for (int i = lane; i < p.B; i += 32) {
+        const int t = tree_len(p.seqlens, p.n_nodes, i, p.T, p.Nk_max, p.status).tiles();
+        all += t;
+        if (i < b) before += t;
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+        before += __shfl_xor_sync(0xffffffffu, before, o);
+        all += __shfl_xor_sync(0xffffffffu, all, o);
+    }
+    const int tiles = tree_len(p.seqlens, p.n_nodes, b, p.T, p.Nk_max, p.status).tiles();
+    const long long total = all * upb;
+    const long long ctas = p.num_ctas < total ? p.num_ctas : total;
+    const long long w = before * upb + static_cast<long long>(unit) * tiles;  // the unit's first tile
+    const int c0 = static_cast<int>(((w + 1) * ctas - 1) / total);            // the CTAs of its first and last tile
+    const int c1 = static_cast<int>(((w + tiles) * ctas - 1) / total);
+    if (c0 == c1) return;  // finished by its CTA
+    const int n = c1 - c0 + 1;
+    const bool head = share_begin(c0, total, ctas) == w;
+    constexpr int V = D / 32;  // columns of a lane
+    for (int q = 0; q < 4; ++q) {
+        const int r = static_cast<int>(blockIdx.y) * 32 + warp * 4 + q;
+        if (r >= rows) return;
+        auto at = [&](int s) -> size_t {
+            return static_cast<size_t>(part_slot(c0 + s, s > 0 || head)) * p.part_rows + static_cast<size_t>(r);
+        };
+        float M = -INFINITY;
+        bool live = false;
+        for (int s = lane; s < n; s += 32) {
+            const float x = __ldg(p.lse_part + at(s));
+            live = live || x != -INFINITY;
+            M = fmaxf(M, x);
+        }
+        live = __any_sync(0xffffffffu, live);
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        float sum = 0.f;
+        for (int s = lane; s < n; s += 32) {
+            const float x = __ldg(p.lse_part + at(s));
+            if (x != -INFINITY) sum += ex2((x - M) * 1.4426950408889634f);
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float L = live ? M + log2f(sum) * 0.69314718055994531f : -INFINITY;
+        float acc[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] = 0.f;
+        if (live) {
+#pragma unroll 4
+            for (int s = 0; s < n; ++s) {
+                const size_t row = at(s);
+                const float x = __ldg(p.lse_part + row);  // the same for the whole warp
+                const float f = x == -INFINITY ? 0.f : ex2((x - L) * 1.4426950408889634f);
+                const float* src = p.o_part + row * D + lane * V;
+                float v[V];
+                if constexpr (V == 4) *reinterpret_cast<float4*>(v) = __ldg(reinterpret_cast<const float4*>(src));
+                else if constexpr (V == 2) *reinterpret_cast<float2*>(v) = __ldg(reinterpret_cast<const float2*>(src));
+                else v[0] = __ldg(src);
+#pragma unroll
+                for (int e = 0; e < V; ++e) acc[e] = fmaf(f, v[e], acc[e]);
+            }
+        }
+        const size_t out = (static_cast<size_t>(b) * p.Hkv + kvh) * p.rows + row_base + r;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            if (p.o_dtype == FA_F32)
+                reinterpret_cast<float*>(p.o)[out * D + lane * V + e] = acc[e];
+            else
+                reinterpret_cast<__nv_bfloat16*>(p.o)[out * D + lane * V + e] = __float2bfloat16_rn(acc[e]);
+        }
+        if (lane == 0 && p.lse != nullptr) p.lse[out] = L;
+    }
+}
+
+template <int D, bool PAIR>
+cudaError_t launch_tree_t(const TreeParams& p, cudaStream_t st)
+{
+    using C = TrCfg<D>;
+    auto kern = fa_tree_kernel<D, PAIR>;
+    static bool configured[64] = {};  // attributes set and registers checked, per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!configured[dev]) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+        if (e != cudaSuccess) return e;
+        cudaFuncAttributes attr;
+        e = cudaFuncGetAttributes(&attr, kern);
+        if (e != cudaSuccess) return e;
+        // a register increase that the launch's pool cannot satisfy would wait forever
+        if (attr.numRegs * kTrThreads < 256 * kTrSoftmaxRegs<D> + 128 * kTrControlRegs<D>)
+            return cudaErrorLaunchOutOfResources;
+        configured[dev] = true;
+    }
+    e = launch_pdl(kern, dim3(static_cast<unsigned>(p.num_ctas)), kTrThreads, C::kSmemBytes, st, p);
+    if (e != cudaSuccess) return e;
+    const dim3 grid(static_cast<unsigned>(p.B) * p.Hkv * p.n_qp, static_cast<unsigned>((p.part_rows + 31) / 32));
+    return launch_pdl(fa_tree_merge_kernel<D>, grid, 256, 0, st, p);
+}
+
+template <int D>
+cudaError_t launch_tree_d(const TreeParams& p, cudaStream_t st)
+{
+    return p.part_rows > kBlockM ? launch_tree_t<D, true>(p, st) : launch_tree_t<D, false>(p, st);
+}
+
+}  // namespace fa

@@ -24,10 +24,19 @@
  *   fa_merge_states     the log-sum-exp combine of partial states on its own
  *                       ("flash_lab.py", section 4 `split_kv_decode` combine, the
  *                       lse form of section 1 `merge_states`).
+ *   fa_qk_norm_rope     a layer's query, key and value projections to fa_fwd's operands: norm of
+ *                       each query and key head, position rotation and head-major layout;
+ *   fa_qk_norm_rope_bwd its gradient from fa_bwd's outputs;
+ *   fa_qk_norm_rope_append  the same for new tokens, keys and values written into a cache.
+ *   fa_decode_tree      decode for a tree of drafted tokens over a cache (several queries for each
+ *                       sequence, each seeing the cached tokens and its ancestors).
+ *   fa_cache_compact    the accepted path of such a tree moved up behind the cached tokens.
  *
  * Conventions shared by every entry point:
  *   - All tensors are dense, row-major, last dimension contiguous, in the layouts
- *     stated per argument ([B,H,rows,cols]).  Device pointers must be 16-byte aligned.
+ *     stated per argument ([B,H,rows,cols]); the projections that the fa_qk_norm_rope calls
+ *     read, and the gradients written for them, have a token stride besides.  Device pointers
+ *     must be 16-byte aligned.
  *   - q, k, v and the caches are bf16.  Arithmetic is fp32 (tensor-core accumulation in
  *     fp32; softmax statistics in fp32).  O is written as bf16 (FA_BF16) or fp32 (FA_F32);
  *     LSE is always fp32, natural log, scale included:
@@ -56,7 +65,8 @@
  *     of range) are recorded in a device status word read by fa_get_device_error.
  *   - Supported head sizes: d = dv, d in {32, 64, 128}.  Other sizes return
  *     FA_ERR_UNSUPPORTED.  Heads are independent; the number of key/value heads equals
- *     the number of query heads except in fa_decode_splitkv_gqa.
+ *     the number of query heads except in fa_decode_splitkv_gqa, fa_decode_tree and the
+ *     fa_qk_norm_rope calls.
  */
 #ifndef FA_H
 #define FA_H
@@ -327,6 +337,144 @@ fa_status fa_decode_splitkv_noalloc(const void* q, const void* k_cache, const vo
  */
 fa_status fa_merge_states(const float* o_parts, const float* lse_parts, int n_parts, int rows,
                           int dv, void* o, float* lse, fa_dtype o_dtype, void* stream);
+
+/*
+ * Operands of exact attention from a layer's projections.  For every token and head, with x the
+ * head's d elements, w the weights and pos the token's position:
+ *   y = x w / sqrt(mean(x^2) + eps)                          (query and key heads)
+ *   (y_a, y_b) -> (y_a c - y_b s, y_a s + y_b c),  c = cos_table[pos][i], s = sin_table[pos][i]
+ * for the pairs i < rot/2 of the first rot elements: (a, b) = (i, i + rot/2), or (2i, 2i + 1) with
+ * interleaved = 1; the elements from rot on stay.  Value heads are copied.  Arithmetic is fp32, each
+ * output element rounded once to bf16.
+ *
+ *   q, k, v    bf16 [B, N, heads, d]   (device; token (b, n) at (b N + n) * stride elements, its heads
+ *              d apart: slices of one projection's output will do.  Strides >= heads * d, multiples
+ *              of 8.  v may be NULL, with v_out.)
+ *   q_weight, k_weight   w_dtype [d]   (device; 4-byte aligned)
+ *   cos_table, sin_table fp32 [max_pos, rot/2]  (device)
+ *   positions  int32 [B, N]            (device; NULL: n.  Values outside [0, max_pos) are clamped and
+ *              recorded as FA_ERR_INVALID_ARG in the device status word.)
+ *   q_out      bf16 [B, Hq, N, d]      (device, written)
+ *   k_out, v_out  bf16 [B, Hkv, N, d], or with expand = 1 [B, Hq, N, d]: head h is key/value head
+ *              h / (Hq / Hkv), as fa_fwd takes them  (device, written)
+ *   d in {32, 64, 128}; Hkv dividing Hq; rot a multiple of 16, at most d; B * N < 2^31; eps >= 0.
+ * Outputs must not overlap inputs.
+ */
+fa_status fa_qk_norm_rope(const void* q, const void* k, const void* v, const void* q_weight,
+                          const void* k_weight, const float* cos_table, const float* sin_table,
+                          const int* positions, void* q_out, void* k_out, void* v_out,
+                          long long q_stride, long long k_stride, long long v_stride, int B, int N,
+                          int Hq, int Hkv, int d, int rot, int max_pos, int interleaved, int expand,
+                          float eps, fa_dtype w_dtype, void* stream);
+
+/* Bytes of workspace fa_qk_norm_rope_bwd needs (8192 * d).  0 on invalid arguments. */
+size_t fa_qk_norm_rope_bwd_workspace_size(int d);
+
+/*
+ * Gradient of fa_qk_norm_rope.  With g the gradient of a rotated head, h = g rotated back, x^ =
+ * x / sqrt(mean(x^2) + eps):
+ *   grad_w = sum over tokens and heads of h x^,
+ *   grad_x = (w h - x^ mean(x^ w h)) / sqrt(mean(x^2) + eps),
+ * and with expand = 1 the gradients of a key/value head's copies are added up first (fp32).
+ *
+ *   grad_q_out, grad_k_out, grad_v_out  grad_out_dtype, shaped as q_out, k_out, v_out (fa_bwd's
+ *              outputs; grad_v_out may be NULL, with grad_v)
+ *   q, k, weights, tables, positions    as given to the forward
+ *   grad_q, grad_k, grad_v  grad_dtype [B, N, heads, d] with token strides  (device, written)
+ *   grad_q_weight, grad_k_weight  fp32 [d]  (device, written)
+ *   workspace  ws_bytes >= fa_qk_norm_rope_bwd_workspace_size(d), 256-byte aligned; its contents on
+ *              entry do not matter.
+ * Every sum is in a fixed order: results are the same from run to run.
+ * Returns FA_ERR_WORKSPACE if ws_bytes is too small (nothing launched).
+ */
+fa_status fa_qk_norm_rope_bwd(const void* grad_q_out, const void* grad_k_out, const void* grad_v_out,
+                              const void* q, const void* k, const void* q_weight,
+                              const void* k_weight, const float* cos_table, const float* sin_table,
+                              const int* positions, void* grad_q, void* grad_k, void* grad_v,
+                              float* grad_q_weight, float* grad_k_weight, void* workspace,
+                              size_t ws_bytes, long long q_stride, long long k_stride,
+                              long long grad_q_stride, long long grad_k_stride,
+                              long long grad_v_stride, int B, int N, int Hq, int Hkv, int d, int rot,
+                              int max_pos, int interleaved, int expand, float eps, fa_dtype w_dtype,
+                              fa_dtype grad_out_dtype, fa_dtype grad_dtype, void* stream);
+
+/* Nodes of a tree of drafted tokens, at most. */
+#define FA_TREE_MAX_NODES 128
+
+/*
+ * Trees of drafted tokens (fa_qk_norm_rope_append, fa_decode_tree, fa_cache_compact): sequence b
+ * has p = seqlens[b] cached tokens in cache rows 0 .. p - 1 and n = n_nodes[b] <= T drafted ones in
+ * rows p .. p + n - 1.  parents[b][t] < t is the node that node t continues, -1 the last cached
+ * token.  n_nodes = NULL: T for every sequence; parents = NULL: a chain (node t continues t - 1).
+ * A length or node count out of range (p + n above Nk_max too) is clamped, a parent that is not an
+ * earlier node is taken as -1; both are recorded as FA_ERR_INVALID_ARG in the device status word.
+ *
+ * fa_qk_norm_rope_append: fa_qk_norm_rope for the n nodes of each sequence, node t at position
+ * p + (number of its ancestors), its key and value heads written to cache row p + t.
+ *
+ *   q, k, v    bf16 [B, T, heads, d] with token strides
+ *   seqlens    int32 [B], parents int32 [B, T] or NULL, n_nodes int32 [B] or NULL  (device)
+ *   q_out      bf16 [B, Hq, T, d]           (device, written; 0 for nodes from n on)
+ *   k_cache, v_cache  bf16 [B, Hkv, Nk_max, d]  (device; rows p .. p + n - 1 written, no other)
+ *   T <= FA_TREE_MAX_NODES (else FA_ERR_UNSUPPORTED); positions past max_pos as in fa_qk_norm_rope.
+ */
+fa_status fa_qk_norm_rope_append(const void* q, const void* k, const void* v, const void* q_weight,
+                                 const void* k_weight, const float* cos_table,
+                                 const float* sin_table, const int* seqlens, const int* parents,
+                                 const int* n_nodes, void* q_out, void* k_cache, void* v_cache,
+                                 long long q_stride, long long k_stride, long long v_stride, int B,
+                                 int T, int Hq, int Hkv, int Nk_max, int d, int rot, int max_pos,
+                                 int interleaved, float eps, fa_dtype w_dtype, void* stream);
+
+/*
+ * Bytes of workspace fa_decode_tree needs on a device with `num_sms` multiprocessors: with rows =
+ * Hq / Hkv * T and r = rows, or 256 above 128 rows, fp32 partial outputs [2 num_sms, r, d] then fp32
+ * log-sum-exps [2 num_sms, r], each 256-byte aligned, whatever the batch and the lengths.  Pure host
+ * function.  0 on invalid arguments.
+ */
+size_t fa_decode_tree_workspace_size(int Hq, int Hkv, int T, int d, int num_sms);
+
+/*
+ * Decode attention for a tree of drafted tokens (above): node t of sequence b attends to the p cached
+ * tokens, to itself and to its ancestors,
+ *   o[b,h,t,:] = sum_j softmax_j(scale q[b,h,t,:] . K[b,g,j,:]) V[b,g,j,:],  g = h / (Hq / Hkv),
+ * over the visible rows j of the cache, lse the log of the sum.  With T = 1 it is
+ * fa_decode_splitkv_gqa over p + 1 cached tokens.
+ *
+ *   q          bf16 [B, Hq, T, d]          (device; fa_qk_norm_rope_append's q_out)
+ *   k_cache, v_cache  bf16 [B, Hkv, Nk_max, d]  (device; rows from p + n on are never used, whatever
+ *              they hold.  A non-finite key reaches only the rows that see it; a non-finite value of
+ *              a visible node may reach every row of its sequence.)
+ *   seqlens_k  int32 [B], parents int32 [B, T] or NULL, n_nodes int32 [B] or NULL  (device)
+ *   o          o_dtype [B, Hq, T, dv]      (device, written; 0 for nodes from n on)
+ *   lse        fp32 [B, Hq, T]             (device, written, -inf for nodes from n on; may be NULL)
+ *   workspace  ws_bytes >= fa_decode_tree_workspace_size(Hq, Hkv, T, d, <SMs of the current device>),
+ *              256-byte aligned; its contents on entry do not matter.  Calls sharing a workspace must
+ *              not overlap on the GPU.
+ *   T <= FA_TREE_MAX_NODES (else FA_ERR_UNSUPPORTED), Hq / Hkv * T <= 2^20.
+ * The result does not depend on other calls, and is the same from run to run.
+ */
+fa_status fa_decode_tree(const void* q, const void* k_cache, const void* v_cache,
+                         const int* seqlens_k, const int* parents, const int* n_nodes, void* o,
+                         float* lse, void* workspace, size_t ws_bytes, int B, int Hq, int Hkv, int T,
+                         int Nk_max, int d, int dv, float scale, fa_dtype o_dtype, void* stream);
+
+/*
+ * Moves the accepted nodes of each sequence up behind its cached tokens: for every layer, key/value
+ * head, and for keys and values, row p + accepted[b][i] goes to row p + i for i < n_accepted[b]; the
+ * rows are read before any is written, so any order (and a node named twice) is fine.  Other rows
+ * stay as they were.  seqlens_out[b] = p + n_accepted[b].
+ *
+ *   k_cache, v_cache  bf16 [L, B, Hkv, Nk_max, d]  (device; L layers' caches behind one another)
+ *   seqlens, n_accepted  int32 [B], accepted int32 [B, T]  (device; 0 <= accepted < T, 0 <= n_accepted
+ *              <= T, rows below Nk_max.  An accepted node out of range is not moved, lengths and counts
+ *              are clamped; both are recorded as FA_ERR_INVALID_ARG in the device status word.)
+ *   seqlens_out  int32 [B]  (device, written; may be NULL; must not overlap seqlens)
+ *   T <= FA_TREE_MAX_NODES (else FA_ERR_UNSUPPORTED), L * B * Hkv < 2^31.
+ */
+fa_status fa_cache_compact(void* k_cache, void* v_cache, const int* seqlens, const int* accepted,
+                           const int* n_accepted, int* seqlens_out, int L, int B, int Hkv,
+                           int Nk_max, int d, int dv, int T, void* stream);
 
 /*
  * Synchronises `stream`, then returns and clears the device status word of the current
