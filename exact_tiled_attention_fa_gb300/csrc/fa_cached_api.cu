@@ -267,7 +267,7 @@ fa_status fa_decode_tree(const void* q, const void* k_cache, const void* v_cache
     p.Nk_max = Nk_max;
     p.part_rows = part;
     p.n_qp = static_cast<int>(n_qp);
-    p.num_ctas = sms;
+    p.num_ctas = sms < fa::kTreeMaxCtas ? sms : fa::kTreeMaxCtas;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.o_dtype = o_dtype;
     p.wait_limit_ns = fa::wait_limit_ns();

@@ -171,6 +171,8 @@ cudaError_t launch_merge(const MergeParams& p, fa_dtype o_dtype, cudaStream_t st
 // Tree decode (fa_tree_kernel.cuh).  A group is a (sequence, key/value head) with its
 // rows = (Hq / Hkv) * T query rows, row = head within the group * T + node; a unit is a block of
 // part_rows of them.
+constexpr int kTreeMaxCtas = 256;  // CTAs of a call at most, and so parts of a unit
+
 struct TreeParams {
     CUtensorMap tm_q;    // bf16 [B*Hkv][rows][d], box {min(d,64), 128, 1}
     CUtensorMap tm_k;    // bf16 [B*Hkv][Nk_max][d]

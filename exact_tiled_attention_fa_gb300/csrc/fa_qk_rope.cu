@@ -11,13 +11,15 @@
 // Where key/value heads were written once per query head, g is first summed over the copies.
 // All of it is fp32; each output element is rounded once.
 //
-// What bounds it: bytes.  A row is read and written once, 16 bytes a lane; D / 8 lanes share a row,
-// so the sums are a few shuffles.  A warp takes one token and walks its heads, holding the token's
-// cosines and sines in registers, with U rows' loads in flight; neighbouring warps take neighbouring
-// tokens, whose rows are neighbours in the head-major output.
+// What bounds it: bytes.  D / 8 lanes share a row, each with four of its pairs, so the rotation stays
+// within a lane and a row's sums are a few shuffles; the arithmetic is done two elements at a time.
+// A warp takes one token and walks its heads, the token's cosines and sines, times the weights, in
+// registers, with the loads of U steps in flight; neighbouring warps take neighbouring tokens, whose
+// rows are neighbours in the head-major output.
 #include <cuda_bf16.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "fa_internal.h"
 #include "fa_kernel_common.cuh"
@@ -29,99 +31,163 @@ namespace {
 
 constexpr int kRopeWarps = 8;
 
-__device__ __forceinline__ void unpack_bf16(const uint4 u, float (&f)[8])
-{
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-}
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-__device__ __forceinline__ uint4 pack_bf16(const float (&f)[8])
-{
-    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
-}
+// A lane's four pairs of a row, a in x[0], x[1] and b in x[2], x[3].
+struct Pairs {
+    float2 x[4];
+};
 
-// Eight weights at element c.
-__device__ __forceinline__ void load_weights(const void* w, fa_dtype t, int c, float (&f)[8])
-{
-    if (t == FA_F32) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = __ldg(reinterpret_cast<const float*>(w) + c + i);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(w)[c + i]);
-    }
-}
-
-// The rotation of a lane's eight elements.  Halves: out = x c + partner s, the partner's elements
-// held by another lane of the row and s carrying the sign (-sin in the first half, +sin in the
-// second; 0, with c = 1, past rot).  Interleaved: four pairs within the lane.
+// Which elements of a row a lane holds.  Interleaved: elements 8 sub .. 8 sub + 7, the pairs side by
+// side.  Halves: elements at .. at + 3 (a) and bt .. bt + 3 (b): the lane's share of the two halves, or
+// past rot two neighbouring pieces that stay as they are.
 template <bool INTERLEAVED>
-struct Turn {
-    float c[INTERLEAVED ? 4 : 8], s[INTERLEAVED ? 4 : 8];
-    int partner;  // lane of the partner elements
-
-    __device__ __forceinline__ void load(const float* cos_t, const float* sin_t, int pos, int rot, int sub, int lane, float sign)
+struct Share {
+    int at, bt;
+    int pair;    // first pair, an index into the tables; -1 past rot
+    __device__ __forceinline__ Share(int sub, int rot)
     {
-        const int half = rot >> 1;
-        const int e = sub * 8;
-        partner = lane;
-        if constexpr (INTERLEAVED) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                c[i] = 1.f;
-                s[i] = 0.f;
-            }
-            if (e < rot) {
-                const size_t at = static_cast<size_t>(pos) * half + (e >> 1);
-                const float4 x = __ldg(reinterpret_cast<const float4*>(cos_t + at));
-                const float4 y = __ldg(reinterpret_cast<const float4*>(sin_t + at));
-                c[0] = x.x, c[1] = x.y, c[2] = x.z, c[3] = x.w;
-                s[0] = sign * y.x, s[1] = sign * y.y, s[2] = sign * y.z, s[3] = sign * y.w;
-            }
+        if (INTERLEAVED) {
+            at = 8 * sub;
+            bt = at + 4;
+            pair = at < rot ? 4 * sub : -1;
+        } else if (8 * sub < rot) {
+            at = 4 * sub;
+            bt = at + (rot >> 1);
+            pair = at;
         } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                c[i] = 1.f;
-                s[i] = 0.f;
-            }
-            if (e < rot) {
-                const bool second = e >= half;
-                const size_t at = static_cast<size_t>(pos) * half + (second ? e - half : e);
-                const float sg = second ? sign : -sign;
-                partner = second ? lane - (half >> 3) : lane + (half >> 3);
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const float4 x = __ldg(reinterpret_cast<const float4*>(cos_t + at) + q);
-                    const float4 y = __ldg(reinterpret_cast<const float4*>(sin_t + at) + q);
-                    c[4 * q] = x.x, c[4 * q + 1] = x.y, c[4 * q + 2] = x.z, c[4 * q + 3] = x.w;
-                    s[4 * q] = sg * y.x, s[4 * q + 1] = sg * y.y, s[4 * q + 2] = sg * y.z, s[4 * q + 3] = sg * y.w;
-                }
-            }
+            at = 8 * sub;
+            bt = at + 4;
+            pair = -1;
         }
     }
-    // Whole warp.
-    __device__ __forceinline__ void apply(float (&y)[8]) const
+    // Eight elements of a row of bf16, raw: two words from at, two from bt.
+    __device__ __forceinline__ uint4 load(const __nv_bfloat16* row) const
     {
-        if constexpr (INTERLEAVED) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float a = y[2 * i], b = y[2 * i + 1];
-                y[2 * i] = fmaf(a, c[i], -b * s[i]);
-                y[2 * i + 1] = fmaf(a, s[i], b * c[i]);
-            }
+        if (INTERLEAVED) return ld_stream_v4(row + at);
+        const uint2 a = ld_stream_v2(row + at), b = ld_stream_v2(row + bt);
+        return make_uint4(a.x, a.y, b.x, b.y);
+    }
+    __device__ __forceinline__ void store(__nv_bfloat16* row, uint4 u) const
+    {
+        if (INTERLEAVED) {
+            *reinterpret_cast<uint4*>(row + at) = u;
         } else {
-            float o[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = __shfl_sync(0xffffffffu, y[i], partner);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = s[i] == 0.f ? y[i] * c[i] : fmaf(y[i], c[i], o[i] * s[i]);
+            *reinterpret_cast<uint2*>(row + at) = make_uint2(u.x, u.y);
+            *reinterpret_cast<uint2*>(row + bt) = make_uint2(u.z, u.w);
         }
+    }
+    __device__ __forceinline__ Pairs unpack(uint4 u) const
+    {
+        Pairs p;
+        if (INTERLEAVED) {
+            p.x[0] = make_float2(bf16_lo(u.x), bf16_lo(u.y)), p.x[1] = make_float2(bf16_lo(u.z), bf16_lo(u.w));
+            p.x[2] = make_float2(bf16_hi(u.x), bf16_hi(u.y)), p.x[3] = make_float2(bf16_hi(u.z), bf16_hi(u.w));
+        } else {
+            p.x[0] = make_float2(bf16_lo(u.x), bf16_hi(u.x)), p.x[1] = make_float2(bf16_lo(u.y), bf16_hi(u.y));
+            p.x[2] = make_float2(bf16_lo(u.z), bf16_hi(u.z)), p.x[3] = make_float2(bf16_lo(u.w), bf16_hi(u.w));
+        }
+        return p;
+    }
+    __device__ __forceinline__ uint4 pack(const Pairs& p) const
+    {
+        if (INTERLEAVED)
+            return make_uint4(pack_bf16x2(p.x[0].x, p.x[2].x), pack_bf16x2(p.x[0].y, p.x[2].y),
+                              pack_bf16x2(p.x[1].x, p.x[3].x), pack_bf16x2(p.x[1].y, p.x[3].y));
+        return make_uint4(pack_bf16x2(p.x[0].x, p.x[0].y), pack_bf16x2(p.x[1].x, p.x[1].y),
+                          pack_bf16x2(p.x[2].x, p.x[2].y), pack_bf16x2(p.x[3].x, p.x[3].y));
+    }
+    // The same eight elements in fp32: four from at, four from bt.
+    __device__ __forceinline__ Pairs unpack32(float4 a, float4 b) const
+    {
+        Pairs p;
+        if (INTERLEAVED) {
+            p.x[0] = make_float2(a.x, a.z), p.x[1] = make_float2(b.x, b.z);
+            p.x[2] = make_float2(a.y, a.w), p.x[3] = make_float2(b.y, b.w);
+        } else {
+            p.x[0] = make_float2(a.x, a.y), p.x[1] = make_float2(a.z, a.w);
+            p.x[2] = make_float2(b.x, b.y), p.x[3] = make_float2(b.z, b.w);
+        }
+        return p;
+    }
+    __device__ __forceinline__ void store32(float* row, const Pairs& p) const
+    {
+        if (INTERLEAVED) {
+            *reinterpret_cast<float4*>(row + at) = make_float4(p.x[0].x, p.x[2].x, p.x[0].y, p.x[2].y);
+            *reinterpret_cast<float4*>(row + bt) = make_float4(p.x[1].x, p.x[3].x, p.x[1].y, p.x[3].y);
+        } else {
+            *reinterpret_cast<float4*>(row + at) = make_float4(p.x[0].x, p.x[0].y, p.x[1].x, p.x[1].y);
+            *reinterpret_cast<float4*>(row + bt) = make_float4(p.x[2].x, p.x[2].y, p.x[3].x, p.x[3].y);
+        }
+    }
+    __device__ __forceinline__ Pairs weights(const void* w, fa_dtype t) const
+    {
+        if (t == FA_F32) {
+            float f[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {  // a weight vector need only be aligned to its elements
+                f[i] = __ldg(reinterpret_cast<const float*>(w) + at + i);
+                f[4 + i] = __ldg(reinterpret_cast<const float*>(w) + bt + i);
+            }
+            return unpack32(make_float4(f[0], f[1], f[2], f[3]), make_float4(f[4], f[5], f[6], f[7]));
+        }
+        const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
+        return unpack(make_uint4(__ldg(u + at / 2), __ldg(u + at / 2 + 1), __ldg(u + bt / 2), __ldg(u + bt / 2 + 1)));
+    }
+    // Cosines and sines of the lane's pairs at position pos: c[0], c[1] and s in c[2], c[3].
+    __device__ __forceinline__ Pairs angles(const float* cos_t, const float* sin_t, int pos, int rot) const
+    {
+        Pairs p;
+        p.x[0] = p.x[1] = make_float2(1.f, 1.f);
+        p.x[2] = p.x[3] = make_float2(0.f, 0.f);
+        if (pair >= 0) {
+            const size_t i = static_cast<size_t>(pos) * (rot >> 1) + pair;
+            const float4 c = __ldg(reinterpret_cast<const float4*>(cos_t + i));
+            const float4 s = __ldg(reinterpret_cast<const float4*>(sin_t + i));
+            p.x[0] = make_float2(c.x, c.y), p.x[1] = make_float2(c.z, c.w);
+            p.x[2] = make_float2(s.x, s.y), p.x[3] = make_float2(s.z, s.w);
+        }
+        return p;
     }
 };
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 neg2(float2 a) { return make_float2(-a.x, -a.y); }
+
+// Norm weights and rotation of a lane in one: a' = r (a aa + b ab), b' = r (a ba + b bb).
+struct Turn {
+    float2 aa[2], ab[2], ba[2], bb[2];
+    __device__ __forceinline__ Turn(const Pairs& w, const Pairs& cs)
+    {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            aa[i] = mul2(w.x[i], cs.x[i]);
+            ab[i] = neg2(mul2(w.x[2 + i], cs.x[2 + i]));
+            ba[i] = mul2(w.x[i], cs.x[2 + i]);
+            bb[i] = mul2(w.x[2 + i], cs.x[i]);
+        }
+    }
+    __device__ __forceinline__ Pairs apply(const Pairs& p, float r) const
+    {
+        const float2 rr = make_float2(r, r);
+        Pairs o;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            o.x[i] = mul2(rr, fma2(p.x[i], aa[i], mul2(p.x[2 + i], ab[i])));
+            o.x[2 + i] = mul2(rr, fma2(p.x[i], ba[i], mul2(p.x[2 + i], bb[i])));
+        }
+        return o;
+    }
+};
+
+// Sum of products of a lane's elements.
+__device__ __forceinline__ float dot(const Pairs& p, const Pairs& q)
+{
+    const float2 t = __fadd2_rn(fma2(p.x[0], q.x[0], mul2(p.x[1], q.x[1])), fma2(p.x[2], q.x[2], mul2(p.x[3], q.x[3])));
+    return t.x + t.y;
+}
 
 template <int LANES>
 __device__ __forceinline__ float row_sum(float x)
@@ -161,19 +227,31 @@ __device__ __forceinline__ int tree_depth(const int* parents, int t, int lane, i
     }
 }
 
-// Grid (tokens / kRopeWarps, head chunks).  A warp: one token, heads blockIdx.y * chunk .. + chunk of
-// the Hq query heads, Hkv key heads and Hkv value heads in this order.
+// The steps of a token: RPW query heads each, then key heads, then value heads.
+template <int RPW>
+struct Steps {
+    int nq, nk, n;
+    __host__ __device__ Steps(int Hq, int Hkv, bool values)
+    {
+        nq = (Hq + RPW - 1) / RPW;
+        nk = (Hkv + RPW - 1) / RPW;
+        n = nq + nk + (values ? nk : 0);
+    }
+};
+
+// Grid (tokens / kRopeWarps, step chunks).  A warp: one token, steps blockIdx.y * chunk .. + chunk.
 // APPEND: token t of sequence b is node t of its tree, at position seqlens[b] + depth, and its key
 // and value go to cache row seqlens[b] + t.  Nodes past n_nodes[b] have zero query rows and no cache
 // row.
 template <int D, bool INTERLEAVED, bool APPEND>
-__global__ void __launch_bounds__(kRopeWarps * 32) fa_qk_rope_kernel(const RopeParams p, int heads, int chunk)
+__global__ void __launch_bounds__(kRopeWarps * 32, 3) fa_qk_rope_kernel(const RopeParams p, int chunk)
 {
     grid_dependency_wait();
     grid_launch_dependents();
     constexpr int LPR = D / 8;    // lanes of a row
     constexpr int RPW = 32 / LPR; // rows of a warp's step
     constexpr int U = 4;          // steps in flight
+    using bf16 = __nv_bfloat16;
     const int lane = threadIdx.x & 31;
     const int sub = lane % LPR;
     const int grp = lane / LPR;
@@ -181,6 +259,23 @@ __global__ void __launch_bounds__(kRopeWarps * 32) fa_qk_rope_kernel(const RopeP
     if (token >= static_cast<long long>(p.B) * p.N) return;
     const int b = static_cast<int>(token / p.N);
     const int t = static_cast<int>(token - static_cast<long long>(b) * p.N);
+    const Share<INTERLEAVED> share(sub, p.rot);
+    const Steps<RPW> steps(p.Hq, p.Hkv, p.v != nullptr);
+    const int begin = static_cast<int>(blockIdx.y) * chunk;
+    const int end = min(steps.n, begin + chunk);
+
+    // U steps' rows at once, from step i of a kind's heads; zeros where there is no head.
+    auto load = [&](uint4 (&raw)[U], const bf16* rows, int i, int to, int heads) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int h = (i + u) * RPW + grp;
+            raw[u] = i + u < to && h < heads ? share.load(rows + h * D) : make_uint4(0, 0, 0, 0);
+        }
+    };
+    // The first rows are on their way while the position is found.
+    uint4 raw[U];
+    const bf16* q = reinterpret_cast<const bf16*>(p.q) + token * p.q_stride;
+    if (begin < steps.nq) load(raw, q, begin, min(end, steps.nq), p.Hq);
 
     bool live = true;  // APPEND: the node is part of the tree
     int row = t;       // row of the key and value in their head
@@ -202,54 +297,60 @@ __global__ void __launch_bounds__(kRopeWarps * 32) fa_qk_rope_kernel(const RopeP
     } else {
         pos = checked_position(p.positions != nullptr ? p.positions[token] : t, p.max_pos, p.status);
     }
-    Turn<INTERLEAVED> turn;
-    turn.load(p.cos_t, p.sin_t, pos, p.rot, sub, lane, 1.f);
-    float wq[8], wk[8];
-    load_weights(p.wq, p.w_dtype, sub * 8, wq);
-    load_weights(p.wk, p.w_dtype, sub * 8, wk);
-    const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(p.q) + token * p.q_stride + sub * 8;
-    const __nv_bfloat16* k = reinterpret_cast<const __nv_bfloat16*>(p.k) + token * p.k_stride + sub * 8;
-    const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(p.v) + token * p.v_stride + sub * 8;
-    const size_t kv_rows = APPEND ? p.Nk_max : p.N;
-    const int h_end = min(heads, (static_cast<int>(blockIdx.y) + 1) * chunk);
-
-    for (int h0 = static_cast<int>(blockIdx.y) * chunk; h0 < h_end; h0 += U * RPW) {
-        uint4 raw[U];
+    const Pairs cs = share.angles(p.cos_t, p.sin_t, pos, p.rot);
+    auto turned = [&](const Turn& turn, uint4 u) -> uint4 {
+        const Pairs x = share.unpack(u);
+        return share.pack(turn.apply(x, rsqrtf(row_sum<LPR>(dot(x, x)) * (1.f / D) + p.eps)));
+    };
+    if (begin < steps.nq) {
+        const Turn turn(share.weights(p.wq, p.w_dtype), cs);
+        bf16* out = reinterpret_cast<bf16*>(p.q_out) + (static_cast<size_t>(b) * p.Hq * p.N + t) * D;
+        const size_t head = static_cast<size_t>(p.N) * D;
+        const int to = min(end, steps.nq);
+        for (int i = begin; i < to; i += U) {
+            if (i != begin) load(raw, q, i, to, p.Hq);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = h0 + u * RPW + grp;
-            const __nv_bfloat16* src = h < p.Hq ? q + static_cast<size_t>(h) * D
-                                     : h < p.Hq + p.Hkv ? k + static_cast<size_t>(h - p.Hq) * D
-                                                        : v + static_cast<size_t>(h - p.Hq - p.Hkv) * D;
-            raw[u] = h < h_end ? ld_stream_v4(src) : make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = h0 + u * RPW + grp;
-            if (h0 + u * RPW >= h_end) break;  // uniform
-            float x[8];
-            unpack_bf16(raw[u], x);
-            float ss = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-            const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
-            const bool is_q = h < p.Hq;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = x[i] * r * (is_q ? wq[i] : wk[i]);
-            turn.apply(x);
-            if (h < h_end && is_q) {
-                const uint4 y = APPEND && !live ? make_uint4(0, 0, 0, 0) : pack_bf16(x);
-                __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.q_out) +
-                                     ((static_cast<size_t>(b) * p.Hq + h) * p.N + t) * D + sub * 8;
-                *reinterpret_cast<uint4*>(dst) = y;
-            } else if (h < h_end && (!APPEND || live)) {
-                const bool is_k = h < p.Hq + p.Hkv;
-                const int hk = is_k ? h - p.Hq : h - p.Hq - p.Hkv;
-                const uint4 y = is_k ? pack_bf16(x) : raw[u];
-                __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(is_k ? p.k_out : p.v_out) +
-                                     ((static_cast<size_t>(b) * p.Hkv + hk) * p.copies * kv_rows + row) * D + sub * 8;
-                for (int c = 0; c < p.copies; ++c) *reinterpret_cast<uint4*>(dst + static_cast<size_t>(c) * kv_rows * D) = y;
+            for (int u = 0; u < U; ++u) {
+                if (i + u >= to) break;  // uniform
+                uint4 y = turned(turn, raw[u]);
+                if (APPEND && !live) y = make_uint4(0, 0, 0, 0);
+                const int h = (i + u) * RPW + grp;
+                if (h < p.Hq) share.store(out + h * head, y);
             }
+        }
+    }
+    if (APPEND && !live) return;  // the whole warp
+    const size_t kv_rows = APPEND ? p.Nk_max : p.N;
+    const size_t head = static_cast<size_t>(p.copies) * kv_rows * D;
+    const size_t at = static_cast<size_t>(b) * p.Hkv * head + static_cast<size_t>(row) * D;
+    auto store = [&](bf16* out, int i, uint4 y) {
+        const int h = i * RPW + grp;
+        if (h < p.Hkv)
+            for (int c = 0; c < p.copies; ++c) share.store(out + h * head + static_cast<size_t>(c) * kv_rows * D, y);
+    };
+    const int kb = max(begin, steps.nq) - steps.nq, ke = min(end, steps.nq + steps.nk) - steps.nq;
+    if (kb < ke) {
+        const Turn turn(share.weights(p.wk, p.w_dtype), cs);
+        const bf16* k = reinterpret_cast<const bf16*>(p.k) + token * p.k_stride;
+        bf16* out = reinterpret_cast<bf16*>(p.k_out) + at;
+        for (int i = kb; i < ke; i += U) {
+            load(raw, k, i, ke, p.Hkv);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (i + u >= ke) break;
+                store(out, i + u, turned(turn, raw[u]));
+            }
+        }
+    }
+    const int vb = max(begin, steps.nq + steps.nk) - steps.nq - steps.nk, ve = end - steps.nq - steps.nk;
+    if (vb < ve) {
+        const bf16* v = reinterpret_cast<const bf16*>(p.v) + token * p.v_stride;
+        bf16* out = reinterpret_cast<bf16*>(p.v_out) + at;
+        for (int i = vb; i < ve; i += U) {
+            load(raw, v, i, ve, p.Hkv);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (i + u < ve) store(out, i + u, raw[u]);
         }
     }
 }
@@ -260,138 +361,150 @@ cudaError_t launch_rope_t(const RopeParams& p, bool append, int sms, cudaStream_
     constexpr int RPW = 32 / (D / 8);
     const long long tokens = static_cast<long long>(p.B) * p.N;
     const long long blocks = (tokens + kRopeWarps - 1) / kRopeWarps;
-    const int heads = p.Hq + p.Hkv + (p.v != nullptr ? p.Hkv : 0);
-    // With few tokens the heads of one are shared out among warps, a step of RPW heads at least
-    const int steps = (heads + RPW - 1) / RPW;
+    // With few tokens the steps of one are shared out among warps
+    const int steps = Steps<RPW>(p.Hq, p.Hkv, p.v != nullptr).n;
     long long chunks = (4LL * sms + blocks - 1) / blocks;
     if (chunks > steps) chunks = steps;
-    const int chunk = static_cast<int>((steps + chunks - 1) / chunks) * RPW;
-    const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((heads + chunk - 1) / chunk));
-    return append ? launch_pdl(fa_qk_rope_kernel<D, INTERLEAVED, true>, grid, kRopeWarps * 32, 0, st, p, heads, chunk)
-                  : launch_pdl(fa_qk_rope_kernel<D, INTERLEAVED, false>, grid, kRopeWarps * 32, 0, st, p, heads, chunk);
+    const int chunk = static_cast<int>((steps + chunks - 1) / chunks);
+    const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((steps + chunk - 1) / chunk));
+    return append ? launch_pdl(fa_qk_rope_kernel<D, INTERLEAVED, true>, grid, kRopeWarps * 32, 0, st, p, chunk)
+                  : launch_pdl(fa_qk_rope_kernel<D, INTERLEAVED, false>, grid, kRopeWarps * 32, 0, st, p, chunk);
 }
 
 // ---- backward ----------------------------------------------------------------------------------
 
-// Eight gradient elements at g.
-__device__ __forceinline__ void load_grad(const void* g, bool f32, size_t at, float (&f)[8])
-{
-    if (f32) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(reinterpret_cast<const float*>(g) + at));
-        const float4 c = __ldg(reinterpret_cast<const float4*>(reinterpret_cast<const float*>(g) + at) + 1);
-        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = c.x, f[5] = c.y, f[6] = c.z, f[7] = c.w;
-    } else {
-        unpack_bf16(ld_stream_v4(reinterpret_cast<const __nv_bfloat16*>(g) + at), f);
-    }
-}
-
-__device__ __forceinline__ void store_grad(void* o, bool f32, size_t at, const float (&f)[8])
-{
-    if (f32) {
-        float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(o) + at);
-        dst[0] = make_float4(f[0], f[1], f[2], f[3]);
-        dst[1] = make_float4(f[4], f[5], f[6], f[7]);
-    } else {
-        *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(o) + at) = pack_bf16(f);
-    }
-}
-
 // A fixed number of CTAs walk the tokens, a warp a token at a time; the weights' gradients stay in
-// registers (eight columns of each a lane) until the CTA adds its warps' up in a fixed order and
+// registers (a lane's eight columns of each) until the CTA adds its warps' up in a fixed order and
 // writes one partial row of each, which fa_rope_weight_kernel adds up, also in a fixed order: the
 // result does not change from run to run.
 template <int D, bool INTERLEAVED, bool GF32>
-__global__ void __launch_bounds__(kRopeWarps * 32) fa_qk_rope_bwd_kernel(const RopeBwdParams p, int heads)
+__global__ void __launch_bounds__(kRopeWarps * 32, 2) fa_qk_rope_bwd_kernel(const RopeBwdParams p)
 {
     grid_dependency_wait();
     grid_launch_dependents();
+    using G = typename std::conditional<GF32, float, __nv_bfloat16>::type;
     constexpr int LPR = D / 8;
     constexpr int RPW = 32 / LPR;
+    constexpr int U = GF32 ? 2 : 4;  // steps in flight
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int sub = lane % LPR;
     const int grp = lane / LPR;
     const bool of32 = p.out_dtype == FA_F32;
-    float wq[8], wk[8], aq[8], ak[8];
-    load_weights(p.wq, p.w_dtype, sub * 8, wq);
-    load_weights(p.wk, p.w_dtype, sub * 8, wk);
+    const Share<INTERLEAVED> share(sub, p.rot);
+    const Pairs wq = share.weights(p.wq, p.w_dtype), wk = share.weights(p.wk, p.w_dtype);
+    Pairs aq, ak;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) aq[i] = ak[i] = 0.f;
+    for (int i = 0; i < 4; ++i) aq.x[i] = ak.x[i] = make_float2(0.f, 0.f);
     const long long tokens = static_cast<long long>(p.B) * p.N;
+    const size_t head = static_cast<size_t>(p.N) * D;  // elements of a head of the gradients
+    // raw gradient elements of a lane
+    struct Raw {
+        uint4 lo, hi;  // bf16: lo; fp32: four elements each
+    };
+    auto load_g = [&](const G* row) -> Raw {
+        Raw g;
+        if constexpr (GF32) {
+            g.lo = ld_stream_v4(row + share.at);
+            g.hi = ld_stream_v4(row + share.bt);
+        } else {
+            g.lo = share.load(row);
+        }
+        return g;
+    };
+    auto unpack_g = [&](const Raw& g) -> Pairs {
+        if constexpr (GF32)
+            return share.unpack32(make_float4(__uint_as_float(g.lo.x), __uint_as_float(g.lo.y), __uint_as_float(g.lo.z), __uint_as_float(g.lo.w)),
+                                  make_float4(__uint_as_float(g.hi.x), __uint_as_float(g.hi.y), __uint_as_float(g.hi.z), __uint_as_float(g.hi.w)));
+        else
+            return share.unpack(g.lo);
+    };
     for (long long token = static_cast<long long>(blockIdx.x) * kRopeWarps + warp; token < tokens;
          token += static_cast<long long>(gridDim.x) * kRopeWarps) {
         const int b = static_cast<int>(token / p.N);
         const int t = static_cast<int>(token - static_cast<long long>(b) * p.N);
         const int pos = checked_position(p.positions != nullptr ? p.positions[token] : t, p.max_pos, p.status);
-        Turn<INTERLEAVED> turn;
-        turn.load(p.cos_t, p.sin_t, pos, p.rot, sub, lane, -1.f);
-        const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(p.q) + token * p.q_stride + sub * 8;
-        const __nv_bfloat16* k = reinterpret_cast<const __nv_bfloat16*>(p.k) + token * p.k_stride + sub * 8;
-        for (int h0 = 0; h0 < heads; h0 += RPW) {
-            const int h = h0 + grp;
-            const bool in = h < heads;
-            const bool is_q = h < p.Hq;
-            const bool is_v = h >= p.Hq + p.Hkv;
-            const int hk = is_v ? h - p.Hq - p.Hkv : h - p.Hq;
-            float x[8], g[8];
+        const Pairs cs = share.angles(p.cos_t, p.sin_t, pos, p.rot);
+        // The steps of one kind of heads.  x: the projections' rows (nullptr for values), gi: the
+        // gradients' rows, `copies` for each head, go: the rows written.
+        auto walk = [&](const __nv_bfloat16* xi, const G* gi, void* go, int heads, int copies, const Pairs& w, Pairs& acc) {
+            const int n = (heads + RPW - 1) / RPW;
+            for (int i = 0; i < n; i += U) {
+                uint4 xr[U];
+                Raw gr[U];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = g[i] = 0.f;
-            if (in) {
-                if (!is_v) unpack_bf16(ld_stream_v4(is_q ? q + static_cast<size_t>(h) * D : k + static_cast<size_t>(hk) * D), x);
-                const void* src = is_q ? p.dq : is_v ? p.dv : p.dk;
-                const int n = is_q ? 1 : p.copies;
-                const size_t head0 = is_q ? static_cast<size_t>(b) * p.Hq + h : (static_cast<size_t>(b) * p.Hkv + hk) * p.copies;
-                for (int c = 0; c < n; ++c) {
-                    float y[8];
-                    load_grad(src, GF32, ((head0 + c) * p.N + t) * D + sub * 8, y);
+                for (int u = 0; u < U; ++u) {
+                    const int h = (i + u) * RPW + grp;
+                    xr[u] = gr[u].lo = gr[u].hi = make_uint4(0, 0, 0, 0);
+                    if (i + u < n && h < heads) {
+                        if (xi != nullptr) xr[u] = share.load(xi + h * D);
+                        gr[u] = load_g(gi + static_cast<size_t>(h) * copies * head);
+                    }
+                }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) g[i] += y[i];
+                for (int u = 0; u < U; ++u) {
+                    if (i + u >= n) break;  // uniform
+                    const int h = (i + u) * RPW + grp;
+                    Pairs g = unpack_g(gr[u]);
+                    if (copies > 1 && h < heads) {
+#pragma unroll 4
+                        for (int c = 1; c < copies; ++c) {
+                            const Pairs y = unpack_g(load_g(gi + (static_cast<size_t>(h) * copies + c) * head));
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) g.x[e] = __fadd2_rn(g.x[e], y.x[e]);
+                        }
+                    }
+                    if (xi != nullptr) {
+                        const Pairs x = share.unpack(xr[u]);
+                        Pairs hb, z;  // the gradient turned back, and times the weights
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            hb.x[e] = fma2(g.x[e], cs.x[e], mul2(g.x[2 + e], cs.x[2 + e]));
+                            hb.x[2 + e] = fma2(g.x[2 + e], cs.x[e], neg2(mul2(g.x[e], cs.x[2 + e])));
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) z.x[e] = mul2(w.x[e], hb.x[e]);
+                        const float ss = row_sum<LPR>(dot(x, x));
+                        const float sz = row_sum<LPR>(dot(x, z));
+                        const float r = rsqrtf(ss * (1.f / D) + p.eps);
+                        const float f = -(r * r) * sz * (1.f / D);
+                        const float2 rr = make_float2(r, r), ff = make_float2(f, f);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            // 0 for lanes without a row
+                            acc.x[e] = fma2(hb.x[e], mul2(x.x[e], rr), acc.x[e]);
+                            g.x[e] = mul2(rr, fma2(x.x[e], ff, z.x[e]));
+                        }
+                    }
+                    if (h < heads) {
+                        if (of32) share.store32(reinterpret_cast<float*>(go) + h * D, g);
+                        else share.store(reinterpret_cast<__nv_bfloat16*>(go) + h * D, share.pack(g));
+                    }
                 }
             }
-            float plain[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) plain[i] = g[i];
-            turn.apply(g);
-            float ss = 0.f, sz = 0.f, z[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                z[i] = (is_q ? wq[i] : wk[i]) * g[i];
-                ss = fmaf(x[i], x[i], ss);
-                sz = fmaf(x[i], z[i], sz);
-            }
-            ss = row_sum<LPR>(ss);
-            sz = row_sum<LPR>(sz);
-            const float r = rsqrtf(ss * (1.f / D) + p.eps);
-            const float f = r * r * sz * (1.f / D);
-            float o[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float dw = g[i] * x[i] * r;  // 0 for value rows and lanes without a row (x = 0)
-                aq[i] += is_q ? dw : 0.f;
-                ak[i] += is_q ? 0.f : dw;
-                o[i] = is_v ? plain[i] : r * (z[i] - x[i] * f);
-            }
-            if (in) {
-                void* dst = is_q ? p.gq : is_v ? p.gv : p.gk;
-                const long long stride = is_q ? p.gq_stride : is_v ? p.gv_stride : p.gk_stride;
-                store_grad(dst, of32, static_cast<size_t>(token * stride) + static_cast<size_t>(is_q ? h : hk) * D + sub * 8, o);
-            }
-        }
+        };
+        auto out = [&](void* o, long long stride) -> void* { return static_cast<char*>(o) + token * stride * (of32 ? 4 : 2); };
+        const size_t row = static_cast<size_t>(t) * D;
+        const size_t kv = static_cast<size_t>(b) * p.Hkv * p.copies * head + row;
+        walk(reinterpret_cast<const __nv_bfloat16*>(p.q) + token * p.q_stride,
+             reinterpret_cast<const G*>(p.dq) + static_cast<size_t>(b) * p.Hq * head + row, out(p.gq, p.gq_stride), p.Hq, 1, wq, aq);
+        walk(reinterpret_cast<const __nv_bfloat16*>(p.k) + token * p.k_stride, reinterpret_cast<const G*>(p.dk) + kv,
+             out(p.gk, p.gk_stride), p.Hkv, p.copies, wk, ak);
+        if (p.dv != nullptr) walk(nullptr, reinterpret_cast<const G*>(p.dv) + kv, out(p.gv, p.gv_stride), p.Hkv, p.copies, wk, ak);
     }
-    __shared__ float sm[kRopeWarps][2][D];
+    __shared__ __align__(16) float sm[kRopeWarps][2][D];
 #pragma unroll
     for (int o = LPR; o < 32; o <<= 1)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            aq[i] += __shfl_xor_sync(0xffffffffu, aq[i], o);
-            ak[i] += __shfl_xor_sync(0xffffffffu, ak[i], o);
+        for (int i = 0; i < 4; ++i) {
+            aq.x[i].x += __shfl_xor_sync(0xffffffffu, aq.x[i].x, o);
+            aq.x[i].y += __shfl_xor_sync(0xffffffffu, aq.x[i].y, o);
+            ak.x[i].x += __shfl_xor_sync(0xffffffffu, ak.x[i].x, o);
+            ak.x[i].y += __shfl_xor_sync(0xffffffffu, ak.x[i].y, o);
         }
     if (grp == 0) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            sm[warp][0][sub * 8 + i] = aq[i];
-            sm[warp][1][sub * 8 + i] = ak[i];
-        }
+        share.store32(sm[warp][0], aq);
+        share.store32(sm[warp][1], ak);
     }
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * D; i += kRopeWarps * 32) {
@@ -427,14 +540,13 @@ template <int D, bool INTERLEAVED>
 cudaError_t launch_rope_bwd_t(const RopeBwdParams& p, int sms, cudaStream_t st)
 {
     const long long tokens = static_cast<long long>(p.B) * p.N;
-    const int heads = p.Hq + p.Hkv + (p.dv != nullptr ? p.Hkv : 0);
     long long grid = (tokens + kRopeWarps - 1) / kRopeWarps;
     const long long most = 4LL * sms < kRopeBwdCtas ? 4LL * sms : kRopeBwdCtas;
     if (grid > most) grid = most;
     const unsigned g = static_cast<unsigned>(grid);
     cudaError_t e = p.g_dtype == FA_F32
-                        ? launch_pdl(fa_qk_rope_bwd_kernel<D, INTERLEAVED, true>, g, kRopeWarps * 32, 0, st, p, heads)
-                        : launch_pdl(fa_qk_rope_bwd_kernel<D, INTERLEAVED, false>, g, kRopeWarps * 32, 0, st, p, heads);
+                        ? launch_pdl(fa_qk_rope_bwd_kernel<D, INTERLEAVED, true>, g, kRopeWarps * 32, 0, st, p)
+                        : launch_pdl(fa_qk_rope_bwd_kernel<D, INTERLEAVED, false>, g, kRopeWarps * 32, 0, st, p);
     if (e != cudaSuccess) return e;
     return launch_pdl(fa_rope_weight_kernel, dim3(D / 32, 2), 1024, 0, st, static_cast<const float*>(p.part),
                       static_cast<int>(grid), D, p.gwq, p.gwk);

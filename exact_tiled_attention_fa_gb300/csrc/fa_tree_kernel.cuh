@@ -809,7 +809,9 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
 
 // Joins the parts of the units that several CTAs share: lse = log sum_s exp(lse_s),
 // o = sum_s exp(lse_s - lse) o_s ("flash_lab.py" section 4).  Block (u, y) serves unit u, rows
-// 32 y .. 32 y + 31, a warp four rows.  The part of the unit's first CTA is that CTA's last
+// 8 y .. 8 y + 7, a warp a row: with few units there are many parts to a row, and the time is the
+// latency of the parts' loads, so all log-sum-exps are read at once and the outputs eight at a time.
+// The part of the unit's first CTA is that CTA's last
 // segment unless its share begins with the unit; the parts of the others are their first segments.
 template <int D>
 __global__ void __launch_bounds__(256) fa_tree_merge_kernel(const __grid_constant__ TreeParams p)
@@ -845,58 +847,62 @@ __global__ void __launch_bounds__(256) fa_tree_merge_kernel(const __grid_constan
     const int n = c1 - c0 + 1;
     const bool head = share_begin(c0, total, ctas) == w;
     constexpr int V = D / 32;  // columns of a lane
-    for (int q = 0; q < 4; ++q) {
-        const int r = static_cast<int>(blockIdx.y) * 32 + warp * 4 + q;
-        if (r >= rows) return;
-        auto at = [&](int s) -> size_t {
-            return static_cast<size_t>(part_slot(c0 + s, s > 0 || head)) * p.part_rows + static_cast<size_t>(r);
-        };
-        float M = -INFINITY;
-        bool live = false;
-        for (int s = lane; s < n; s += 32) {
-            const float x = __ldg(p.lse_part + at(s));
-            live = live || x != -INFINITY;
-            M = fmaxf(M, x);
-        }
-        live = __any_sync(0xffffffffu, live);
+    const int r = static_cast<int>(blockIdx.y) * 8 + warp;
+    if (r >= rows) return;
+    auto at = [&](int s) -> size_t {
+        return static_cast<size_t>(part_slot(c0 + s, s > 0 || head)) * p.part_rows + static_cast<size_t>(r);
+    };
+    constexpr int kHeld = kTreeMaxCtas / 32;  // log-sum-exps a lane holds: at most a part for each CTA
+    float x[kHeld];
+    float M = -INFINITY;
+    bool live = false;
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        float sum = 0.f;
-        for (int s = lane; s < n; s += 32) {
-            const float x = __ldg(p.lse_part + at(s));
-            if (x != -INFINITY) sum += ex2((x - M) * 1.4426950408889634f);
-        }
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const float L = live ? M + log2f(sum) * 0.69314718055994531f : -INFINITY;
-        float acc[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] = 0.f;
-        if (live) {
-#pragma unroll 4
-            for (int s = 0; s < n; ++s) {
-                const size_t row = at(s);
-                const float x = __ldg(p.lse_part + row);  // the same for the whole warp
-                const float f = x == -INFINITY ? 0.f : ex2((x - L) * 1.4426950408889634f);
-                const float* src = p.o_part + row * D + lane * V;
-                float v[V];
-                if constexpr (V == 4) *reinterpret_cast<float4*>(v) = __ldg(reinterpret_cast<const float4*>(src));
-                else if constexpr (V == 2) *reinterpret_cast<float2*>(v) = __ldg(reinterpret_cast<const float2*>(src));
-                else v[0] = __ldg(src);
-#pragma unroll
-                for (int e = 0; e < V; ++e) acc[e] = fmaf(f, v[e], acc[e]);
-            }
-        }
-        const size_t out = (static_cast<size_t>(b) * p.Hkv + kvh) * p.rows + row_base + r;
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            if (p.o_dtype == FA_F32)
-                reinterpret_cast<float*>(p.o)[out * D + lane * V + e] = acc[e];
-            else
-                reinterpret_cast<__nv_bfloat16*>(p.o)[out * D + lane * V + e] = __float2bfloat16_rn(acc[e]);
-        }
-        if (lane == 0 && p.lse != nullptr) p.lse[out] = L;
+    for (int i = 0; i < kHeld; ++i) {
+        const int s = 32 * i + lane;
+        x[i] = s < n ? __ldg(p.lse_part + at(s)) : -INFINITY;
+        live = live || x[i] != -INFINITY;
+        M = fmaxf(M, x[i]);
     }
+    live = __any_sync(0xffffffffu, live);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        x[i] = x[i] == -INFINITY ? 0.f : ex2((x[i] - M) * 1.4426950408889634f);
+        sum += x[i];
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float L = live ? M + log2f(sum) * 0.69314718055994531f : -INFINITY;
+    const float inv = live ? 1.f / sum : 0.f;
+    float acc[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        const int m = min(32, n - 32 * i);
+#pragma unroll 8
+        for (int j = 0; j < m; ++j) {
+            const float f = __shfl_sync(0xffffffffu, x[i], j) * inv;  // an empty part's output is 0
+            const float* src = p.o_part + at(32 * i + j) * D + lane * V;
+            float v[V];
+            if constexpr (V == 4) *reinterpret_cast<float4*>(v) = __ldg(reinterpret_cast<const float4*>(src));
+            else if constexpr (V == 2) *reinterpret_cast<float2*>(v) = __ldg(reinterpret_cast<const float2*>(src));
+            else v[0] = __ldg(src);
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc[e] = fmaf(f, v[e], acc[e]);
+        }
+    }
+            const size_t out = (static_cast<size_t>(b) * p.Hkv + kvh) * p.rows + row_base + r;
+    #pragma unroll
+            for (int e = 0; e < V; ++e) {
+                if (p.o_dtype == FA_F32)
+                    reinterpret_cast<float*>(p.o)[out * D + lane * V + e] = acc[e];
+                else
+                    reinterpret_cast<__nv_bfloat16*>(p.o)[out * D + lane * V + e] = __float2bfloat16_rn(acc[e]);
+            }
+    if (lane == 0 && p.lse != nullptr) p.lse[out] = L;
 }
 
 template <int D, bool PAIR>
@@ -922,7 +928,7 @@ cudaError_t launch_tree_t(const TreeParams& p, cudaStream_t st)
     }
     e = launch_pdl(kern, dim3(static_cast<unsigned>(p.num_ctas)), kTrThreads, C::kSmemBytes, st, p);
     if (e != cudaSuccess) return e;
-    const dim3 grid(static_cast<unsigned>(p.B) * p.Hkv * p.n_qp, static_cast<unsigned>((p.part_rows + 31) / 32));
+    const dim3 grid(static_cast<unsigned>(p.B) * p.Hkv * p.n_qp, static_cast<unsigned>((p.part_rows + 7) / 8));
     return launch_pdl(fa_tree_merge_kernel<D>, grid, 256, 0, st, p);
 }
 

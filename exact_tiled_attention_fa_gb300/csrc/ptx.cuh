@@ -487,4 +487,12 @@ __device__ __forceinline__ uint4 ld_stream_v4(const void* p)
     return r;
 }
 
+// The same for 8 bytes.
+__device__ __forceinline__ uint2 ld_stream_v2(const void* p)
+{
+    uint2 r;
+    asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+    return r;
+}
+
 }  // namespace fa
