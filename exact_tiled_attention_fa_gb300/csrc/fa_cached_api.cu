@@ -220,7 +220,8 @@ size_t fa_decode_tree_workspace_size(int Hq, int Hkv, int T, int d, int num_sms)
     const long long rows = static_cast<long long>(Hq / Hkv) * T;
     const size_t part = rows > fa::kBlockM ? 2 * fa::kBlockM : static_cast<size_t>(rows);
     const size_t slots = 2 * static_cast<size_t>(num_sms) * part;
-    return round_up(slots * d * sizeof(float), kAlign) + round_up(slots * sizeof(float), kAlign);
+    return round_up(slots * d * sizeof(float), kAlign) + round_up(slots * sizeof(float), kAlign) +
+           round_up(static_cast<size_t>(num_sms) * sizeof(fa::TreeJoin), kAlign);
 }
 
 fa_status fa_decode_tree(const void* q, const void* k_cache, const void* v_cache, const int* seqlens_k, const int* parents,
@@ -258,8 +259,10 @@ fa_status fa_decode_tree(const void* q, const void* k_cache, const void* v_cache
     p.o = o;
     p.lse = lse;
     p.o_part = static_cast<float*>(workspace);
-    p.lse_part = reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                          round_up(2 * static_cast<size_t>(sms) * part * d * sizeof(float), kAlign));
+    const size_t slots = 2 * static_cast<size_t>(sms) * part;
+    char* at = static_cast<char*>(workspace) + round_up(slots * d * sizeof(float), kAlign);
+    p.lse_part = reinterpret_cast<float*>(at);
+    p.joins = reinterpret_cast<fa::TreeJoin*>(at + round_up(slots * sizeof(float), kAlign));
     p.B = B;
     p.Hkv = Hkv;
     p.rows = static_cast<int>(rows);

@@ -173,6 +173,12 @@ cudaError_t launch_merge(const MergeParams& p, fa_dtype o_dtype, cudaStream_t st
 // part_rows of them.
 constexpr int kTreeMaxCtas = 256;  // CTAs of a call at most, and so parts of a unit
 
+// What the merge has to join: the unit that a CTA began and did not finish.
+struct TreeJoin {
+    long long first_row;  // in the output
+    int rows, parts;      // parts = 0: none
+};
+
 struct TreeParams {
     CUtensorMap tm_q;    // bf16 [B*Hkv][rows][d], box {min(d,64), 128, 1}
     CUtensorMap tm_k;    // bf16 [B*Hkv][Nk_max][d]
@@ -184,6 +190,7 @@ struct TreeParams {
     float* lse;          // [B*Hkv][rows] or nullptr
     float* o_part;       // fp32 [2 * num_ctas][part_rows][d]
     float* lse_part;     // fp32 [2 * num_ctas][part_rows]
+    TreeJoin* joins;     // [num_ctas]
     int* status;
     int B, Hkv, rows, T, Nk_max;
     int part_rows;       // min(rows, 128), or 256 for more than 128 rows (PAIR form)

@@ -14,7 +14,7 @@
 // Work division.  A unit is a group's block of up to 128 query rows (256 in PAIR form); it has
 // ceil((p + n) / 128) key tiles.  The tiles of all units, in order, are cut into as many equal
 // shares as there are CTAs (one per SM), from lengths that only the device knows: each CTA scans
-// the lengths once.  A share crosses unit borders, and the rings of K and V tiles run on across
+// the lengths once (a unit's start and end count as kUnitCost tiles).  A share crosses unit borders, and the rings of K and V tiles run on across
 // them, so a CTA pays its start-up once, however short the caches are.  A unit that lies in one
 // CTA's share is finished there; the parts of the others go to at most two slots per CTA (the
 // share's first and last unit) and fa_tree_merge_kernel joins them.  The slots are thus bounded by
@@ -76,8 +76,22 @@ enum : int {
     kTbKEmpty = 24,
     kTbVFull = 28,    // + V stage (up to 4)
     kTbVEmpty = 32,
-    kTbCount = 36
+    kTbSegFull = 36,  // + segment mod kTrSegs: the segment's record is in shared memory
+    kTbCount = 44
 };
+
+// A segment as the producer hands it to the other roles: a run of key tiles of one unit.
+struct TreeSeg {
+    int n;              // tiles; 0: the share is done
+    int tile;           // the first one
+    int prefix, nodes;  // of the sequence
+    int b, group, qp;
+    int slot;           // of its part; -1: the unit is whole
+};
+// Records in flight.  The producer is at most two segments ahead of the scores (two query buffers),
+// and those at most three ahead of a softmax warpgroup (one it has just finished, one whose tiles
+// are all the other's, one whose scores are there): 8 never overwrite a record in use.
+constexpr int kTrSegs = 8;
 
 template <int D>
 struct TrCfg {
@@ -98,9 +112,11 @@ struct TrCfg {
     static constexpr int kOffK = 2 * kTileBytes;
     static constexpr int kOffV = kOffK + kStages * kTileBytes;
     static constexpr int kOffML = kOffV + kStages * kTileBytes;  // [2 warpgroups][128] (max, sum)
-    static constexpr int kOffBar = kOffML + 2 * kBlockM * 8;
+    static constexpr int kOffStage = kOffML + 2 * kBlockM * 8;  // [8 warps][32 rows of 64 bytes]: rows on their way out
+    static constexpr int kOffSeg = kOffStage + 8 * 2048;
+    static constexpr int kOffBar = kOffSeg + kTrSegs * static_cast<int>(sizeof(TreeSeg));
     static constexpr int kOffStart = kOffBar + kTbCount * 8;
-    static constexpr int kUsedBytes = kOffStart + 48;
+    static constexpr int kUsedBytes = kOffStart + 80;
     // At least 120 KB, so that no second CTA (which would wait for the 512 TMEM columns) shares the SM.
     static constexpr int kSmemBytes = kUsedBytes + 1024 > 120 * 1024 ? kUsedBytes + 1024 : 120 * 1024;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
@@ -128,11 +144,9 @@ struct TreeLen {
     }
 };
 
-__device__ __forceinline__ TreeLen tree_len(const int* seqlens, const int* n_nodes, int b, int T, int Nk_max, int* status)
+__device__ __forceinline__ TreeLen tree_clamp(int prefix, int nodes, int T, int Nk_max, int* status)
 {
-    TreeLen x;
-    x.prefix = seqlens[b];
-    x.nodes = n_nodes != nullptr ? n_nodes[b] : T;
+    TreeLen x{prefix, nodes};
     const bool bad = x.prefix < 0 || x.prefix > Nk_max || x.nodes < 0 || x.nodes > T || x.prefix > Nk_max - x.nodes;
     if (bad) {
         atomicCAS(status, 0, FA_ERR_INVALID_ARG);
@@ -142,39 +156,54 @@ __device__ __forceinline__ TreeLen tree_len(const int* seqlens, const int* n_nod
     return x;
 }
 
-// The share of CTA c: tiles [w0, w1) of all units in order, and the unit and tile it starts in.
+__device__ __forceinline__ TreeLen tree_len(const int* seqlens, const int* n_nodes, int b, int T, int Nk_max, int* status)
+{
+    return tree_clamp(seqlens[b], n_nodes != nullptr ? n_nodes[b] : T, T, Nk_max, status);
+}
+
+// A unit counts for its tiles and kUnitCost more, about what its start and end cost a CTA in tiles
+// (see fa_tree_kernel): they take the places before its tiles.  Without them a CTA whose share was
+// made of short units finished last.
+constexpr int kUnitCost = 3;
+
+// The share of CTA c: places [w0, w1) of all units in order, and the unit and place it starts in.
 struct TreeStart {
     long long w0, w1;
-    int b, unit, tile;  // sequence, unit within the sequence, tile within the unit
+    long long total, ctas;
+    int b, unit, at;    // sequence, unit within the sequence, place within the unit
+    int prefix, nodes;  // of the sequence
 };
 
 __device__ __forceinline__ long long share_begin(long long c, long long total, long long ctas) { return c * total / ctas; }
 
-// Sum of the sequences' tile counts by one warp.
-__device__ __forceinline__ long long tree_total(const TreeParams& p, int lane)
+__device__ __forceinline__ TreeLen tree_at(const TreeParams& p, int b)
 {
-    long long sum = 0;
-    for (int b = lane; b < p.B; b += 32) sum += tree_len(p.seqlens, p.n_nodes, b, p.T, p.Nk_max, p.status).tiles();
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    return sum;
+    return tree_len(p.seqlens, p.n_nodes, b, p.T, p.Nk_max, p.status);
 }
+__device__ __forceinline__ int tree_places(const TreeParams& p, int b) { return tree_at(p, b).tiles() + kUnitCost; }
 
-// By one warp; every lane returns the same.  Empty (w0 = w1) for CTAs past the number of tiles.
+// By one warp; every lane returns the same.  Empty (w0 = w1) for CTAs past the number of places.
 __device__ __forceinline__ TreeStart tree_locate(const TreeParams& p, int c, int lane)
 {
     const long long upb = static_cast<long long>(p.Hkv) * p.n_qp;
-    const long long total = tree_total(p, lane) * upb;
+    TreeLen len{0, 0};  // the first 32 sequences'
+    if (lane < p.B) len = tree_at(p, lane);
+    long long total = lane < p.B ? len.tiles() + kUnitCost : 0;
+    for (int b = 32 + lane; b < p.B; b += 32) total += tree_places(p, b);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    total *= upb;
     const long long ctas = p.num_ctas < total ? p.num_ctas : total;
-    TreeStart s{0, 0, 0, 0, 0};
+    TreeStart s{0, 0, total, ctas, 0, 0, 0, 0, 0};
     if (c >= ctas) return s;
     s.w0 = share_begin(c, total, ctas);
     s.w1 = share_begin(c + 1, total, ctas);
     long long base = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
         const int b = b0 + lane;
-        const int tiles = b < p.B ? tree_len(p.seqlens, p.n_nodes, b, p.T, p.Nk_max, p.status).tiles() : 0;
-        long long incl = tiles * upb;
+        if (b0 > 0 && b < p.B) len = tree_at(p, b);
+        const int places = b < p.B ? len.tiles() + kUnitCost : 0;
+        long long incl = places * upb;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long x = __shfl_up_sync(0xffffffffu, incl, o);
@@ -183,11 +212,13 @@ __device__ __forceinline__ TreeStart tree_locate(const TreeParams& p, int c, int
         const unsigned past = __ballot_sync(0xffffffffu, base + incl > s.w0);
         if (past != 0u) {
             const int j = __ffs(past) - 1;  // the first sequence that ends after w0
-            const int tj = __shfl_sync(0xffffffffu, tiles, j);
-            const long long at = s.w0 - (base + __shfl_sync(0xffffffffu, incl, j) - tj * upb);
+            const int pj = __shfl_sync(0xffffffffu, places, j);
+            const long long in = s.w0 - (base + __shfl_sync(0xffffffffu, incl, j) - pj * upb);
             s.b = b0 + j;
-            s.unit = static_cast<int>(at / tj);
-            s.tile = static_cast<int>(at - static_cast<long long>(s.unit) * tj);
+            s.unit = static_cast<int>(in / pj);
+            s.at = static_cast<int>(in - static_cast<long long>(s.unit) * pj);
+            s.prefix = __shfl_sync(0xffffffffu, len.prefix, j);
+            s.nodes = __shfl_sync(0xffffffffu, len.nodes, j);
             return s;
         }
         base += __shfl_sync(0xffffffffu, incl, 31);
@@ -196,72 +227,97 @@ __device__ __forceinline__ TreeStart tree_locate(const TreeParams& p, int c, int
     return s;
 }
 
-// A CTA's share, segment by segment: a segment is a run of tiles of one unit.
+// A CTA's share, segment by segment (the producer's).
 struct TreeWalk {
-    int left;            // tiles of the share not walked yet, this segment's included
+    int left;            // places of the share from this segment on
+    int used;            // places of this segment
     int b, kvh, qp;      // sequence, key/value head, query block
     int tile, tiles, n;  // first tile of the segment, tiles of the unit, tiles of the segment
     TreeLen len;
-    bool first;          // the share's first segment
-    __device__ __forceinline__ void load(const TreeParams& p) { len = tree_len(p.seqlens, p.n_nodes, b, p.T, p.Nk_max, p.status); }
+    int next_len, next_nodes;  // of sequence b + 1, read one sequence ahead
+
     __device__ __forceinline__ void begin(const TreeParams& p, const TreeStart& s)
     {
         left = static_cast<int>(s.w1 - s.w0);
-        first = true;
+        b = kvh = qp = tile = tiles = n = 0;
+        len = TreeLen{0, 0};
         if (left == 0) return;
         b = s.b;
         kvh = s.unit / p.n_qp;
         qp = s.unit - kvh * p.n_qp;
-        tile = s.tile;
-        load(p);
+        len = TreeLen{s.prefix, s.nodes};
         tiles = len.tiles();
-        n = min(tiles - tile, left);
+        ahead(p);
+        take(p, s.at);
     }
     __device__ __forceinline__ bool live() const { return left > 0; }
     __device__ __forceinline__ void next(const TreeParams& p)
     {
-        left -= n;
-        first = false;
+        left -= used;
         if (left == 0) return;
-        tile = 0;
-        if (++qp == p.n_qp) {
-            qp = 0;
-            if (++kvh == p.Hkv) {
-                kvh = 0;
-                ++b;
-                load(p);
-                tiles = len.tiles();
-            }
-        }
-        n = min(tiles, left);
+        step(p);
+        take(p, 0);
+    }
+    // the segment at place `at` of the current unit; left = 0 if nothing but a unit's first places is left
+    __device__ __forceinline__ void take(const TreeParams& p, int at)
+    {
+        used = min(tiles + kUnitCost - at, left);
+        tile = max(at - kUnitCost, 0);
+        n = at + used - kUnitCost - tile;
+        if (n <= 0) left = 0;  // the share ends in the unit's first places: its tiles are the next CTA's
+    }
+    __device__ __forceinline__ void step(const TreeParams& p)
+    {
+        if (++qp < p.n_qp) return;
+        qp = 0;
+        if (++kvh < p.Hkv) return;
+        kvh = 0;
+        ++b;
+        len = tree_clamp(next_len, next_nodes, p.T, p.Nk_max, p.status);
+        tiles = len.tiles();
+        ahead(p);
+    }
+    __device__ __forceinline__ void ahead(const TreeParams& p)
+    {
+        const int i = min(b + 1, p.B - 1);
+        next_len = p.seqlens[i];
+        next_nodes = p.n_nodes != nullptr ? p.n_nodes[i] : p.T;
     }
     __device__ __forceinline__ int group(const TreeParams& p) const { return b * p.Hkv + kvh; }
-    __device__ __forceinline__ bool whole() const { return n == tiles; }
+    // Slot of a part: of the units that a share holds without finishing them alone, one was begun by
+    // the CTA before (it is the share's first) and one is begun here (its last).
+    __device__ __forceinline__ int slot() const
+    {
+        return n == tiles ? -1 : 2 * static_cast<int>(blockIdx.x) + (tile == 0 ? 1 : 0);
+    }
 };
 
-// The slot of a part: a CTA's share holds at most two units that it does not finish alone, the one
-// that it starts in (slot 2c) and the one that it ends in (2c + 1, or 2c when they are the same).
-__device__ __forceinline__ int part_slot(int cta, bool first) { return 2 * cta + (first ? 0 : 1); }
-
-// Ancestors of node t (and t) as 128 bits.
-__device__ __forceinline__ void tree_ancestors(const int* parents, int t, int* status, uint32_t (&vis)[4])
+// Ancestors of each lane's node t (and t itself) as 128 bits; t < 0: none.  Whole warp: it holds the
+// parents, so that a step up is a shuffle instead of a load that waits for the one before it (with
+// loads a unit's start took about 3 us).
+__device__ __forceinline__ void tree_ancestors(const int* parents, int T, int t, int lane, int* status, uint32_t (&vis)[4])
 {
 #pragma unroll
-    for (int w = 0; w < 4; ++w) vis[w] = 0u;
-    if (parents == nullptr) {  // a chain: node t sees nodes 0 .. t
+    for (int w = 0; w < 4; ++w) {
+        const int bits = min(max(t + 1 - 32 * w, 0), 32);
+        vis[w] = parents != nullptr ? 0u : bits == 32 ? 0xffffffffu : (1u << bits) - 1u;  // a chain: nodes 0 .. t
+    }
+    if (parents == nullptr) return;
+    int par[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) par[i] = 32 * i + lane < T ? __ldg(parents + 32 * i + lane) : -1;
+    int cur = t;
+    while (__any_sync(0xffffffffu, cur >= 0)) {  // strictly decreasing: at most T steps
+        int up = -1;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-            const int bits = min(max(t + 1 - 32 * w, 0), 32);
-            vis[w] = bits == 32 ? 0xffffffffu : (1u << bits) - 1u;
+            const int x = __shfl_sync(0xffffffffu, par[w], cur & 31);
+            if (cur >> 5 == w) {
+                vis[w] |= 1u << (cur & 31);
+                up = x;
+            }
         }
-        return;
-    }
-    int cur = t;
-    while (cur >= 0) {  // strictly decreasing: at most T steps
-#pragma unroll
-        for (int w = 0; w < 4; ++w) vis[w] |= (cur >> 5) == w ? 1u << (cur & 31) : 0u;
-        int up = __ldg(parents + cur);
-        if (up >= cur || up < -1) {  // not a node before it: taken as a child of the last cached token
+        if (cur >= 0 && (up >= cur || up < -1)) {  // not a node before it: taken as a child of the last cached token
             atomicCAS(status, 0, FA_ERR_INVALID_ARG);
             up = -1;
         }
@@ -271,22 +327,53 @@ __device__ __forceinline__ void tree_ancestors(const int* parents, int t, int* s
 
 // ---- kernel ------------------------------------------------------------------------------------
 
-// Converts and stores D / 2 consecutive fp32 values (D for a whole row) at element `at` of a row.
-template <int W>
-__device__ __forceinline__ void tree_store(const TreeParams& p, bool part, float* orow_part, void* o, size_t at, const float (&v)[W])
-{
-    static_assert(W == 16 || W == 32, "16 or 32 values");
-    if (part) {
-        if constexpr (W == 32) store_row32<float>(orow_part, v);
-        else store_row16<float>(orow_part, v);
-    } else if (p.o_dtype == FA_F32) {
-        if constexpr (W == 32) store_row32<float>(reinterpret_cast<float*>(o) + at, v);
-        else store_row16<float>(reinterpret_cast<float*>(o) + at, v);
-    } else {
-        if constexpr (W == 32) store_row32<__nv_bfloat16>(reinterpret_cast<__nv_bfloat16*>(o) + at, v);
-        else store_row16<__nv_bfloat16>(reinterpret_cast<__nv_bfloat16*>(o) + at, v);
+// A warp's 32 consecutive rows on their way out, 16 columns at a time through shared memory: a thread's
+// row written by itself would be 16-byte pieces of 32 lines an instruction.  A row's 64 bytes are read
+// back by four lanes, the 16-byte pieces exchanged by bits of the row, so that neither side has bank
+// conflicts.  (The end of a unit is latency: addresses and row tests are made once.)
+template <int D>
+struct RowsOut {
+    char* at;             // this lane's piece of row lane / 4
+    uint32_t put, get;    // its places in the warp's 2 KB of shared memory
+    int rows;             // of the warp
+    bool f32;
+    __device__ __forceinline__ RowsOut(uint32_t stage, void* o, bool f32_, size_t first_row, int rows_, int lane)
+    {
+        const int r = lane >> 2, j = lane & 3;
+        f32 = f32_;
+        rows = rows_ - r;
+        at = static_cast<char*>(o) + (first_row + r) * (D * (f32 ? 4 : 2)) + j * (f32 ? 16 : 8);
+        put = stage + lane * 64 + (((lane >> 1) & 3) << 4);
+        get = stage + r * 64 + ((j ^ ((r >> 1) & 3)) << 4);
     }
-}
+    // columns c .. c + 15 of the lane's row (as 2 x 8)
+    __device__ __forceinline__ void store(int c, const float2 (&x)[8]) const
+    {
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            st_shared_v4(put ^ (j << 4), __float_as_uint(x[2 * j].x), __float_as_uint(x[2 * j].y), __float_as_uint(x[2 * j + 1].x),
+                         __float_as_uint(x[2 * j + 1].y));
+        __syncwarp();
+        float4 v[4];
+#pragma unroll
+        for (int it = 0; it < 4; ++it) v[it] = ld_shared_f4(get + it * 512);  // rows r, r + 8, ..: the same exchange
+        if (f32) {
+            char* dst = at + c * 4;
+#pragma unroll
+            for (int it = 0; it < 4; ++it)
+                if (8 * it < rows) *reinterpret_cast<float4*>(dst + it * 8 * D * 4) = v[it];
+        } else {
+            char* dst = at + c * 2;
+#pragma unroll
+            for (int it = 0; it < 4; ++it)
+                if (8 * it < rows)
+                    *reinterpret_cast<uint2*>(dst + it * 8 * D * 2) = make_uint2(pack_bf16x2(v[it].x, v[it].y), pack_bf16x2(v[it].z, v[it].w));
+        }
+    }
+};
+
+__device__ __forceinline__ float2 as_float2(uint32_t a, uint32_t b) { return make_float2(__uint_as_float(a), __uint_as_float(b)); }
 
 template <int D, bool PAIR>
 __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_constant__ TreeParams p)
@@ -300,9 +387,9 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
     const uint32_t bar0 = sbase + C::kOffBar;
     auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
     TreeStart* start_slot = reinterpret_cast<TreeStart*>(smem + C::kOffStart);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffStart + 32);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffStart + 64);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    static_assert(sizeof(TreeStart) <= 32, "start record");
+    static_assert(sizeof(TreeStart) <= 64, "start record");
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -321,6 +408,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
             mbar_init(bar(kTbDrain + i), 1);
         }
         mbar_init(bar(kTbMLFull), 2 * kBlockM);
+        for (int i = 0; i < kTrSegs; ++i) mbar_init(bar(kTbSegFull + i), 1);
         for (int s = 0; s < S; ++s) {
             mbar_init(bar(kTbKFull + s), 1);
             mbar_init(bar(kTbKEmpty + s), PAIR ? 2 : 1);
@@ -344,26 +432,57 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    const TreeStart start = *start_slot;
-    const int total = static_cast<int>(start.w1 - start.w0);
+    const TreeSeg* seg_ring = reinterpret_cast<const TreeSeg*>(smem + C::kOffSeg);
+    // Record of segment i (of any role but the producer); n = 0 past the last, and when a wait ran out.
+    auto segment = [&](int i, bool& ok) -> TreeSeg {
+        TreeSeg x;
+        x.n = 0;
+        ok = mbar_wait(bar(kTbSegFull + i % kTrSegs), static_cast<uint32_t>(i / kTrSegs) & 1, limit, abort_flag);
+        if (ok) x = seg_ring[i % kTrSegs];
+        return x;
+    };
 
     if (warp >= kTrWarpProducer) {
         regs_decrease<kTrControlRegs<D>>();
         if (warp == kTrWarpProducer) {
             // ======================================================== producer
-            if (lane == 0 && total > 0) {
+            if (lane == 0) {
                 prefetch_tensormap(&p.tm_q);
                 prefetch_tensormap(&p.tm_k);
                 prefetch_tensormap(&p.tm_v);
                 // K and V are read again only by a group's further query blocks
                 const uint64_t pol_kv = p.n_qp > 1 ? policy_evict_last() : policy_evict_first();
                 const uint64_t pol_q = policy_evict_first();
+                const TreeStart start = *start_slot;
                 TreeWalk kw, vw;  // K runs one tile ahead of V
                 kw.begin(p, start);
                 vw.begin(p, start);
                 int kj = 0, vj = 0;  // tile within the segment
                 int segs = 0;        // query loads issued
                 int k_issued = 0, v_issued = 0;
+                TreeSeg* ring = reinterpret_cast<TreeSeg*>(smem + C::kOffSeg);
+                TreeJoin join{0, 0, 0};
+                auto publish = [&](int n) {  // the walk's segment to the other roles
+                    TreeSeg x;
+                    x.n = n;
+                    x.tile = kw.tile;
+                    x.prefix = kw.len.prefix;
+                    x.nodes = kw.len.nodes;
+                    x.b = kw.b;
+                    x.group = kw.group(p);
+                    x.qp = kw.qp;
+                    x.slot = kw.slot();
+                    if (n > 0 && x.slot >= 0 && kw.tile == 0) {
+                        // begun here, finished by the CTA of its last place
+                        const long long last = start.w1 + (kw.tiles - kw.n);
+                        join.first_row = static_cast<long long>(x.group) * p.rows + static_cast<long long>(kw.qp) * p.part_rows;
+                        join.rows = min(p.part_rows, p.rows - kw.qp * p.part_rows);
+                        join.parts = static_cast<int>((last * start.ctas - 1) / start.total) - static_cast<int>(blockIdx.x) + 1;
+                    }
+                    ring[segs % kTrSegs] = x;
+                    mbar_arrive(bar(kTbSegFull + segs % kTrSegs));
+                    ++segs;
+                };
                 auto load_k = [&]() -> bool {
                     const int g = kw.group(p);
                     if (kj == 0) {  // the segment's query rows
@@ -378,7 +497,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                             for (int cb = 0; cb < C::kNumCB; ++cb)
                                 tma_load_3d(sbase + C::kOffQ + (buf + i) * C::kTileBytes + cb * C::kBlkBytes, &p.tm_q,
                                             bar(kTbQFull + buf), cb * C::kCB, row0 + i * kBlockM, g, pol_q);
-                        ++segs;
+                        publish(kw.n);
                     }
                     const int s = k_issued % S;
                     if (k_issued >= S &&
@@ -411,12 +530,15 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                     }
                     return true;
                 };
-                bool ok = load_k();
-                for (int t = 0; ok && t < total; ++t) ok = (t + 1 >= total || load_k()) && load_v();
+                bool ok = !kw.live() || load_k();
+                while (ok && vw.live()) ok = (!kw.live() || load_k()) && load_v();
+                const int loads = segs;  // query loads issued
+                if (ok) publish(0);
+                p.joins[blockIdx.x] = join;
                 if (!ok && !*abort_flag) record_failure(p.status, abort_flag, FA_ERR_TIMEOUT);
                 // Every issued copy must land before the CTA may exit (its last phase per barrier).
                 const int q_bufs = PAIR ? 1 : 2;
-                for (int t = segs - q_bufs < 0 ? 0 : segs - q_bufs; t < segs; ++t)
+                for (int t = loads - q_bufs < 0 ? 0 : loads - q_bufs; t < loads; ++t)
                     mbar_wait(bar(kTbQFull + t % q_bufs), static_cast<uint32_t>(t / q_bufs) & 1, kDrainLimitNs, nullptr);
                 for (int t = k_issued - S < 0 ? 0 : k_issued - S; t < k_issued; ++t)
                     mbar_wait(bar(kTbKFull + t % S), static_cast<uint32_t>(t / S) & 1, kDrainLimitNs, nullptr);
@@ -425,7 +547,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
             }
         } else if (warp == kTrWarpMma || warp == kTrWarpMma + 1) {
             // ======================================================== MMA issuers
-            if (lane == 0 && total > 0) {
+            if (lane == 0) {
                 const int i = warp - kTrWarpMma;  // warpgroup of this issuer
                 const uint32_t d_s = tmem + C::col_s(i);
                 const uint32_t d_o = tmem + C::col_o(i);
@@ -468,8 +590,9 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                     if (last) umma_commit(bar(kTbQEmpty + q_buf));
                     return true;
                 };
-                TreeWalk w;
-                for (w.begin(p, start); ok && w.live(); w.next(p)) {
+                while (ok) {
+                    const TreeSeg w = segment(segs, ok);
+                    if (w.n == 0) break;
                     const int q_buf = PAIR ? 0 : segs & 1;
                     const int q_use = PAIR ? segs : segs >> 1;
                     const int q_tile = PAIR ? i : q_buf;
@@ -544,9 +667,14 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
         int tiles = 0;                 // key tiles processed by this warpgroup
         int ready[2] = {0, 0};         // segments with tiles so far, per warpgroup
         int segs = 0, k = 0;
+        uint32_t vis[4] = {0u, 0u, 0u, 0u};
+        int vis_b = -1, vis_qp = -1;
         bool ok = true;
-        TreeWalk w;
-        for (w.begin(p, start); ok && w.live(); w.next(p)) {
+        const uint32_t stage = sbase + C::kOffStage + warp * 2048;
+        while (ok) {
+            const TreeSeg w = segment(segs, ok);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok || w.n == 0) break;
             const int row0 = PAIR ? w.qp * 2 * kBlockM + wg * kBlockM : 0;
             const int rows = min(p.rows - row0, kBlockM);  // rows of this warpgroup's tile (<= 0: none)
             if (PAIR && rows <= 0) {
@@ -554,16 +682,19 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                 ++segs;
                 continue;
             }
-            const int row = row0 + r;
-            const int node = row % p.T;
-            const bool valid = r < rows;
-            const bool warp_live = 32 * (warp & 3) < rows;
+            const int rows_warp = rows - 32 * (warp & 3);  // of this warp (<= 0: none)
+            const bool warp_live = rows_warp > 0;
             const int step = PAIR ? 1 : 2;
             const int j0 = PAIR ? 0 : (k + wg) & 1;
-            const int end = w.len.prefix + w.len.nodes;  // keys of the sequence
-            uint32_t vis[4] = {0u, 0u, 0u, 0u};
-            if ((w.tile + w.n) * kBlockN > w.len.prefix && valid && node < w.len.nodes)
-                tree_ancestors(p.parents != nullptr ? p.parents + static_cast<size_t>(w.b) * p.T : nullptr, node, p.status, vis);
+            const int end = w.prefix + w.nodes;  // keys of the sequence
+            // the row's ancestors, kept while the sequence and the row stay the same
+            if ((w.tile + w.n) * kBlockN > w.prefix && (w.b != vis_b || (PAIR && w.qp != vis_qp))) {
+                vis_b = w.b;
+                vis_qp = w.qp;
+                const int node = (row0 + r) % p.T;
+                tree_ancestors(p.parents != nullptr ? p.parents + static_cast<size_t>(w.b) * p.T : nullptr, p.T,
+                               r < rows && node < w.nodes ? node : -1, lane, p.status, vis);
+            }
             float m_run = -INFINITY;  // running max of scale * log2(e) * S over visible keys
             float l = 0.f;
             for (int j = j0; j < w.n; j += step) {
@@ -571,7 +702,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                 if (!ok) break;
                 tc_fence_after_sync();
                 const int k0 = (w.tile + j) * kBlockN;
-                const int stage = (k + j) % S;
+                const int vs = (k + j) % S;  // V stage
                 if (warp_live) {
                     uint32_t u[kBlockN];
                     float mrow;
@@ -597,8 +728,8 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                     float s[kBlockN];
 #pragma unroll
                     for (int c = 0; c < kBlockN; ++c) s[c] = __uint_as_float(u[c]);
-                    if (k0 + kBlockN > w.len.prefix) {  // the tile holds drafted rows, or rows past them
-                        const int shift = k0 - w.len.prefix;  // node index of the tile's first key
+                    if (k0 + kBlockN > w.prefix) {  // the tile holds drafted rows, or rows past them
+                        const int shift = k0 - w.prefix;  // node index of the tile's first key
                         auto word = [&](int q) -> uint32_t {
                             return q == 0 ? vis[0] : q == 1 ? vis[1] : q == 2 ? vis[2] : q == 3 ? vis[3] : 0u;
                         };
@@ -630,44 +761,63 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                     float2 rs[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                                     make_float2(0.f, 0.f)};
                     uint32_t pk[kBlockN / 2];
+                    auto exps = [&](int c0) {  // weights of columns c0 .. c0 + 31
 #pragma unroll
-                    for (int c = 0; c < kBlockN; c += 8) {
+                        for (int c = c0; c < c0 + 32; c += 8) {
 #pragma unroll
-                        for (int h = 0; h < 4; ++h) {
-                            const float2 x = __ffma2_rn(make_float2(s[c + 2 * h], s[c + 2 * h + 1]), sl2x2, negm);
-                            const float2 e = make_float2(ex2(x.x), ex2(x.y));
-                            rs[h] = __fadd2_rn(rs[h], e);
-                            // the weights are rounded to bf16 for the product (half a step, 2^-8 of each
-                            // weight); the sum l keeps the fp32 ones
-                            pk[c / 2 + h] = pack_bf16x2(e.x, e.y);
+                            for (int h = 0; h < 4; ++h) {
+                                const float2 x = __ffma2_rn(make_float2(s[c + 2 * h], s[c + 2 * h + 1]), sl2x2, negm);
+                                const float2 e = make_float2(ex2(x.x), ex2(x.y));
+                                rs[h] = __fadd2_rn(rs[h], e);
+                                // the weights are rounded to bf16 for the product (half a step, 2^-8 of each
+                                // weight); the sum l keeps the fp32 ones
+                                pk[c / 2 + h] = pack_bf16x2(e.x, e.y);
+                            }
                         }
-                    }
-                    // O_i and P_i are free once the previous product has completed (with P aliased into
-                    // S_i the arrival of S_i implies it)
-                    if (!C::kAliasP && j > j0) {
-                        ok = __all_sync(0xffffffffu, mbar_wait(bar(kTbPVDone + wg), (tiles - 1) & 1, limit, abort_flag));
-                        if (!ok) break;
-                        tc_fence_after_sync();
-                    }
-                    if (j > j0 && __any_sync(0xffffffffu, grow)) {
-                        constexpr int kRescale = D <= 64 ? D : 32;
-                        const float2 a2 = make_float2(alpha, alpha);
+                    };
+                    const float2 a2 = make_float2(alpha, alpha);
+                    auto scale = [&](uint32_t (&oc)[32]) {
 #pragma unroll
-                        for (int c0 = 0; c0 < D; c0 += kRescale) {
-                            uint32_t oc[kRescale];
+                        for (int e = 0; e < 32; e += 2) {
+                            const float2 x = __fmul2_rn(make_float2(__uint_as_float(oc[e]), __uint_as_float(oc[e + 1])), a2);
+                            oc[e] = __float_as_uint(x.x);
+                            oc[e + 1] = __float_as_uint(x.y);
+                        }
+                    };
+                    const bool rescale = __any_sync(0xffffffffu, grow) && j > j0;
+                    if constexpr (C::kAliasP) {
+                        // The previous product has completed (the arrival of S_i implies it): where the
+                        // max grew, O_i is rescaled 32 columns at a time under the exponentials of 32.
 #pragma unroll
-                            for (int c = 0; c < kRescale; c += 32)
-                                tmem_ld32(t_o + static_cast<uint32_t>(c0 + c), *reinterpret_cast<uint32_t(*)[32]>(&oc[c]));
+                        for (int c = 0; c < kBlockN; c += 32) {
+                            uint32_t oc[32];
+                            if (rescale) tmem_ld32(t_o + static_cast<uint32_t>(c), oc);
+                            exps(c);
+                            if (rescale) {
+                                tmem_ld_wait();
+                                scale(oc);
+                                tmem_st32(t_o + static_cast<uint32_t>(c), oc);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < kBlockN; c += 32) exps(c);
+                        // O_i and P_i are free once the previous product has completed
+                        if (j > j0) {
+                            ok = __all_sync(0xffffffffu, mbar_wait(bar(kTbPVDone + wg), (tiles - 1) & 1, limit, abort_flag));
+                            if (!ok) break;
+                            tc_fence_after_sync();
+                        }
+                        if (rescale) {
+                            uint32_t oc[D / 32][32];
+#pragma unroll
+                            for (int c = 0; c < D / 32; ++c) tmem_ld32(t_o + 32u * c, oc[c]);
                             tmem_ld_wait();
 #pragma unroll
-                            for (int e = 0; e < kRescale; e += 2) {
-                                const float2 x = __fmul2_rn(make_float2(__uint_as_float(oc[e]), __uint_as_float(oc[e + 1])), a2);
-                                oc[e] = __float_as_uint(x.x);
-                                oc[e + 1] = __float_as_uint(x.y);
+                            for (int c = 0; c < D / 32; ++c) {
+                                scale(oc[c]);
+                                tmem_st32(t_o + 32u * c, oc[c]);
                             }
-#pragma unroll
-                            for (int c = 0; c < kRescale; c += 32)
-                                tmem_st32(t_o + static_cast<uint32_t>(c0 + c), *reinterpret_cast<uint32_t(*)[32]>(&oc[c]));
                         }
                     }
                     tmem_st32(t_p + 0, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
@@ -686,11 +836,11 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                 if (k0 + kBlockN > end) {
                     // V rows past the tree may hold anything: zero them before the product reads them.
                     // (The stage's previous tile has been consumed: see kStages.)
-                    ok = __all_sync(0xffffffffu, mbar_wait(bar(kTbVFull + stage), static_cast<uint32_t>((k + j) / S) & 1,
+                    ok = __all_sync(0xffffffffu, mbar_wait(bar(kTbVFull + vs), static_cast<uint32_t>((k + j) / S) & 1,
                                                            limit, abort_flag));
                     if (!ok) break;
                     if (k0 + r >= end) {
-                        const uint32_t vrow = sbase + C::kOffV + stage * C::kTileBytes + r * C::kRowBytes;
+                        const uint32_t vrow = sbase + C::kOffV + vs * C::kTileBytes + r * C::kRowBytes;
 #pragma unroll
                         for (int cb = 0; cb < C::kNumCB; ++cb)
 #pragma unroll
@@ -705,11 +855,18 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
             }
             if (!ok) break;
             // ---- end of the segment: its rows' output and log-sum-exp, final or to a slot
-            const bool part = !w.whole();
-            const int slot = part_slot(blockIdx.x, w.first);
-            const bool shown = node < w.len.nodes;  // rows of nodes past the tree: O = 0, LSE = -inf
-            const size_t out_row = static_cast<size_t>(w.group(p)) * p.rows + row;
-            const size_t part_row = static_cast<size_t>(slot) * p.part_rows + (PAIR ? wg * kBlockM : 0) + r;
+            const bool part = w.slot >= 0;
+            const bool shown = (row0 + r) % p.T < w.nodes;  // rows of nodes past the tree: O = 0, LSE = -inf
+            // first row of the warp in the output (or the slots)
+            const size_t first = part ? static_cast<size_t>(w.slot) * p.part_rows + (PAIR ? wg * kBlockM : 0) + 32 * (warp & 3)
+                                      : static_cast<size_t>(w.group) * p.rows + row0 + 32 * (warp & 3);
+            const RowsOut<D> out(stage, part ? static_cast<void*>(p.o_part) : p.o, part || p.o_dtype == FA_F32, first, rows_warp, lane);
+            auto store_lse = [&](float lse) {
+                if (lane < rows_warp) {
+                    if (part) p.lse_part[first + lane] = lse;
+                    else if (p.lse != nullptr) p.lse[first + lane] = lse;
+                }
+            };
             if constexpr (PAIR) {
                 ok = __all_sync(0xffffffffu, mbar_wait(bar(kTbOReady + wg), ready[0] & 1, limit, abort_flag));
                 if (!ok) break;
@@ -717,21 +874,24 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                 tc_fence_after_sync();
                 if (warp_live) {
                     const float inv = (l == 0.f || !shown) ? 0.f : 1.f / l;
-#pragma unroll
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t o[32];
-                        float x[32];
-                        tmem_ld32(t_o + static_cast<uint32_t>(c), o);
+                    const bool hide = __any_sync(0xffffffffu, !shown);
+                    const float2 inv2 = make_float2(inv, inv);
+                    uint32_t o[16];
+                    tmem_ld16(t_o, o);
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
+                        float2 x[8];
                         tmem_ld_wait();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) x[e] = shown ? __uint_as_float(o[e]) * inv : 0.f;
-                        if (valid) tree_store<32>(p, part, p.o_part + part_row * D + c, p.o, out_row * D + c, x);
+                        for (int e = 0; e < 8; ++e) x[e] = __fmul2_rn(as_float2(o[2 * e], o[2 * e + 1]), inv2);
+                        if (c + 16 < D) tmem_ld16(t_o + static_cast<uint32_t>(c + 16), o);  // on its way while these are stored
+                        if (hide) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) x[e] = shown ? x[e] : make_float2(0.f, 0.f);
+                        }
+                        out.store(c, x);
                     }
-                    const float lse = (l == 0.f || !shown) ? -INFINITY : (m_run + lg2_approx(l)) * 0.69314718055994531f;
-                    if (valid) {
-                        if (part) p.lse_part[part_row] = lse;
-                        else if (p.lse != nullptr) p.lse[out_row] = lse;
-                    }
+                    store_lse((l == 0.f || !shown) ? -INFINITY : (m_run + lg2_approx(l)) * 0.69314718055994531f);
                 }
                 tc_fence_before_sync();
                 mbar_arrive(bar(kTbOFree + wg));
@@ -761,32 +921,40 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                     const bool none = L == 0.f || !shown;
                     const float inv = none ? 0.f : 1.f / L;
                     const float g0 = f0 * inv, g1 = f1 * inv;
-                    constexpr int W = D / 2 < 32 ? D / 2 : 32;  // this warpgroup's half of the columns, W at a time
-#pragma unroll
-                    for (int c = 0; c < D / 2; c += W) {
-                        const uint32_t col = static_cast<uint32_t>(wg * (D / 2) + c);
-                        uint32_t a[W], b[W];
-                        float x[W];
-                        if constexpr (W == 32) {
-                            if (has0) tmem_ld32(tmem + lane_base + C::col_o(0) + col, a);
-                            if (has1) tmem_ld32(tmem + lane_base + C::col_o(1) + col, b);
-                        } else {
-                            if (has0) tmem_ld16(tmem + lane_base + C::col_o(0) + col, a);
-                            if (has1) tmem_ld16(tmem + lane_base + C::col_o(1) + col, b);
-                        }
+                    // this warpgroup's half of the columns
+                    const uint32_t col0 = static_cast<uint32_t>(wg * (D / 2));
+                    const uint32_t t_o0 = tmem + lane_base + C::col_o(0) + col0;
+                    const uint32_t t_o1 = tmem + lane_base + C::col_o(1) + col0;
+                    const bool hide = __any_sync(0xffffffffu, none);
+                    const float2 w0 = make_float2(g0, g0), w1 = make_float2(g1, g1);
+                    uint32_t a[16], b[16];
+                    auto load = [&](uint32_t c) {  // a warpgroup without tiles has nothing in its columns
+                        if (has0) tmem_ld16(t_o0 + c, a);
+                        if (has1) tmem_ld16(t_o1 + c, b);
+                    };
+                    load(0u);
+#pragma unroll 1
+                    for (int c = 0; c < D / 2; c += 16) {
+                        float2 x[8];
                         tmem_ld_wait();
 #pragma unroll
-                        for (int e = 0; e < W; ++e) {
-                            const float y0 = has0 ? __uint_as_float(a[e]) * g0 : 0.f;
-                            x[e] = none ? 0.f : has1 ? fmaf(__uint_as_float(b[e]), g1, y0) : y0;
+                        for (int e = 0; e < 8; ++e) x[e] = make_float2(0.f, 0.f);
+                        if (has0) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) x[e] = __fmul2_rn(as_float2(a[2 * e], a[2 * e + 1]), w0);
                         }
-                        if (valid) tree_store<W>(p, part, p.o_part + part_row * D + col, p.o, out_row * D + col, x);
+                        if (has1) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) x[e] = __ffma2_rn(as_float2(b[2 * e], b[2 * e + 1]), w1, x[e]);
+                        }
+                        if (c + 16 < D / 2) load(static_cast<uint32_t>(c + 16));  // on their way while these are stored
+                        if (hide) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) x[e] = none ? make_float2(0.f, 0.f) : x[e];
+                        }
+                        out.store(static_cast<int>(col0) + c, x);
                     }
-                    if (valid && wg == 0) {
-                        const float lse = none ? -INFINITY : (M + lg2_approx(L)) * 0.69314718055994531f;
-                        if (part) p.lse_part[part_row] = lse;
-                        else if (p.lse != nullptr) p.lse[out_row] = lse;
-                    }
+                    if (wg == 0) store_lse(none ? -INFINITY : (M + lg2_approx(L)) * 0.69314718055994531f);
                 }
                 tc_fence_before_sync();
                 mbar_arrive(bar(kTbOFree + 0));
@@ -808,58 +976,80 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
 }
 
 // Joins the parts of the units that several CTAs share: lse = log sum_s exp(lse_s),
-// o = sum_s exp(lse_s - lse) o_s ("flash_lab.py" section 4).  Block (u, y) serves unit u, rows
-// 8 y .. 8 y + 7, a warp a row: with few units there are many parts to a row, and the time is the
-// latency of the parts' loads, so all log-sum-exps are read at once and the outputs eight at a time.
-// The part of the unit's first CTA is that CTA's last
-// segment unless its share begins with the unit; the parts of the others are their first segments.
+// o = sum_s exp(lse_s - lse) o_s ("flash_lab.py" section 4).  Blocks (c, y) serve the unit that CTA c
+// began and did not finish, if there is one (joins[c]): its part is in that CTA's second slot, the
+// others in the following CTAs' first (slot()).  The time is the latency of the parts' loads, so all of
+// them are in flight at once where they are few (up to 4: eight lanes to a row, 32 rows a block), and
+// eight at a time otherwise (a warp a row, 8 rows a block).
 template <int D>
 __global__ void __launch_bounds__(256) fa_tree_merge_kernel(const __grid_constant__ TreeParams p)
 {
-    const int warp = threadIdx.x >> 5;
-    const int lane = threadIdx.x & 31;
-    const int upb = p.Hkv * p.n_qp;
-    const int b = static_cast<int>(blockIdx.x / upb);
-    const int unit = static_cast<int>(blockIdx.x - static_cast<unsigned>(b) * upb);
-    const int kvh = unit / p.n_qp;
-    const int row_base = (unit - kvh * p.n_qp) * p.part_rows;  // first row of the unit within its group
-    const int rows = min(p.part_rows, p.rows - row_base);
     grid_dependency_wait();
     grid_launch_dependents();
-    long long before = 0, all = 0;  // tiles per unit of the sequences before b, and of all
-    for (int i = lane; i < p.B; i += 32) {
-        const int t = tree_len(p.seqlens, p.n_nodes, i, p.T, p.Nk_max, p.status).tiles();
-        all += t;
-        if (i < b) before += t;
-    }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-        before += __shfl_xor_sync(0xffffffffu, before, o);
-        all += __shfl_xor_sync(0xffffffffu, all, o);
-    }
-    const int tiles = tree_len(p.seqlens, p.n_nodes, b, p.T, p.Nk_max, p.status).tiles();
-    const long long total = all * upb;
-    const long long ctas = p.num_ctas < total ? p.num_ctas : total;
-    const long long w = before * upb + static_cast<long long>(unit) * tiles;  // the unit's first tile
-    const int c0 = static_cast<int>(((w + 1) * ctas - 1) / total);            // the CTAs of its first and last tile
-    const int c1 = static_cast<int>(((w + tiles) * ctas - 1) / total);
-    if (c0 == c1) return;  // finished by its CTA
-    const int n = c1 - c0 + 1;
-    const bool head = share_begin(c0, total, ctas) == w;
-    constexpr int V = D / 32;  // columns of a lane
-    const int r = static_cast<int>(blockIdx.y) * 8 + warp;
-    if (r >= rows) return;
-    auto at = [&](int s) -> size_t {
-        return static_cast<size_t>(part_slot(c0 + s, s > 0 || head)) * p.part_rows + static_cast<size_t>(r);
+    const int c0 = blockIdx.x;
+    const TreeJoin join = p.joins[c0];
+    const int n = join.parts;
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
+    auto at = [&](int s, int r) -> size_t {  // row of part s in the slots
+        return static_cast<size_t>(2 * (c0 + s) + (s == 0 ? 1 : 0)) * p.part_rows + static_cast<size_t>(r);
     };
+    auto write = [&](size_t i, float4 v) {
+        if (p.o_dtype == FA_F32) reinterpret_cast<float4*>(p.o)[i / 4] = v;
+        else *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.o) + i) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+    };
+    if (n <= 4) {
+        if (blockIdx.y % 4 != 0) return;
+        const int r = static_cast<int>(blockIdx.y) * 8 + warp * 4 + (lane >> 3);
+        if (r >= join.rows) return;  // (no warp-wide operation below)
+        const int l8 = lane & 7;
+        float x[4];
+        float4 v[4][D / 32];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            x[s] = -INFINITY;
+            if (s < n) {
+                x[s] = __ldg(p.lse_part + at(s, r));
+                const float4* src = reinterpret_cast<const float4*>(p.o_part + at(s, r) * D) + l8;
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) v[s][i] = __ldg(src + 8 * i);
+            }
+        }
+        const float M = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+        const bool live = x[0] != -INFINITY || x[1] != -INFINITY || x[2] != -INFINITY || x[3] != -INFINITY;
+        float sum = 0.f;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            x[s] = x[s] == -INFINITY ? 0.f : ex2((x[s] - M) * kLog2e);
+            sum += x[s];
+        }
+        const float inv = live ? 1.f / sum : 0.f;
+        const size_t row = static_cast<size_t>(join.first_row) + r;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const float f = x[s] * inv;  // an empty part's output is 0
+                if (s < n) a = make_float4(fmaf(f, v[s][i].x, a.x), fmaf(f, v[s][i].y, a.y), fmaf(f, v[s][i].z, a.z), fmaf(f, v[s][i].w, a.w));
+            }
+            write(row * D + 4 * (l8 + 8 * i), a);
+        }
+        if (l8 == 0 && p.lse != nullptr) p.lse[row] = live ? M + log2f(sum) * kLn2 : -INFINITY;
+        return;
+    }
+    const int r = static_cast<int>(blockIdx.y) * 8 + warp;
+    if (r >= join.rows) return;
     constexpr int kHeld = kTreeMaxCtas / 32;  // log-sum-exps a lane holds: at most a part for each CTA
+    constexpr int V = D / 32;                 // columns of a lane
     float x[kHeld];
     float M = -INFINITY;
     bool live = false;
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
         const int s = 32 * i + lane;
-        x[i] = s < n ? __ldg(p.lse_part + at(s)) : -INFINITY;
+        x[i] = s < n ? __ldg(p.lse_part + at(s, r)) : -INFINITY;
         live = live || x[i] != -INFINITY;
         M = fmaxf(M, x[i]);
     }
@@ -869,12 +1059,11 @@ __global__ void __launch_bounds__(256) fa_tree_merge_kernel(const __grid_constan
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
-        x[i] = x[i] == -INFINITY ? 0.f : ex2((x[i] - M) * 1.4426950408889634f);
+        x[i] = x[i] == -INFINITY ? 0.f : ex2((x[i] - M) * kLog2e);
         sum += x[i];
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const float L = live ? M + log2f(sum) * 0.69314718055994531f : -INFINITY;
     const float inv = live ? 1.f / sum : 0.f;
     float acc[V];
 #pragma unroll
@@ -884,8 +1073,8 @@ __global__ void __launch_bounds__(256) fa_tree_merge_kernel(const __grid_constan
         const int m = min(32, n - 32 * i);
 #pragma unroll 8
         for (int j = 0; j < m; ++j) {
-            const float f = __shfl_sync(0xffffffffu, x[i], j) * inv;  // an empty part's output is 0
-            const float* src = p.o_part + at(32 * i + j) * D + lane * V;
+            const float f = __shfl_sync(0xffffffffu, x[i], j) * inv;
+            const float* src = p.o_part + at(32 * i + j, r) * D + lane * V;
             float v[V];
             if constexpr (V == 4) *reinterpret_cast<float4*>(v) = __ldg(reinterpret_cast<const float4*>(src));
             else if constexpr (V == 2) *reinterpret_cast<float2*>(v) = __ldg(reinterpret_cast<const float2*>(src));
@@ -894,15 +1083,15 @@ __global__ void __launch_bounds__(256) fa_tree_merge_kernel(const __grid_constan
             for (int e = 0; e < V; ++e) acc[e] = fmaf(f, v[e], acc[e]);
         }
     }
-            const size_t out = (static_cast<size_t>(b) * p.Hkv + kvh) * p.rows + row_base + r;
-    #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                if (p.o_dtype == FA_F32)
-                    reinterpret_cast<float*>(p.o)[out * D + lane * V + e] = acc[e];
-                else
-                    reinterpret_cast<__nv_bfloat16*>(p.o)[out * D + lane * V + e] = __float2bfloat16_rn(acc[e]);
-            }
-    if (lane == 0 && p.lse != nullptr) p.lse[out] = L;
+    const size_t row = static_cast<size_t>(join.first_row) + r;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        if (p.o_dtype == FA_F32)
+            reinterpret_cast<float*>(p.o)[row * D + lane * V + e] = acc[e];
+        else
+            reinterpret_cast<__nv_bfloat16*>(p.o)[row * D + lane * V + e] = __float2bfloat16_rn(acc[e]);
+    }
+    if (lane == 0 && p.lse != nullptr) p.lse[row] = live ? M + log2f(sum) * kLn2 : -INFINITY;
 }
 
 template <int D, bool PAIR>
@@ -928,7 +1117,7 @@ cudaError_t launch_tree_t(const TreeParams& p, cudaStream_t st)
     }
     e = launch_pdl(kern, dim3(static_cast<unsigned>(p.num_ctas)), kTrThreads, C::kSmemBytes, st, p);
     if (e != cudaSuccess) return e;
-    const dim3 grid(static_cast<unsigned>(p.B) * p.Hkv * p.n_qp, static_cast<unsigned>((p.part_rows + 7) / 8));
+    const dim3 grid(static_cast<unsigned>(p.num_ctas), static_cast<unsigned>((p.part_rows + 7) / 8));
     return launch_pdl(fa_tree_merge_kernel<D>, grid, 256, 0, st, p);
 }
 
