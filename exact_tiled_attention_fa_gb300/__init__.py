@@ -469,53 +469,89 @@ def merge_states(o_parts, lse_parts, out_dtype=torch.float32, out=None, lse=None
     return out, lse
 
 
-def _token_stride(t, name, device=None, dtype=torch.bfloat16):
-    """Checks a projection [B, N, heads, d] whose tokens are evenly spaced; returns (device index, stride)."""
+# The operators below are called once or twice a layer in a serving loop, where a call's host time is
+# most of it: each argument is checked and its pointer taken in one step, and the messages are made
+# only when something is wrong.
+
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _refuse(t, name, dtype, device, shape):
+    """Says what is wrong with an argument that failed its check."""
+    _need(t, name, dtype, device)
+    raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _arg(t, name, dtype, device, shape):
+    """Data pointer of a contiguous tensor of this type and shape on this device (an index)."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, dtype, device, shape)
+
+
+def _first(t, name, ndim=4):
+    """Device index and shape of a call's first argument."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     di = t.get_device()
+    if t.dtype is not torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
     if di < 0:
         raise ValueError(f"{name} must be on a CUDA device")
-    if device is not None and di != device:
-        raise ValueError(f"{name} is on cuda:{di}, expected cuda:{device}")
-    if t.dim() != 4:
-        raise ValueError(f"{name} must be [B, N, heads, head_dim]")
-    B, N, H, d = t.shape
-    sb, sn, sh, sd = t.stride()
-    tok = sn if N > 1 else sb if B > 1 else H * d
-    if (d > 1 and sd != 1) or (H > 1 and sh != d) or (B > 1 and sb != N * tok):
-        raise ValueError(f"{name} must have its heads contiguous and its tokens evenly spaced")
-    return di, tok
+    shape = t.shape
+    if len(shape) != ndim:
+        raise ValueError(f"{name} must have {ndim} dimensions")
+    return di, shape
+
+
+def _tokens(t, name, dtype, device, shape):
+    """Data pointer and token stride of [B, N, heads, head_dim] with its heads contiguous and its tokens
+    evenly spaced: a whole tensor, or a slice of the heads of one."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device:
+            B, N, H, d = shape
+            if t.is_contiguous():
+                return t.data_ptr(), H * d
+            sb, sn, sh, sd = t.stride()
+            tok = sn if N > 1 else sb if B > 1 else H * d
+            if (d == 1 or sd == 1) and (H == 1 or sh == d) and (B == 1 or sb == N * tok):
+                return t.data_ptr(), tok
+            raise ValueError(f"{name} must have its heads contiguous and its tokens evenly spaced")
+    except AttributeError:
+        pass
+    _refuse(t.contiguous() if isinstance(t, torch.Tensor) else t, name, dtype, device, shape)
+
+
+def _call(device, f, *args):
+    """Calls a library function on the device's current stream, which it takes last."""
+    if _current_device() == device:
+        return f(*args, _stream(device))
+    with torch.cuda.device(device):
+        return f(*args, _stream(device))
 
 
 def _rope_args(q, k, q_weight, k_weight, cos, sin):
-    """The checks that the norm's forms share; returns (device index, token strides, sizes, weight dtype)."""
-    di, qs = _token_stride(q, "q")
-    _, ks = _token_stride(k, "k", di)
-    B, N, Hq, d = q.shape
+    """What the norm's forms share, checked: (device, sizes, weight dtype, pointers, token strides)."""
+    di, (B, N, Hq, d) = _first(q, "q")
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("k must be [B, N, heads, head_dim]")
     Hkv = k.shape[2]
-    if tuple(k.shape) != (B, N, Hkv, d):
-        raise ValueError("shape mismatch between q and k")
+    qp, qs = _tokens(q, "q", torch.bfloat16, di, (B, N, Hq, d))
+    kp, ks = _tokens(k, "k", torch.bfloat16, di, (B, N, Hkv, d))
     wt = q_weight.dtype if isinstance(q_weight, torch.Tensor) else None
-    _need(q_weight, "q_weight", wt, di)
-    _need(k_weight, "k_weight", wt, di)
-    if wt != torch.bfloat16 and wt != torch.float32:
+    wqp = _arg(q_weight, "q_weight", wt, di, (d,))
+    wkp = _arg(k_weight, "k_weight", wt, di, (d,))
+    if wt is not torch.bfloat16 and wt is not torch.float32:
         raise ValueError("weights must be bfloat16 or float32")
-    _need(cos, "cos", torch.float32, di)
-    _need(sin, "sin", torch.float32, di)
-    if tuple(q_weight.shape) != (d,) or tuple(k_weight.shape) != (d,):
-        raise ValueError("weights must be [head_dim]")
-    if cos.dim() != 2 or cos.shape != sin.shape:
+    if not isinstance(cos, torch.Tensor) or cos.dim() != 2:
         raise ValueError("cos and sin must be [max_pos, rot / 2]")
-    return di, qs, ks, B, N, Hq, Hkv, d, 2 * cos.shape[1], cos.shape[0], _odt(wt)
-
-
-def _need_shape(t, name, dtype, di, shape):
-    _need(t, name, dtype, di)
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {list(shape)}")
+    max_pos, half = shape = cos.shape
+    cp = _arg(cos, "cos", torch.float32, di, shape)
+    sp = _arg(sin, "sin", torch.float32, di, shape)
+    return di, B, N, Hq, Hkv, d, 2 * half, max_pos, FA_BF16 if wt is torch.bfloat16 else FA_F32, (qp, kp, wqp, wkp, cp, sp), qs, ks
 
 
 def qk_norm_rope(q, k, v, q_weight, k_weight, cos, sin, positions=None, eps=1e-6, interleaved=False, expand=False,
@@ -529,32 +565,27 @@ def qk_norm_rope(q, k, v, q_weight, k_weight, cos, sin, positions=None, eps=1e-6
     their query heads.  Returns (q [B,Hq,N,d], k, v [B,Hkv or Hq,N,d] or None), bf16.
     """
     lib = _load()
-    di, qs, ks, B, N, Hq, Hkv, d, rot, max_pos, wdt = _rope_args(q, k, q_weight, k_weight, cos, sin)
-    vs = 0
+    di, B, N, Hq, Hkv, d, rot, max_pos, wdt, (qp, kp, wqp, wkp, cp, sp), qs, ks = _rope_args(q, k, q_weight, k_weight, cos, sin)
+    bf16 = torch.bfloat16
+    kv = (B, Hq if expand else Hkv, N, d)
+    vp, vs, vop = None, 0, None
     if v is not None:
-        _, vs = _token_stride(v, "v", di)
-        if tuple(v.shape) != (B, N, Hkv, d):
-            raise ValueError("shape mismatch between k and v")
+        vp, vs = _tokens(v, "v", bf16, di, (B, N, Hkv, d))
+        if v_out is None:
+            v_out = torch.empty(kv, dtype=bf16, device=q.device)
+        vop = _arg(v_out, "v_out", bf16, di, kv)
     elif v_out is not None:
         raise ValueError("v_out without v")
-    if positions is not None:
-        _need_shape(positions, "positions", torch.int32, di, (B, N))
-    Ho = Hq if expand else Hkv
+    pp = None if positions is None else _arg(positions, "positions", torch.int32, di, (B, N))
     if q_out is None:
-        q_out = torch.empty((B, Hq, N, d), dtype=torch.bfloat16, device=q.device)
+        q_out = torch.empty((B, Hq, N, d), dtype=bf16, device=q.device)
     if k_out is None:
-        k_out = torch.empty((B, Ho, N, d), dtype=torch.bfloat16, device=q.device)
-    if v is not None and v_out is None:
-        v_out = torch.empty((B, Ho, N, d), dtype=torch.bfloat16, device=q.device)
-    _need_shape(q_out, "q_out", torch.bfloat16, di, (B, Hq, N, d))
-    _need_shape(k_out, "k_out", torch.bfloat16, di, (B, Ho, N, d))
-    if v is not None:
-        _need_shape(v_out, "v_out", torch.bfloat16, di, (B, Ho, N, d))
-    with _on_device(di):
-        st = lib.fa_qk_norm_rope(_ptr(q), _ptr(k), _ptr(v), _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin),
-                                 _ptr(positions), _ptr(q_out), _ptr(k_out), _ptr(v_out), qs, ks, vs, B, N, Hq, Hkv, d,
-                                 rot, max_pos, int(bool(interleaved)), int(bool(expand)), float(eps), wdt, _stream(di))
-    _check(st, "fa_qk_norm_rope")
+        k_out = torch.empty(kv, dtype=bf16, device=q.device)
+    st = _call(di, lib.fa_qk_norm_rope, qp, kp, vp, wqp, wkp, cp, sp, pp, _arg(q_out, "q_out", bf16, di, (B, Hq, N, d)),
+               _arg(k_out, "k_out", bf16, di, kv), vop, qs, ks, vs, B, N, Hq, Hkv, d, rot, max_pos,
+               1 if interleaved else 0, 1 if expand else 0, eps, wdt)
+    if st != FA_OK:
+        raise FaError(st, "fa_qk_norm_rope")
     return q_out, k_out, v_out
 
 
@@ -568,55 +599,42 @@ def qk_norm_rope_bwd(dq, dk, dv, q, k, q_weight, k_weight, cos, sin, positions=N
     returns them; dv may be None) and the forward's other arguments.
 
     ``grads`` is an optional (grad_q, grad_k, grad_v) triple of ``out_dtype`` [B,N,heads,d] tensors with
-    evenly spaced tokens to write into (slices of one buffer will do).  Returns (grad_q, grad_k, grad_v
-    or None, grad_q_weight fp32 [d], grad_k_weight fp32 [d]); the same from run to run.
+    evenly spaced tokens to write into (slices of one buffer will do); ``workspace`` a uint8 CUDA tensor of
+    at least ``qk_norm_rope_bwd_workspace_size`` bytes (allocated here when omitted).  Returns (grad_q,
+    grad_k, grad_v or None, grad_q_weight fp32 [d], grad_k_weight fp32 [d]); the same from run to run.
     """
     lib = _load()
-    di, qs, ks, B, N, Hq, Hkv, d, rot, max_pos, wdt = _rope_args(q, k, q_weight, k_weight, cos, sin)
-    if positions is not None:
-        _need_shape(positions, "positions", torch.int32, di, (B, N))
-    Ho = Hq if expand else Hkv
+    di, B, N, Hq, Hkv, d, rot, max_pos, wdt, (qp, kp, wqp, wkp, cp, sp), qs, ks = _rope_args(q, k, q_weight, k_weight, cos, sin)
+    pp = None if positions is None else _arg(positions, "positions", torch.int32, di, (B, N))
     gt = dq.dtype if isinstance(dq, torch.Tensor) else None
-    _need_shape(dq, "dq", gt, di, (B, Hq, N, d))
-    _need_shape(dk, "dk", gt, di, (B, Ho, N, d))
-    if dv is not None:
-        _need_shape(dv, "dv", gt, di, (B, Ho, N, d))
+    kv = (B, Hq if expand else Hkv, N, d)
+    dqp = _arg(dq, "dq", gt, di, (B, Hq, N, d))
+    dkp = _arg(dk, "dk", gt, di, kv)
+    dvp = None if dv is None else _arg(dv, "dv", gt, di, kv)
     gdt, odt = _odt(gt), _odt(out_dtype)
+    dev = q.device
     if grads is None:
-        grads = (torch.empty((B, N, Hq, d), dtype=out_dtype, device=q.device),
-                 torch.empty((B, N, Hkv, d), dtype=out_dtype, device=q.device),
-                 torch.empty((B, N, Hkv, d), dtype=out_dtype, device=q.device) if dv is not None else None)
+        grads = (torch.empty((B, N, Hq, d), dtype=out_dtype, device=dev),
+                 torch.empty((B, N, Hkv, d), dtype=out_dtype, device=dev),
+                 torch.empty((B, N, Hkv, d), dtype=out_dtype, device=dev) if dv is not None else None)
     gq, gk, gv = grads
-    _, gqs = _token_stride(gq, "grad_q", di, out_dtype)
-    _, gks = _token_stride(gk, "grad_k", di, out_dtype)
-    gvs = 0
     if (gv is None) != (dv is None):
         raise ValueError("grad_v goes with dv")
-    if gv is not None:
-        _, gvs = _token_stride(gv, "grad_v", di, out_dtype)
-    if (tuple(gq.shape) != (B, N, Hq, d) or tuple(gk.shape) != (B, N, Hkv, d)
-            or (gv is not None and tuple(gv.shape) != (B, N, Hkv, d))):
-        raise ValueError("gradient buffers have the wrong shape")
-    gwq = torch.empty((d,), dtype=torch.float32, device=q.device)
-    gwk = torch.empty((d,), dtype=torch.float32, device=q.device)
+    gqp, gqs = _tokens(gq, "grad_q", out_dtype, di, (B, N, Hq, d))
+    gkp, gks = _tokens(gk, "grad_k", out_dtype, di, (B, N, Hkv, d))
+    gvp, gvs = (None, 0) if gv is None else _tokens(gv, "grad_v", out_dtype, di, (B, N, Hkv, d))
+    gw = torch.empty((2, d), dtype=torch.float32, device=dev)
     if workspace is None:
-        workspace = torch.empty(qk_norm_rope_bwd_workspace_size(d), dtype=torch.uint8, device=q.device)
+        workspace = torch.empty(qk_norm_rope_bwd_workspace_size(d), dtype=torch.uint8, device=dev)
     _need(workspace, "workspace", torch.uint8, di)
-    with _on_device(di):
-        st = lib.fa_qk_norm_rope_bwd(_ptr(dq), _ptr(dk), _ptr(dv), _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight),
-                                     _ptr(cos), _ptr(sin), _ptr(positions), _ptr(gq), _ptr(gk), _ptr(gv), _ptr(gwq),
-                                     _ptr(gwk), _ptr(workspace), workspace.numel(), qs, ks, gqs, gks, gvs, B, N, Hq, Hkv,
-                                     d, rot, max_pos, int(bool(interleaved)), int(bool(expand)), float(eps), wdt, gdt, odt,
-                                     _stream(di))
-    _check(st, "fa_qk_norm_rope_bwd")
+    gwp = gw.data_ptr()
+    st = _call(di, lib.fa_qk_norm_rope_bwd, dqp, dkp, dvp, qp, kp, wqp, wkp, cp, sp, pp, gqp, gkp, gvp, gwp, gwp + 4 * d,
+               workspace.data_ptr(), workspace.numel(), qs, ks, gqs, gks, gvs, B, N, Hq, Hkv, d, rot, max_pos,
+               1 if interleaved else 0, 1 if expand else 0, eps, wdt, gdt, odt)
+    if st != FA_OK:
+        raise FaError(st, "fa_qk_norm_rope_bwd")
+    gwq, gwk = gw.unbind()
     return gq, gk, gv, gwq, gwk
-
-
-def _tree_args(di, B, T, parents, n_nodes):
-    if parents is not None:
-        _need_shape(parents, "parents", torch.int32, di, (B, T))
-    if n_nodes is not None:
-        _need_shape(n_nodes, "n_nodes", torch.int32, di, (B,))
 
 
 def qk_norm_rope_append(q, k, v, q_weight, k_weight, cos, sin, k_cache, v_cache, seqlens, parents=None, n_nodes=None,
@@ -630,27 +648,23 @@ def qk_norm_rope_append(q, k, v, q_weight, k_weight, cos, sin, k_cache, v_cache,
     ancestors.  ``seqlens`` stays as it is.  Returns q [B,Hq,T,d] bf16 (0 for tokens that are not there).
     """
     lib = _load()
-    di, qs, ks, B, T, Hq, Hkv, d, rot, max_pos, wdt = _rope_args(q, k, q_weight, k_weight, cos, sin)
-    _, vs = _token_stride(v, "v", di)
-    if tuple(v.shape) != (B, T, Hkv, d):
-        raise ValueError("shape mismatch between k and v")
-    _need(k_cache, "k_cache", torch.bfloat16, di)
-    if k_cache.dim() != 4:
+    di, B, T, Hq, Hkv, d, rot, max_pos, wdt, (qp, kp, wqp, wkp, cp, sp), qs, ks = _rope_args(q, k, q_weight, k_weight, cos, sin)
+    bf16, i32 = torch.bfloat16, torch.int32
+    vp, vs = _tokens(v, "v", bf16, di, (B, T, Hkv, d))
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
         raise ValueError("k_cache must be [B, Hkv, Nk_max, head_dim]")
     Nk_max = k_cache.shape[2]
-    _need_shape(k_cache, "k_cache", torch.bfloat16, di, (B, Hkv, Nk_max, d))
-    _need_shape(v_cache, "v_cache", torch.bfloat16, di, (B, Hkv, Nk_max, d))
-    _need_shape(seqlens, "seqlens", torch.int32, di, (B,))
-    _tree_args(di, B, T, parents, n_nodes)
+    cache = (B, Hkv, Nk_max, d)
     if q_out is None:
-        q_out = torch.empty((B, Hq, T, d), dtype=torch.bfloat16, device=q.device)
-    _need_shape(q_out, "q_out", torch.bfloat16, di, (B, Hq, T, d))
-    with _on_device(di):
-        st = lib.fa_qk_norm_rope_append(_ptr(q), _ptr(k), _ptr(v), _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin),
-                                        _ptr(seqlens), _ptr(parents), _ptr(n_nodes), _ptr(q_out), _ptr(k_cache),
-                                        _ptr(v_cache), qs, ks, vs, B, T, Hq, Hkv, Nk_max, d, rot, max_pos,
-                                        int(bool(interleaved)), float(eps), wdt, _stream(di))
-    _check(st, "fa_qk_norm_rope_append")
+        q_out = torch.empty((B, Hq, T, d), dtype=bf16, device=q.device)
+    st = _call(di, lib.fa_qk_norm_rope_append, qp, kp, vp, wqp, wkp, cp, sp, _arg(seqlens, "seqlens", i32, di, (B,)),
+               None if parents is None else _arg(parents, "parents", i32, di, (B, T)),
+               None if n_nodes is None else _arg(n_nodes, "n_nodes", i32, di, (B,)),
+               _arg(q_out, "q_out", bf16, di, (B, Hq, T, d)), _arg(k_cache, "k_cache", bf16, di, cache),
+               _arg(v_cache, "v_cache", bf16, di, cache), qs, ks, vs, B, T, Hq, Hkv, Nk_max, d, rot, max_pos,
+               1 if interleaved else 0, eps, wdt)
+    if st != FA_OK:
+        raise FaError(st, "fa_qk_norm_rope_append")
     return q_out
 
 
@@ -669,34 +683,29 @@ def decode_tree(q, k_cache, v_cache, seqlens, parents=None, n_nodes=None, scale=
     [B,Hq,T] or None); O = 0 and LSE = -inf for tokens that are not there.
     """
     lib = _load()
-    di = _need(q, "q", torch.bfloat16)
-    _need(k_cache, "k_cache", torch.bfloat16, di)
-    if q.dim() != 4 or k_cache.dim() != 4:
-        raise ValueError("q and the caches must be [B, heads, rows, head_dim]")
-    B, Hq, T, d = q.shape
-    Hkv, Nk_max = k_cache.shape[1], k_cache.shape[2]
-    if tuple(k_cache.shape) != (B, Hkv, Nk_max, d):
-        raise ValueError("shape mismatch between q and k_cache")
-    _need_shape(v_cache, "v_cache", torch.bfloat16, di, (B, Hkv, Nk_max, d))
-    _need_shape(seqlens, "seqlens", torch.int32, di, (B,))
-    _tree_args(di, B, T, parents, n_nodes)
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    di, (B, Hq, T, d) = _first(q, "q")
+    _, (_, Hkv, Nk_max, _) = _first(k_cache, "k_cache")
+    bf16, i32 = torch.bfloat16, torch.int32
+    cache = (B, Hkv, Nk_max, d)
+    dev = q.device
     if workspace is None:
-        workspace = torch.empty(max(decode_tree_workspace_size(Hq, Hkv, T, d, num_sms(q.device)), 256), dtype=torch.uint8,
-                                device=q.device)
+        workspace = torch.empty(max(decode_tree_workspace_size(Hq, Hkv, T, d, num_sms(dev)), 256), dtype=torch.uint8, device=dev)
     _need(workspace, "workspace", torch.uint8, di)
     if out is None:
-        out = torch.empty((B, Hq, T, d), dtype=out_dtype, device=q.device)
-    _need_shape(out, "out", out.dtype, di, (B, Hq, T, d))
+        out = torch.empty_like(q, dtype=out_dtype)
+    odt = _odt(out.dtype)
     if lse is None and return_lse:
-        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device)
-    if lse is not None:
-        _need_shape(lse, "lse", torch.float32, di, (B, Hq, T))
-    with _on_device(di):
-        st = lib.fa_decode_tree(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(seqlens), _ptr(parents), _ptr(n_nodes),
-                                _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), B, Hq, Hkv, T, Nk_max, d, d,
-                                scale, _odt(out.dtype), _stream(di))
-    _check(st, "fa_decode_tree")
+        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=dev)
+    st = _call(di, lib.fa_decode_tree, _arg(q, "q", bf16, di, (B, Hq, T, d)), _arg(k_cache, "k_cache", bf16, di, cache),
+               _arg(v_cache, "v_cache", bf16, di, cache), _arg(seqlens, "seqlens", i32, di, (B,)),
+               None if parents is None else _arg(parents, "parents", i32, di, (B, T)),
+               None if n_nodes is None else _arg(n_nodes, "n_nodes", i32, di, (B,)),
+               _arg(out, "out", out.dtype, di, (B, Hq, T, d)),
+               None if lse is None else _arg(lse, "lse", torch.float32, di, (B, Hq, T)),
+               workspace.data_ptr(), workspace.numel(), B, Hq, Hkv, T, Nk_max, d, d,
+               1.0 / math.sqrt(d) if scale is None else scale, odt)
+    if st != FA_OK:
+        raise FaError(st, "fa_decode_tree")
     return out, lse
 
 
@@ -708,24 +717,22 @@ def cache_compact(k_cache, v_cache, seqlens, accepted, n_accepted, seqlens_out=N
     with T <= 128.  Returns seqlens + n_accepted, in ``seqlens_out`` (which must not overlap seqlens).
     """
     lib = _load()
-    di = _need(k_cache, "k_cache", torch.bfloat16)
-    if k_cache.dim() not in (4, 5):
-        raise ValueError("caches must be [B, Hkv, Nk_max, head_dim], with or without layers before")
-    _need_shape(v_cache, "v_cache", torch.bfloat16, di, tuple(k_cache.shape))
-    B, Hkv, Nk_max, d = k_cache.shape[-4:]
-    L = k_cache.shape[0] if k_cache.dim() == 5 else 1
-    _need(accepted, "accepted", torch.int32, di)
-    if accepted.dim() != 2 or accepted.shape[0] != B:
+    ndim = k_cache.dim() if isinstance(k_cache, torch.Tensor) else 4
+    di, shape = _first(k_cache, "k_cache", 5 if ndim == 5 else 4)
+    B, Hkv, Nk_max, d = shape[-4:]
+    L = shape[0] if ndim == 5 else 1
+    if not isinstance(accepted, torch.Tensor) or accepted.dim() != 2:
         raise ValueError("accepted must be [B, T]")
-    _need_shape(seqlens, "seqlens", torch.int32, di, (B,))
-    _need_shape(n_accepted, "n_accepted", torch.int32, di, (B,))
+    T = accepted.shape[1]
+    bf16, i32 = torch.bfloat16, torch.int32
     if seqlens_out is None:
-        seqlens_out = torch.empty((B,), dtype=torch.int32, device=k_cache.device)
-    _need_shape(seqlens_out, "seqlens_out", torch.int32, di, (B,))
-    with _on_device(di):
-        st = lib.fa_cache_compact(_ptr(k_cache), _ptr(v_cache), _ptr(seqlens), _ptr(accepted), _ptr(n_accepted),
-                                  _ptr(seqlens_out), L, B, Hkv, Nk_max, d, d, accepted.shape[1], _stream(di))
-    _check(st, "fa_cache_compact")
+        seqlens_out = torch.empty_like(seqlens)
+    st = _call(di, lib.fa_cache_compact, _arg(k_cache, "k_cache", bf16, di, shape), _arg(v_cache, "v_cache", bf16, di, shape),
+               _arg(seqlens, "seqlens", i32, di, (B,)), _arg(accepted, "accepted", i32, di, (B, T)),
+               _arg(n_accepted, "n_accepted", i32, di, (B,)), _arg(seqlens_out, "seqlens_out", i32, di, (B,)),
+               L, B, Hkv, Nk_max, d, d, T)
+    if st != FA_OK:
+        raise FaError(st, "fa_cache_compact")
     return seqlens_out
 
 

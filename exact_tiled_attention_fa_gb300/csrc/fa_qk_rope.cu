@@ -69,6 +69,13 @@ struct Share {
         const uint2 a = ld_stream_v2(row + at), b = ld_stream_v2(row + bt);
         return make_uint4(a.x, a.y, b.x, b.y);
     }
+    // The same from shared memory.
+    __device__ __forceinline__ uint4 read(const __nv_bfloat16* row) const
+    {
+        if (INTERLEAVED) return *reinterpret_cast<const uint4*>(row + at);
+        const uint2 a = *reinterpret_cast<const uint2*>(row + at), b = *reinterpret_cast<const uint2*>(row + bt);
+        return make_uint4(a.x, a.y, b.x, b.y);
+    }
     __device__ __forceinline__ void store(__nv_bfloat16* row, uint4 u) const
     {
         if (INTERLEAVED) {
@@ -134,6 +141,19 @@ struct Share {
         }
         const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
         return unpack(make_uint4(__ldg(u + at / 2), __ldg(u + at / 2 + 1), __ldg(u + bt / 2), __ldg(u + bt / 2 + 1)));
+    }
+    // Cosines and sines of the lane's pairs from a token's cosines and, 64 values on, sines.
+    __device__ __forceinline__ Pairs angles_at(const float* t) const
+    {
+        Pairs p;
+        p.x[0] = p.x[1] = make_float2(1.f, 1.f);
+        p.x[2] = p.x[3] = make_float2(0.f, 0.f);
+        if (pair >= 0) {
+            const float4 c = *reinterpret_cast<const float4*>(t + pair), s = *reinterpret_cast<const float4*>(t + 64 + pair);
+            p.x[0] = make_float2(c.x, c.y), p.x[1] = make_float2(c.z, c.w);
+            p.x[2] = make_float2(s.x, s.y), p.x[3] = make_float2(s.z, s.w);
+        }
+        return p;
     }
     // Cosines and sines of the lane's pairs at position pos: c[0], c[1] and s in c[2], c[3].
     __device__ __forceinline__ Pairs angles(const float* cos_t, const float* sin_t, int pos, int rot) const
@@ -373,126 +393,244 @@ cudaError_t launch_rope_t(const RopeParams& p, bool append, int sms, cudaStream_
 
 // ---- backward ----------------------------------------------------------------------------------
 
-// A fixed number of CTAs walk the tokens, a warp a token at a time; the weights' gradients stay in
-// registers (a lane's eight columns of each) until the CTA adds its warps' up in a fixed order and
-// writes one partial row of each, which fa_rope_weight_kernel adds up, also in a fixed order: the
-// result does not change from run to run.
-template <int D, bool INTERLEAVED, bool GF32>
+// Two CTAs for each SM; a warp walks its tokens, of each the query, key and value heads, in batches of U
+// row sets (RPW heads' rows, or RPW heads' copies of one number).  Batches go through a ring of kStages
+// in shared memory, filled by asynchronous copies two batches ahead (a token's angles too), so that the
+// bytes in flight do not depend on registers: with the rows loaded into registers the kernel was bound
+// by latency whatever the split (four rows in flight, 16 warps an SM 214 us on B=64 N=1024 H=16 d=64;
+// two rows, 24 warps 227 us).  The weights' gradients stay in registers (a lane's eight columns of
+// each) until the CTA adds its warps' up in a fixed order and writes one partial row of each, which
+// fa_rope_weight_kernel adds up, also in a fixed order: the result does not change from run to run.
+constexpr int kBwdStages = 3;
+template <bool GF32>
+struct RopeBwdCfg {
+    static constexpr int U = GF32 ? 2 : 4;
+    static constexpr int kSet = GF32 ? 1536 : 1024;          // a row set: x (512 bytes), then the gradient's
+    static constexpr int kAngles = U * kSet * kBwdStages;    // cosines (256 bytes) and sines of a token, a ring too
+    static constexpr int kWarp = kAngles + 512 * kBwdStages; // bytes of a warp
+    static constexpr int kSmem = kRopeWarps * kWarp;
+};
+
+// MULTI: key and value heads have several copies; a row set is then one copy's.
+template <int D, bool INTERLEAVED, bool GF32, bool MULTI>
 __global__ void __launch_bounds__(kRopeWarps * 32, 2) fa_qk_rope_bwd_kernel(const RopeBwdParams p)
 {
     grid_dependency_wait();
     grid_launch_dependents();
+    using C = RopeBwdCfg<GF32>;
     using G = typename std::conditional<GF32, float, __nv_bfloat16>::type;
+    using bf16 = __nv_bfloat16;
     constexpr int LPR = D / 8;
     constexpr int RPW = 32 / LPR;
-    constexpr int U = GF32 ? 2 : 4;  // steps in flight
+    constexpr int U = C::U;
+    extern __shared__ __align__(16) uint8_t rb_smem[];
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int sub = lane % LPR;
     const int grp = lane / LPR;
-    const bool of32 = p.out_dtype == FA_F32;
+    uint8_t* mine = rb_smem + warp * C::kWarp;
+    const uint32_t ring = smem_u32(mine);
     const Share<INTERLEAVED> share(sub, p.rot);
+    const bool of32 = p.out_dtype == FA_F32;
+    const size_t head = static_cast<size_t>(p.N) * D;  // elements of a head of the gradients
+    const int nq = (p.Hq + RPW - 1) / RPW, nk = (p.Hkv + RPW - 1) / RPW;
+    const int kinds = p.dv != nullptr ? 3 : 2;
     const Pairs wq = share.weights(p.wq, p.w_dtype), wk = share.weights(p.wk, p.w_dtype);
     Pairs aq, ak;
 #pragma unroll
     for (int i = 0; i < 4; ++i) aq.x[i] = ak.x[i] = make_float2(0.f, 0.f);
-    const long long tokens = static_cast<long long>(p.B) * p.N;
-    const size_t head = static_cast<size_t>(p.N) * D;  // elements of a head of the gradients
-    // raw gradient elements of a lane
-    struct Raw {
-        uint4 lo, hi;  // bf16: lo; fp32: four elements each
+
+    // Tokens are below 2^31, and unsigned holds a stride or two more.
+    const unsigned tokens = static_cast<unsigned>(p.B) * static_cast<unsigned>(p.N);
+    const unsigned stride = gridDim.x * kRopeWarps;
+    // A place in the walk: token, kind of heads (0 query, 1 key, 2 value), step of RPW heads, copy.
+    struct Place {
+        unsigned token;
+        int kind, step, copy;
     };
-    auto load_g = [&](const G* row) -> Raw {
-        Raw g;
-        if constexpr (GF32) {
-            g.lo = ld_stream_v4(row + share.at);
-            g.hi = ld_stream_v4(row + share.bt);
-        } else {
-            g.lo = share.load(row);
+    const int copies = MULTI ? p.copies : 1;
+    // `sets` row sets on, within the kind; true at its end (and then at the next kind's, or token's, start).
+    auto advance = [&](Place& x, int sets) {
+        if (MULTI && x.kind > 0) {
+            if (++x.copy < copies) return false;
+            x.copy = 0;
         }
-        return g;
+        x.step += sets;
+        if (x.step < (x.kind == 0 ? nq : nk)) return false;
+        x.step = 0;
+        if (++x.kind == kinds) {
+            x.kind = 0;
+            x.token += stride;
+        }
+        return true;
     };
-    auto unpack_g = [&](const Raw& g) -> Pairs {
-        if constexpr (GF32)
-            return share.unpack32(make_float4(__uint_as_float(g.lo.x), __uint_as_float(g.lo.y), __uint_as_float(g.lo.z), __uint_as_float(g.lo.w)),
-                                  make_float4(__uint_as_float(g.hi.x), __uint_as_float(g.hi.y), __uint_as_float(g.hi.z), __uint_as_float(g.hi.w)));
-        else
-            return share.unpack(g.lo);
+    Place ahead{blockIdx.x * kRopeWarps + warp, 0, 0, 0}, at = ahead;
+    auto position = [&](unsigned i) -> int {
+        return p.positions != nullptr ? __ldg(p.positions + i) : static_cast<int>(i % static_cast<unsigned>(p.N));
     };
-    for (long long token = static_cast<long long>(blockIdx.x) * kRopeWarps + warp; token < tokens;
-         token += static_cast<long long>(gridDim.x) * kRopeWarps) {
-        const int b = static_cast<int>(token / p.N);
-        const int t = static_cast<int>(token - static_cast<long long>(b) * p.N);
-        const int pos = checked_position(p.positions != nullptr ? p.positions[token] : t, p.max_pos, p.status);
-        const Pairs cs = share.angles(p.cos_t, p.sin_t, pos, p.rot);
-        // The steps of one kind of heads.  x: the projections' rows (nullptr for values), gi: the
-        // gradients' rows, `copies` for each head, go: the rows written.
-        auto walk = [&](const __nv_bfloat16* xi, const G* gi, void* go, int heads, int copies, const Pairs& w, Pairs& acc) {
-            const int n = (heads + RPW - 1) / RPW;
-            for (int i = 0; i < n; i += U) {
-                uint4 xr[U];
-                Raw gr[U];
+    int pos = ahead.token < tokens ? position(ahead.token) : 0;  // of the next token to be copied
+    int token_slot = 0;                                          // of its angles
+    const int half = p.rot >> 1;
+
+    size_t token_b = 0, token_t = 0;  // sequence of the token being copied, and its elements into a head
+    // The copies of one batch into a stage: at most U row sets of one kind.
+    auto copy_batch = [&](int stage) {
+        if (ahead.token < tokens) {
+            const int kind = ahead.kind;
+            if (kind == 0 && ahead.step == 0) {  // a new token: its angles
+                token_b = ahead.token / static_cast<unsigned>(p.N);
+                token_t = (ahead.token - token_b * static_cast<unsigned>(p.N)) * D;
+                const size_t i = static_cast<size_t>(checked_position(pos, p.max_pos, p.status)) * half;
+                const int piece = lane & 15;
+                if (4 * piece < half)
+                    cp_async16(ring + C::kAngles + token_slot * 512 + (lane >> 4) * 256 + piece * 16,
+                               (lane < 16 ? p.cos_t : p.sin_t) + i + 4 * piece, 16);
+                token_slot = token_slot == kBwdStages - 1 ? 0 : token_slot + 1;
+                if (ahead.token + stride < tokens) pos = position(ahead.token + stride);
+            }
+            const int heads = kind == 0 ? p.Hq : p.Hkv;
+            const size_t each = MULTI && kind > 0 ? copies * head : head;  // elements of a head's copies
+            const bf16* x = (kind == 0 ? reinterpret_cast<const bf16*>(p.q) + static_cast<long long>(ahead.token) * p.q_stride
+                                       : reinterpret_cast<const bf16*>(p.k) + static_cast<long long>(ahead.token) * p.k_stride) +
+                            lane * 8;  // a step's rows are 256 elements, whatever the head size
+            const G* g = reinterpret_cast<const G*>(kind == 0 ? p.dq : kind == 1 ? p.dk : p.dv) + token_b * (heads * each) + token_t;
+            const uint32_t to = ring + stage * (U * C::kSet);
+            // one row set; zeros where there is no head
+            auto copy_set = [&](int u, const bf16* xs, const G* row, int h) {
+                const int bytes = h < heads ? 16 : 0;
+                if (kind < 2 && (!MULTI || ahead.copy == 0)) cp_async16(to + u * C::kSet + lane * 16, h < heads ? xs : x, bytes);
+                if constexpr (GF32) {
+                    cp_async16(to + u * C::kSet + 512 + grp * (D * 4) + sub * 16, row + sub * 4, bytes);
+                    cp_async16(to + u * C::kSet + 512 + grp * (D * 4) + (LPR + sub) * 16, row + (LPR + sub) * 4, bytes);
+                } else {
+                    cp_async16(to + u * C::kSet + 512 + lane * 16, row + sub * 8, bytes);
+                }
+            };
+            if constexpr (MULTI) {
+                bool end = false;
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const int h = (i + u) * RPW + grp;
-                    xr[u] = gr[u].lo = gr[u].hi = make_uint4(0, 0, 0, 0);
-                    if (i + u < n && h < heads) {
-                        if (xi != nullptr) xr[u] = share.load(xi + h * D);
-                        gr[u] = load_g(gi + static_cast<size_t>(h) * copies * head);
-                    }
+                    if (end) continue;
+                    const int h = ahead.step * RPW + grp;
+                    copy_set(u, x + ahead.step * 256, g + (h < heads ? h : 0) * each + ahead.copy * head, h);
+                    end = advance(ahead, 1);
                 }
+            } else {
+                const int n = (kind == 0 ? nq : nk) - ahead.step;
+                const G* row = g + static_cast<size_t>(ahead.step * RPW + grp) * each;
+                const bf16* xs = x + ahead.step * 256;
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    if (i + u >= n) break;  // uniform
-                    const int h = (i + u) * RPW + grp;
-                    Pairs g = unpack_g(gr[u]);
-                    if (copies > 1 && h < heads) {
-#pragma unroll 4
-                        for (int c = 1; c < copies; ++c) {
-                            const Pairs y = unpack_g(load_g(gi + (static_cast<size_t>(h) * copies + c) * head));
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) g.x[e] = __fadd2_rn(g.x[e], y.x[e]);
-                        }
-                    }
-                    if (xi != nullptr) {
-                        const Pairs x = share.unpack(xr[u]);
-                        Pairs hb, z;  // the gradient turned back, and times the weights
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            hb.x[e] = fma2(g.x[e], cs.x[e], mul2(g.x[2 + e], cs.x[2 + e]));
-                            hb.x[2 + e] = fma2(g.x[2 + e], cs.x[e], neg2(mul2(g.x[e], cs.x[2 + e])));
-                        }
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) z.x[e] = mul2(w.x[e], hb.x[e]);
-                        const float ss = row_sum<LPR>(dot(x, x));
-                        const float sz = row_sum<LPR>(dot(x, z));
-                        const float r = rsqrtf(ss * (1.f / D) + p.eps);
-                        const float f = -(r * r) * sz * (1.f / D);
-                        const float2 rr = make_float2(r, r), ff = make_float2(f, f);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            // 0 for lanes without a row
-                            acc.x[e] = fma2(hb.x[e], mul2(x.x[e], rr), acc.x[e]);
-                            g.x[e] = mul2(rr, fma2(x.x[e], ff, z.x[e]));
-                        }
-                    }
-                    if (h < heads) {
-                        if (of32) share.store32(reinterpret_cast<float*>(go) + h * D, g);
-                        else share.store(reinterpret_cast<__nv_bfloat16*>(go) + h * D, share.pack(g));
+                    if (u < n) {
+                        const int h = (ahead.step + u) * RPW + grp;
+                        copy_set(u, xs + u * 256, h < heads ? row : g, h);
+                        row += RPW * each;
                     }
                 }
+                advance(ahead, U);
+            }
+        }
+        cp_async_commit();
+    };
+    for (int i = 0; i < kBwdStages - 1; ++i) copy_batch(i);
+
+    Pairs cs, g;
+    uint4 xr = make_uint4(0, 0, 0, 0);
+    int cs_slot = 0;
+    // one row: its gradient g to the projection's
+    auto finish = [&](const Pairs& w, Pairs& acc) {
+        const Pairs x = share.unpack(xr);
+        Pairs hb, z;  // the gradient turned back, and times the weights
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            hb.x[e] = fma2(g.x[e], cs.x[e], mul2(g.x[2 + e], cs.x[2 + e]));
+            hb.x[2 + e] = fma2(g.x[2 + e], cs.x[e], neg2(mul2(g.x[e], cs.x[2 + e])));
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z.x[e] = mul2(w.x[e], hb.x[e]);
+        const float ss = row_sum<LPR>(dot(x, x));
+        const float sz = row_sum<LPR>(dot(x, z));
+        const float r = rsqrtf(ss * (1.f / D) + p.eps);
+        const float f = -(r * r) * sz * (1.f / D);
+        const float2 rr = make_float2(r, r), ff = make_float2(f, f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            acc.x[e] = fma2(hb.x[e], mul2(x.x[e], rr), acc.x[e]);  // 0 for lanes without a row
+            g.x[e] = mul2(rr, fma2(x.x[e], ff, z.x[e]));
+        }
+    };
+    int stage = 0;
+    while (at.token < tokens) {
+        copy_batch(stage == 0 ? kBwdStages - 1 : stage - 1);
+        cp_async_wait<kBwdStages - 1>();
+        __syncwarp();
+        const int kind = at.kind;
+        if (kind == 0 && at.step == 0) {
+            cs = share.angles_at(reinterpret_cast<const float*>(mine + C::kAngles + cs_slot * 512));
+            cs_slot = cs_slot == kBwdStages - 1 ? 0 : cs_slot + 1;
+        }
+        const uint8_t* from = mine + stage * (U * C::kSet) + grp * (D * 2);
+        char* out = static_cast<char*>(kind == 0 ? p.gq : kind == 1 ? p.gk : p.gv);
+        const long long row = static_cast<long long>(at.token) * (kind == 0 ? p.gq_stride : kind == 1 ? p.gk_stride : p.gv_stride);
+        const int heads = kind == 0 ? p.Hq : p.Hkv;
+        auto gradient = [&](int u) -> Pairs {
+            if constexpr (GF32) {
+                const float* sg = reinterpret_cast<const float*>(from + u * C::kSet + 512 + grp * (D * 2));
+                return share.unpack32(*reinterpret_cast<const float4*>(sg + share.at), *reinterpret_cast<const float4*>(sg + share.bt));
+            } else {
+                return share.unpack(share.read(reinterpret_cast<const bf16*>(from + u * C::kSet + 512)));
             }
         };
-        auto out = [&](void* o, long long stride) -> void* { return static_cast<char*>(o) + token * stride * (of32 ? 4 : 2); };
-        const size_t row = static_cast<size_t>(t) * D;
-        const size_t kv = static_cast<size_t>(b) * p.Hkv * p.copies * head + row;
-        walk(reinterpret_cast<const __nv_bfloat16*>(p.q) + token * p.q_stride,
-             reinterpret_cast<const G*>(p.dq) + static_cast<size_t>(b) * p.Hq * head + row, out(p.gq, p.gq_stride), p.Hq, 1, wq, aq);
-        walk(reinterpret_cast<const __nv_bfloat16*>(p.k) + token * p.k_stride, reinterpret_cast<const G*>(p.dk) + kv,
-             out(p.gk, p.gk_stride), p.Hkv, p.copies, wk, ak);
-        if (p.dv != nullptr) walk(nullptr, reinterpret_cast<const G*>(p.dv) + kv, out(p.gv, p.gv_stride), p.Hkv, p.copies, wk, ak);
+        auto write = [&](int step) {
+            const int h = step * RPW + grp;
+            if (h < heads) {
+                if (of32) share.store32(reinterpret_cast<float*>(out) + row + h * D, g);
+                else share.store(reinterpret_cast<bf16*>(out) + row + h * D, share.pack(g));
+            }
+        };
+        if constexpr (MULTI) {
+            bool end = false;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (end) continue;  // uniform
+                const Pairs y = gradient(u);
+                if (at.copy == 0) {
+                    g = y;
+                    if (kind < 2) xr = share.read(reinterpret_cast<const bf16*>(from + u * C::kSet));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) g.x[e] = __fadd2_rn(g.x[e], y.x[e]);
+                }
+                if (kind == 0 || at.copy == copies - 1) {
+                    if (kind == 0) finish(wq, aq);
+                    else if (kind == 1) finish(wk, ak);
+                    write(at.step);
+                }
+                end = advance(at, 1);
+            }
+        } else {
+            const int n = (kind == 0 ? nq : nk) - at.step;
+            auto sets = [&](auto turn) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (u < n) {
+                        g = gradient(u);
+                        turn(u);
+                        write(at.step + u);
+                    }
+                }
+            };
+            auto read_x = [&](int u) { xr = share.read(reinterpret_cast<const bf16*>(from + u * C::kSet)); };
+            if (kind == 0) sets([&](int u) { read_x(u), finish(wq, aq); });
+            else if (kind == 1) sets([&](int u) { read_x(u), finish(wk, ak); });
+            else sets([](int) {});
+            advance(at, U);
+        }
+        __syncwarp();  // the stage may be filled again
+        stage = stage == kBwdStages - 1 ? 0 : stage + 1;
     }
-    __shared__ __align__(16) float sm[kRopeWarps][2][D];
+    __syncthreads();  // (no copy is in flight: the batches ahead of the last were empty)
+    float(*sm)[2][D] = reinterpret_cast<float(*)[2][D]>(rb_smem);
 #pragma unroll
     for (int o = LPR; o < 32; o <<= 1)
 #pragma unroll
@@ -536,20 +674,38 @@ __global__ void __launch_bounds__(1024) fa_rope_weight_kernel(const float* part,
     }
 }
 
+template <int D, bool INTERLEAVED, bool GF32, bool MULTI>
+cudaError_t launch_rope_bwd_g(const RopeBwdParams& p, int grid, cudaStream_t st)
+{
+    auto kern = fa_qk_rope_bwd_kernel<D, INTERLEAVED, GF32, MULTI>;
+    static bool configured[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!configured[dev]) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, RopeBwdCfg<GF32>::kSmem);
+        if (e != cudaSuccess) return e;
+        configured[dev] = true;
+    }
+    return launch_pdl(kern, static_cast<unsigned>(grid), kRopeWarps * 32, RopeBwdCfg<GF32>::kSmem, st, p);
+}
+
 template <int D, bool INTERLEAVED>
 cudaError_t launch_rope_bwd_t(const RopeBwdParams& p, int sms, cudaStream_t st)
 {
     const long long tokens = static_cast<long long>(p.B) * p.N;
-    long long grid = (tokens + kRopeWarps - 1) / kRopeWarps;
-    const long long most = 4LL * sms < kRopeBwdCtas ? 4LL * sms : kRopeBwdCtas;
-    if (grid > most) grid = most;
-    const unsigned g = static_cast<unsigned>(grid);
-    cudaError_t e = p.g_dtype == FA_F32
-                        ? launch_pdl(fa_qk_rope_bwd_kernel<D, INTERLEAVED, true>, g, kRopeWarps * 32, 0, st, p)
-                        : launch_pdl(fa_qk_rope_bwd_kernel<D, INTERLEAVED, false>, g, kRopeWarps * 32, 0, st, p);
+    long long n = (tokens + kRopeWarps - 1) / kRopeWarps;
+    if (n > 2LL * sms) n = 2LL * sms;
+    if (n > kRopeBwdCtas) n = kRopeBwdCtas;
+    const int grid = static_cast<int>(n);
+    const bool f32 = p.g_dtype == FA_F32;
+    const cudaError_t e = p.copies > 1 ? (f32 ? launch_rope_bwd_g<D, INTERLEAVED, true, true>(p, grid, st)
+                                              : launch_rope_bwd_g<D, INTERLEAVED, false, true>(p, grid, st))
+                                       : (f32 ? launch_rope_bwd_g<D, INTERLEAVED, true, false>(p, grid, st)
+                                              : launch_rope_bwd_g<D, INTERLEAVED, false, false>(p, grid, st));
     if (e != cudaSuccess) return e;
-    return launch_pdl(fa_rope_weight_kernel, dim3(D / 32, 2), 1024, 0, st, static_cast<const float*>(p.part),
-                      static_cast<int>(grid), D, p.gwq, p.gwk);
+    return launch_pdl(fa_rope_weight_kernel, dim3(D / 32, 2), 1024, 0, st, static_cast<const float*>(p.part), grid, D, p.gwq, p.gwk);
 }
 
 }  // namespace

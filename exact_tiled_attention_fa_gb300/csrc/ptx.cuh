@@ -495,4 +495,14 @@ __device__ __forceinline__ uint2 ld_stream_v2(const void* p)
     return r;
 }
 
+// Asynchronous 16-byte copy global -> shared past L1: `bytes` (16 or 0) are read, the rest is zeros.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes)
+{
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most N of the thread's committed groups are in flight.
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 }  // namespace fa
