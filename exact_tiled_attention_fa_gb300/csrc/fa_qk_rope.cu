@@ -260,11 +260,14 @@ struct Steps {
 };
 
 // Grid (tokens / kRopeWarps, step chunks).  A warp: one token, steps blockIdx.y * chunk .. + chunk.
+// Four rows in flight and four CTAs an SM (64 registers): B=64 N=1024 H=16 d=64 126 us, 6.4 TB/s of
+// reads and writes; three CTAs 136, two with eight rows 168, five (48 registers, which spill) 145.  Rows
+// through a ring of asynchronous copies, as in the backward kernel: 128 us there, 6-10 % slower at d = 128.
 // APPEND: token t of sequence b is node t of its tree, at position seqlens[b] + depth, and its key
 // and value go to cache row seqlens[b] + t.  Nodes past n_nodes[b] have zero query rows and no cache
 // row.
 template <int D, bool INTERLEAVED, bool APPEND>
-__global__ void __launch_bounds__(kRopeWarps * 32, 3) fa_qk_rope_kernel(const RopeParams p, int chunk)
+__global__ void __launch_bounds__(kRopeWarps * 32, 4) fa_qk_rope_kernel(const RopeParams p, int chunk)
 {
     grid_dependency_wait();
     grid_launch_dependents();
@@ -317,6 +320,13 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 3) fa_qk_rope_kernel(const Ro
     } else {
         pos = checked_position(p.positions != nullptr ? p.positions[token] : t, p.max_pos, p.status);
     }
+    if (APPEND && !live) {  // the whole warp: zero query rows, nothing else
+        bf16* out = reinterpret_cast<bf16*>(p.q_out) + (static_cast<size_t>(b) * p.Hq * p.N + t) * D;
+        for (int i = begin; i < min(end, steps.nq); ++i)
+            if (i * RPW + grp < p.Hq)
+                *reinterpret_cast<uint4*>(out + static_cast<size_t>(i * RPW + grp) * p.N * D + sub * 8) = make_uint4(0, 0, 0, 0);
+        return;
+    }
     const Pairs cs = share.angles(p.cos_t, p.sin_t, pos, p.rot);
     auto turned = [&](const Turn& turn, uint4 u) -> uint4 {
         const Pairs x = share.unpack(u);
@@ -332,14 +342,12 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 3) fa_qk_rope_kernel(const Ro
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (i + u >= to) break;  // uniform
-                uint4 y = turned(turn, raw[u]);
-                if (APPEND && !live) y = make_uint4(0, 0, 0, 0);
+                const uint4 y = turned(turn, raw[u]);
                 const int h = (i + u) * RPW + grp;
                 if (h < p.Hq) share.store(out + h * head, y);
             }
         }
     }
-    if (APPEND && !live) return;  // the whole warp
     const size_t kv_rows = APPEND ? p.Nk_max : p.N;
     const size_t head = static_cast<size_t>(p.copies) * kv_rows * D;
     const size_t at = static_cast<size_t>(b) * p.Hkv * head + static_cast<size_t>(row) * D;
@@ -381,10 +389,11 @@ cudaError_t launch_rope_t(const RopeParams& p, bool append, int sms, cudaStream_
     constexpr int RPW = 32 / (D / 8);
     const long long tokens = static_cast<long long>(p.B) * p.N;
     const long long blocks = (tokens + kRopeWarps - 1) / kRopeWarps;
-    // With few tokens the steps of one are shared out among warps
+    // With few tokens the steps of one are shared out among warps, as far as two rounds of CTAs go
     const int steps = Steps<RPW>(p.Hq, p.Hkv, p.v != nullptr).n;
-    long long chunks = (4LL * sms + blocks - 1) / blocks;
+    long long chunks = 8LL * sms / blocks;
     if (chunks > steps) chunks = steps;
+    if (chunks < 1) chunks = 1;
     const int chunk = static_cast<int>((steps + chunks - 1) / chunks);
     const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((steps + chunk - 1) / chunk));
     return append ? launch_pdl(fa_qk_rope_kernel<D, INTERLEAVED, true>, grid, kRopeWarps * 32, 0, st, p, chunk)
