@@ -470,88 +470,22 @@ def merge_states(o_parts, lse_parts, out_dtype=torch.float32, out=None, lse=None
 
 
 # The operators below are called once or twice a layer in a serving loop, where a call's host time is
-# most of it: each argument is checked and its pointer taken in one step, and the messages are made
-# only when something is wrong.
+# most of it: their arguments are checked and marshalled natively (csrc/fa_binding.cpp).  A call there
+# returns its outputs as a tuple, or the status of the C ABI.
 
-_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-
-
-def _refuse(t, name, dtype, device, shape):
-    """Says what is wrong with an argument that failed its check."""
-    _need(t, name, dtype, device)
-    raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+_binding = None
 
 
-def _arg(t, name, dtype, device, shape):
-    """Data pointer of a contiguous tensor of this type and shape on this device (an index)."""
-    try:
-        if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
-            return t.data_ptr()
-    except AttributeError:
-        pass
-    _refuse(t, name, dtype, device, shape)
-
-
-def _first(t, name, ndim=4):
-    """Device index and shape of a call's first argument."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    di = t.get_device()
-    if t.dtype is not torch.bfloat16:
-        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if di < 0:
-        raise ValueError(f"{name} must be on a CUDA device")
-    shape = t.shape
-    if len(shape) != ndim:
-        raise ValueError(f"{name} must have {ndim} dimensions")
-    return di, shape
-
-
-def _tokens(t, name, dtype, device, shape):
-    """Data pointer and token stride of [B, N, heads, head_dim] with its heads contiguous and its tokens
-    evenly spaced: a whole tensor, or a slice of the heads of one."""
-    try:
-        if t.dtype is dtype and t.shape == shape and t.get_device() == device:
-            B, N, H, d = shape
-            if t.is_contiguous():
-                return t.data_ptr(), H * d
-            sb, sn, sh, sd = t.stride()
-            tok = sn if N > 1 else sb if B > 1 else H * d
-            if (d == 1 or sd == 1) and (H == 1 or sh == d) and (B == 1 or sb == N * tok):
-                return t.data_ptr(), tok
-            raise ValueError(f"{name} must have its heads contiguous and its tokens evenly spaced")
-    except AttributeError:
-        pass
-    _refuse(t.contiguous() if isinstance(t, torch.Tensor) else t, name, dtype, device, shape)
-
-
-def _call(device, f, *args):
-    """Calls a library function on the device's current stream, which it takes last."""
-    if _current_device() == device:
-        return f(*args, _stream(device))
-    with torch.cuda.device(device):
-        return f(*args, _stream(device))
-
-
-def _rope_args(q, k, q_weight, k_weight, cos, sin):
-    """What the norm's forms share, checked: (device, sizes, weight dtype, pointers, token strides)."""
-    di, (B, N, Hq, d) = _first(q, "q")
-    if not isinstance(k, torch.Tensor) or k.dim() != 4:
-        raise ValueError("k must be [B, N, heads, head_dim]")
-    Hkv = k.shape[2]
-    qp, qs = _tokens(q, "q", torch.bfloat16, di, (B, N, Hq, d))
-    kp, ks = _tokens(k, "k", torch.bfloat16, di, (B, N, Hkv, d))
-    wt = q_weight.dtype if isinstance(q_weight, torch.Tensor) else None
-    wqp = _arg(q_weight, "q_weight", wt, di, (d,))
-    wkp = _arg(k_weight, "k_weight", wt, di, (d,))
-    if wt is not torch.bfloat16 and wt is not torch.float32:
-        raise ValueError("weights must be bfloat16 or float32")
-    if not isinstance(cos, torch.Tensor) or cos.dim() != 2:
-        raise ValueError("cos and sin must be [max_pos, rot / 2]")
-    max_pos, half = shape = cos.shape
-    cp = _arg(cos, "cos", torch.float32, di, shape)
-    sp = _arg(sin, "sin", torch.float32, di, shape)
-    return di, B, N, Hq, Hkv, d, 2 * half, max_pos, FA_BF16 if wt is torch.bfloat16 else FA_F32, (qp, kp, wqp, wkp, cp, sp), qs, ks
+def _native():
+    global _binding
+    if _binding is None:
+        _load()
+        try:
+            from . import _fa_binding
+        except ImportError as e:
+            raise RuntimeError(f"_fa_binding.so is not built or does not load ({e}); run __graft_entry__.build() first") from e
+        _binding = _fa_binding
+    return _binding
 
 
 def qk_norm_rope(q, k, v, q_weight, k_weight, cos, sin, positions=None, eps=1e-6, interleaved=False, expand=False,
@@ -564,29 +498,11 @@ def qk_norm_rope(q, k, v, q_weight, k_weight, cos, sin, positions=None, eps=1e-6
     (i, i + rot/2), or (2i, 2i+1) with ``interleaved``.  With ``expand`` key/value heads are repeated for
     their query heads.  Returns (q [B,Hq,N,d], k, v [B,Hkv or Hq,N,d] or None), bf16.
     """
-    lib = _load()
-    di, B, N, Hq, Hkv, d, rot, max_pos, wdt, (qp, kp, wqp, wkp, cp, sp), qs, ks = _rope_args(q, k, q_weight, k_weight, cos, sin)
-    bf16 = torch.bfloat16
-    kv = (B, Hq if expand else Hkv, N, d)
-    vp, vs, vop = None, 0, None
-    if v is not None:
-        vp, vs = _tokens(v, "v", bf16, di, (B, N, Hkv, d))
-        if v_out is None:
-            v_out = torch.empty(kv, dtype=bf16, device=q.device)
-        vop = _arg(v_out, "v_out", bf16, di, kv)
-    elif v_out is not None:
-        raise ValueError("v_out without v")
-    pp = None if positions is None else _arg(positions, "positions", torch.int32, di, (B, N))
-    if q_out is None:
-        q_out = torch.empty((B, Hq, N, d), dtype=bf16, device=q.device)
-    if k_out is None:
-        k_out = torch.empty(kv, dtype=bf16, device=q.device)
-    st = _call(di, lib.fa_qk_norm_rope, qp, kp, vp, wqp, wkp, cp, sp, pp, _arg(q_out, "q_out", bf16, di, (B, Hq, N, d)),
-               _arg(k_out, "k_out", bf16, di, kv), vop, qs, ks, vs, B, N, Hq, Hkv, d, rot, max_pos,
-               1 if interleaved else 0, 1 if expand else 0, eps, wdt)
-    if st != FA_OK:
-        raise FaError(st, "fa_qk_norm_rope")
-    return q_out, k_out, v_out
+    r = (_binding or _native()).qk_norm_rope(q, k, v, q_weight, k_weight, cos, sin, positions, eps, interleaved, expand,
+                                             q_out, k_out, v_out)
+    if type(r) is int:
+        raise FaError(r, "fa_qk_norm_rope")
+    return r
 
 
 def qk_norm_rope_bwd_workspace_size(d):
@@ -603,38 +519,12 @@ def qk_norm_rope_bwd(dq, dk, dv, q, k, q_weight, k_weight, cos, sin, positions=N
     at least ``qk_norm_rope_bwd_workspace_size`` bytes (allocated here when omitted).  Returns (grad_q,
     grad_k, grad_v or None, grad_q_weight fp32 [d], grad_k_weight fp32 [d]); the same from run to run.
     """
-    lib = _load()
-    di, B, N, Hq, Hkv, d, rot, max_pos, wdt, (qp, kp, wqp, wkp, cp, sp), qs, ks = _rope_args(q, k, q_weight, k_weight, cos, sin)
-    pp = None if positions is None else _arg(positions, "positions", torch.int32, di, (B, N))
-    gt = dq.dtype if isinstance(dq, torch.Tensor) else None
-    kv = (B, Hq if expand else Hkv, N, d)
-    dqp = _arg(dq, "dq", gt, di, (B, Hq, N, d))
-    dkp = _arg(dk, "dk", gt, di, kv)
-    dvp = None if dv is None else _arg(dv, "dv", gt, di, kv)
-    gdt, odt = _odt(gt), _odt(out_dtype)
-    dev = q.device
-    if grads is None:
-        grads = (torch.empty((B, N, Hq, d), dtype=out_dtype, device=dev),
-                 torch.empty((B, N, Hkv, d), dtype=out_dtype, device=dev),
-                 torch.empty((B, N, Hkv, d), dtype=out_dtype, device=dev) if dv is not None else None)
-    gq, gk, gv = grads
-    if (gv is None) != (dv is None):
-        raise ValueError("grad_v goes with dv")
-    gqp, gqs = _tokens(gq, "grad_q", out_dtype, di, (B, N, Hq, d))
-    gkp, gks = _tokens(gk, "grad_k", out_dtype, di, (B, N, Hkv, d))
-    gvp, gvs = (None, 0) if gv is None else _tokens(gv, "grad_v", out_dtype, di, (B, N, Hkv, d))
-    gw = torch.empty((2, d), dtype=torch.float32, device=dev)
-    if workspace is None:
-        workspace = torch.empty(qk_norm_rope_bwd_workspace_size(d), dtype=torch.uint8, device=dev)
-    _need(workspace, "workspace", torch.uint8, di)
-    gwp = gw.data_ptr()
-    st = _call(di, lib.fa_qk_norm_rope_bwd, dqp, dkp, dvp, qp, kp, wqp, wkp, cp, sp, pp, gqp, gkp, gvp, gwp, gwp + 4 * d,
-               workspace.data_ptr(), workspace.numel(), qs, ks, gqs, gks, gvs, B, N, Hq, Hkv, d, rot, max_pos,
-               1 if interleaved else 0, 1 if expand else 0, eps, wdt, gdt, odt)
-    if st != FA_OK:
-        raise FaError(st, "fa_qk_norm_rope_bwd")
-    gwq, gwk = gw.unbind()
-    return gq, gk, gv, gwq, gwk
+    gq, gk, gv = grads if grads is not None else (None, None, None)
+    r = (_binding or _native()).qk_norm_rope_bwd(dq, dk, dv, q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved,
+                                                 expand, _odt(out_dtype), gq, gk, gv, workspace)
+    if type(r) is int:
+        raise FaError(r, "fa_qk_norm_rope_bwd")
+    return r
 
 
 def qk_norm_rope_append(q, k, v, q_weight, k_weight, cos, sin, k_cache, v_cache, seqlens, parents=None, n_nodes=None,
@@ -647,25 +537,11 @@ def qk_norm_rope_append(q, k, v, q_weight, k_weight, cos, sin, k_cache, v_cache,
     there are (None: all).  Token t goes to cache row seqlens + t, at position seqlens + the number of its
     ancestors.  ``seqlens`` stays as it is.  Returns q [B,Hq,T,d] bf16 (0 for tokens that are not there).
     """
-    lib = _load()
-    di, B, T, Hq, Hkv, d, rot, max_pos, wdt, (qp, kp, wqp, wkp, cp, sp), qs, ks = _rope_args(q, k, q_weight, k_weight, cos, sin)
-    bf16, i32 = torch.bfloat16, torch.int32
-    vp, vs = _tokens(v, "v", bf16, di, (B, T, Hkv, d))
-    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
-        raise ValueError("k_cache must be [B, Hkv, Nk_max, head_dim]")
-    Nk_max = k_cache.shape[2]
-    cache = (B, Hkv, Nk_max, d)
-    if q_out is None:
-        q_out = torch.empty((B, Hq, T, d), dtype=bf16, device=q.device)
-    st = _call(di, lib.fa_qk_norm_rope_append, qp, kp, vp, wqp, wkp, cp, sp, _arg(seqlens, "seqlens", i32, di, (B,)),
-               None if parents is None else _arg(parents, "parents", i32, di, (B, T)),
-               None if n_nodes is None else _arg(n_nodes, "n_nodes", i32, di, (B,)),
-               _arg(q_out, "q_out", bf16, di, (B, Hq, T, d)), _arg(k_cache, "k_cache", bf16, di, cache),
-               _arg(v_cache, "v_cache", bf16, di, cache), qs, ks, vs, B, T, Hq, Hkv, Nk_max, d, rot, max_pos,
-               1 if interleaved else 0, eps, wdt)
-    if st != FA_OK:
-        raise FaError(st, "fa_qk_norm_rope_append")
-    return q_out
+    r = (_binding or _native()).qk_norm_rope_append(q, k, v, q_weight, k_weight, cos, sin, k_cache, v_cache, seqlens, parents,
+                                                    n_nodes, eps, interleaved, q_out)
+    if type(r) is int:
+        raise FaError(r, "fa_qk_norm_rope_append")
+    return r[0]
 
 
 def decode_tree_workspace_size(Hq, Hkv, T, d, num_sms):
@@ -682,31 +558,12 @@ def decode_tree(q, k_cache, v_cache, seqlens, parents=None, n_nodes=None, scale=
     ``decode_tree_workspace_size`` bytes (allocated here when omitted).  Returns (O [B,Hq,T,d], LSE fp32
     [B,Hq,T] or None); O = 0 and LSE = -inf for tokens that are not there.
     """
-    lib = _load()
-    di, (B, Hq, T, d) = _first(q, "q")
-    _, (_, Hkv, Nk_max, _) = _first(k_cache, "k_cache")
-    bf16, i32 = torch.bfloat16, torch.int32
-    cache = (B, Hkv, Nk_max, d)
-    dev = q.device
-    if workspace is None:
-        workspace = torch.empty(max(decode_tree_workspace_size(Hq, Hkv, T, d, num_sms(dev)), 256), dtype=torch.uint8, device=dev)
-    _need(workspace, "workspace", torch.uint8, di)
-    if out is None:
-        out = torch.empty_like(q, dtype=out_dtype)
-    odt = _odt(out.dtype)
-    if lse is None and return_lse:
-        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=dev)
-    st = _call(di, lib.fa_decode_tree, _arg(q, "q", bf16, di, (B, Hq, T, d)), _arg(k_cache, "k_cache", bf16, di, cache),
-               _arg(v_cache, "v_cache", bf16, di, cache), _arg(seqlens, "seqlens", i32, di, (B,)),
-               None if parents is None else _arg(parents, "parents", i32, di, (B, T)),
-               None if n_nodes is None else _arg(n_nodes, "n_nodes", i32, di, (B,)),
-               _arg(out, "out", out.dtype, di, (B, Hq, T, d)),
-               None if lse is None else _arg(lse, "lse", torch.float32, di, (B, Hq, T)),
-               workspace.data_ptr(), workspace.numel(), B, Hq, Hkv, T, Nk_max, d, d,
-               1.0 / math.sqrt(d) if scale is None else scale, odt)
-    if st != FA_OK:
-        raise FaError(st, "fa_decode_tree")
-    return out, lse
+    sms = num_sms(q.device) if workspace is None and isinstance(q, torch.Tensor) and q.is_cuda else 0
+    r = (_binding or _native()).decode_tree(q, k_cache, v_cache, seqlens, parents, n_nodes, scale, _odt(out_dtype), out, lse,
+                                            return_lse, workspace, sms)
+    if type(r) is int:
+        raise FaError(r, "fa_decode_tree")
+    return r
 
 
 def cache_compact(k_cache, v_cache, seqlens, accepted, n_accepted, seqlens_out=None):
@@ -716,24 +573,10 @@ def cache_compact(k_cache, v_cache, seqlens, accepted, n_accepted, seqlens_out=N
     caches [B,Hkv,Nk_max,d] or [L,B,Hkv,Nk_max,d] bf16, seqlens and n_accepted int32 [B], accepted int32 [B,T]
     with T <= 128.  Returns seqlens + n_accepted, in ``seqlens_out`` (which must not overlap seqlens).
     """
-    lib = _load()
-    ndim = k_cache.dim() if isinstance(k_cache, torch.Tensor) else 4
-    di, shape = _first(k_cache, "k_cache", 5 if ndim == 5 else 4)
-    B, Hkv, Nk_max, d = shape[-4:]
-    L = shape[0] if ndim == 5 else 1
-    if not isinstance(accepted, torch.Tensor) or accepted.dim() != 2:
-        raise ValueError("accepted must be [B, T]")
-    T = accepted.shape[1]
-    bf16, i32 = torch.bfloat16, torch.int32
-    if seqlens_out is None:
-        seqlens_out = torch.empty_like(seqlens)
-    st = _call(di, lib.fa_cache_compact, _arg(k_cache, "k_cache", bf16, di, shape), _arg(v_cache, "v_cache", bf16, di, shape),
-               _arg(seqlens, "seqlens", i32, di, (B,)), _arg(accepted, "accepted", i32, di, (B, T)),
-               _arg(n_accepted, "n_accepted", i32, di, (B,)), _arg(seqlens_out, "seqlens_out", i32, di, (B,)),
-               L, B, Hkv, Nk_max, d, d, T)
-    if st != FA_OK:
-        raise FaError(st, "fa_cache_compact")
-    return seqlens_out
+    r = (_binding or _native()).cache_compact(k_cache, v_cache, seqlens, accepted, n_accepted, seqlens_out)
+    if type(r) is int:
+        raise FaError(r, "fa_cache_compact")
+    return r[0]
 
 
 def get_device_error(device=None):

@@ -1,9 +1,11 @@
-"""Build libfa.so in-tree with nvcc for sm_103a.
+"""Build libfa.so in-tree with nvcc for sm_103a, and the binding's native part with g++.
 
 Each .cu translation unit is compiled in parallel to an object file, then
 the objects are linked into ``libfa.so`` next to this file (the CUDA runtime
 is linked statically, the driver API is reached through the runtime's
 entry-point query, so the library loads on machines without a GPU).
+``_fa_binding.so`` (csrc/fa_binding.cpp) checks and marshals the Python calls of the operators around
+cached attention; it is compiled against the installed torch and links ``libfa.so`` beside it.
 """
 from __future__ import annotations
 
@@ -11,11 +13,13 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfa.so")
+BINDING = os.path.join(HERE, "_fa_binding.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -41,10 +45,13 @@ def _deps():
 
 def build(force=False, verbose=False, extra_flags=()):
     """Compile every kernel and the C ABI into ``libfa.so``; returns its path."""
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps():
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps() for f in (LIB, BINDING)):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
+    import torch
+    torch_dir = os.path.dirname(torch.__file__)
+    cxx = os.environ.get("CXX") or shutil.which("g++") or "c++"
 
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
@@ -56,15 +63,36 @@ def build(force=False, verbose=False, extra_flags=()):
             print(r.stderr)
         return obj
 
+    def compile_binding():
+        obj = os.path.join(BUILD, "fa_binding.o")
+        inc = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")]
+        cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+               *[f for i in inc for f in ("-I", i)], "-c", os.path.join(CSRC, "fa_binding.cpp"), "-o", obj]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"{cxx} failed on fa_binding.cpp:\n{r.stderr}")
+        return obj
+
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, srcs))
+        binding_obj = binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    tmp = BINDING + f".tmp{os.getpid()}"
+    libs = os.path.join(torch_dir, "lib")
+    cmd = [cxx, "-shared", "-o", tmp, binding_obj, "-L", HERE, "-l:libfa.so", "-Wl,-rpath,$ORIGIN", "-L", libs,
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stderr}")
+    os.replace(tmp, BINDING)
     return LIB
 
 
