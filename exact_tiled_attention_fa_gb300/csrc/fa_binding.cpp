@@ -278,7 +278,8 @@ PyObject* qk_norm_rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n)
     void* dv = optional_arg(a[2], "dv", gt, r.device, dkvs);
     const bool values = dv != nullptr;
     const bool given = a[14] != Py_None;  // all of the gradients' buffers, or none
-    if (given && (a[16] != Py_None) != values) refuse("grad_v goes with dv");
+    if ((a[15] != Py_None) != given) refuse("grad_q goes with grad_k");
+    if (a[16] != Py_None ? !given || !values : given && values) refuse("grad_v goes with dv and the other gradients");
     Tensor gq, gk, gv;
     Rows rq, rk, rv;
     if (given) {
