@@ -218,10 +218,11 @@ size_t fa_decode_tree_workspace_size(int Hq, int Hkv, int T, int d, int num_sms)
 {
     if (Hq <= 0 || Hkv <= 0 || T <= 0 || d <= 0 || num_sms <= 0 || Hq % Hkv != 0) return 0;
     const long long rows = static_cast<long long>(Hq / Hkv) * T;
-    const size_t part = rows > fa::kBlockM ? 2 * fa::kBlockM : static_cast<size_t>(rows);
-    const size_t slots = 2 * static_cast<size_t>(num_sms) * part;
+    const bool pair = rows > fa::kBlockM;  // up to 128 rows: room for either form
+    const size_t shares = (pair ? 1 : 2) * static_cast<size_t>(num_sms);
+    const size_t slots = 2 * shares * (pair ? 2 * fa::kBlockM : static_cast<size_t>(rows));  // rows of them
     return round_up(slots * d * sizeof(float), kAlign) + round_up(slots * sizeof(float), kAlign) +
-           round_up(static_cast<size_t>(num_sms) * sizeof(fa::TreeJoin), kAlign);
+           round_up(shares * sizeof(fa::TreeJoin), kAlign);
 }
 
 fa_status fa_decode_tree(const void* q, const void* k_cache, const void* v_cache, const int* seqlens_k, const int* parents,
@@ -259,7 +260,20 @@ fa_status fa_decode_tree(const void* q, const void* k_cache, const void* v_cache
     p.o = o;
     p.lse = lse;
     p.o_part = static_cast<float*>(workspace);
-    const size_t slots = 2 * static_cast<size_t>(sms) * part;
+    const bool pair = rows > fa::kBlockM;
+    p.num_ctas = sms < fa::kTreeMaxShares / 2 ? sms : fa::kTreeMaxShares / 2;
+    // Which form (fa_tree_kernel.cuh).  Measured on GB300, 4 query heads per key/value head, 8 nodes, d = 128
+    // (ALT / SOLO, us): 2048 units of at most 400 tokens 114 / 93, 1500 tokens 215 / 211, 4500 tokens
+    // 521 / 540; 1024 units 63 / 54, 114 / 113, 266 / 279; 512 units 37 / 35, 63 / 64, 140 / 148; 128 units
+    // of 1-32K tokens 168 / 177.  d = 64, 1500 tokens: 2048 units 127 / 104.  The lengths are only known on
+    // the device: many units are taken to be short ones (at most 5 % lost), fewer only if none can be long.
+    const long long units = groups * n_qp;
+    const bool solo = !pair && (units >= 6LL * p.num_ctas || (units >= 3LL * p.num_ctas && Nk_max <= 1536));
+    p.num_shares = solo ? 2 * p.num_ctas : p.num_ctas;
+    // a unit's start and end took a CTA about three tiles' time (one share's last units of 9 tiles each: the
+    // CTA ended 30 us after the others without it), two under the other warpgroup's tiles
+    p.unit_cost = solo ? 2 : 3;
+    const size_t slots = 2 * static_cast<size_t>(p.num_shares) * part;
     char* at = static_cast<char*>(workspace) + round_up(slots * d * sizeof(float), kAlign);
     p.lse_part = reinterpret_cast<float*>(at);
     p.joins = reinterpret_cast<fa::TreeJoin*>(at + round_up(slots * sizeof(float), kAlign));
@@ -270,7 +284,6 @@ fa_status fa_decode_tree(const void* q, const void* k_cache, const void* v_cache
     p.Nk_max = Nk_max;
     p.part_rows = part;
     p.n_qp = static_cast<int>(n_qp);
-    p.num_ctas = sms < fa::kTreeMaxCtas ? sms : fa::kTreeMaxCtas;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.o_dtype = o_dtype;
     p.wait_limit_ns = fa::wait_limit_ns();

@@ -171,9 +171,9 @@ cudaError_t launch_merge(const MergeParams& p, fa_dtype o_dtype, cudaStream_t st
 // Tree decode (fa_tree_kernel.cuh).  A group is a (sequence, key/value head) with its
 // rows = (Hq / Hkv) * T query rows, row = head within the group * T + node; a unit is a block of
 // part_rows of them.
-constexpr int kTreeMaxCtas = 256;  // CTAs of a call at most, and so parts of a unit
+constexpr int kTreeMaxShares = 320;  // of a call, and so parts of a unit
 
-// What the merge has to join: the unit that a CTA began and did not finish.
+// What the merge has to join: the unit that a share began and did not finish.
 struct TreeJoin {
     long long first_row;  // in the output
     int rows, parts;      // parts = 0: none
@@ -188,14 +188,16 @@ struct TreeParams {
     const int* n_nodes;  // int32 [B] or nullptr (T everywhere)
     void* o;             // [B*Hkv][rows][d]
     float* lse;          // [B*Hkv][rows] or nullptr
-    float* o_part;       // fp32 [2 * num_ctas][part_rows][d]
-    float* lse_part;     // fp32 [2 * num_ctas][part_rows]
-    TreeJoin* joins;     // [num_ctas]
+    float* o_part;       // fp32 [2 * num_shares][part_rows][d]
+    float* lse_part;     // fp32 [2 * num_shares][part_rows]
+    TreeJoin* joins;     // [num_shares]
     int* status;
     int B, Hkv, rows, T, Nk_max;
     int part_rows;       // min(rows, 128), or 256 for more than 128 rows (PAIR form)
     int n_qp;            // units per group: ceil(rows / part_rows)
     int num_ctas;        // one per SM
+    int num_shares;      // num_ctas, or two for each CTA (up to 128 rows)
+    int unit_cost;       // a unit's start and end, in key tiles
     float scale_log2;
     fa_dtype o_dtype;
     unsigned long long wait_limit_ns;

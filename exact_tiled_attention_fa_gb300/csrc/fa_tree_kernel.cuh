@@ -12,26 +12,31 @@
 // and key ranges are joined by section 4's log-sum-exp combine.
 //
 // Work division.  A unit is a group's block of up to 128 query rows (256 in PAIR form); it has
-// ceil((p + n) / 128) key tiles.  The tiles of all units, in order, are cut into as many equal
-// shares as there are CTAs (one per SM), from lengths that only the device knows: each CTA scans
-// the lengths once (a unit's start and end count as kUnitCost tiles).  A share crosses unit borders, and the rings of K and V tiles run on across
-// them, so a CTA pays its start-up once, however short the caches are.  A unit that lies in one
-// CTA's share is finished there; the parts of the others go to at most two slots per CTA (the
-// share's first and last unit) and fa_tree_merge_kernel joins them.  The slots are thus bounded by
-// the number of CTAs, not by the number of units.
+// ceil((p + n) / 128) key tiles, and counts for unit_cost more, about what its start and end cost.
+// The tiles of all units, in order, are cut into equal shares, from lengths that only the device
+// knows: each CTA scans the lengths once.  A share crosses unit borders, and the rings of K and V
+// tiles run on across them, so a CTA pays its start-up once, however short the caches are.  A unit
+// that lies in one share is finished there; the parts of the others go to at most two slots a share
+// (its first and its last unit) and fa_tree_merge_kernel joins them.  The slots are thus bounded by the
+// number of shares, not by the number of units.
 //
-// Roles of a CTA (12 warps):
+// Roles of a CTA, one per SM (12 warps):
 //   warps 0-3 / 4-7  softmax warpgroups 0 / 1: thread t owns row t of a 128-row tile (TMEM lane t).
-//   warp 8           TMA producer: query tiles, K and V tiles into rings of their own.
+//   warps 8, 11      TMA producers: query tiles, K and V tiles into rings of their own (11: SOLO only).
 //   warps 9, 10      tcgen05 issuers of warpgroup 0 / 1: S = Q K^T, O += P V (P from tensor memory).
-// ALT form (groups of at most 128 rows): both warpgroups hold the same 128 query rows and take the
-// key tiles in turn (tile k of the CTA's share goes to warpgroup k mod 2), each with its own running
-// max, sum and O accumulator, so one warpgroup's exponentials run under the other's products
-// although there is a single query tile.  At the end of a unit the two exchange max and sum through
-// shared memory and each reads half of the columns of both accumulators out of tensor memory (warps
-// w and w + 4 reach the same lanes).
+// A single query tile would leave the tensor core idle under its exponentials and the exponentials
+// under its products, so the two warpgroups work on different keys (or different rows):
+// ALT form (groups of at most 128 rows, few units): both hold the same 128 query rows and take the key
+// tiles of the CTA's share in turn (tile k goes to warpgroup k mod 2), each with its own running max,
+// sum and O accumulator.  At the end of a unit the two exchange max and sum through shared memory and
+// each reads half of the columns of both accumulators out of tensor memory (warps w and w + 4 reach
+// the same lanes).
+// SOLO form (at most 128 rows, many units): each warpgroup has a share, a producer and rings of its own,
+// so the start and end of one's units run under the other's tiles; but there are twice as many shares,
+// and so parts to write and join.
 // PAIR form (more than 128 rows): warpgroup i takes query rows 128 i .. 128 i + 127 of the unit and
-// both walk every key tile, so that K and V are read once for 256 rows.
+// both walk every key tile of the CTA's share, so that K and V are read once for 256 rows.
+// (fa_cached_api.cu chooses, with what the forms measured.)
 //
 // Masks.  Only the tiles that hold drafted rows are masked, by four 32-bit words per query row (its
 // ancestors), shifted to the tile; hidden scores become -inf by selection, so a non-finite key
@@ -63,20 +68,20 @@ constexpr int kTrControlRegs = D == 128 ? 56 : 72;
 
 enum : int {
     kTbQFull = 0,     // + query buffer
-    kTbQEmpty = 2,    // + query buffer: both issuers are done with it
+    kTbQEmpty = 2,    // + query buffer: its issuers are done with it
     kTbSFull = 4,     // + warpgroup
     kTbSFree = 6,     // + warpgroup: S_i has been read out of TMEM
     kTbPFull = 8,     // + warpgroup
     kTbPVDone = 10,   // + warpgroup
     kTbOReady = 12,   // + warpgroup: the last product of a unit has completed
-    kTbOFree = 14,    // + warpgroup: O_i has been read out of TMEM
+    kTbOFree = 14,    // + warpgroup, ALT: O_i has been read out of TMEM by both
     kTbMLFull = 16,   // ALT: both warpgroups' max and sum are in shared memory
     kTbDrain = 17,    // + warpgroup
     kTbKFull = 20,    // + K stage (up to 4)
     kTbKEmpty = 24,
     kTbVFull = 28,    // + V stage (up to 4)
     kTbVEmpty = 32,
-    kTbSegFull = 36,  // + segment mod kTrSegs: the segment's record is in shared memory
+    kTbSegFull = 36,  // + place in the ring of records: the segment's is in shared memory
     kTbCount = 44
 };
 
@@ -88,10 +93,13 @@ struct TreeSeg {
     int b, group, qp;
     int slot;           // of its part; -1: the unit is whole
 };
-// Records in flight.  The producer is at most two segments ahead of the scores (two query buffers),
-// and those at most three ahead of a softmax warpgroup (one it has just finished, one whose tiles
-// are all the other's, one whose scores are there): 8 never overwrite a record in use.
+// Records in the ring, 8 for the one stream of tiles (ALT, PAIR) or 4 for each of two (SOLO).  The producer
+// is at most two segments ahead of the scores (ALT; one otherwise: the query buffers), those at most two
+// ahead of a softmax warpgroup (ALT; one otherwise), which copies a record when it comes to it: a record
+// is never overwritten before it has been read.
 constexpr int kTrSegs = 8;
+
+enum TreeForm { kAlt, kSolo, kPair };
 
 template <int D>
 struct TrCfg {
@@ -103,20 +111,20 @@ struct TrCfg {
     static constexpr int kAtomBytes = 8 * kRowBytes;
     static constexpr int kBlkBytes = kBlockM * kRowBytes;
     static constexpr int kTileBytes = kNumCB * kBlkBytes;  // 128 x D bf16
-    // Stages of each ring.  Even, so that in ALT form a stage always serves the same warpgroup: a
-    // stage's previous tile was then consumed by the very thread that waits for its next one,
-    // which the phase parity of the wait relies on.
+    // Stages of K and of V, all streams' together.  Even: in ALT form a stage then always serves the same
+    // warpgroup, so its tile before was consumed by the very thread that waits for the next one, which the
+    // phase parity of the wait relies on.
     static constexpr int kStages = D == 128 ? 2 : 4;
     static_assert(kStages % 2 == 0 && kStages <= 4, "ring stages");
-    static constexpr int kOffQ = 0;  // two query tiles: two units' (ALT) or a unit's two (PAIR)
+    static constexpr int kOffQ = 0;  // two query tiles: two units' (ALT), a warpgroup's each (SOLO, PAIR)
     static constexpr int kOffK = 2 * kTileBytes;
     static constexpr int kOffV = kOffK + kStages * kTileBytes;
-    static constexpr int kOffML = kOffV + kStages * kTileBytes;  // [2 warpgroups][128] (max, sum)
+    static constexpr int kOffML = kOffV + kStages * kTileBytes;  // ALT: [2 warpgroups][128] (max, sum)
     static constexpr int kOffStage = kOffML + 2 * kBlockM * 8;  // [8 warps][32 rows of 64 bytes]: rows on their way out
     static constexpr int kOffSeg = kOffStage + 8 * 2048;
     static constexpr int kOffBar = kOffSeg + kTrSegs * static_cast<int>(sizeof(TreeSeg));
     static constexpr int kOffStart = kOffBar + kTbCount * 8;
-    static constexpr int kUsedBytes = kOffStart + 80;
+    static constexpr int kUsedBytes = kOffStart + 2 * 64 + 16;
     // At least 120 KB, so that no second CTA (which would wait for the 512 TMEM columns) shares the SM.
     static constexpr int kSmemBytes = kUsedBytes + 1024 > 120 * 1024 ? kUsedBytes + 1024 : 120 * 1024;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
@@ -161,48 +169,44 @@ __device__ __forceinline__ TreeLen tree_len(const int* seqlens, const int* n_nod
     return tree_clamp(seqlens[b], n_nodes != nullptr ? n_nodes[b] : T, T, Nk_max, status);
 }
 
-// A unit counts for its tiles and kUnitCost more, about what its start and end cost a CTA in tiles
-// (see fa_tree_kernel): they take the places before its tiles.  Without them a CTA whose share was
-// made of short units finished last.
-constexpr int kUnitCost = 3;
-
-// The share of CTA c: places [w0, w1) of all units in order, and the unit and place it starts in.
+// Share c: places [w0, w1) of all units in order (a unit's unit_cost places come before its tiles), and
+// the unit and place it starts in.
 struct TreeStart {
     long long w0, w1;
-    long long total, ctas;
+    long long total, shares;
     int b, unit, at;    // sequence, unit within the sequence, place within the unit
     int prefix, nodes;  // of the sequence
 };
 
-__device__ __forceinline__ long long share_begin(long long c, long long total, long long ctas) { return c * total / ctas; }
+__device__ __forceinline__ long long share_begin(long long c, long long total, long long shares) { return c * total / shares; }
 
 __device__ __forceinline__ TreeLen tree_at(const TreeParams& p, int b)
 {
     return tree_len(p.seqlens, p.n_nodes, b, p.T, p.Nk_max, p.status);
 }
-__device__ __forceinline__ int tree_places(const TreeParams& p, int b) { return tree_at(p, b).tiles() + kUnitCost; }
+__device__ __forceinline__ int tree_places(const TreeParams& p, int b) { return tree_at(p, b).tiles() + p.unit_cost; }
 
-// By one warp; every lane returns the same.  Empty (w0 = w1) for CTAs past the number of places.
+// By one warp; every lane returns the same.  Empty (w0 = w1) for shares past the number of places.
 __device__ __forceinline__ TreeStart tree_locate(const TreeParams& p, int c, int lane)
 {
     const long long upb = static_cast<long long>(p.Hkv) * p.n_qp;
     TreeLen len{0, 0};  // the first 32 sequences'
     if (lane < p.B) len = tree_at(p, lane);
-    long long total = lane < p.B ? len.tiles() + kUnitCost : 0;
+    long long total = lane < p.B ? len.tiles() + p.unit_cost : 0;
     for (int b = 32 + lane; b < p.B; b += 32) total += tree_places(p, b);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     total *= upb;
-    const long long ctas = p.num_ctas < total ? p.num_ctas : total;
-    TreeStart s{0, 0, total, ctas, 0, 0, 0, 0, 0};
-    if (c >= ctas) return s;
-    s.w0 = share_begin(c, total, ctas);
-    s.w1 = share_begin(c + 1, total, ctas);
+    const long long shares = p.num_shares < total ? p.num_shares : total;
+    TreeStart s{0, 0, total, shares, 0, 0, 0, 0, 0};
+    if (c >= shares) return s;
+    s.w0 = share_begin(c, total, shares);
+    s.w1 = share_begin(c + 1, total, shares);
     long long base = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
         const int b = b0 + lane;
         if (b0 > 0 && b < p.B) len = tree_at(p, b);
-        const int places = b < p.B ? len.tiles() + kUnitCost : 0;
+        const int places = b < p.B ? len.tiles() + p.unit_cost : 0;
         long long incl = places * upb;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -227,7 +231,7 @@ __device__ __forceinline__ TreeStart tree_locate(const TreeParams& p, int c, int
     return s;
 }
 
-// A CTA's share, segment by segment (the producer's).
+// A share, segment by segment (the producer's).
 struct TreeWalk {
     int left;            // places of the share from this segment on
     int used;            // places of this segment
@@ -261,10 +265,10 @@ struct TreeWalk {
     // the segment at place `at` of the current unit; left = 0 if nothing but a unit's first places is left
     __device__ __forceinline__ void take(const TreeParams& p, int at)
     {
-        used = min(tiles + kUnitCost - at, left);
-        tile = max(at - kUnitCost, 0);
-        n = at + used - kUnitCost - tile;
-        if (n <= 0) left = 0;  // the share ends in the unit's first places: its tiles are the next CTA's
+        used = min(tiles + p.unit_cost - at, left);
+        tile = max(at - p.unit_cost, 0);
+        n = at + used - p.unit_cost - tile;
+        if (n <= 0) left = 0;  // the share ends in the unit's first places: its tiles are the next share's
     }
     __device__ __forceinline__ void step(const TreeParams& p)
     {
@@ -284,12 +288,9 @@ struct TreeWalk {
         next_nodes = p.n_nodes != nullptr ? p.n_nodes[i] : p.T;
     }
     __device__ __forceinline__ int group(const TreeParams& p) const { return b * p.Hkv + kvh; }
-    // Slot of a part: of the units that a share holds without finishing them alone, one was begun by
-    // the CTA before (it is the share's first) and one is begun here (its last).
-    __device__ __forceinline__ int slot() const
-    {
-        return n == tiles ? -1 : 2 * static_cast<int>(blockIdx.x) + (tile == 0 ? 1 : 0);
-    }
+    // Slot of a part: of the units that a share holds without finishing them alone, one was begun in the
+    // share before (it is the share's first) and one is begun here (its last).
+    __device__ __forceinline__ int slot(int share) const { return n == tiles ? -1 : 2 * share + (tile == 0 ? 1 : 0); }
 };
 
 // Ancestors of each lane's node t (and t itself) as 128 bits; t < 0: none.  Whole warp: it holds the
@@ -375,11 +376,14 @@ struct RowsOut {
 
 __device__ __forceinline__ float2 as_float2(uint32_t a, uint32_t b) { return make_float2(__uint_as_float(a), __uint_as_float(b)); }
 
-template <int D, bool PAIR>
+template <int D, TreeForm FORM>
 __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_constant__ TreeParams p)
 {
     using C = TrCfg<D>;
-    constexpr int S = C::kStages;
+    constexpr bool ALT = FORM == kAlt, SOLO = FORM == kSolo, PAIR = FORM == kPair;
+    constexpr int kStreams = SOLO ? 2 : 1;         // shares, producers, rings
+    constexpr int S = C::kStages / kStreams;       // stages of a stream's ring
+    constexpr int kSegs = kTrSegs / kStreams;      // records of a stream
     extern __shared__ uint8_t tr_smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(tr_smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
@@ -387,7 +391,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
     const uint32_t bar0 = sbase + C::kOffBar;
     auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
     TreeStart* start_slot = reinterpret_cast<TreeStart*>(smem + C::kOffStart);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffStart + 64);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffStart + 2 * 64);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     static_assert(sizeof(TreeStart) <= 64, "start record");
 
@@ -398,18 +402,18 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(kTbQFull + i), 1);
-            mbar_init(bar(kTbQEmpty + i), 2);
+            mbar_init(bar(kTbQEmpty + i), SOLO ? 1 : 2);
             mbar_init(bar(kTbSFull + i), 1);
             mbar_init(bar(kTbSFree + i), kBlockM);
             mbar_init(bar(kTbPFull + i), kBlockM);
             mbar_init(bar(kTbPVDone + i), 1);
             mbar_init(bar(kTbOReady + i), 1);
-            mbar_init(bar(kTbOFree + i), PAIR ? kBlockM : 2 * kBlockM);
+            mbar_init(bar(kTbOFree + i), 2 * kBlockM);
             mbar_init(bar(kTbDrain + i), 1);
         }
         mbar_init(bar(kTbMLFull), 2 * kBlockM);
         for (int i = 0; i < kTrSegs; ++i) mbar_init(bar(kTbSegFull + i), 1);
-        for (int s = 0; s < S; ++s) {
+        for (int s = 0; s < C::kStages; ++s) {
             mbar_init(bar(kTbKFull + s), 1);
             mbar_init(bar(kTbKEmpty + s), PAIR ? 2 : 1);
             mbar_init(bar(kTbVFull + s), 1);
@@ -424,27 +428,31 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
     }
     grid_dependency_wait();    // launched as a programmatic dependent of the previous kernel
     grid_launch_dependents();  // the merge may begin launching (it waits for this grid)
-    if (warp == 0) {
-        const TreeStart s = tree_locate(p, blockIdx.x, lane);
-        if (lane == 0) *start_slot = s;
+    if (warp % 4 == 0 && warp / 4 < kStreams) {  // share `stream * CTAs + CTA`: few shares go to different SMs
+        const int stream = warp / 4;
+        const TreeStart s = tree_locate(p, stream * static_cast<int>(gridDim.x) + blockIdx.x, lane);
+        if (lane == 0) *reinterpret_cast<TreeStart*>(reinterpret_cast<uint8_t*>(start_slot) + 64 * stream) = s;
     }
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    const TreeSeg* seg_ring = reinterpret_cast<const TreeSeg*>(smem + C::kOffSeg);
-    // Record of segment i (of any role but the producer); n = 0 past the last, and when a wait ran out.
-    auto segment = [&](int i, bool& ok) -> TreeSeg {
+    TreeSeg* seg_ring = reinterpret_cast<TreeSeg*>(smem + C::kOffSeg);
+    // Record of segment i of a stream (of any role but the producer); n = 0 past the last, and when a wait
+    // ran out.
+    auto segment = [&](int stream, int i, bool& ok) -> TreeSeg {
+        const int at = stream * kSegs + i % kSegs;
         TreeSeg x;
         x.n = 0;
-        ok = mbar_wait(bar(kTbSegFull + i % kTrSegs), static_cast<uint32_t>(i / kTrSegs) & 1, limit, abort_flag);
-        if (ok) x = seg_ring[i % kTrSegs];
+        ok = mbar_wait(bar(kTbSegFull + at), static_cast<uint32_t>(i / kSegs) & 1, limit, abort_flag);
+        if (ok) x = seg_ring[at];
         return x;
     };
 
     if (warp >= kTrWarpProducer) {
         regs_decrease<kTrControlRegs<D>>();
-        if (warp == kTrWarpProducer) {
+        const int stream = warp == kTrWarpProducer ? 0 : warp == kTrWarpProducer + 3 ? 1 : kStreams;
+        if (stream < kStreams) {
             // ======================================================== producer
             if (lane == 0) {
                 prefetch_tensormap(&p.tm_q);
@@ -453,14 +461,15 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                 // K and V are read again only by a group's further query blocks
                 const uint64_t pol_kv = p.n_qp > 1 ? policy_evict_last() : policy_evict_first();
                 const uint64_t pol_q = policy_evict_first();
-                const TreeStart start = *start_slot;
+                const TreeStart start = *reinterpret_cast<TreeStart*>(reinterpret_cast<uint8_t*>(start_slot) + 64 * stream);
+                const int share = stream * static_cast<int>(gridDim.x) + blockIdx.x;
+                const int stage0 = stream * S;
                 TreeWalk kw, vw;  // K runs one tile ahead of V
                 kw.begin(p, start);
                 vw.begin(p, start);
                 int kj = 0, vj = 0;  // tile within the segment
-                int segs = 0;        // query loads issued
+                int segs = 0;        // records written
                 int k_issued = 0, v_issued = 0;
-                TreeSeg* ring = reinterpret_cast<TreeSeg*>(smem + C::kOffSeg);
                 TreeJoin join{0, 0, 0};
                 auto publish = [&](int n) {  // the walk's segment to the other roles
                     TreeSeg x;
@@ -471,23 +480,24 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                     x.b = kw.b;
                     x.group = kw.group(p);
                     x.qp = kw.qp;
-                    x.slot = kw.slot();
+                    x.slot = kw.slot(share);
                     if (n > 0 && x.slot >= 0 && kw.tile == 0) {
-                        // begun here, finished by the CTA of its last place
+                        // begun here, finished in the share of its last place
                         const long long last = start.w1 + (kw.tiles - kw.n);
                         join.first_row = static_cast<long long>(x.group) * p.rows + static_cast<long long>(kw.qp) * p.part_rows;
                         join.rows = min(p.part_rows, p.rows - kw.qp * p.part_rows);
-                        join.parts = static_cast<int>((last * start.ctas - 1) / start.total) - static_cast<int>(blockIdx.x) + 1;
+                        join.parts = static_cast<int>((last * start.shares - 1) / start.total) - share + 1;
                     }
-                    ring[segs % kTrSegs] = x;
-                    mbar_arrive(bar(kTbSegFull + segs % kTrSegs));
+                    const int at = stream * kSegs + segs % kSegs;
+                    seg_ring[at] = x;
+                    mbar_arrive(bar(kTbSegFull + at));
                     ++segs;
                 };
                 auto load_k = [&]() -> bool {
                     const int g = kw.group(p);
                     if (kj == 0) {  // the segment's query rows
-                        const int buf = PAIR ? 0 : segs & 1;
-                        const int use = PAIR ? segs : segs >> 1;
+                        const int buf = ALT ? segs & 1 : stream;
+                        const int use = ALT ? segs >> 1 : segs;
                         if (use > 0 && !mbar_wait(bar(kTbQEmpty + buf), static_cast<uint32_t>(use - 1) & 1, limit, abort_flag))
                             return false;
                         const int row0 = kw.qp * (PAIR ? 2 : 1) * kBlockM;
@@ -499,7 +509,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                                             bar(kTbQFull + buf), cb * C::kCB, row0 + i * kBlockM, g, pol_q);
                         publish(kw.n);
                     }
-                    const int s = k_issued % S;
+                    const int s = stage0 + k_issued % S;
                     if (k_issued >= S &&
                         !mbar_wait(bar(kTbKEmpty + s), static_cast<uint32_t>(k_issued / S - 1) & 1, limit, abort_flag))
                         return false;
@@ -515,7 +525,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                     return true;
                 };
                 auto load_v = [&]() -> bool {
-                    const int s = v_issued % S;
+                    const int s = stage0 + v_issued % S;
                     if (v_issued >= S &&
                         !mbar_wait(bar(kTbVEmpty + s), static_cast<uint32_t>(v_issued / S - 1) & 1, limit, abort_flag))
                         return false;
@@ -534,16 +544,19 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                 while (ok && vw.live()) ok = (!kw.live() || load_k()) && load_v();
                 const int loads = segs;  // query loads issued
                 if (ok) publish(0);
-                p.joins[blockIdx.x] = join;
+                p.joins[share] = join;
                 if (!ok && !*abort_flag) record_failure(p.status, abort_flag, FA_ERR_TIMEOUT);
                 // Every issued copy must land before the CTA may exit (its last phase per barrier).
-                const int q_bufs = PAIR ? 1 : 2;
-                for (int t = loads - q_bufs < 0 ? 0 : loads - q_bufs; t < loads; ++t)
-                    mbar_wait(bar(kTbQFull + t % q_bufs), static_cast<uint32_t>(t / q_bufs) & 1, kDrainLimitNs, nullptr);
+                if constexpr (ALT) {
+                    for (int t = loads - 2 < 0 ? 0 : loads - 2; t < loads; ++t)
+                        mbar_wait(bar(kTbQFull + (t & 1)), static_cast<uint32_t>(t >> 1) & 1, kDrainLimitNs, nullptr);
+                } else if (loads > 0) {
+                    mbar_wait(bar(kTbQFull + stream), static_cast<uint32_t>(loads - 1) & 1, kDrainLimitNs, nullptr);
+                }
                 for (int t = k_issued - S < 0 ? 0 : k_issued - S; t < k_issued; ++t)
-                    mbar_wait(bar(kTbKFull + t % S), static_cast<uint32_t>(t / S) & 1, kDrainLimitNs, nullptr);
+                    mbar_wait(bar(kTbKFull + stage0 + t % S), static_cast<uint32_t>(t / S) & 1, kDrainLimitNs, nullptr);
                 for (int t = v_issued - S < 0 ? 0 : v_issued - S; t < v_issued; ++t)
-                    mbar_wait(bar(kTbVFull + t % S), static_cast<uint32_t>(t / S) & 1, kDrainLimitNs, nullptr);
+                    mbar_wait(bar(kTbVFull + stage0 + t % S), static_cast<uint32_t>(t / S) & 1, kDrainLimitNs, nullptr);
             }
         } else if (warp == kTrWarpMma || warp == kTrWarpMma + 1) {
             // ======================================================== MMA issuers
@@ -554,8 +567,11 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                 const uint32_t a_p = tmem + C::col_p(i);
                 int tiles = 0;   // products issued by this issuer
                 int s_done = 0;  // score tiles issued
-                int k = 0;       // tile of the CTA's share
-                int segs = 0, o_uses = 0;  // segments walked; OFree phases that precede the next first product
+                int k = 0;       // tile of the share
+                int segs = 0;    // segments walked
+                int o_uses = 0;  // ALT: OFree phases that precede the next first product
+                const int my = SOLO ? i : 0;  // stream
+                const int stage0 = my * S;
                 bool ok = true;
                 auto issue_s = [&](int q_tile, int stage) {
                     const uint64_t a0 = smem_desc(sbase + C::kOffQ + q_tile * C::kTileBytes, 16, C::kAtomBytes, C::kLayout);
@@ -577,7 +593,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                 // S_i of share tile kk.  Its columns must have been read (and, where P overwrites
                 // them, the product that reads P must have completed).
                 auto do_s = [&](int q_tile, int q_buf, int kk, bool last) -> bool {
-                    const int s = kk % S;
+                    const int s = stage0 + kk % S;
                     if (!mbar_wait(bar(kTbKFull + s), static_cast<uint32_t>(kk / S) & 1, limit, abort_flag)) return false;
                     if (s_done > 0 && !mbar_wait(bar((C::kAliasP ? kTbPVDone : kTbSFree) + i),
                                                  static_cast<uint32_t>(s_done - 1) & 1, limit, abort_flag))
@@ -590,22 +606,21 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                     if (last) umma_commit(bar(kTbQEmpty + q_buf));
                     return true;
                 };
+                constexpr int step = ALT ? 2 : 1;
                 while (ok) {
-                    const TreeSeg w = segment(segs, ok);
+                    const TreeSeg w = segment(my, segs, ok);
                     if (w.n == 0) break;
-                    const int q_buf = PAIR ? 0 : segs & 1;
-                    const int q_use = PAIR ? segs : segs >> 1;
-                    const int q_tile = PAIR ? i : q_buf;
-                    const bool mine = !PAIR || i == 0 || p.rows - w.qp * 2 * kBlockM > kBlockM;
-                    const int step = PAIR ? 1 : 2;
-                    const int j0 = PAIR ? 0 : (k + i) & 1;  // first tile of the segment for this warpgroup
+                    const int q_buf = ALT ? segs & 1 : my;
+                    const int q_tile = ALT ? q_buf : i;
+                    const int j0 = ALT ? (k + i) & 1 : 0;  // first tile of the segment for this warpgroup
                     // Also without tiles of its own in the segment: an issuer that skipped a phase of the
                     // query barrier could take the phase before it for the one it needs.
-                    ok = mbar_wait(bar(kTbQFull + q_buf), static_cast<uint32_t>(q_use) & 1, limit, abort_flag);
+                    ok = mbar_wait(bar(kTbQFull + q_buf), static_cast<uint32_t>(ALT ? segs >> 1 : segs) & 1, limit, abort_flag);
                     if (!ok) break;
-                    if (!mine || j0 >= w.n) {
-                        // (before the loop: the producer may be waiting to load the next unit's queries
-                        // ahead of this unit's last V)
+                    const bool rows = !PAIR || i == 0 || p.rows - w.qp * 2 * kBlockM > kBlockM;
+                    if (!rows || j0 >= w.n) {
+                        // (The queries first: the producer may be waiting to load the next unit's ahead of
+                        // this unit's last V.)
                         mbar_arrive(bar(kTbQEmpty + q_buf));
                         if (PAIR) {  // no rows: pass every tile on
                             for (int j = 0; ok && j < w.n; ++j) {
@@ -623,16 +638,17 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                         ok = do_s(q_tile, q_buf, k + j0, j0 == j_last);
                         for (int j = j0; ok && j < w.n; j += step) {
                             const int kk = k + j;
-                            const int s = kk % S;
+                            const int s = stage0 + kk % S;
                             // Without aliasing the next scores need only the current ones read: they run
                             // while this tile is still being exponentiated.
                             if (!C::kAliasP && j + step < w.n) ok = do_s(q_tile, q_buf, kk + step, j + step == j_last);
                             ok = ok && mbar_wait(bar(kTbPFull + i), static_cast<uint32_t>(tiles) & 1, limit, abort_flag) &&
                                  mbar_wait(bar(kTbVFull + s), static_cast<uint32_t>(kk / S) & 1, limit, abort_flag);
-                            // The first product of a segment overwrites O_i: the previous segment's must have
-                            // been read.  Waited for after P: this warpgroup has then been through every
-                            // earlier segment's exchange, so the barrier is at most one phase behind.
-                            if (ok && j == j0 && o_uses > 0)
+                            // The first product of a segment overwrites O_i: the last segment's must have been
+                            // read.  P's arrival means that for this warpgroup; in ALT form the other reads O_i
+                            // too.  (Waited for after P: this warpgroup has then been through every earlier
+                            // segment's exchange, so the barrier is at most one phase behind.)
+                            if (ALT && ok && j == j0 && o_uses > 0)
                                 ok = mbar_wait(bar(kTbOFree + i), static_cast<uint32_t>(o_uses - 1) & 1, limit, abort_flag);
                             if (!ok) break;
                             tc_fence_after_sync();
@@ -644,7 +660,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                             if (C::kAliasP && j + step < w.n) ok = do_s(q_tile, q_buf, kk + step, j + step == j_last);
                         }
                     }
-                    if (!PAIR || mine) ++o_uses;
+                    ++o_uses;
                     k += w.n;
                     ++segs;
                 }
@@ -662,17 +678,19 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
         const uint32_t t_s = tmem + lane_base + C::col_s(wg);
         const uint32_t t_o = tmem + lane_base + C::col_o(wg);
         const uint32_t t_p = tmem + lane_base + C::col_p(wg);
-        float2* ml = reinterpret_cast<float2*>(smem + C::kOffML);
         const float sl2 = p.scale_log2;
         int tiles = 0;                 // key tiles processed by this warpgroup
-        int ready[2] = {0, 0};         // segments with tiles so far, per warpgroup
+        int ready[2] = {0, 0};         // segments with tiles of warpgroup 0, 1 (ALT); this warpgroup's (else, [0])
         int segs = 0, k = 0;
+        const int my = SOLO ? wg : 0;  // stream
+        float2* ml = reinterpret_cast<float2*>(smem + C::kOffML);
+        constexpr int step = ALT ? 2 : 1;
         uint32_t vis[4] = {0u, 0u, 0u, 0u};
         int vis_b = -1, vis_qp = -1;
         bool ok = true;
         const uint32_t stage = sbase + C::kOffStage + warp * 2048;
         while (ok) {
-            const TreeSeg w = segment(segs, ok);
+            const TreeSeg w = segment(my, segs, ok);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok || w.n == 0) break;
             const int row0 = PAIR ? w.qp * 2 * kBlockM + wg * kBlockM : 0;
@@ -684,9 +702,8 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
             }
             const int rows_warp = rows - 32 * (warp & 3);  // of this warp (<= 0: none)
             const bool warp_live = rows_warp > 0;
-            const int step = PAIR ? 1 : 2;
-            const int j0 = PAIR ? 0 : (k + wg) & 1;
-            const int end = w.prefix + w.nodes;  // keys of the sequence
+            const int j0 = ALT ? (k + wg) & 1 : 0;  // first tile of the segment for this warpgroup
+            const int end = w.prefix + w.nodes;     // keys of the sequence
             // the row's ancestors, kept while the sequence and the row stay the same
             if ((w.tile + w.n) * kBlockN > w.prefix && (w.b != vis_b || (PAIR && w.qp != vis_qp))) {
                 vis_b = w.b;
@@ -702,7 +719,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                 if (!ok) break;
                 tc_fence_after_sync();
                 const int k0 = (w.tile + j) * kBlockN;
-                const int vs = (k + j) % S;  // V stage
+                const int vs = my * S + (k + j) % S;  // V stage
                 if (warp_live) {
                     uint32_t u[kBlockN];
                     float mrow;
@@ -835,7 +852,8 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                 }
                 if (k0 + kBlockN > end) {
                     // V rows past the tree may hold anything: zero them before the product reads them.
-                    // (The stage's previous tile has been consumed: see kStages.)
+                    // (The stage's tile before it has been consumed, by the issuer that then issued these
+                    // scores, so the phase parity cannot mean that one.)
                     ok = __all_sync(0xffffffffu, mbar_wait(bar(kTbVFull + vs), static_cast<uint32_t>((k + j) / S) & 1,
                                                            limit, abort_flag));
                     if (!ok) break;
@@ -867,14 +885,15 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                     else if (p.lse != nullptr) p.lse[first + lane] = lse;
                 }
             };
-            if constexpr (PAIR) {
+            if constexpr (!ALT) {
                 ok = __all_sync(0xffffffffu, mbar_wait(bar(kTbOReady + wg), ready[0] & 1, limit, abort_flag));
                 if (!ok) break;
                 ++ready[0];
                 tc_fence_after_sync();
                 if (warp_live) {
-                    const float inv = (l == 0.f || !shown) ? 0.f : 1.f / l;
-                    const bool hide = __any_sync(0xffffffffu, !shown);
+                    const bool none = l == 0.f || !shown;
+                    const bool hide = __any_sync(0xffffffffu, none);
+                    const float inv = none ? 0.f : 1.f / l;
                     const float2 inv2 = make_float2(inv, inv);
                     uint32_t o[16];
                     tmem_ld16(t_o, o);
@@ -887,14 +906,12 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                         if (c + 16 < D) tmem_ld16(t_o + static_cast<uint32_t>(c + 16), o);  // on its way while these are stored
                         if (hide) {
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) x[e] = shown ? x[e] : make_float2(0.f, 0.f);
+                            for (int e = 0; e < 8; ++e) x[e] = none ? make_float2(0.f, 0.f) : x[e];
                         }
                         out.store(c, x);
                     }
-                    store_lse((l == 0.f || !shown) ? -INFINITY : (m_run + lg2_approx(l)) * 0.69314718055994531f);
+                    store_lse(none ? -INFINITY : (m_run + lg2_approx(l)) * 0.69314718055994531f);
                 }
-                tc_fence_before_sync();
-                mbar_arrive(bar(kTbOFree + wg));
             } else {
                 const int jw[2] = {k & 1, (k + 1) & 1};  // first tile of the segment for warpgroups 0 and 1
                 const bool has0 = jw[0] < w.n, has1 = jw[1] < w.n;
@@ -976,11 +993,13 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
 }
 
 // Joins the parts of the units that several CTAs share: lse = log sum_s exp(lse_s),
-// o = sum_s exp(lse_s - lse) o_s ("flash_lab.py" section 4).  Blocks (c, y) serve the unit that CTA c
-// began and did not finish, if there is one (joins[c]): its part is in that CTA's second slot, the
-// others in the following CTAs' first (slot()).  The time is the latency of the parts' loads, so all of
-// them are in flight at once where they are few (up to 4: eight lanes to a row, 32 rows a block), and
-// eight at a time otherwise (a warp a row, 8 rows a block).
+// o = sum_s exp(lse_s - lse) o_s ("flash_lab.py" section 4).  Blocks (c, y) serve the unit that share
+// c began and did not finish, if there is one (joins[c]): its part is in that share's second slot, the
+// others in the following shares' first (slot()).  The time is the latency of the parts' loads, so all of
+// them are in flight at once, or in two goes, where they are few (up to 8: eight lanes to a row, 32 rows a
+// block), and eight at a time otherwise (a warp a row, 8 rows a block).
+constexpr int kFew = 8;
+
 template <int D>
 __global__ void __launch_bounds__(256) fa_tree_merge_kernel(const __grid_constant__ TreeParams p)
 {
@@ -999,49 +1018,66 @@ __global__ void __launch_bounds__(256) fa_tree_merge_kernel(const __grid_constan
         if (p.o_dtype == FA_F32) reinterpret_cast<float4*>(p.o)[i / 4] = v;
         else *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.o) + i) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
     };
-    if (n <= 4) {
+    if (n <= kFew) {
         if (blockIdx.y % 4 != 0) return;
         const int r = static_cast<int>(blockIdx.y) * 8 + warp * 4 + (lane >> 3);
         if (r >= join.rows) return;  // (no warp-wide operation below)
         const int l8 = lane & 7;
-        float x[4];
-        float4 v[4][D / 32];
+        constexpr int Q = D / 32;  // float4 of a lane
+        float4 v[4][Q];
+        auto load = [&](int s0) {
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            x[s] = -INFINITY;
-            if (s < n) {
-                x[s] = __ldg(p.lse_part + at(s, r));
-                const float4* src = reinterpret_cast<const float4*>(p.o_part + at(s, r) * D) + l8;
+            for (int j = 0; j < 4; ++j) {
+                if (s0 + j >= n) continue;
+                const float4* src = reinterpret_cast<const float4*>(p.o_part + at(s0 + j, r) * D) + l8;
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) v[s][i] = __ldg(src + 8 * i);
+                for (int i = 0; i < Q; ++i) v[j][i] = __ldg(src + 8 * i);
             }
+        };
+        float x[kFew];
+#pragma unroll
+        for (int s = 0; s < kFew; ++s) x[s] = s < n ? __ldg(p.lse_part + at(s, r)) : -INFINITY;
+        load(0);  // with the log-sum-exps
+        float M = -INFINITY;
+        bool live = false;
+#pragma unroll
+        for (int s = 0; s < kFew; ++s) {
+            live = live || x[s] != -INFINITY;
+            M = fmaxf(M, x[s]);
         }
-        const float M = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-        const bool live = x[0] != -INFINITY || x[1] != -INFINITY || x[2] != -INFINITY || x[3] != -INFINITY;
         float sum = 0.f;
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
+        for (int s = 0; s < kFew; ++s) {
             x[s] = x[s] == -INFINITY ? 0.f : ex2((x[s] - M) * kLog2e);
             sum += x[s];
         }
         const float inv = live ? 1.f / sum : 0.f;
+        float4 a[Q];
+#pragma unroll
+        for (int i = 0; i < Q; ++i) a[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int s0 = 0; s0 < kFew; s0 += 4) {
+            if (s0 >= n) continue;
+            if (s0 > 0) load(s0);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float f = x[s0 + j] * inv;  // an empty part's output is 0
+                if (s0 + j >= n) continue;
+#pragma unroll
+                for (int i = 0; i < Q; ++i)
+                    a[i] = make_float4(fmaf(f, v[j][i].x, a[i].x), fmaf(f, v[j][i].y, a[i].y), fmaf(f, v[j][i].z, a[i].z),
+                                       fmaf(f, v[j][i].w, a[i].w));
+            }
+        }
         const size_t row = static_cast<size_t>(join.first_row) + r;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const float f = x[s] * inv;  // an empty part's output is 0
-                if (s < n) a = make_float4(fmaf(f, v[s][i].x, a.x), fmaf(f, v[s][i].y, a.y), fmaf(f, v[s][i].z, a.z), fmaf(f, v[s][i].w, a.w));
-            }
-            write(row * D + 4 * (l8 + 8 * i), a);
-        }
+        for (int i = 0; i < Q; ++i) write(row * D + 4 * (l8 + 8 * i), a[i]);
         if (l8 == 0 && p.lse != nullptr) p.lse[row] = live ? M + log2f(sum) * kLn2 : -INFINITY;
         return;
     }
     const int r = static_cast<int>(blockIdx.y) * 8 + warp;
     if (r >= join.rows) return;
-    constexpr int kHeld = kTreeMaxCtas / 32;  // log-sum-exps a lane holds: at most a part for each CTA
+    constexpr int kHeld = kTreeMaxShares / 32;  // log-sum-exps a lane holds: at most a part for each share
     constexpr int V = D / 32;                 // columns of a lane
     float x[kHeld];
     float M = -INFINITY;
@@ -1094,11 +1130,11 @@ __global__ void __launch_bounds__(256) fa_tree_merge_kernel(const __grid_constan
     if (lane == 0 && p.lse != nullptr) p.lse[row] = live ? M + log2f(sum) * kLn2 : -INFINITY;
 }
 
-template <int D, bool PAIR>
+template <int D, TreeForm FORM>
 cudaError_t launch_tree_t(const TreeParams& p, cudaStream_t st)
 {
     using C = TrCfg<D>;
-    auto kern = fa_tree_kernel<D, PAIR>;
+    auto kern = fa_tree_kernel<D, FORM>;
     static bool configured[64] = {};  // attributes set and registers checked, per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1117,14 +1153,15 @@ cudaError_t launch_tree_t(const TreeParams& p, cudaStream_t st)
     }
     e = launch_pdl(kern, dim3(static_cast<unsigned>(p.num_ctas)), kTrThreads, C::kSmemBytes, st, p);
     if (e != cudaSuccess) return e;
-    const dim3 grid(static_cast<unsigned>(p.num_ctas), static_cast<unsigned>((p.part_rows + 7) / 8));
+    const dim3 grid(static_cast<unsigned>(p.num_shares), static_cast<unsigned>((p.part_rows + 7) / 8));
     return launch_pdl(fa_tree_merge_kernel<D>, grid, 256, 0, st, p);
 }
 
 template <int D>
 cudaError_t launch_tree_d(const TreeParams& p, cudaStream_t st)
 {
-    return p.part_rows > kBlockM ? launch_tree_t<D, true>(p, st) : launch_tree_t<D, false>(p, st);
+    if (p.part_rows > kBlockM) return launch_tree_t<D, kPair>(p, st);
+    return p.num_shares > p.num_ctas ? launch_tree_t<D, kSolo>(p, st) : launch_tree_t<D, kAlt>(p, st);
 }
 
 }  // namespace fa

@@ -428,9 +428,9 @@ fa_status fa_qk_norm_rope_append(const void* q, const void* k, const void* v, co
 
 /*
  * Bytes of workspace fa_decode_tree needs on a device with `num_sms` multiprocessors: with rows =
- * Hq / Hkv * T and r = rows, or 256 above 128 rows, fp32 partial outputs [2 num_sms, r, d], fp32
- * log-sum-exps [2 num_sms, r] and 16 num_sms bytes of records, each 256-byte aligned, whatever the
- * batch and the lengths.  Pure host function.  0 on invalid arguments.
+ * Hq / Hkv * T, and s = 2 num_sms and r = rows, or s = num_sms and r = 256 above 128 rows, fp32
+ * partial outputs [2 s, r, d], fp32 log-sum-exps [2 s, r] and 16 s bytes of records, each 256-byte
+ * aligned, whatever the batch and the lengths.  Pure host function.  0 on invalid arguments.
  */
 size_t fa_decode_tree_workspace_size(int Hq, int Hkv, int T, int d, int num_sms);
 

@@ -114,7 +114,7 @@ def test_tree_refusals(lib):
         assert call(**kw) == UNSUPPORTED, kw
     size = lib.fa_decode_tree_workspace_size
     up = lambda x: (x + 255) // 256 * 256  # noqa: E731
-    assert size(8, 2, 5, 128, 152) == up(2 * 152 * 20 * 512) + up(2 * 152 * 20 * 4) + up(16 * 152)
+    assert size(8, 2, 5, 128, 152) == up(4 * 152 * 20 * 512) + up(4 * 152 * 20 * 4) + up(32 * 152)
     assert size(8, 2, 100, 64, 152) == up(2 * 152 * 256 * 256) + up(2 * 152 * 256 * 4) + up(16 * 152)
     assert size(3, 2, 5, 64, 152) == 0 and size(4, 2, 0, 64, 152) == 0 and size(4, 2, 1, 64, 0) == 0
 

@@ -94,6 +94,27 @@ def test_shares_cross_units(B, Hkv, hi, T):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("R,T", [(4, 4), (2, 64), (1, 1)])
+def test_many_units(d, R, T):
+    """Enough (sequence, head) pairs that each warpgroup has a share of its own, with lengths of 0 to 5 key
+    tiles, one long sequence among them, and absent nodes; up to 128 rows."""
+    B, Hkv, hi = 310, 3, 600
+    g = torch.Generator().manual_seed(d + T)
+    lens = torch.randint(0, hi + 1, (B,), generator=g).to(torch.int32)
+    lens[5], lens[6], lens[7] = 0, 2500, 127
+    cnt = torch.randint(0, T + 1, (B,), generator=g).to(torch.int32)
+    q, k, v = inputs(B, Hkv * R, Hkv, T, 2500 + T, d, lens, cnt, seed=T)
+    par = random_parents(B, T, seed=d)
+    ref = tree_attention(q, k, v, lens, par, cnt, 1 / math.sqrt(d))
+    o, lse = call(q, k, v, lens, par, cnt, out_dtype=torch.float32)
+    o2, lse2 = call(q, k, v, lens, par, cnt, out_dtype=torch.float32)
+    assert fa().get_device_error() == 0
+    check_tree(o, lse, ref, f"d={d} R={R} T={T}")
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    check_tree(*call(q, k, v, lens, par, cnt), ref, "bf16")
+
+
 @pytest.mark.parametrize("d,T,R", [(128, 9, 4), (64, 60, 3)])
 def test_chain_and_shallow_trees(d, T, R):
     """No parents: a chain, the same as parents t - 1.  All nodes children of the last token: each sees itself only."""
