@@ -571,7 +571,7 @@ def cache_compact(k_cache, v_cache, seqlens, accepted, n_accepted, seqlens_out=N
     (rows are read before any is written: any order will do).
 
     caches [B,Hkv,Nk_max,d] or [L,B,Hkv,Nk_max,d] bf16, seqlens and n_accepted int32 [B], accepted int32 [B,T]
-    with T <= 128.  Returns seqlens + n_accepted, in ``seqlens_out`` (which must not overlap seqlens).
+    with T <= 128.  Returns seqlens + n_accepted, in ``seqlens_out`` (which must not overlap the other integers).
     """
     r = (_binding or _native()).cache_compact(k_cache, v_cache, seqlens, accepted, n_accepted, seqlens_out)
     if type(r) is int:

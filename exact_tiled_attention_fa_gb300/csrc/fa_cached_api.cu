@@ -16,6 +16,13 @@ bool dtype_ok(fa_dtype t) { return t == FA_BF16 || t == FA_F32; }
 bool flag_ok(int f) { return f == 0 || f == 1; }
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
+// Whether two buffers of a and b bytes overlap.
+bool overlap(const void* p, size_t a, const void* q, size_t b)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(p), y = reinterpret_cast<uintptr_t>(q);
+    return x < y + b && y < x + a;
+}
+
 // Token stride of `heads` heads of d elements: heads do not overlap the next token's, rows stay on
 // 16 bytes (a multiple of 8 elements of either type).
 bool stride_ok(long long s, long long heads, int d) { return s >= heads * d && s % 8 == 0; }
@@ -177,6 +184,8 @@ fa_status fa_qk_norm_rope_append(const void* q, const void* k, const void* v, co
     if (!aligned(v, 16) || !aligned(q_out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(seqlens, 4) ||
         !aligned(parents, 4) || !aligned(n_nodes, 4) || !stride_ok(v_stride, Hkv, d))
         return FA_ERR_INVALID_ARG;
+    const size_t cache = static_cast<size_t>(B) * Hkv * static_cast<size_t>(Nk_max) * d * 2;
+    if (overlap(k_cache, cache, v_cache, cache)) return FA_ERR_INVALID_ARG;
     if (bad != FA_OK) return bad;
     if (T > FA_TREE_MAX_NODES) return FA_ERR_UNSUPPORTED;
     fa::RopeParams p{};
@@ -301,9 +310,14 @@ fa_status fa_cache_compact(void* k_cache, void* v_cache, const int* seqlens, con
     if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(seqlens, 4) || !aligned(accepted, 4) ||
         !aligned(n_accepted, 4) || !aligned(seqlens_out, 4))
         return FA_ERR_INVALID_ARG;
-    // lengths are read by every CTA and written by one: not in place
-    if (seqlens_out != nullptr && seqlens_out < seqlens + B && seqlens < seqlens_out + B) return FA_ERR_INVALID_ARG;
     if (static_cast<long long>(L) * B > 0x7fffffffLL / Hkv) return FA_ERR_INVALID_ARG;
+    // lengths and counts are read by every CTA and written by one: not in place
+    const size_t b4 = static_cast<size_t>(B) * sizeof(int);
+    if (seqlens_out != nullptr && (overlap(seqlens_out, b4, seqlens, b4) || overlap(seqlens_out, b4, n_accepted, b4) ||
+                                   overlap(seqlens_out, b4, accepted, b4 * static_cast<size_t>(T))))
+        return FA_ERR_INVALID_ARG;
+    const size_t cache = static_cast<size_t>(L) * B * Hkv * static_cast<size_t>(Nk_max) * d * 2;
+    if (overlap(k_cache, cache, v_cache, cache)) return FA_ERR_INVALID_ARG;
     if (!head_ok(d) || dv != d || T > FA_TREE_MAX_NODES) return FA_ERR_UNSUPPORTED;
     fa::CompactParams p{};
     if (fa::device_status_word(&p.status) != cudaSuccess) return FA_ERR_CUDA;

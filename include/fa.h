@@ -358,7 +358,8 @@ fa_status fa_merge_states(const float* o_parts, const float* lse_parts, int n_pa
  *   k_out, v_out  bf16 [B, Hkv, N, d], or with expand = 1 [B, Hq, N, d]: head h is key/value head
  *              h / (Hq / Hkv), as fa_fwd takes them  (device, written)
  *   d in {32, 64, 128}; Hkv dividing Hq; rot a multiple of 16, at most d; B * N < 2^31; eps >= 0.
- * Outputs must not overlap inputs.
+ * Outputs must not overlap inputs.  mean(x^2) is an fp32 sum: where it overflows (elements of about 1e18
+ * and more) the row is written as 0.
  */
 fa_status fa_qk_norm_rope(const void* q, const void* k, const void* v, const void* q_weight,
                           const void* k_weight, const float* cos_table, const float* sin_table,
@@ -384,7 +385,8 @@ size_t fa_qk_norm_rope_bwd_workspace_size(int d);
  *   grad_q_weight, grad_k_weight  fp32 [d]  (device, written)
  *   workspace  ws_bytes >= fa_qk_norm_rope_bwd_workspace_size(d), 256-byte aligned; its contents on
  *              entry do not matter.
- * Every sum is in a fixed order: results are the same from run to run.
+ * Every sum is in a fixed order: results are the same from run to run.  Outputs must not overlap
+ * inputs.
  * Returns FA_ERR_WORKSPACE if ws_bytes is too small (nothing launched).
  */
 fa_status fa_qk_norm_rope_bwd(const void* grad_q_out, const void* grad_k_out, const void* grad_v_out,
@@ -415,7 +417,8 @@ fa_status fa_qk_norm_rope_bwd(const void* grad_q_out, const void* grad_k_out, co
  *   q, k, v    bf16 [B, T, heads, d] with token strides
  *   seqlens    int32 [B], parents int32 [B, T] or NULL, n_nodes int32 [B] or NULL  (device)
  *   q_out      bf16 [B, Hq, T, d]           (device, written; 0 for nodes from n on)
- *   k_cache, v_cache  bf16 [B, Hkv, Nk_max, d]  (device; rows p .. p + n - 1 written, no other)
+ *   k_cache, v_cache  bf16 [B, Hkv, Nk_max, d]  (device; rows p .. p + n - 1 written, no other; they must
+ *              not overlap)
  *   T <= FA_TREE_MAX_NODES (else FA_ERR_UNSUPPORTED); positions past max_pos as in fa_qk_norm_rope.
  */
 fa_status fa_qk_norm_rope_append(const void* q, const void* k, const void* v, const void* q_weight,
@@ -465,11 +468,12 @@ fa_status fa_decode_tree(const void* q, const void* k_cache, const void* v_cache
  * rows are read before any is written, so any order (and a node named twice) is fine.  Other rows
  * stay as they were.  seqlens_out[b] = p + n_accepted[b].
  *
- *   k_cache, v_cache  bf16 [L, B, Hkv, Nk_max, d]  (device; L layers' caches behind one another)
+ *   k_cache, v_cache  bf16 [L, B, Hkv, Nk_max, d]  (device; L layers' caches behind one another; they must
+ *              not overlap)
  *   seqlens, n_accepted  int32 [B], accepted int32 [B, T]  (device; 0 <= accepted < T, 0 <= n_accepted
  *              <= T, rows below Nk_max.  An accepted node out of range is not moved, lengths and counts
  *              are clamped; both are recorded as FA_ERR_INVALID_ARG in the device status word.)
- *   seqlens_out  int32 [B]  (device, written; may be NULL; must not overlap seqlens)
+ *   seqlens_out  int32 [B]  (device, written; may be NULL; must not overlap the other int32 arrays)
  *   T <= FA_TREE_MAX_NODES (else FA_ERR_UNSUPPORTED), L * B * Hkv < 2^31.
  */
 fa_status fa_cache_compact(void* k_cache, void* v_cache, const int* seqlens, const int* accepted,

@@ -159,6 +159,43 @@ def test_verification_steps_together():
     assert fa().get_device_error() == 0
 
 
+def test_rows_past_32_bit_offsets():
+    """A cache of more than 2^31 elements: the last rows are appended, attended to and moved.  Every key but the
+    appended ones is 0 (score 0, weight 1), every value 0; the appended keys are long enough to carry most of
+    the weight."""
+    Hq, d, T, Nk = 2, 128, 4, (1 << 24) + 40
+    g = torch.Generator().manual_seed(3)
+    kc, vc = (torch.zeros((1, 1, Nk, d), dtype=BF16, device=DEV) for _ in range(2))
+    at = Nk - 9
+    lens = torch.tensor([at], dtype=torch.int32, device=DEV)
+    x = torch.randn((1, T, Hq + 2, d), generator=g).to(BF16)
+    par = torch.tensor([[-1, 0, 0, 2]], dtype=torch.int32, device=DEV)
+    ones = torch.full((d,), 1.5, dtype=torch.float32, device=DEV)
+    cos, sin = torch.ones((Nk, 8), device=DEV), torch.zeros((Nk, 8), device=DEV)
+    gx = x.to(DEV)
+    q = fa().qk_norm_rope_append(gx[:, :, :Hq], gx[:, :, Hq:Hq + 1], gx[:, :, Hq + 1:], ones, ones, cos, sin, kc, vc, lens, parents=par)
+    assert int((kc != 0).any(-1).sum()) == T and int((vc != 0).any(-1).sum()) == T
+    k, v = kc[0, 0, at:at + T].double().cpu(), vc[0, 0, at:at + T].double().cpu()
+    assert torch.equal(v, x[0, :, Hq + 1].double())
+    scale = 2.0
+    o, lse = fa().decode_tree(q, kc, vc, lens, parents=par, scale=scale, out_dtype=torch.float32)
+    see = torch.tensor([[1, 0, 0, 0], [1, 1, 0, 0], [1, 0, 1, 0], [1, 0, 1, 1]], dtype=torch.bool)
+    s = torch.where(see, q[0].double().cpu() @ k.T * scale, -math.inf)
+    L = torch.logsumexp(torch.cat((s, torch.full((Hq, T, 1), math.log(at), dtype=torch.float64)), -1), -1)
+    O = torch.exp(s - L[..., None]) @ v
+    # scores: 4 d 2^-24 of |q||k| scale; weights 2^-8 more; 2^17 tiles' sums of equal terms are exact in fp32 (weights
+    # of 1 in up to 2^24 of them, split over the shares), then at most 2^9 additions of the parts
+    e = 4 * d * 2.0 ** -24 * float((q[0].double().cpu().abs() @ k.abs().T).max()) * scale
+    bound = (torch.exp(s - L[..., None]) @ v.abs()) * (2.0 ** -8 + 2 * e + 2.0 ** -14)
+    assert float(((o[0].double().cpu() - O).abs() - bound).max()) <= 0
+    assert float((lse[0].double().cpu() - L).abs().max()) <= e + 2.0 ** -14
+    keep = torch.tensor([[0, 2, 3, 0]], dtype=torch.int32, device=DEV)
+    n = fa().cache_compact(kc, vc, lens, keep, torch.tensor([3], dtype=torch.int32, device=DEV))
+    assert n.tolist() == [at + 3] and torch.equal(kc[0, 0, at:at + 4].double().cpu(), k[[0, 2, 3, 3]])
+    assert torch.equal(vc[0, 0, at:at + 4].double().cpu(), v[[0, 2, 3, 3]])
+    assert fa().get_device_error() == 0
+
+
 def test_training_step_together():
     """qk_norm_rope -> fwd -> bwd -> qk_norm_rope_bwd with shared heads: the gradients of the packed projection
     against fp64 differentiation of the whole.  bwd's gradients carry bf16 operands (P, dS and dO rounded: three

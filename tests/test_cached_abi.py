@@ -10,6 +10,7 @@ import exact_tiled_attention_fa_gb300 as fa
 from exact_tiled_attention_fa_gb300 import build as fa_build
 
 P = ctypes.c_void_p(0x10000000)  # never dereferenced: each call below is rejected first
+V = ctypes.c_void_p(0x12000000)
 NULL = ctypes.c_void_p(0)
 ODD = ctypes.c_void_p(0x10000008)
 INVALID, UNSUPPORTED, WORKSPACE = fa.FA_ERR_INVALID_ARG, fa.FA_ERR_UNSUPPORTED, fa.FA_ERR_WORKSPACE
@@ -45,7 +46,7 @@ def bwd(lib):
 
 
 def append(lib):
-    spec = [(n, P) for n in ("q", "k", "v", "wq", "wk", "cos", "sin", "lens", "par", "cnt", "qo", "ko", "vo")]
+    spec = [(n, P) for n in ("q", "k", "v", "wq", "wk", "cos", "sin", "lens", "par", "cnt", "qo", "ko")] + [("vo", V)]
     spec += [("qs", 512), ("ks", 512), ("vs", 512), ("B", 2), ("N", 5), ("Hq", 4), ("Hkv", 2), ("Nk", 64), ("d", 64), ("rot", 64),
              ("max_pos", 100), ("interleaved", 0), ("eps", 1e-6), ("wdt", 0), ("stream", NULL)]
     return caller(lib.fa_qk_norm_rope_append, [n for n, _ in spec], [v for _, v in spec])
@@ -59,7 +60,7 @@ def tree(lib):
 
 
 def compact(lib):
-    spec = [(n, P) for n in ("k", "v")] + [("lens", ctypes.c_void_p(0x20000000)), ("acc", P), ("cnt", P), ("out", P)]
+    spec = [("k", P), ("v", V), ("lens", ctypes.c_void_p(0x20000000)), ("acc", P), ("cnt", P), ("out", ctypes.c_void_p(0x30000000))]
     spec += [("L", 1), ("B", 2), ("Hkv", 2), ("Nk", 64), ("d", 64), ("dv", 64), ("T", 8), ("stream", NULL)]
     return caller(lib.fa_cache_compact, [n for n, _ in spec], [v for _, v in spec])
 
@@ -98,7 +99,7 @@ def test_norm_backward_refusals(lib):
 def test_append_refusals(lib):
     call = append(lib)
     for kw in (dict(v=NULL), dict(lens=NULL), dict(qo=NULL), dict(ko=NULL), dict(vo=NULL), dict(Nk=0), dict(ko=ODD),
-               dict(par=ctypes.c_void_p(0x10000002)), dict(vs=64)):
+               dict(par=ctypes.c_void_p(0x10000002)), dict(vs=64), dict(vo=P), dict(vo=ctypes.c_void_p(0x10007ff0))):
         assert call(**kw) == INVALID, kw
     assert call(N=129) == UNSUPPORTED
 
@@ -123,7 +124,8 @@ def test_compact_refusals(lib):
     call = compact(lib)
     for kw in (dict(k=NULL), dict(v=NULL), dict(lens=NULL), dict(acc=NULL), dict(cnt=NULL), dict(k=ODD), dict(L=0), dict(B=0),
                dict(T=0), dict(Nk=0), dict(out=ctypes.c_void_p(0x20000000)), dict(out=ctypes.c_void_p(0x20000004)),
-               dict(out=ctypes.c_void_p(0x1ffffffc)), dict(L=1 << 15, B=1 << 15, Hkv=4)):
+               dict(out=ctypes.c_void_p(0x1ffffffc)), dict(out=P), dict(acc=ctypes.c_void_p(0x2fffffe0)), dict(v=P),
+               dict(v=ctypes.c_void_p(0x10007ff0)), dict(L=1 << 15, B=1 << 15, Hkv=4)):
         assert call(**kw) == INVALID, kw
     for kw in (dict(T=129), dict(d=96, dv=96), dict(dv=32)):
         assert call(**kw) == UNSUPPORTED, kw
