@@ -59,30 +59,23 @@ namespace fa {
 constexpr int kTrThreads = 384;  // 12 warps = 3 warpgroups
 constexpr int kTrWarpProducer = 8;
 constexpr int kTrWarpMma = 9;  // and 10
-// Registers after the split of fa_fwd_kernel.cuh's kernels without a correction warpgroup:
-// 256 * softmax + 128 * control = 64512 = 384 * 168, checked by the launcher.
-template <int D>
-constexpr int kTrSoftmaxRegs = D == 128 ? 224 : 216;
-template <int D>
-constexpr int kTrControlRegs = D == 128 ? 56 : 72;
-
 enum : int {
     kTbQFull = 0,     // + query buffer
     kTbQEmpty = 2,    // + query buffer: its issuers are done with it
-    kTbSFull = 4,     // + warpgroup
-    kTbSFree = 6,     // + warpgroup: S_i has been read out of TMEM
-    kTbPFull = 8,     // + warpgroup
-    kTbPVDone = 10,   // + warpgroup
-    kTbOReady = 12,   // + warpgroup: the last product of a unit has completed
-    kTbOFree = 14,    // + warpgroup, ALT: O_i has been read out of TMEM by both
-    kTbMLFull = 16,   // ALT: both warpgroups' max and sum are in shared memory
-    kTbDrain = 17,    // + warpgroup
-    kTbKFull = 20,    // + K stage (up to 4)
-    kTbKEmpty = 24,
-    kTbVFull = 28,    // + V stage (up to 4)
-    kTbVEmpty = 32,
-    kTbSegFull = 36,  // + place in the ring of records: the segment's is in shared memory
-    kTbCount = 44
+    kTbSFull = 4,     // + 2 * warpgroup + step: scores of a step's keys
+    kTbPFull = 8,     // + 2 * warpgroup + step: their weights
+    kTbPVDone = 12,   // + 2 * warpgroup + step: the product with them has completed
+    kTbOReady = 16,   // + warpgroup: the last product of a unit has completed
+    kTbOFree = 18,    // + warpgroup, ALT: O_i has been read out of TMEM by both
+    kTbMLFull = 20,   // ALT: both warpgroups' max and sum are in shared memory
+    kTbDrain = 21,    // + warpgroup
+    kTbSFree = 48,    // + warpgroup, d <= 64: S_i has been read out of TMEM
+    kTbKFull = 24,    // + K stage (up to 4)
+    kTbKEmpty = 28,
+    kTbVFull = 32,    // + V stage (up to 4)
+    kTbVEmpty = 36,
+    kTbSegFull = 40,  // + place in the ring of records: the segment's is in shared memory
+    kTbCount = 50
 };
 
 // A segment as the producer hands it to the other roles: a run of key tiles of one unit.
@@ -101,9 +94,23 @@ constexpr int kTrSegs = 8;
 
 enum TreeForm { kAlt, kSolo, kPair };
 
-template <int D>
+template <int D, TreeForm FORM>
 struct TrCfg {
     static_assert(D == 32 || D == 64 || D == 128, "head size");
+    // Steps of a tile.  At d = 128 tensor memory has no room for P beside S and O: P overwrites S, and a
+    // tile's scores wait for the product of the tile before.  In PAIR form, where the tensor core is what
+    // counts, a tile therefore goes in two steps of 64 keys whose columns are used in turn: one's product
+    // and its next scores run under the other's exponentials (16 sequences of 1 - 32K tokens, 64 nodes,
+    // 32/8 heads: 288 us in one step, 259 in two; 64 of 1000 tokens: 101 and 94).  The other forms wait for
+    // memory, and a tile in two steps reads the queries from shared memory twice: one step (16 nodes 170 us,
+    // in two steps 177; d = 64, 64 nodes 111 and 155).
+    static constexpr int kSteps = D == 128 && FORM == kPair ? 2 : 1;
+    static constexpr int kStep = kBlockN / kSteps;  // keys
+    // Registers after the split: 256 * softmax + 128 * control = 64512 = 384 * 168, checked by the launcher.
+    // A softmax thread holds the scores of a step.  (With 224 and 56 at d = 128 the producers and issuers
+    // spilled: 256 sequences of 300 tokens 77.7 us, with 216 and 72 they take 72.9.)
+    static constexpr int kSoftmaxRegs = kSteps == 2 ? 192 : D == 128 ? 216 : 208;
+    static constexpr int kControlRegs = kSteps == 2 ? 120 : D == 128 ? 72 : 88;
     static constexpr int kCB = D < 64 ? D : 64;
     static constexpr int kNumCB = D / kCB;
     static constexpr int kRowBytes = kCB * 2;
@@ -130,13 +137,10 @@ struct TrCfg {
     static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
     static constexpr int kTmemCols = 512;
     static constexpr bool kAliasP = D == 128;
-    __host__ __device__ static constexpr uint32_t col_s(int i) { return 128u * i; }
+    __host__ __device__ static constexpr uint32_t col_s(int i) { return 128u * i; }  // a step's columns: + kStep * step
     __host__ __device__ static constexpr uint32_t col_o(int i) { return 256u + static_cast<uint32_t>(D) * i; }
-    __host__ __device__ static constexpr uint32_t col_p(int i)
-    {
-        return kAliasP ? col_s(i) : 256u + 2u * D + 64u * i;
-    }
-    static constexpr uint32_t kIdescS = idesc_bf16(kBlockM, kBlockN, false);
+    __host__ __device__ static constexpr uint32_t col_p(int i) { return kAliasP ? col_s(i) : 256u + 2u * D + 64u * i; }
+    static constexpr uint32_t kIdescS = idesc_bf16(kBlockM, kStep, false);
     static constexpr uint32_t kIdescO = idesc_bf16(kBlockM, D, true);
 };
 
@@ -376,14 +380,92 @@ struct RowsOut {
 
 __device__ __forceinline__ float2 as_float2(uint32_t a, uint32_t b) { return make_float2(__uint_as_float(a), __uint_as_float(b)); }
 
+// Masks scores s of the N keys from node index `shift` on (keys before node 0 are cached tokens, seen by
+// all) by the row's ancestors; their max.
+template <int N>
+__device__ __forceinline__ float tree_mask(float (&s)[N], int shift, const uint32_t (&vis)[4])
+{
+    auto word = [&](int q) -> uint32_t {
+        return q == 0 ? vis[0] : q == 1 ? vis[1] : q == 2 ? vis[2] : q == 3 ? vis[3] : 0u;
+    };
+    float a[N / 32];
+#pragma unroll
+    for (int q = 0; q < N / 32; ++q) {
+        const int bit = shift + 32 * q;
+        const int cached = min(max(-bit, 0), 32);  // columns that are cached tokens
+        const uint32_t seen = __funnelshift_r(word(bit >> 5), word((bit >> 5) + 1), bit & 31) |
+                              (cached == 32 ? 0xffffffffu : (1u << cached) - 1u);
+        a[q] = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+            s[32 * q + c] = (seen >> c) & 1u ? s[32 * q + c] : -INFINITY;
+            a[q] = fmaxf(a[q], s[32 * q + c]);
+        }
+    }
+    if constexpr (N == 64) return fmaxf(a[0], a[1]);
+    else return fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
+}
+
+// A row's running max (of scale * log2(e) * S over visible keys) and sum, for scores with max `mrow`.
+struct TreeRow {
+    float m = -INFINITY, l = 0.f;
+    float alpha;  // what a grown max scales the sum and O by
+    __device__ __forceinline__ bool grow(float mrow, float sl2)
+    {
+        const float mt = mrow * sl2;
+        alpha = 1.f;
+        if (!(mt > m)) return false;
+        alpha = ex2(m - mt);  // 0 when m = -inf
+        m = mt;
+        return true;
+    }
+    __device__ __forceinline__ void add(const float2 (&rs)[4])
+    {
+        l = l * alpha + (((rs[0].x + rs[0].y) + (rs[1].x + rs[1].y)) + ((rs[2].x + rs[2].y) + (rs[3].x + rs[3].y)));
+    }
+};
+
+// Weights 2^(sl2 s - m) of columns c0 .. c0 + N - 1 into pk, rounded to bf16 for the product (half a step,
+// 2^-8 of each weight); their fp32 values are added to the four partial sums rs.
+template <int N, int KS>
+__device__ __forceinline__ void tree_exps(int c0, const float (&s)[KS], float sl2, float m, float2 (&rs)[4], uint32_t (&pk)[KS / 2])
+{
+    const float m_use = m == -INFINITY ? 0.f : m;
+    const float2 sl2x2 = make_float2(sl2, sl2), negm = make_float2(-m_use, -m_use);
+#pragma unroll
+    for (int cc = 0; cc < N; cc += 8) {
+        const int c = c0 + cc;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float2 x = __ffma2_rn(make_float2(s[c + 2 * q], s[c + 2 * q + 1]), sl2x2, negm);
+            const float2 e = make_float2(ex2(x.x), ex2(x.y));
+            rs[q] = __fadd2_rn(rs[q], e);
+            pk[c / 2 + q] = pack_bf16x2(e.x, e.y);
+        }
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void tree_scale(uint32_t (&o)[N], float alpha)
+{
+    const float2 a2 = make_float2(alpha, alpha);
+#pragma unroll
+    for (int e = 0; e < N; e += 2) {
+        const float2 x = __fmul2_rn(as_float2(o[e], o[e + 1]), a2);
+        o[e] = __float_as_uint(x.x);
+        o[e + 1] = __float_as_uint(x.y);
+    }
+}
+
 template <int D, TreeForm FORM>
 __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_constant__ TreeParams p)
 {
-    using C = TrCfg<D>;
+    using C = TrCfg<D, FORM>;
     constexpr bool ALT = FORM == kAlt, SOLO = FORM == kSolo, PAIR = FORM == kPair;
     constexpr int kStreams = SOLO ? 2 : 1;         // shares, producers, rings
     constexpr int S = C::kStages / kStreams;       // stages of a stream's ring
     constexpr int kSegs = kTrSegs / kStreams;      // records of a stream
+    constexpr int H = C::kSteps, KS = C::kStep;    // steps of a tile, keys of a step
     extern __shared__ uint8_t tr_smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(tr_smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
@@ -403,10 +485,12 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(kTbQFull + i), 1);
             mbar_init(bar(kTbQEmpty + i), SOLO ? 1 : 2);
-            mbar_init(bar(kTbSFull + i), 1);
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(bar(kTbSFull + 2 * i + h), 1);
+                mbar_init(bar(kTbPFull + 2 * i + h), kBlockM);
+                mbar_init(bar(kTbPVDone + 2 * i + h), 1);
+            }
             mbar_init(bar(kTbSFree + i), kBlockM);
-            mbar_init(bar(kTbPFull + i), kBlockM);
-            mbar_init(bar(kTbPVDone + i), 1);
             mbar_init(bar(kTbOReady + i), 1);
             mbar_init(bar(kTbOFree + i), 2 * kBlockM);
             mbar_init(bar(kTbDrain + i), 1);
@@ -450,7 +534,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
     };
 
     if (warp >= kTrWarpProducer) {
-        regs_decrease<kTrControlRegs<D>>();
+        regs_decrease<C::kControlRegs>();
         const int stream = warp == kTrWarpProducer ? 0 : warp == kTrWarpProducer + 3 ? 1 : kStreams;
         if (stream < kStreams) {
             // ======================================================== producer
@@ -565,45 +649,48 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                 const uint32_t d_s = tmem + C::col_s(i);
                 const uint32_t d_o = tmem + C::col_o(i);
                 const uint32_t a_p = tmem + C::col_p(i);
-                int tiles = 0;   // products issued by this issuer
-                int s_done = 0;  // score tiles issued
+                int tiles = 0;   // tiles whose products have been issued
+                int s_done = 0;  // tiles whose scores have been issued
                 int k = 0;       // tile of the share
                 int segs = 0;    // segments walked
                 int o_uses = 0;  // ALT: OFree phases that precede the next first product
                 const int my = SOLO ? i : 0;  // stream
                 const int stage0 = my * S;
                 bool ok = true;
-                auto issue_s = [&](int q_tile, int stage) {
+                auto issue_s = [&](int q_tile, int stage, int h) {
                     const uint64_t a0 = smem_desc(sbase + C::kOffQ + q_tile * C::kTileBytes, 16, C::kAtomBytes, C::kLayout);
-                    const uint64_t b0 = smem_desc(sbase + C::kOffK + stage * C::kTileBytes, 16, C::kAtomBytes, C::kLayout);
+                    const uint64_t b0 = smem_desc(sbase + C::kOffK + stage * C::kTileBytes + h * KS * C::kRowBytes, 16,
+                                                  C::kAtomBytes, C::kLayout);
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off = ((kk * 16) / C::kCB * C::kBlkBytes + ((kk * 16) % C::kCB) * 2) >> 4;
-                        umma_ss(d_s, a0 + off, b0 + off, C::kIdescS, kk > 0 ? 1u : 0u);
+                        umma_ss(d_s + KS * h, a0 + off, b0 + off, C::kIdescS, kk > 0 ? 1u : 0u);
                     }
                 };
-                auto issue_pv = [&](int stage, bool accumulate) {
-                    const uint64_t b0 = smem_desc(sbase + C::kOffV + stage * C::kTileBytes, C::kBlkBytes, C::kAtomBytes,
-                                                  C::kLayout);
+                auto issue_pv = [&](int stage, int h, bool accumulate) {
+                    const uint64_t b0 = smem_desc(sbase + C::kOffV + stage * C::kTileBytes + h * KS * C::kRowBytes, C::kBlkBytes,
+                                                  C::kAtomBytes, C::kLayout);
 #pragma unroll
-                    for (int kk = 0; kk < kBlockN / 16; ++kk)
-                        umma_ts(d_o, a_p + 8u * kk, b0 + ((kk * 16 * C::kRowBytes) >> 4), C::kIdescO,
+                    for (int kk = 0; kk < KS / 16; ++kk)
+                        umma_ts(d_o, a_p + KS * h + 8u * kk, b0 + ((kk * 16 * C::kRowBytes) >> 4), C::kIdescO,
                                 (accumulate || kk > 0) ? 1u : 0u);
                 };
-                // S_i of share tile kk.  Its columns must have been read (and, where P overwrites
-                // them, the product that reads P must have completed).
-                auto do_s = [&](int q_tile, int q_buf, int kk, bool last) -> bool {
+                // Step h of S_i of share tile kk: its columns must have been read (and, where the weights
+                // overwrite them, the product with those must have completed).
+                auto do_s = [&](int q_tile, int q_buf, int kk, int h, bool last) -> bool {
                     const int s = stage0 + kk % S;
-                    if (!mbar_wait(bar(kTbKFull + s), static_cast<uint32_t>(kk / S) & 1, limit, abort_flag)) return false;
-                    if (s_done > 0 && !mbar_wait(bar((C::kAliasP ? kTbPVDone : kTbSFree) + i),
+                    if (h == 0 && !mbar_wait(bar(kTbKFull + s), static_cast<uint32_t>(kk / S) & 1, limit, abort_flag)) return false;
+                    if (s_done > 0 && !mbar_wait(bar(C::kAliasP ? kTbPVDone + 2 * i + h : kTbSFree + i),
                                                  static_cast<uint32_t>(s_done - 1) & 1, limit, abort_flag))
                         return false;
-                    ++s_done;
                     tc_fence_after_sync();
-                    issue_s(q_tile, s);
-                    umma_commit(bar(kTbSFull + i));
-                    umma_commit(bar(kTbKEmpty + s));
-                    if (last) umma_commit(bar(kTbQEmpty + q_buf));
+                    issue_s(q_tile, s, h);
+                    umma_commit(bar(kTbSFull + 2 * i + h));
+                    if (h == H - 1) {
+                        ++s_done;
+                        umma_commit(bar(kTbKEmpty + s));
+                        if (last) umma_commit(bar(kTbQEmpty + q_buf));
+                    }
                     return true;
                 };
                 constexpr int step = ALT ? 2 : 1;
@@ -635,29 +722,59 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                         }
                     } else {
                         const int j_last = j0 + (w.n - 1 - j0) / step * step;
-                        ok = do_s(q_tile, q_buf, k + j0, j0 == j_last);
+                        for (int h = 0; ok && h < H; ++h) ok = do_s(q_tile, q_buf, k + j0, h, j0 == j_last);
                         for (int j = j0; ok && j < w.n; j += step) {
                             const int kk = k + j;
                             const int s = stage0 + kk % S;
-                            // Without aliasing the next scores need only the current ones read: they run
-                            // while this tile is still being exponentiated.
-                            if (!C::kAliasP && j + step < w.n) ok = do_s(q_tile, q_buf, kk + step, j + step == j_last);
-                            ok = ok && mbar_wait(bar(kTbPFull + i), static_cast<uint32_t>(tiles) & 1, limit, abort_flag) &&
-                                 mbar_wait(bar(kTbVFull + s), static_cast<uint32_t>(kk / S) & 1, limit, abort_flag);
-                            // The first product of a segment overwrites O_i: the last segment's must have been
-                            // read.  P's arrival means that for this warpgroup; in ALT form the other reads O_i
-                            // too.  (Waited for after P: this warpgroup has then been through every earlier
-                            // segment's exchange, so the barrier is at most one phase behind.)
-                            if (ALT && ok && j == j0 && o_uses > 0)
-                                ok = mbar_wait(bar(kTbOFree + i), static_cast<uint32_t>(o_uses - 1) & 1, limit, abort_flag);
-                            if (!ok) break;
-                            tc_fence_after_sync();
-                            issue_pv(s, j > j0);
-                            umma_commit(bar(kTbPVDone + i));
-                            if (j == j_last) umma_commit(bar(kTbOReady + i));
-                            umma_commit(bar(kTbVEmpty + s));
-                            ++tiles;
-                            if (C::kAliasP && j + step < w.n) ok = do_s(q_tile, q_buf, kk + step, j + step == j_last);
+                            const uint32_t ph = static_cast<uint32_t>(tiles) & 1;
+                            if constexpr (H == 1) {
+                                // Without aliasing the next scores need only the current ones read: they run
+                                // while this tile is still being exponentiated.
+                                if (!C::kAliasP && j + step < w.n) ok = do_s(q_tile, q_buf, kk + step, 0, j + step == j_last);
+                                ok = ok && mbar_wait(bar(kTbPFull + 2 * i), ph, limit, abort_flag) &&
+                                     mbar_wait(bar(kTbVFull + s), static_cast<uint32_t>(kk / S) & 1, limit, abort_flag);
+                                // The first product of a segment overwrites O_i: the last segment's must have been
+                                // read.  P's arrival means that for this warpgroup; in ALT form the other reads O_i
+                                // too.  (Waited for after P: this warpgroup has then been through every earlier
+                                // segment's exchange, so the barrier is at most one phase behind.)
+                                if (ALT && ok && j == j0 && o_uses > 0)
+                                    ok = mbar_wait(bar(kTbOFree + i), static_cast<uint32_t>(o_uses - 1) & 1, limit, abort_flag);
+                                if (!ok) break;
+                                tc_fence_after_sync();
+                                issue_pv(s, 0, j > j0);
+                                umma_commit(bar(kTbPVDone + 2 * i));
+                                if (j == j_last) umma_commit(bar(kTbOReady + i));
+                                umma_commit(bar(kTbVEmpty + s));
+                                ++tiles;
+                                if (C::kAliasP && j + step < w.n) ok = do_s(q_tile, q_buf, kk + step, 0, j + step == j_last);
+                            } else {
+                                static_assert(H == 1 || (PAIR && C::kAliasP), "two steps");
+                                // Scores run a step or more ahead of the weights: while the softmax works on one
+                                // step, the other's product and its next scores are under way.
+                                bool early = false;
+                                for (int h = 0; ok && h < 2; ++h) {
+                                    ok = mbar_wait(bar(kTbPFull + 2 * i + h), ph, limit, abort_flag);
+                                    if (h == 0) ok = ok && mbar_wait(bar(kTbVFull + s), static_cast<uint32_t>(kk / S) & 1, limit, abort_flag);
+                                    if (!ok) break;
+                                    tc_fence_after_sync();
+                                    issue_pv(s, h, j > j0 || h > 0);
+                                    umma_commit(bar(kTbPVDone + 2 * i + h));
+                                    if (h == 1) {
+                                        if (j == j_last) umma_commit(bar(kTbOReady + i));
+                                        umma_commit(bar(kTbVEmpty + s));
+                                    }
+                                    // The next tile's scores in the columns that this product frees; its first step's
+                                    // now only if its keys are there already: the second step's product must not wait
+                                    // for them (V's stage, and with it the next V, would wait too).
+                                    if (j + step < w.n) {
+                                        const int nx = stage0 + (kk + step) % S;
+                                        if (h == 0) early = mbar_test(bar(kTbKFull + nx), static_cast<uint32_t>((kk + step) / S) & 1);
+                                        if (h == 0 ? early : !early) ok = do_s(q_tile, q_buf, kk + step, 0, j + step == j_last);
+                                        if (h == 1) ok = ok && do_s(q_tile, q_buf, kk + step, 1, j + step == j_last);
+                                    }
+                                }
+                                ++tiles;
+                            }
                         }
                     }
                     ++o_uses;
@@ -670,7 +787,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
             }
         }
     } else {
-        regs_increase<kTrSoftmaxRegs<D>>();
+        regs_increase<C::kSoftmaxRegs>();
         // ============================================================ softmax + epilogue
         const int wg = warp >> 2;
         const int r = threadIdx.x & 127;  // row of the tile == TMEM lane
@@ -712,163 +829,164 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                 tree_ancestors(p.parents != nullptr ? p.parents + static_cast<size_t>(w.b) * p.T : nullptr, p.T,
                                r < rows && node < w.nodes ? node : -1, lane, p.status, vis);
             }
-            float m_run = -INFINITY;  // running max of scale * log2(e) * S over visible keys
-            float l = 0.f;
-            for (int j = j0; j < w.n; j += step) {
-                ok = __all_sync(0xffffffffu, mbar_wait(bar(kTbSFull + wg), tiles & 1, limit, abort_flag));
-                if (!ok) break;
-                tc_fence_after_sync();
-                const int k0 = (w.tile + j) * kBlockN;
+            TreeRow row;
+            // V rows past the tree may hold anything: zero them before the product reads them.  (The stage's
+            // tile before has been consumed, by the issuer that then issued this tile's scores, so the phase
+            // parity cannot mean that one.)
+            auto zero_tail = [&](int j, int k0) {
                 const int vs = my * S + (k + j) % S;  // V stage
-                if (warp_live) {
-                    uint32_t u[kBlockN];
-                    float mrow;
-                    if constexpr (D == 128) {
-                        float mh[2];
-                        tmem_ld64_max(t_s + 0, *reinterpret_cast<uint32_t(*)[64]>(&u[0]), mh[0]);
-                        tmem_ld64_max(t_s + 64, *reinterpret_cast<uint32_t(*)[64]>(&u[64]), mh[1]);
-                        tmem_ld_wait();
-                        mrow = fmaxf(mh[0], mh[1]);
-                    } else {
-                        float mq[4];
-                        tmem_ld32_max(t_s + 0, *reinterpret_cast<uint32_t(*)[32]>(&u[0]), mq[0]);
-                        tmem_ld32_max(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(&u[32]), mq[1]);
-                        tmem_ld32_max(t_s + 64, *reinterpret_cast<uint32_t(*)[32]>(&u[64]), mq[2]);
-                        tmem_ld32_max(t_s + 96, *reinterpret_cast<uint32_t(*)[32]>(&u[96]), mq[3]);
-                        tmem_ld_wait();
-                        mrow = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
-                    }
-                    if constexpr (!C::kAliasP) {
-                        tc_fence_before_sync();
-                        mbar_arrive(bar(kTbSFree + wg));
-                    }
-                    float s[kBlockN];
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(kTbVFull + vs), static_cast<uint32_t>((k + j) / S) & 1, limit, abort_flag));
+                if (!ok) return;
+                if (k0 + r >= end) {
+                    const uint32_t vrow = sbase + C::kOffV + vs * C::kTileBytes + r * C::kRowBytes;
 #pragma unroll
-                    for (int c = 0; c < kBlockN; ++c) s[c] = __uint_as_float(u[c]);
-                    if (k0 + kBlockN > w.prefix) {  // the tile holds drafted rows, or rows past them
-                        const int shift = k0 - w.prefix;  // node index of the tile's first key
-                        auto word = [&](int q) -> uint32_t {
-                            return q == 0 ? vis[0] : q == 1 ? vis[1] : q == 2 ? vis[2] : q == 3 ? vis[3] : 0u;
-                        };
-                        float a[4];
+                    for (int cb = 0; cb < C::kNumCB; ++cb)
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const int bit = shift + 32 * q;
-                            const int cached = min(max(-bit, 0), 32);  // columns that are cached tokens
-                            const uint32_t seen = __funnelshift_r(word(bit >> 5), word((bit >> 5) + 1), bit & 31) |
-                                                  (cached == 32 ? 0xffffffffu : (1u << cached) - 1u);
-                            a[q] = -INFINITY;
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) {
-                                s[32 * q + c] = (seen >> c) & 1u ? s[32 * q + c] : -INFINITY;
-                                a[q] = fmaxf(a[q], s[32 * q + c]);
-                            }
-                        }
-                        mrow = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
-                    }
-                    const float mt = mrow * sl2;
-                    const bool grow = mt > m_run;
-                    float alpha = 1.f;
-                    if (grow) {
-                        alpha = ex2(m_run - mt);  // 0 when m_run = -inf
-                        m_run = mt;
-                    }
-                    const float m_use = m_run == -INFINITY ? 0.f : m_run;
-                    const float2 sl2x2 = make_float2(sl2, sl2), negm = make_float2(-m_use, -m_use);
-                    float2 rs[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
-                                    make_float2(0.f, 0.f)};
-                    uint32_t pk[kBlockN / 2];
-                    auto exps = [&](int c0) {  // weights of columns c0 .. c0 + 31
-#pragma unroll
-                        for (int c = c0; c < c0 + 32; c += 8) {
-#pragma unroll
-                            for (int h = 0; h < 4; ++h) {
-                                const float2 x = __ffma2_rn(make_float2(s[c + 2 * h], s[c + 2 * h + 1]), sl2x2, negm);
-                                const float2 e = make_float2(ex2(x.x), ex2(x.y));
-                                rs[h] = __fadd2_rn(rs[h], e);
-                                // the weights are rounded to bf16 for the product (half a step, 2^-8 of each
-                                // weight); the sum l keeps the fp32 ones
-                                pk[c / 2 + h] = pack_bf16x2(e.x, e.y);
-                            }
-                        }
-                    };
-                    const float2 a2 = make_float2(alpha, alpha);
-                    auto scale = [&](uint32_t (&oc)[32]) {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            const float2 x = __fmul2_rn(make_float2(__uint_as_float(oc[e]), __uint_as_float(oc[e + 1])), a2);
-                            oc[e] = __float_as_uint(x.x);
-                            oc[e + 1] = __float_as_uint(x.y);
-                        }
-                    };
-                    const bool rescale = __any_sync(0xffffffffu, grow) && j > j0;
-                    if constexpr (C::kAliasP) {
-                        // The previous product has completed (the arrival of S_i implies it): where the
-                        // max grew, O_i is rescaled 32 columns at a time under the exponentials of 32.
-#pragma unroll
-                        for (int c = 0; c < kBlockN; c += 32) {
-                            uint32_t oc[32];
-                            if (rescale) tmem_ld32(t_o + static_cast<uint32_t>(c), oc);
-                            exps(c);
-                            if (rescale) {
-                                tmem_ld_wait();
-                                scale(oc);
-                                tmem_st32(t_o + static_cast<uint32_t>(c), oc);
-                            }
-                        }
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < kBlockN; c += 32) exps(c);
-                        // O_i and P_i are free once the previous product has completed
-                        if (j > j0) {
-                            ok = __all_sync(0xffffffffu, mbar_wait(bar(kTbPVDone + wg), (tiles - 1) & 1, limit, abort_flag));
-                            if (!ok) break;
-                            tc_fence_after_sync();
-                        }
-                        if (rescale) {
-                            uint32_t oc[D / 32][32];
-#pragma unroll
-                            for (int c = 0; c < D / 32; ++c) tmem_ld32(t_o + 32u * c, oc[c]);
+                        for (int c16 = 0; c16 < C::kRowBytes; c16 += 16)
+                            st_shared_v4(vrow + cb * C::kBlkBytes + c16, 0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_shared();
+            };
+            for (int j = j0; ok && j < w.n; j += step) {
+                const int k0 = (w.tile + j) * kBlockN;
+                if constexpr (H == 1) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(bar(kTbSFull + 2 * wg), tiles & 1, limit, abort_flag));
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    if (warp_live) {
+                        uint32_t u[kBlockN];
+                        float mrow;
+                        if constexpr (D == 128) {
+                            float mh[2];
+                            tmem_ld64_max(t_s + 0, *reinterpret_cast<uint32_t(*)[64]>(&u[0]), mh[0]);
+                            tmem_ld64_max(t_s + 64, *reinterpret_cast<uint32_t(*)[64]>(&u[64]), mh[1]);
                             tmem_ld_wait();
+                            mrow = fmaxf(mh[0], mh[1]);
+                        } else {
+                            float mq[4];
+                            tmem_ld32_max(t_s + 0, *reinterpret_cast<uint32_t(*)[32]>(&u[0]), mq[0]);
+                            tmem_ld32_max(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(&u[32]), mq[1]);
+                            tmem_ld32_max(t_s + 64, *reinterpret_cast<uint32_t(*)[32]>(&u[64]), mq[2]);
+                            tmem_ld32_max(t_s + 96, *reinterpret_cast<uint32_t(*)[32]>(&u[96]), mq[3]);
+                            tmem_ld_wait();
+                            mrow = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
+                        }
+                        if constexpr (!C::kAliasP) {
+                            tc_fence_before_sync();
+                            mbar_arrive(bar(kTbSFree + wg));
+                        }
+                        float s[kBlockN];
 #pragma unroll
-                            for (int c = 0; c < D / 32; ++c) {
-                                scale(oc[c]);
-                                tmem_st32(t_o + 32u * c, oc[c]);
+                        for (int c = 0; c < kBlockN; ++c) s[c] = __uint_as_float(u[c]);
+                        if (k0 + kBlockN > w.prefix) mrow = tree_mask(s, k0 - w.prefix, vis);  // drafted rows, or rows past them
+                        const bool rescale = __any_sync(0xffffffffu, row.grow(mrow, sl2)) && j > j0;
+                        float2 rs[4] = {};
+                        uint32_t pk[kBlockN / 2];
+                        if constexpr (C::kAliasP) {
+                            // The previous product has completed (the arrival of S_i implies it): where the
+                            // max grew, O_i is rescaled 32 columns at a time under the exponentials of 32.
+#pragma unroll
+                            for (int c = 0; c < kBlockN; c += 32) {
+                                uint32_t oc[32];
+                                if (rescale) tmem_ld32(t_o + static_cast<uint32_t>(c), oc);
+                                tree_exps<32>(c, s, sl2, row.m, rs, pk);
+                                if (rescale) {
+                                    tmem_ld_wait();
+                                    tree_scale(oc, row.alpha);
+                                    tmem_st32(t_o + static_cast<uint32_t>(c), oc);
+                                }
+                            }
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < kBlockN; c += 32) tree_exps<32>(c, s, sl2, row.m, rs, pk);
+                            // O_i and P_i are free once the previous product has completed
+                            if (j > j0) {
+                                ok = __all_sync(0xffffffffu, mbar_wait(bar(kTbPVDone + 2 * wg), (tiles - 1) & 1, limit, abort_flag));
+                                if (!ok) break;
+                                tc_fence_after_sync();
+                            }
+                            if (rescale) {
+                                uint32_t oc[D / 32][32];
+#pragma unroll
+                                for (int c = 0; c < D / 32; ++c) tmem_ld32(t_o + 32u * c, oc[c]);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int c = 0; c < D / 32; ++c) {
+                                    tree_scale(oc[c], row.alpha);
+                                    tmem_st32(t_o + 32u * c, oc[c]);
+                                }
                             }
                         }
+                        tmem_st32(t_p + 0, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
+                        tmem_st32(t_p + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
+                        tmem_st_wait();
+                        row.add(rs);
+                    } else if (!C::kAliasP) {
+                        mbar_arrive(bar(kTbSFree + wg));
+                        // A warp without rows waits for the previous product too: with the next scores
+                        // already there, it could otherwise arrive twice in one phase of PFull.
+                        if (j > j0) {
+                            ok = __all_sync(0xffffffffu, mbar_wait(bar(kTbPVDone + 2 * wg), (tiles - 1) & 1, limit, abort_flag));
+                            if (!ok) break;
+                        }
                     }
-                    tmem_st32(t_p + 0, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
-                    tmem_st32(t_p + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
-                    tmem_st_wait();
-                    l = l * alpha + (((rs[0].x + rs[0].y) + (rs[1].x + rs[1].y)) + ((rs[2].x + rs[2].y) + (rs[3].x + rs[3].y)));
-                } else if (!C::kAliasP) {
-                    mbar_arrive(bar(kTbSFree + wg));
-                    // A warp without rows waits for the previous product too: with the next scores
-                    // already there, it could otherwise arrive twice in one phase of PFull.
-                    if (j > j0) {
-                        ok = __all_sync(0xffffffffu, mbar_wait(bar(kTbPVDone + wg), (tiles - 1) & 1, limit, abort_flag));
+                    if (k0 + kBlockN > end) {
+                        zero_tail(j, k0);
                         if (!ok) break;
                     }
-                }
-                if (k0 + kBlockN > end) {
-                    // V rows past the tree may hold anything: zero them before the product reads them.
-                    // (The stage's tile before it has been consumed, by the issuer that then issued these
-                    // scores, so the phase parity cannot mean that one.)
-                    ok = __all_sync(0xffffffffu, mbar_wait(bar(kTbVFull + vs), static_cast<uint32_t>((k + j) / S) & 1,
-                                                           limit, abort_flag));
-                    if (!ok) break;
-                    if (k0 + r >= end) {
-                        const uint32_t vrow = sbase + C::kOffV + vs * C::kTileBytes + r * C::kRowBytes;
+                    tc_fence_before_sync();
+                    mbar_arrive(bar(kTbPFull + 2 * wg));
+                } else {
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        ok = __all_sync(0xffffffffu, mbar_wait(bar(kTbSFull + 2 * wg + h), tiles & 1, limit, abort_flag));
+                        if (!ok) break;
+                        tc_fence_after_sync();
+                        if (warp_live) {
+                            uint32_t u[KS];
+                            float mrow;
+                            tmem_ld64_max(t_s + KS * h, u, mrow);
+                            tmem_ld_wait();
+                            float s[KS];
 #pragma unroll
-                        for (int cb = 0; cb < C::kNumCB; ++cb)
+                            for (int c = 0; c < KS; ++c) s[c] = __uint_as_float(u[c]);
+                            const int shift = k0 + KS * h - w.prefix;
+                            if (shift > -KS) mrow = tree_mask(s, shift, vis);  // drafted rows, or rows past them
+                            const bool grow = row.grow(mrow, sl2);
+                            float2 rs[4] = {};
+                            uint32_t pk[KS / 2];
+                            tree_exps<KS>(0, s, sl2, row.m, rs, pk);
+                            row.add(rs);
+                            // the columns of these scores are free: each thread has read its own
+                            tmem_st32(t_p + KS * h, pk);
+                            if (__any_sync(0xffffffffu, grow) && (j > j0 || h > 0)) {
+                                // O_i can be rescaled once the product before (the other step's) has completed.  (The
+                                // one before that has: the arrival of these scores means it, so the parity is clear.)
+                                const uint32_t ph = static_cast<uint32_t>(h == 1 ? tiles : tiles - 1) & 1;
+                                ok = __all_sync(0xffffffffu, mbar_wait(bar(kTbPVDone + 2 * wg + 1 - h), ph, limit, abort_flag));
+                                if (!ok) break;
+                                tc_fence_after_sync();
 #pragma unroll
-                            for (int c16 = 0; c16 < C::kRowBytes; c16 += 16)
-                                st_shared_v4(vrow + cb * C::kBlkBytes + c16, 0u, 0u, 0u, 0u);
+                                for (int c0 = 0; c0 < D; c0 += 64) {
+                                    uint32_t oc[64];
+#pragma unroll
+                                    for (int c = 0; c < 64; c += 32) tmem_ld32(t_o + static_cast<uint32_t>(c0 + c), *reinterpret_cast<uint32_t(*)[32]>(&oc[c]));
+                                    tmem_ld_wait();
+                                    tree_scale(oc, row.alpha);
+#pragma unroll
+                                    for (int c = 0; c < 64; c += 32) tmem_st32(t_o + static_cast<uint32_t>(c0 + c), *reinterpret_cast<uint32_t(*)[32]>(&oc[c]));
+                                }
+                            }
+                            tmem_st_wait();
+                        }
+                        if (k0 + kBlockN > end && h == 0) {
+                            zero_tail(j, k0);
+                            if (!ok) break;
+                        }
+                        tc_fence_before_sync();
+                        mbar_arrive(bar(kTbPFull + 2 * wg + h));
                     }
-                    fence_proxy_async_shared();
                 }
-                tc_fence_before_sync();
-                mbar_arrive(bar(kTbPFull + wg));
                 ++tiles;
             }
             if (!ok) break;
@@ -891,9 +1009,9 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                 ++ready[0];
                 tc_fence_after_sync();
                 if (warp_live) {
-                    const bool none = l == 0.f || !shown;
+                    const bool none = row.l == 0.f || !shown;
                     const bool hide = __any_sync(0xffffffffu, none);
-                    const float inv = none ? 0.f : 1.f / l;
+                    const float inv = none ? 0.f : 1.f / row.l;
                     const float2 inv2 = make_float2(inv, inv);
                     uint32_t o[16];
                     tmem_ld16(t_o, o);
@@ -910,7 +1028,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                         }
                         out.store(c, x);
                     }
-                    store_lse(none ? -INFINITY : (m_run + lg2_approx(l)) * 0.69314718055994531f);
+                    store_lse(none ? -INFINITY : (row.m + lg2_approx(row.l)) * 0.69314718055994531f);
                 }
             } else {
                 const int jw[2] = {k & 1, (k + 1) & 1};  // first tile of the segment for warpgroups 0 and 1
@@ -919,7 +1037,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                 if (segs > 0) ok = mbar_wait(bar(kTbOFree + wg), static_cast<uint32_t>(segs - 1) & 1, limit, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                ml[wg * kBlockM + r] = make_float2(m_run, l);
+                ml[wg * kBlockM + r] = make_float2(row.m, row.l);
                 mbar_arrive(bar(kTbMLFull));
                 ok = mbar_wait(bar(kTbMLFull), static_cast<uint32_t>(segs) & 1, limit, abort_flag);
                 if (ok && has0) ok = mbar_wait(bar(kTbOReady + 0), ready[0] & 1, limit, abort_flag);
@@ -1133,7 +1251,7 @@ __global__ void __launch_bounds__(256) fa_tree_merge_kernel(const __grid_constan
 template <int D, TreeForm FORM>
 cudaError_t launch_tree_t(const TreeParams& p, cudaStream_t st)
 {
-    using C = TrCfg<D>;
+    using C = TrCfg<D, FORM>;
     auto kern = fa_tree_kernel<D, FORM>;
     static bool configured[64] = {};  // attributes set and registers checked, per device
     int dev = 0;
@@ -1147,7 +1265,7 @@ cudaError_t launch_tree_t(const TreeParams& p, cudaStream_t st)
         e = cudaFuncGetAttributes(&attr, kern);
         if (e != cudaSuccess) return e;
         // a register increase that the launch's pool cannot satisfy would wait forever
-        if (attr.numRegs * kTrThreads < 256 * kTrSoftmaxRegs<D> + 128 * kTrControlRegs<D>)
+        if (attr.numRegs * kTrThreads < 256 * C::kSoftmaxRegs + 128 * C::kControlRegs)
             return cudaErrorLaunchOutOfResources;
         configured[dev] = true;
     }
