@@ -271,13 +271,17 @@ fa_status fa_decode_tree(const void* q, const void* k_cache, const void* v_cache
     p.o_part = static_cast<float*>(workspace);
     const bool pair = rows > fa::kBlockM;
     p.num_ctas = sms < fa::kTreeMaxShares / 2 ? sms : fa::kTreeMaxShares / 2;
-    // Which form (fa_tree_kernel.cuh).  Measured on GB300, 4 query heads per key/value head, 8 nodes, d = 128
-    // (ALT / SOLO, us): 2048 units of at most 400 tokens 114 / 93, 1500 tokens 215 / 211, 4500 tokens
-    // 521 / 540; 1024 units 63 / 54, 114 / 113, 266 / 279; 512 units 37 / 35, 63 / 64, 140 / 148; 128 units
-    // of 1-32K tokens 168 / 177.  d = 64, 1500 tokens: 2048 units 127 / 104.  The lengths are only known on
-    // the device: many units are taken to be short ones (at most 5 % lost), fewer only if none can be long.
+    // Which form (fa_tree_kernel.cuh).  Measured on GB300, 4 query heads per key/value head, 8 nodes (ALT /
+    // SOLO, us).  d = 128, where K and V bound both: 2048 units of at most 400 tokens 113 / 86, 1500 tokens
+    // 213 / 202, 4500 tokens 519 / 531; 512 units 37 / 32, 63 / 61, 139 / 144; 384 units 31 / 28, 51 / 49; 256
+    // units 23 / 22, 37 / 38; 128 units of 16K 123 / 128.  The lengths are only known on the device: many
+    // units are taken to be short ones (at most 4 % lost), fewer only if none can be long.
+    // d = 64, where a tile is less to wait for: 2048 units of 1500 tokens 132 / 103, 4500 278 / 263; 128
+    // units of 1500 18.3 / 16.4, 16K 67.6 / 66.3 (32 nodes 71.2 / 72.2); 64 units 14.0 / 13.4, but with 32
+    // nodes 16.5 / 18.1; 32 units 12.2 / 12.8.  d = 32, 128 units of 16K: 61 / 53; 32 units 11.1 / 12.1.
     const long long units = groups * n_qp;
-    const bool solo = !pair && (units >= 6LL * p.num_ctas || (units >= 3LL * p.num_ctas && Nk_max <= 1536));
+    const bool solo = !pair && (d < 128 ? 4 * units >= 3LL * p.num_ctas
+                                        : units >= 6LL * p.num_ctas || (units >= 2LL * p.num_ctas && Nk_max <= 1536));
     p.num_shares = solo ? 2 * p.num_ctas : p.num_ctas;
     // a unit's start and end took a CTA about three tiles' time (one share's last units of 9 tiles each: the
     // CTA ended 30 us after the others without it), two under the other warpgroup's tiles
