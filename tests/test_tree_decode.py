@@ -115,6 +115,46 @@ def test_many_units(d, R, T):
     check_tree(*call(q, k, v, lens, par, cnt), ref, "bf16")
 
 
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("R,T", [(4, 40), (2, 128), (5, 60), (3, 100)])
+def test_many_units_of_more_rows(d, R, T):
+    """More than 128 rows (one block whose second half is short or full, or a second block of 44 rows), enough
+    units that a CTA walks several: growing and falling maxima across tiles, empty and absent ones among them."""
+    B, Hkv, hi = 90, 2, 500
+    g = torch.Generator().manual_seed(d + T)
+    lens = torch.randint(0, hi + 1, (B,), generator=g).to(torch.int32)
+    lens[5], lens[6], lens[7] = 0, 1500, 127
+    cnt = torch.randint(0, T + 1, (B,), generator=g).to(torch.int32)
+    q, k, v = inputs(B, Hkv * R, Hkv, T, 1500 + T, d, lens, cnt, seed=T)
+    k[6, :, :1500] *= torch.linspace(0.1, 8, 1500)[None, :, None].to(BF16)
+    par = random_parents(B, T, seed=d)
+    ref = tree_attention(q, k, v, lens, par, cnt, 1 / math.sqrt(d))
+    o, lse = call(q, k, v, lens, par, cnt, out_dtype=torch.float32)
+    o2, lse2 = call(q, k, v, lens, par, cnt, out_dtype=torch.float32)
+    assert fa().get_device_error() == 0
+    check_tree(o, lse, ref, f"d={d} R={R} T={T}")
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,R,T", [(3, 4, 8), (300, 4, 8), (20, 4, 64)])
+def test_wait_limit_is_reported_and_the_next_call_is_right(B, R, T, d):
+    """With a limit of 1 ns waits run out in each form of the kernel: the status says so, every role ends, and
+    the next call with the usual limit is right."""
+    lens = torch.full((B,), 300, dtype=torch.int32)
+    q, k, v = inputs(B, 2 * R, 2, T, 400, d, lens, seed=3)
+    fa().set_wait_timeout_ns(1)
+    try:
+        call(q, k, v, lens)
+        status = fa().get_device_error()
+    finally:
+        fa().set_wait_timeout_ns(0)
+    assert status == fa().FA_ERR_TIMEOUT
+    o, lse = call(q, k, v, lens, out_dtype=torch.float32)
+    assert fa().get_device_error() == 0
+    check_tree(o, lse, tree_attention(q, k, v, lens, None, None, 1 / math.sqrt(d)), "after")
+
+
 @pytest.mark.parametrize("d,T,R", [(128, 9, 4), (64, 60, 3)])
 def test_chain_and_shallow_trees(d, T, R):
     """No parents: a chain, the same as parents t - 1.  All nodes children of the last token: each sees itself only."""
