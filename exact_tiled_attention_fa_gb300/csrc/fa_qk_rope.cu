@@ -673,7 +673,7 @@ __global__ void __launch_bounds__(1024) fa_rope_weight_kernel(const float* part,
     const int slice = threadIdx.x >> 5;
     float s = 0.f;
 #pragma unroll 8
-    for (int c = slice; c < n; c += 32) s += __ldg(part + (static_cast<size_t>(c) * 2 + blockIdx.y) * d + col);
+    for (int c = slice; c < n; c += 32) s += __ldcg(part + (static_cast<size_t>(c) * 2 + blockIdx.y) * d + col);
     sm[slice][threadIdx.x & 31] = s;
     __syncthreads();
     if (slice == 0) {

@@ -1155,12 +1155,12 @@ __global__ void __launch_bounds__(256) fa_tree_merge_kernel(const __grid_constan
                 if (s0 + j >= n) continue;
                 const float4* src = reinterpret_cast<const float4*>(p.o_part + at(s0 + j, r) * D) + l8;
 #pragma unroll
-                for (int i = 0; i < Q; ++i) v[j][i] = __ldg(src + 8 * i);
+                for (int i = 0; i < Q; ++i) v[j][i] = __ldcg(src + 8 * i);
             }
         };
         float x[kFew];
 #pragma unroll
-        for (int s = 0; s < kFew; ++s) x[s] = s < n ? __ldg(p.lse_part + at(s, r)) : -INFINITY;
+        for (int s = 0; s < kFew; ++s) x[s] = s < n ? __ldcg(p.lse_part + at(s, r)) : -INFINITY;
         load(0);  // with the log-sum-exps
         float M = -INFINITY;
         bool live = false;
@@ -1209,7 +1209,7 @@ __global__ void __launch_bounds__(256) fa_tree_merge_kernel(const __grid_constan
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
         const int s = 32 * i + lane;
-        x[i] = s < n ? __ldg(p.lse_part + at(s, r)) : -INFINITY;
+        x[i] = s < n ? __ldcg(p.lse_part + at(s, r)) : -INFINITY;
         live = live || x[i] != -INFINITY;
         M = fmaxf(M, x[i]);
     }
@@ -1236,9 +1236,9 @@ __global__ void __launch_bounds__(256) fa_tree_merge_kernel(const __grid_constan
             const float f = __shfl_sync(0xffffffffu, x[i], j) * inv;
             const float* src = p.o_part + at(32 * i + j, r) * D + lane * V;
             float v[V];
-            if constexpr (V == 4) *reinterpret_cast<float4*>(v) = __ldg(reinterpret_cast<const float4*>(src));
-            else if constexpr (V == 2) *reinterpret_cast<float2*>(v) = __ldg(reinterpret_cast<const float2*>(src));
-            else v[0] = __ldg(src);
+            if constexpr (V == 4) *reinterpret_cast<float4*>(v) = __ldcg(reinterpret_cast<const float4*>(src));
+            else if constexpr (V == 2) *reinterpret_cast<float2*>(v) = __ldcg(reinterpret_cast<const float2*>(src));
+            else v[0] = __ldcg(src);
 #pragma unroll
             for (int e = 0; e < V; ++e) acc[e] = fmaf(f, v[e], acc[e]);
         }
