@@ -404,20 +404,26 @@ cudaError_t launch_rope_t(const RopeParams& p, bool append, int sms, cudaStream_
 
 // Two CTAs for each SM; a warp walks its tokens, of each the query, key and value heads, in batches of U
 // row sets (RPW heads' rows, or RPW heads' copies of one number).  Batches go through a ring of kStages
-// in shared memory, filled by asynchronous copies two batches ahead (a token's angles too), so that the
-// bytes in flight do not depend on registers.  Measured with bf16 gradients on B=64 N=1024 H=16 d=64: 192 us a
-// call, of which this kernel moves its 1.07 GB in 170 (6.3 TB/s); with the rows loaded into registers it
-// was bound by latency whatever the split (four rows in flight, 16 warps an SM 214 us; two rows, 24 warps
-// 227).  fp32 gradients of 4 copies, B=2 N=4097 32/8 heads d=128: 113 us, 6.1 TB/s.  The weights' gradients stay in registers (a lane's eight columns of
-// each) until the CTA adds its warps' up in a fixed order and writes one partial row of each, which
-// fa_rope_weight_kernel adds up, also in a fixed order: the result does not change from run to run.
-constexpr int kBwdStages = 3;
-template <bool GF32>
+// in shared memory, filled by asynchronous copies kStages - 1 batches ahead (a token's angles too), so that
+// the bytes in flight do not depend on registers.  Measured with bf16 gradients on B=64 N=1024 H=16 d=64:
+// 165 us a call, 6.5 TB/s; with the rows loaded into registers it was bound by latency whatever the split
+// (four rows in flight, 16 warps an SM 214 us; two rows, 24 warps 227).  fp32 gradients of 4 copies,
+// B=2 N=4097 32/8 heads d=128: 112 us, 6.2 TB/s.  The weights' gradients stay in registers (a lane's
+// eight columns of each) until the CTA adds its warps' up in a fixed order and writes one partial row of
+// each, which fa_rope_weight_kernel adds up, also in a fixed order: the result does not change from run
+// to run.
+// Batches: 64 to 96 KB in flight an SM do best; three stages of four sets (128 KB) took 193 us on the first
+// case, two of two 172.  In share of the copy's rate, two stages of four sets / three of two, bf16
+// gradients: d = 64 16 heads 94 / 93 %, 12 heads 91 / 82, 25 heads 89 / 80, 8 heads 77 / 88; d = 128 32
+// heads 87 / 94, 32/8 90 / 90; d = 32 16 heads 78 / 90, 12 heads 61 / 67.  (Three CTAs an SM spill: 250 us.)
+template <int D, bool GF32, bool MULTI>
 struct RopeBwdCfg {
-    static constexpr int U = GF32 ? 2 : 4;
-    static constexpr int kSet = GF32 ? 1536 : 1024;          // a row set: x (512 bytes), then the gradient's
-    static constexpr int kAngles = U * kSet * kBwdStages;    // cosines (256 bytes) and sines of a token, a ring too
-    static constexpr int kWarp = kAngles + 512 * kBwdStages; // bytes of a warp
+    static constexpr bool kThin = !GF32 && !MULTI && D != 64;
+    static constexpr int kStages = kThin ? 3 : 2;
+    static constexpr int U = kThin ? 2 : 4;
+    static constexpr int kSet = GF32 ? 1536 : 1024;        // a row set: x (512 bytes), then the gradient's
+    static constexpr int kAngles = U * kSet * kStages;     // cosines (256 bytes) and sines of a token, a ring too
+    static constexpr int kWarp = kAngles + 512 * kStages;  // bytes of a warp
     static constexpr int kSmem = kRopeWarps * kWarp;
 };
 
@@ -427,7 +433,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 2) fa_qk_rope_bwd_kernel(cons
 {
     grid_dependency_wait();
     grid_launch_dependents();
-    using C = RopeBwdCfg<GF32>;
+    using C = RopeBwdCfg<D, GF32, MULTI>;
     using G = typename std::conditional<GF32, float, __nv_bfloat16>::type;
     using bf16 = __nv_bfloat16;
     constexpr int LPR = D / 8;
@@ -482,6 +488,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 2) fa_qk_rope_bwd_kernel(cons
     int token_slot = 0;                                          // of its angles
     const int half = p.rot >> 1;
 
+    const G* copy_row = nullptr;  // MULTI: of the row set being copied
     size_t token_b = 0, token_t = 0;  // sequence of the token being copied, and its elements into a head
     // The copies of one batch into a stage: at most U row sets of one kind.
     auto copy_batch = [&](int stage) {
@@ -495,7 +502,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 2) fa_qk_rope_bwd_kernel(cons
                 if (4 * piece < half)
                     cp_async16(ring + C::kAngles + token_slot * 512 + (lane >> 4) * 256 + piece * 16,
                                (lane < 16 ? p.cos_t : p.sin_t) + i + 4 * piece, 16);
-                token_slot = token_slot == kBwdStages - 1 ? 0 : token_slot + 1;
+                token_slot = token_slot == C::kStages - 1 ? 0 : token_slot + 1;
                 if (ahead.token + stride < tokens) pos = position(ahead.token + stride);
             }
             const int heads = kind == 0 ? p.Hq : p.Hkv;
@@ -516,13 +523,16 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 2) fa_qk_rope_bwd_kernel(cons
                     cp_async16(to + u * C::kSet + 512 + lane * 16, row + sub * 8, bytes);
                 }
             };
-            if constexpr (MULTI) {
+            if (MULTI && kind > 0) {  // (step, copy) in order; a head's copies lie behind one another
+                if (ahead.step == 0 && ahead.copy == 0) copy_row = g + (grp < heads ? grp * each : 0);
                 bool end = false;
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    if (end) continue;
+                    if (end) continue;  // uniform
                     const int h = ahead.step * RPW + grp;
-                    copy_set(u, x + ahead.step * 256, g + (h < heads ? h : 0) * each + ahead.copy * head, h);
+                    copy_set(u, x + ahead.step * 256, h < heads ? copy_row : g, h);
+                    copy_row += head;
+                    if (ahead.copy == copies - 1) copy_row += (RPW - 1) * each;
                     end = advance(ahead, 1);
                 }
             } else {
@@ -542,7 +552,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 2) fa_qk_rope_bwd_kernel(cons
         }
         cp_async_commit();
     };
-    for (int i = 0; i < kBwdStages - 1; ++i) copy_batch(i);
+    for (int i = 0; i < C::kStages - 1; ++i) copy_batch(i);
 
     Pairs cs, g;
     uint4 xr = make_uint4(0, 0, 0, 0);
@@ -571,13 +581,13 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 2) fa_qk_rope_bwd_kernel(cons
     };
     int stage = 0;
     while (at.token < tokens) {
-        copy_batch(stage == 0 ? kBwdStages - 1 : stage - 1);
-        cp_async_wait<kBwdStages - 1>();
+        copy_batch(stage == 0 ? C::kStages - 1 : stage - 1);
+        cp_async_wait<C::kStages - 1>();
         __syncwarp();
         const int kind = at.kind;
         if (kind == 0 && at.step == 0) {
             cs = share.angles_at(reinterpret_cast<const float*>(mine + C::kAngles + cs_slot * 512));
-            cs_slot = cs_slot == kBwdStages - 1 ? 0 : cs_slot + 1;
+            cs_slot = cs_slot == C::kStages - 1 ? 0 : cs_slot + 1;
         }
         const uint8_t* from = mine + stage * (U * C::kSet) + grp * (D * 2);
         char* out = static_cast<char*>(kind == 0 ? p.gq : kind == 1 ? p.gk : p.gv);
@@ -598,7 +608,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 2) fa_qk_rope_bwd_kernel(cons
                 else share.store(reinterpret_cast<bf16*>(out) + row + h * D, share.pack(g));
             }
         };
-        if constexpr (MULTI) {
+        if (MULTI && kind > 0) {
             bool end = false;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -606,14 +616,13 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 2) fa_qk_rope_bwd_kernel(cons
                 const Pairs y = gradient(u);
                 if (at.copy == 0) {
                     g = y;
-                    if (kind < 2) xr = share.read(reinterpret_cast<const bf16*>(from + u * C::kSet));
+                    if (kind == 1) xr = share.read(reinterpret_cast<const bf16*>(from + u * C::kSet));
                 } else {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) g.x[e] = __fadd2_rn(g.x[e], y.x[e]);
                 }
-                if (kind == 0 || at.copy == copies - 1) {
-                    if (kind == 0) finish(wq, aq);
-                    else if (kind == 1) finish(wk, ak);
+                if (at.copy == copies - 1) {
+                    if (kind == 1) finish(wk, ak);
                     write(at.step);
                 }
                 end = advance(at, 1);
@@ -632,12 +641,12 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 2) fa_qk_rope_bwd_kernel(cons
             };
             auto read_x = [&](int u) { xr = share.read(reinterpret_cast<const bf16*>(from + u * C::kSet)); };
             if (kind == 0) sets([&](int u) { read_x(u), finish(wq, aq); });
-            else if (kind == 1) sets([&](int u) { read_x(u), finish(wk, ak); });
+            else if (kind == 1) sets([&](int u) { read_x(u), finish(wk, ak); });  // (not MULTI)
             else sets([](int) {});
             advance(at, U);
         }
         __syncwarp();  // the stage may be filled again
-        stage = stage == kBwdStages - 1 ? 0 : stage + 1;
+        stage = stage == C::kStages - 1 ? 0 : stage + 1;
     }
     __syncthreads();  // (no copy is in flight: the batches ahead of the last were empty)
     float(*sm)[2][D] = reinterpret_cast<float(*)[2][D]>(rb_smem);
@@ -694,11 +703,11 @@ cudaError_t launch_rope_bwd_g(const RopeBwdParams& p, int grid, cudaStream_t st)
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!configured[dev]) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, RopeBwdCfg<GF32>::kSmem);
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, RopeBwdCfg<D, GF32, MULTI>::kSmem);
         if (e != cudaSuccess) return e;
         configured[dev] = true;
     }
-    return launch_pdl(kern, static_cast<unsigned>(grid), kRopeWarps * 32, RopeBwdCfg<GF32>::kSmem, st, p);
+    return launch_pdl(kern, static_cast<unsigned>(grid), kRopeWarps * 32, RopeBwdCfg<D, GF32, MULTI>::kSmem, st, p);
 }
 
 template <int D, bool INTERLEAVED>
