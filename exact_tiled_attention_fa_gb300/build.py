@@ -88,7 +88,7 @@ def build(force=False, verbose=False, extra_flags=()):
     tmp = BINDING + f".tmp{os.getpid()}"
     libs = os.path.join(torch_dir, "lib")
     cmd = [cxx, "-shared", "-o", tmp, binding_obj, "-L", HERE, "-l:libfa.so", "-Wl,-rpath,$ORIGIN", "-L", libs,
-           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
