@@ -260,7 +260,7 @@ struct Steps {
 };
 
 // Grid (tokens / kRopeWarps, step chunks).  A warp: one token, steps blockIdx.y * chunk .. + chunk.
-// Four rows in flight and four CTAs an SM (64 registers): B=64 N=1024 H=16 d=64 126 us, 6.4 TB/s of
+// Four rows in flight and four CTAs an SM (64 registers): B=64 N=1024 H=16 d=64 123 us, 6.6 TB/s of
 // reads and writes; three CTAs 136, two with eight rows 168, five (48 registers, which spill) 145.  Rows
 // through a ring of asynchronous copies, as in the backward kernel: 128 us there, 6-10 % slower at d = 128.
 // APPEND: token t of sequence b is node t of its tree, at position seqlens[b] + depth, and its key
@@ -278,10 +278,11 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) fa_qk_rope_kernel(const Ro
     const int lane = threadIdx.x & 31;
     const int sub = lane % LPR;
     const int grp = lane / LPR;
-    const long long token = static_cast<long long>(blockIdx.x) * kRopeWarps + (threadIdx.x >> 5);
-    if (token >= static_cast<long long>(p.B) * p.N) return;
-    const int b = static_cast<int>(token / p.N);
-    const int t = static_cast<int>(token - static_cast<long long>(b) * p.N);
+    // (tokens are below 2^31: a 64-bit division here was a tenth of a small token's instructions)
+    const unsigned token = blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
+    if (token >= static_cast<unsigned>(p.B) * static_cast<unsigned>(p.N)) return;
+    const unsigned b = token / static_cast<unsigned>(p.N);
+    const int t = static_cast<int>(token - b * static_cast<unsigned>(p.N));
     const Share<INTERLEAVED> share(sub, p.rot);
     const Steps<RPW> steps(p.Hq, p.Hkv, p.v != nullptr);
     const int begin = static_cast<int>(blockIdx.y) * chunk;
@@ -297,7 +298,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) fa_qk_rope_kernel(const Ro
     };
     // The first rows are on their way while the position is found.
     uint4 raw[U];
-    const bf16* q = reinterpret_cast<const bf16*>(p.q) + token * p.q_stride;
+    const bf16* q = reinterpret_cast<const bf16*>(p.q) + static_cast<long long>(token) * p.q_stride;
     if (begin < steps.nq) load(raw, q, begin, min(end, steps.nq), p.Hq);
 
     bool live = true;  // APPEND: the node is part of the tree
@@ -353,13 +354,16 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) fa_qk_rope_kernel(const Ro
     const size_t at = static_cast<size_t>(b) * p.Hkv * head + static_cast<size_t>(row) * D;
     auto store = [&](bf16* out, int i, uint4 y) {
         const int h = i * RPW + grp;
-        if (h < p.Hkv)
-            for (int c = 0; c < p.copies; ++c) share.store(out + h * head + static_cast<size_t>(c) * kv_rows * D, y);
+        if (h < p.Hkv) {
+            bf16* to = out + h * head;
+            share.store(to, y);
+            for (int c = 1; c < p.copies; ++c) share.store(to + static_cast<size_t>(c) * kv_rows * D, y);
+        }
     };
     const int kb = max(begin, steps.nq) - steps.nq, ke = min(end, steps.nq + steps.nk) - steps.nq;
     if (kb < ke) {
         const Turn turn(share.weights(p.wk, p.w_dtype), cs);
-        const bf16* k = reinterpret_cast<const bf16*>(p.k) + token * p.k_stride;
+        const bf16* k = reinterpret_cast<const bf16*>(p.k) + static_cast<long long>(token) * p.k_stride;
         bf16* out = reinterpret_cast<bf16*>(p.k_out) + at;
         for (int i = kb; i < ke; i += U) {
             load(raw, k, i, ke, p.Hkv);
@@ -372,13 +376,23 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) fa_qk_rope_kernel(const Ro
     }
     const int vb = max(begin, steps.nq + steps.nk) - steps.nq - steps.nk, ve = end - steps.nq - steps.nk;
     if (vb < ve) {
-        const bf16* v = reinterpret_cast<const bf16*>(p.v) + token * p.v_stride;
+        const bf16* v = reinterpret_cast<const bf16*>(p.v) + static_cast<long long>(token) * p.v_stride;
         bf16* out = reinterpret_cast<bf16*>(p.v_out) + at;
         for (int i = vb; i < ve; i += U) {
-            load(raw, v, i, ve, p.Hkv);
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (i + u < ve) store(out, i + u, raw[u]);
+            for (int u = 0; u < U; ++u) {
+                const int h = (i + u) * RPW + grp;
+                raw[u] = i + u < ve && h < p.Hkv ? ld_stream_v4(v + h * D + sub * 8) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (i + u >= ve) break;
+                const int h = (i + u) * RPW + grp;
+                if (h < p.Hkv) {
+                    bf16* to = out + h * head + sub * 8;
+                    for (int c = 0; c < p.copies; ++c, to += kv_rows * D) *reinterpret_cast<uint4*>(to) = raw[u];
+                }
+            }
         }
     }
 }
