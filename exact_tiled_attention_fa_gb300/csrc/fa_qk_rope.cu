@@ -274,6 +274,11 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) fa_qk_rope_kernel(const Ro
     constexpr int LPR = D / 8;    // lanes of a row
     constexpr int RPW = 32 / LPR; // rows of a warp's step
     constexpr int U = 4;          // steps in flight
+    // Whether the first values are copied while the position and the angles are on their way: with the
+    // smaller heads a token has few steps to hide that under (share of the copy's rate with and without,
+    // d = 64: 12 heads 91 / 87 %, 8 heads 81 / 77, 16 heads 96 / 96; d = 32 16 heads 80 / 77; d = 128, where
+    // the registers are short: 32/8 heads 93 / 95).  Nodes that are not there are not read.
+    constexpr bool EARLY = D < 128 && !APPEND;
     using bf16 = __nv_bfloat16;
     const int lane = threadIdx.x & 31;
     const int sub = lane % LPR;
@@ -296,8 +301,19 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) fa_qk_rope_kernel(const Ro
             raw[u] = i + u < to && h < heads ? share.load(rows + h * D) : make_uint4(0, 0, 0, 0);
         }
     };
+    // Values pass through: 16 bytes a lane.
+    const int vb = max(begin, steps.nq + steps.nk) - steps.nq - steps.nk, ve = end - steps.nq - steps.nk;
+    const bf16* v = reinterpret_cast<const bf16*>(p.v) + static_cast<long long>(token) * p.v_stride + sub * 8;
+    auto load_v = [&](uint4 (&x)[U], int i) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int h = (i + u) * RPW + grp;
+            x[u] = i + u < ve && h < p.Hkv ? ld_stream_v4(v + h * D) : make_uint4(0, 0, 0, 0);
+        }
+    };
     // The first rows are on their way while the position is found.
-    uint4 raw[U];
+    uint4 raw[U], first_v[U];
+    if (EARLY && vb < ve) load_v(first_v, vb);
     const bf16* q = reinterpret_cast<const bf16*>(p.q) + static_cast<long long>(token) * p.q_stride;
     if (begin < steps.nq) load(raw, q, begin, min(end, steps.nq), p.Hq);
 
@@ -328,7 +344,23 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) fa_qk_rope_kernel(const Ro
                 *reinterpret_cast<uint4*>(out + static_cast<size_t>(i * RPW + grp) * p.N * D + sub * 8) = make_uint4(0, 0, 0, 0);
         return;
     }
+    const size_t kv_rows = APPEND ? p.Nk_max : p.N;
+    const size_t head = static_cast<size_t>(p.copies) * kv_rows * D;
+    const size_t at = static_cast<size_t>(b) * p.Hkv * head + static_cast<size_t>(row) * D;
+    auto store_v = [&](const uint4 (&x)[U], int i) {
+        bf16* out = reinterpret_cast<bf16*>(p.v_out) + at + sub * 8;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (i + u >= ve) break;  // uniform
+            const int h = (i + u) * RPW + grp;
+            if (h < p.Hkv) {
+                bf16* to = out + h * head;
+                for (int c = 0; c < p.copies; ++c, to += kv_rows * D) *reinterpret_cast<uint4*>(to) = x[u];
+            }
+        }
+    };
     const Pairs cs = share.angles(p.cos_t, p.sin_t, pos, p.rot);
+    if (EARLY && vb < ve) store_v(first_v, vb);
     auto turned = [&](const Turn& turn, uint4 u) -> uint4 {
         const Pairs x = share.unpack(u);
         return share.pack(turn.apply(x, rsqrtf(row_sum<LPR>(dot(x, x)) * (1.f / D) + p.eps)));
@@ -336,7 +368,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) fa_qk_rope_kernel(const Ro
     if (begin < steps.nq) {
         const Turn turn(share.weights(p.wq, p.w_dtype), cs);
         bf16* out = reinterpret_cast<bf16*>(p.q_out) + (static_cast<size_t>(b) * p.Hq * p.N + t) * D;
-        const size_t head = static_cast<size_t>(p.N) * D;
+        const size_t q_head = static_cast<size_t>(p.N) * D;
         const int to = min(end, steps.nq);
         for (int i = begin; i < to; i += U) {
             if (i != begin) load(raw, q, i, to, p.Hq);
@@ -345,13 +377,10 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) fa_qk_rope_kernel(const Ro
                 if (i + u >= to) break;  // uniform
                 const uint4 y = turned(turn, raw[u]);
                 const int h = (i + u) * RPW + grp;
-                if (h < p.Hq) share.store(out + h * head, y);
+                if (h < p.Hq) share.store(out + h * q_head, y);
             }
         }
     }
-    const size_t kv_rows = APPEND ? p.Nk_max : p.N;
-    const size_t head = static_cast<size_t>(p.copies) * kv_rows * D;
-    const size_t at = static_cast<size_t>(b) * p.Hkv * head + static_cast<size_t>(row) * D;
     auto store = [&](bf16* out, int i, uint4 y) {
         const int h = i * RPW + grp;
         if (h < p.Hkv) {
@@ -374,26 +403,9 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) fa_qk_rope_kernel(const Ro
             }
         }
     }
-    const int vb = max(begin, steps.nq + steps.nk) - steps.nq - steps.nk, ve = end - steps.nq - steps.nk;
-    if (vb < ve) {
-        const bf16* v = reinterpret_cast<const bf16*>(p.v) + static_cast<long long>(token) * p.v_stride;
-        bf16* out = reinterpret_cast<bf16*>(p.v_out) + at;
-        for (int i = vb; i < ve; i += U) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int h = (i + u) * RPW + grp;
-                raw[u] = i + u < ve && h < p.Hkv ? ld_stream_v4(v + h * D + sub * 8) : make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (i + u >= ve) break;
-                const int h = (i + u) * RPW + grp;
-                if (h < p.Hkv) {
-                    bf16* to = out + h * head + sub * 8;
-                    for (int c = 0; c < p.copies; ++c, to += kv_rows * D) *reinterpret_cast<uint4*>(to) = raw[u];
-                }
-            }
-        }
+    for (int i = EARLY ? vb + U : vb; i < ve; i += U) {
+        load_v(raw, i);
+        store_v(raw, i);
     }
 }
 
