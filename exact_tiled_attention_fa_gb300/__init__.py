@@ -554,7 +554,9 @@ def decode_tree(q, k_cache, v_cache, seqlens, parents=None, n_nodes=None, scale=
     cache rows seqlens .. seqlens + n_nodes - 1: each sees the cached tokens, itself and its ancestors.
 
     q [B,Hq,T,d] bf16, caches [B,Hkv,Nk_max,d] bf16 with Hkv dividing Hq, seqlens int32 [B] (without the tree),
-    parents and n_nodes as for ``qk_norm_rope_append``.  ``workspace`` is a uint8 CUDA tensor of at least
+    parents and n_nodes as for ``qk_norm_rope_append``.  Cache rows behind the tree may hold anything; a
+    non-finite key reaches only the tokens that see it, a non-finite value of a drafted token may reach the
+    whole sequence's.  ``workspace`` is a uint8 CUDA tensor of at least
     ``decode_tree_workspace_size`` bytes (allocated here when omitted).  Returns (O [B,Hq,T,d], LSE fp32
     [B,Hq,T] or None); O = 0 and LSE = -inf for tokens that are not there.
     """
