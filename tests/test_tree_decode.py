@@ -155,6 +155,21 @@ def test_wait_limit_is_reported_and_the_next_call_is_right(B, R, T, d):
     check_tree(o, lse, tree_attention(q, k, v, lens, None, None, 1 / math.sqrt(d)), "after")
 
 
+@pytest.mark.parametrize("B,R,T,Nk,d,hi", [(1, 300, 128, 700, 64, 500), (5000, 2, 2, 8, 32, 3), (600, 3, 100, 110, 128, 5),
+                                           (3, 130, 1, 900, 128, 800), (2, 128, 1, 900, 128, 800), (152, 1, 1, 130, 128, 129)])
+def test_many_rows_and_many_sequences(B, R, T, Nk, d, hi):
+    """Far more rows than two blocks', thousands of sequences of a few tokens, a row more or less than a block."""
+    g = torch.Generator().manual_seed(B + T)
+    lens = torch.randint(0, hi + 1, (B,), generator=g).to(torch.int32)
+    cnt = torch.randint(0, T + 1, (B,), generator=g).to(torch.int32)
+    cnt[0] = T
+    q, k, v = inputs(B, R, 1, T, Nk, d, lens, cnt, seed=1)
+    par = random_parents(B, T, seed=2)
+    o, lse = call(q, k, v, lens, par, cnt, out_dtype=torch.float32)
+    assert fa().get_device_error() == 0
+    check_tree(o, lse, tree_attention(q, k, v, lens, par, cnt, 1 / math.sqrt(d)), f"B={B} R={R} T={T}")
+
+
 @pytest.mark.parametrize("d,T,R", [(128, 9, 4), (64, 60, 3)])
 def test_chain_and_shallow_trees(d, T, R):
     """No parents: a chain, the same as parents t - 1.  All nodes children of the last token: each sees itself only."""
