@@ -583,8 +583,9 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 2) fa_qk_rope_bwd_kernel(cons
     Pairs cs, g;
     uint4 xr = make_uint4(0, 0, 0, 0);
     int cs_slot = 0;
-    // one row: its gradient g to the projection's
-    auto finish = [&](const Pairs& w, Pairs& acc) {
+    // one row: its gradient g to the projection's.  A lane without a row (not `live`) has zeros, whose
+    // norm is infinite at eps = 0: it takes r = 0, so that it adds 0 to acc.
+    auto finish = [&](const Pairs& w, Pairs& acc, bool live) {
         const Pairs x = share.unpack(xr);
         Pairs hb, z;  // the gradient turned back, and times the weights
 #pragma unroll
@@ -596,12 +597,12 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 2) fa_qk_rope_bwd_kernel(cons
         for (int e = 0; e < 4; ++e) z.x[e] = mul2(w.x[e], hb.x[e]);
         const float ss = row_sum<LPR>(dot(x, x));
         const float sz = row_sum<LPR>(dot(x, z));
-        const float r = rsqrtf(ss * (1.f / D) + p.eps);
+        const float r = live ? rsqrtf(ss * (1.f / D) + p.eps) : 0.f;
         const float f = -(r * r) * sz * (1.f / D);
         const float2 rr = make_float2(r, r), ff = make_float2(f, f);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            acc.x[e] = fma2(hb.x[e], mul2(x.x[e], rr), acc.x[e]);  // 0 for lanes without a row
+            acc.x[e] = fma2(hb.x[e], mul2(x.x[e], rr), acc.x[e]);
             g.x[e] = mul2(rr, fma2(x.x[e], ff, z.x[e]));
         }
     };
@@ -648,7 +649,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 2) fa_qk_rope_bwd_kernel(cons
                     for (int e = 0; e < 4; ++e) g.x[e] = __fadd2_rn(g.x[e], y.x[e]);
                 }
                 if (at.copy == copies - 1) {
-                    if (kind == 1) finish(wk, ak);
+                    if (kind == 1) finish(wk, ak, at.step * RPW + grp < heads);
                     write(at.step);
                 }
                 end = advance(at, 1);
@@ -666,8 +667,9 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 2) fa_qk_rope_bwd_kernel(cons
                 }
             };
             auto read_x = [&](int u) { xr = share.read(reinterpret_cast<const bf16*>(from + u * C::kSet)); };
-            if (kind == 0) sets([&](int u) { read_x(u), finish(wq, aq); });
-            else if (kind == 1) sets([&](int u) { read_x(u), finish(wk, ak); });  // (not MULTI)
+            auto live = [&](int u) { return (at.step + u) * RPW + grp < heads; };
+            if (kind == 0) sets([&](int u) { read_x(u), finish(wq, aq, live(u)); });
+            else if (kind == 1) sets([&](int u) { read_x(u), finish(wk, ak, live(u)); });  // (not MULTI)
             else sets([](int) {});
             advance(at, U);
         }
