@@ -176,7 +176,8 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 __device__ __forceinline__ float2 neg2(float2 a) { return make_float2(-a.x, -a.y); }
 
-// Norm weights and rotation of a lane in one: a' = r (a aa + b ab), b' = r (a ba + b bb).
+// Norm weights and rotation of a lane in one: a' = (r a) aa + (r b) ab, b' = (r a) ba + (r b) bb.  (r first:
+// where the sum of squares overflows r is 0, and the row times its weights may be past fp32.)
 struct Turn {
     float2 aa[2], ab[2], ba[2], bb[2];
     __device__ __forceinline__ Turn(const Pairs& w, const Pairs& cs)
@@ -195,8 +196,9 @@ struct Turn {
         Pairs o;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            o.x[i] = mul2(rr, fma2(p.x[i], aa[i], mul2(p.x[2 + i], ab[i])));
-            o.x[2 + i] = mul2(rr, fma2(p.x[i], ba[i], mul2(p.x[2 + i], bb[i])));
+            const float2 a = mul2(rr, p.x[i]), b = mul2(rr, p.x[2 + i]);
+            o.x[i] = fma2(a, aa[i], mul2(b, ab[i]));
+            o.x[2 + i] = fma2(a, ba[i], mul2(b, bb[i]));
         }
         return o;
     }
@@ -598,7 +600,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 2) fa_qk_rope_bwd_kernel(cons
         const float ss = row_sum<LPR>(dot(x, x));
         const float sz = row_sum<LPR>(dot(x, z));
         const float r = live ? rsqrtf(ss * (1.f / D) + p.eps) : 0.f;
-        const float f = -(r * r) * sz * (1.f / D);
+        const float f = r == 0.f ? 0.f : -(r * r) * sz * (1.f / D);  // (then sz may have overflowed too)
         const float2 rr = make_float2(r, r), ff = make_float2(f, f);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
