@@ -313,15 +313,17 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) fa_qk_rope_kernel(const Ro
             x[u] = i + u < ve && h < p.Hkv ? ld_stream_v4(v + h * D) : make_uint4(0, 0, 0, 0);
         }
     };
-    // The first rows are on their way while the position is found.
-    uint4 raw[U], first_v[U];
-    if (EARLY && vb < ve) load_v(first_v, vb);
+    // The first rows are on their way while the position is found.  Nodes that are not there are not read:
+    // where there may be some, whether this one is comes first.
     const bf16* q = reinterpret_cast<const bf16*>(p.q) + static_cast<long long>(token) * p.q_stride;
-    if (begin < steps.nq) load(raw, q, begin, min(end, steps.nq), p.Hq);
-
-    bool live = true;  // APPEND: the node is part of the tree
-    int row = t;       // row of the key and value in their head
-    int pos;
+    uint4 raw[U], first_v[U];
+    auto first_rows = [&] {
+        if (EARLY && vb < ve) load_v(first_v, vb);
+        if (begin < steps.nq) load(raw, q, begin, min(end, steps.nq), p.Hq);
+    };
+    const bool ragged = APPEND && p.n_nodes != nullptr;
+    if (!ragged) first_rows();
+    int row = t;  // row of the key and value in their head
     if constexpr (APPEND) {
         const int len = p.seqlens[b];
         const int nodes = p.n_nodes != nullptr ? p.n_nodes[b] : p.N;
@@ -329,23 +331,22 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) fa_qk_rope_kernel(const Ro
         const int from = min(max(len, 0), p.Nk_max);
         const int n = min(min(max(nodes, 0), p.N), p.Nk_max - from);
         if (bad && lane == 0) atomicCAS(p.status, 0, FA_ERR_INVALID_ARG);
-        live = t < n;
-        row = from + t;
-        pos = 0;
-        if (live) {
-            pos = from + (p.parents != nullptr ? tree_depth(p.parents + static_cast<size_t>(b) * p.N, t, lane, p.status) : t);
-            pos = checked_position(pos, p.max_pos, p.status);
+        if (t >= n) {  // the whole warp: zero query rows, nothing else
+            bf16* out = reinterpret_cast<bf16*>(p.q_out) + (static_cast<size_t>(b) * p.Hq * p.N + t) * D;
+            for (int i = begin; i < min(end, steps.nq); ++i)
+                if (i * RPW + grp < p.Hq)
+                    *reinterpret_cast<uint4*>(out + static_cast<size_t>(i * RPW + grp) * p.N * D + sub * 8) = make_uint4(0, 0, 0, 0);
+            return;
         }
-    } else {
-        pos = checked_position(p.positions != nullptr ? p.positions[token] : t, p.max_pos, p.status);
+        row = from + t;
     }
-    if (APPEND && !live) {  // the whole warp: zero query rows, nothing else
-        bf16* out = reinterpret_cast<bf16*>(p.q_out) + (static_cast<size_t>(b) * p.Hq * p.N + t) * D;
-        for (int i = begin; i < min(end, steps.nq); ++i)
-            if (i * RPW + grp < p.Hq)
-                *reinterpret_cast<uint4*>(out + static_cast<size_t>(i * RPW + grp) * p.N * D + sub * 8) = make_uint4(0, 0, 0, 0);
-        return;
-    }
+    if (ragged) first_rows();
+    int pos;
+    if constexpr (APPEND)
+        pos = p.parents != nullptr ? row - t + tree_depth(p.parents + static_cast<size_t>(b) * p.N, t, lane, p.status) : row;
+    else
+        pos = p.positions != nullptr ? p.positions[token] : t;
+    pos = checked_position(pos, p.max_pos, p.status);
     const size_t kv_rows = APPEND ? p.Nk_max : p.N;
     const size_t head = static_cast<size_t>(p.copies) * kv_rows * D;
     const size_t at = static_cast<size_t>(b) * p.Hkv * head + static_cast<size_t>(row) * D;

@@ -239,3 +239,25 @@ def test_graph_and_streams():
                 got.append(fa().qk_norm_rope_bwd(*want, *x[:2], *rest))
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for t in got for a, b in zip(t, back))
+
+
+@pytest.mark.parametrize("B,T,Hq,Hkv,d", [(64, 64, 32, 8, 128), (200, 40, 9, 3, 64), (3, 9, 5, 5, 32)])
+def test_append_uses_nothing_of_absent_nodes(B, T, Hq, Hkv, d):
+    """Rows, parents and values of nodes past n_nodes may hold anything; the others come out as they do alone, from
+    one warp to a few heads up to one warp to a token."""
+    q, k, v, w, cos, sin, _ = make(B, T, Hq, Hkv, d, d, True, B + T, extra=200)
+    g = torch.Generator().manual_seed(B)
+    cnt = torch.randint(0, T + 1, (B,), generator=g).to(torch.int32)
+    lens = torch.randint(0, 100, (B,), generator=g).to(torch.int32)
+    par = random_parents(B, T, T)
+    rest = (w[0].to(DEV), w[1].to(DEV), cos.to(DEV), sin.to(DEV))
+    out = []
+    for fill in (0.0, float("nan")):
+        gone = torch.arange(T) >= cnt[:, None]
+        q._base[gone] = fill
+        par[gone] = 0 if fill == 0.0 else 1 << 30
+        kc, vc = (torch.zeros((B, Hkv, 100 + T, d), dtype=BF16, device=DEV) for _ in range(2))
+        qo = fa().qk_norm_rope_append(*dev(q, k, v), *rest, kc, vc, lens.to(DEV), parents=par.to(DEV), n_nodes=cnt.to(DEV))
+        out.append((qo, kc, vc))
+    assert all(torch.equal(a, b) for a, b in zip(*out)) and fa().get_device_error() == 0
+    assert torch.all(out[0][0].cpu().transpose(1, 2)[gone] == 0)
