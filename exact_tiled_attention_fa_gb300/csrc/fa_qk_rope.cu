@@ -262,9 +262,10 @@ struct Steps {
 };
 
 // Grid (tokens / kRopeWarps, step chunks).  A warp: one token, steps blockIdx.y * chunk .. + chunk.
-// Four rows in flight and four CTAs an SM (64 registers): B=64 N=1024 H=16 d=64 123 us, 6.6 TB/s of
-// reads and writes; three CTAs 136, two with eight rows 168, five (48 registers, which spill) 145.  Rows
-// through a ring of asynchronous copies, as in the backward kernel: 128 us there, 6-10 % slower at d = 128.
+// Four rows in flight and four CTAs an SM (64 registers): B=64 N=1024 H=16 d=64 120 us, 6.7 TB/s of
+// reads and writes; three CTAs 136, two with eight rows 168, five (48 registers, which spill) 145 (at 123 for
+// four).  Rows through a ring of asynchronous copies, as in the backward kernel: 128 us there, 6-10 % slower at
+// d = 128.
 // APPEND: token t of sequence b is node t of its tree, at position seqlens[b] + depth, and its key
 // and value go to cache row seqlens[b] + t.  Nodes past n_nodes[b] have zero query rows and no cache
 // row.
@@ -276,11 +277,11 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) fa_qk_rope_kernel(const Ro
     constexpr int LPR = D / 8;    // lanes of a row
     constexpr int RPW = 32 / LPR; // rows of a warp's step
     constexpr int U = 4;          // steps in flight
-    // Whether the first values are copied while the position and the angles are on their way: with the
-    // smaller heads a token has few steps to hide that under (share of the copy's rate with and without,
-    // d = 64: 12 heads 91 / 87 %, 8 heads 81 / 77, 16 heads 96 / 96; d = 32 16 heads 80 / 77; d = 128, where
-    // the registers are short: 32/8 heads 93 / 95).  Nodes that are not there are not read.
-    constexpr bool EARLY = D < 128 && !APPEND;
+    // The first values are copied while the position and the angles are on their way: a token may have few steps
+    // to hide that under (share of the copy's rate with and without, d = 64: 16 heads 98 / 95 %, 12 heads 93 / 86,
+    // 8 heads 84 / 76; d = 32: 16 heads 84 / 77, 12 heads 70 / 64; d = 128: 32/8 heads 95 / 94).  Not for a cache,
+    // whose rows are known with the length only.
+    constexpr bool EARLY = !APPEND;
     using bf16 = __nv_bfloat16;
     const int lane = threadIdx.x & 31;
     const int sub = lane % LPR;
@@ -305,8 +306,8 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) fa_qk_rope_kernel(const Ro
     };
     // Values pass through: 16 bytes a lane.
     const int vb = max(begin, steps.nq + steps.nk) - steps.nq - steps.nk, ve = end - steps.nq - steps.nk;
-    const bf16* v = reinterpret_cast<const bf16*>(p.v) + static_cast<long long>(token) * p.v_stride + sub * 8;
     auto load_v = [&](uint4 (&x)[U], int i) {
+        const bf16* v = reinterpret_cast<const bf16*>(p.v) + static_cast<long long>(token) * p.v_stride + sub * 8;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int h = (i + u) * RPW + grp;
@@ -349,8 +350,17 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) fa_qk_rope_kernel(const Ro
     pos = checked_position(pos, p.max_pos, p.status);
     const size_t kv_rows = APPEND ? p.Nk_max : p.N;
     const size_t head = static_cast<size_t>(p.copies) * kv_rows * D;
-    const size_t at = static_cast<size_t>(b) * p.Hkv * head + static_cast<size_t>(row) * D;
-    auto store_v = [&](const uint4 (&x)[U], int i) {
+    // Elements into the keys or values of the warp's token, first head.  The first values ask for it early; kept
+    // across the query heads it would take registers that are short there, so the later kinds of heads work it out
+    // anew (the empty statement hides that it is the same).  In the APPEND form the key heads' angles are read
+    // again for the same reason.  With both kept the forms spilled: B=64 N=1024 H=16 d=64 123.5 us against 120,
+    // 12 heads 98 against 95; 64 full trees of 64 nodes into a cache 18.9 against 17.9, d=32 5.9 against 5.8.
+    auto kv_at = [&]() -> size_t {
+        unsigned i = b;
+        if (EARLY) asm volatile("" : "+r"(i));
+        return static_cast<size_t>(i) * p.Hkv * head + static_cast<size_t>(row) * D;
+    };
+    auto store_v = [&](const uint4 (&x)[U], int i, size_t at) {
         bf16* out = reinterpret_cast<bf16*>(p.v_out) + at + sub * 8;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -363,7 +373,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) fa_qk_rope_kernel(const Ro
         }
     };
     const Pairs cs = share.angles(p.cos_t, p.sin_t, pos, p.rot);
-    if (EARLY && vb < ve) store_v(first_v, vb);
+    if (EARLY && vb < ve) store_v(first_v, vb, kv_at());
     auto turned = [&](const Turn& turn, uint4 u) -> uint4 {
         const Pairs x = share.unpack(u);
         return share.pack(turn.apply(x, rsqrtf(row_sum<LPR>(dot(x, x)) * (1.f / D) + p.eps)));
@@ -394,9 +404,11 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) fa_qk_rope_kernel(const Ro
     };
     const int kb = max(begin, steps.nq) - steps.nq, ke = min(end, steps.nq + steps.nk) - steps.nq;
     if (kb < ke) {
-        const Turn turn(share.weights(p.wk, p.w_dtype), cs);
+        int again = pos;  // (see kv_at)
+        if (APPEND) asm volatile("" : "+r"(again));
+        const Turn turn(share.weights(p.wk, p.w_dtype), APPEND ? share.angles(p.cos_t, p.sin_t, again, p.rot) : cs);
         const bf16* k = reinterpret_cast<const bf16*>(p.k) + static_cast<long long>(token) * p.k_stride;
-        bf16* out = reinterpret_cast<bf16*>(p.k_out) + at;
+        bf16* out = reinterpret_cast<bf16*>(p.k_out) + kv_at();
         for (int i = kb; i < ke; i += U) {
             load(raw, k, i, ke, p.Hkv);
 #pragma unroll
@@ -408,7 +420,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) fa_qk_rope_kernel(const Ro
     }
     for (int i = EARLY ? vb + U : vb; i < ve; i += U) {
         load_v(raw, i);
-        store_v(raw, i);
+        store_v(raw, i, kv_at());
     }
 }
 
