@@ -5,7 +5,9 @@ the objects are linked into ``libfa.so`` next to this file (the CUDA runtime
 is linked statically, the driver API is reached through the runtime's
 entry-point query, so the library loads on machines without a GPU).
 ``_fa_binding.so`` (csrc/fa_binding.cpp) checks and marshals the Python calls of the operators around
-cached attention; it is compiled against the installed torch and links ``libfa.so`` beside it.
+cached attention; it is compiled against the installed torch and links ``libfa.so`` beside it.  The
+library itself needs neither torch nor g++: ``python exact_tiled_attention_fa_gb300/build.py`` leaves it
+there for C callers also where the binding cannot be built.
 """
 from __future__ import annotations
 
@@ -20,6 +22,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfa.so")
 BINDING = os.path.join(HERE, "_fa_binding.so")
+BINDING_SRC = "fa_binding.cpp"
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -38,19 +41,24 @@ def sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
 
 
-def _deps():
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "fa.h")]
-    return max(os.path.getmtime(f) for f in files)
+def _fresh(target, binding):
+    """Whether a target is at least as new as its sources: the binding's file, or all others."""
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if (f == BINDING_SRC) == binding] + [os.path.join(INCLUDE, "fa.h")]
+    return os.path.exists(target) and os.path.getmtime(target) >= max(os.path.getmtime(f) for f in files)
 
 
 def build(force=False, verbose=False, extra_flags=()):
-    """Compile every kernel and the C ABI into ``libfa.so``; returns its path."""
-    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps() for f in (LIB, BINDING)):
+    """Compile every kernel and the C ABI into ``libfa.so``, and the binding; returns the library's path.
+
+    The library needs nvcc alone: it is linked whether or not the binding, which needs torch and a C++
+    compiler, can be built.  That raises afterwards.
+    """
+    library = force or not _fresh(LIB, False)
+    binding = force or not _fresh(BINDING, True)
+    if not library and not binding:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
-    import torch
-    torch_dir = os.path.dirname(torch.__file__)
     cxx = os.environ.get("CXX") or shutil.which("g++") or "c++"
 
     def compile_one(src):
@@ -63,36 +71,38 @@ def build(force=False, verbose=False, extra_flags=()):
             print(r.stderr)
         return obj
 
+    def link(target, *cmd):
+        tmp = target + f".tmp{os.getpid()}"
+        r = subprocess.run([*cmd, "-o", tmp], capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n{r.stderr}")
+        os.replace(tmp, target)
+
     def compile_binding():
+        import torch
+        torch_dir = os.path.dirname(torch.__file__)
         obj = os.path.join(BUILD, "fa_binding.o")
         inc = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
                sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")]
         cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-               *[f for i in inc for f in ("-I", i)], "-c", os.path.join(CSRC, "fa_binding.cpp"), "-o", obj]
+               *[f for i in inc for f in ("-I", i)], "-c", os.path.join(CSRC, BINDING_SRC), "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"{cxx} failed on fa_binding.cpp:\n{r.stderr}")
-        return obj
+            raise RuntimeError(f"{cxx} failed on {BINDING_SRC}:\n{r.stderr}")
+        return obj, os.path.join(torch_dir, "lib")
 
     srcs = sources()
     with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
-        binding = ex.submit(compile_binding)
-        objs = list(ex.map(compile_one, srcs))
-        binding_obj = binding.result()
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stderr}")
-    os.replace(tmp, LIB)
-    tmp = BINDING + f".tmp{os.getpid()}"
-    libs = os.path.join(torch_dir, "lib")
-    cmd = [cxx, "-shared", "-o", tmp, binding_obj, "-L", HERE, "-l:libfa.so", "-Wl,-rpath,$ORIGIN", "-L", libs,
-           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stderr}")
-    os.replace(tmp, BINDING)
+        made = ex.submit(compile_binding) if binding else None
+        if library:
+            link(LIB, nvcc, *ARCH, "-shared", "-cudart", "static", *ex.map(compile_one, srcs))
+    if made is not None:
+        try:
+            obj, libs = made.result()
+            link(BINDING, cxx, "-shared", obj, "-L", HERE, "-l:libfa.so", "-Wl,-rpath,$ORIGIN", "-L", libs,
+                 "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python")
+        except (RuntimeError, ImportError, OSError) as e:
+            raise RuntimeError(f"libfa.so is built, _fa_binding.so is not: {e}") from e
     return LIB
 
 
