@@ -15,6 +15,7 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -23,6 +24,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfa.so")
 BINDING = os.path.join(HERE, "_fa_binding.so")
 BINDING_SRC = "fa_binding.cpp"
+STAMP = os.path.join(BUILD, "fa_binding.host")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -47,6 +49,23 @@ def _fresh(target, binding):
     return os.path.exists(target) and os.path.getmtime(target) >= max(os.path.getmtime(f) for f in files)
 
 
+def _host():
+    """What the binding was compiled for: it uses torch's and Python's internal C++ interfaces."""
+    try:
+        import torch
+    except ImportError:
+        return None  # it cannot be built: the attempt says so
+    return f"torch {torch.__version__} abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)} python {sys.version} {sysconfig.get_platform()}"
+
+
+def _made_for_host():
+    try:
+        with open(STAMP) as f:
+            return f.read() == _host()
+    except OSError:
+        return False
+
+
 def build(force=False, verbose=False, extra_flags=()):
     """Compile every kernel and the C ABI into ``libfa.so``, and the binding; returns the library's path.
 
@@ -54,7 +73,7 @@ def build(force=False, verbose=False, extra_flags=()):
     compiler, can be built.  That raises afterwards.
     """
     library = force or not _fresh(LIB, False)
-    binding = force or not _fresh(BINDING, True)
+    binding = force or not _fresh(BINDING, True) or not _made_for_host()
     if not library and not binding:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
@@ -101,6 +120,8 @@ def build(force=False, verbose=False, extra_flags=()):
             obj, libs = made.result()
             link(BINDING, cxx, "-shared", obj, "-L", HERE, "-l:libfa.so", "-Wl,-rpath,$ORIGIN", "-L", libs,
                  "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python")
+            with open(STAMP, "w") as f:
+                f.write(_host())
         except (RuntimeError, ImportError, OSError) as e:
             raise RuntimeError(f"libfa.so is built, _fa_binding.so is not: {e}") from e
     return LIB

@@ -76,3 +76,14 @@ def test_only_what_changed_is_built(tree):
     os.utime(tree.pkg.parent / "include" / "fa.h")
     assert tree()[1:] == (n + 1, 2)
     assert tree(force=True)[1:] == (n + 1, 2)
+
+
+def test_binding_is_built_again_for_another_torch_or_python(tree):
+    """The binding alone: the library does not depend on them."""
+    n = len(fa_build.sources())
+    assert tree()[1:] == (n + 1, 2)
+    other = "import torch; torch.__version__ += '.other'"
+    assert tree(before=other)[1:] == (0, 2)
+    assert tree(before=other)[1:] == (0, 0)
+    assert tree()[1:] == (0, 2)
+    assert tree(before="sys.version = 'another'")[1:] == (0, 2)
