@@ -496,7 +496,8 @@ def qk_norm_rope(q, k, v, q_weight, k_weight, cos, sin, positions=None, eps=1e-6
     q [B,N,Hq,d], k and v [B,N,Hkv,d] bf16 with evenly spaced tokens (slices of one projection will do;
     v may be None); cos, sin fp32 [max_pos, rot/2]; positions int32 [B,N] (None: 0 .. N-1).  Pairs are
     (i, i + rot/2), or (2i, 2i+1) with ``interleaved``.  With ``expand`` key/value heads are repeated for
-    their query heads.  Returns (q [B,Hq,N,d], k, v [B,Hkv or Hq,N,d] or None), bf16.
+    their query heads.  Returns (q [B,Hq,N,d], k, v [B,Hkv or Hq,N,d] or None), bf16.  A row whose sum of squares
+    overflows fp32 is 0; with eps = 0 a row of zeros is NaN.
     """
     r = (_binding or _native()).qk_norm_rope(q, k, v, q_weight, k_weight, cos, sin, positions, eps, interleaved, expand,
                                              q_out, k_out, v_out)
@@ -558,7 +559,8 @@ def decode_tree(q, k_cache, v_cache, seqlens, parents=None, n_nodes=None, scale=
     non-finite key reaches only the tokens that see it, a non-finite value of a drafted token may reach the
     whole sequence's.  ``workspace`` is a uint8 CUDA tensor of at least
     ``decode_tree_workspace_size`` bytes (allocated here when omitted).  Returns (O [B,Hq,T,d], LSE fp32
-    [B,Hq,T] or None); O = 0 and LSE = -inf for tokens that are not there.
+    [B,Hq,T] or None); O = 0 and LSE = -inf for tokens that are not there.  The softmax's weights are rounded to
+    bf16 before they multiply V, also where O is fp32.
     """
     sms = num_sms(q.device) if workspace is None and isinstance(q, torch.Tensor) and q.is_cuda else 0
     r = (_binding or _native()).decode_tree(q, k_cache, v_cache, seqlens, parents, n_nodes, scale, _odt(out_dtype), out, lse,

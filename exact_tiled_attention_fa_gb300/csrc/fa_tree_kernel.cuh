@@ -39,10 +39,14 @@
 // (fa_cached_api.cu chooses, with what the forms measured.)
 //
 // What bounds it, and what it takes with the merge (16 sequences of 1 - 32K tokens, 32/8 heads, d = 128):
-// with 16 nodes K and V, 170 us, 6.5 TB/s; with 64 nodes the softmax's chain between two products (scores
-// out of tensor memory, exponentials, weights back, two barriers), 258 us, 1100 TFLOP/s, tensor cores 47 %
-// busy.  One sequence of 2000 tokens, 8 nodes: 12.3 us, latency: two launches, lengths, the first tiles,
-// one tile's softmax, its rows out and in again.
+// with 16 nodes K and V, 168-173 us, 6.5 TB/s; with 64 nodes the softmax's chain between two products (scores
+// out of tensor memory, exponentials, weights back, two barriers), 258 us, 1100 TFLOP/s in a short series and
+// 275 us, 1030 TFLOP/s in a long one at the power limit's clock, tensor cores 47 % busy.  One sequence of 2000
+// tokens, 8 nodes: 12.1 us, latency: two launches, lengths, the first tiles, one tile's softmax, its rows out
+// and in again.  Many short caches (256 sequences of 150 - 300 tokens, 4 nodes) 73 us, half the copy's rate: a
+// unit's end, its rows out by the warps that are to take the next one's scores, comes once in two or three
+// tiles, and at d = 128 a SOLO stream has one stage each of K and V, so a tile is asked for only when the
+// product before it is done.
 //
 // Masks.  Only the tiles that hold drafted rows are masked, by four 32-bit words per query row (its
 // ancestors), shifted to the tile; hidden scores become -inf by selection, so a non-finite key
@@ -114,7 +118,8 @@ struct TrCfg {
     static constexpr int kStep = kBlockN / kSteps;  // keys
     // Registers after the split: 256 * softmax + 128 * control = 64512 = 384 * 168, checked by the launcher.
     // A softmax thread holds the scores of a step.  (With 224 and 56 at d = 128 the producers and issuers
-    // spilled: 256 sequences of 300 tokens 77.7 us, with 216 and 72 they take 72.9.)
+    // spilled more: 256 sequences of 300 tokens 77.7 us, with 216 and 72 they take 72.9.  Bytes stored and
+    // loaded that still spill: d = 128 ALT 136/164, SOLO 56/72, PAIR 24/128; d <= 64 ALT 60/80, others none.)
     static constexpr int kSoftmaxRegs = kSteps == 2 ? 192 : D == 128 ? 216 : 208;
     static constexpr int kControlRegs = kSteps == 2 ? 120 : D == 128 ? 72 : 88;
     static constexpr int kCB = D < 64 ? D : 64;

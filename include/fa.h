@@ -38,7 +38,11 @@
  *     read, and the gradients written for them, have a token stride besides.  Device pointers
  *     must be 16-byte aligned.
  *   - q, k, v and the caches are bf16.  Arithmetic is fp32 (tensor-core accumulation in
- *     fp32; softmax statistics in fp32).  O is written as bf16 (FA_BF16) or fp32 (FA_F32);
+ *     fp32; softmax statistics in fp32), but what a first product gives a second one on the
+ *     tensor core is rounded to bf16 between them, by at most 2^-8 of each number: the softmax
+ *     weights for the product with V (fa_fwd, fa_fwd_splitkv, fa_decode_tree, and
+ *     fa_decode_splitkv_gqa but for groups of 1, 2 and, below d = 128, 4 heads), and P and
+ *     scale * dS in fa_bwd, whatever the output's type.  O is written as bf16 (FA_BF16) or fp32 (FA_F32);
  *     LSE is always fp32, natural log, scale included:
  *       LSE[i] = log sum_{visible j} exp(scale * q_i . k_j).
  *   - Causal masking places query i at position Nk - N + i and key j at position j
@@ -385,9 +389,10 @@ size_t fa_qk_norm_rope_bwd_workspace_size(int d);
  *   grad_q, grad_k, grad_v  grad_dtype [B, N, heads, d] with token strides  (device, written)
  *   grad_q_weight, grad_k_weight  fp32 [d]  (device, written)
  *   workspace  ws_bytes >= fa_qk_norm_rope_bwd_workspace_size(d), 256-byte aligned; its contents on
- *              entry do not matter.
- * Every sum is in a fixed order: results are the same from run to run.  Outputs must not overlap
- * inputs.
+ *              entry do not matter.  Calls sharing a workspace must not overlap on the GPU.
+ * Every sum is in a fixed order: results are the same from run to run.  grad_w is an fp32 sum, in which a
+ * warp adds its rows one after the other (a token in 2432 on 152 SMs) before the warps' sums are joined.
+ * Outputs must not overlap inputs.
  * Returns FA_ERR_WORKSPACE if ws_bytes is too small (nothing launched).
  */
 fa_status fa_qk_norm_rope_bwd(const void* grad_q_out, const void* grad_k_out, const void* grad_v_out,
@@ -443,7 +448,10 @@ size_t fa_decode_tree_workspace_size(int Hq, int Hkv, int T, int d, int num_sms)
  * tokens, to itself and to its ancestors,
  *   o[b,h,t,:] = sum_j softmax_j(scale q[b,h,t,:] . K[b,g,j,:]) V[b,g,j,:],  g = h / (Hq / Hkv),
  * over the visible rows j of the cache, lse the log of the sum.  With T = 1 it is
- * fa_decode_splitkv_gqa over p + 1 cached tokens.
+ * fa_decode_splitkv_gqa over p + 1 cached tokens.  The weights that multiply V are rounded to bf16, their
+ * sum is not: o is off by up to 2^-8 of sum_j weight_j |V_j|, also where it is written in fp32 (on normally
+ * distributed inputs 0.0014 of o, in the root mean square; writing o in bf16 is off by 0.0017).  lse does not
+ * depend on it.
  *
  *   q          bf16 [B, Hq, T, d]          (device; fa_qk_norm_rope_append's q_out)
  *   k_cache, v_cache  bf16 [B, Hkv, Nk_max, d]  (device; rows from p + n on are never used, whatever
