@@ -497,7 +497,7 @@ def qk_norm_rope(q, k, v, q_weight, k_weight, cos, sin, positions=None, eps=1e-6
     v may be None); cos, sin fp32 [max_pos, rot/2]; positions int32 [B,N] (None: 0 .. N-1).  Pairs are
     (i, i + rot/2), or (2i, 2i+1) with ``interleaved``.  With ``expand`` key/value heads are repeated for
     their query heads.  Returns (q [B,Hq,N,d], k, v [B,Hkv or Hq,N,d] or None), bf16.  A row whose sum of squares
-    overflows fp32 is 0; with eps = 0 a row of zeros is NaN.
+    overflows fp32 is 0; with eps = 0 a row of zeros has no norm and is NaN.
     """
     r = (_binding or _native()).qk_norm_rope(q, k, v, q_weight, k_weight, cos, sin, positions, eps, interleaved, expand,
                                              q_out, k_out, v_out)

@@ -363,8 +363,8 @@ fa_status fa_merge_states(const float* o_parts, const float* lse_parts, int n_pa
  *              h / (Hq / Hkv), as fa_fwd takes them  (device, written)
  *   d in {32, 64, 128}; Hkv dividing Hq; rot a multiple of 16, at most d; B * N < 2^31; eps >= 0.
  * Outputs must not overlap inputs.  mean(x^2) is an fp32 sum: where it overflows (elements of about 1e18
- * and more) the row is written as 0, and its gradient is 0.  With eps = 0 a row of zeros has no norm: it becomes NaN, here and
- * in the gradients.
+ * and more) the row is written as 0, and its gradient is 0.  With eps = 0 a row whose squares are 0 in fp32
+ * (zeros, or elements below about 1e-23) has no norm: it becomes NaN or infinite, here and in the gradients.
  */
 fa_status fa_qk_norm_rope(const void* q, const void* k, const void* v, const void* q_weight,
                           const void* k_weight, const float* cos_table, const float* sin_table,
