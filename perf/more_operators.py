@@ -259,7 +259,7 @@ def _own(s, case):
     if "ws" not in s:
         size = fa.fwd_rules_workspace_size(case["B"], case["N"])
         if train:
-            size = max(size, fa.bwd_rules_workspace_size(case["B"], case["Hq"], case["N"], case["Nk"], case["d"]))
+            size = max(size, fa.bwd_rules_workspace_size(*(case[n] for n in ("B", "Hq", "Hkv", "N", "Nk", "d")), fa.num_sms()))
         s["ws"] = torch.empty(size, dtype=torch.uint8, device=DEV)
     o, lse = fa.fwd_rules(s["q"], s["k"], s["v"], workspace=s["ws"], **rules)
     if not train:
