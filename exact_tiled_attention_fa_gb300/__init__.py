@@ -18,7 +18,11 @@ Entry points (same names as the C ABI, without the ``fa_`` prefix):
   qk_norm_rope_append  the same for new tokens, keys and values written into a cache
   decode_tree      decode for a tree of drafted tokens over a cache
   cache_compact    the accepted path of a tree moved up behind the cached tokens
-  decode_default_splits, decode_gqa_default_splits, decode_workspace_size,
+  fwd_rules        the forward with rules for its scores (cap by tanh, distance bias), masks (documents, prefix)
+                   and shared key/value heads
+  bwd_rules        its gradient
+  decode_default_splits, decode_gqa_default_splits, decode_workspace_size, fwd_rules_workspace_size,
+  bwd_rules_workspace_size,
   decode_tree_workspace_size, qk_norm_rope_bwd_workspace_size, get_device_error,
   set_wait_timeout_ns, status_string
 """
@@ -98,6 +102,14 @@ def _load():
     lib.fa_decode_tree.restype = i
     lib.fa_cache_compact.argtypes = [vp] * 6 + [i] * 7 + [vp]
     lib.fa_cache_compact.restype = i
+    lib.fa_fwd_rules_workspace_size.argtypes = [i] * 2
+    lib.fa_fwd_rules_workspace_size.restype = sz
+    lib.fa_fwd_rules.argtypes = [vp] * 9 + [sz] + [i] * 8 + [f, f, i, vp]
+    lib.fa_fwd_rules.restype = i
+    lib.fa_bwd_rules_workspace_size.argtypes = [i] * 7
+    lib.fa_bwd_rules_workspace_size.restype = sz
+    lib.fa_bwd_rules.argtypes = [vp] * 13 + [sz] + [i] * 8 + [f, f, i, i, vp]
+    lib.fa_bwd_rules.restype = i
     lib.fa_get_device_error.argtypes = [vp]
     lib.fa_get_device_error.restype = i
     lib.fa_set_wait_timeout_ns.argtypes = [ull]
@@ -581,6 +593,51 @@ def cache_compact(k_cache, v_cache, seqlens, accepted, n_accepted, seqlens_out=N
     if type(r) is int:
         raise FaError(r, "fa_cache_compact")
     return r[0]
+
+
+def fwd_rules_workspace_size(B, N):
+    return int(_load().fa_fwd_rules_workspace_size(B, N))
+
+
+def fwd_rules(q, k, v, causal=False, scale=None, softcap=0.0, slopes=None, documents=None, prefix_lens=None,
+              out_dtype=torch.bfloat16, out=None, lse=None, workspace=None, return_lse=True):
+    """Exact attention forward under score rules.  q [B,Hq,N,d], k, v [B,Hkv,Nk,d] bf16 with Hkv dividing Hq (query
+    head h uses key/value head h // (Hq // Hkv)); query i sits at position Nk - N + i.
+
+    ``softcap`` c > 0 makes scores c * tanh(s / c); ``slopes`` fp32 [Hq] then takes slope * distance off them.  With
+    ``causal`` a query sees the keys up to its position and those before ``prefix_lens`` int32 [B].  ``documents``
+    int32 [B,Nk]: query and key see each other only within one run of equal numbers >= 0; a number below 0 is
+    padding, whose queries see nothing (O = 0, LSE = -inf).  ``workspace`` is a uint8 CUDA tensor of at least
+    ``fwd_rules_workspace_size`` bytes, needed (and allocated here when omitted) only with documents.  q and v must be
+    finite, also in padding.  Returns (O [B,Hq,N,d] of ``out_dtype``, LSE fp32 [B,Hq,N] or None).
+    """
+    r = (_binding or _native()).fwd_rules(q, k, v, causal, scale, softcap, slopes, documents, prefix_lens, _odt(out_dtype), out,
+                                          lse, return_lse, workspace)
+    if type(r) is int:
+        raise FaError(r, "fa_fwd_rules")
+    return r
+
+
+def bwd_rules_workspace_size(B, Hq, Hkv, N, Nk, d, num_sms):
+    return int(_load().fa_bwd_rules_workspace_size(B, Hq, Hkv, N, Nk, d, num_sms))
+
+
+def bwd_rules(q, k, v, o, lse, do, causal=False, scale=None, softcap=0.0, slopes=None, documents=None, prefix_lens=None,
+              out_dtype=torch.bfloat16, grads=None, workspace=None):
+    """Gradient of ``fwd_rules`` for the gradient ``do`` (bf16) of its output ``o`` (bf16 or fp32), with its log-sum-exp
+    and the same rules; the slopes are constants.
+
+    ``grads`` is an optional (dq, dk, dv) triple to write into; ``workspace`` a uint8 CUDA tensor of at least
+    ``bwd_rules_workspace_size`` bytes (allocated here when omitted).  q, k, v and do must be finite, also in padding.
+    Returns (dq [B,Hq,N,d], dk, dv [B,Hkv,Nk,d]) of ``out_dtype``; dk and dv are added up over a group's query heads.
+    """
+    sms = num_sms(q.device) if workspace is None and isinstance(q, torch.Tensor) and q.is_cuda else 0
+    dq, dk, dv = grads if grads is not None else (None, None, None)
+    r = (_binding or _native()).bwd_rules(q, k, v, o, lse, do, causal, scale, softcap, slopes, documents, prefix_lens,
+                                          _odt(out_dtype), dq, dk, dv, workspace, sms)
+    if type(r) is int:
+        raise FaError(r, "fa_bwd_rules")
+    return r
 
 
 def get_device_error(device=None):

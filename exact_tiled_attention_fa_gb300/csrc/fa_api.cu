@@ -259,6 +259,10 @@ cudaError_t device_status_word(int** out) { return status_word(out); }
 cudaError_t device_sm_count(int* out) { return sm_count(out); }
 unsigned long long wait_limit_ns() { return g_wait_ns.load(); }
 bool bf16_tile_map(CUtensorMap* m, const void* ptr, int BH, int rows, int d) { return make_map(m, ptr, BH, rows, d); }
+bool out_tile_map(CUtensorMap* m, void* ptr, int BH, int rows, int d, fa_dtype t, int box_rows)
+{
+    return make_out_map(m, ptr, BH, rows, d, t, box_rows);
+}
 }  // namespace fa
 
 extern "C" {
@@ -355,7 +359,7 @@ fa_status fa_bwd(const void* q, const void* k, const void* v, const void* o, con
     float* dsc = reinterpret_cast<float*>(reinterpret_cast<char*>(lse2) + round_up(rows * sizeof(float), kAlign));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
 
-    fa::BwdPrepParams pp;
+    fa::BwdPrepParams pp{};
     pp.o = o;
     pp.d_o = grad_o;
     pp.lse = lse;

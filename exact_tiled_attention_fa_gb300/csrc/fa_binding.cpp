@@ -404,6 +404,126 @@ PyObject* decode_tree(PyObject*, PyObject* const* a, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
+// Workspace: the given one, or `bytes` made here.
+struct Space {
+    Tensor made;
+    void* ptr = nullptr;
+    size_t bytes = 0;
+    Space(PyObject* o, const Tensor& like, int device, size_t need)
+    {
+        if (o == Py_None) {
+            if (need == 0) return;
+            made = output(Py_None, like, at::kByte, {static_cast<int64_t>(need)});
+            ptr = made.data_ptr();
+            bytes = need;
+        } else {
+            const Tensor& w = tensor(o, "workspace");
+            ptr = arg(o, "workspace", at::kByte, device, w.sizes());
+            bytes = static_cast<size_t>(w.numel());
+        }
+    }
+};
+
+int sm_count(PyObject* o)
+{
+    const long sms = PyLong_AsLong(o);
+    if (sms == -1 && PyErr_Occurred()) throw python_error();
+    return static_cast<int>(sms);
+}
+
+// What forward and backward under score rules share: q k v and causal scale softcap slopes documents prefix_lens.
+struct Rules {
+    int device;
+    int64_t B, Hq, Hkv, N, Nk, d;
+    std::array<int64_t, 4> qs, kvs;
+    void *q, *k, *v;
+    int causal;
+    float scale, softcap;
+    const float* slopes;
+    const int *documents, *prefix_lens;
+    const Tensor* like;
+    Rules(PyObject* const* a, PyObject* const* r)
+    {
+        const char* layout = "[B, heads, rows, head_dim]";
+        const Tensor& t = first(a[0], "q", 4, layout);
+        const Tensor& u = first(a[1], "k", 4, layout);
+        like = &t;
+        device = static_cast<int>(t.get_device());
+        B = t.size(0), Hq = t.size(1), N = t.size(2), d = t.size(3), Hkv = u.size(1), Nk = u.size(2);
+        qs = {B, Hq, N, d};
+        kvs = {B, Hkv, Nk, d};
+        q = arg(a[0], "q", kBf16, device, qs);
+        k = arg(a[1], "k", kBf16, device, kvs);
+        v = arg(a[2], "v", kBf16, device, kvs);
+        causal = flag(r[0]);
+        scale = static_cast<float>(r[1] == Py_None ? 1.0 / std::sqrt(static_cast<double>(d)) : number(r[1]));
+        softcap = static_cast<float>(number(r[2]));
+        slopes = static_cast<const float*>(optional_arg(r[3], "slopes", kF32, device, {Hq}));
+        documents = static_cast<const int*>(optional_arg(r[4], "documents", kI32, device, {B, Nk}));
+        prefix_lens = static_cast<const int*>(optional_arg(r[5], "prefix_lens", kI32, device, {B}));
+    }
+};
+
+PyObject* fwd_rules(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    // q k v causal scale softcap slopes documents prefix_lens out_f32 out lse return_lse workspace
+    expect(n, 14);
+    const Rules r(a, a + 3);
+    const at::ScalarType ot = a[10] != Py_None ? tensor(a[10], "out").scalar_type() : flag(a[9]) ? kF32 : kBf16;
+    const fa_dtype od = out_type(ot);
+    const Tensor out = output(a[10], *r.like, ot, r.qs);
+    void* op = pointer_of(a[10], out, "out", ot, r.device, r.qs);
+    Tensor lse;
+    void* lp = nullptr;
+    const bool want = a[11] != Py_None || flag(a[12]);
+    if (want) {
+        lse = output(a[11], *r.like, kF32, {r.B, r.Hq, r.N});
+        lp = pointer_of(a[11], lse, "lse", kF32, r.device, {r.B, r.Hq, r.N});
+    }
+    const Space ws(a[13], *r.like, r.device, r.documents != nullptr ? fa_fwd_rules_workspace_size(as_int(r.B), as_int(r.N)) : 0);
+    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(r.device));
+    const fa_status s = fa_fwd_rules(r.q, r.k, r.v, r.slopes, r.documents, r.prefix_lens, op, static_cast<float*>(lp), ws.ptr,
+                                     ws.bytes, as_int(r.B), as_int(r.Hq), as_int(r.Hkv), as_int(r.N), as_int(r.Nk), as_int(r.d),
+                                     as_int(r.d), r.causal, r.scale, r.softcap, od, stream(r.device));
+    if (s != FA_OK) return status_only(s);
+    return tuple({result(a[10], out), want ? result(a[11], lse) : result(Py_None, Tensor())});
+    END_HANDLE_TH_ERRORS
+}
+
+PyObject* bwd_rules(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    // q k v o lse do causal scale softcap slopes documents prefix_lens out_f32 dq dk dv workspace num_sms
+    expect(n, 18);
+    const Rules r(a, a + 6);
+    const at::ScalarType it = tensor(a[3], "o").scalar_type();
+    const fa_dtype id = out_type(it);
+    void* o = arg(a[3], "o", it, r.device, r.qs);
+    void* lse = arg(a[4], "lse", kF32, r.device, {r.B, r.Hq, r.N});
+    void* g = arg(a[5], "do", kBf16, r.device, r.qs);
+    const bool given = a[13] != Py_None;  // all of the gradients' buffers, or none
+    if ((a[14] != Py_None) != given || (a[15] != Py_None) != given) refuse("grads must hold dq, dk and dv");
+    const at::ScalarType ot = given ? tensor(a[13], "dq").scalar_type() : flag(a[12]) ? kF32 : kBf16;
+    const fa_dtype od = out_type(ot);
+    const Tensor dq = output(a[13], *r.like, ot, r.qs), dk = output(a[14], *r.like, ot, r.kvs), dv = output(a[15], *r.like, ot, r.kvs);
+    void* qp = pointer_of(a[13], dq, "dq", ot, r.device, r.qs);
+    void* kp = pointer_of(a[14], dk, "dk", ot, r.device, r.kvs);
+    void* vp = pointer_of(a[15], dv, "dv", ot, r.device, r.kvs);
+    const size_t need = a[16] != Py_None ? 0
+                                         : fa_bwd_rules_workspace_size(as_int(r.B), as_int(r.Hq), as_int(r.Hkv), as_int(r.N),
+                                                                       as_int(r.Nk), as_int(r.d), sm_count(a[17]));
+    const Space ws(a[16], *r.like, r.device, need > 256 ? need : 256);
+    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(r.device));
+    const fa_status s = fa_bwd_rules(r.q, r.k, r.v, o, static_cast<const float*>(lse), g, r.slopes, r.documents, r.prefix_lens, qp,
+                                     kp, vp, ws.ptr, ws.bytes, as_int(r.B), as_int(r.Hq), as_int(r.Hkv), as_int(r.N),
+                                     as_int(r.Nk), as_int(r.d), as_int(r.d), r.causal, r.scale, r.softcap, id, od,
+                                     stream(r.device));
+    if (s != FA_OK) return status_only(s);
+    return tuple({result(a[13], dq), result(a[14], dk), result(a[15], dv)});
+    END_HANDLE_TH_ERRORS
+}
+
 PyObject* cache_compact(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
     HANDLE_TH_ERRORS
@@ -446,6 +566,8 @@ PyMethodDef methods[] = {
     method<qk_norm_rope_append>("qk_norm_rope_append"),
     method<decode_tree>("decode_tree"),
     method<cache_compact>("cache_compact"),
+    method<fwd_rules>("fwd_rules"),
+    method<bwd_rules>("bwd_rules"),
     {nullptr, nullptr, 0, nullptr},
 };
 

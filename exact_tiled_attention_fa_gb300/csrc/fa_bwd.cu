@@ -48,6 +48,7 @@ __global__ void __launch_bounds__(kPrepThreads) fa_bwd_prep_kernel(const BwdPrep
 {
     grid_dependency_wait();    // O, dO and LSE are written by earlier kernels on the stream
     grid_launch_dependents();  // the tensor-core kernel may begin its setup (it waits for this grid)
+    if (p.counter != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *p.counter = 0;
     const int G = p.d / 8;
     const long long rows = static_cast<long long>(p.BH) * p.Tr * kBlockM;
     const long long t = static_cast<long long>(blockIdx.x) * kPrepThreads + threadIdx.x;

@@ -96,6 +96,7 @@ struct BwdPrepParams {
     float* dq_acc;
     int BH, N, Tr, d;
     float scale;
+    int* counter;       // set to 0 (fa_rules_bwd_kernel's items); nullptr: none
 };
 
 struct BwdDqParams {
@@ -257,12 +258,77 @@ struct CompactParams {
 
 cudaError_t launch_cache_compact(const CompactParams& p, cudaStream_t st);
 
+// Attention under score rules (fa_rules_*.cu, fa_rules_*.cuh).  Scores are scale q.k, capped by a tanh and lowered
+// by slope * distance; what a query sees is one interval of keys, what sees a key one interval of queries.
+struct ScoreRules {
+    float cap_in;         // scale / cap, so that cap * tanh(cap_in * S) is the capped score; 0: no cap
+    float mult;           // capped scores in base 2 are mult * tanh, others mult * S: cap or scale, times log2(e)
+    const float* slopes;  // fp32 [Hq] or nullptr
+};
+
+// A run of equal document numbers, and what a query or a key has of it (fa_rules_ranges_kernel).
+struct RangesParams {
+    const int* docs;    // int32 [B][Nk]
+    const int* prefix;  // int32 [B] or nullptr
+    int2* each;         // [B][n]: keys [x, y) of query x, or queries [x, y) of key x; empty: (0, 0)
+    int2* tile;         // [B][tiles]: 128-tiles [x, y) of the other side that one of its 128 has to do with
+    int* counter;       // of work items, set to 0
+    int* status;
+    int B, N, Nk, tiles, causal;
+};
+
+// The documents' intervals: of every query (keys = false) or of every key.
+cudaError_t launch_rules_ranges(const RangesParams& p, bool keys, cudaStream_t st);
+
+struct FwdRulesParams {
+    FwdParams f;        // without splits; tm_k and tm_v over B * Hkv heads
+    ScoreRules rules;
+    const int* prefix;  // int32 [B] or nullptr
+    const int2* each;   // with documents: keys of each query [B][N], key tiles of each query tile [B][ceil(N / 128)]
+    const int2* tile;
+    int* counter;       // with documents: work items handed out
+    int Hq, Hkv, causal;
+};
+
+cudaError_t launch_fwd_rules_32(const FwdRulesParams& p, fa_dtype o_dtype, cudaStream_t st);
+cudaError_t launch_fwd_rules_64(const FwdRulesParams& p, fa_dtype o_dtype, cudaStream_t st);
+cudaError_t launch_fwd_rules_128(const FwdRulesParams& p, fa_dtype o_dtype, cudaStream_t st);
+
+struct BwdRulesParams {
+    BwdParams b;        // BH = B * Hq; tm_k, tm_v, tm_dk, tm_dv over B * Hkv heads
+    ScoreRules rules;
+    const int* prefix;
+    const int2* each;   // with documents: queries of each key [B][Nk], query tiles of each key tile [B][ceil(Nk / 128)]
+    const int2* tile;
+    int* counter;       // work items handed out, 0 at the start
+    int B, Hq, Hkv, causal;
+    int parts, part_heads;  // items that share a key tile's query heads, and query heads of each; with parts > 1 tm_dk,
+                            // tm_dv, dk and dv are fp32 sums [parts][B * Hkv][Nk][d]
+    int n_items;            // B * Hkv * parts * Tc
+};
+
+cudaError_t launch_bwd_rules_32(const BwdRulesParams& p, fa_dtype grad_dtype, cudaStream_t st);
+cudaError_t launch_bwd_rules_64(const BwdRulesParams& p, fa_dtype grad_dtype, cudaStream_t st);
+cudaError_t launch_bwd_rules_128(const BwdRulesParams& p, fa_dtype grad_dtype, cudaStream_t st);
+
+// out[i] = sum over parts of part[p][i], in order, for i < n (a multiple of 32); both of dK and dV.
+struct RulesSumParams {
+    const float *dk_part, *dv_part;
+    void *dk, *dv;
+    long long n;
+    int parts;
+};
+
+cudaError_t launch_rules_sum(const RulesSumParams& p, fa_dtype grad_dtype, cudaStream_t st);
+
 // Host helpers of the C ABI files (fa_api.cu).
 cudaError_t device_status_word(int** out);  // the current device's status word
 cudaError_t device_sm_count(int* out);
 unsigned long long wait_limit_ns();
 // Tensor map of a bf16 tensor [BH][rows][d] with 128-row boxes, from the thread's cache when possible.
 bool bf16_tile_map(CUtensorMap* m, const void* ptr, int BH, int rows, int d);
+// Tensor map of an output [BH][rows][d] for bulk stores of box_rows rows (encode_out_map), the same way.
+bool out_tile_map(CUtensorMap* m, void* ptr, int BH, int rows, int d, fa_dtype t, int box_rows);
 
 // Status word helpers (device side records the first failure only).
 enum : int { kStatusOk = 0 };

@@ -1,0 +1,262 @@
+// fa_rules_api.cu -- the C ABI of attention under score rules (include/fa.h): forward, backward.  Argument checks,
+// workspace layout and dispatch, host code only; and the kernel that adds up the parts of shared heads' gradients.
+#include <cmath>
+#include <cstdint>
+
+#include "fa_internal.h"
+#include "fa_rules_common.cuh"
+
+namespace fa {
+
+// A thread for 8 consecutive gradients of dK (blockIdx.y 0) or dV (1): the parts are added in order.
+template <typename GradT>
+__global__ void __launch_bounds__(256) fa_rules_sum_kernel(const RulesSumParams p)
+{
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const long long i = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) * 8;
+    if (i >= p.n) return;
+    const float* src = (blockIdx.y == 0 ? p.dk_part : p.dv_part) + i;
+    float a[8] = {};
+    for (int s = 0; s < p.parts; ++s, src += p.n) {
+        const float4 x = __ldcs(reinterpret_cast<const float4*>(src)), y = __ldcs(reinterpret_cast<const float4*>(src) + 1);
+        a[0] += x.x, a[1] += x.y, a[2] += x.z, a[3] += x.w;
+        a[4] += y.x, a[5] += y.y, a[6] += y.z, a[7] += y.w;
+    }
+    GradT* dst = static_cast<GradT*>(blockIdx.y == 0 ? p.dk : p.dv) + i;
+    if constexpr (sizeof(GradT) == 4) {
+        reinterpret_cast<float4*>(dst)[0] = make_float4(a[0], a[1], a[2], a[3]);
+        reinterpret_cast<float4*>(dst)[1] = make_float4(a[4], a[5], a[6], a[7]);
+    } else {
+        *reinterpret_cast<uint4*>(dst) =
+            make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]), pack_bf16x2(a[6], a[7]));
+    }
+}
+
+cudaError_t launch_rules_sum(const RulesSumParams& p, fa_dtype grad_dtype, cudaStream_t st)
+{
+    const long long blocks = (p.n / 8 + 255) / 256;
+    if (blocks <= 0 || blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    const dim3 grid(static_cast<unsigned>(blocks), 2);
+    return grad_dtype == FA_F32 ? launch_pdl(fa_rules_sum_kernel<float>, grid, 256, 0, st, p)
+                                : launch_pdl(fa_rules_sum_kernel<__nv_bfloat16>, grid, 256, 0, st, p);
+}
+
+}  // namespace fa
+
+namespace {
+
+constexpr size_t kAlign = 256;
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+bool head_ok(int d) { return d == 32 || d == 64 || d == 128; }
+bool dtype_ok(fa_dtype t) { return t == FA_BF16 || t == FA_F32; }
+size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+int tiles_of(int n) { return static_cast<int>((static_cast<long long>(n) + fa::kBlockM - 1) / fa::kBlockM); }
+
+// Documents' part of a workspace: a counter of work items, an interval for each of B * n rows and for each tile of them.
+size_t ranges_size(int B, int n)
+{
+    return kAlign + round_up(static_cast<size_t>(B) * n * sizeof(int2), kAlign) +
+           round_up(static_cast<size_t>(B) * tiles_of(n) * sizeof(int2), kAlign);
+}
+
+struct Ranges {
+    int* counter;
+    int2 *each, *tile;
+    Ranges(char* at, int B, int n)
+        : counter(reinterpret_cast<int*>(at)),
+          each(reinterpret_cast<int2*>(at + kAlign)),
+          tile(reinterpret_cast<int2*>(at + kAlign + round_up(static_cast<size_t>(B) * n * sizeof(int2), kAlign)))
+    {
+    }
+};
+
+// Scale and cap as the kernels take them; false for a cap or scale that fp32 cannot hold so.
+bool make_rules(fa::ScoreRules* r, float scale, float softcap, const float* slopes)
+{
+    if (!(std::isfinite(scale) && scale > 0.f) || !(std::isfinite(softcap) && softcap >= 0.f)) return false;
+    r->cap_in = softcap > 0.f ? scale / softcap : 0.f;
+    r->mult = (softcap > 0.f ? softcap : scale) * fa::kLog2e;
+    r->slopes = slopes;
+    return std::isfinite(r->mult) && r->mult > 0.f && std::isfinite(r->cap_in) && (softcap == 0.f || r->cap_in > 0.f);
+}
+
+// The checks that forward and backward share.
+fa_status check_rules(const void* q, const void* k, const void* v, const float* slopes, const int* documents, const int* prefix_lens,
+                      int B, int Hq, int Hkv, int N, int Nk, int d, int dv, int causal, float scale, float softcap)
+{
+    if (q == nullptr || k == nullptr || v == nullptr) return FA_ERR_INVALID_ARG;
+    if (B <= 0 || Hq <= 0 || Hkv <= 0 || N <= 0 || Nk <= 0 || d <= 0 || dv <= 0) return FA_ERR_INVALID_ARG;
+    if (Hq % Hkv != 0 || (causal != 0 && causal != 1)) return FA_ERR_INVALID_ARG;
+    fa::ScoreRules r;
+    if (!make_rules(&r, scale, softcap, slopes)) return FA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(slopes, 4) || !aligned(documents, 4) || !aligned(prefix_lens, 4))
+        return FA_ERR_INVALID_ARG;
+    // positions and tile indices are 32-bit, with room for a tile past the end
+    if (N > 0x7fffff00 || Nk > 0x7fffff00) return FA_ERR_INVALID_ARG;
+    const long long tiles = static_cast<long long>(B) * Hq * (tiles_of(N) > tiles_of(Nk) ? tiles_of(N) : tiles_of(Nk));
+    if (static_cast<long long>(B) * Hq > 0x3fffffffLL || tiles > 0x3fffffffLL) return FA_ERR_INVALID_ARG;
+    return FA_OK;
+}
+
+// Items of the backward that share a key tile's R query heads.
+int bwd_parts(int B, int Hkv, int R, int Nk, int sms)
+{
+    const long long items = static_cast<long long>(B) * Hkv * tiles_of(Nk);
+    long long parts = (3LL * sms + items - 1) / items;
+    if (parts > R) parts = R;
+    if (parts < 1) parts = 1;
+    const int heads = (R + static_cast<int>(parts) - 1) / static_cast<int>(parts);
+    return (R + heads - 1) / heads;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fa_fwd_rules_workspace_size(int B, int N)
+{
+    return B <= 0 || N <= 0 ? 0 : ranges_size(B, N);
+}
+
+fa_status fa_fwd_rules(const void* q, const void* k, const void* v, const float* slopes, const int* documents,
+                       const int* prefix_lens, void* o, float* lse, void* workspace, size_t ws_bytes, int B, int Hq, int Hkv,
+                       int N, int Nk, int d, int dv, int causal, float scale, float softcap, fa_dtype o_dtype, void* stream)
+{
+    const fa_status bad = check_rules(q, k, v, slopes, documents, prefix_lens, B, Hq, Hkv, N, Nk, d, dv, causal, scale, softcap);
+    if (bad != FA_OK) return bad;
+    if (o == nullptr || !dtype_ok(o_dtype) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(workspace, kAlign))
+        return FA_ERR_INVALID_ARG;
+    if (documents != nullptr && workspace == nullptr) return FA_ERR_INVALID_ARG;
+    if (!head_ok(d) || dv != d) return FA_ERR_UNSUPPORTED;
+    if (documents != nullptr && ws_bytes < fa_fwd_rules_workspace_size(B, N)) return FA_ERR_WORKSPACE;
+    fa::FwdRulesParams p{};
+    make_rules(&p.rules, scale, softcap, slopes);
+    fa::FwdParams& f = p.f;
+    if (!fa::bf16_tile_map(&f.tm_q, q, B * Hq, N, d) || !fa::bf16_tile_map(&f.tm_k, k, B * Hkv, Nk, d) ||
+        !fa::bf16_tile_map(&f.tm_v, v, B * Hkv, Nk, dv) || !fa::out_tile_map(&f.tm_o, o, B * Hq, N, dv, o_dtype, 32))
+        return FA_ERR_CUDA;
+    if (fa::device_status_word(&f.status) != cudaSuccess || fa::device_sm_count(&f.num_ctas) != cudaSuccess) return FA_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    f.o = o;
+    f.lse = lse;
+    f.BH = B * Hq;
+    f.N = N;
+    f.Nk = Nk;
+    f.n_qp = (tiles_of(N) + 1) / 2;
+    f.n_items = f.BH * f.n_qp;
+    f.wait_limit_ns = fa::wait_limit_ns();
+    f.n_splits = 1;
+    p.prefix = prefix_lens;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.causal = causal;
+    if (documents != nullptr) {
+        const Ranges r(static_cast<char*>(workspace), B, N);
+        const fa::RangesParams rp{documents, prefix_lens, r.each, r.tile, r.counter, f.status, B, N, Nk, tiles_of(N), causal};
+        if (fa::launch_rules_ranges(rp, false, st) != cudaSuccess) return FA_ERR_CUDA;
+        p.each = r.each;
+        p.tile = r.tile;
+        p.counter = r.counter;
+    }
+    const cudaError_t e = d == 32   ? fa::launch_fwd_rules_32(p, o_dtype, st)
+                          : d == 64 ? fa::launch_fwd_rules_64(p, o_dtype, st)
+                                    : fa::launch_fwd_rules_128(p, o_dtype, st);
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+size_t fa_bwd_rules_workspace_size(int B, int Hq, int Hkv, int N, int Nk, int d, int num_sms)
+{
+    if (B <= 0 || Hq <= 0 || Hkv <= 0 || N <= 0 || Nk <= 0 || d <= 0 || num_sms <= 0 || Hq % Hkv != 0) return 0;
+    const int parts = bwd_parts(B, Hkv, Hq / Hkv, Nk, num_sms);
+    const size_t sums = parts > 1 ? 2 * round_up(static_cast<size_t>(parts) * B * Hkv * Nk * d * sizeof(float), kAlign) : 0;
+    return fa_bwd_workspace_size(B, Hq, N, d) + ranges_size(B, Nk) + sums;
+}
+
+fa_status fa_bwd_rules(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* grad_o,
+                       const float* slopes, const int* documents, const int* prefix_lens, void* grad_q, void* grad_k,
+                       void* grad_v, void* workspace, size_t ws_bytes, int B, int Hq, int Hkv, int N, int Nk, int d, int dv,
+                       int causal, float scale, float softcap, fa_dtype o_dtype, fa_dtype grad_dtype, void* stream)
+{
+    const fa_status bad = check_rules(q, k, v, slopes, documents, prefix_lens, B, Hq, Hkv, N, Nk, d, dv, causal, scale, softcap);
+    if (bad != FA_OK) return bad;
+    if (o == nullptr || lse == nullptr || grad_o == nullptr || grad_q == nullptr || grad_k == nullptr || grad_v == nullptr ||
+        workspace == nullptr || !dtype_ok(o_dtype) || !dtype_ok(grad_dtype))
+        return FA_ERR_INVALID_ARG;
+    if (!aligned(o, 16) || !aligned(lse, 4) || !aligned(grad_o, 16) || !aligned(grad_q, 16) || !aligned(grad_k, 16) ||
+        !aligned(grad_v, 16) || !aligned(workspace, kAlign))
+        return FA_ERR_INVALID_ARG;
+    if (!head_ok(d) || dv != d) return FA_ERR_UNSUPPORTED;
+    fa::BwdRulesParams p{};
+    make_rules(&p.rules, scale, softcap, slopes);
+    fa::BwdParams& b = p.b;
+    if (fa::device_status_word(&b.status) != cudaSuccess || fa::device_sm_count(&b.num_ctas) != cudaSuccess) return FA_ERR_CUDA;
+    if (ws_bytes < fa_bwd_rules_workspace_size(B, Hq, Hkv, N, Nk, d, b.num_ctas)) return FA_ERR_WORKSPACE;
+    const int R = Hq / Hkv, Tr = tiles_of(N), Tc = tiles_of(Nk);
+    const int parts = bwd_parts(B, Hkv, R, Nk, b.num_ctas);
+    // workspace: fa_bwd's (dQ accumulator, log-sum-exps, row terms), the documents' ranges, the parts' sums
+    char* ws = static_cast<char*>(workspace);
+    const size_t rows = static_cast<size_t>(B) * Hq * Tr * fa::kBlockM;
+    float* dq_acc = reinterpret_cast<float*>(ws);
+    float* lse2 = reinterpret_cast<float*>(ws + round_up(rows * d * sizeof(float), kAlign));
+    float* dsc = reinterpret_cast<float*>(reinterpret_cast<char*>(lse2) + round_up(rows * sizeof(float), kAlign));
+    ws += fa_bwd_workspace_size(B, Hq, N, d);
+    const Ranges r(ws, B, Nk);
+    ws += ranges_size(B, Nk);
+    const size_t n_sum = static_cast<size_t>(B) * Hkv * Nk * d;
+    float* dk_part = reinterpret_cast<float*>(ws);
+    float* dv_part = reinterpret_cast<float*>(ws + round_up(parts * n_sum * sizeof(float), kAlign));
+    void* dk = parts > 1 ? static_cast<void*>(dk_part) : grad_k;
+    void* dv_ = parts > 1 ? static_cast<void*>(dv_part) : grad_v;
+    const fa_dtype kv_type = parts > 1 ? FA_F32 : grad_dtype;
+    if (static_cast<long long>(B) * Hkv * parts * Tc > 0x3fffffffLL) return FA_ERR_INVALID_ARG;
+    if (!fa::bf16_tile_map(&b.tm_q, q, B * Hq, N, d) || !fa::bf16_tile_map(&b.tm_k, k, B * Hkv, Nk, d) ||
+        !fa::bf16_tile_map(&b.tm_v, v, B * Hkv, Nk, dv) || !fa::bf16_tile_map(&b.tm_do, grad_o, B * Hq, N, dv) ||
+        !fa::out_tile_map(&b.tm_dk, dk, B * Hkv * parts, Nk, d, kv_type, fa::kBlockM) ||
+        !fa::out_tile_map(&b.tm_dv, dv_, B * Hkv * parts, Nk, dv, kv_type, fa::kBlockM))
+        return FA_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (documents != nullptr) {
+        const fa::RangesParams rp{documents, prefix_lens, r.each, r.tile, r.counter, b.status, B, N, Nk, Tc, causal};
+        if (fa::launch_rules_ranges(rp, true, st) != cudaSuccess) return FA_ERR_CUDA;
+        p.each = r.each;
+        p.tile = r.tile;
+    }
+    const fa::BwdPrepParams pp{o, grad_o, lse, lse2, dsc, dq_acc, B * Hq, N, Tr, d, scale, r.counter};
+    if (fa::launch_bwd_prep(pp, o_dtype, st) != cudaSuccess) return FA_ERR_CUDA;
+    b.lse2 = lse2;
+    b.dsc = dsc;
+    b.dq_acc = dq_acc;
+    b.dk = dk;
+    b.dv = dv_;
+    b.BH = B * Hq;
+    b.N = N;
+    b.Nk = Nk;
+    b.Tr = Tr;
+    b.Tc = Tc;
+    b.scale = scale;
+    b.wait_limit_ns = fa::wait_limit_ns();
+    p.prefix = prefix_lens;
+    p.counter = r.counter;
+    p.B = B;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.causal = causal;
+    p.parts = parts;
+    p.part_heads = (R + parts - 1) / parts;
+    p.n_items = B * Hkv * parts * Tc;
+    const cudaError_t e = d == 32   ? fa::launch_bwd_rules_32(p, kv_type, st)
+                          : d == 64 ? fa::launch_bwd_rules_64(p, kv_type, st)
+                                    : fa::launch_bwd_rules_128(p, kv_type, st);
+    if (e != cudaSuccess) return FA_ERR_CUDA;
+    const fa::BwdDqParams dp{dq_acc, grad_q, B * Hq, N, Tr, d};
+    if (fa::launch_bwd_dq(dp, grad_dtype, st) != cudaSuccess) return FA_ERR_CUDA;
+    if (parts > 1) {
+        const fa::RulesSumParams sp{dk_part, dv_part, grad_k, grad_v, static_cast<long long>(n_sum), parts};
+        if (fa::launch_rules_sum(sp, grad_dtype, st) != cudaSuccess) return FA_ERR_CUDA;
+    }
+    return FA_OK;
+}
+
+}  // extern "C"

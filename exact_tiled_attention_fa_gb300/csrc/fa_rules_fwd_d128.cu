@@ -1,0 +1,9 @@
+// Forward under score rules, instances for head size 128 (bf16 / fp32 output).
+#include "fa_rules_fwd_kernel.cuh"
+
+namespace fa {
+cudaError_t launch_fwd_rules_128(const FwdRulesParams& p, fa_dtype o_dtype, cudaStream_t st)
+{
+    return launch_fwd_rules_d<128>(p, o_dtype, st);
+}
+}  // namespace fa

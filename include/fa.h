@@ -31,6 +31,10 @@
  *   fa_decode_tree      decode for a tree of drafted tokens over a cache (several queries for each
  *                       sequence, each seeing the cached tokens and its ancestors).
  *   fa_cache_compact    the accepted path of such a tree moved up behind the cached tokens.
+ *   fa_fwd_rules        fa_fwd with rules for its scores (a cap by tanh, a bias that falls with the
+ *                       distance) and for what a query sees (documents packed into a sequence, a
+ *                       prefix that all see), and with shared key/value heads;
+ *   fa_bwd_rules        its gradient.
  *
  * Conventions shared by every entry point:
  *   - All tensors are dense, row-major, last dimension contiguous, in the layouts
@@ -488,6 +492,83 @@ fa_status fa_decode_tree(const void* q, const void* k_cache, const void* v_cache
 fa_status fa_cache_compact(void* k_cache, void* v_cache, const int* seqlens, const int* accepted,
                            const int* n_accepted, int* seqlens_out, int L, int B, int Hkv,
                            int Nk_max, int d, int dv, int T, void* stream);
+
+/*
+ * Attention under score rules (fa_fwd_rules, fa_bwd_rules).  Query i of a sequence sits at position
+ * Nk - N + i, key j at position j, query head h reads key/value head g = h / (Hq / Hkv).
+ *   Scores:  x = scale * q_i . k_j;  softcap > 0: s = softcap * tanh(x / softcap), softcap = 0: s = x;
+ *            then, with slopes, s -= slopes[h] * |Nk - N + i - j|.
+ *   Masks:   with causal = 1, key j is hidden from query i if j > Nk - N + i, but for the keys j <
+ *            prefix_lens[b], which all queries of sequence b see.  With documents, query i and key j
+ *            see each other only in one document: a run of equal numbers documents[b][j] >= 0 along the
+ *            keys (a query is where its position is).  A number below 0 is padding, in no document; a
+ *            query there, or before position 0, sees nothing.  Two runs of the same number are two
+ *            documents.
+ *
+ *   slopes       fp32 [Hq]      (device; finite; NULL: no bias.  Distances are exact up to 2^24.)
+ *   documents    int32 [B, Nk]  (device; NULL: one document)
+ *   prefix_lens  int32 [B]      (device; NULL: 0.  Without causal it has no effect.  Values outside
+ *                [0, Nk] are clamped and recorded as FA_ERR_INVALID_ARG in the device status word.)
+ *
+ * A non-finite score of a hidden pair reaches nothing; a non-finite q, v or grad_o, or k in the gradient, may
+ * reach every row whose 128-row tile meets its own (its weight there is 0, and 0 times NaN is NaN), so rows of
+ * padding must be finite too.
+ */
+
+/* Bytes of workspace fa_fwd_rules needs with documents, 0 on invalid arguments.  Without documents it needs none. */
+size_t fa_fwd_rules_workspace_size(int B, int N);
+
+/*
+ * Exact attention forward under score rules:
+ *   O[b,h,i,:] = sum_j softmax_j(s_ij) V[b,g,j,:],  lse[b,h,i] = log sum_j exp(s_ij)
+ * over the keys j that query i sees; O = 0 and lse = -inf where there are none.  Without rules it is
+ * fa_fwd.  Weights are rounded to bf16 for the product with V, also where O is fp32; lse sums them unrounded.
+ *
+ *   q          bf16 [B, Hq, N, d]        (device)
+ *   k, v       bf16 [B, Hkv, Nk, d]      (device)
+ *   o          o_dtype [B, Hq, N, d]     (device, written)
+ *   lse        fp32 [B, Hq, N]           (device, written; may be NULL)
+ *   workspace  with documents: ws_bytes >= fa_fwd_rules_workspace_size(B, N), 256-byte aligned; its
+ *              contents on entry do not matter.  Calls sharing a workspace must not overlap on the GPU.
+ *              Without documents it may be NULL.
+ *   Hkv dividing Hq; d = dv in {32, 64, 128}; scale > 0, softcap >= 0, both finite.
+ * The result is the same from run to run.
+ */
+fa_status fa_fwd_rules(const void* q, const void* k, const void* v, const float* slopes,
+                       const int* documents, const int* prefix_lens, void* o, float* lse,
+                       void* workspace, size_t ws_bytes, int B, int Hq, int Hkv, int N, int Nk, int d,
+                       int dv, int causal, float scale, float softcap, fa_dtype o_dtype, void* stream);
+
+/*
+ * Bytes of workspace fa_bwd_rules needs on a device with `num_sms` multiprocessors: fa_bwd's, room for
+ * the documents' intervals, and, where key/value heads are few, fp32 sums of dK and dV for parts of
+ * their query heads.  Pure host function.  0 on invalid arguments.
+ */
+size_t fa_bwd_rules_workspace_size(int B, int Hq, int Hkv, int N, int Nk, int d, int num_sms);
+
+/*
+ * Gradient of fa_fwd_rules.  With P_ij = exp(s_ij - lse_i) for pairs that see each other and D_i =
+ * dO_i . O_i:
+ *   dV = P^T dO,  dX_ij = P_ij (dO_i . V_j - D_i) scale (1 - tanh^2(x_ij / softcap)),
+ *   dQ = dX K,  dK = dX^T Q,
+ * dK and dV added up over the query heads of a key/value head.  The slopes are constants.
+ *
+ *   q, k, v, o, lse, rules  as given to and returned by the forward, with the same scale and softcap
+ *   grad_o     bf16 [B, Hq, N, d]        (device)
+ *   grad_q     grad_dtype [B, Hq, N, d], grad_k, grad_v grad_dtype [B, Hkv, Nk, d]  (device, every
+ *              element written)
+ *   workspace  ws_bytes >= fa_bwd_rules_workspace_size(B, Hq, Hkv, N, Nk, d, <SMs of the current
+ *              device>), 256-byte aligned; its contents on entry do not matter.  Calls sharing a
+ *              workspace must not overlap on the GPU.
+ * P and dX are rounded to bf16 for the products, as in fa_bwd.  grad_q's sums run in whatever order
+ * the key tiles come to it, so that it can differ in its last bits from run to run; grad_k and grad_v are
+ * summed in a fixed order.  Returns FA_ERR_WORKSPACE if ws_bytes is too small (nothing launched).
+ */
+fa_status fa_bwd_rules(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                       const void* grad_o, const float* slopes, const int* documents,
+                       const int* prefix_lens, void* grad_q, void* grad_k, void* grad_v, void* workspace,
+                       size_t ws_bytes, int B, int Hq, int Hkv, int N, int Nk, int d, int dv, int causal,
+                       float scale, float softcap, fa_dtype o_dtype, fa_dtype grad_dtype, void* stream);
 
 /*
  * Synchronises `stream`, then returns and clears the device status word of the current
