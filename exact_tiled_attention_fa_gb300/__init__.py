@@ -21,8 +21,9 @@ Entry points (same names as the C ABI, without the ``fa_`` prefix):
   fwd_rules        the forward with rules for its scores (cap by tanh, distance bias), masks (documents, prefix)
                    and shared key/value heads
   bwd_rules        its gradient
+  decode_prefix    single-query decode behind a prefix that the whole batch shares, under the same score rules
   decode_default_splits, decode_gqa_default_splits, decode_workspace_size, fwd_rules_workspace_size,
-  bwd_rules_workspace_size,
+  bwd_rules_workspace_size, decode_prefix_workspace_size,
   decode_tree_workspace_size, qk_norm_rope_bwd_workspace_size, get_device_error,
   set_wait_timeout_ns, status_string
 """
@@ -110,6 +111,10 @@ def _load():
     lib.fa_bwd_rules_workspace_size.restype = sz
     lib.fa_bwd_rules.argtypes = [vp] * 13 + [sz] + [i] * 8 + [f, f, i, i, vp]
     lib.fa_bwd_rules.restype = i
+    lib.fa_decode_prefix_workspace_size.argtypes = [i] * 5
+    lib.fa_decode_prefix_workspace_size.restype = sz
+    lib.fa_decode_prefix.argtypes = [vp] * 11 + [sz] + [i] * 7 + [f, f, i, vp]
+    lib.fa_decode_prefix.restype = i
     lib.fa_get_device_error.argtypes = [vp]
     lib.fa_get_device_error.restype = i
     lib.fa_set_wait_timeout_ns.argtypes = [ull]
@@ -637,6 +642,29 @@ def bwd_rules(q, k, v, o, lse, do, causal=False, scale=None, softcap=0.0, slopes
                                           _odt(out_dtype), dq, dk, dv, workspace, sms)
     if type(r) is int:
         raise FaError(r, "fa_bwd_rules")
+    return r
+
+
+def decode_prefix_workspace_size(B, Hq, Hkv, d, num_sms):
+    return int(_load().fa_decode_prefix_workspace_size(B, Hq, Hkv, d, num_sms))
+
+
+def decode_prefix(q, k_prefix, v_prefix, k_cache, v_cache, seqlens, prefix_len=None, scale=None, softcap=0.0, slopes=None,
+                  out_dtype=torch.bfloat16, out=None, lse=None, workspace=None, return_lse=True):
+    """Single-query decode of a batch whose sequences begin with the same tokens: their keys and values are held, and read,
+    once.  q [B,Hq,1,d], k_prefix, v_prefix [Hkv,P,d] (both None: no prefix), caches [B,Hkv,Nk_max,d] with each
+    sequence's own tokens, all bf16, Hkv dividing Hq into groups of at most 128; seqlens int32 [B] own tokens,
+    prefix_len int32 [1] how many of the P there are (None: all).
+
+    Sequence b sees the prefix and its own tokens, its query being the last of them; ``softcap`` and ``slopes`` are those of
+    ``fwd_rules``.  ``workspace`` is a uint8 CUDA tensor of at least ``decode_prefix_workspace_size`` bytes (allocated here
+    when omitted).  Rows behind the lengths may hold anything.  Returns (O [B,Hq,1,d], LSE fp32 [B,Hq,1] or None).
+    """
+    sms = num_sms(q.device) if workspace is None and isinstance(q, torch.Tensor) and q.is_cuda else 0
+    r = (_binding or _native()).decode_prefix(q, k_prefix, v_prefix, k_cache, v_cache, seqlens, prefix_len, scale, softcap, slopes,
+                                              _odt(out_dtype), out, lse, return_lse, workspace, sms)
+    if type(r) is int:
+        raise FaError(r, "fa_decode_prefix")
     return r
 
 

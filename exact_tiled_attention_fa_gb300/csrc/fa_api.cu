@@ -151,7 +151,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
 // unique across the process's devices, so the key needs no device).
 struct MapKey {
     const void* ptr;
-    int BH, rows, d, kind, box_rows;  // kind: 0 bf16 input, 1 bf16 output, 2 fp32 output
+    int BH, rows, d, kind, box_rows;  // kind: 0 bf16 input, 1 bf16 output, 2 fp32 output, 16 + R: make_group_map (rows: Hkv)
     bool operator==(const MapKey& o) const
     {
         return ptr == o.ptr && BH == o.BH && rows == o.rows && d == o.d && kind == o.kind && box_rows == o.box_rows;
@@ -244,6 +244,28 @@ bool encode_out_map(CUtensorMap* m, void* ptr, int BH, int rows, int d, fa_dtype
     return r == CUDA_SUCCESS;
 }
 
+// bf16 tensor [B][Hkv][R][d] as a 4-D tiled map with a {min(d,64), R, 1, seqs} box: the rows of one key/value head of
+// `seqs` sequences behind one another, swizzled as in encode_map.
+bool make_group_map(CUtensorMap* m, const void* ptr, int B, int Hkv, int R, int d, int seqs)
+{
+    const MapKey k{ptr, B, Hkv, d, 16 + R, seqs};
+    if (t_maps.find(k, m)) return true;
+    auto enc = encode_fn();
+    if (enc == nullptr) return false;
+    const int cb = d < 64 ? d : 64;
+    const cuuint64_t row = static_cast<cuuint64_t>(d) * 2;
+    cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(R), static_cast<cuuint64_t>(Hkv), static_cast<cuuint64_t>(B)};
+    cuuint64_t strides[3] = {row, row * R, row * R * Hkv};
+    cuuint32_t box[4] = {static_cast<cuuint32_t>(cb), static_cast<cuuint32_t>(R), 1, static_cast<cuuint32_t>(seqs)};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    if (enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            cb == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return false;
+    t_maps.put(k, *m);
+    return true;
+}
+
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 bool head_ok(int d) { return d == 32 || d == 64 || d == 128; }
 bool dtype_ok(fa_dtype t) { return t == FA_BF16 || t == FA_F32; }
@@ -259,6 +281,10 @@ cudaError_t device_status_word(int** out) { return status_word(out); }
 cudaError_t device_sm_count(int* out) { return sm_count(out); }
 unsigned long long wait_limit_ns() { return g_wait_ns.load(); }
 bool bf16_tile_map(CUtensorMap* m, const void* ptr, int BH, int rows, int d) { return make_map(m, ptr, BH, rows, d); }
+bool bf16_group_map(CUtensorMap* m, const void* ptr, int B, int Hkv, int R, int d, int seqs)
+{
+    return make_group_map(m, ptr, B, Hkv, R, d, seqs);
+}
 bool out_tile_map(CUtensorMap* m, void* ptr, int BH, int rows, int d, fa_dtype t, int box_rows)
 {
     return make_out_map(m, ptr, BH, rows, d, t, box_rows);

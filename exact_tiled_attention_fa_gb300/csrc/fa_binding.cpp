@@ -524,6 +524,57 @@ PyObject* bwd_rules(PyObject*, PyObject* const* a, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
+PyObject* decode_prefix(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    // q k_prefix v_prefix k_cache v_cache seqlens prefix_len scale softcap slopes out_f32 out lse return_lse workspace num_sms
+    expect(n, 16);
+    const Tensor& q = first(a[0], "q", 4, "[B, heads, 1, head_dim]");
+    const Tensor& k = first(a[3], "k_cache", 4, "[B, Hkv, Nk_max, head_dim]");
+    const int device = static_cast<int>(q.get_device());
+    const int64_t B = q.size(0), Hq = q.size(1), d = q.size(3), Hkv = k.size(1), Nk = k.size(2);
+    const std::array<int64_t, 4> qs{B, Hq, 1, d}, cs{B, Hkv, Nk, d};
+    void* qp = arg(a[0], "q", kBf16, device, qs);
+    void* kp = arg(a[3], "k_cache", kBf16, device, cs);
+    void* vp = arg(a[4], "v_cache", kBf16, device, cs);
+    void* lens = arg(a[5], "seqlens", kI32, device, {B});
+    int64_t P = 0;
+    void *kpre = nullptr, *vpre = nullptr, *plen = nullptr;
+    if (a[1] != Py_None) {
+        P = first(a[1], "k_prefix", 3, "[Hkv, prefix, head_dim]").size(1);
+        const std::array<int64_t, 3> ps{Hkv, P, d};
+        kpre = arg(a[1], "k_prefix", kBf16, device, ps);
+        vpre = arg(a[2], "v_prefix", kBf16, device, ps);
+        plen = optional_arg(a[6], "prefix_len", kI32, device, {1});
+    } else if (a[2] != Py_None || a[6] != Py_None) {
+        refuse("v_prefix and prefix_len go with k_prefix");
+    }
+    const double scale = a[7] == Py_None ? 1.0 / std::sqrt(static_cast<double>(d)) : number(a[7]);
+    void* slopes = optional_arg(a[9], "slopes", kF32, device, {Hq});
+    const at::ScalarType ot = a[11] != Py_None ? tensor(a[11], "out").scalar_type() : flag(a[10]) ? kF32 : kBf16;
+    const fa_dtype od = out_type(ot);
+    const Tensor out = output(a[11], q, ot, qs);
+    void* op = pointer_of(a[11], out, "out", ot, device, qs);
+    Tensor lse;
+    void* lp = nullptr;
+    const bool want = a[12] != Py_None || flag(a[13]);
+    if (want) {
+        lse = output(a[12], q, kF32, {B, Hq, 1});
+        lp = pointer_of(a[12], lse, "lse", kF32, device, {B, Hq, 1});
+    }
+    const size_t need = a[14] != Py_None ? 0
+                                         : fa_decode_prefix_workspace_size(as_int(B), as_int(Hq), as_int(Hkv), as_int(d), sm_count(a[15]));
+    const Space ws(a[14], q, device, need > 256 ? need : 256);
+    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(device));
+    const fa_status s = fa_decode_prefix(qp, kpre, vpre, static_cast<const int*>(plen), kp, vp, static_cast<const int*>(lens),
+                                         static_cast<const float*>(slopes), op, static_cast<float*>(lp), ws.ptr, ws.bytes, as_int(B),
+                                         as_int(Hq), as_int(Hkv), as_int(P), as_int(Nk), as_int(d), as_int(d),
+                                         static_cast<float>(scale), static_cast<float>(number(a[8])), od, stream(device));
+    if (s != FA_OK) return status_only(s);
+    return tuple({result(a[11], out), want ? result(a[12], lse) : result(Py_None, Tensor())});
+    END_HANDLE_TH_ERRORS
+}
+
 PyObject* cache_compact(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
     HANDLE_TH_ERRORS
@@ -568,6 +619,7 @@ PyMethodDef methods[] = {
     method<cache_compact>("cache_compact"),
     method<fwd_rules>("fwd_rules"),
     method<bwd_rules>("bwd_rules"),
+    method<decode_prefix>("decode_prefix"),
     {nullptr, nullptr, 0, nullptr},
 };
 

@@ -173,14 +173,6 @@ struct FwdCfg {
     static constexpr uint32_t kIdescO = idesc_bf16(kBlockM, D, true);
 };
 
-
-__device__ __forceinline__ float max3(float a, float b, float c)
-{
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-
 // Layout of a staged output tile: column blocks of 128-byte rows (64-byte rows for bf16 with
 // d = 32), 128 rows each, swizzled like the tensor map that stores them (the 16-byte chunk
 // index of row r XOR r mod 8 for 128-byte rows, XOR (r / 2) mod 4 for 64-byte rows), so that

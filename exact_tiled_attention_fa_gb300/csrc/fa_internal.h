@@ -177,7 +177,7 @@ constexpr int kTreeMaxShares = 320;  // of a call, and so parts of a unit
 // What the merge has to join: the unit that a share began and did not finish.
 struct TreeJoin {
     long long first_row;  // in the output
-    int rows, parts;      // parts = 0: none
+    int rows, parts;      // parts = 0: none.  (Decode behind a prefix: of each unit, rows is the share that begins it.)
 };
 
 struct TreeParams {
@@ -321,12 +321,52 @@ struct RulesSumParams {
 
 cudaError_t launch_rules_sum(const RulesSumParams& p, fa_dtype grad_dtype, cudaStream_t st);
 
+// Decode behind a shared prefix (fa_tree_kernel.cuh, SHARED).  Units are a key/value head's prefix with a block of the
+// batch's rows, and then a sequence's own keys with its R rows: either kind may be left to another launch.  Of the
+// tree's parameters rows, T, parents and n_nodes have no meaning, joins holds a record for each unit.
+struct PrefixParams : TreeParams {
+    CUtensorMap tm_q1;      // bf16 [B][Hkv][R][d], box {min(d,64), R, 1, 1}; tm_q: box {min(d,64), R, 1, seqs}
+    CUtensorMap tm_kp;      // bf16 [Hkv][P_max][d]
+    CUtensorMap tm_vp;      // bf16 [Hkv][P_max][d]
+    const int* prefix_len;  // int32 [1] or nullptr (P_max)
+    ScoreRules rules;
+    int P_max, R;
+    int seqs;               // sequences of a query tile of the prefix: min(B, 128 / R)
+    int n_pre;              // prefix units of this launch, Hkv * n_qp or 0
+    int n_seq;              // sequences of this launch, B or 0
+    int rows_all;           // B * R
+    // where whole units go, fp32: prefix ones [Hkv][B * R] rows, others [B][Hkv][R] rows (or, as they are, to o and
+    // lse where there is no prefix: o_own = nullptr)
+    float *o_pre, *lse_pre, *o_own, *lse_own;
+};
+
+// Joins what prefix and own keys gave each row.
+struct PrefixSide {
+    const TreeJoin* units;  // {-, first share, parts}
+    const float *o_part, *lse_part, *o_whole, *lse_whole;
+    int part_rows;
+};
+struct PrefixMergeParams {
+    PrefixSide pre, own;  // pre.units = nullptr: no prefix
+    void* o;
+    float* lse;
+    int B, Hkv, R, seqs, pair, n_qp;
+    fa_dtype o_dtype;
+};
+
+cudaError_t launch_prefix_32(const PrefixParams& p, cudaStream_t st);
+cudaError_t launch_prefix_64(const PrefixParams& p, cudaStream_t st);
+cudaError_t launch_prefix_128(const PrefixParams& p, cudaStream_t st);
+cudaError_t launch_prefix_merge(const PrefixMergeParams& p, int d, cudaStream_t st);
+
 // Host helpers of the C ABI files (fa_api.cu).
 cudaError_t device_status_word(int** out);  // the current device's status word
 cudaError_t device_sm_count(int* out);
 unsigned long long wait_limit_ns();
 // Tensor map of a bf16 tensor [BH][rows][d] with 128-row boxes, from the thread's cache when possible.
 bool bf16_tile_map(CUtensorMap* m, const void* ptr, int BH, int rows, int d);
+// Tensor map of q [B][Hkv][R][d] whose box is the R rows of one key/value head of `seqs` sequences, the same way.
+bool bf16_group_map(CUtensorMap* m, const void* ptr, int B, int Hkv, int R, int d, int seqs);
 // Tensor map of an output [BH][rows][d] for bulk stores of box_rows rows (encode_out_map), the same way.
 bool out_tile_map(CUtensorMap* m, void* ptr, int BH, int rows, int d, fa_dtype t, int box_rows);
 

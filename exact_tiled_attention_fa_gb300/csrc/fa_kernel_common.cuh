@@ -17,6 +17,13 @@ __device__ __forceinline__ void record_failure(int* status, volatile int* abort_
     atomicCAS(status, 0, code);
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 template <typename OutT>
 __device__ __forceinline__ void store_row32(OutT* dst, const float (&v)[32]);
 

@@ -1,0 +1,6 @@
+// Decode behind a shared prefix (fa_tree_kernel, SHARED), head size 64.
+#include "fa_tree_kernel.cuh"
+
+namespace fa {
+cudaError_t launch_prefix_64(const PrefixParams& p, cudaStream_t st) { return launch_prefix_d<64>(p, st); }
+}  // namespace fa

@@ -260,3 +260,169 @@ fa_status fa_bwd_rules(const void* q, const void* k, const void* v, const void* 
 }
 
 }  // extern "C"
+
+namespace {
+
+// How a call of fa_decode_prefix is divided and where its workspace holds what.
+struct PrefixPlan {
+    int R, seqs;      // rows of a group, sequences of a query tile of the prefix
+    bool pair;        // more rows than a tile: the prefix in a launch of its own, 256 rows to a unit
+    int n_qp, ctas;
+    int part_pre, part_own;    // rows of a slot
+    size_t slots_pre, slots_own;
+    size_t o_pre, lse_pre, o_own, lse_own, whole, whole_lse, joins, total;  // offsets; whole: two of each
+    int units_pre, units_own;
+    PrefixPlan(int B, int Hq, int Hkv, int d, int sms)
+    {
+        R = Hq / Hkv;
+        seqs = fa::kBlockM / R < B ? fa::kBlockM / R : B;
+        pair = B > seqs;
+        n_qp = pair ? (B + 2 * seqs - 1) / (2 * seqs) : 1;
+        ctas = sms < fa::kTreeMaxShares / 2 ? sms : fa::kTreeMaxShares / 2;
+        part_pre = pair ? 2 * fa::kBlockM : seqs * R;
+        part_own = pair ? R : seqs * R;
+        units_pre = Hkv * n_qp;
+        units_own = B * Hkv;
+        // two slots a share; a share for each CTA (PAIR) or at most two
+        slots_pre = pair ? 2 * static_cast<size_t>(ctas) * part_pre : 0;
+        slots_own = 4 * static_cast<size_t>(ctas) * part_own;
+        const size_t rows = static_cast<size_t>(B) * Hq, row = static_cast<size_t>(d) * sizeof(float);
+        size_t at = 0;
+        auto take = [&](size_t bytes) {
+            const size_t x = at;
+            at += round_up(bytes, kAlign);
+            return x;
+        };
+        o_pre = take(slots_pre * row);
+        lse_pre = take(slots_pre * sizeof(float));
+        o_own = take(slots_own * row);
+        lse_own = take(slots_own * sizeof(float));
+        whole = take(2 * rows * row);
+        whole_lse = take(2 * rows * sizeof(float));
+        joins = take((static_cast<size_t>(units_pre) + units_own) * sizeof(fa::TreeJoin));
+        total = at;
+    }
+};
+
+bool prefix_sizes_ok(int B, int Hq, int Hkv, int d)
+{
+    return B > 0 && Hq > 0 && Hkv > 0 && d > 0 && Hq % Hkv == 0 && static_cast<long long>(B) * Hq <= 0x3fffffffLL;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fa_decode_prefix_workspace_size(int B, int Hq, int Hkv, int d, int num_sms)
+{
+    if (!prefix_sizes_ok(B, Hq, Hkv, d) || num_sms <= 0 || Hq / Hkv > fa::kBlockM) return 0;
+    return PrefixPlan(B, Hq, Hkv, d, num_sms).total;
+}
+
+fa_status fa_decode_prefix(const void* q, const void* k_prefix, const void* v_prefix, const int* prefix_len, const void* k_cache,
+                           const void* v_cache, const int* seqlens_k, const float* slopes, void* o, float* lse, void* workspace,
+                           size_t ws_bytes, int B, int Hq, int Hkv, int P_max, int Nk_max, int d, int dv, float scale, float softcap,
+                           fa_dtype o_dtype, void* stream)
+{
+    if (q == nullptr || k_cache == nullptr || v_cache == nullptr || seqlens_k == nullptr || o == nullptr || workspace == nullptr)
+        return FA_ERR_INVALID_ARG;
+    // a prefix, or none
+    const bool pre = k_prefix != nullptr;
+    if (pre != (v_prefix != nullptr) || (pre ? P_max <= 0 : P_max != 0 || prefix_len != nullptr)) return FA_ERR_INVALID_ARG;
+    if (!prefix_sizes_ok(B, Hq, Hkv, d) || dv <= 0 || Nk_max <= 0 || !dtype_ok(o_dtype)) return FA_ERR_INVALID_ARG;
+    fa::ScoreRules rules;
+    if (!make_rules(&rules, scale, softcap, slopes)) return FA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k_prefix, 16) || !aligned(v_prefix, 16) || !aligned(prefix_len, 4) || !aligned(k_cache, 16) ||
+        !aligned(v_cache, 16) || !aligned(seqlens_k, 4) || !aligned(slopes, 4) || !aligned(o, 16) || !aligned(lse, 4) ||
+        !aligned(workspace, kAlign))
+        return FA_ERR_INVALID_ARG;
+    if (P_max > 0x3fffff00 || Nk_max > 0x3fffff00) return FA_ERR_INVALID_ARG;  // positions behind both are 32-bit
+    if (!head_ok(d) || dv != d || Hq / Hkv > fa::kBlockM) return FA_ERR_UNSUPPORTED;
+    int sms = 0;
+    if (fa::device_sm_count(&sms) != cudaSuccess) return FA_ERR_CUDA;
+    const PrefixPlan plan(B, Hq, Hkv, d, sms);
+    if (ws_bytes < plan.total) return FA_ERR_WORKSPACE;
+    char* ws = static_cast<char*>(workspace);
+    auto at = [&](size_t off) { return reinterpret_cast<float*>(ws + off); };
+    const size_t rows = static_cast<size_t>(B) * Hq;
+    fa::PrefixParams p{};
+    if (!fa::bf16_group_map(&p.tm_q1, q, B, Hkv, plan.R, d, 1) || !fa::bf16_tile_map(&p.tm_k, k_cache, B * Hkv, Nk_max, d) ||
+        !fa::bf16_tile_map(&p.tm_v, v_cache, B * Hkv, Nk_max, dv))
+        return FA_ERR_CUDA;
+    if (pre && (!fa::bf16_group_map(&p.tm_q, q, B, Hkv, plan.R, d, plan.seqs) || !fa::bf16_tile_map(&p.tm_kp, k_prefix, Hkv, P_max, d) ||
+                !fa::bf16_tile_map(&p.tm_vp, v_prefix, Hkv, P_max, dv)))
+        return FA_ERR_CUDA;
+    if (fa::device_status_word(&p.status) != cudaSuccess) return FA_ERR_CUDA;
+    p.seqlens = seqlens_k;
+    p.o = o;
+    p.lse = lse;
+    p.B = B;
+    p.Hkv = Hkv;
+    p.rows = plan.R;
+    p.T = 1;
+    p.Nk_max = Nk_max;
+    p.num_ctas = plan.ctas;
+    p.o_dtype = o_dtype;
+    p.wait_limit_ns = fa::wait_limit_ns();
+    p.prefix_len = prefix_len;
+    p.rules = rules;
+    p.P_max = P_max;
+    p.R = plan.R;
+    p.seqs = plan.seqs;
+    p.rows_all = B * plan.R;
+    p.scale_log2 = rules.mult;
+    p.o_pre = at(plan.whole);
+    p.lse_pre = at(plan.whole_lse);
+    p.o_own = pre ? p.o_pre + rows * d : nullptr;
+    p.lse_own = pre ? p.lse_pre + rows : nullptr;
+    fa::TreeJoin* joins = reinterpret_cast<fa::TreeJoin*>(ws + plan.joins);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    auto launch = [&] {
+        return d == 32 ? fa::launch_prefix_32(p, st) : d == 64 ? fa::launch_prefix_64(p, st) : fa::launch_prefix_128(p, st);
+    };
+    if (pre && plan.pair) {
+        p.joins = joins;
+        p.o_part = at(plan.o_pre);
+        p.lse_part = at(plan.lse_pre);
+        p.part_rows = plan.part_pre;
+        p.n_qp = plan.n_qp;
+        p.num_shares = plan.ctas;
+        p.unit_cost = 3;
+        p.n_pre = plan.units_pre;
+        p.n_seq = 0;
+        if (launch() != cudaSuccess) return FA_ERR_CUDA;
+    }
+    const bool both = pre && !plan.pair;  // the prefix's units in the same launch
+    p.joins = both ? joins : joins + plan.units_pre;
+    p.o_part = at(plan.o_own);
+    p.lse_part = at(plan.lse_own);
+    p.part_rows = both ? plan.part_own : plan.R;
+    p.n_qp = 1;
+    p.n_pre = both ? plan.units_pre : 0;
+    p.n_seq = B;
+    // which form: as fa_decode_tree
+    const long long units = static_cast<long long>(p.n_pre) + plan.units_own;
+    const bool solo = d < 128 ? 4 * units >= 3LL * plan.ctas
+                              : units >= 6LL * plan.ctas || (units >= 2LL * plan.ctas && Nk_max <= 1536 && P_max <= 1536);
+    p.num_shares = solo ? 2 * plan.ctas : plan.ctas;
+    p.unit_cost = solo ? 2 : 3;
+    if (launch() != cudaSuccess) return FA_ERR_CUDA;
+    fa::PrefixMergeParams m{};
+    m.own = fa::PrefixSide{joins + plan.units_pre, at(plan.o_own), at(plan.lse_own), p.o_own, p.lse_own, p.part_rows};
+    if (pre) {
+        m.pre = fa::PrefixSide{joins, at(plan.pair ? plan.o_pre : plan.o_own), at(plan.pair ? plan.lse_pre : plan.lse_own), p.o_pre,
+                               p.lse_pre, plan.part_pre};
+    }
+    m.o = o;
+    m.lse = lse;
+    m.B = B;
+    m.Hkv = Hkv;
+    m.R = plan.R;
+    m.seqs = plan.seqs;
+    m.pair = plan.pair ? 1 : 0;
+    m.n_qp = plan.n_qp;
+    m.o_dtype = o_dtype;
+    return fa::launch_prefix_merge(m, d, st) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -96,6 +96,24 @@ __device__ __forceinline__ void add_bias(float* s, float mult, float slope2, flo
     }
 }
 
+// The largest of N numbers (a multiple of 32), NaN left out.
+template <int N>
+__device__ __forceinline__ float max_of(const float* s)
+{
+    float m[N / 32];
+#pragma unroll
+    for (int q = 0; q < N / 32; ++q) {
+        const float* t = s + 32 * q;
+        float a = max3(t[0], t[1], t[2]);
+#pragma unroll
+        for (int c = 3; c < 31; c += 2) a = max3(a, t[c], t[c + 1]);
+        m[q] = fmaxf(a, t[31]);
+    }
+    if constexpr (N == 32) return m[0];
+    else if constexpr (N == 64) return fmaxf(m[0], m[1]);
+    else return max3(m[0], m[1], fmaxf(m[2], m[3]));
+}
+
 // Bits 0 .. n - 1 of a word (n is clamped to 0 .. 32).
 __device__ __forceinline__ uint32_t low_bits(int n)
 {

@@ -115,20 +115,6 @@ __device__ __forceinline__ void rules_mask(float* s, int lo, int hi)
     }
 }
 
-__device__ __forceinline__ float max_of_row(const float* s)
-{
-    float m[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const float* t = s + 32 * q;
-        float a = max3(t[0], t[1], t[2]);
-#pragma unroll
-        for (int c = 3; c < 31; c += 2) a = max3(a, t[c], t[c + 1]);
-        m[q] = fmaxf(a, t[31]);
-    }
-    return max3(m[0], m[1], fmaxf(m[2], m[3]));
-}
-
 template <int D, typename OutT>
 __global__ void __launch_bounds__(kFwdThreads, 1) fa_rules_fwd_kernel(const __grid_constant__ FwdRulesParams p)
 {
@@ -463,7 +449,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_rules_fwd_kernel(const __gr
                 }
                 const bool mask = !__all_sync(0xffffffffu, lo <= k0 && hi >= k0 + kBlockN);
                 if (mask) rules_mask(s, lo - k0, hi - k0);
-                if (cap || bias || mask) mrow = max_of_row(s);
+                if (cap || bias || mask) mrow = max_of<kBlockN>(s);
                 const float mt = mrow * mult;
                 const bool grow = mt > m_run;
                 float alpha = 1.f;

@@ -59,9 +59,11 @@
 
 #include <cuda_bf16.h>
 #include <cstdint>
+#include <type_traits>
 
 #include "fa_internal.h"
 #include "fa_kernel_common.cuh"
+#include "fa_rules_common.cuh"
 #include "ptx.cuh"
 
 namespace fa {
@@ -93,7 +95,7 @@ struct TreeSeg {
     int n;              // tiles; 0: the share is done
     int tile;           // the first one
     int prefix, nodes;  // of the sequence
-    int b, group, qp;
+    int b, group, qp;   // (SHARED: b < 0 a prefix unit, group its key/value head)
     int slot;           // of its part; -1: the unit is whole
 };
 // Records in the ring, 8 for the one stream of tiles (ALT, PAIR) or 4 for each of two (SOLO).  The producer
@@ -308,6 +310,107 @@ struct TreeWalk {
     __device__ __forceinline__ int slot(int share) const { return n == tiles ? -1 : 2 * share + (tile == 0 ? 1 : 0); }
 };
 
+// The same for the units of decode behind a shared prefix: key/value head by head the prefix with each block of the
+// batch's rows (b = -1), then each sequence's own keys.
+__device__ __forceinline__ TreeLen shared_prefix(const PrefixParams& p)
+{
+    return tree_clamp(p.prefix_len != nullptr ? *p.prefix_len : p.P_max, 0, 0, p.P_max, p.status);
+}
+__device__ __forceinline__ TreeLen shared_own(const PrefixParams& p, int b) { return tree_clamp(p.seqlens[b], 0, 0, p.Nk_max, p.status); }
+
+__device__ __forceinline__ TreeStart shared_locate(const PrefixParams& p, int c, int lane)
+{
+    const TreeLen pre = p.n_pre > 0 ? shared_prefix(p) : TreeLen{0, 0};
+    const int pre_places = pre.tiles() + p.unit_cost;
+    const long long pre_total = static_cast<long long>(p.n_pre) * pre_places;
+    TreeLen len{0, 0};  // the first 32 sequences'
+    if (lane < p.n_seq) len = shared_own(p, lane);
+    long long total = lane < p.n_seq ? len.tiles() + p.unit_cost : 0;
+    for (int b = 32 + lane; b < p.n_seq; b += 32) total += shared_own(p, b).tiles() + p.unit_cost;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    total = total * p.Hkv + pre_total;
+    const long long shares = p.num_shares < total ? p.num_shares : total;
+    TreeStart s{0, 0, total, shares, 0, 0, 0, 0, 0};
+    if (c >= shares) return s;
+    s.w0 = share_begin(c, total, shares);
+    s.w1 = share_begin(c + 1, total, shares);
+    if (s.w0 < pre_total) {
+        s.b = -1;
+        s.unit = static_cast<int>(s.w0 / pre_places);
+        s.at = static_cast<int>(s.w0 - static_cast<long long>(s.unit) * pre_places);
+        s.prefix = pre.prefix;
+        return s;
+    }
+    long long base = pre_total;
+    for (int b0 = 0; b0 < p.n_seq; b0 += 32) {
+        const int b = b0 + lane;
+        if (b0 > 0 && b < p.n_seq) len = shared_own(p, b);
+        const int places = b < p.n_seq ? len.tiles() + p.unit_cost : 0;
+        long long incl = static_cast<long long>(places) * p.Hkv;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += x;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, base + incl > s.w0);
+        if (past != 0u) {
+            const int j = __ffs(past) - 1;  // the first sequence that ends after w0
+            const int pj = __shfl_sync(0xffffffffu, places, j);
+            const long long in = s.w0 - (base + __shfl_sync(0xffffffffu, incl, j) - static_cast<long long>(pj) * p.Hkv);
+            s.b = b0 + j;
+            s.unit = static_cast<int>(in / pj);
+            s.at = static_cast<int>(in - static_cast<long long>(s.unit) * pj);
+            s.prefix = __shfl_sync(0xffffffffu, len.prefix, j);
+            return s;
+        }
+        base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    s.w1 = s.w0;
+    return s;
+}
+
+struct SharedWalk : TreeWalk {
+    __device__ __forceinline__ void begin(const PrefixParams& p, const TreeStart& s)
+    {
+        left = static_cast<int>(s.w1 - s.w0);
+        b = kvh = qp = tile = tiles = n = 0;
+        len = TreeLen{0, 0};
+        next_len = 0;
+        if (left == 0) return;
+        b = s.b;
+        kvh = b < 0 ? s.unit / p.n_qp : s.unit;
+        qp = b < 0 ? s.unit - kvh * p.n_qp : 0;
+        len = TreeLen{s.prefix, 0};
+        tiles = len.tiles();
+        ahead(p);
+        take(p, s.at);
+    }
+    __device__ __forceinline__ void next(const PrefixParams& p)
+    {
+        left -= used;
+        if (left == 0) return;
+        step(p);
+        take(p, 0);
+    }
+    __device__ __forceinline__ void step(const PrefixParams& p)
+    {
+        if (b < 0 && ++qp < p.n_qp) return;
+        qp = 0;
+        if (++kvh < p.Hkv) return;
+        kvh = 0;
+        ++b;
+        len = tree_clamp(next_len, 0, 0, p.Nk_max, p.status);
+        tiles = len.tiles();
+        ahead(p);
+    }
+    __device__ __forceinline__ void ahead(const PrefixParams& p)
+    {
+        if (p.n_seq > 0) next_len = p.seqlens[min(b + 1, p.n_seq - 1)];
+    }
+    __device__ __forceinline__ int group(const PrefixParams& p) const { return b < 0 ? kvh : b * p.Hkv + kvh; }
+};
+
 // Ancestors of each lane's node t (and t itself) as 128 bits; t < 0: none.  Whole warp: it holds the
 // parents, so that a step up is a shuffle instead of a load that waits for the one before it (with
 // loads a unit's start took about 3 us).
@@ -468,8 +571,13 @@ __device__ __forceinline__ void tree_scale(uint32_t (&o)[N], float alpha)
     }
 }
 
-template <int D, TreeForm FORM>
-__global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_constant__ TreeParams p)
+// SHARED: decode of one query a sequence behind a prefix that all sequences have in common, under score rules
+// (fa_decode_prefix).  The prefix is read once for a block of rows of many sequences, instead of once for each; rows of
+// a sequence's own keys are the R query heads of a group.  Every unit has its parts recorded, and whole ones go to
+// buffers of their own, for the merge to join a row's two sides.
+template <int D, TreeForm FORM, bool SHARED = false>
+__global__ void __launch_bounds__(kTrThreads, 1)
+    fa_tree_kernel(const __grid_constant__ std::conditional_t<SHARED, PrefixParams, TreeParams> p)
 {
     using C = TrCfg<D, FORM>;
     constexpr bool ALT = FORM == kAlt, SOLO = FORM == kSolo, PAIR = FORM == kPair;
@@ -525,7 +633,10 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
     grid_launch_dependents();  // the merge may begin launching (it waits for this grid)
     if (warp % 4 == 0 && warp / 4 < kStreams) {  // share `stream * CTAs + CTA`: few shares go to different SMs
         const int stream = warp / 4;
-        const TreeStart s = tree_locate(p, stream * static_cast<int>(gridDim.x) + blockIdx.x, lane);
+        const int c = stream * static_cast<int>(gridDim.x) + blockIdx.x;
+        TreeStart s;
+        if constexpr (SHARED) s = shared_locate(p, c, lane);
+        else s = tree_locate(p, c, lane);
         if (lane == 0) *reinterpret_cast<TreeStart*>(reinterpret_cast<uint8_t*>(start_slot) + 64 * stream) = s;
     }
     tc_fence_before_sync();
@@ -550,16 +661,26 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
         if (stream < kStreams) {
             // ======================================================== producer
             if (lane == 0) {
-                prefetch_tensormap(&p.tm_q);
+                if constexpr (SHARED) {
+                    prefetch_tensormap(&p.tm_q1);
+                    if (p.n_pre > 0) {
+                        prefetch_tensormap(&p.tm_q);
+                        prefetch_tensormap(&p.tm_kp);
+                        prefetch_tensormap(&p.tm_vp);
+                    }
+                } else {
+                    prefetch_tensormap(&p.tm_q);
+                }
                 prefetch_tensormap(&p.tm_k);
                 prefetch_tensormap(&p.tm_v);
                 // K and V are read again only by a group's further query blocks
-                const uint64_t pol_kv = p.n_qp > 1 ? policy_evict_last() : policy_evict_first();
+                const uint64_t pol_kv = p.n_qp > 1 ? policy_evict_last() : policy_evict_first();  // (SHARED: the prefix's)
+                const uint64_t pol_own = SHARED ? policy_evict_first() : pol_kv;
                 const uint64_t pol_q = policy_evict_first();
                 const TreeStart start = *reinterpret_cast<TreeStart*>(reinterpret_cast<uint8_t*>(start_slot) + 64 * stream);
                 const int share = stream * static_cast<int>(gridDim.x) + blockIdx.x;
                 const int stage0 = stream * S;
-                TreeWalk kw, vw;  // K runs one tile ahead of V
+                std::conditional_t<SHARED, SharedWalk, TreeWalk> kw, vw;  // K runs one tile ahead of V
                 kw.begin(p, start);
                 vw.begin(p, start);
                 int kj = 0, vj = 0;  // tile within the segment
@@ -576,7 +697,14 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                     x.group = kw.group(p);
                     x.qp = kw.qp;
                     x.slot = kw.slot(share);
-                    if (n > 0 && x.slot >= 0 && kw.tile == 0) {
+                    if constexpr (SHARED) {
+                        if (n > 0 && kw.tile == 0) {  // begun here: the merge is told where to find it
+                            const long long last = start.w1 + (kw.tiles - kw.n);
+                            const int unit = kw.b < 0 ? kw.kvh * p.n_qp + kw.qp : p.n_pre + x.group;
+                            p.joins[unit] = TreeJoin{
+                                0, share, x.slot < 0 ? 1 : static_cast<int>((last * start.shares - 1) / start.total) - share + 1};
+                        }
+                    } else if (n > 0 && x.slot >= 0 && kw.tile == 0) {
                         // begun here, finished in the share of its last place
                         const long long last = start.w1 + (kw.tiles - kw.n);
                         join.first_row = static_cast<long long>(x.group) * p.rows + static_cast<long long>(kw.qp) * p.part_rows;
@@ -595,13 +723,27 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                         const int use = ALT ? segs >> 1 : segs;
                         if (use > 0 && !mbar_wait(bar(kTbQEmpty + buf), static_cast<uint32_t>(use - 1) & 1, limit, abort_flag))
                             return false;
-                        const int row0 = kw.qp * (PAIR ? 2 : 1) * kBlockM;
-                        const int q_tiles = PAIR && p.rows - row0 > kBlockM ? 2 : 1;
-                        mbar_arrive_expect_tx(bar(kTbQFull + buf), q_tiles * C::kTileBytes);
-                        for (int i = 0; i < q_tiles; ++i)
-                            for (int cb = 0; cb < C::kNumCB; ++cb)
-                                tma_load_3d(sbase + C::kOffQ + (buf + i) * C::kTileBytes + cb * C::kBlkBytes, &p.tm_q,
-                                            bar(kTbQFull + buf), cb * C::kCB, row0 + i * kBlockM, g, pol_q);
+                        if constexpr (SHARED) {
+                            // rows of `seqs` sequences for the prefix, of one otherwise; a box past the last sequence is filled
+                            // with zeros
+                            const bool pre = kw.b < 0;
+                            const int seq0 = pre ? kw.qp * (PAIR ? 2 : 1) * p.seqs : kw.b;
+                            const int q_tiles = PAIR && pre && seq0 + p.seqs < p.B ? 2 : 1;
+                            const CUtensorMap* map = pre ? &p.tm_q : &p.tm_q1;
+                            mbar_arrive_expect_tx(bar(kTbQFull + buf), q_tiles * (pre ? p.seqs : 1) * p.R * C::kRowBytes * C::kNumCB);
+                            for (int i = 0; i < q_tiles; ++i)
+                                for (int cb = 0; cb < C::kNumCB; ++cb)
+                                    tma_load_4d(sbase + C::kOffQ + (buf + i) * C::kTileBytes + cb * C::kBlkBytes, map,
+                                                bar(kTbQFull + buf), cb * C::kCB, 0, kw.kvh, seq0 + i * p.seqs, pol_q);
+                        } else {
+                            const int row0 = kw.qp * (PAIR ? 2 : 1) * kBlockM;
+                            const int q_tiles = PAIR && p.rows - row0 > kBlockM ? 2 : 1;
+                            mbar_arrive_expect_tx(bar(kTbQFull + buf), q_tiles * C::kTileBytes);
+                            for (int i = 0; i < q_tiles; ++i)
+                                for (int cb = 0; cb < C::kNumCB; ++cb)
+                                    tma_load_3d(sbase + C::kOffQ + (buf + i) * C::kTileBytes + cb * C::kBlkBytes, &p.tm_q,
+                                                bar(kTbQFull + buf), cb * C::kCB, row0 + i * kBlockM, g, pol_q);
+                        }
                         publish(kw.n);
                     }
                     const int s = stage0 + k_issued % S;
@@ -609,9 +751,11 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                         !mbar_wait(bar(kTbKEmpty + s), static_cast<uint32_t>(k_issued / S - 1) & 1, limit, abort_flag))
                         return false;
                     mbar_arrive_expect_tx(bar(kTbKFull + s), C::kTileBytes);
+                    const CUtensorMap* map = &p.tm_k;
+                    if constexpr (SHARED) map = kw.b < 0 ? &p.tm_kp : map;
                     for (int cb = 0; cb < C::kNumCB; ++cb)
-                        tma_load_3d(sbase + C::kOffK + s * C::kTileBytes + cb * C::kBlkBytes, &p.tm_k, bar(kTbKFull + s),
-                                    cb * C::kCB, (kw.tile + kj) * kBlockN, g, pol_kv);
+                        tma_load_3d(sbase + C::kOffK + s * C::kTileBytes + cb * C::kBlkBytes, map, bar(kTbKFull + s),
+                                    cb * C::kCB, (kw.tile + kj) * kBlockN, g, kw.b < 0 ? pol_kv : pol_own);
                     ++k_issued;
                     if (++kj == kw.n) {
                         kj = 0;
@@ -625,9 +769,11 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                         !mbar_wait(bar(kTbVEmpty + s), static_cast<uint32_t>(v_issued / S - 1) & 1, limit, abort_flag))
                         return false;
                     mbar_arrive_expect_tx(bar(kTbVFull + s), C::kTileBytes);
+                    const CUtensorMap* map = &p.tm_v;
+                    if constexpr (SHARED) map = vw.b < 0 ? &p.tm_vp : map;
                     for (int cb = 0; cb < C::kNumCB; ++cb)
-                        tma_load_3d(sbase + C::kOffV + s * C::kTileBytes + cb * C::kBlkBytes, &p.tm_v, bar(kTbVFull + s),
-                                    cb * C::kCB, (vw.tile + vj) * kBlockN, vw.group(p), pol_kv);
+                        tma_load_3d(sbase + C::kOffV + s * C::kTileBytes + cb * C::kBlkBytes, map, bar(kTbVFull + s),
+                                    cb * C::kCB, (vw.tile + vj) * kBlockN, vw.group(p), vw.b < 0 ? pol_kv : pol_own);
                     ++v_issued;
                     if (++vj == vw.n) {
                         vj = 0;
@@ -639,7 +785,7 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                 while (ok && vw.live()) ok = (!kw.live() || load_k()) && load_v();
                 const int loads = segs;  // query loads issued
                 if (ok) publish(0);
-                p.joins[share] = join;
+                if constexpr (!SHARED) p.joins[share] = join;
                 if (!ok && !*abort_flag) record_failure(p.status, abort_flag, FA_ERR_TIMEOUT);
                 // Every issued copy must land before the CTA may exit (its last phase per barrier).
                 if constexpr (ALT) {
@@ -715,7 +861,9 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                     // query barrier could take the phase before it for the one it needs.
                     ok = mbar_wait(bar(kTbQFull + q_buf), static_cast<uint32_t>(ALT ? segs >> 1 : segs) & 1, limit, abort_flag);
                     if (!ok) break;
-                    const bool rows = !PAIR || i == 0 || p.rows - w.qp * 2 * kBlockM > kBlockM;
+                    bool rows = true;
+                    if constexpr (PAIR && SHARED) rows = i == 0 || (w.b < 0 && (w.qp * 2 + 1) * p.seqs < p.B);
+                    else if constexpr (PAIR) rows = i == 0 || p.rows - w.qp * 2 * kBlockM > kBlockM;
                     if (!rows || j0 >= w.n) {
                         // (The queries first: the producer may be waiting to load the next unit's ahead of
                         // this unit's last V.)
@@ -806,7 +954,14 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
         const uint32_t t_s = tmem + lane_base + C::col_s(wg);
         const uint32_t t_o = tmem + lane_base + C::col_o(wg);
         const uint32_t t_p = tmem + lane_base + C::col_p(wg);
-        const float sl2 = p.scale_log2;
+        bool cap = false, bias = false;
+        float cap_in = 0.f, sl2 = p.scale_log2;  // sl2: of what the exponentials take
+        if constexpr (SHARED) {
+            cap_in = p.rules.cap_in;
+            cap = cap_in > 0.f;
+            bias = p.rules.slopes != nullptr;
+            sl2 = bias ? 1.f : p.rules.mult;
+        }
         int tiles = 0;                 // key tiles processed by this warpgroup
         int ready[2] = {0, 0};         // segments with tiles of warpgroup 0, 1 (ALT); this warpgroup's (else, [0])
         int segs = 0, k = 0;
@@ -821,8 +976,23 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
             const TreeSeg w = segment(my, segs, ok);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok || w.n == 0) break;
-            const int row0 = PAIR ? w.qp * 2 * kBlockM + wg * kBlockM : 0;
-            const int rows = min(p.rows - row0, kBlockM);  // rows of this warpgroup's tile (<= 0: none)
+            int row0, rows;  // rows of this warpgroup's tile (<= 0: none), its first row
+            float slope2 = 0.f;
+            int qpos = 0;  // SHARED: the row's position less that of the unit's first key
+            if constexpr (SHARED) {
+                const int seq0 = w.b < 0 ? (PAIR ? w.qp * 2 + wg : w.qp) * p.seqs : w.b;  // the tile's first sequence
+                row0 = w.b < 0 ? seq0 * p.R : 0;
+                rows = w.b < 0 ? min(p.seqs, p.B - seq0) * p.R : PAIR && wg > 0 ? 0 : p.R;
+                if (bias && r < rows) {
+                    const int j = r / p.R;
+                    const int kvh = w.b < 0 ? w.group : w.group - w.b * p.Hkv;
+                    slope2 = p.rules.slopes[kvh * p.R + (r - j * p.R)] * kLog2e;
+                    qpos = (w.b < 0 ? w.prefix + shared_own(p, seq0 + j).prefix : w.prefix) - 1;
+                }
+            } else {
+                row0 = PAIR ? w.qp * 2 * kBlockM + wg * kBlockM : 0;
+                rows = min(p.rows - row0, kBlockM);
+            }
             if (PAIR && rows <= 0) {
                 k += w.n;
                 ++segs;
@@ -833,13 +1003,27 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
             const int j0 = ALT ? (k + wg) & 1 : 0;  // first tile of the segment for this warpgroup
             const int end = w.prefix + w.nodes;     // keys of the sequence
             // the row's ancestors, kept while the sequence and the row stay the same
-            if ((w.tile + w.n) * kBlockN > w.prefix && (w.b != vis_b || (PAIR && w.qp != vis_qp))) {
+            if (!SHARED && (w.tile + w.n) * kBlockN > w.prefix && (w.b != vis_b || (PAIR && w.qp != vis_qp))) {
                 vis_b = w.b;
                 vis_qp = w.qp;
                 const int node = (row0 + r) % p.T;
                 tree_ancestors(p.parents != nullptr ? p.parents + static_cast<size_t>(w.b) * p.T : nullptr, p.T,
                                r < rows && node < w.nodes ? node : -1, lane, p.status, vis);
             }
+            // What the rules make of N scores of keys from k0 on: their largest (mx: as loaded, of absolute values under a
+            // cap; rows that are not there take no part in what the warp decides).
+            auto apply = [&](auto& x, float mx, int k0) -> float {
+                if constexpr (SHARED) {
+                    constexpr int N = sizeof(x) / sizeof(float);
+                    if (cap) {
+                        if (__all_sync(0xffffffffu, r >= rows || mx * cap_in <= kTanhRange)) tanh_small<N>(x, cap_in);
+                        else tanh_any<N>(x, cap_in);
+                    }
+                    if (bias) add_bias<N>(x, p.rules.mult, slope2, static_cast<float>(qpos - k0), 1);
+                    if (cap || bias) mx = max_of<N>(x);
+                }
+                return mx;
+            };
             TreeRow row;
             // V rows past the tree may hold anything: zero them before the product reads them.  (The stage's
             // tile before has been consumed, by the issuer that then issued this tile's scores, so the phase
@@ -869,16 +1053,27 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                         float mrow;
                         if constexpr (D == 128) {
                             float mh[2];
-                            tmem_ld64_max(t_s + 0, *reinterpret_cast<uint32_t(*)[64]>(&u[0]), mh[0]);
-                            tmem_ld64_max(t_s + 64, *reinterpret_cast<uint32_t(*)[64]>(&u[64]), mh[1]);
+                            if (SHARED && cap) {
+                                tmem_ld64_absmax(t_s + 0, *reinterpret_cast<uint32_t(*)[64]>(&u[0]), mh[0]);
+                                tmem_ld64_absmax(t_s + 64, *reinterpret_cast<uint32_t(*)[64]>(&u[64]), mh[1]);
+                            } else {
+                                tmem_ld64_max(t_s + 0, *reinterpret_cast<uint32_t(*)[64]>(&u[0]), mh[0]);
+                                tmem_ld64_max(t_s + 64, *reinterpret_cast<uint32_t(*)[64]>(&u[64]), mh[1]);
+                            }
                             tmem_ld_wait();
                             mrow = fmaxf(mh[0], mh[1]);
                         } else {
                             float mq[4];
-                            tmem_ld32_max(t_s + 0, *reinterpret_cast<uint32_t(*)[32]>(&u[0]), mq[0]);
-                            tmem_ld32_max(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(&u[32]), mq[1]);
-                            tmem_ld32_max(t_s + 64, *reinterpret_cast<uint32_t(*)[32]>(&u[64]), mq[2]);
-                            tmem_ld32_max(t_s + 96, *reinterpret_cast<uint32_t(*)[32]>(&u[96]), mq[3]);
+                            if (SHARED && cap) {
+#pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    tmem_ld32_absmax(t_s + 32u * q, *reinterpret_cast<uint32_t(*)[32]>(&u[32 * q]), mq[q]);
+                            } else {
+                                tmem_ld32_max(t_s + 0, *reinterpret_cast<uint32_t(*)[32]>(&u[0]), mq[0]);
+                                tmem_ld32_max(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(&u[32]), mq[1]);
+                                tmem_ld32_max(t_s + 64, *reinterpret_cast<uint32_t(*)[32]>(&u[64]), mq[2]);
+                                tmem_ld32_max(t_s + 96, *reinterpret_cast<uint32_t(*)[32]>(&u[96]), mq[3]);
+                            }
                             tmem_ld_wait();
                             mrow = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
                         }
@@ -889,7 +1084,9 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                         float s[kBlockN];
 #pragma unroll
                         for (int c = 0; c < kBlockN; ++c) s[c] = __uint_as_float(u[c]);
+                        mrow = apply(s, mrow, k0);
                         if (k0 + kBlockN > w.prefix) mrow = tree_mask(s, k0 - w.prefix, vis);  // drafted rows, or rows past them
+                        if (SHARED && r >= rows) mrow = -INFINITY;  // not a row: no reason to rescale
                         const bool rescale = __any_sync(0xffffffffu, row.grow(mrow, sl2)) && j > j0;
                         float2 rs[4] = {};
                         uint32_t pk[kBlockN / 2];
@@ -956,13 +1153,16 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
                         if (warp_live) {
                             uint32_t u[KS];
                             float mrow;
-                            tmem_ld64_max(t_s + KS * h, u, mrow);
+                            if (SHARED && cap) tmem_ld64_absmax(t_s + KS * h, u, mrow);
+                            else tmem_ld64_max(t_s + KS * h, u, mrow);
                             tmem_ld_wait();
                             float s[KS];
 #pragma unroll
                             for (int c = 0; c < KS; ++c) s[c] = __uint_as_float(u[c]);
+                            mrow = apply(s, mrow, k0 + KS * h);
                             const int shift = k0 + KS * h - w.prefix;
                             if (shift > -KS) mrow = tree_mask(s, shift, vis);  // drafted rows, or rows past them
+                            if (SHARED && r >= rows) mrow = -INFINITY;  // not a row: no reason to rescale
                             const bool grow = row.grow(mrow, sl2);
                             float2 rs[4] = {};
                             uint32_t pk[KS / 2];
@@ -1003,16 +1203,31 @@ __global__ void __launch_bounds__(kTrThreads, 1) fa_tree_kernel(const __grid_con
             if (!ok) break;
             // ---- end of the segment: its rows' output and log-sum-exp, final or to a slot
             const bool part = w.slot >= 0;
-            const bool shown = (row0 + r) % p.T < w.nodes;  // rows of nodes past the tree: O = 0, LSE = -inf
-            // first row of the warp in the output (or the slots)
-            const size_t first = part ? static_cast<size_t>(w.slot) * p.part_rows + (PAIR ? wg * kBlockM : 0) + 32 * (warp & 3)
-                                      : static_cast<size_t>(w.group) * p.rows + row0 + 32 * (warp & 3);
-            const RowsOut<D> out(stage, part ? static_cast<void*>(p.o_part) : p.o, part || p.o_dtype == FA_F32, first, rows_warp, lane);
-            auto store_lse = [&](float lse) {
-                if (lane < rows_warp) {
-                    if (part) p.lse_part[first + lane] = lse;
-                    else if (p.lse != nullptr) p.lse[first + lane] = lse;
+            bool shown = true;  // rows of nodes past the tree: O = 0, LSE = -inf
+            if constexpr (!SHARED) shown = (row0 + r) % p.T < w.nodes;
+            // first row of the warp in the output (or the slots), and those
+            size_t first = static_cast<size_t>(w.slot) * p.part_rows + (PAIR ? wg * kBlockM : 0) + 32 * (warp & 3);
+            void* o_to = p.o_part;
+            float* lse_to = p.lse_part;
+            bool f32 = true;
+            if (!part) {
+                o_to = p.o;
+                lse_to = p.lse;
+                f32 = p.o_dtype == FA_F32;
+                if constexpr (SHARED) {
+                    first = static_cast<size_t>(w.group) * (w.b < 0 ? p.rows_all : p.R) + row0 + 32 * (warp & 3);
+                    if (w.b < 0 || p.o_own != nullptr) {
+                        o_to = w.b < 0 ? p.o_pre : p.o_own;
+                        lse_to = w.b < 0 ? p.lse_pre : p.lse_own;
+                        f32 = true;
+                    }
+                } else {
+                    first = static_cast<size_t>(w.group) * p.rows + row0 + 32 * (warp & 3);
                 }
+            }
+            const RowsOut<D> out(stage, o_to, f32, first, rows_warp, lane);
+            auto store_lse = [&](float lse) {
+                if (lane < rows_warp && lse_to != nullptr) lse_to[first + lane] = lse;
             };
             if constexpr (!ALT) {
                 ok = __all_sync(0xffffffffu, mbar_wait(bar(kTbOReady + wg), ready[0] & 1, limit, abort_flag));
@@ -1259,11 +1474,11 @@ __global__ void __launch_bounds__(256) fa_tree_merge_kernel(const __grid_constan
     if (lane == 0 && p.lse != nullptr) p.lse[row] = live ? M + log2f(sum) * kLn2 : -INFINITY;
 }
 
-template <int D, TreeForm FORM>
-cudaError_t launch_tree_t(const TreeParams& p, cudaStream_t st)
+template <int D, TreeForm FORM, typename Params>
+cudaError_t launch_tree_main(const Params& p, cudaStream_t st)
 {
     using C = TrCfg<D, FORM>;
-    auto kern = fa_tree_kernel<D, FORM>;
+    auto kern = fa_tree_kernel<D, FORM, std::is_same_v<Params, PrefixParams>>;
     static bool configured[64] = {};  // attributes set and registers checked, per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1280,7 +1495,13 @@ cudaError_t launch_tree_t(const TreeParams& p, cudaStream_t st)
             return cudaErrorLaunchOutOfResources;
         configured[dev] = true;
     }
-    e = launch_pdl(kern, dim3(static_cast<unsigned>(p.num_ctas)), kTrThreads, C::kSmemBytes, st, p);
+    return launch_pdl(kern, dim3(static_cast<unsigned>(p.num_ctas)), kTrThreads, C::kSmemBytes, st, p);
+}
+
+template <int D, TreeForm FORM>
+cudaError_t launch_tree_t(const TreeParams& p, cudaStream_t st)
+{
+    const cudaError_t e = launch_tree_main<D, FORM>(p, st);
     if (e != cudaSuccess) return e;
     const dim3 grid(static_cast<unsigned>(p.num_shares), static_cast<unsigned>((p.part_rows + 7) / 8));
     return launch_pdl(fa_tree_merge_kernel<D>, grid, 256, 0, st, p);
@@ -1291,6 +1512,14 @@ cudaError_t launch_tree_d(const TreeParams& p, cudaStream_t st)
 {
     if (p.part_rows > kBlockM) return launch_tree_t<D, kPair>(p, st);
     return p.num_shares > p.num_ctas ? launch_tree_t<D, kSolo>(p, st) : launch_tree_t<D, kAlt>(p, st);
+}
+
+// Decode behind a prefix: PAIR only for launches of the prefix alone (a sequence's own rows are at most 128).
+template <int D>
+cudaError_t launch_prefix_d(const PrefixParams& p, cudaStream_t st)
+{
+    if (p.part_rows > kBlockM) return launch_tree_main<D, kPair>(p, st);
+    return p.num_shares > p.num_ctas ? launch_tree_main<D, kSolo>(p, st) : launch_tree_main<D, kAlt>(p, st);
 }
 
 }  // namespace fa

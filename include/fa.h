@@ -35,6 +35,8 @@
  *                       distance) and for what a query sees (documents packed into a sequence, a
  *                       prefix that all see), and with shared key/value heads;
  *   fa_bwd_rules        its gradient.
+ *   fa_decode_prefix    decode, one query a sequence, behind a prefix that the whole batch shares and that is
+ *                       read once for it, under the same rules for the scores.
  *
  * Conventions shared by every entry point:
  *   - All tensors are dense, row-major, last dimension contiguous, in the layouts
@@ -569,6 +571,41 @@ fa_status fa_bwd_rules(const void* q, const void* k, const void* v, const void* 
                        const int* prefix_lens, void* grad_q, void* grad_k, void* grad_v, void* workspace,
                        size_t ws_bytes, int B, int Hq, int Hkv, int N, int Nk, int d, int dv, int causal,
                        float scale, float softcap, fa_dtype o_dtype, fa_dtype grad_dtype, void* stream);
+
+/*
+ * Bytes of workspace fa_decode_prefix needs on a device with `num_sms` multiprocessors, whatever the
+ * lengths.  Pure host function.  0 on invalid arguments.
+ */
+size_t fa_decode_prefix_workspace_size(int B, int Hq, int Hkv, int d, int num_sms);
+
+/*
+ * Decode attention, one query a sequence, for a batch whose sequences begin with the same P tokens.  With
+ * n = seqlens_k[b] tokens of its own, sequence b's query sits at position P + n - 1 and sees the prefix's
+ * keys (positions 0 .. P - 1) and its own (P .. P + n - 1):
+ *   o[b,h,:] = sum_j softmax_j(s_j) V_j,  lse[b,h] = log sum_j exp(s_j),
+ * the scores as under score rules (above).  The prefix's keys and values are read once for the whole batch.
+ * The weights that multiply V are rounded to bf16, as in fa_decode_tree.
+ *
+ *   q          bf16 [B, Hq, 1, d]          (device)
+ *   k_prefix, v_prefix  bf16 [Hkv, P_max, d]  (device; both NULL with P_max = 0: no prefix)
+ *   prefix_len int32 [1]                   (device; P; NULL: P_max)
+ *   k_cache, v_cache  bf16 [B, Hkv, Nk_max, d]  (device)
+ *   seqlens_k  int32 [B]                   (device; lengths out of range, P too, are clamped and recorded as
+ *              FA_ERR_INVALID_ARG in the device status word.  With no key at all o = 0 and lse = -inf.)
+ *   slopes     fp32 [Hq] or NULL           (device)
+ *   o          o_dtype [B, Hq, 1, d]       (device, written)
+ *   lse        fp32 [B, Hq, 1]             (device, written; may be NULL)
+ *   workspace  ws_bytes >= fa_decode_prefix_workspace_size(B, Hq, Hkv, d, <SMs of the current device>),
+ *              256-byte aligned; its contents on entry do not matter.  Calls sharing a workspace must not
+ *              overlap on the GPU.
+ *   Hkv dividing Hq, Hq / Hkv <= 128 (else FA_ERR_UNSUPPORTED).
+ * Rows behind P or n are never used, whatever they hold.  The result is the same from run to run.
+ */
+fa_status fa_decode_prefix(const void* q, const void* k_prefix, const void* v_prefix,
+                           const int* prefix_len, const void* k_cache, const void* v_cache,
+                           const int* seqlens_k, const float* slopes, void* o, float* lse, void* workspace,
+                           size_t ws_bytes, int B, int Hq, int Hkv, int P_max, int Nk_max, int d, int dv,
+                           float scale, float softcap, fa_dtype o_dtype, void* stream);
 
 /*
  * Synchronises `stream`, then returns and clears the device status word of the current

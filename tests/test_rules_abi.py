@@ -120,3 +120,58 @@ def test_binding_refusals_on_the_device(lib):
     assert e.value.status == WORKSPACE
     with pytest.raises(ValueError, match="grads"):
         fa.bwd_rules(q, k, k, o, lse, q, grads=(torch.empty_like(q), None, None))
+
+
+def decode(lib):
+    return caller(lib.fa_decode_prefix, [(n, P) for n in ("q", "kp", "vp", "plen", "k", "v", "lens", "slopes", "o", "lse", "ws")] +
+                  [("ws_bytes", 1 << 40), ("B", 2), ("Hq", 4), ("Hkv", 2), ("P_max", 300), ("Nk", 64), ("d", 64), ("dv", 64),
+                   ("scale", 0.125), ("cap", 0.0), ("odt", 0), ("stream", NULL)])
+
+
+def test_decode_prefix_refusals(lib):
+    call = decode(lib)
+    for kw in (dict(q=NULL), dict(k=NULL), dict(v=NULL), dict(lens=NULL), dict(o=NULL), dict(ws=NULL), dict(kp=NULL), dict(vp=NULL),
+               dict(kp=NULL, vp=NULL), dict(kp=NULL, vp=NULL, P_max=0), dict(P_max=0), dict(P_max=-1), dict(q=ODD), dict(kp=ODD),
+               dict(vp=ODD), dict(k=ODD), dict(v=ODD), dict(o=ODD), dict(lse=ODD4), dict(plen=ODD4), dict(lens=ODD4), dict(slopes=ODD4),
+               dict(ws=ctypes.c_void_p(0x10000080)), dict(B=0), dict(Hq=0), dict(Hkv=3), dict(Hkv=0), dict(Nk=0), dict(d=0), dict(dv=0),
+               dict(scale=0.0), dict(cap=-1.0), dict(cap=float("nan")), dict(odt=2), dict(P_max=0x40000000), dict(Nk=0x40000000),
+               dict(B=1 << 16, Hq=1 << 16, Hkv=1 << 15)):
+        assert call(**kw) == INVALID, kw
+    for kw in (dict(d=96, dv=96), dict(dv=32), dict(Hq=258, Hkv=2)):
+        assert call(**kw) == UNSUPPORTED, kw
+
+
+def test_decode_prefix_workspace_size(lib):
+    up = lambda x: (x + 255) // 256 * 256  # noqa: E731
+    size = lib.fa_decode_prefix_workspace_size
+    # 16 sequences of 4 rows: one tile of 64
+    own = 4 * 152 * 64
+    assert size(16, 32, 8, 128, 152) == (up(own * 512) + up(own * 4) + up(2 * 16 * 32 * 512) + up(2 * 16 * 32 * 4) + up((8 + 128) * 16))
+    # 64 sequences of 4 rows: units of 256 for the prefix
+    pre, own = 2 * 152 * 256, 4 * 152 * 4
+    assert size(64, 32, 8, 64, 152) == (up(pre * 256) + up(pre * 4) + up(own * 256) + up(own * 4) + up(2 * 64 * 32 * 256) +
+                                        up(2 * 64 * 32 * 4) + up((8 + 512) * 16))
+    assert size(0, 4, 2, 64, 152) == 0 and size(1, 3, 2, 64, 152) == 0 and size(1, 4, 2, 64, 0) == 0 and size(1, 258, 2, 64, 152) == 0
+
+
+@pytest.mark.gpu
+def test_decode_prefix_binding_refusals(lib):
+    z = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    q, kp, k = z(2, 4, 1, 64), z(2, 30, 64), z(2, 2, 40, 64)
+    n = torch.ones(2, dtype=torch.int32, device="cuda")
+    fa.decode_prefix(q, kp, kp, k, k, n)
+    with pytest.raises(ValueError, match="q must be"):
+        fa.decode_prefix(z(2, 4, 2, 64), kp, kp, k, k, n)
+    with pytest.raises(ValueError, match="v_prefix"):
+        fa.decode_prefix(q, kp, kp[:, :29].contiguous(), k, k, n)
+    with pytest.raises(ValueError, match="go with"):
+        fa.decode_prefix(q, None, kp, k, k, n)
+    with pytest.raises(ValueError, match="go with"):
+        fa.decode_prefix(q, None, None, k, k, n, prefix_len=n[:1])
+    with pytest.raises(ValueError, match="prefix_len"):
+        fa.decode_prefix(q, kp, kp, k, k, n, prefix_len=n)
+    with pytest.raises(ValueError, match="seqlens"):
+        fa.decode_prefix(q, kp, kp, k, k, n.long())
+    with pytest.raises(fa.FaError) as e:
+        fa.decode_prefix(q, kp, kp, k, k, n, workspace=torch.empty(1024, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == WORKSPACE
