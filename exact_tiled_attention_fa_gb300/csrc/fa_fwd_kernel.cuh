@@ -186,19 +186,21 @@ struct OStage {
     static constexpr int kChunks = kRowBytes / 16;
 };
 
-// Writes row r of a staged output tile: the raw fp32 O words times inv, converted to OutT.
-template <typename OutT, int D>
-__device__ __forceinline__ void stage_row(uint32_t stg, int r, const uint32_t (&o)[D], float inv)
+// Writes columns c0 .. c0 + N - 1 (multiples of 32) of row r of a staged output tile: the raw fp32 O words times inv,
+// converted to OutT.
+template <typename OutT, int D, int N>
+__device__ __forceinline__ void stage_cols(uint32_t stg, int r, int c0, const uint32_t (&o)[N], float inv)
 {
     using OS = OStage<OutT, D>;
     constexpr int kEpc = 16 / static_cast<int>(sizeof(OutT));  // elements per 16-byte chunk
     const uint32_t row_addr = stg + static_cast<uint32_t>(r) * OS::kRowBytes;
     const uint32_t sw = OS::kRowBytes == 128 ? static_cast<uint32_t>(r & 7) : static_cast<uint32_t>((r >> 1) & 3);
 #pragma unroll
-    for (int g = 0; g < D / kEpc; ++g) {
+    for (int i = 0; i < N / kEpc; ++i) {
+        const int g = c0 / kEpc + i;
         const uint32_t addr = row_addr + static_cast<uint32_t>((g / OS::kChunks) * OS::kBlkBytes) +
                               ((static_cast<uint32_t>(g % OS::kChunks) ^ sw) << 4);
-        const int e = g * kEpc;
+        const int e = i * kEpc;
         if constexpr (sizeof(OutT) == 2) {
             st_shared_v4(addr, pack_bf16x2(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv),
                          pack_bf16x2(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv),
@@ -209,6 +211,13 @@ __device__ __forceinline__ void stage_row(uint32_t stg, int r, const uint32_t (&
                          __float_as_uint(__uint_as_float(o[e + 2]) * inv), __float_as_uint(__uint_as_float(o[e + 3]) * inv));
         }
     }
+}
+
+// The whole row.
+template <typename OutT, int D>
+__device__ __forceinline__ void stage_row(uint32_t stg, int r, const uint32_t (&o)[D], float inv)
+{
+    stage_cols<OutT, D, D>(stg, r, 0, o, inv);
 }
 
 // Shape of one work item (head bh, query rows [i0, i0 + 256)).  Query tile slot i (warpgroup i,

@@ -264,6 +264,9 @@ struct ScoreRules {
     float cap_in;         // scale / cap, so that cap * tanh(cap_in * S) is the capped score; 0: no cap
     float mult;           // capped scores in base 2 are mult * tanh, others mult * S: cap or scale, times log2(e)
     const float* slopes;  // fp32 [Hq] or nullptr
+    // tanh(cap_in * S), times mult except in the backward, as S P(S^2) (fa_rules_common.cuh, cap_factor)
+    float near[3], wide[5];
+    float near_in, wide_in;  // cap_in over the polynomials' ranges: |S| times it is at most 1 where they hold; +inf: nowhere
 };
 
 // A run of equal document numbers, and what a query or a key has of it (fa_rules_ranges_kernel).
@@ -290,9 +293,12 @@ struct FwdRulesParams {
     int Hq, Hkv, causal;
 };
 
-cudaError_t launch_fwd_rules_32(const FwdRulesParams& p, fa_dtype o_dtype, cudaStream_t st);
-cudaError_t launch_fwd_rules_64(const FwdRulesParams& p, fa_dtype o_dtype, cudaStream_t st);
-cudaError_t launch_fwd_rules_128(const FwdRulesParams& p, fa_dtype o_dtype, cudaStream_t st);
+// The kernels under score rules are compiled for each head size and kind of rules: kCap, kBias, both or neither.
+enum RuleKinds { kNoRules = 0, kCap = 1, kBias = 2 };
+inline int rule_kind(const ScoreRules& r) { return (r.cap_in > 0.f ? kCap : 0) + (r.slopes != nullptr ? kBias : 0); }
+
+template <int D, int RULES>
+cudaError_t launch_fwd_rules(const FwdRulesParams& p, fa_dtype o_dtype, cudaStream_t st);
 
 struct BwdRulesParams {
     BwdParams b;        // BH = B * Hq; tm_k, tm_v, tm_dk, tm_dv over B * Hkv heads
@@ -307,9 +313,8 @@ struct BwdRulesParams {
     int n_items;            // B * Hkv * parts * Tc
 };
 
-cudaError_t launch_bwd_rules_32(const BwdRulesParams& p, fa_dtype grad_dtype, cudaStream_t st);
-cudaError_t launch_bwd_rules_64(const BwdRulesParams& p, fa_dtype grad_dtype, cudaStream_t st);
-cudaError_t launch_bwd_rules_128(const BwdRulesParams& p, fa_dtype grad_dtype, cudaStream_t st);
+template <int D, int RULES>
+cudaError_t launch_bwd_rules(const BwdRulesParams& p, fa_dtype grad_dtype, cudaStream_t st);
 
 // out[i] = sum over parts of part[p][i], in order, for i < n (a multiple of 32); both of dK and dV.
 struct RulesSumParams {
@@ -354,9 +359,8 @@ struct PrefixMergeParams {
     fa_dtype o_dtype;
 };
 
-cudaError_t launch_prefix_32(const PrefixParams& p, cudaStream_t st);
-cudaError_t launch_prefix_64(const PrefixParams& p, cudaStream_t st);
-cudaError_t launch_prefix_128(const PrefixParams& p, cudaStream_t st);
+template <int D, int RULES>
+cudaError_t launch_prefix(const PrefixParams& p, cudaStream_t st);
 cudaError_t launch_prefix_merge(const PrefixMergeParams& p, int d, cudaStream_t st);
 
 // Host helpers of the C ABI files (fa_api.cu).

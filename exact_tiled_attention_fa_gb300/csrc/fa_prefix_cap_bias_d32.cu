@@ -1,0 +1,7 @@
+// Decode behind a shared prefix (fa_tree_kernel, SHARED), head size 32, scores with a cap and a bias.
+#include "fa_tree_kernel.cuh"
+
+namespace fa {
+template <>
+cudaError_t launch_prefix<32, 3>(const PrefixParams& p, cudaStream_t st) { return launch_prefix_d<32, 3>(p, st); }
+}  // namespace fa

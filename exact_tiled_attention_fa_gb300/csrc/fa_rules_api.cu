@@ -2,6 +2,7 @@
 // workspace layout and dispatch, host code only; and the kernel that adds up the parts of shared heads' gradients.
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "fa_internal.h"
 #include "fa_rules_common.cuh"
@@ -72,14 +73,44 @@ struct Ranges {
     }
 };
 
-// Scale and cap as the kernels take them; false for a cap or scale that fp32 cannot hold so.
-bool make_rules(fa::ScoreRules* r, float scale, float softcap, const float* slopes)
+// Scale and cap as the kernels take them (`score`: the polynomials with mult in them); false for a cap or scale that fp32
+// cannot hold so.
+bool make_rules(fa::ScoreRules* r, float scale, float softcap, const float* slopes, bool score)
 {
     if (!(std::isfinite(scale) && scale > 0.f) || !(std::isfinite(softcap) && softcap >= 0.f)) return false;
     r->cap_in = softcap > 0.f ? scale / softcap : 0.f;
     r->mult = (softcap > 0.f ? softcap : scale) * fa::kLog2e;
     r->slopes = slopes;
-    return std::isfinite(r->mult) && r->mult > 0.f && std::isfinite(r->cap_in) && (softcap == 0.f || r->cap_in > 0.f);
+    if (!(std::isfinite(r->mult) && r->mult > 0.f && std::isfinite(r->cap_in)) || (softcap > 0.f && r->cap_in == 0.f)) return false;
+    r->near_in = r->wide_in = INFINITY;
+    // powers of cap_in up to the ninth must be normal numbers, with mult in them too
+    if (r->cap_in < 1e-4f || r->cap_in > 1e3f) return true;
+    const double near[] = {FA_TANH_NEAR}, wide[] = {FA_TANH_WIDE}, k = r->cap_in;
+    double at = k * (score ? r->mult : 1.0);
+    for (int i = 0; i < 5; ++i, at *= k * k) {
+        if (i < 3) r->near[i] = static_cast<float>(near[i] * at);
+        r->wide[i] = static_cast<float>(wide[i] * at);
+    }
+    r->near_in = r->cap_in / fa::kNearRange;
+    r->wide_in = r->cap_in / fa::kWideRange;
+    return true;
+}
+
+// f with the head size and the kind of rules as constants.
+template <typename F>
+cudaError_t by_kind(int d, const fa::ScoreRules& r, F f)
+{
+    auto kinds = [&](auto D) {
+        using std::integral_constant;
+        switch (fa::rule_kind(r)) {
+        case 0: return f(D, integral_constant<int, 0>());
+        case 1: return f(D, integral_constant<int, 1>());
+        case 2: return f(D, integral_constant<int, 2>());
+        default: return f(D, integral_constant<int, 3>());
+        }
+    };
+    return d == 32 ? kinds(std::integral_constant<int, 32>()) : d == 64 ? kinds(std::integral_constant<int, 64>())
+                                                                        : kinds(std::integral_constant<int, 128>());
 }
 
 // The checks that forward and backward share.
@@ -90,7 +121,7 @@ fa_status check_rules(const void* q, const void* k, const void* v, const float* 
     if (B <= 0 || Hq <= 0 || Hkv <= 0 || N <= 0 || Nk <= 0 || d <= 0 || dv <= 0) return FA_ERR_INVALID_ARG;
     if (Hq % Hkv != 0 || (causal != 0 && causal != 1)) return FA_ERR_INVALID_ARG;
     fa::ScoreRules r;
-    if (!make_rules(&r, scale, softcap, slopes)) return FA_ERR_INVALID_ARG;
+    if (!make_rules(&r, scale, softcap, slopes, true)) return FA_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(slopes, 4) || !aligned(documents, 4) || !aligned(prefix_lens, 4))
         return FA_ERR_INVALID_ARG;
     // positions and tile indices are 32-bit, with room for a tile past the end
@@ -132,7 +163,7 @@ fa_status fa_fwd_rules(const void* q, const void* k, const void* v, const float*
     if (!head_ok(d) || dv != d) return FA_ERR_UNSUPPORTED;
     if (documents != nullptr && ws_bytes < fa_fwd_rules_workspace_size(B, N)) return FA_ERR_WORKSPACE;
     fa::FwdRulesParams p{};
-    make_rules(&p.rules, scale, softcap, slopes);
+    make_rules(&p.rules, scale, softcap, slopes, true);
     fa::FwdParams& f = p.f;
     if (!fa::bf16_tile_map(&f.tm_q, q, B * Hq, N, d) || !fa::bf16_tile_map(&f.tm_k, k, B * Hkv, Nk, d) ||
         !fa::bf16_tile_map(&f.tm_v, v, B * Hkv, Nk, dv) || !fa::out_tile_map(&f.tm_o, o, B * Hq, N, dv, o_dtype, 32))
@@ -160,9 +191,7 @@ fa_status fa_fwd_rules(const void* q, const void* k, const void* v, const float*
         p.tile = r.tile;
         p.counter = r.counter;
     }
-    const cudaError_t e = d == 32   ? fa::launch_fwd_rules_32(p, o_dtype, st)
-                          : d == 64 ? fa::launch_fwd_rules_64(p, o_dtype, st)
-                                    : fa::launch_fwd_rules_128(p, o_dtype, st);
+    const cudaError_t e = by_kind(d, p.rules, [&](auto D, auto kind) { return fa::launch_fwd_rules<D(), kind()>(p, o_dtype, st); });
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -189,7 +218,7 @@ fa_status fa_bwd_rules(const void* q, const void* k, const void* v, const void* 
         return FA_ERR_INVALID_ARG;
     if (!head_ok(d) || dv != d) return FA_ERR_UNSUPPORTED;
     fa::BwdRulesParams p{};
-    make_rules(&p.rules, scale, softcap, slopes);
+    make_rules(&p.rules, scale, softcap, slopes, false);
     fa::BwdParams& b = p.b;
     if (fa::device_status_word(&b.status) != cudaSuccess || fa::device_sm_count(&b.num_ctas) != cudaSuccess) return FA_ERR_CUDA;
     if (ws_bytes < fa_bwd_rules_workspace_size(B, Hq, Hkv, N, Nk, d, b.num_ctas)) return FA_ERR_WORKSPACE;
@@ -246,9 +275,7 @@ fa_status fa_bwd_rules(const void* q, const void* k, const void* v, const void* 
     p.parts = parts;
     p.part_heads = (R + parts - 1) / parts;
     p.n_items = B * Hkv * parts * Tc;
-    const cudaError_t e = d == 32   ? fa::launch_bwd_rules_32(p, kv_type, st)
-                          : d == 64 ? fa::launch_bwd_rules_64(p, kv_type, st)
-                                    : fa::launch_bwd_rules_128(p, kv_type, st);
+    const cudaError_t e = by_kind(d, p.rules, [&](auto D, auto kind) { return fa::launch_bwd_rules<D(), kind()>(p, kv_type, st); });
     if (e != cudaSuccess) return FA_ERR_CUDA;
     const fa::BwdDqParams dp{dq_acc, grad_q, B * Hq, N, Tr, d};
     if (fa::launch_bwd_dq(dp, grad_dtype, st) != cudaSuccess) return FA_ERR_CUDA;
@@ -331,7 +358,7 @@ fa_status fa_decode_prefix(const void* q, const void* k_prefix, const void* v_pr
     if (pre != (v_prefix != nullptr) || (pre ? P_max <= 0 : P_max != 0 || prefix_len != nullptr)) return FA_ERR_INVALID_ARG;
     if (!prefix_sizes_ok(B, Hq, Hkv, d) || dv <= 0 || Nk_max <= 0 || !dtype_ok(o_dtype)) return FA_ERR_INVALID_ARG;
     fa::ScoreRules rules;
-    if (!make_rules(&rules, scale, softcap, slopes)) return FA_ERR_INVALID_ARG;
+    if (!make_rules(&rules, scale, softcap, slopes, true)) return FA_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(k_prefix, 16) || !aligned(v_prefix, 16) || !aligned(prefix_len, 4) || !aligned(k_cache, 16) ||
         !aligned(v_cache, 16) || !aligned(seqlens_k, 4) || !aligned(slopes, 4) || !aligned(o, 16) || !aligned(lse, 4) ||
         !aligned(workspace, kAlign))
@@ -377,9 +404,7 @@ fa_status fa_decode_prefix(const void* q, const void* k_prefix, const void* v_pr
     p.lse_own = pre ? p.lse_pre + rows : nullptr;
     fa::TreeJoin* joins = reinterpret_cast<fa::TreeJoin*>(ws + plan.joins);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    auto launch = [&] {
-        return d == 32 ? fa::launch_prefix_32(p, st) : d == 64 ? fa::launch_prefix_64(p, st) : fa::launch_prefix_128(p, st);
-    };
+    auto launch = [&] { return by_kind(d, rules, [&](auto D, auto kind) { return fa::launch_prefix<D(), kind()>(p, st); }); };
     if (pre && plan.pair) {
         p.joins = joins;
         p.o_part = at(plan.o_pre);

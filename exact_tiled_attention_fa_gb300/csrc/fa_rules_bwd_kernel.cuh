@@ -77,22 +77,21 @@ __device__ __forceinline__ RulesBwdItem rules_bwd_item(const BwdRulesParams& rp,
     return it;
 }
 
-// P and P times the cap's slope for 64 scores of one key (columns: queries).  CAP: 0 none, 1 tanh_small's polynomial,
-// 2 any argument.  BIAS: -slope2 |dist + c|; sign 1 where dist + c >= 0 in every column that counts, -1 where <= 0, 0 either.
+// P and P times the cap's slope for 64 scores of one key (columns: queries).  CAP: -1 none, else the range that cap_range
+// found.  BIAS: -slope2 |dist + c|; sign 1 where dist + c >= 0 in every column that counts, -1 where <= 0, 0 either.
 template <int CAP, bool BIAS>
 __device__ __forceinline__ void rules_weights(const uint32_t (&u)[64], float (&pf)[64], uint32_t (&pk)[32], uint32_t l_addr,
-                                              float cap_in, float mult, float slope2, float dist, int sign)
+                                              const ScoreRules& r, float slope2, float dist, int sign)
 {
-    const float2 m2 = make_float2(mult, mult);
+    const float2 m2 = two(r.mult);
     const float sg = sign < 0 ? slope2 : -slope2;
-    const float2 stride = make_float2(8.f * sg, 8.f * sg);
+    const float2 stride = two(8.f * sg);
 #pragma unroll
     for (int c0 = 0; c0 < 64; c0 += 32) {
         float t[32];
 #pragma unroll
         for (int c = 0; c < 32; ++c) t[c] = __uint_as_float(u[c0 + c]);
-        if constexpr (CAP == 1) tanh_small<32>(t, cap_in);
-        if constexpr (CAP == 2) tanh_any<32>(t, cap_in);
+        if constexpr (CAP == 0) tanh_any<32>(t, r.cap_in);
         float2 b[4];
         if constexpr (BIAS) {
 #pragma unroll
@@ -107,7 +106,9 @@ __device__ __forceinline__ void rules_weights(const uint32_t (&u)[64], float (&p
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int i = c + 2 * (h + e);
-                    const float2 y = make_float2(t[i], t[i + 1]);
+                    float2 y = make_float2(t[i], t[i + 1]);
+                    if constexpr (CAP == 2) y = __fmul2_rn(y, cap_factor(y, r.near));
+                    if constexpr (CAP == 1) y = __fmul2_rn(y, cap_factor(y, r.wide));
                     float2 x = __ffma2_rn(y, m2, e == 0 ? make_float2(-l4.x, -l4.y) : make_float2(-l4.z, -l4.w));
                     if constexpr (BIAS) {
                         if (sign != 0) {
@@ -121,7 +122,7 @@ __device__ __forceinline__ void rules_weights(const uint32_t (&u)[64], float (&p
                     const float2 w = make_float2(ex2(x.x), ex2(x.y));
                     pk[(c0 + i) / 2] = pack_bf16x2(w.x, w.y);
                     float2 g = w;
-                    if constexpr (CAP != 0) g = __fmul2_rn(w, __ffma2_rn(make_float2(-y.x, -y.y), y, make_float2(1.f, 1.f)));
+                    if constexpr (CAP >= 0) g = __fmul2_rn(w, __ffma2_rn(make_float2(-y.x, -y.y), y, make_float2(1.f, 1.f)));
                     pf[c0 + i] = g.x;
                     pf[c0 + i + 1] = g.y;
                 }
@@ -130,10 +131,11 @@ __device__ __forceinline__ void rules_weights(const uint32_t (&u)[64], float (&p
     }
 }
 
-template <int D, typename GradT>
+template <int D, int RULES, typename GradT>
 __global__ void __launch_bounds__(kBwdThreads, 1) fa_rules_bwd_kernel(const __grid_constant__ BwdRulesParams rp)
 {
     using C = RulesBwdCfg<D>;
+    constexpr bool kWithCap = (RULES & kCap) != 0, kWithBias = (RULES & kBias) != 0;
     const BwdParams& p = rp.b;
     // No grid_launch_dependents here: letting the dQ conversion that follows launch early made
     // the backward 6 % slower (B=64 H=16 N=1024 d=64); it starts once this grid's CTAs have exited.
@@ -527,10 +529,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1) fa_rules_bwd_kernel(const __gr
         int staged = 0;            // items whose dK, dV went out through the staging tiles
         float slope2 = 0.f;
         bool stage_busy = false;   // the last of those stores may still be reading the dS buffer
-        const float cap_in = rp.rules.cap_in;
-        const bool cap = cap_in > 0.f;
-        const bool bias = rp.rules.slopes != nullptr;
-        const float mult = rp.rules.mult;
         for (int i = 0; ok; ++i) {
             RulesBwdItem it;
             ok = __all_sync(0xffffffffu, take(i, it));
@@ -569,18 +567,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1) fa_rules_bwd_kernel(const __gr
             for (int t = 0, bh = it.bh0, tile = it.i_first; t < n; ++t, ++g, step(it, bh, tile)) {
                 const int s = g % QS;
                 const int i0 = tile * kBlockM;
-                if (bias && tile == it.i_first) slope2 = rp.rules.slopes[bh - it.b * rp.Hq] * kLog2e;
+                if (kWithBias && tile == it.i_first) slope2 = rp.rules.slopes[bh - it.b * rp.Hq] * kLog2e;
                 ok = __all_sync(0xffffffffu, mbar_wait(bar(kBbSFull), g & 1, limit, abort_flag));
                 if (!ok) break;
                 tc_fence_after_sync();
                 uint32_t u[64];
-                bool small = true;  // every |S| is within the polynomial's range
-                if (cap) {
+                int range = 0;
+                if constexpr (kWithCap) {
                     float mx[2];
                     tmem_ld32_absmax(t_s, *reinterpret_cast<uint32_t(*)[32]>(&u[0]), mx[0]);
                     tmem_ld32_absmax(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(&u[32]), mx[1]);
                     tmem_ld_wait();
-                    small = __all_sync(0xffffffffu, fmaxf(mx[0], mx[1]) * cap_in <= kTanhRange);
+                    range = cap_range(rp.rules, fmaxf(mx[0], mx[1]));
                 } else {
                     tmem_ld32(t_s, *reinterpret_cast<uint32_t(*)[32]>(&u[0]));
                     tmem_ld32(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(&u[32]));
@@ -596,18 +594,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1) fa_rules_bwd_kernel(const __gr
                 const int q0 = i0 + 64 * h;  // this thread's first query
                 float pf[64];
                 uint32_t pk[32];
-                const int sign = !bias ? 0 : __all_sync(0xffffffffu, off + q0 >= key || (rp.causal && key >= it.prefix)) ? 1
-                                      : __all_sync(0xffffffffu, off + q0 + 63 <= key) ? -1 : 0;
+                int sign = 0;
+                if constexpr (kWithBias)
+                    sign = __all_sync(0xffffffffu, off + q0 >= key || (rp.causal && key >= it.prefix)) ? 1
+                           : __all_sync(0xffffffffu, off + q0 + 63 <= key)                             ? -1
+                                                                                                       : 0;
                 const float dist = static_cast<float>(off + q0 - key);
-                if (!bias) {
-                    if (!cap) rules_weights<0, false>(u, pf, pk, l_addr, cap_in, mult, 0.f, 0.f, 0);
-                    else if (small) rules_weights<1, false>(u, pf, pk, l_addr, cap_in, mult, 0.f, 0.f, 0);
-                    else rules_weights<2, false>(u, pf, pk, l_addr, cap_in, mult, 0.f, 0.f, 0);
-                } else {
-                    if (!cap) rules_weights<0, true>(u, pf, pk, l_addr, cap_in, mult, slope2, dist, sign);
-                    else if (small) rules_weights<1, true>(u, pf, pk, l_addr, cap_in, mult, slope2, dist, sign);
-                    else rules_weights<2, true>(u, pf, pk, l_addr, cap_in, mult, slope2, dist, sign);
-                }
+                if (kWithCap && range == 2) rules_weights<2, kWithBias>(u, pf, pk, l_addr, rp.rules, slope2, dist, sign);
+                else if (kWithCap && range == 1) rules_weights<1, kWithBias>(u, pf, pk, l_addr, rp.rules, slope2, dist, sign);
+                else rules_weights<kWithCap ? 0 : -1, kWithBias>(u, pf, pk, l_addr, rp.rules, slope2, dist, sign);
                 if (!__all_sync(0xffffffffu, qa <= q0 && qe >= q0 + 64)) {  // hidden pairs: P = 0
 #pragma unroll
                     for (int w = 0; w < 2; ++w) {
@@ -773,11 +768,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) fa_rules_bwd_kernel(const __gr
     }
 }
 
-template <int D, typename GradT>
+template <int D, int RULES, typename GradT>
 cudaError_t launch_bwd_rules_t(const BwdRulesParams& p, cudaStream_t st)
 {
     using C = RulesBwdCfg<D>;
-    auto kern = fa_rules_bwd_kernel<D, GradT>;
+    auto kern = fa_rules_bwd_kernel<D, RULES, GradT>;
     static bool configured[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -797,10 +792,10 @@ cudaError_t launch_bwd_rules_t(const BwdRulesParams& p, cudaStream_t st)
     return launch_pdl(kern, static_cast<unsigned>(grid), kBwdThreads, C::kSmem, st, p);
 }
 
-template <int D>
+template <int D, int RULES>
 cudaError_t launch_bwd_rules_d(const BwdRulesParams& p, fa_dtype grad_dtype, cudaStream_t st)
 {
-    return grad_dtype == FA_F32 ? launch_bwd_rules_t<D, float>(p, st) : launch_bwd_rules_t<D, __nv_bfloat16>(p, st);
+    return grad_dtype == FA_F32 ? launch_bwd_rules_t<D, RULES, float>(p, st) : launch_bwd_rules_t<D, RULES, __nv_bfloat16>(p, st);
 }
 
 }  // namespace fa

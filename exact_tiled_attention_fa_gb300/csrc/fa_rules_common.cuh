@@ -25,35 +25,33 @@ __device__ __forceinline__ float rcp_approx(float x)
     return y;
 }
 
-// tanh of N numbers k * s, in place.  Arguments up to kTanhRange, where scores that a cap is meant for almost
-// always are, take an odd polynomial on the FMA units: u P(u^2) with P the minimax polynomial of degree 5 for
-// tanh(u) / u (Remez exchange on u^2 in [0, 0.5625], relative error 2.9e-8).  Others take 1 - 2 / (1 + e^2u), two
-// operations of the special function unit that the softmax's exponentials also need; its absolute error of 2e-7
-// is one of 1e-5 of a weight at a cap of 50.  +-infinity gives +-1, NaN NaN.  (The device's own tanh instruction
-// is off by 2^-11 of its result: at a score of 20 by 0.01, and the weight by as much.) 
-constexpr float kTanhRange = 0.75f;
+// The cap.  tanh(u) for |u| <= kWideRange, where the scores that a cap is meant for almost always are, is u P(u^2) with
+// P the minimax polynomial for tanh(u) / u (Remez exchange on u^2): degree 2 up to kNearRange (relative error 1.2e-6),
+// degree 4 up to kWideRange (5.7e-7).  With cap_in and mult in its coefficients a capped score is S Q(S^2): n + 1
+// operations and the one that takes the maximum off it anyway.  (What bounds them is the FMA units, 128 lanes an SM,
+// whether two operations go in one instruction or not: a polynomial of degree 5 for every argument, scaled before it,
+// took 8 and the causal prefill of 4 sequences of 4097 tokens, 16 heads of 128, 487 us; without a cap 341; PLACEHOLDER.)
+// Other arguments take 1 - 2 / (1 + e^2u): two operations of the special function unit that the exponentials also need
+// (586 us); its absolute error of 2e-7 is one of 1e-5 of a weight at a cap of 50.  +-infinity gives +-1, NaN NaN.  (The
+// device's own tanh instruction is off by 2^-11 of its result: at a score of 20 by 0.01, and the weight by as much.)
+constexpr float kNearRange = 0.3f, kWideRange = 0.75f;
+#define FA_TANH_NEAR 0.999998838848, -0.333100215997, 0.126339459894
+#define FA_TANH_WIDE 0.999999434926, -0.33328251533, 0.132589832157, -0.0500563024273, 0.0129296321186
 
+__device__ __forceinline__ float2 two(float x) { return make_float2(x, x); }
+
+// Q of a pair of scores; a capped score is s * Q.
 template <int N>
-__device__ __forceinline__ void tanh_small(float* s, float k)
+__device__ __forceinline__ float2 cap_factor(float2 s, const float (&c)[N])
 {
-    constexpr float c0 = 0.99999997101f, c1 = -0.3333295888f, c2 = 0.13325406021f, c3 = -0.053344430265f, c4 = 0.019582908378f,
-                    c5 = -0.0047162573577f;
-    auto two = [](float x) { return make_float2(x, x); };
+    const float2 w = __fmul2_rn(s, s);
+    float2 q = two(c[N - 1]);
 #pragma unroll
-    for (int c = 0; c < N; c += 2) {
-        const float2 u = __fmul2_rn(make_float2(s[c], s[c + 1]), two(k));
-        const float2 w = __fmul2_rn(u, u);
-        float2 q = __ffma2_rn(w, two(c5), two(c4));
-        q = __ffma2_rn(w, q, two(c3));
-        q = __ffma2_rn(w, q, two(c2));
-        q = __ffma2_rn(w, q, two(c1));
-        q = __ffma2_rn(w, q, two(c0));
-        q = __fmul2_rn(u, q);
-        s[c] = q.x;
-        s[c + 1] = q.y;
-    }
+    for (int i = N - 2; i >= 0; --i) q = __ffma2_rn(w, q, two(c[i]));
+    return q;
 }
 
+// tanh of N numbers k * s, in place.
 template <int N>
 __device__ __forceinline__ void tanh_any(float* s, float k)
 {
@@ -62,28 +60,35 @@ __device__ __forceinline__ void tanh_any(float* s, float k)
     for (int c = 0; c < N; ++c) s[c] = fmaf(-2.f, rcp_approx(1.f + ex2(s[c] * k2)), 1.f);
 }
 
-// s <- mult * s - slope2 * |dist - c| for columns c = 0 .. N - 1 (dist: the position of the row less that of column
-// 0).  sign = 1 where every column lies at or before its row's position, -1 where behind it: the bias is then linear
-// in c, a start for each 32 columns and steps of 8 added to it (four roundings).  0: either.
-template <int N>
-__device__ __forceinline__ void add_bias(float* s, float mult, float slope2, float dist, int sign)
+// Whether every lane's |S| (its largest, mx) lies in the polynomials' ranges: 2 the near one, 1 the wide one, 0 neither.
+__device__ __forceinline__ int cap_range(const ScoreRules& r, float mx, bool counts = true)
 {
-    const float2 m2 = make_float2(mult, mult);
+    if (__all_sync(0xffffffffu, !counts || mx * r.near_in <= 1.f)) return 2;
+    return __all_sync(0xffffffffu, !counts || mx * r.wide_in <= 1.f) ? 1 : 0;
+}
+
+// s <- f(s, -slope2 * |dist - c|) by pairs, for columns c = 0 .. N - 1 (dist: the position of the row less that of column
+// 0).  sign = 1 where every column that counts lies at or before its row's position, -1 where behind it: the bias is then
+// linear in c, a start for each 32 columns and steps of 8 added to it (four roundings).  0: either.
+template <int N, typename F>
+__device__ __forceinline__ void add_bias(float* s, float slope2, float dist, int sign, F f)
+{
     if (sign != 0) {
         const float sg = sign > 0 ? slope2 : -slope2;
         const float base = -sg * dist;
-        const float2 step = make_float2(8.f * sg, 8.f * sg);
+        const float2 step = two(8.f * sg);
 #pragma unroll
         for (int c0 = 0; c0 < N; c0 += 32) {
             float2 b[4];
 #pragma unroll
-            for (int h = 0; h < 4; ++h) b[h] = make_float2(fmaf(static_cast<float>(c0 + 2 * h), sg, base), fmaf(static_cast<float>(c0 + 2 * h + 1), sg, base));
+            for (int h = 0; h < 4; ++h)
+                b[h] = make_float2(fmaf(static_cast<float>(c0 + 2 * h), sg, base), fmaf(static_cast<float>(c0 + 2 * h + 1), sg, base));
 #pragma unroll
             for (int c = 0; c < 32; c += 8) {
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
                     const int i = c0 + c + 2 * h;
-                    const float2 y = __ffma2_rn(make_float2(s[i], s[i + 1]), m2, b[h]);
+                    const float2 y = f(make_float2(s[i], s[i + 1]), b[h]);
                     s[i] = y.x;
                     s[i + 1] = y.y;
                     if (c + 8 < 32) b[h] = __fadd2_rn(b[h], step);
@@ -92,7 +97,26 @@ __device__ __forceinline__ void add_bias(float* s, float mult, float slope2, flo
         }
     } else {
 #pragma unroll
-        for (int c = 0; c < N; ++c) s[c] = fmaf(-slope2, fabsf(dist - static_cast<float>(c)), s[c] * mult);
+        for (int c = 0; c < N; c += 2) {
+            const float2 y = f(make_float2(s[c], s[c + 1]), make_float2(-slope2 * fabsf(dist - static_cast<float>(c)),
+                                                                        -slope2 * fabsf(dist - static_cast<float>(c + 1))));
+            s[c] = y.x;
+            s[c + 1] = y.y;
+        }
+    }
+}
+
+// Scores s of N keys under a bias, and a cap if CAP: in base 2, in place.
+template <int N, bool CAP>
+__device__ __forceinline__ void biased_scores(float* s, const ScoreRules& r, int range, float slope2, float dist, int sign)
+{
+    if (CAP && range == 2) {
+        add_bias<N>(s, slope2, dist, sign, [&](float2 x, float2 b) { return __ffma2_rn(x, cap_factor(x, r.near), b); });
+    } else if (CAP && range == 1) {
+        add_bias<N>(s, slope2, dist, sign, [&](float2 x, float2 b) { return __ffma2_rn(x, cap_factor(x, r.wide), b); });
+    } else {
+        if (CAP) tanh_any<N>(s, r.cap_in);
+        add_bias<N>(s, slope2, dist, sign, [&](float2 x, float2 b) { return __ffma2_rn(x, two(r.mult), b); });
     }
 }
 

@@ -47,8 +47,8 @@ struct RulesCfg : FwdCfg<D, OutBytes> {
     static constexpr int kUsed = kOffItems + kRulesItems * static_cast<int>(sizeof(RulesItem)) + 1024;  // 1 KB to align
     static_assert(kUsed <= 227 * 1024, "shared memory per CTA");
     static constexpr int kSmem = kUsed > 120 * 1024 ? kUsed : 120 * 1024;  // one CTA on an SM, as FwdCfg
-    static constexpr int kSoftRegs = kSoftmaxRegs<D>;
-    static constexpr int kCtrlRegs = kControlRegs<D>;
+    static constexpr int kSoftRegs = 216;
+    static constexpr int kCtrlRegs = 72;
 };
 
 // Item `item`: query pair t of head bh, in the order of fa_fwd_kernel.cuh's causal walk.
@@ -115,11 +115,12 @@ __device__ __forceinline__ void rules_mask(float* s, int lo, int hi)
     }
 }
 
-template <int D, typename OutT>
+template <int D, int RULES, typename OutT>
 __global__ void __launch_bounds__(kFwdThreads, 1) fa_rules_fwd_kernel(const __grid_constant__ FwdRulesParams p)
 {
     using C = RulesCfg<D, static_cast<int>(sizeof(OutT))>;
     constexpr int S = C::kStages;
+    constexpr bool kWithCap = (RULES & kCap) != 0, kWithBias = (RULES & kBias) != 0;
     extern __shared__ uint8_t rules_smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(rules_smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
@@ -364,10 +365,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_rules_fwd_kernel(const __gr
         const uint32_t t_s = tmem + lane_base + C::col_s(wg);
         const uint32_t t_o = tmem + lane_base + C::col_o(wg);
         const uint32_t t_p = tmem + lane_base + C::col_p(wg);
-        const float cap_in = p.rules.cap_in;
-        const bool cap = cap_in > 0.f;
-        const bool bias = p.rules.slopes != nullptr;
-        const float mult = bias ? 1.f : p.rules.mult;  // of what the exponentials take
         const int off = f.Nk - f.N;
         int tiles = 0;   // (query tile, key tile) pairs processed by this warpgroup
         int uses = 0;    // items in which this warpgroup had key tiles
@@ -375,30 +372,38 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_rules_fwd_kernel(const __gr
         bool ok = true;
 
         for (int k = 0; ok; ++k) {
-            RulesItem it;
-            ok = __all_sync(0xffffffffu, take(k, it));
+            // (read field by field where it is used, so that the tiles' loop does not hold it in registers)
+            const volatile RulesItem& it = items[k % kRulesItems];
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarItemFull + k % kRulesItems), static_cast<uint32_t>(k / kRulesItems) & 1, limit, abort_flag));
             if (!ok || it.n_kv < 0) break;
-            __syncwarp();  // every lane has its copy
-            if (lane == 0) mbar_arrive(bar(kBarItemEmpty + k % kRulesItems));
-            const int rows = wg ? it.rows[1] : it.rows[0];
-            if (rows == 0) continue;  // tile lies past N
-            const int a = wg ? it.a[1] : it.a[0];
-            const int n = wg ? it.n[1] : it.n[0];
-            const int row0 = wg ? it.r0[1] : it.r0[0];  // first query row of this tile
-            const int qpos = off + row0 + r;
+            auto release = [&] {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kBarItemEmpty + k % kRulesItems));
+            };
+            if (it.rows[wg] == 0) {  // tile lies past N
+                release();
+                continue;
+            }
+            const int a = it.a[wg];
+            const int n = it.n[wg];
+            const int qpos = off + it.r0[wg] + r;
             // the row's keys [lo, hi); rows past N take the last row's
             int lo = 0, hi = f.Nk;
-            if (p.each != nullptr) {
-                const int2 x = p.each[static_cast<size_t>(it.b) * f.N + row0 + min(r, rows - 1)];
-                lo = x.x;
-                hi = x.y;
-            } else if (p.causal) {
-                hi = min(f.Nk, max(off + row0 + min(r, rows - 1) + 1, it.prefix));
+            {
+                const int row = it.r0[wg] + min(r, it.rows[wg] - 1);
+                if (p.each != nullptr) {
+                    const int2 x = p.each[static_cast<size_t>(it.b) * f.N + row];
+                    lo = x.x;
+                    hi = x.y;
+                } else if (p.causal) {
+                    hi = min(f.Nk, max(off + row + 1, it.prefix));
+                }
             }
-            const float slope2 = bias ? p.rules.slopes[it.bh - it.b * p.Hq] * kLog2e : 0.f;
+            const float slope2 = kWithBias ? p.rules.slopes[it.bh - it.b * p.Hq] * kLog2e : 0.f;
             float m_run = -INFINITY;  // running max of the scores in base 2 over visible keys
             float l = 0.f;
-            for (int j = a; j < n; ++j) {
+            int k0 = (it.j0 + a) * kBlockN;  // first key of the tile
+            for (int j = a; j < n; ++j, k0 += kBlockN) {
                 ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarSFull + wg), tiles & 1, limit, abort_flag));
                 if (!ok) break;
                 tc_fence_after_sync();
@@ -406,7 +411,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_rules_fwd_kernel(const __gr
                 float mrow;  // the row's largest score, or under a cap the largest absolute one
                 if constexpr (D == 128) {
                     float mh[2];
-                    if (cap) {
+                    if constexpr (kWithCap) {
                         tmem_ld64_absmax(t_s + 0, *reinterpret_cast<uint32_t(*)[64]>(&u[0]), mh[0]);
                         tmem_ld64_absmax(t_s + 64, *reinterpret_cast<uint32_t(*)[64]>(&u[64]), mh[1]);
                     } else {
@@ -417,7 +422,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_rules_fwd_kernel(const __gr
                     mrow = fmaxf(mh[0], mh[1]);
                 } else {
                     float mq[4];
-                    if (cap) {
+                    if constexpr (kWithCap) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
                             tmem_ld32_absmax(t_s + 32u * q, *reinterpret_cast<uint32_t(*)[32]>(&u[32 * q]), mq[q]);
@@ -436,42 +441,78 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_rules_fwd_kernel(const __gr
                 float s[kBlockN];
 #pragma unroll
                 for (int c = 0; c < kBlockN; ++c) s[c] = __uint_as_float(u[c]);
-                const int k0 = (it.j0 + j) * kBlockN;
-                if (cap) {
-                    if (__all_sync(0xffffffffu, mrow * cap_in <= kTanhRange)) tanh_small<kBlockN>(s, cap_in);
-                    else tanh_any<kBlockN>(s, cap_in);
-                }
-                if (bias) {
-                    // keys behind a causal row's position are hidden below, whatever bias they get
-                    const bool before = __all_sync(0xffffffffu, k0 + kBlockN - 1 <= qpos || (p.causal && hi <= qpos + 1));
-                    const bool behind = __all_sync(0xffffffffu, k0 >= qpos);
-                    add_bias<kBlockN>(s, p.rules.mult, slope2, static_cast<float>(qpos - k0), before ? 1 : behind ? -1 : 0);
-                }
                 const bool mask = !__all_sync(0xffffffffu, lo <= k0 && hi >= k0 + kBlockN);
-                if (mask) rules_mask(s, lo - k0, hi - k0);
-                if (cap || bias || mask) mrow = max_of<kBlockN>(s);
-                const float mt = mrow * mult;
-                const bool grow = mt > m_run;
-                float alpha = 1.f;
-                if (grow) {
-                    alpha = ex2(m_run - mt);  // 0 when m_run = -inf
-                    m_run = mt;
-                }
-                const float m_use = (m_run == -INFINITY) ? 0.f : m_run;
-                // Test now whether P_i(j-1) V_{j-1} has completed; the answer is needed only after the exponentials.
-                const bool pv_ready = C::kAliasP || j == a || mbar_test(bar(kBarPVDone + wg), (tiles - 1) & 1);
-                const float2 mult2 = make_float2(mult, mult);
-                const float2 negm = make_float2(-m_use, -m_use);
+                // Raises the running max to mt; the weights are then 2^(score - m_use).
+                bool grow;
+                float alpha = 1.f, m_use;
+                auto raise = [&](float mt) {
+                    grow = mt > m_run;
+                    if (grow) {
+                        alpha = ex2(m_run - mt);  // 0 when m_run = -inf
+                        m_run = mt;
+                    }
+                    m_use = m_run == -INFINITY ? 0.f : m_run;
+                };
                 float2 rs[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                 uint32_t pk[kBlockN / 2];  // weights, rounded to bf16 for the product with V (half a step, 2^-8 of each)
+                // Weights of scores g(s, -max), their sums in four running pairs.
+                auto weigh = [&](auto g) {
+                    const float2 negm = two(-m_use);
 #pragma unroll
-                for (int c = 0; c < kBlockN; c += 8) {
+                    for (int c = 0; c < kBlockN; c += 8) {
 #pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        const float2 x = __ffma2_rn(make_float2(s[c + 2 * h], s[c + 2 * h + 1]), mult2, negm);
-                        const float2 e = make_float2(ex2(x.x), ex2(x.y));
-                        rs[h] = __fadd2_rn(rs[h], e);
-                        pk[c / 2 + h] = pack_bf16x2(e.x, e.y);
+                        for (int h = 0; h < 4; ++h) {
+                            const float2 x = g(make_float2(s[c + 2 * h], s[c + 2 * h + 1]), negm);
+                            const float2 e = make_float2(ex2(x.x), ex2(x.y));
+                            rs[h] = __fadd2_rn(rs[h], e);
+                            pk[c / 2 + h] = pack_bf16x2(e.x, e.y);
+                        }
+                    }
+                };
+                // Test whether P_i(j-1) V_{j-1} has completed before the exponentials; the answer is needed after them.
+                bool pv_ready = true;
+                auto test_pv = [&] {
+                    if (!C::kAliasP && j > a) pv_ready = mbar_test(bar(kBarPVDone + wg), (tiles - 1) & 1);
+                };
+                const int range = kWithCap ? cap_range(p.rules, mrow) : 0;
+                if (kWithCap && !kWithBias && range != 0 && !mask) {
+                    // tanh rises with its argument: the largest raw score is the largest capped one
+                    const float2 top = two(max_of<kBlockN>(s));
+                    raise(__fmul2_rn(top, range == 2 ? cap_factor(top, p.rules.near) : cap_factor(top, p.rules.wide)).x);
+                    test_pv();
+                    if (range == 2) weigh([&](float2 x, float2 m) { return __ffma2_rn(x, cap_factor(x, p.rules.near), m); });
+                    else weigh([&](float2 x, float2 m) { return __ffma2_rn(x, cap_factor(x, p.rules.wide), m); });
+                } else {
+                    if constexpr (kWithBias) {
+                        // keys behind a causal row's position are hidden below, whatever bias they get
+                        const bool before = __all_sync(0xffffffffu, k0 + kBlockN - 1 <= qpos || (p.causal && hi <= qpos + 1));
+                        const bool behind = __all_sync(0xffffffffu, k0 >= qpos);
+                        biased_scores<kBlockN, kWithCap>(s, p.rules, range, slope2, static_cast<float>(qpos - k0), before ? 1 : behind ? -1 : 0);
+                    } else if constexpr (kWithCap) {
+                        if (range != 0) {
+#pragma unroll
+                            for (int c = 0; c < kBlockN; c += 2) {
+                                float2 x = make_float2(s[c], s[c + 1]);
+                                x = __fmul2_rn(x, cap_factor(x, p.rules.wide));
+                                s[c] = x.x;
+                                s[c + 1] = x.y;
+                            }
+                        } else {
+                            tanh_any<kBlockN>(s, p.rules.cap_in);
+#pragma unroll
+                            for (int c = 0; c < kBlockN; ++c) s[c] *= p.rules.mult;
+                        }
+                    }
+                    if (mask) rules_mask(s, lo - k0, hi - k0);
+                    if (RULES != kNoRules || mask) mrow = max_of<kBlockN>(s);
+                    if constexpr (RULES == kNoRules) {
+                        raise(mrow * p.rules.mult);
+                        test_pv();
+                        weigh([&](float2 x, float2 m) { return __ffma2_rn(x, two(p.rules.mult), m); });
+                    } else {
+                        raise(mrow);
+                        test_pv();
+                        weigh([&](float2 x, float2 m) { return __fadd2_rn(x, m); });
                     }
                 }
                 // O_i and the P_i columns are free once P_i(j-1) V_{j-1} has completed.  With P aliased into S_i this is
@@ -520,8 +561,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_rules_fwd_kernel(const __gr
             const bool none = l == 0.f;  // a row that sees no key: O = 0, LSE = -inf
             const bool hide = __any_sync(0xffffffffu, none);
             const float inv = none ? 0.f : 1.f / l;
-            const size_t row = static_cast<size_t>(it.bh) * f.N + static_cast<size_t>(row0 + r);
-            const bool valid = r < rows;
+            const int bh = it.bh, row0 = it.r0[wg];
+            const size_t row = static_cast<size_t>(bh) * f.N + static_cast<size_t>(row0 + r);
+            const bool valid = r < it.rows[wg];
+            release();
             if constexpr (C::kStoreO) {
                 using OS = OStage<OutT, D>;
                 const uint32_t stg = sbase + C::kOffStage + static_cast<uint32_t>(wg) * C::kStageTileBytes;
@@ -530,24 +573,26 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_rules_fwd_kernel(const __gr
                 const int wq = warp & 3;
                 if (lane == 0 && staged > 0) bulk_wait_read_all();
                 __syncwarp();
-                uint32_t o[D];
-                if (n > 0) {
 #pragma unroll
-                    for (int c = 0; c < D / 32; ++c) tmem_ld32(t_o + 32u * c, *reinterpret_cast<uint32_t(*)[32]>(&o[32 * c]));
-                    tmem_ld_wait();
-                }
-                if (n == 0 || hide) {
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    if (n > 0) {
+                        tmem_ld32(t_o + static_cast<uint32_t>(c), o);
+                        tmem_ld_wait();
+                    }
+                    if (n == 0 || hide) {
 #pragma unroll
-                    for (int e = 0; e < D; ++e) o[e] = n == 0 || none ? 0u : o[e];
+                        for (int e = 0; e < 32; ++e) o[e] = n == 0 || none ? 0u : o[e];
+                    }
+                    stage_cols<OutT, D>(stg, r, c, o, inv);
                 }
-                stage_row<OutT, D>(stg, r, o, inv);
                 fence_proxy_async_shared();
                 __syncwarp();
                 if (lane == 0 && row0 + 32 * wq < f.N) {  // rows past N lie outside the map and are skipped
 #pragma unroll
                     for (int cb = 0; cb < OS::kNumCB; ++cb)
                         tma_store_3d(&f.tm_o, stg + cb * OS::kBlkBytes + wq * 32 * OS::kRowBytes, cb * OS::kElems,
-                                     row0 + 32 * wq, it.bh);
+                                     row0 + 32 * wq, bh);
                     bulk_commit_group();
                 }
                 ++staged;
@@ -582,11 +627,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_rules_fwd_kernel(const __gr
     }
 }
 
-template <int D, typename OutT>
+template <int D, int RULES, typename OutT>
 cudaError_t launch_fwd_rules_t(const FwdRulesParams& p, cudaStream_t st)
 {
     using C = RulesCfg<D, static_cast<int>(sizeof(OutT))>;
-    auto kern = fa_rules_fwd_kernel<D, OutT>;
+    auto kern = fa_rules_fwd_kernel<D, RULES, OutT>;
     static bool configured[64] = {};  // attributes set and registers checked, per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -614,10 +659,10 @@ cudaError_t launch_fwd_rules_t(const FwdRulesParams& p, cudaStream_t st)
     return launch_pdl(kern, static_cast<unsigned>(grid), kFwdThreads, C::kSmem, st, q);
 }
 
-template <int D>
+template <int D, int RULES>
 cudaError_t launch_fwd_rules_d(const FwdRulesParams& p, fa_dtype o_dtype, cudaStream_t st)
 {
-    return o_dtype == FA_F32 ? launch_fwd_rules_t<D, float>(p, st) : launch_fwd_rules_t<D, __nv_bfloat16>(p, st);
+    return o_dtype == FA_F32 ? launch_fwd_rules_t<D, RULES, float>(p, st) : launch_fwd_rules_t<D, RULES, __nv_bfloat16>(p, st);
 }
 
 }  // namespace fa

@@ -575,10 +575,13 @@ __device__ __forceinline__ void tree_scale(uint32_t (&o)[N], float alpha)
 // (fa_decode_prefix).  The prefix is read once for a block of rows of many sequences, instead of once for each; rows of
 // a sequence's own keys are the R query heads of a group.  Every unit has its parts recorded, and whole ones go to
 // buffers of their own, for the merge to join a row's two sides.
-template <int D, TreeForm FORM, bool SHARED = false>
+// RULES: kNoRules, or kCap and kBias.  (Decided at run time, they cost the calls without them half as much again:
+// PLACEHOLDER.)
+template <int D, TreeForm FORM, int RULES = -1>
 __global__ void __launch_bounds__(kTrThreads, 1)
-    fa_tree_kernel(const __grid_constant__ std::conditional_t<SHARED, PrefixParams, TreeParams> p)
+    fa_tree_kernel(const __grid_constant__ std::conditional_t<(RULES >= 0), PrefixParams, TreeParams> p)
 {
+    constexpr bool SHARED = RULES >= 0, kWithCap = SHARED && (RULES & kCap) != 0, kWithBias = SHARED && (RULES & kBias) != 0;
     using C = TrCfg<D, FORM>;
     constexpr bool ALT = FORM == kAlt, SOLO = FORM == kSolo, PAIR = FORM == kPair;
     constexpr int kStreams = SOLO ? 2 : 1;         // shares, producers, rings
@@ -954,14 +957,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         const uint32_t t_s = tmem + lane_base + C::col_s(wg);
         const uint32_t t_o = tmem + lane_base + C::col_o(wg);
         const uint32_t t_p = tmem + lane_base + C::col_p(wg);
-        bool cap = false, bias = false;
-        float cap_in = 0.f, sl2 = p.scale_log2;  // sl2: of what the exponentials take
-        if constexpr (SHARED) {
-            cap_in = p.rules.cap_in;
-            cap = cap_in > 0.f;
-            bias = p.rules.slopes != nullptr;
-            sl2 = bias ? 1.f : p.rules.mult;
-        }
+        const float sl2 = kWithCap || kWithBias ? 1.f : p.scale_log2;  // of what the exponentials take
         int tiles = 0;                 // key tiles processed by this warpgroup
         int ready[2] = {0, 0};         // segments with tiles of warpgroup 0, 1 (ALT); this warpgroup's (else, [0])
         int segs = 0, k = 0;
@@ -983,7 +979,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 const int seq0 = w.b < 0 ? (PAIR ? w.qp * 2 + wg : w.qp) * p.seqs : w.b;  // the tile's first sequence
                 row0 = w.b < 0 ? seq0 * p.R : 0;
                 rows = w.b < 0 ? min(p.seqs, p.B - seq0) * p.R : PAIR && wg > 0 ? 0 : p.R;
-                if (bias && r < rows) {
+                if (kWithBias && r < rows) {
                     const int j = r / p.R;
                     const int kvh = w.b < 0 ? w.group : w.group - w.b * p.Hkv;
                     slope2 = p.rules.slopes[kvh * p.R + (r - j * p.R)] * kLog2e;
@@ -1010,19 +1006,29 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 tree_ancestors(p.parents != nullptr ? p.parents + static_cast<size_t>(w.b) * p.T : nullptr, p.T,
                                r < rows && node < w.nodes ? node : -1, lane, p.status, vis);
             }
-            // What the rules make of N scores of keys from k0 on: their largest (mx: as loaded, of absolute values under a
-            // cap; rows that are not there take no part in what the warp decides).
+            // What the rules make of the scores x of keys from k0 on, in base 2, and their largest (mx: the largest absolute
+            // one, as loaded; rows that are not there take no part in what the warp decides).
             auto apply = [&](auto& x, float mx, int k0) -> float {
+                constexpr int N = sizeof(x) / sizeof(float);
                 if constexpr (SHARED) {
-                    constexpr int N = sizeof(x) / sizeof(float);
-                    if (cap) {
-                        if (__all_sync(0xffffffffu, r >= rows || mx * cap_in <= kTanhRange)) tanh_small<N>(x, cap_in);
-                        else tanh_any<N>(x, cap_in);
+                    const int range = kWithCap ? cap_range(p.rules, mx, r < rows) : 0;
+                    if constexpr (kWithBias) {
+                        biased_scores<N, kWithCap>(x, p.rules, range, slope2, static_cast<float>(qpos - k0), 1);
+                    } else if (range != 0) {
+#pragma unroll
+                        for (int c = 0; c < N; c += 2) {
+                            float2 y = make_float2(x[c], x[c + 1]);
+                            y = __fmul2_rn(y, cap_factor(y, p.rules.wide));
+                            x[c] = y.x;
+                            x[c + 1] = y.y;
+                        }
+                    } else {
+                        tanh_any<N>(x, p.rules.cap_in);
+#pragma unroll
+                        for (int c = 0; c < N; ++c) x[c] *= p.rules.mult;
                     }
-                    if (bias) add_bias<N>(x, p.rules.mult, slope2, static_cast<float>(qpos - k0), 1);
-                    if (cap || bias) mx = max_of<N>(x);
                 }
-                return mx;
+                return max_of<N>(x);
             };
             TreeRow row;
             // V rows past the tree may hold anything: zero them before the product reads them.  (The stage's
@@ -1053,7 +1059,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                         float mrow;
                         if constexpr (D == 128) {
                             float mh[2];
-                            if (SHARED && cap) {
+                            if constexpr (kWithCap) {
                                 tmem_ld64_absmax(t_s + 0, *reinterpret_cast<uint32_t(*)[64]>(&u[0]), mh[0]);
                                 tmem_ld64_absmax(t_s + 64, *reinterpret_cast<uint32_t(*)[64]>(&u[64]), mh[1]);
                             } else {
@@ -1064,7 +1070,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                             mrow = fmaxf(mh[0], mh[1]);
                         } else {
                             float mq[4];
-                            if (SHARED && cap) {
+                            if constexpr (kWithCap) {
 #pragma unroll
                                 for (int q = 0; q < 4; ++q)
                                     tmem_ld32_absmax(t_s + 32u * q, *reinterpret_cast<uint32_t(*)[32]>(&u[32 * q]), mq[q]);
@@ -1084,7 +1090,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                         float s[kBlockN];
 #pragma unroll
                         for (int c = 0; c < kBlockN; ++c) s[c] = __uint_as_float(u[c]);
-                        mrow = apply(s, mrow, k0);
+                        if constexpr (kWithCap || kWithBias) mrow = apply(s, mrow, k0);
                         if (k0 + kBlockN > w.prefix) mrow = tree_mask(s, k0 - w.prefix, vis);  // drafted rows, or rows past them
                         if (SHARED && r >= rows) mrow = -INFINITY;  // not a row: no reason to rescale
                         const bool rescale = __any_sync(0xffffffffu, row.grow(mrow, sl2)) && j > j0;
@@ -1153,13 +1159,13 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                         if (warp_live) {
                             uint32_t u[KS];
                             float mrow;
-                            if (SHARED && cap) tmem_ld64_absmax(t_s + KS * h, u, mrow);
+                            if constexpr (kWithCap) tmem_ld64_absmax(t_s + KS * h, u, mrow);
                             else tmem_ld64_max(t_s + KS * h, u, mrow);
                             tmem_ld_wait();
                             float s[KS];
 #pragma unroll
                             for (int c = 0; c < KS; ++c) s[c] = __uint_as_float(u[c]);
-                            mrow = apply(s, mrow, k0 + KS * h);
+                            if constexpr (kWithCap || kWithBias) mrow = apply(s, mrow, k0 + KS * h);
                             const int shift = k0 + KS * h - w.prefix;
                             if (shift > -KS) mrow = tree_mask(s, shift, vis);  // drafted rows, or rows past them
                             if (SHARED && r >= rows) mrow = -INFINITY;  // not a row: no reason to rescale
@@ -1474,11 +1480,11 @@ __global__ void __launch_bounds__(256) fa_tree_merge_kernel(const __grid_constan
     if (lane == 0 && p.lse != nullptr) p.lse[row] = live ? M + log2f(sum) * kLn2 : -INFINITY;
 }
 
-template <int D, TreeForm FORM, typename Params>
+template <int D, TreeForm FORM, int RULES, typename Params>
 cudaError_t launch_tree_main(const Params& p, cudaStream_t st)
 {
     using C = TrCfg<D, FORM>;
-    auto kern = fa_tree_kernel<D, FORM, std::is_same_v<Params, PrefixParams>>;
+    auto kern = fa_tree_kernel<D, FORM, RULES>;
     static bool configured[64] = {};  // attributes set and registers checked, per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1501,7 +1507,7 @@ cudaError_t launch_tree_main(const Params& p, cudaStream_t st)
 template <int D, TreeForm FORM>
 cudaError_t launch_tree_t(const TreeParams& p, cudaStream_t st)
 {
-    const cudaError_t e = launch_tree_main<D, FORM>(p, st);
+    const cudaError_t e = launch_tree_main<D, FORM, -1>(p, st);
     if (e != cudaSuccess) return e;
     const dim3 grid(static_cast<unsigned>(p.num_shares), static_cast<unsigned>((p.part_rows + 7) / 8));
     return launch_pdl(fa_tree_merge_kernel<D>, grid, 256, 0, st, p);
@@ -1515,11 +1521,11 @@ cudaError_t launch_tree_d(const TreeParams& p, cudaStream_t st)
 }
 
 // Decode behind a prefix: PAIR only for launches of the prefix alone (a sequence's own rows are at most 128).
-template <int D>
+template <int D, int RULES>
 cudaError_t launch_prefix_d(const PrefixParams& p, cudaStream_t st)
 {
-    if (p.part_rows > kBlockM) return launch_tree_main<D, kPair>(p, st);
-    return p.num_shares > p.num_ctas ? launch_tree_main<D, kSolo>(p, st) : launch_tree_main<D, kAlt>(p, st);
+    if (p.part_rows > kBlockM) return launch_tree_main<D, kPair, RULES>(p, st);
+    return p.num_shares > p.num_ctas ? launch_tree_main<D, kSolo, RULES>(p, st) : launch_tree_main<D, kAlt, RULES>(p, st);
 }
 
 }  // namespace fa
