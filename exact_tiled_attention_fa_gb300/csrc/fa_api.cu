@@ -425,7 +425,7 @@ fa_status fa_bwd(const void* q, const void* k, const void* v, const void* o, con
     p.wait_limit_ns = g_wait_ns.load();
     if (fa::launch_bwd(p, d, causal != 0, grad_dtype, st) != cudaSuccess) return FA_ERR_CUDA;
 
-    fa::BwdDqParams dp;
+    fa::BwdDqParams dp{};
     dp.dq_acc = dq_acc;
     dp.dq = grad_q;
     dp.BH = static_cast<int>(BH);

@@ -86,6 +86,31 @@ __global__ void __launch_bounds__(kPrepThreads) fa_bwd_prep_kernel(const BwdPrep
     }
 }
 
+// Eight consecutive gradients of dK or dV: the parts' sums, added in order.
+template <typename GradT>
+__device__ __forceinline__ void sum_parts(const BwdDqParams& p, int block)
+{
+    const bool v = block >= p.sum_blocks;
+    const long long i = (static_cast<long long>(v ? block - p.sum_blocks : block) * 128 + threadIdx.x) * 8;
+    if (i >= p.n_sum) return;
+    const float* src = (v ? p.dv_part : p.dk_part) + i;
+    float a[8] = {};
+#pragma unroll 4
+    for (int s = 0; s < p.parts; ++s, src += p.n_sum) {
+        const float4 x = __ldcs(reinterpret_cast<const float4*>(src)), y = __ldcs(reinterpret_cast<const float4*>(src) + 1);
+        a[0] += x.x, a[1] += x.y, a[2] += x.z, a[3] += x.w;
+        a[4] += y.x, a[5] += y.y, a[6] += y.z, a[7] += y.w;
+    }
+    GradT* dst = static_cast<GradT*>(v ? p.dv : p.dk) + i;
+    if constexpr (sizeof(GradT) == 4) {
+        reinterpret_cast<float4*>(dst)[0] = make_float4(a[0], a[1], a[2], a[3]);
+        reinterpret_cast<float4*>(dst)[1] = make_float4(a[4], a[5], a[6], a[7]);
+    } else {
+        *reinterpret_cast<uint4*>(dst) =
+            make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]), pack_bf16x2(a[6], a[7]));
+    }
+}
+
 // One thread per query row: reads its row from the d / 4 planes (a warp reads 512
 // contiguous bytes per plane), all of them before the first store, and writes it contiguously.
 template <typename GradT, int D>
@@ -93,6 +118,10 @@ __global__ void __launch_bounds__(128) fa_bwd_dq_kernel(const BwdDqParams p)
 {
     grid_dependency_wait();  // the accumulator is complete once the tensor-core kernel has finished
     grid_launch_dependents();
+    if (p.parts > 0 && static_cast<int>(blockIdx.x) >= p.dq_blocks) {
+        sum_parts<GradT>(p, static_cast<int>(blockIdx.x) - p.dq_blocks);
+        return;
+    }
     const long long row = static_cast<long long>(blockIdx.x) * 128 + threadIdx.x;
     if (row >= static_cast<long long>(p.BH) * p.N) return;
     const int bh = static_cast<int>(row / p.N);
@@ -124,12 +153,17 @@ cudaError_t launch_bwd_prep(const BwdPrepParams& p, fa_dtype o_dtype, cudaStream
     return launch_pdl(fa_bwd_prep_kernel<__nv_bfloat16>, static_cast<unsigned>(blocks), kPrepThreads, 0, st, p);
 }
 
-cudaError_t launch_bwd_dq(const BwdDqParams& p, fa_dtype grad_dtype, cudaStream_t st)
+cudaError_t launch_bwd_dq(const BwdDqParams& given, fa_dtype grad_dtype, cudaStream_t st)
 {
+    BwdDqParams p = given;
     const long long rows = static_cast<long long>(p.BH) * p.N;
-    const long long blocks = (rows + 127) / 128;
+    const long long dq_blocks = (rows + 127) / 128;
+    const long long sum_blocks = p.parts > 0 ? (p.n_sum / 8 + 127) / 128 : 0;
+    const long long blocks = dq_blocks + 2 * sum_blocks;
     if (blocks <= 0) return cudaSuccess;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    p.dq_blocks = static_cast<int>(dq_blocks);
+    p.sum_blocks = static_cast<int>(sum_blocks);
     const unsigned g = static_cast<unsigned>(blocks);
     const bool f32 = grad_dtype == FA_F32;
     switch (p.d) {

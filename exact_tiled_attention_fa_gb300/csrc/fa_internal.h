@@ -103,6 +103,13 @@ struct BwdDqParams {
     const float* dq_acc;
     void* dq;           // [B*H][N][d], gradient dtype
     int BH, N, Tr, d;
+    // blocks from dq_blocks on add up parts of dK and dV (fa_bwd_rules): out[i] = sum over parts of part[p][i], in order,
+    // for i < n_sum (a multiple of 32)
+    const float *dk_part, *dv_part;
+    void *dk, *dv;
+    long long n_sum;
+    int parts;          // 0: none
+    int dq_blocks, sum_blocks;  // set by the launcher
 };
 
 cudaError_t launch_bwd(const BwdParams& p, int d, bool causal, fa_dtype grad_dtype, cudaStream_t st);
@@ -265,8 +272,8 @@ struct ScoreRules {
     float mult;           // capped scores in base 2 are mult * tanh, others mult * S: cap or scale, times log2(e)
     const float* slopes;  // fp32 [Hq] or nullptr
     // tanh(cap_in * S), times mult except in the backward, as S P(S^2) (fa_rules_common.cuh, cap_factor)
-    float near[3], wide[5];
-    float near_in, wide_in;  // cap_in over the polynomials' ranges: |S| times it is at most 1 where they hold; +inf: nowhere
+    float2 near[3], mid[4], wide[6];  // (each twice, as the two-wide operations take them)
+    float near_in, mid_in, wide_in;  // cap_in over the polynomials' ranges: |S| times it is at most 1 where they hold; +inf: nowhere
 };
 
 // A run of equal document numbers, and what a query or a key has of it (fa_rules_ranges_kernel).
@@ -315,16 +322,6 @@ struct BwdRulesParams {
 
 template <int D, int RULES>
 cudaError_t launch_bwd_rules(const BwdRulesParams& p, fa_dtype grad_dtype, cudaStream_t st);
-
-// out[i] = sum over parts of part[p][i], in order, for i < n (a multiple of 32); both of dK and dV.
-struct RulesSumParams {
-    const float *dk_part, *dv_part;
-    void *dk, *dv;
-    long long n;
-    int parts;
-};
-
-cudaError_t launch_rules_sum(const RulesSumParams& p, fa_dtype grad_dtype, cudaStream_t st);
 
 // Decode behind a shared prefix (fa_tree_kernel.cuh, SHARED).  Units are a key/value head's prefix with a block of the
 // batch's rows, and then a sequence's own keys with its R rows: either kind may be left to another launch.  Of the

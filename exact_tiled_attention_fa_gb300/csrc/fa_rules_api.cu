@@ -1,49 +1,12 @@
-// fa_rules_api.cu -- the C ABI of attention under score rules (include/fa.h): forward, backward.  Argument checks,
-// workspace layout and dispatch, host code only; and the kernel that adds up the parts of shared heads' gradients.
+// fa_rules_api.cu -- the C ABI of attention under score rules (include/fa.h): forward, backward, decode behind
+// a shared prefix.  Argument checks,
+// workspace layout and dispatch, host code only.
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
 
 #include "fa_internal.h"
 #include "fa_rules_common.cuh"
-
-namespace fa {
-
-// A thread for 8 consecutive gradients of dK (blockIdx.y 0) or dV (1): the parts are added in order.
-template <typename GradT>
-__global__ void __launch_bounds__(256) fa_rules_sum_kernel(const RulesSumParams p)
-{
-    grid_dependency_wait();
-    grid_launch_dependents();
-    const long long i = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) * 8;
-    if (i >= p.n) return;
-    const float* src = (blockIdx.y == 0 ? p.dk_part : p.dv_part) + i;
-    float a[8] = {};
-    for (int s = 0; s < p.parts; ++s, src += p.n) {
-        const float4 x = __ldcs(reinterpret_cast<const float4*>(src)), y = __ldcs(reinterpret_cast<const float4*>(src) + 1);
-        a[0] += x.x, a[1] += x.y, a[2] += x.z, a[3] += x.w;
-        a[4] += y.x, a[5] += y.y, a[6] += y.z, a[7] += y.w;
-    }
-    GradT* dst = static_cast<GradT*>(blockIdx.y == 0 ? p.dk : p.dv) + i;
-    if constexpr (sizeof(GradT) == 4) {
-        reinterpret_cast<float4*>(dst)[0] = make_float4(a[0], a[1], a[2], a[3]);
-        reinterpret_cast<float4*>(dst)[1] = make_float4(a[4], a[5], a[6], a[7]);
-    } else {
-        *reinterpret_cast<uint4*>(dst) =
-            make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]), pack_bf16x2(a[6], a[7]));
-    }
-}
-
-cudaError_t launch_rules_sum(const RulesSumParams& p, fa_dtype grad_dtype, cudaStream_t st)
-{
-    const long long blocks = (p.n / 8 + 255) / 256;
-    if (blocks <= 0 || blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    const dim3 grid(static_cast<unsigned>(blocks), 2);
-    return grad_dtype == FA_F32 ? launch_pdl(fa_rules_sum_kernel<float>, grid, 256, 0, st, p)
-                                : launch_pdl(fa_rules_sum_kernel<__nv_bfloat16>, grid, 256, 0, st, p);
-}
-
-}  // namespace fa
 
 namespace {
 
@@ -82,17 +45,20 @@ bool make_rules(fa::ScoreRules* r, float scale, float softcap, const float* slop
     r->mult = (softcap > 0.f ? softcap : scale) * fa::kLog2e;
     r->slopes = slopes;
     if (!(std::isfinite(r->mult) && r->mult > 0.f && std::isfinite(r->cap_in)) || (softcap > 0.f && r->cap_in == 0.f)) return false;
-    r->near_in = r->wide_in = INFINITY;
-    // powers of cap_in up to the ninth must be normal numbers, with mult in them too
-    if (r->cap_in < 1e-4f || r->cap_in > 1e3f) return true;
-    const double near[] = {FA_TANH_NEAR}, wide[] = {FA_TANH_WIDE}, k = r->cap_in;
+    r->near_in = r->mid_in = r->wide_in = INFINITY;
+    // the polynomials' coefficients, powers of cap_in up to the seventh and the eleventh, must be normal numbers
+    const double near[] = {FA_TANH_NEAR}, mid[] = {FA_TANH_MID}, wide[] = {FA_TANH_WIDE}, k = r->cap_in;
+    if (k < 1e-5 || k > 1e2) return true;
     double at = k * (score ? r->mult : 1.0);
-    for (int i = 0; i < 5; ++i, at *= k * k) {
-        if (i < 3) r->near[i] = static_cast<float>(near[i] * at);
-        r->wide[i] = static_cast<float>(wide[i] * at);
+    for (int i = 0; i < 6; ++i, at *= k * k) {
+        auto twice = [&](double c) { return make_float2(static_cast<float>(c * at), static_cast<float>(c * at)); };
+        if (i < 3) r->near[i] = twice(near[i]);
+        if (i < 4) r->mid[i] = twice(mid[i]);
+        r->wide[i] = twice(wide[i]);
     }
     r->near_in = r->cap_in / fa::kNearRange;
-    r->wide_in = r->cap_in / fa::kWideRange;
+    r->mid_in = r->cap_in / fa::kMidRange;
+    if (k >= 8e-4) r->wide_in = r->cap_in / fa::kWideRange;
     return true;
 }
 
@@ -277,13 +243,16 @@ fa_status fa_bwd_rules(const void* q, const void* k, const void* v, const void* 
     p.n_items = B * Hkv * parts * Tc;
     const cudaError_t e = by_kind(d, p.rules, [&](auto D, auto kind) { return fa::launch_bwd_rules<D(), kind()>(p, kv_type, st); });
     if (e != cudaSuccess) return FA_ERR_CUDA;
-    const fa::BwdDqParams dp{dq_acc, grad_q, B * Hq, N, Tr, d};
-    if (fa::launch_bwd_dq(dp, grad_dtype, st) != cudaSuccess) return FA_ERR_CUDA;
+    fa::BwdDqParams dp{dq_acc, grad_q, B * Hq, N, Tr, d};
     if (parts > 1) {
-        const fa::RulesSumParams sp{dk_part, dv_part, grad_k, grad_v, static_cast<long long>(n_sum), parts};
-        if (fa::launch_rules_sum(sp, grad_dtype, st) != cudaSuccess) return FA_ERR_CUDA;
+        dp.dk_part = dk_part;
+        dp.dv_part = dv_part;
+        dp.dk = grad_k;
+        dp.dv = grad_v;
+        dp.n_sum = static_cast<long long>(n_sum);
+        dp.parts = parts;
     }
-    return FA_OK;
+    return fa::launch_bwd_dq(dp, grad_dtype, st) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // extern "C"

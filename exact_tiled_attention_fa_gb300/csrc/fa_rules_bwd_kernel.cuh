@@ -11,8 +11,8 @@
 // 128-key tile whose dK and dV stay in tensor memory while Q and dO tiles pass by).  What differs:
 //  - An item is a key tile of a key/value head and walks the query tiles of several of its query heads, one head
 //    after the other, so that their dK and dV are added up in tensor memory.  With few items (long sequences with few
-//    key/value heads) a group's query heads are divided over `parts` items, whose fp32 dK and dV a last kernel adds
-//    up in order (launch_rules_sum): PLACEHOLDER.
+//    key/value heads) a group's query heads are divided over `parts` items, whose fp32 dK and dV the last kernel adds
+//    up in order.
 //  - Items' lengths depend on masks and documents: each CTA asks a counter for its next one, in an order that is
 //    head by head and, with a causal mask, from a head's longest item to its shortest.  The producer hands items to
 //    the other roles by records in shared memory.
@@ -35,6 +35,11 @@ struct RulesBwdItem {
     int prefix;           // of the sequence
 };
 enum : int { kBbItemFull = kBbCount, kBbItemEmpty = kBbItemFull + kRulesItems, kRulesBbCount = kBbItemEmpty + kRulesItems };
+
+// Registers after the split (fa_bwd_kernel.cuh): with its 184 / 80 / 64 the control and dQ warps spill up to 290 bytes.
+constexpr int kRulesBwdComputeRegs = 168;
+constexpr int kRulesBwdControlRegs = 104;
+constexpr int kRulesBwdDqRegs = 72;
 
 template <int D>
 struct RulesBwdCfg : BwdCfg<D> {
@@ -77,8 +82,8 @@ __device__ __forceinline__ RulesBwdItem rules_bwd_item(const BwdRulesParams& rp,
     return it;
 }
 
-// P and P times the cap's slope for 64 scores of one key (columns: queries).  CAP: -1 none, else the range that cap_range
-// found.  BIAS: -slope2 |dist + c|; sign 1 where dist + c >= 0 in every column that counts, -1 where <= 0, 0 either.
+// P and P times the cap's slope for 64 scores of one key (columns: queries).  CAP: -1 none, 3 the near and 2 the
+// middle range (cap_range), 0 any.  BIAS: -slope2 |dist + c|; sign 1 where dist + c >= 0 in every column that counts, -1 where <= 0, 0 either.
 template <int CAP, bool BIAS>
 __device__ __forceinline__ void rules_weights(const uint32_t (&u)[64], float (&pf)[64], uint32_t (&pk)[32], uint32_t l_addr,
                                               const ScoreRules& r, float slope2, float dist, int sign)
@@ -107,8 +112,8 @@ __device__ __forceinline__ void rules_weights(const uint32_t (&u)[64], float (&p
                 for (int e = 0; e < 2; ++e) {
                     const int i = c + 2 * (h + e);
                     float2 y = make_float2(t[i], t[i + 1]);
-                    if constexpr (CAP == 2) y = __fmul2_rn(y, cap_factor(y, r.near));
-                    if constexpr (CAP == 1) y = __fmul2_rn(y, cap_factor(y, r.wide));
+                    if constexpr (CAP == 3) y = __fmul2_rn(y, cap_factor(y, r.near));
+                    if constexpr (CAP == 2) y = __fmul2_rn(y, cap_factor(y, r.mid));
                     float2 x = __ffma2_rn(y, m2, e == 0 ? make_float2(-l4.x, -l4.y) : make_float2(-l4.z, -l4.w));
                     if constexpr (BIAS) {
                         if (sign != 0) {
@@ -229,7 +234,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) fa_rules_bwd_kernel(const __gr
     grid_dependency_wait();
 
     if (warp >= 8 && warp < 12) {
-        regs_decrease<kBwdControlRegs>();
+        regs_decrease<kRulesBwdControlRegs>();
         if (warp == kBwdWarpProducer && lane == 0) {
             // ============================================================ producer
             prefetch_tensormap(&p.tm_q);
@@ -423,7 +428,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) fa_rules_bwd_kernel(const __gr
             mbar_wait(bar(kBbDrain + me), 0, kDrainLimitNs, nullptr);
         }
     } else if (warp >= kBwdWarpDq) {
-        regs_decrease<kBwdDqRegs>();
+        regs_decrease<kRulesBwdDqRegs>();
         // ============================================================ dQ reduction
         const int r = threadIdx.x & 127;  // query row of the tile == TMEM lane
         const uint32_t t_dq = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + C::kColDQ;
@@ -512,7 +517,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) fa_rules_bwd_kernel(const __gr
         }
         if (!ok && !*abort_flag) record_failure(p.status, abort_flag, FA_ERR_TIMEOUT);
     } else {
-        regs_increase<kBwdComputeRegs>();
+        regs_increase<kRulesBwdComputeRegs>();
         // ============================================================ compute
         const int h = warp >> 2;                 // query half of the tile
         const int kr = threadIdx.x & 127;        // key row of the tile == TMEM lane
@@ -600,8 +605,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) fa_rules_bwd_kernel(const __gr
                            : __all_sync(0xffffffffu, off + q0 + 63 <= key)                             ? -1
                                                                                                        : 0;
                 const float dist = static_cast<float>(off + q0 - key);
-                if (kWithCap && range == 2) rules_weights<2, kWithBias>(u, pf, pk, l_addr, rp.rules, slope2, dist, sign);
-                else if (kWithCap && range == 1) rules_weights<1, kWithBias>(u, pf, pk, l_addr, rp.rules, slope2, dist, sign);
+                if (kWithCap && range == 3) rules_weights<3, kWithBias>(u, pf, pk, l_addr, rp.rules, slope2, dist, sign);
+                else if (kWithCap && range == 2) rules_weights<2, kWithBias>(u, pf, pk, l_addr, rp.rules, slope2, dist, sign);
                 else rules_weights<kWithCap ? 0 : -1, kWithBias>(u, pf, pk, l_addr, rp.rules, slope2, dist, sign);
                 if (!__all_sync(0xffffffffu, qa <= q0 && qe >= q0 + 64)) {  // hidden pairs: P = 0
 #pragma unroll
@@ -784,7 +789,7 @@ cudaError_t launch_bwd_rules_t(const BwdRulesParams& p, cudaStream_t st)
         cudaFuncAttributes attr;
         e = cudaFuncGetAttributes(&attr, kern);
         if (e != cudaSuccess) return e;
-        if (attr.numRegs * kBwdThreads < 256 * kBwdComputeRegs + 128 * (kBwdControlRegs + kBwdDqRegs))
+        if (attr.numRegs * kBwdThreads < 256 * kRulesBwdComputeRegs + 128 * (kRulesBwdControlRegs + kRulesBwdDqRegs))
             return cudaErrorLaunchOutOfResources;  // the register split would not fit
         configured[dev] = true;
     }

@@ -26,28 +26,29 @@ __device__ __forceinline__ float rcp_approx(float x)
 }
 
 // The cap.  tanh(u) for |u| <= kWideRange, where the scores that a cap is meant for almost always are, is u P(u^2) with
-// P the minimax polynomial for tanh(u) / u (Remez exchange on u^2): degree 2 up to kNearRange (relative error 1.2e-6),
-// degree 4 up to kWideRange (5.7e-7).  With cap_in and mult in its coefficients a capped score is S Q(S^2): n + 1
+// P the minimax polynomial for tanh(u) / u (Remez exchange on u^2): degree n = 2 up to kNearRange (relative error
+// 1.2e-6), 3 up to kMidRange (1.1e-6), 5 up to kWideRange (5.9e-7).  With cap_in and mult in its coefficients a capped score is S Q(S^2): n + 1
 // operations and the one that takes the maximum off it anyway.  (What bounds them is the FMA units, 128 lanes an SM,
 // whether two operations go in one instruction or not: a polynomial of degree 5 for every argument, scaled before it,
 // took 8 and the causal prefill of 4 sequences of 4097 tokens, 16 heads of 128, 487 us; without a cap 341; PLACEHOLDER.)
 // Other arguments take 1 - 2 / (1 + e^2u): two operations of the special function unit that the exponentials also need
 // (586 us); its absolute error of 2e-7 is one of 1e-5 of a weight at a cap of 50.  +-infinity gives +-1, NaN NaN.  (The
 // device's own tanh instruction is off by 2^-11 of its result: at a score of 20 by 0.01, and the weight by as much.)
-constexpr float kNearRange = 0.3f, kWideRange = 0.75f;
+constexpr float kNearRange = 0.3f, kMidRange = 0.55f, kWideRange = 1.f;
 #define FA_TANH_NEAR 0.999998838848, -0.333100215997, 0.126339459894
-#define FA_TANH_WIDE 0.999999434926, -0.33328251533, 0.132589832157, -0.0500563024273, 0.0129296321186
+#define FA_TANH_MID 0.999998880298, -0.333213872584, 0.131312313762, -0.0426959989808
+#define FA_TANH_WIDE 0.999999413602, -0.333290423701, 0.132814338124, -0.051605672318, 0.0167431133877, -0.00306705973621
 
 __device__ __forceinline__ float2 two(float x) { return make_float2(x, x); }
 
 // Q of a pair of scores; a capped score is s * Q.
 template <int N>
-__device__ __forceinline__ float2 cap_factor(float2 s, const float (&c)[N])
+__device__ __forceinline__ float2 cap_factor(float2 s, const float2 (&c)[N])
 {
     const float2 w = __fmul2_rn(s, s);
-    float2 q = two(c[N - 1]);
+    float2 q = c[N - 1];
 #pragma unroll
-    for (int i = N - 2; i >= 0; --i) q = __ffma2_rn(w, q, two(c[i]));
+    for (int i = N - 2; i >= 0; --i) q = __ffma2_rn(w, q, c[i]);
     return q;
 }
 
@@ -60,11 +61,35 @@ __device__ __forceinline__ void tanh_any(float* s, float k)
     for (int c = 0; c < N; ++c) s[c] = fmaf(-2.f, rcp_approx(1.f + ex2(s[c] * k2)), 1.f);
 }
 
-// Whether every lane's |S| (its largest, mx) lies in the polynomials' ranges: 2 the near one, 1 the wide one, 0 neither.
+// Whether every lane's |S| (its largest, mx) lies in the polynomials' ranges: 3 the near one, 2 the middle one, 1 the wide
+// one, 0 none.
 __device__ __forceinline__ int cap_range(const ScoreRules& r, float mx, bool counts = true)
 {
-    if (__all_sync(0xffffffffu, !counts || mx * r.near_in <= 1.f)) return 2;
+    if (__all_sync(0xffffffffu, !counts || mx * r.near_in <= 1.f)) return 3;
+    if (__all_sync(0xffffffffu, !counts || mx * r.mid_in <= 1.f)) return 2;
     return __all_sync(0xffffffffu, !counts || mx * r.wide_in <= 1.f) ? 1 : 0;
+}
+
+// Scores s of N keys under a cap, in base 2, in place.
+template <int N>
+__device__ __forceinline__ void capped_scores(float* s, const ScoreRules& r, int range)
+{
+    auto poly = [&](const auto& c) {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            const float2 x = make_float2(s[i], s[i + 1]);
+            const float2 y = __fmul2_rn(x, cap_factor(x, c));
+            s[i] = y.x;
+            s[i + 1] = y.y;
+        }
+    };
+    if (range >= 2) poly(r.mid);
+    else if (range == 1) poly(r.wide);
+    else {
+        tanh_any<N>(s, r.cap_in);
+#pragma unroll
+        for (int i = 0; i < N; ++i) s[i] *= r.mult;
+    }
 }
 
 // s <- f(s, -slope2 * |dist - c|) by pairs, for columns c = 0 .. N - 1 (dist: the position of the row less that of column
@@ -110,10 +135,8 @@ __device__ __forceinline__ void add_bias(float* s, float slope2, float dist, int
 template <int N, bool CAP>
 __device__ __forceinline__ void biased_scores(float* s, const ScoreRules& r, int range, float slope2, float dist, int sign)
 {
-    if (CAP && range == 2) {
-        add_bias<N>(s, slope2, dist, sign, [&](float2 x, float2 b) { return __ffma2_rn(x, cap_factor(x, r.near), b); });
-    } else if (CAP && range == 1) {
-        add_bias<N>(s, slope2, dist, sign, [&](float2 x, float2 b) { return __ffma2_rn(x, cap_factor(x, r.wide), b); });
+    if (CAP && range >= 2) {
+        add_bias<N>(s, slope2, dist, sign, [&](float2 x, float2 b) { return __ffma2_rn(x, cap_factor(x, r.mid), b); });
     } else {
         if (CAP) tanh_any<N>(s, r.cap_in);
         add_bias<N>(s, slope2, dist, sign, [&](float2 x, float2 b) { return __ffma2_rn(x, two(r.mult), b); });

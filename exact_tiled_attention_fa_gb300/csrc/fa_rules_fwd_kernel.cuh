@@ -368,7 +368,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_rules_fwd_kernel(const __gr
         const int off = f.Nk - f.N;
         int tiles = 0;   // (query tile, key tile) pairs processed by this warpgroup
         int uses = 0;    // items in which this warpgroup had key tiles
-        int staged = 0;  // output tiles this warpgroup wrote through the staging tile
         bool ok = true;
 
         for (int k = 0; ok; ++k) {
@@ -475,13 +474,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_rules_fwd_kernel(const __gr
                     if (!C::kAliasP && j > a) pv_ready = mbar_test(bar(kBarPVDone + wg), (tiles - 1) & 1);
                 };
                 const int range = kWithCap ? cap_range(p.rules, mrow) : 0;
-                if (kWithCap && !kWithBias && range != 0 && !mask) {
+                if (kWithCap && !kWithBias && range == 3 && !mask) {
                     // tanh rises with its argument: the largest raw score is the largest capped one
                     const float2 top = two(max_of<kBlockN>(s));
-                    raise(__fmul2_rn(top, range == 2 ? cap_factor(top, p.rules.near) : cap_factor(top, p.rules.wide)).x);
+                    raise(__fmul2_rn(top, cap_factor(top, p.rules.near)).x);
                     test_pv();
-                    if (range == 2) weigh([&](float2 x, float2 m) { return __ffma2_rn(x, cap_factor(x, p.rules.near), m); });
-                    else weigh([&](float2 x, float2 m) { return __ffma2_rn(x, cap_factor(x, p.rules.wide), m); });
+                    weigh([&](float2 x, float2 m) { return __ffma2_rn(x, cap_factor(x, p.rules.near), m); });
                 } else {
                     if constexpr (kWithBias) {
                         // keys behind a causal row's position are hidden below, whatever bias they get
@@ -489,19 +487,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_rules_fwd_kernel(const __gr
                         const bool behind = __all_sync(0xffffffffu, k0 >= qpos);
                         biased_scores<kBlockN, kWithCap>(s, p.rules, range, slope2, static_cast<float>(qpos - k0), before ? 1 : behind ? -1 : 0);
                     } else if constexpr (kWithCap) {
-                        if (range != 0) {
-#pragma unroll
-                            for (int c = 0; c < kBlockN; c += 2) {
-                                float2 x = make_float2(s[c], s[c + 1]);
-                                x = __fmul2_rn(x, cap_factor(x, p.rules.wide));
-                                s[c] = x.x;
-                                s[c + 1] = x.y;
-                            }
-                        } else {
-                            tanh_any<kBlockN>(s, p.rules.cap_in);
-#pragma unroll
-                            for (int c = 0; c < kBlockN; ++c) s[c] *= p.rules.mult;
-                        }
+                        capped_scores<kBlockN>(s, p.rules, range);
                     }
                     if (mask) rules_mask(s, lo - k0, hi - k0);
                     if (RULES != kNoRules || mask) mrow = max_of<kBlockN>(s);
@@ -571,7 +557,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_rules_fwd_kernel(const __gr
                 // Each warp stages its 32 rows and stores them itself (a 32-row box): lane 0 first waits until the
                 // warp's previous store has read its rows (issued one item ago, long done).
                 const int wq = warp & 3;
-                if (lane == 0 && staged > 0) bulk_wait_read_all();
+                if (lane == 0) bulk_wait_read_all();
                 __syncwarp();
 #pragma unroll
                 for (int c = 0; c < D; c += 32) {
@@ -595,7 +581,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_rules_fwd_kernel(const __gr
                                      row0 + 32 * wq, bh);
                     bulk_commit_group();
                 }
-                ++staged;
             } else {
                 OutT* orow = reinterpret_cast<OutT*>(f.o) + row * D;
 #pragma unroll
@@ -614,7 +599,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_rules_fwd_kernel(const __gr
             if (valid && f.lse != nullptr) f.lse[row] = none ? -INFINITY : (m_run + lg2_approx(l)) * kLn2;
         }
         // Bulk stores must finish before the CTA's shared memory goes away.
-        if (C::kStoreO && lane == 0 && staged > 0) bulk_wait_all();
+        if (C::kStoreO && lane == 0) bulk_wait_all();
         if (!ok && !*abort_flag) record_failure(f.status, abort_flag, FA_ERR_TIMEOUT);
     }
 

@@ -1014,18 +1014,8 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                     const int range = kWithCap ? cap_range(p.rules, mx, r < rows) : 0;
                     if constexpr (kWithBias) {
                         biased_scores<N, kWithCap>(x, p.rules, range, slope2, static_cast<float>(qpos - k0), 1);
-                    } else if (range != 0) {
-#pragma unroll
-                        for (int c = 0; c < N; c += 2) {
-                            float2 y = make_float2(x[c], x[c + 1]);
-                            y = __fmul2_rn(y, cap_factor(y, p.rules.wide));
-                            x[c] = y.x;
-                            x[c + 1] = y.y;
-                        }
                     } else {
-                        tanh_any<N>(x, p.rules.cap_in);
-#pragma unroll
-                        for (int c = 0; c < N; ++c) x[c] *= p.rules.mult;
+                        capped_scores<N>(x, p.rules, range);
                     }
                 }
                 return max_of<N>(x);
