@@ -298,6 +298,7 @@ struct FwdRulesParams {
     const int2* tile;
     int* counter;       // with documents: work items handed out
     int Hq, Hkv, causal;
+    int chunk;          // causal, without documents: items go out by as many query heads at a time, longest first
 };
 
 // The kernels under score rules are compiled for each head size and kind of rules: kCap, kBias, both or neither.
@@ -318,6 +319,8 @@ struct BwdRulesParams {
     int parts, part_heads;  // items that share a key tile's query heads, and query heads of each; with parts > 1 tm_dk,
                             // tm_dv, dk and dv are fp32 sums [parts][B * Hkv][Nk][d]
     int n_items;            // B * Hkv * parts * Tc
+    int chunk;              // items go out by as many (key/value head, part)s at a time: of all of these the first key tile,
+                            // then the second ..; 1: head by head
 };
 
 template <int D, int RULES>

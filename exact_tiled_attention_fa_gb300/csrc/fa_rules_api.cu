@@ -97,15 +97,39 @@ fa_status check_rules(const void* q, const void* k, const void* v, const float* 
     return FA_OK;
 }
 
-// Items of the backward that share a key tile's R query heads.
-int bwd_parts(int B, int Hkv, int R, int Nk, int sms)
+// As many of `heads` at a time as the L2 (129 MB) holds the data of, `bytes` each, but at least kAtOnce: with fewer
+// heads than CTAs some share what they read all the same.  In chunks of one size.  (4 sequences of 4097 tokens, 16 heads,
+// causal: forward d = 64 all 64 heads at once 155 us, 44 181; d = 128 285, 32 heads 303; backward d = 128 799, 15 heads
+// 844.  64 sequences of 1024, d = 64: 128, 183 and single heads within 2 %.)
+constexpr long long kAtOnce = 100;
+int chunk_of(long long heads, long long bytes)
 {
-    const long long items = static_cast<long long>(B) * Hkv * tiles_of(Nk);
-    long long parts = (3LL * sms + items - 1) / items;
-    if (parts > R) parts = R;
-    if (parts < 1) parts = 1;
-    const int heads = (R + static_cast<int>(parts) - 1) / static_cast<int>(parts);
-    return (R + heads - 1) / heads;
+    long long n = (96LL << 20) / bytes;
+    if (n < kAtOnce) n = kAtOnce;
+    const long long chunks = (heads + n - 1) / n;
+    return static_cast<int>((heads + chunks - 1) / chunks);
+}
+
+// Items of the backward that share a key tile's R query heads: the number for which an estimate of the longest CTA's
+// time is least, counted in steps of one query tile with one key tile (about 0.008 d us).  Equal items (`uniform`: no
+// causal mask and no documents) come in rounds of one for each CTA; others are handed out one by one, and the
+// last to end is up to the longest item behind the mean.  An item's start and end take 3 steps; the
+// parts' sums go out and in again, half of it past the L2.  Measured, us for 1 / 2 / 4 parts, causal but the last: 32/4
+// heads of 128, 8192 tokens 2575 / 1931 / 1631; 16/4, 4097 tokens 443 / 431 / 339; 8 sequences of 1024, 32/8 heads
+// 349 / 377 / -; without a mask 2048 tokens, 32/8 heads 218 / - / 238.
+int bwd_parts(int B, int Hkv, int R, int N, int Nk, bool uniform, int sms)
+{
+    const double groups = static_cast<double>(B) * Hkv, Tr = tiles_of(N), Tc = tiles_of(Nk);
+    int best = 1;
+    double least = INFINITY;
+    for (int heads = R; heads >= 1; heads = heads > 8 ? heads / 2 : heads - 1) {
+        const int parts = (R + heads - 1) / heads;
+        const double items = groups * parts * Tc, item = heads * Tr + 3;
+        const double sums = parts > 1 ? parts * groups * Nk * 1.5e-4 : 0;
+        const double steps = uniform ? std::ceil(items / sms) * item : (groups * R * Tr * Tc / 2 + 3 * items) / sms + item;
+        if (steps + sums < least) least = steps + sums, best = parts;
+    }
+    return best;
 }
 
 }  // namespace
@@ -149,6 +173,7 @@ fa_status fa_fwd_rules(const void* q, const void* k, const void* v, const float*
     p.Hq = Hq;
     p.Hkv = Hkv;
     p.causal = causal;
+    p.chunk = chunk_of(B * Hkv, 4LL * Nk * d) * (Hq / Hkv);
     if (documents != nullptr) {
         const Ranges r(static_cast<char*>(workspace), B, N);
         const fa::RangesParams rp{documents, prefix_lens, r.each, r.tile, r.counter, f.status, B, N, Nk, tiles_of(N), causal};
@@ -164,7 +189,8 @@ fa_status fa_fwd_rules(const void* q, const void* k, const void* v, const float*
 size_t fa_bwd_rules_workspace_size(int B, int Hq, int Hkv, int N, int Nk, int d, int num_sms)
 {
     if (B <= 0 || Hq <= 0 || Hkv <= 0 || N <= 0 || Nk <= 0 || d <= 0 || num_sms <= 0 || Hq % Hkv != 0) return 0;
-    const int parts = bwd_parts(B, Hkv, Hq / Hkv, Nk, num_sms);
+    const int even = bwd_parts(B, Hkv, Hq / Hkv, N, Nk, true, num_sms), other = bwd_parts(B, Hkv, Hq / Hkv, N, Nk, false, num_sms);
+    const int parts = even > other ? even : other;  // whatever the masks
     const size_t sums = parts > 1 ? 2 * round_up(static_cast<size_t>(parts) * B * Hkv * Nk * d * sizeof(float), kAlign) : 0;
     return fa_bwd_workspace_size(B, Hq, N, d) + ranges_size(B, Nk) + sums;
 }
@@ -189,7 +215,7 @@ fa_status fa_bwd_rules(const void* q, const void* k, const void* v, const void* 
     if (fa::device_status_word(&b.status) != cudaSuccess || fa::device_sm_count(&b.num_ctas) != cudaSuccess) return FA_ERR_CUDA;
     if (ws_bytes < fa_bwd_rules_workspace_size(B, Hq, Hkv, N, Nk, d, b.num_ctas)) return FA_ERR_WORKSPACE;
     const int R = Hq / Hkv, Tr = tiles_of(N), Tc = tiles_of(Nk);
-    const int parts = bwd_parts(B, Hkv, R, Nk, b.num_ctas);
+    const int parts = bwd_parts(B, Hkv, R, N, Nk, causal == 0 && documents == nullptr, b.num_ctas);
     // workspace: fa_bwd's (dQ accumulator, log-sum-exps, row terms), the documents' ranges, the parts' sums
     char* ws = static_cast<char*>(workspace);
     const size_t rows = static_cast<size_t>(B) * Hq * Tr * fa::kBlockM;
@@ -239,8 +265,9 @@ fa_status fa_bwd_rules(const void* q, const void* k, const void* v, const void* 
     p.Hkv = Hkv;
     p.causal = causal;
     p.parts = parts;
-    p.part_heads = (R + parts - 1) / parts;
+    p.part_heads = (R + parts - 1) / parts;  // (the heads that this number of parts was made from)
     p.n_items = B * Hkv * parts * Tc;
+    p.chunk = causal != 0 || documents != nullptr ? chunk_of(B * Hkv * parts, 8LL * N * d * p.part_heads) : 1;
     const cudaError_t e = by_kind(d, p.rules, [&](auto D, auto kind) { return fa::launch_bwd_rules<D(), kind()>(p, kv_type, st); });
     if (e != cudaSuccess) return FA_ERR_CUDA;
     fa::BwdDqParams dp{dq_acc, grad_q, B * Hq, N, Tr, d};

@@ -13,9 +13,12 @@
 //    after the other, so that their dK and dV are added up in tensor memory.  With few items (long sequences with few
 //    key/value heads) a group's query heads are divided over `parts` items, whose fp32 dK and dV the last kernel adds
 //    up in order.
-//  - Items' lengths depend on masks and documents: each CTA asks a counter for its next one, in an order that is
-//    head by head and, with a causal mask, from a head's longest item to its shortest.  The producer hands items to
-//    the other roles by records in shared memory.
+//  - Items' lengths depend on masks and documents: each CTA asks a counter for its next one.  Where they differ, they
+//    go out key tile by key tile (with a causal mask the longest first) over as many heads at a time as the L2 holds
+//    the Q, dO and dQ of, so that short ones fill the end: causal, 4097 tokens, 16 heads of 64 and 128 head by head 151
+//    and 287 us, so 111 and 212.  (64 sequences of 1024 tokens, whose 268 MB of Q and dO the L2 does not hold, all at
+//    once 740 us, head by head 613; chunk_of in fa_rules_api.cu.)  The producer hands items to the other roles by
+//    records in shared memory.
 //  - P's recomputation has the cap and the bias, and dS the cap's slope, made beside P from the same tanh.
 //
 // What bounds it: as in fa_bwd_kernel.cuh the chain S -> P -> dV and dP -> dS -> dK, dQ between the roles, lengthened by
@@ -56,8 +59,10 @@ __device__ __forceinline__ RulesBwdItem rules_bwd_item(const BwdRulesParams& rp,
 {
     const BwdParams& p = rp.b;
     RulesBwdItem it;
-    const int group = item / p.Tc;  // (key/value head, part)
-    const int j = item - group * p.Tc;
+    const int first = item / (rp.chunk * p.Tc) * rp.chunk;              // of the chunk of (key/value head, part)s
+    const int many = min(rp.chunk, rp.n_items / p.Tc - first);
+    const int at = item - first * p.Tc;
+    const int j = at / many, group = first + at - j * many;
     const int part = group % rp.parts;
     const int R = rp.Hq / rp.Hkv;
     it.kv = group / rp.parts;

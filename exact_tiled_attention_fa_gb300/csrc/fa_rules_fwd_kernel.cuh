@@ -10,9 +10,11 @@
 // The tiles, roles, tensor memory, pipeline and bounded waits are those of fa_fwd_kernel.cuh (two query tiles of 128
 // rows share a ring of K and V tiles; two softmax warpgroups, a producer, an issuer for each query tile).  What
 // differs:
-//  - The producer alone knows the work items; the others take them from a ring of records in shared memory.  Without
-//    documents items go to CTAs in the fixed order of fa_fwd_kernel.cuh.  With documents their lengths depend on data,
-//    and each CTA asks a counter for its next one (an item's result does not depend on who computes it).
+//  - The producer alone knows the work items; the others take them from a ring of records in shared memory.  With
+//    documents their lengths depend on data, and each CTA asks a counter for its next one (an item's result does not
+//    depend on who computes it).  Under a causal mask alone they go round by round to the CTAs, longest first over as
+//    many heads at a time as may be (chunk_of), one round forward and one back: 4 sequences of 4097 tokens, 16 heads,
+//    d = 64 155 us and d = 128 285, in heavy and light pairs head by head (fa_fwd) 181 and 318.
 //  - An item's two query tiles may begin and end at different key tiles: K and V run over both, and the issuer of a
 //    tile passes on the stages that it does not visit.
 //  - Between a row's scores and its exponentials stand the cap and the bias, in registers.  Both can change which score
@@ -51,9 +53,9 @@ struct RulesCfg : FwdCfg<D, OutBytes> {
     static constexpr int kCtrlRegs = 72;
 };
 
-// Item `item`: query pair t of head bh, in the order of fa_fwd_kernel.cuh's causal walk.
-template <int D>
-__device__ __forceinline__ RulesItem rules_item(const FwdRulesParams& p, int item, int bh, int t)
+// Query pair qp of head bh.  `swap`: the tiles change places (as in decode_item, where it evens out which of them walks
+// further under a causal mask).
+__device__ __forceinline__ RulesItem rules_item(const FwdRulesParams& p, int bh, int qp, int swap)
 {
     const FwdParams& f = p.f;
     RulesItem it;
@@ -61,10 +63,8 @@ __device__ __forceinline__ RulesItem rules_item(const FwdRulesParams& p, int ite
     it.b = bh / p.Hq;
     it.kv = bh / (p.Hq / p.Hkv);
     it.prefix = p.causal ? rules_prefix(p.prefix, it.b, f.Nk, f.status) : 0;
-    const int qp = (t & 1) ? (t >> 1) : f.n_qp - 1 - (t >> 1);
     const int off = f.Nk - f.N;
     const int n_all = (f.Nk + kBlockN - 1) / kBlockN;
-    const int swap = D <= 64 && p.causal ? item & 1 : 0;  // as decode_item
     const int q_tiles = (f.N + kBlockM - 1) / kBlockM;
     int from[2], to[2];
 #pragma unroll
@@ -195,21 +195,27 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_rules_fwd_kernel(const __gr
                 long long g = 0;          // K/V tiles issued so far (ring position)
                 int k = 0;                // items published
                 bool ok = true;
-                ItemCursor cur = first_item(f, f.pairs);
-                int asked = ask ? atomicAdd(p.counter, 1) : 0;  // the next item, asked for one ahead
+                const int G = static_cast<int>(gridDim.x);
+                int next = ask ? atomicAdd(p.counter, 1) : static_cast<int>(blockIdx.x);  // (asked for one item ahead)
                 while (true) {
                     RulesItem it;
                     it.n_kv = -1;
-                    if (ask) {
-                        const int item = asked;
-                        if (item < f.n_items) {
-                            asked = atomicAdd(p.counter, 1);
-                            const int bh = item / f.n_qp;
-                            it = rules_item<D>(p, item, bh, item - bh * f.n_qp);
+                    if (next < f.n_items) {
+                        const int swap = C::kAlternate && p.causal ? k & 1 : 0;
+                        if (ask || !p.causal) {  // head by head
+                            const int bh = next / f.n_qp;
+                            const int qp = next - bh * f.n_qp;
+                            next = ask ? atomicAdd(p.counter, 1) : next + G;
+                            it = rules_item(p, bh, qp, swap);
+                        } else {
+                            const int first = next / (p.chunk * f.n_qp) * p.chunk;  // head of the chunk
+                            const int many = min(p.chunk, f.BH - first);
+                            const int place = next - first * f.n_qp;
+                            const int t = place / many;
+                            // there and back: the CTA with the longest item of a round has the shortest of the next
+                            next = (k + 1) * G + ((k & 1) ? static_cast<int>(blockIdx.x) : G - 1 - static_cast<int>(blockIdx.x));
+                            it = rules_item(p, first + place - t * many, f.n_qp - 1 - t, swap);
                         }
-                    } else if (cur.item < f.n_items) {
-                        it = rules_item<D>(p, cur.item, cur.bh, cur.t);
-                        next_item(f, cur, f.pairs);
                     }
                     const int at = k % kRulesItems;
                     if (k >= kRulesItems &&
@@ -632,16 +638,8 @@ cudaError_t launch_fwd_rules_t(const FwdRulesParams& p, cudaStream_t st)
         if (attr.numRegs * kFwdThreads < 256 * C::kSoftRegs + 128 * C::kCtrlRegs) return cudaErrorLaunchOutOfResources;
         configured[dev] = true;
     }
-    FwdRulesParams q = p;
-    const FwdParams& f = p.f;
-    // the fixed order's steps (fa_fwd_kernel.cuh, first_item and next_item)
-    q.f.pairs = (p.causal && p.counter == nullptr && f.n_items > f.num_ctas) ? 1 : 0;
-    const int units = q.f.pairs ? (f.n_items + 1) / 2 : f.n_items;
-    const int grid = units < f.num_ctas ? units : f.num_ctas;
-    const long long step = q.f.pairs ? 2LL * grid - 1 : grid;
-    q.f.step_heads = static_cast<int>(step / f.n_qp);
-    q.f.step_rem = static_cast<int>(step % f.n_qp);
-    return launch_pdl(kern, static_cast<unsigned>(grid), kFwdThreads, C::kSmem, st, q);
+    const int grid = p.f.n_items < p.f.num_ctas ? p.f.n_items : p.f.num_ctas;
+    return launch_pdl(kern, static_cast<unsigned>(grid), kFwdThreads, C::kSmem, st, p);
 }
 
 template <int D, int RULES>
