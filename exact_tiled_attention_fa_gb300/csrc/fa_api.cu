@@ -280,7 +280,10 @@ namespace fa {
 cudaError_t device_status_word(int** out) { return status_word(out); }
 cudaError_t device_sm_count(int* out) { return sm_count(out); }
 unsigned long long wait_limit_ns() { return g_wait_ns.load(); }
-bool bf16_tile_map(CUtensorMap* m, const void* ptr, int BH, int rows, int d) { return make_map(m, ptr, BH, rows, d); }
+bool bf16_tile_map(CUtensorMap* m, const void* ptr, int BH, int rows, int d, int box_rows)
+{
+    return make_map(m, ptr, BH, rows, d, box_rows);
+}
 bool bf16_group_map(CUtensorMap* m, const void* ptr, int B, int Hkv, int R, int d, int seqs)
 {
     return make_group_map(m, ptr, B, Hkv, R, d, seqs);

@@ -326,9 +326,9 @@ struct BwdRulesParams {
 template <int D, int RULES>
 cudaError_t launch_bwd_rules(const BwdRulesParams& p, fa_dtype grad_dtype, cudaStream_t st);
 
-// Decode behind a shared prefix (fa_tree_kernel.cuh, SHARED).  Units are a key/value head's prefix with a block of the
-// batch's rows, and then a sequence's own keys with its R rows: either kind may be left to another launch.  Of the
-// tree's parameters rows, T, parents and n_nodes have no meaning, joins holds a record for each unit.
+// Decode behind a shared prefix (fa_tree_kernel.cuh, SHARED).  Units are a key/value head's prefix with a query tile of the
+// batch's rows, and then a sequence's own keys with its R rows.  Of the tree's parameters rows, T, parents and n_nodes
+// have no meaning, joins holds a record for each unit.
 struct PrefixParams : TreeParams {
     CUtensorMap tm_q1;      // bf16 [B][Hkv][R][d], box {min(d,64), R, 1, 1}; tm_q: box {min(d,64), R, 1, seqs}
     CUtensorMap tm_kp;      // bf16 [Hkv][P_max][d]
@@ -337,8 +337,7 @@ struct PrefixParams : TreeParams {
     ScoreRules rules;
     int P_max, R;
     int seqs;               // sequences of a query tile of the prefix: min(B, 128 / R)
-    int n_pre;              // prefix units of this launch, Hkv * n_qp or 0
-    int n_seq;              // sequences of this launch, B or 0
+    int n_pre;              // prefix units, Hkv * n_qp, or 0
     int rows_all;           // B * R
     // where whole units go, fp32: prefix ones [Hkv][B * R] rows, others [B][Hkv][R] rows (or, as they are, to o and
     // lse where there is no prefix: o_own = nullptr)
@@ -348,14 +347,15 @@ struct PrefixParams : TreeParams {
 // Joins what prefix and own keys gave each row.
 struct PrefixSide {
     const TreeJoin* units;  // {-, first share, parts}
-    const float *o_part, *lse_part, *o_whole, *lse_whole;
-    int part_rows;
+    const float *o_whole, *lse_whole;
 };
 struct PrefixMergeParams {
     PrefixSide pre, own;  // pre.units = nullptr: no prefix
+    const float *o_part, *lse_part;
+    int part_rows;
     void* o;
     float* lse;
-    int B, Hkv, R, seqs, pair, n_qp;
+    int B, Hkv, R, seqs, n_qp;
     fa_dtype o_dtype;
 };
 
@@ -367,8 +367,8 @@ cudaError_t launch_prefix_merge(const PrefixMergeParams& p, int d, cudaStream_t 
 cudaError_t device_status_word(int** out);  // the current device's status word
 cudaError_t device_sm_count(int* out);
 unsigned long long wait_limit_ns();
-// Tensor map of a bf16 tensor [BH][rows][d] with 128-row boxes, from the thread's cache when possible.
-bool bf16_tile_map(CUtensorMap* m, const void* ptr, int BH, int rows, int d);
+// Tensor map of a bf16 tensor [BH][rows][d] with boxes of 128 (or box_rows) rows, from the thread's cache when possible.
+bool bf16_tile_map(CUtensorMap* m, const void* ptr, int BH, int rows, int d, int box_rows = kBlockM);
 // Tensor map of q [B][Hkv][R][d] whose box is the R rows of one key/value head of `seqs` sequences, the same way.
 bool bf16_group_map(CUtensorMap* m, const void* ptr, int B, int Hkv, int R, int d, int seqs);
 // Tensor map of an output [BH][rows][d] for bulk stores of box_rows rows (encode_out_map), the same way.

@@ -26,9 +26,8 @@ __global__ void __launch_bounds__(256) fa_prefix_merge_kernel(const __grid_const
     const int r = static_cast<int>(row - static_cast<long long>(group) * p.R);
     const int b = group / p.Hkv, kvh = group - b * p.Hkv;
     // the row's place in its prefix unit
-    const int block = b / p.seqs;  // query tile
-    const int qp = p.pair ? block >> 1 : block;
-    const int row_pre = (p.pair ? (block & 1) * kBlockM : 0) + (b - block * p.seqs) * p.R + r;
+    const int qp = b / p.seqs;  // query tile
+    const int row_pre = (b - qp * p.seqs) * p.R + r;
     TreeJoin jp{0, 0, 0};
     const TreeJoin jo = p.own.units[group];
     if (p.pre.units != nullptr) jp = p.pre.units[kvh * p.n_qp + qp];
@@ -45,9 +44,9 @@ __global__ void __launch_bounds__(256) fa_prefix_merge_kernel(const __grid_const
             lse = side.lse_whole;
             return pre ? (static_cast<size_t>(kvh) * p.B + b) * p.R + r : static_cast<size_t>(row);
         }
-        o = side.o_part;
-        lse = side.lse_part;
-        return static_cast<size_t>(2 * (j.rows + k) + (k == 0 ? 1 : 0)) * side.part_rows + static_cast<size_t>(pre ? row_pre : r);
+        o = p.o_part;
+        lse = p.lse_part;
+        return static_cast<size_t>(2 * (j.rows + k) + (k == 0 ? 1 : 0)) * p.part_rows + static_cast<size_t>(pre ? row_pre : r);
     };
     auto load = [&](int s, float (&v)[V]) {
         const float *o, *lse;

@@ -288,38 +288,29 @@ namespace {
 
 // How a call of fa_decode_prefix is divided and where its workspace holds what.
 struct PrefixPlan {
-    int R, seqs;      // rows of a group, sequences of a query tile of the prefix
-    bool pair;        // more rows than a tile: the prefix in a launch of its own, 256 rows to a unit
-    int n_qp, ctas;
-    int part_pre, part_own;    // rows of a slot
-    size_t slots_pre, slots_own;
-    size_t o_pre, lse_pre, o_own, lse_own, whole, whole_lse, joins, total;  // offsets; whole: two of each
-    int units_pre, units_own;
+    int R, seqs, n_qp;  // rows of a group, sequences of a query tile of the prefix, such tiles
+    int ctas, part_rows, units_pre, units_own;
+    size_t o_part, lse_part, whole, whole_lse, joins, total;  // offsets; whole: of both sides
     PrefixPlan(int B, int Hq, int Hkv, int d, int sms)
     {
         R = Hq / Hkv;
         seqs = fa::kBlockM / R < B ? fa::kBlockM / R : B;
-        pair = B > seqs;
-        n_qp = pair ? (B + 2 * seqs - 1) / (2 * seqs) : 1;
+        n_qp = (B + seqs - 1) / seqs;
         ctas = sms < fa::kTreeMaxShares / 2 ? sms : fa::kTreeMaxShares / 2;
-        part_pre = pair ? 2 * fa::kBlockM : seqs * R;
-        part_own = pair ? R : seqs * R;
+        part_rows = seqs * R;
         units_pre = Hkv * n_qp;
         units_own = B * Hkv;
-        // two slots a share; a share for each CTA (PAIR) or at most two
-        slots_pre = pair ? 2 * static_cast<size_t>(ctas) * part_pre : 0;
-        slots_own = 4 * static_cast<size_t>(ctas) * part_own;
-        const size_t rows = static_cast<size_t>(B) * Hq, row = static_cast<size_t>(d) * sizeof(float);
+        // two slots a share, up to two shares a CTA
+        const size_t slots = 4 * static_cast<size_t>(ctas) * part_rows, rows = static_cast<size_t>(B) * Hq;
+        const size_t row = static_cast<size_t>(d) * sizeof(float);
         size_t at = 0;
         auto take = [&](size_t bytes) {
             const size_t x = at;
             at += round_up(bytes, kAlign);
             return x;
         };
-        o_pre = take(slots_pre * row);
-        lse_pre = take(slots_pre * sizeof(float));
-        o_own = take(slots_own * row);
-        lse_own = take(slots_own * sizeof(float));
+        o_part = take(slots * row);
+        lse_part = take(slots * sizeof(float));
         whole = take(2 * rows * row);
         whole_lse = take(2 * rows * sizeof(float));
         joins = take((static_cast<size_t>(units_pre) + units_own) * sizeof(fa::TreeJoin));
@@ -369,11 +360,18 @@ fa_status fa_decode_prefix(const void* q, const void* k_prefix, const void* v_pr
     auto at = [&](size_t off) { return reinterpret_cast<float*>(ws + off); };
     const size_t rows = static_cast<size_t>(B) * Hq;
     fa::PrefixParams p{};
-    if (!fa::bf16_group_map(&p.tm_q1, q, B, Hkv, plan.R, d, 1) || !fa::bf16_tile_map(&p.tm_k, k_cache, B * Hkv, Nk_max, d) ||
-        !fa::bf16_tile_map(&p.tm_v, v_cache, B * Hkv, Nk_max, dv))
+    const int n_pre = pre ? plan.units_pre : 0;
+    const long long units = static_cast<long long>(n_pre) + plan.units_own;
+    // Which form (ALT / SOLO, us).  d = 128, where SOLO's K and V come in halves: 2 sequences behind 512 tokens 12.8 / 11.1,
+    // 16 behind 8192 38.6 / 31.8, 64 behind 32K 114 / 103, 64 without a prefix 63.8 / 50.9.  d = 64, 5 heads, 37 sequences
+    // behind 3000 tokens 19.7 / 21.7, without a prefix 19.0 / 15.5; 8 heads, 64 sequences behind 32K 68 / 53.
+    const bool solo = d == 128 || (pre ? units >= 2LL * plan.ctas : 4 * units >= 3LL * plan.ctas);
+    const int box = solo && d == 128 ? fa::kBlockN / 2 : fa::kBlockN;  // TrCfg::kHalves
+    if (!fa::bf16_group_map(&p.tm_q1, q, B, Hkv, plan.R, d, 1) || !fa::bf16_tile_map(&p.tm_k, k_cache, B * Hkv, Nk_max, d, box) ||
+        !fa::bf16_tile_map(&p.tm_v, v_cache, B * Hkv, Nk_max, dv, box))
         return FA_ERR_CUDA;
-    if (pre && (!fa::bf16_group_map(&p.tm_q, q, B, Hkv, plan.R, d, plan.seqs) || !fa::bf16_tile_map(&p.tm_kp, k_prefix, Hkv, P_max, d) ||
-                !fa::bf16_tile_map(&p.tm_vp, v_prefix, Hkv, P_max, dv)))
+    if (pre && (!fa::bf16_group_map(&p.tm_q, q, B, Hkv, plan.R, d, plan.seqs) || !fa::bf16_tile_map(&p.tm_kp, k_prefix, Hkv, P_max, d, box) ||
+                !fa::bf16_tile_map(&p.tm_vp, v_prefix, Hkv, P_max, dv, box)))
         return FA_ERR_CUDA;
     if (fa::device_status_word(&p.status) != cudaSuccess) return FA_ERR_CUDA;
     p.seqlens = seqlens_k;
@@ -400,47 +398,27 @@ fa_status fa_decode_prefix(const void* q, const void* k_prefix, const void* v_pr
     p.lse_own = pre ? p.lse_pre + rows : nullptr;
     fa::TreeJoin* joins = reinterpret_cast<fa::TreeJoin*>(ws + plan.joins);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    auto launch = [&] { return by_kind(d, rules, [&](auto D, auto kind) { return fa::launch_prefix<D(), kind()>(p, st); }); };
-    if (pre && plan.pair) {
-        p.joins = joins;
-        p.o_part = at(plan.o_pre);
-        p.lse_part = at(plan.lse_pre);
-        p.part_rows = plan.part_pre;
-        p.n_qp = plan.n_qp;
-        p.num_shares = plan.ctas;
-        p.unit_cost = 3;
-        p.n_pre = plan.units_pre;
-        p.n_seq = 0;
-        if (launch() != cudaSuccess) return FA_ERR_CUDA;
-    }
-    const bool both = pre && !plan.pair;  // the prefix's units in the same launch
-    p.joins = both ? joins : joins + plan.units_pre;
-    p.o_part = at(plan.o_own);
-    p.lse_part = at(plan.lse_own);
-    p.part_rows = both ? plan.part_own : plan.R;
-    p.n_qp = 1;
-    p.n_pre = both ? plan.units_pre : 0;
-    p.n_seq = B;
-    // which form: as fa_decode_tree
-    const long long units = static_cast<long long>(p.n_pre) + plan.units_own;
-    const bool solo = d < 128 ? 4 * units >= 3LL * plan.ctas
-                              : units >= 6LL * plan.ctas || (units >= 2LL * plan.ctas && Nk_max <= 1536 && P_max <= 1536);
+    p.joins = joins;
+    p.o_part = at(plan.o_part);
+    p.lse_part = at(plan.lse_part);
+    p.part_rows = plan.part_rows;
+    p.n_qp = plan.n_qp;
+    p.n_pre = n_pre;
     p.num_shares = solo ? 2 * plan.ctas : plan.ctas;
-    p.unit_cost = solo ? 2 : 3;
-    if (launch() != cudaSuccess) return FA_ERR_CUDA;
+    p.unit_cost = solo ? 2 : 3;  // as fa_decode_tree
+    if (by_kind(d, rules, [&](auto D, auto kind) { return fa::launch_prefix<D(), kind()>(p, st); }) != cudaSuccess) return FA_ERR_CUDA;
     fa::PrefixMergeParams m{};
-    m.own = fa::PrefixSide{joins + plan.units_pre, at(plan.o_own), at(plan.lse_own), p.o_own, p.lse_own, p.part_rows};
-    if (pre) {
-        m.pre = fa::PrefixSide{joins, at(plan.pair ? plan.o_pre : plan.o_own), at(plan.pair ? plan.lse_pre : plan.lse_own), p.o_pre,
-                               p.lse_pre, plan.part_pre};
-    }
+    m.own = fa::PrefixSide{joins + n_pre, p.o_own, p.lse_own};
+    if (pre) m.pre = fa::PrefixSide{joins, p.o_pre, p.lse_pre};
+    m.o_part = p.o_part;
+    m.lse_part = p.lse_part;
+    m.part_rows = p.part_rows;
     m.o = o;
     m.lse = lse;
     m.B = B;
     m.Hkv = Hkv;
     m.R = plan.R;
     m.seqs = plan.seqs;
-    m.pair = plan.pair ? 1 : 0;
     m.n_qp = plan.n_qp;
     m.o_dtype = o_dtype;
     return fa::launch_prefix_merge(m, d, st) == cudaSuccess ? FA_OK : FA_ERR_CUDA;

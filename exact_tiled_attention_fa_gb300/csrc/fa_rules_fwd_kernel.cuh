@@ -95,23 +95,18 @@ __device__ __forceinline__ RulesItem rules_item(const FwdRulesParams& p, int bh,
     return it;
 }
 
-// Sets scores s of columns k0 .. k0 + 127 that the row's [lo, hi) does not hold to -infinity, 32 columns at a time:
-// those that every row of the warp sees are left alone, those that none sees are set in one go.  (By selection:
-// a non-finite score of a hidden key does not reach the row.)
+// Sets the scores s of a tile that the row's keys [lo, hi) (counted from the tile's first) do not hold to -infinity.  (By
+// selection: a non-finite score of a hidden key does not reach the row.)  Bits of four words and no branches: 64
+// sequences of 1024 tokens in documents of 60 - 320, 16 heads of 64, 144 us; telling apart pieces of 32 columns that
+// all rows of the warp see, some or none 160; passing over the exponentials of the latter too 206.
 __device__ __forceinline__ void rules_mask(float* s, int lo, int hi)
 {
 #pragma unroll
     for (int q = 0; q < kBlockN / 32; ++q) {
         float* t = s + 32 * q;
-        const int l = lo - 32 * q, h = hi - 32 * q;
-        if (__all_sync(0xffffffffu, h <= 0 || l >= 32)) {
+        const uint32_t see = low_bits(hi - 32 * q) & ~low_bits(lo - 32 * q);
 #pragma unroll
-            for (int c = 0; c < 32; ++c) t[c] = h <= 0 || l >= 32 ? -INFINITY : t[c];
-        } else if (!__all_sync(0xffffffffu, l <= 0 && h >= 32)) {
-            const uint32_t see = low_bits(h) & ~low_bits(l);
-#pragma unroll
-            for (int c = 0; c < 32; ++c) t[c] = (see >> c) & 1u ? t[c] : -INFINITY;
-        }
+        for (int c = 0; c < 32; ++c) t[c] = (see >> c) & 1u ? t[c] : -INFINITY;
     }
 }
 

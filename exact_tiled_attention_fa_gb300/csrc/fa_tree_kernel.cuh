@@ -106,7 +106,7 @@ constexpr int kTrSegs = 8;
 
 enum TreeForm { kAlt, kSolo, kPair };
 
-template <int D, TreeForm FORM>
+template <int D, TreeForm FORM, bool SHARED = false>
 struct TrCfg {
     static_assert(D == 32 || D == 64 || D == 128, "head size");
     // Steps of a tile.  At d = 128 tensor memory has no room for P beside S and O: P overwrites S, and a
@@ -116,7 +116,12 @@ struct TrCfg {
     // 32/8 heads: 288 us in one step, 259 in two; 64 of 1000 tokens: 101 and 94).  The other forms wait for
     // memory, and a tile in two steps reads the queries from shared memory twice: one step (16 nodes 170 us,
     // in two steps 177; d = 64, 64 nodes 111 and 155).
-    static constexpr int kSteps = D == 128 && FORM == kPair ? 2 : 1;
+    // Decode behind a shared prefix in SOLO form is in two steps too, and its K and V come in halves of a tile, two stages
+    // of each a stream: with one stage of a whole tile the next is asked for only when the product before is done, and
+    // a stream took 3.5 us a tile whatever it read (64 sequences of up to 2000 tokens, 32/8 heads: 56 us,
+    // so 51, with a cap 68 and 53; behind a prefix of 8K 16 such sequences 36 and 32).
+    static constexpr bool kHalves = SHARED && FORM == kSolo && D == 128;
+    static constexpr int kSteps = D == 128 && (FORM == kPair || kHalves) ? 2 : 1;
     static constexpr int kStep = kBlockN / kSteps;  // keys
     // Registers after the split: 256 * softmax + 128 * control = 64512 = 384 * 168, checked by the launcher.
     // A softmax thread holds the scores of a step.  (With 224 and 56 at d = 128 the producers and issuers
@@ -134,12 +139,15 @@ struct TrCfg {
     // Stages of K and of V, all streams' together.  Even: in ALT form a stage then always serves the same
     // warpgroup, so its tile before was consumed by the very thread that waits for the next one, which the
     // phase parity of the wait relies on.
-    static constexpr int kStages = D == 128 ? 2 : 4;
+    static constexpr int kStages = D == 128 && !kHalves ? 2 : 4;
     static_assert(kStages % 2 == 0 && kStages <= 4, "ring stages");
+    static constexpr int kLoads = kHalves ? 2 : 1;                // of a tile of K or V, each a stage
+    static constexpr int kStageBytes = kTileBytes / kLoads;
+    static constexpr int kKVBlkBytes = kBlkBytes / kLoads;        // a stage's column block
     static constexpr int kOffQ = 0;  // two query tiles: two units' (ALT), a warpgroup's each (SOLO, PAIR)
     static constexpr int kOffK = 2 * kTileBytes;
-    static constexpr int kOffV = kOffK + kStages * kTileBytes;
-    static constexpr int kOffML = kOffV + kStages * kTileBytes;  // ALT: [2 warpgroups][128] (max, sum)
+    static constexpr int kOffV = kOffK + kStages * kStageBytes;
+    static constexpr int kOffML = kOffV + kStages * kStageBytes;  // ALT: [2 warpgroups][128] (max, sum)
     static constexpr int kOffStage = kOffML + 2 * kBlockM * 8;  // [8 warps][32 rows of 64 bytes]: rows on their way out
     static constexpr int kOffSeg = kOffStage + 8 * 2048;
     static constexpr int kOffBar = kOffSeg + kTrSegs * static_cast<int>(sizeof(TreeSeg));
@@ -324,9 +332,9 @@ __device__ __forceinline__ TreeStart shared_locate(const PrefixParams& p, int c,
     const int pre_places = pre.tiles() + p.unit_cost;
     const long long pre_total = static_cast<long long>(p.n_pre) * pre_places;
     TreeLen len{0, 0};  // the first 32 sequences'
-    if (lane < p.n_seq) len = shared_own(p, lane);
-    long long total = lane < p.n_seq ? len.tiles() + p.unit_cost : 0;
-    for (int b = 32 + lane; b < p.n_seq; b += 32) total += shared_own(p, b).tiles() + p.unit_cost;
+    if (lane < p.B) len = shared_own(p, lane);
+    long long total = lane < p.B ? len.tiles() + p.unit_cost : 0;
+    for (int b = 32 + lane; b < p.B; b += 32) total += shared_own(p, b).tiles() + p.unit_cost;
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     total = total * p.Hkv + pre_total;
@@ -343,10 +351,10 @@ __device__ __forceinline__ TreeStart shared_locate(const PrefixParams& p, int c,
         return s;
     }
     long long base = pre_total;
-    for (int b0 = 0; b0 < p.n_seq; b0 += 32) {
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
         const int b = b0 + lane;
-        if (b0 > 0 && b < p.n_seq) len = shared_own(p, b);
-        const int places = b < p.n_seq ? len.tiles() + p.unit_cost : 0;
+        if (b0 > 0 && b < p.B) len = shared_own(p, b);
+        const int places = b < p.B ? len.tiles() + p.unit_cost : 0;
         long long incl = static_cast<long long>(places) * p.Hkv;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -406,7 +414,7 @@ struct SharedWalk : TreeWalk {
     }
     __device__ __forceinline__ void ahead(const PrefixParams& p)
     {
-        if (p.n_seq > 0) next_len = p.seqlens[min(b + 1, p.n_seq - 1)];
+        next_len = p.seqlens[min(b + 1, p.B - 1)];
     }
     __device__ __forceinline__ int group(const PrefixParams& p) const { return b < 0 ? kvh : b * p.Hkv + kvh; }
 };
@@ -572,22 +580,26 @@ __device__ __forceinline__ void tree_scale(uint32_t (&o)[N], float alpha)
 }
 
 // SHARED: decode of one query a sequence behind a prefix that all sequences have in common, under score rules
-// (fa_decode_prefix).  The prefix is read once for a block of rows of many sequences, instead of once for each; rows of
-// a sequence's own keys are the R query heads of a group.  Every unit has its parts recorded, and whole ones go to
-// buffers of their own, for the merge to join a row's two sides.
-// RULES: kNoRules, or kCap and kBias.  (Decided at run time, they cost the calls without them half as much again:
-// PLACEHOLDER.)
+// (fa_decode_prefix).  The prefix is read once for a query tile of many sequences' rows, instead of once for each; rows
+// of a sequence's own keys are the R query heads of a group.  Both kinds of units are in one launch, so that the
+// streams that have products to wait for share their SM with streams that have bytes to wait for: 64 sequences behind
+// 32K tokens with up to 2000 of their own, 32/8 heads of 128, 103 us; the prefix in PAIR form in a launch of its own 107.
+// Every unit has its parts recorded, and whole ones go to buffers of their own, for the merge to join a row's two sides.
+// RULES: kNoRules, or kCap and kBias.  (Decided at run time they cost calls without them, by the registers that spilled:
+// 64 sequences of up to 2000 tokens of their own alone 82 us, so 63.)
 template <int D, TreeForm FORM, int RULES = -1>
 __global__ void __launch_bounds__(kTrThreads, 1)
     fa_tree_kernel(const __grid_constant__ std::conditional_t<(RULES >= 0), PrefixParams, TreeParams> p)
 {
     constexpr bool SHARED = RULES >= 0, kWithCap = SHARED && (RULES & kCap) != 0, kWithBias = SHARED && (RULES & kBias) != 0;
-    using C = TrCfg<D, FORM>;
+    using C = TrCfg<D, FORM, SHARED>;
     constexpr bool ALT = FORM == kAlt, SOLO = FORM == kSolo, PAIR = FORM == kPair;
+    static_assert(!SHARED || !PAIR, "a unit's rows are one query tile");
     constexpr int kStreams = SOLO ? 2 : 1;         // shares, producers, rings
     constexpr int S = C::kStages / kStreams;       // stages of a stream's ring
     constexpr int kSegs = kTrSegs / kStreams;      // records of a stream
     constexpr int H = C::kSteps, KS = C::kStep;    // steps of a tile, keys of a step
+    constexpr int HL = C::kLoads;                  // loads, and stages, of a tile of K or V
     extern __shared__ uint8_t tr_smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(tr_smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
@@ -686,7 +698,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 std::conditional_t<SHARED, SharedWalk, TreeWalk> kw, vw;  // K runs one tile ahead of V
                 kw.begin(p, start);
                 vw.begin(p, start);
-                int kj = 0, vj = 0;  // tile within the segment
+                int kj = 0, vj = 0;  // load within the segment
                 int segs = 0;        // records written
                 int k_issued = 0, v_issued = 0;
                 TreeJoin join{0, 0, 0};
@@ -730,14 +742,11 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                             // rows of `seqs` sequences for the prefix, of one otherwise; a box past the last sequence is filled
                             // with zeros
                             const bool pre = kw.b < 0;
-                            const int seq0 = pre ? kw.qp * (PAIR ? 2 : 1) * p.seqs : kw.b;
-                            const int q_tiles = PAIR && pre && seq0 + p.seqs < p.B ? 2 : 1;
                             const CUtensorMap* map = pre ? &p.tm_q : &p.tm_q1;
-                            mbar_arrive_expect_tx(bar(kTbQFull + buf), q_tiles * (pre ? p.seqs : 1) * p.R * C::kRowBytes * C::kNumCB);
-                            for (int i = 0; i < q_tiles; ++i)
-                                for (int cb = 0; cb < C::kNumCB; ++cb)
-                                    tma_load_4d(sbase + C::kOffQ + (buf + i) * C::kTileBytes + cb * C::kBlkBytes, map,
-                                                bar(kTbQFull + buf), cb * C::kCB, 0, kw.kvh, seq0 + i * p.seqs, pol_q);
+                            mbar_arrive_expect_tx(bar(kTbQFull + buf), (pre ? p.seqs : 1) * p.R * C::kRowBytes * C::kNumCB);
+                            for (int cb = 0; cb < C::kNumCB; ++cb)
+                                tma_load_4d(sbase + C::kOffQ + buf * C::kTileBytes + cb * C::kBlkBytes, map, bar(kTbQFull + buf),
+                                            cb * C::kCB, 0, kw.kvh, pre ? kw.qp * p.seqs : kw.b, pol_q);
                         } else {
                             const int row0 = kw.qp * (PAIR ? 2 : 1) * kBlockM;
                             const int q_tiles = PAIR && p.rows - row0 > kBlockM ? 2 : 1;
@@ -753,14 +762,14 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                     if (k_issued >= S &&
                         !mbar_wait(bar(kTbKEmpty + s), static_cast<uint32_t>(k_issued / S - 1) & 1, limit, abort_flag))
                         return false;
-                    mbar_arrive_expect_tx(bar(kTbKFull + s), C::kTileBytes);
+                    mbar_arrive_expect_tx(bar(kTbKFull + s), C::kStageBytes);
                     const CUtensorMap* map = &p.tm_k;
                     if constexpr (SHARED) map = kw.b < 0 ? &p.tm_kp : map;
                     for (int cb = 0; cb < C::kNumCB; ++cb)
-                        tma_load_3d(sbase + C::kOffK + s * C::kTileBytes + cb * C::kBlkBytes, map, bar(kTbKFull + s),
-                                    cb * C::kCB, (kw.tile + kj) * kBlockN, g, kw.b < 0 ? pol_kv : pol_own);
+                        tma_load_3d(sbase + C::kOffK + s * C::kStageBytes + cb * C::kKVBlkBytes, map, bar(kTbKFull + s),
+                                    cb * C::kCB, kw.tile * kBlockN + kj * (kBlockN / HL), g, kw.b < 0 ? pol_kv : pol_own);
                     ++k_issued;
-                    if (++kj == kw.n) {
+                    if (++kj == kw.n * HL) {
                         kj = 0;
                         kw.next(p);
                     }
@@ -771,14 +780,14 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                     if (v_issued >= S &&
                         !mbar_wait(bar(kTbVEmpty + s), static_cast<uint32_t>(v_issued / S - 1) & 1, limit, abort_flag))
                         return false;
-                    mbar_arrive_expect_tx(bar(kTbVFull + s), C::kTileBytes);
+                    mbar_arrive_expect_tx(bar(kTbVFull + s), C::kStageBytes);
                     const CUtensorMap* map = &p.tm_v;
                     if constexpr (SHARED) map = vw.b < 0 ? &p.tm_vp : map;
                     for (int cb = 0; cb < C::kNumCB; ++cb)
-                        tma_load_3d(sbase + C::kOffV + s * C::kTileBytes + cb * C::kBlkBytes, map, bar(kTbVFull + s),
-                                    cb * C::kCB, (vw.tile + vj) * kBlockN, vw.group(p), vw.b < 0 ? pol_kv : pol_own);
+                        tma_load_3d(sbase + C::kOffV + s * C::kStageBytes + cb * C::kKVBlkBytes, map, bar(kTbVFull + s),
+                                    cb * C::kCB, vw.tile * kBlockN + vj * (kBlockN / HL), vw.group(p), vw.b < 0 ? pol_kv : pol_own);
                     ++v_issued;
-                    if (++vj == vw.n) {
+                    if (++vj == vw.n * HL) {
                         vj = 0;
                         vw.next(p);
                     }
@@ -819,17 +828,18 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 bool ok = true;
                 auto issue_s = [&](int q_tile, int stage, int h) {
                     const uint64_t a0 = smem_desc(sbase + C::kOffQ + q_tile * C::kTileBytes, 16, C::kAtomBytes, C::kLayout);
-                    const uint64_t b0 = smem_desc(sbase + C::kOffK + stage * C::kTileBytes + h * KS * C::kRowBytes, 16,
+                    const uint64_t b0 = smem_desc(sbase + C::kOffK + stage * C::kStageBytes + (HL == 1 ? h * KS * C::kRowBytes : 0), 16,
                                                   C::kAtomBytes, C::kLayout);
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = ((kk * 16) / C::kCB * C::kBlkBytes + ((kk * 16) % C::kCB) * 2) >> 4;
-                        umma_ss(d_s + KS * h, a0 + off, b0 + off, C::kIdescS, kk > 0 ? 1u : 0u);
+                        const uint32_t in = ((kk * 16) % C::kCB) * 2, cb = (kk * 16) / C::kCB;
+                        umma_ss(d_s + KS * h, a0 + ((cb * C::kBlkBytes + in) >> 4), b0 + ((cb * C::kKVBlkBytes + in) >> 4), C::kIdescS,
+                                kk > 0 ? 1u : 0u);
                     }
                 };
                 auto issue_pv = [&](int stage, int h, bool accumulate) {
-                    const uint64_t b0 = smem_desc(sbase + C::kOffV + stage * C::kTileBytes + h * KS * C::kRowBytes, C::kBlkBytes,
-                                                  C::kAtomBytes, C::kLayout);
+                    const uint64_t b0 = smem_desc(sbase + C::kOffV + stage * C::kStageBytes + (HL == 1 ? h * KS * C::kRowBytes : 0),
+                                                  C::kKVBlkBytes, C::kAtomBytes, C::kLayout);
 #pragma unroll
                     for (int kk = 0; kk < KS / 16; ++kk)
                         umma_ts(d_o, a_p + KS * h + 8u * kk, b0 + ((kk * 16 * C::kRowBytes) >> 4), C::kIdescO,
@@ -838,17 +848,18 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 // Step h of S_i of share tile kk: its columns must have been read (and, where the weights
                 // overwrite them, the product with those must have completed).
                 auto do_s = [&](int q_tile, int q_buf, int kk, int h, bool last) -> bool {
-                    const int s = stage0 + kk % S;
-                    if (h == 0 && !mbar_wait(bar(kTbKFull + s), static_cast<uint32_t>(kk / S) & 1, limit, abort_flag)) return false;
+                    const int load = kk * HL + (HL == 2 ? h : 0);
+                    const int s = stage0 + load % S;
+                    if ((h == 0 || HL == 2) && !mbar_wait(bar(kTbKFull + s), static_cast<uint32_t>(load / S) & 1, limit, abort_flag)) return false;
                     if (s_done > 0 && !mbar_wait(bar(C::kAliasP ? kTbPVDone + 2 * i + h : kTbSFree + i),
                                                  static_cast<uint32_t>(s_done - 1) & 1, limit, abort_flag))
                         return false;
                     tc_fence_after_sync();
                     issue_s(q_tile, s, h);
                     umma_commit(bar(kTbSFull + 2 * i + h));
+                    if (h == H - 1 || HL == 2) umma_commit(bar(kTbKEmpty + s));
                     if (h == H - 1) {
                         ++s_done;
-                        umma_commit(bar(kTbKEmpty + s));
                         if (last) umma_commit(bar(kTbQEmpty + q_buf));
                     }
                     return true;
@@ -865,8 +876,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                     ok = mbar_wait(bar(kTbQFull + q_buf), static_cast<uint32_t>(ALT ? segs >> 1 : segs) & 1, limit, abort_flag);
                     if (!ok) break;
                     bool rows = true;
-                    if constexpr (PAIR && SHARED) rows = i == 0 || (w.b < 0 && (w.qp * 2 + 1) * p.seqs < p.B);
-                    else if constexpr (PAIR) rows = i == 0 || p.rows - w.qp * 2 * kBlockM > kBlockM;
+                    if constexpr (PAIR) rows = i == 0 || p.rows - w.qp * 2 * kBlockM > kBlockM;
                     if (!rows || j0 >= w.n) {
                         // (The queries first: the producer may be waiting to load the next unit's ahead of
                         // this unit's last V.)
@@ -910,27 +920,29 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                                 ++tiles;
                                 if (C::kAliasP && j + step < w.n) ok = do_s(q_tile, q_buf, kk + step, 0, j + step == j_last);
                             } else {
-                                static_assert(H == 1 || (PAIR && C::kAliasP), "two steps");
+                                static_assert(H == 1 || ((PAIR || C::kHalves) && C::kAliasP), "two steps");
                                 // Scores run a step or more ahead of the weights: while the softmax works on one
                                 // step, the other's product and its next scores are under way.
                                 bool early = false;
                                 for (int h = 0; ok && h < 2; ++h) {
+                                    const int load = kk * HL + (HL == 2 ? h : 0);
+                                    const int sv = stage0 + load % S;
                                     ok = mbar_wait(bar(kTbPFull + 2 * i + h), ph, limit, abort_flag);
-                                    if (h == 0) ok = ok && mbar_wait(bar(kTbVFull + s), static_cast<uint32_t>(kk / S) & 1, limit, abort_flag);
+                                    if (h == 0 || HL == 2)
+                                        ok = ok && mbar_wait(bar(kTbVFull + sv), static_cast<uint32_t>(load / S) & 1, limit, abort_flag);
                                     if (!ok) break;
                                     tc_fence_after_sync();
-                                    issue_pv(s, h, j > j0 || h > 0);
+                                    issue_pv(sv, h, j > j0 || h > 0);
                                     umma_commit(bar(kTbPVDone + 2 * i + h));
-                                    if (h == 1) {
-                                        if (j == j_last) umma_commit(bar(kTbOReady + i));
-                                        umma_commit(bar(kTbVEmpty + s));
-                                    }
+                                    if (h == 1 && j == j_last) umma_commit(bar(kTbOReady + i));
+                                    if (h == 1 || HL == 2) umma_commit(bar(kTbVEmpty + sv));
                                     // The next tile's scores in the columns that this product frees; its first step's
                                     // now only if its keys are there already: the second step's product must not wait
                                     // for them (V's stage, and with it the next V, would wait too).
                                     if (j + step < w.n) {
-                                        const int nx = stage0 + (kk + step) % S;
-                                        if (h == 0) early = mbar_test(bar(kTbKFull + nx), static_cast<uint32_t>((kk + step) / S) & 1);
+                                        const int nl = (kk + step) * HL;
+                                        const int nx = stage0 + nl % S;
+                                        if (h == 0) early = mbar_test(bar(kTbKFull + nx), static_cast<uint32_t>(nl / S) & 1);
                                         if (h == 0 ? early : !early) ok = do_s(q_tile, q_buf, kk + step, 0, j + step == j_last);
                                         if (h == 1) ok = ok && do_s(q_tile, q_buf, kk + step, 1, j + step == j_last);
                                     }
@@ -976,9 +988,9 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             float slope2 = 0.f;
             int qpos = 0;  // SHARED: the row's position less that of the unit's first key
             if constexpr (SHARED) {
-                const int seq0 = w.b < 0 ? (PAIR ? w.qp * 2 + wg : w.qp) * p.seqs : w.b;  // the tile's first sequence
+                const int seq0 = w.b < 0 ? w.qp * p.seqs : w.b;  // the tile's first sequence
                 row0 = w.b < 0 ? seq0 * p.R : 0;
-                rows = w.b < 0 ? min(p.seqs, p.B - seq0) * p.R : PAIR && wg > 0 ? 0 : p.R;
+                rows = w.b < 0 ? min(p.seqs, p.B - seq0) * p.R : p.R;
                 if (kWithBias && r < rows) {
                     const int j = r / p.R;
                     const int kvh = w.b < 0 ? w.group : w.group - w.b * p.Hkv;
@@ -1024,17 +1036,18 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             // V rows past the tree may hold anything: zero them before the product reads them.  (The stage's
             // tile before has been consumed, by the issuer that then issued this tile's scores, so the phase
             // parity cannot mean that one.)
-            auto zero_tail = [&](int j, int k0) {
-                const int vs = my * S + (k + j) % S;  // V stage
-                ok = __all_sync(0xffffffffu, mbar_wait(bar(kTbVFull + vs), static_cast<uint32_t>((k + j) / S) & 1, limit, abort_flag));
+            auto zero_tail = [&](int j, int first, int h) {  // the stage's keys from `first` on
+                const int load = (k + j) * HL + h;
+                const int vs = my * S + load % S;  // V stage
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(kTbVFull + vs), static_cast<uint32_t>(load / S) & 1, limit, abort_flag));
                 if (!ok) return;
-                if (k0 + r >= end) {
-                    const uint32_t vrow = sbase + C::kOffV + vs * C::kTileBytes + r * C::kRowBytes;
+                if (r < kBlockN / HL && first + r >= end) {
+                    const uint32_t vrow = sbase + C::kOffV + vs * C::kStageBytes + r * C::kRowBytes;
 #pragma unroll
                     for (int cb = 0; cb < C::kNumCB; ++cb)
 #pragma unroll
                         for (int c16 = 0; c16 < C::kRowBytes; c16 += 16)
-                            st_shared_v4(vrow + cb * C::kBlkBytes + c16, 0u, 0u, 0u, 0u);
+                            st_shared_v4(vrow + cb * C::kKVBlkBytes + c16, 0u, 0u, 0u, 0u);
                 }
                 fence_proxy_async_shared();
             };
@@ -1135,7 +1148,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                         }
                     }
                     if (k0 + kBlockN > end) {
-                        zero_tail(j, k0);
+                        zero_tail(j, k0, 0);
                         if (!ok) break;
                     }
                     tc_fence_before_sync();
@@ -1186,8 +1199,8 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                             }
                             tmem_st_wait();
                         }
-                        if (k0 + kBlockN > end && h == 0) {
-                            zero_tail(j, k0);
+                        if (HL == 2 ? k0 + KS * (h + 1) > end : k0 + kBlockN > end && h == 0) {
+                            zero_tail(j, k0 + (HL == 2 ? KS * h : 0), HL == 2 ? h : 0);
                             if (!ok) break;
                         }
                         tc_fence_before_sync();
@@ -1473,7 +1486,7 @@ __global__ void __launch_bounds__(256) fa_tree_merge_kernel(const __grid_constan
 template <int D, TreeForm FORM, int RULES, typename Params>
 cudaError_t launch_tree_main(const Params& p, cudaStream_t st)
 {
-    using C = TrCfg<D, FORM>;
+    using C = TrCfg<D, FORM, (RULES >= 0)>;
     auto kern = fa_tree_kernel<D, FORM, RULES>;
     static bool configured[64] = {};  // attributes set and registers checked, per device
     int dev = 0;
@@ -1510,12 +1523,12 @@ cudaError_t launch_tree_d(const TreeParams& p, cudaStream_t st)
     return p.num_shares > p.num_ctas ? launch_tree_t<D, kSolo>(p, st) : launch_tree_t<D, kAlt>(p, st);
 }
 
-// Decode behind a prefix: PAIR only for launches of the prefix alone (a sequence's own rows are at most 128).
+// Decode behind a prefix.
 template <int D, int RULES>
 cudaError_t launch_prefix_d(const PrefixParams& p, cudaStream_t st)
 {
-    if (p.part_rows > kBlockM) return launch_tree_main<D, kPair, RULES>(p, st);
-    return p.num_shares > p.num_ctas ? launch_tree_main<D, kSolo, RULES>(p, st) : launch_tree_main<D, kAlt, RULES>(p, st);
+    if constexpr (D == 128) return launch_tree_main<D, kSolo, RULES>(p, st);  // (fa_rules_api.cu asks for no other)
+    else return p.num_shares > p.num_ctas ? launch_tree_main<D, kSolo, RULES>(p, st) : launch_tree_main<D, kAlt, RULES>(p, st);
 }
 
 }  // namespace fa

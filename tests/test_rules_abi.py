@@ -147,10 +147,9 @@ def test_decode_prefix_workspace_size(lib):
     # 16 sequences of 4 rows: one tile of 64
     own = 4 * 152 * 64
     assert size(16, 32, 8, 128, 152) == (up(own * 512) + up(own * 4) + up(2 * 16 * 32 * 512) + up(2 * 16 * 32 * 4) + up((8 + 128) * 16))
-    # 64 sequences of 4 rows: units of 256 for the prefix
-    pre, own = 2 * 152 * 256, 4 * 152 * 4
-    assert size(64, 32, 8, 64, 152) == (up(pre * 256) + up(pre * 4) + up(own * 256) + up(own * 4) + up(2 * 64 * 32 * 256) +
-                                        up(2 * 64 * 32 * 4) + up((8 + 512) * 16))
+    # 64 sequences of 4 rows: two tiles of 128
+    own = 4 * 152 * 128
+    assert size(64, 32, 8, 64, 152) == (up(own * 256) + up(own * 4) + up(2 * 64 * 32 * 256) + up(2 * 64 * 32 * 4) + up((16 + 512) * 16))
     assert size(0, 4, 2, 64, 152) == 0 and size(1, 3, 2, 64, 152) == 0 and size(1, 4, 2, 64, 0) == 0 and size(1, 258, 2, 64, 152) == 0
 
 
