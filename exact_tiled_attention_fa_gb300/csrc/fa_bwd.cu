@@ -17,6 +17,7 @@
 
 #include "fa_internal.h"
 #include "fa_kernel_common.cuh"
+#include "fa_rules_ranges.cuh"
 
 namespace fa {
 
@@ -44,14 +45,12 @@ __device__ __forceinline__ void load8(const float* p, float (&v)[8])
 // One thread per 8 elements of a padded row; the G = d / 8 threads of a row are
 // consecutive lanes of one warp and reduce with shuffles.
 template <typename OT>
-__global__ void __launch_bounds__(kPrepThreads) fa_bwd_prep_kernel(const BwdPrepParams p)
+__device__ __forceinline__ void bwd_prep(const BwdPrepParams& p, int block)
 {
-    grid_dependency_wait();    // O, dO and LSE are written by earlier kernels on the stream
-    grid_launch_dependents();  // the tensor-core kernel may begin its setup (it waits for this grid)
-    if (p.counter != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *p.counter = 0;
+    if (p.counter != nullptr && block == 0 && threadIdx.x == 0) *p.counter = 0;
     const int G = p.d / 8;
     const long long rows = static_cast<long long>(p.BH) * p.Tr * kBlockM;
-    const long long t = static_cast<long long>(blockIdx.x) * kPrepThreads + threadIdx.x;
+    const long long t = static_cast<long long>(block) * kPrepThreads + threadIdx.x;
     const long long row = t / G;
     const int c = static_cast<int>(t - row * G);
     const bool in_range = row < rows;
@@ -84,6 +83,26 @@ __global__ void __launch_bounds__(kPrepThreads) fa_bwd_prep_kernel(const BwdPrep
         p.lse2[row] = l2;
         p.dsc[row] = ds;
     }
+}
+
+template <typename OT>
+__global__ void __launch_bounds__(kPrepThreads) fa_bwd_prep_kernel(const BwdPrepParams p)
+{
+    grid_dependency_wait();    // O, dO and LSE are written by earlier kernels on the stream
+    grid_launch_dependents();  // the tensor-core kernel may begin its setup (it waits for this grid)
+    bwd_prep<OT>(p, static_cast<int>(blockIdx.x));
+}
+
+// The same for documents: the first B * tiles blocks make the keys' intervals of queries.
+static_assert(kPrepThreads == kRangeThreads, "one launch for both");
+template <typename OT>
+__global__ void __launch_bounds__(kPrepThreads) fa_bwd_prep_ranges_kernel(const BwdPrepParams p, const RangesParams r)
+{
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int ranges = r.B * r.tiles;
+    if (static_cast<int>(blockIdx.x) < ranges) rules_ranges<true>(r, static_cast<int>(blockIdx.x));
+    else bwd_prep<OT>(p, static_cast<int>(blockIdx.x) - ranges);
 }
 
 // Eight consecutive gradients of dK or dV: the parts' sums, added in order.
@@ -151,6 +170,16 @@ cudaError_t launch_bwd_prep(const BwdPrepParams& p, fa_dtype o_dtype, cudaStream
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
     if (o_dtype == FA_F32) return launch_pdl(fa_bwd_prep_kernel<float>, static_cast<unsigned>(blocks), kPrepThreads, 0, st, p);
     return launch_pdl(fa_bwd_prep_kernel<__nv_bfloat16>, static_cast<unsigned>(blocks), kPrepThreads, 0, st, p);
+}
+
+cudaError_t launch_bwd_prep_ranges(const BwdPrepParams& p, const RangesParams& r, fa_dtype o_dtype, cudaStream_t st)
+{
+    const long long threads = static_cast<long long>(p.BH) * p.Tr * kBlockM * (p.d / 8);
+    const long long blocks = (threads + kPrepThreads - 1) / kPrepThreads + static_cast<long long>(r.B) * r.tiles;
+    if (blocks <= 0 || blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    const unsigned g = static_cast<unsigned>(blocks);
+    return o_dtype == FA_F32 ? launch_pdl(fa_bwd_prep_ranges_kernel<float>, g, kPrepThreads, 0, st, p, r)
+                             : launch_pdl(fa_bwd_prep_ranges_kernel<__nv_bfloat16>, g, kPrepThreads, 0, st, p, r);
 }
 
 cudaError_t launch_bwd_dq(const BwdDqParams& given, fa_dtype grad_dtype, cudaStream_t st)

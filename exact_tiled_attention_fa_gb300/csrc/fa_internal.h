@@ -114,6 +114,9 @@ struct BwdDqParams {
 
 cudaError_t launch_bwd(const BwdParams& p, int d, bool causal, fa_dtype grad_dtype, cudaStream_t st);
 cudaError_t launch_bwd_prep(const BwdPrepParams& p, fa_dtype o_dtype, cudaStream_t st);
+struct RangesParams;
+// The same, and the documents' intervals of every key.
+cudaError_t launch_bwd_prep_ranges(const BwdPrepParams& p, const RangesParams& r, fa_dtype o_dtype, cudaStream_t st);
 cudaError_t launch_bwd_dq(const BwdDqParams& p, fa_dtype grad_dtype, cudaStream_t st);
 
 // Split-KV on the tensor core: one CTA per (key split, 128-row query tile, group).  A group is
@@ -282,13 +285,13 @@ struct RangesParams {
     const int* prefix;  // int32 [B] or nullptr
     int2* each;         // [B][n]: keys [x, y) of query x, or queries [x, y) of key x; empty: (0, 0)
     int2* tile;         // [B][tiles]: 128-tiles [x, y) of the other side that one of its 128 has to do with
-    int* counter;       // of work items, set to 0
+    int* counter;       // of work items, set to 0 (by fa_rules_ranges_kernel)
     int* status;
     int B, N, Nk, tiles, causal;
 };
 
-// The documents' intervals: of every query (keys = false) or of every key.
-cudaError_t launch_rules_ranges(const RangesParams& p, bool keys, cudaStream_t st);
+// The documents' intervals of every query.
+cudaError_t launch_rules_ranges(const RangesParams& p, cudaStream_t st);
 
 struct FwdRulesParams {
     FwdParams f;        // without splits; tm_k and tm_v over B * Hkv heads

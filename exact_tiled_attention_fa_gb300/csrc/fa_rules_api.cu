@@ -177,7 +177,7 @@ fa_status fa_fwd_rules(const void* q, const void* k, const void* v, const float*
     if (documents != nullptr) {
         const Ranges r(static_cast<char*>(workspace), B, N);
         const fa::RangesParams rp{documents, prefix_lens, r.each, r.tile, r.counter, f.status, B, N, Nk, tiles_of(N), causal};
-        if (fa::launch_rules_ranges(rp, false, st) != cudaSuccess) return FA_ERR_CUDA;
+        if (fa::launch_rules_ranges(rp, st) != cudaSuccess) return FA_ERR_CUDA;
         p.each = r.each;
         p.tile = r.tile;
         p.counter = r.counter;
@@ -238,14 +238,15 @@ fa_status fa_bwd_rules(const void* q, const void* k, const void* v, const void* 
         !fa::out_tile_map(&b.tm_dv, dv_, B * Hkv * parts, Nk, dv, kv_type, fa::kBlockM))
         return FA_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const fa::BwdPrepParams pp{o, grad_o, lse, lse2, dsc, dq_acc, B * Hq, N, Tr, d, scale, r.counter};
     if (documents != nullptr) {
-        const fa::RangesParams rp{documents, prefix_lens, r.each, r.tile, r.counter, b.status, B, N, Nk, Tc, causal};
-        if (fa::launch_rules_ranges(rp, true, st) != cudaSuccess) return FA_ERR_CUDA;
+        const fa::RangesParams rp{documents, prefix_lens, r.each, r.tile, nullptr, b.status, B, N, Nk, Tc, causal};
+        if (fa::launch_bwd_prep_ranges(pp, rp, o_dtype, st) != cudaSuccess) return FA_ERR_CUDA;
         p.each = r.each;
         p.tile = r.tile;
+    } else if (fa::launch_bwd_prep(pp, o_dtype, st) != cudaSuccess) {
+        return FA_ERR_CUDA;
     }
-    const fa::BwdPrepParams pp{o, grad_o, lse, lse2, dsc, dq_acc, B * Hq, N, Tr, d, scale, r.counter};
-    if (fa::launch_bwd_prep(pp, o_dtype, st) != cudaSuccess) return FA_ERR_CUDA;
     b.lse2 = lse2;
     b.dsc = dsc;
     b.dq_acc = dq_acc;

@@ -5,7 +5,7 @@
 //   dV_j = sum_i P dO_i,  dP = dO_i . V_j,  dS = P (dP - D_i),  dX = dS (1 - tanh^2(x / cap)) scale,
 //   dQ_i = sum_j dX K_j,  dK_j = sum_i dX Q_i,
 // the sums of dK and dV over all query heads of the key/value head.  What sees a key is one interval of queries
-// (fa_rules_ranges.cu): a key tile visits one run of query tiles and only its first and last ones are masked.
+// (fa_rules_ranges.cuh): a key tile visits one run of query tiles and only its first and last ones are masked.
 //
 // The tiles, roles, tensor memory, pipeline and bounded waits are those of fa_bwd_kernel.cuh (a work item is a
 // 128-key tile whose dK and dV stay in tensor memory while Q and dO tiles pass by).  What differs:

@@ -5,7 +5,7 @@
 //   O_i = sum_j softmax_j(s) V_j over the keys that i sees,  LSE_i = log sum_j exp(s)
 // i sees j unless a causal mask hides it (j after i's position and not in the sequence's prefix) or the two are in
 // different documents.  What a query sees is one interval of keys [lo, hi) whose ends never fall from a row to the
-// next (fa_rules_ranges.cu), so a query tile visits one run of key tiles, and only its first and last ones are masked.
+// next (fa_rules_ranges.cuh), so a query tile visits one run of key tiles, and only its first and last ones are masked.
 //
 // The tiles, roles, tensor memory, pipeline and bounded waits are those of fa_fwd_kernel.cuh (two query tiles of 128
 // rows share a ring of K and V tiles; two softmax warpgroups, a producer, an issuer for each query tile).  What
@@ -39,6 +39,8 @@ struct RulesItem {
     int a[2], n[2];
     int j0, n_kv;   // first key tile, key tiles
 };
+// Steepest slope (base 2) whose bias varies by at most 64 within a tile.
+constexpr float kBoundSlope2 = 64.f / (kBlockN - 1);
 enum : int { kBarItemFull = kBarCount, kBarItemEmpty = kBarItemFull + kRulesItems, kRulesBarCount = kBarItemEmpty + kRulesItems };
 
 template <int D, int OutBytes>
@@ -455,14 +457,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_rules_fwd_kernel(const __gr
                 };
                 float2 rs[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                 uint32_t pk[kBlockN / 2];  // weights, rounded to bf16 for the product with V (half a step, 2^-8 of each)
-                // Weights of scores g(s, -max), their sums in four running pairs.
+                // Weights of scores g(s, -max, column), their sums in four running pairs.
                 auto weigh = [&](auto g) {
                     const float2 negm = two(-m_use);
 #pragma unroll
                     for (int c = 0; c < kBlockN; c += 8) {
 #pragma unroll
                         for (int h = 0; h < 4; ++h) {
-                            const float2 x = g(make_float2(s[c + 2 * h], s[c + 2 * h + 1]), negm);
+                            const float2 x = g(make_float2(s[c + 2 * h], s[c + 2 * h + 1]), negm, c + 2 * h);
                             const float2 e = make_float2(ex2(x.x), ex2(x.y));
                             rs[h] = __fadd2_rn(rs[h], e);
                             pk[c / 2 + h] = pack_bf16x2(e.x, e.y);
@@ -475,17 +477,41 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_rules_fwd_kernel(const __gr
                     if (!C::kAliasP && j > a) pv_ready = mbar_test(bar(kBarPVDone + wg), (tiles - 1) & 1);
                 };
                 const int range = kWithCap ? cap_range(p.rules, mrow) : 0;
+                bool done = false;
                 if (kWithCap && !kWithBias && range == 3 && !mask) {
                     // tanh rises with its argument: the largest raw score is the largest capped one
                     const float2 top = two(max_of<kBlockN>(s));
                     raise(__fmul2_rn(top, cap_factor(top, p.rules.near)).x);
                     test_pv();
-                    weigh([&](float2 x, float2 m) { return __ffma2_rn(x, cap_factor(x, p.rules.near), m); });
-                } else {
+                    weigh([&](float2 x, float2 m, int) { return __ffma2_rn(x, cap_factor(x, p.rules.near), m); });
+                    done = true;
+                }
+                bool before = false, behind = false;  // every key that counts lies at or before, behind every row's position
+                if constexpr (kWithBias) {
+                    // (keys behind a causal row's position are hidden, whatever bias they get)
+                    before = __all_sync(0xffffffffu, k0 + kBlockN - 1 <= qpos || (p.causal && hi <= qpos + 1));
+                    behind = __all_sync(0xffffffffu, k0 >= qpos);
+                }
+                if (kWithBias && !kWithCap && !mask && (before || behind) && slope2 >= 0.f && slope2 <= kBoundSlope2) {
+                    // The largest raw score with the nearest key's bias stands for the largest biased score: it is at
+                    // most 127 slope2 <= 64 above it, and the maximum need not be looked for nor taken off by itself (d = 64,
+                    // 4 sequences of 4097 tokens, 16 heads: 206 us, so 192).  No weight is 1 then, and all are rounded alike.
+                    const float dist = static_cast<float>(qpos - k0);
+                    const float sg = before ? slope2 : -slope2;  // bias of column c: sg (c - dist)
+                    raise(fmaf(mrow, p.rules.mult, sg * ((before ? kBlockN - 1.f : 0.f) - dist)));
+                    test_pv();
+                    const float base = fmaf(-sg, dist, -m_use);
+                    float2 b[4];
+                    weigh([&](float2 x, float2, int c) {
+                        float2& y = b[(c >> 1) & 3];  // a start for each 32 columns and steps of 8, as add_bias
+                        if (c % 32 < 8) y = make_float2(fmaf(static_cast<float>(c), sg, base), fmaf(static_cast<float>(c + 1), sg, base));
+                        else y = __fadd2_rn(y, two(8.f * sg));
+                        return __ffma2_rn(x, two(p.rules.mult), y);
+                    });
+                    done = true;
+                }
+                if (!done) {
                     if constexpr (kWithBias) {
-                        // keys behind a causal row's position are hidden below, whatever bias they get
-                        const bool before = __all_sync(0xffffffffu, k0 + kBlockN - 1 <= qpos || (p.causal && hi <= qpos + 1));
-                        const bool behind = __all_sync(0xffffffffu, k0 >= qpos);
                         biased_scores<kBlockN, kWithCap>(s, p.rules, range, slope2, static_cast<float>(qpos - k0), before ? 1 : behind ? -1 : 0);
                     } else if constexpr (kWithCap) {
                         capped_scores<kBlockN>(s, p.rules, range);
@@ -495,11 +521,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_rules_fwd_kernel(const __gr
                     if constexpr (RULES == kNoRules) {
                         raise(mrow * p.rules.mult);
                         test_pv();
-                        weigh([&](float2 x, float2 m) { return __ffma2_rn(x, two(p.rules.mult), m); });
+                        weigh([&](float2 x, float2 m, int) { return __ffma2_rn(x, two(p.rules.mult), m); });
                     } else {
                         raise(mrow);
                         test_pv();
-                        weigh([&](float2 x, float2 m) { return __fadd2_rn(x, m); });
+                        weigh([&](float2 x, float2 m, int) { return __fadd2_rn(x, m); });
                     }
                 }
                 // O_i and the P_i columns are free once P_i(j-1) V_{j-1} has completed.  With P aliased into S_i this is
