@@ -3,17 +3,18 @@
 // Either side of a row is one result of its unit, or the parts of a unit that several shares hold (fa_tree_kernel.cuh):
 //   lse = log sum_s exp(lse_s),  o = sum_s exp(lse_s - lse) o_s
 // over all of them ("flash_lab.py", section 4).  A warp a row.  The time is that of three loads one behind the other
-// (the units' records, the log-sum-exps, the outputs) and of the launch; up to 8 results are loaded beside their
-// log-sum-exps.
+// (the units' records, the log-sum-exps, the outputs) and of the launch; up to FEW results are loaded beside their
+// log-sum-exps.  More of them take registers, which counts where there are many rows: 16 sequences behind 8192 tokens
+// with 13 parts a row 31.5 us at 8 or 12, 28.2 at 16; 64 behind 32K with 10 parts 102, 100 and 103; 256 97.7, 99.9 and 104.
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "fa_rules_common.cuh"
 
 namespace fa {
 
-constexpr int kMergeFew = 8;
-
-template <int D>
+template <int D, int FEW>
 __global__ void __launch_bounds__(256) fa_prefix_merge_kernel(const __grid_constant__ PrefixMergeParams p)
 {
     grid_dependency_wait();
@@ -68,26 +69,26 @@ __global__ void __launch_bounds__(256) fa_prefix_merge_kernel(const __grid_const
     for (int e = 0; e < V; ++e) acc[e] = 0.f;
     float M = -INFINITY, sum = 0.f;
     bool live = false;
-    if (n <= kMergeFew) {
-        float x[kMergeFew], v[kMergeFew][V];
+    if (n <= FEW) {
+        float x[FEW], v[FEW][V];
 #pragma unroll
-        for (int s = 0; s < kMergeFew; ++s) {
+        for (int s = 0; s < FEW; ++s) {
             x[s] = load_lse(s);
             if (s < n) load(s, v[s]);
         }
 #pragma unroll
-        for (int s = 0; s < kMergeFew; ++s) {
+        for (int s = 0; s < FEW; ++s) {
             live = live || x[s] != -INFINITY;
             M = fmaxf(M, x[s]);
         }
 #pragma unroll
-        for (int s = 0; s < kMergeFew; ++s) {
+        for (int s = 0; s < FEW; ++s) {
             x[s] = x[s] == -INFINITY ? 0.f : ex2((x[s] - M) * kLog2e);
             sum += x[s];
         }
         const float inv = live ? 1.f / sum : 0.f;
 #pragma unroll
-        for (int s = 0; s < kMergeFew; ++s) {
+        for (int s = 0; s < FEW; ++s) {
             if (s >= n) continue;
             const float f = x[s] * inv;  // an empty result is 0
 #pragma unroll
@@ -145,12 +146,16 @@ cudaError_t launch_prefix_merge(const PrefixMergeParams& p, int d, cudaStream_t 
 {
     const long long rows = static_cast<long long>(p.B) * p.Hkv * p.R;
     const unsigned grid = static_cast<unsigned>((rows + 7) / 8);
-    switch (d) {
-    case 32: return launch_pdl(fa_prefix_merge_kernel<32>, grid, 256, 0, st, p);
-    case 64: return launch_pdl(fa_prefix_merge_kernel<64>, grid, 256, 0, st, p);
-    case 128: return launch_pdl(fa_prefix_merge_kernel<128>, grid, 256, 0, st, p);
-    default: return cudaErrorInvalidValue;
-    }
+    auto with = [&](auto few) {
+        switch (d) {
+        case 32: return launch_pdl(fa_prefix_merge_kernel<32, few()>, grid, 256, 0, st, p);
+        case 64: return launch_pdl(fa_prefix_merge_kernel<64, few()>, grid, 256, 0, st, p);
+        case 128: return launch_pdl(fa_prefix_merge_kernel<128, few()>, grid, 256, 0, st, p);
+        default: return cudaErrorInvalidValue;
+        }
+    };
+    if (rows <= 1024) return with(std::integral_constant<int, 16>());
+    return rows <= 4096 ? with(std::integral_constant<int, 12>()) : with(std::integral_constant<int, 8>());
 }
 
 }  // namespace fa

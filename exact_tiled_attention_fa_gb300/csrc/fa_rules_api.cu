@@ -353,6 +353,9 @@ fa_status fa_decode_prefix(const void* q, const void* k_prefix, const void* v_pr
         return FA_ERR_INVALID_ARG;
     if (P_max > 0x3fffff00 || Nk_max > 0x3fffff00) return FA_ERR_INVALID_ARG;  // positions behind both are 32-bit
     if (!head_ok(d) || dv != d || Hq / Hkv > fa::kBlockM) return FA_ERR_UNSUPPORTED;
+    // the kernel counts tiles, and a few more for each unit, in 32 bits
+    const double units_most = static_cast<double>(B) * Hkv, tiles_most = units_most * (tiles_of(Nk_max) + tiles_of(P_max) + 8.0);
+    if (tiles_most > 0x3fffffff) return FA_ERR_INVALID_ARG;
     int sms = 0;
     if (fa::device_sm_count(&sms) != cudaSuccess) return FA_ERR_CUDA;
     const PrefixPlan plan(B, Hq, Hkv, d, sms);

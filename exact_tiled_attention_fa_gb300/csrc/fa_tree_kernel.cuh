@@ -326,49 +326,50 @@ __device__ __forceinline__ TreeLen shared_prefix(const PrefixParams& p)
 }
 __device__ __forceinline__ TreeLen shared_own(const PrefixParams& p, int b) { return tree_clamp(p.seqlens[b], 0, 0, p.Nk_max, p.status); }
 
+// (32-bit arithmetic: the host bounds the places.  c * total / shares is c * (total / shares) and the remainder's share.)
 __device__ __forceinline__ TreeStart shared_locate(const PrefixParams& p, int c, int lane)
 {
-    const TreeLen pre = p.n_pre > 0 ? shared_prefix(p) : TreeLen{0, 0};
-    const int pre_places = pre.tiles() + p.unit_cost;
-    const long long pre_total = static_cast<long long>(p.n_pre) * pre_places;
     TreeLen len{0, 0};  // the first 32 sequences'
     if (lane < p.B) len = shared_own(p, lane);
-    long long total = lane < p.B ? len.tiles() + p.unit_cost : 0;
+    const TreeLen pre = p.n_pre > 0 ? shared_prefix(p) : TreeLen{0, 0};
+    const int pre_places = pre.tiles() + p.unit_cost;
+    const int pre_total = p.n_pre * pre_places;
+    int total = lane < p.B ? len.tiles() + p.unit_cost : 0;
     for (int b = 32 + lane; b < p.B; b += 32) total += shared_own(p, b).tiles() + p.unit_cost;
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    total = total * p.Hkv + pre_total;
-    const long long shares = p.num_shares < total ? p.num_shares : total;
+    total = __reduce_add_sync(0xffffffffu, total) * p.Hkv + pre_total;
+    const int shares = min(p.num_shares, total);
     TreeStart s{0, 0, total, shares, 0, 0, 0, 0, 0};
     if (c >= shares) return s;
-    s.w0 = share_begin(c, total, shares);
-    s.w1 = share_begin(c + 1, total, shares);
-    if (s.w0 < pre_total) {
+    const int each = total / shares, rest = total - each * shares;
+    const int w0 = c * each + c * rest / shares;
+    s.w0 = w0;
+    s.w1 = (c + 1) * each + (c + 1) * rest / shares;
+    if (w0 < pre_total) {
         s.b = -1;
-        s.unit = static_cast<int>(s.w0 / pre_places);
-        s.at = static_cast<int>(s.w0 - static_cast<long long>(s.unit) * pre_places);
+        s.unit = w0 / pre_places;
+        s.at = w0 - s.unit * pre_places;
         s.prefix = pre.prefix;
         return s;
     }
-    long long base = pre_total;
+    int base = pre_total;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
         const int b = b0 + lane;
         if (b0 > 0 && b < p.B) len = shared_own(p, b);
         const int places = b < p.B ? len.tiles() + p.unit_cost : 0;
-        long long incl = static_cast<long long>(places) * p.Hkv;
+        int incl = places * p.Hkv;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+            const int x = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += x;
         }
-        const unsigned past = __ballot_sync(0xffffffffu, base + incl > s.w0);
+        const unsigned past = __ballot_sync(0xffffffffu, base + incl > w0);
         if (past != 0u) {
             const int j = __ffs(past) - 1;  // the first sequence that ends after w0
             const int pj = __shfl_sync(0xffffffffu, places, j);
-            const long long in = s.w0 - (base + __shfl_sync(0xffffffffu, incl, j) - static_cast<long long>(pj) * p.Hkv);
+            const int in = w0 - (base + __shfl_sync(0xffffffffu, incl, j) - pj * p.Hkv);
             s.b = b0 + j;
-            s.unit = static_cast<int>(in / pj);
-            s.at = static_cast<int>(in - static_cast<long long>(s.unit) * pj);
+            s.unit = in / pj;
+            s.at = in - s.unit * pj;
             s.prefix = __shfl_sync(0xffffffffu, len.prefix, j);
             return s;
         }
@@ -644,6 +645,18 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
         tmem_relinquish();
     }
+    if constexpr (SHARED) {  // (maps are arguments: no need to wait for the kernel before)
+        if (warp == kTrWarpProducer && lane == 0) {
+            prefetch_tensormap(&p.tm_q1);
+            prefetch_tensormap(&p.tm_k);
+            prefetch_tensormap(&p.tm_v);
+            if (p.n_pre > 0) {
+                prefetch_tensormap(&p.tm_q);
+                prefetch_tensormap(&p.tm_kp);
+                prefetch_tensormap(&p.tm_vp);
+            }
+        }
+    }
     grid_dependency_wait();    // launched as a programmatic dependent of the previous kernel
     grid_launch_dependents();  // the merge may begin launching (it waits for this grid)
     if (warp % 4 == 0 && warp / 4 < kStreams) {  // share `stream * CTAs + CTA`: few shares go to different SMs
@@ -676,18 +689,11 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         if (stream < kStreams) {
             // ======================================================== producer
             if (lane == 0) {
-                if constexpr (SHARED) {
-                    prefetch_tensormap(&p.tm_q1);
-                    if (p.n_pre > 0) {
-                        prefetch_tensormap(&p.tm_q);
-                        prefetch_tensormap(&p.tm_kp);
-                        prefetch_tensormap(&p.tm_vp);
-                    }
-                } else {
+                if constexpr (!SHARED) {
                     prefetch_tensormap(&p.tm_q);
+                    prefetch_tensormap(&p.tm_k);
+                    prefetch_tensormap(&p.tm_v);
                 }
-                prefetch_tensormap(&p.tm_k);
-                prefetch_tensormap(&p.tm_v);
                 // K and V are read again only by a group's further query blocks
                 const uint64_t pol_kv = p.n_qp > 1 ? policy_evict_last() : policy_evict_first();  // (SHARED: the prefix's)
                 const uint64_t pol_own = SHARED ? policy_evict_first() : pol_kv;

@@ -135,7 +135,7 @@ def test_decode_prefix_refusals(lib):
                dict(vp=ODD), dict(k=ODD), dict(v=ODD), dict(o=ODD), dict(lse=ODD4), dict(plen=ODD4), dict(lens=ODD4), dict(slopes=ODD4),
                dict(ws=ctypes.c_void_p(0x10000080)), dict(B=0), dict(Hq=0), dict(Hkv=3), dict(Hkv=0), dict(Nk=0), dict(d=0), dict(dv=0),
                dict(scale=0.0), dict(cap=-1.0), dict(cap=float("nan")), dict(odt=2), dict(P_max=0x40000000), dict(Nk=0x40000000),
-               dict(B=1 << 16, Hq=1 << 16, Hkv=1 << 15)):
+               dict(B=1 << 16, Hq=1 << 16, Hkv=1 << 15), dict(B=1 << 12, Hq=1 << 10, Hkv=1 << 10, Nk=1 << 25)):
         assert call(**kw) == INVALID, kw
     for kw in (dict(d=96, dv=96), dict(dv=32), dict(Hq=258, Hkv=2)):
         assert call(**kw) == UNSUPPORTED, kw
