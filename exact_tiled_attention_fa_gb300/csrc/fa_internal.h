@@ -274,7 +274,8 @@ struct ScoreRules {
     float cap_in;         // scale / cap, so that cap * tanh(cap_in * S) is the capped score; 0: no cap
     float mult;           // capped scores in base 2 are mult * tanh, others mult * S: cap or scale, times log2(e)
     const float* slopes;  // fp32 [Hq] or nullptr
-    // tanh(cap_in * S), times mult except in the backward, as S P(S^2) (fa_rules_common.cuh, cap_factor)
+    float bias_in;        // log2(e) / mult: slopes[h] * bias_in * distance is taken off what mult multiplies
+    // tanh(cap_in * S), times mult in forward kernels without a bias, as S P(S^2) (fa_rules_common.cuh, cap_factor)
     float2 near[3], mid[4], wide[6];  // (each twice, as the two-wide operations take them)
     float near_in, mid_in, wide_in;  // cap_in over the polynomials' ranges: |S| times it is at most 1 where they hold; +inf: nowhere
 };
@@ -355,7 +356,7 @@ struct PrefixSide {
 struct PrefixMergeParams {
     PrefixSide pre, own;  // pre.units = nullptr: no prefix
     const float *o_part, *lse_part;
-    int part_rows;
+    int part_rows, num_shares;
     void* o;
     float* lse;
     int B, Hkv, R, seqs, n_qp;

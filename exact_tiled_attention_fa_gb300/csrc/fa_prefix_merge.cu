@@ -29,9 +29,16 @@ __global__ void __launch_bounds__(256) fa_prefix_merge_kernel(const __grid_const
     // the row's place in its prefix unit
     const int qp = b / p.seqs;  // query tile
     const int row_pre = (b - qp * p.seqs) * p.R + r;
+    // A unit's record, or none: where a wait ran out it may not have been written, and what stands there is not to be
+    // followed out of the slots.
+    auto record = [&](const TreeJoin* at) -> TreeJoin {
+        TreeJoin j = *at;
+        if (j.rows < 0 || j.rows >= p.num_shares || j.parts < 0 || j.parts > p.num_shares - j.rows) j = TreeJoin{0, 0, 0};
+        return j;
+    };
     TreeJoin jp{0, 0, 0};
-    const TreeJoin jo = p.own.units[group];
-    if (p.pre.units != nullptr) jp = p.pre.units[kvh * p.n_qp + qp];
+    const TreeJoin jo = record(p.own.units + group);
+    if (p.pre.units != nullptr) jp = record(p.pre.units + (kvh * p.n_qp + qp));
     else if (jo.parts == 1) return;  // written where it was made
     const int n1 = jp.parts, n = n1 + jo.parts;
     // row of result s among its side's, and that side's arrays

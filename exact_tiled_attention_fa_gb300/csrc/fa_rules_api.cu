@@ -1,8 +1,8 @@
 // fa_rules_api.cu -- the C ABI of attention under score rules (include/fa.h): forward, backward, decode behind
-// a shared prefix.  Argument checks,
-// workspace layout and dispatch, host code only.
+// a shared prefix.  Argument checks, workspace layout and dispatch, host code only.
 #include <cmath>
 #include <cstdint>
+#include <limits>
 #include <type_traits>
 
 #include "fa_internal.h"
@@ -36,28 +36,32 @@ struct Ranges {
     }
 };
 
-// Scale and cap as the kernels take them (`score`: the polynomials with mult in them); false for a cap or scale that fp32
-// cannot hold so.
-bool make_rules(fa::ScoreRules* r, float scale, float softcap, const float* slopes, bool score)
+// Scale and cap as the kernels take them (`forward`: the polynomials with mult in them, unless there is a bias); false
+// for a cap or scale that fp32 cannot hold so.
+bool make_rules(fa::ScoreRules* r, float scale, float softcap, const float* slopes, bool forward)
 {
     if (!(std::isfinite(scale) && scale > 0.f) || !(std::isfinite(softcap) && softcap >= 0.f)) return false;
     r->cap_in = softcap > 0.f ? scale / softcap : 0.f;
     r->mult = (softcap > 0.f ? softcap : scale) * fa::kLog2e;
     r->slopes = slopes;
-    if (!(std::isfinite(r->mult) && r->mult > 0.f && std::isfinite(r->cap_in)) || (softcap > 0.f && r->cap_in == 0.f)) return false;
+    r->bias_in = fa::kLog2e / r->mult;
+    auto normal = [](float x) { return std::isfinite(x) && x >= std::numeric_limits<float>::min(); };
+    if (!normal(r->mult) || (softcap > 0.f && !normal(r->cap_in)) || (slopes != nullptr && !normal(r->bias_in))) return false;
     r->near_in = r->mid_in = r->wide_in = INFINITY;
-    // the polynomials' coefficients, powers of cap_in up to the seventh and the eleventh, must be normal numbers
     const double near[] = {FA_TANH_NEAR}, mid[] = {FA_TANH_MID}, wide[] = {FA_TANH_WIDE}, k = r->cap_in;
-    if (k < 1e-5 || k > 1e2) return true;
-    double at = k * (score ? r->mult : 1.0);
+    if (softcap == 0.f || k > 1e2) return true;  // (above, powers of cap_in up to the eleventh leave fp32)
+    // Below 1e-5 and 8e-4 the seventh and the eleventh power come near fp32's least.  The near polynomial is then taken
+    // alone: where its own higher terms vanish they are below 1e-7 of scores up to 10^6.
+    const bool low = k < 1e-5;
+    double at = k * (forward && slopes == nullptr ? r->mult : 1.0);
     for (int i = 0; i < 6; ++i, at *= k * k) {
         auto twice = [&](double c) { return make_float2(static_cast<float>(c * at), static_cast<float>(c * at)); };
         if (i < 3) r->near[i] = twice(near[i]);
-        if (i < 4) r->mid[i] = twice(mid[i]);
+        if (i < 4) r->mid[i] = twice(!low ? mid[i] : i < 3 ? near[i] : 0.0);
         r->wide[i] = twice(wide[i]);
     }
     r->near_in = r->cap_in / fa::kNearRange;
-    r->mid_in = r->cap_in / fa::kMidRange;
+    if (!low) r->mid_in = r->cap_in / fa::kMidRange;
     if (k >= 8e-4) r->wide_in = r->cap_in / fa::kWideRange;
     return true;
 }
@@ -417,6 +421,7 @@ fa_status fa_decode_prefix(const void* q, const void* k_prefix, const void* v_pr
     m.o_part = p.o_part;
     m.lse_part = p.lse_part;
     m.part_rows = p.part_rows;
+    m.num_shares = p.num_shares;
     m.o = o;
     m.lse = lse;
     m.B = B;

@@ -94,20 +94,18 @@ __device__ __forceinline__ void rules_weights(const uint32_t (&u)[64], float (&p
                                               const ScoreRules& r, float slope2, float dist, int sign)
 {
     const float2 m2 = two(r.mult);
-    const float sg = sign < 0 ? slope2 : -slope2;
-    const float2 stride = two(8.f * sg);
+    const float2 sg = two(sign < 0 ? slope2 : -slope2), eight = two(8.f);
+    float2 away[4];  // distances, exact and counted on by eights
+    if constexpr (BIAS) {
+#pragma unroll
+        for (int h = 0; h < 4; ++h) away[h] = make_float2(dist + static_cast<float>(2 * h), dist + static_cast<float>(2 * h + 1));
+    }
 #pragma unroll
     for (int c0 = 0; c0 < 64; c0 += 32) {
         float t[32];
 #pragma unroll
         for (int c = 0; c < 32; ++c) t[c] = __uint_as_float(u[c0 + c]);
         if constexpr (CAP == 0) tanh_any<32>(t, r.cap_in);
-        float2 b[4];
-        if constexpr (BIAS) {
-#pragma unroll
-            for (int h = 0; h < 4; ++h)
-                b[h] = make_float2(sg * (dist + static_cast<float>(c0 + 2 * h)), sg * (dist + static_cast<float>(c0 + 2 * h + 1)));
-        }
 #pragma unroll
         for (int c = 0; c < 32; c += 8) {
 #pragma unroll
@@ -122,8 +120,8 @@ __device__ __forceinline__ void rules_weights(const uint32_t (&u)[64], float (&p
                     float2 x = __ffma2_rn(y, m2, e == 0 ? make_float2(-l4.x, -l4.y) : make_float2(-l4.z, -l4.w));
                     if constexpr (BIAS) {
                         if (sign != 0) {
-                            x = __fadd2_rn(x, b[h + e]);
-                            if (c + 8 < 32) b[h + e] = __fadd2_rn(b[h + e], stride);
+                            x = __ffma2_rn(sg, away[h + e], x);
+                            if (c0 + c + 8 < 64) away[h + e] = __fadd2_rn(away[h + e], eight);
                         } else {
                             x.x = fmaf(-slope2, fabsf(dist + static_cast<float>(c0 + i)), x.x);
                             x.y = fmaf(-slope2, fabsf(dist + static_cast<float>(c0 + i + 1)), x.y);

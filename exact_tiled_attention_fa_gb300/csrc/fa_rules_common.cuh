@@ -2,7 +2,7 @@
 //
 // Scores.  With x = scale q.k, a cap c > 0 makes it c tanh(x / c), whose slope is 1 - tanh^2; a bias then takes
 // slope_h |i - j| off (i, j the positions of query and key).  In base 2, as the exponentials want them:
-// mult * tanh(cap_in * S) - slope2 * |i - j|, S = q.k.
+// mult * (tanh(cap_in * S) - slope * |i - j|), S = q.k, slope = slope_h * bias_in.
 #pragma once
 
 #include <cstdint>
@@ -27,13 +27,15 @@ __device__ __forceinline__ float rcp_approx(float x)
 
 // The cap.  tanh(u) for |u| <= kWideRange, where the scores that a cap is meant for almost always are, is u P(u^2) with
 // P the minimax polynomial for tanh(u) / u (Remez exchange on u^2): degree n = 2 up to kNearRange (relative error
-// 1.2e-6), 3 up to kMidRange (1.1e-6), 5 up to kWideRange (5.9e-7).  With cap_in and mult in its coefficients a capped score is S Q(S^2): n + 1
-// operations and the one that takes the maximum off it anyway.  (What bounds them is the FMA units, 128 lanes an SM,
-// whether two operations go in one instruction or not: a polynomial of degree 5 for every argument, scaled before it,
-// took 8 and the causal prefill of 4 sequences of 4097 tokens, 16 heads of 128, 487 us; without a cap 341; PLACEHOLDER.)
+// 1.2e-6), 3 up to kMidRange (1.1e-6), 5 up to kWideRange (5.9e-7).  With cap_in and mult in its coefficients a capped
+// score is S Q(S^2): n + 1 operations and the one that takes the maximum off it anyway.  (What bounds them is the FMA
+// units, 128 lanes an SM, whether two operations go in one instruction or not.  Causal prefill of 4 sequences of 4097
+// tokens, 16 heads of 128, a cap of 50 that leaves most tiles in the near range: a polynomial of degree 5 for every
+// argument, scaled before it, 487 us, the three 348, without a cap 286.)
 // Other arguments take 1 - 2 / (1 + e^2u): two operations of the special function unit that the exponentials also need
-// (586 us); its absolute error of 2e-7 is one of 1e-5 of a weight at a cap of 50.  +-infinity gives +-1, NaN NaN.  (The
-// device's own tanh instruction is off by 2^-11 of its result: at a score of 20 by 0.01, and the weight by as much.)
+// (586 us for all tiles); its absolute error of 2e-7 is one of 1e-5 of a weight at a cap of 50.  +-infinity gives +-1, NaN
+// NaN.  (The device's own tanh instruction is off by 2^-11 of its result: at a score of 20 by 0.01, and the weight by as
+// much.)
 constexpr float kNearRange = 0.3f, kMidRange = 0.55f, kWideRange = 1.f;
 #define FA_TANH_NEAR 0.999998838848, -0.333100215997, 0.126339459894
 #define FA_TANH_MID 0.999998880298, -0.333213872584, 0.131312313762, -0.0426959989808
@@ -92,54 +94,48 @@ __device__ __forceinline__ void capped_scores(float* s, const ScoreRules& r, int
     }
 }
 
-// s <- f(s, -slope2 * |dist - c|) by pairs, for columns c = 0 .. N - 1 (dist: the position of the row less that of column
-// 0).  sign = 1 where every column that counts lies at or before its row's position, -1 where behind it: the bias is then
-// linear in c, a start for each 32 columns and steps of 8 added to it (four roundings).  0: either.
+// s <- f(s) - slope * |dist - c| by pairs, for columns c = 0 .. N - 1 (dist: the position of the row less that of column
+// 0).  sign = 1 where every column that counts lies at or before its row's position, -1 where behind it: the distance is
+// then one sign's, counted on by eights.  0: either.  (Distances are whole numbers and exact.  Adding multiples of the
+// slope instead is as fast, but the bias of a key next to the row is then off by the rounding of one a tile away.)
 template <int N, typename F>
-__device__ __forceinline__ void add_bias(float* s, float slope2, float dist, int sign, F f)
+__device__ __forceinline__ void add_bias(float* s, float slope, float dist, int sign, F f)
 {
     if (sign != 0) {
-        const float sg = sign > 0 ? slope2 : -slope2;
-        const float base = -sg * dist;
-        const float2 step = two(8.f * sg);
+        const float2 sg = two(sign > 0 ? slope : -slope), eight = two(8.f);
+        float2 d[4];
 #pragma unroll
-        for (int c0 = 0; c0 < N; c0 += 32) {
-            float2 b[4];
+        for (int h = 0; h < 4; ++h) d[h] = make_float2(static_cast<float>(2 * h) - dist, static_cast<float>(2 * h + 1) - dist);
 #pragma unroll
-            for (int h = 0; h < 4; ++h)
-                b[h] = make_float2(fmaf(static_cast<float>(c0 + 2 * h), sg, base), fmaf(static_cast<float>(c0 + 2 * h + 1), sg, base));
+        for (int c = 0; c < N; c += 8) {
 #pragma unroll
-            for (int c = 0; c < 32; c += 8) {
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    const int i = c0 + c + 2 * h;
-                    const float2 y = f(make_float2(s[i], s[i + 1]), b[h]);
-                    s[i] = y.x;
-                    s[i + 1] = y.y;
-                    if (c + 8 < 32) b[h] = __fadd2_rn(b[h], step);
-                }
+            for (int h = 0; h < 4; ++h) {
+                const int i = c + 2 * h;
+                const float2 y = __ffma2_rn(sg, d[h], f(make_float2(s[i], s[i + 1])));
+                s[i] = y.x;
+                s[i + 1] = y.y;
+                if (c + 8 < N) d[h] = __fadd2_rn(d[h], eight);
             }
         }
     } else {
 #pragma unroll
         for (int c = 0; c < N; c += 2) {
-            const float2 y = f(make_float2(s[c], s[c + 1]), make_float2(-slope2 * fabsf(dist - static_cast<float>(c)),
-                                                                        -slope2 * fabsf(dist - static_cast<float>(c + 1))));
-            s[c] = y.x;
-            s[c + 1] = y.y;
+            const float2 y = f(make_float2(s[c], s[c + 1]));
+            s[c] = fmaf(-slope, fabsf(dist - static_cast<float>(c)), y.x);
+            s[c + 1] = fmaf(-slope, fabsf(dist - static_cast<float>(c + 1)), y.y);
         }
     }
 }
 
-// Scores s of N keys under a bias, and a cap if CAP: in base 2, in place.
+// Scores s of N keys under a bias, and a cap if CAP, in place, over mult (as S and tanh are).
 template <int N, bool CAP>
-__device__ __forceinline__ void biased_scores(float* s, const ScoreRules& r, int range, float slope2, float dist, int sign)
+__device__ __forceinline__ void biased_scores(float* s, const ScoreRules& r, int range, float slope, float dist, int sign)
 {
     if (CAP && range >= 2) {
-        add_bias<N>(s, slope2, dist, sign, [&](float2 x, float2 b) { return __ffma2_rn(x, cap_factor(x, r.mid), b); });
+        add_bias<N>(s, slope, dist, sign, [&](float2 x) { return __fmul2_rn(x, cap_factor(x, r.mid)); });
     } else {
         if (CAP) tanh_any<N>(s, r.cap_in);
-        add_bias<N>(s, slope2, dist, sign, [&](float2 x, float2 b) { return __ffma2_rn(x, two(r.mult), b); });
+        add_bias<N>(s, slope, dist, sign, [&](float2 x) { return x; });
     }
 }
 

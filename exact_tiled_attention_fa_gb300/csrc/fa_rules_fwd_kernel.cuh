@@ -18,11 +18,15 @@
 //  - An item's two query tiles may begin and end at different key tiles: K and V run over both, and the issuer of a
 //    tile passes on the stages that it does not visit.
 //  - Between a row's scores and its exponentials stand the cap and the bias, in registers.  Both can change which score
-//    is the largest, so its row's maximum is taken after them (without them the loads from tensor memory bring it).
-//    tanh is the expensive one; tanh_small has what was chosen and why.
+//    is the largest, so the row's maximum is taken after them (without them the loads from tensor memory bring it, and
+//    under a cap whose tile lies in the near range the largest raw score gives it).  What was chosen for tanh, and why,
+//    stands in fa_rules_common.cuh.
 //
-// What bounds it: the softmax's chain between two products, as in fa_fwd_kernel.cuh, lengthened by the cap's 4 and the
-// bias's 1 instruction a score.
+// What bounds it: the softmax's chain between two products, as in fa_fwd_kernel.cuh, lengthened by the FMA units' work on
+// the rules: at the shape above d = 64 153 us, with a bias 200, a cap of 50 216, both 301; d = 128 286, 315, 348, 391.
+// In documents (64 sequences of 1024 tokens, 16 heads of 64) 144 us: 3.7 TB/s of the 541 MB that have to move;
+// by the counters tensor cores 21 % busy, the ALUs (masks by bits, packing) 37 %, issue slots 42 %.  A correction warpgroup (fa_fwd at d = 128) was not taken
+// over: without masks fa_fwd is the faster one there (64 x 1024 tokens 458 us against 568), with causal masks it is not.
 #pragma once
 
 #include "fa_fwd_kernel.cuh"
@@ -39,8 +43,6 @@ struct RulesItem {
     int a[2], n[2];
     int j0, n_kv;   // first key tile, key tiles
 };
-// Steepest slope (base 2) whose bias varies by at most 64 within a tile.
-constexpr float kBoundSlope2 = 64.f / (kBlockN - 1);
 enum : int { kBarItemFull = kBarCount, kBarItemEmpty = kBarItemFull + kRulesItems, kRulesBarCount = kBarItemEmpty + kRulesItems };
 
 template <int D, int OutBytes>
@@ -401,7 +403,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_rules_fwd_kernel(const __gr
                     hi = min(f.Nk, max(off + row + 1, it.prefix));
                 }
             }
-            const float slope2 = kWithBias ? p.rules.slopes[it.bh - it.b * p.Hq] * kLog2e : 0.f;
+            const float slope = kWithBias ? p.rules.slopes[it.bh - it.b * p.Hq] * p.rules.bias_in : 0.f;
             float m_run = -INFINITY;  // running max of the scores in base 2 over visible keys
             float l = 0.f;
             int k0 = (it.j0 + a) * kBlockN;  // first key of the tile
@@ -457,14 +459,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_rules_fwd_kernel(const __gr
                 };
                 float2 rs[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                 uint32_t pk[kBlockN / 2];  // weights, rounded to bf16 for the product with V (half a step, 2^-8 of each)
-                // Weights of scores g(s, -max, column), their sums in four running pairs.
+                // Weights of scores g(s, -max), their sums in four running pairs.
                 auto weigh = [&](auto g) {
                     const float2 negm = two(-m_use);
 #pragma unroll
                     for (int c = 0; c < kBlockN; c += 8) {
 #pragma unroll
                         for (int h = 0; h < 4; ++h) {
-                            const float2 x = g(make_float2(s[c + 2 * h], s[c + 2 * h + 1]), negm, c + 2 * h);
+                            const float2 x = g(make_float2(s[c + 2 * h], s[c + 2 * h + 1]), negm);
                             const float2 e = make_float2(ex2(x.x), ex2(x.y));
                             rs[h] = __fadd2_rn(rs[h], e);
                             pk[c / 2 + h] = pack_bf16x2(e.x, e.y);
@@ -483,7 +485,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_rules_fwd_kernel(const __gr
                     const float2 top = two(max_of<kBlockN>(s));
                     raise(__fmul2_rn(top, cap_factor(top, p.rules.near)).x);
                     test_pv();
-                    weigh([&](float2 x, float2 m, int) { return __ffma2_rn(x, cap_factor(x, p.rules.near), m); });
+                    weigh([&](float2 x, float2 m) { return __ffma2_rn(x, cap_factor(x, p.rules.near), m); });
                     done = true;
                 }
                 bool before = false, behind = false;  // every key that counts lies at or before, behind every row's position
@@ -492,40 +494,22 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_rules_fwd_kernel(const __gr
                     before = __all_sync(0xffffffffu, k0 + kBlockN - 1 <= qpos || (p.causal && hi <= qpos + 1));
                     behind = __all_sync(0xffffffffu, k0 >= qpos);
                 }
-                if (kWithBias && !kWithCap && !mask && (before || behind) && slope2 >= 0.f && slope2 <= kBoundSlope2) {
-                    // The largest raw score with the nearest key's bias stands for the largest biased score: it is at
-                    // most 127 slope2 <= 64 above it, and the maximum need not be looked for nor taken off by itself (d = 64,
-                    // 4 sequences of 4097 tokens, 16 heads: 206 us, so 192).  No weight is 1 then, and all are rounded alike.
-                    const float dist = static_cast<float>(qpos - k0);
-                    const float sg = before ? slope2 : -slope2;  // bias of column c: sg (c - dist)
-                    raise(fmaf(mrow, p.rules.mult, sg * ((before ? kBlockN - 1.f : 0.f) - dist)));
-                    test_pv();
-                    const float base = fmaf(-sg, dist, -m_use);
-                    float2 b[4];
-                    weigh([&](float2 x, float2, int c) {
-                        float2& y = b[(c >> 1) & 3];  // a start for each 32 columns and steps of 8, as add_bias
-                        if (c % 32 < 8) y = make_float2(fmaf(static_cast<float>(c), sg, base), fmaf(static_cast<float>(c + 1), sg, base));
-                        else y = __fadd2_rn(y, two(8.f * sg));
-                        return __ffma2_rn(x, two(p.rules.mult), y);
-                    });
-                    done = true;
-                }
                 if (!done) {
                     if constexpr (kWithBias) {
-                        biased_scores<kBlockN, kWithCap>(s, p.rules, range, slope2, static_cast<float>(qpos - k0), before ? 1 : behind ? -1 : 0);
+                        biased_scores<kBlockN, kWithCap>(s, p.rules, range, slope, static_cast<float>(qpos - k0), before ? 1 : behind ? -1 : 0);
                     } else if constexpr (kWithCap) {
                         capped_scores<kBlockN>(s, p.rules, range);
                     }
                     if (mask) rules_mask(s, lo - k0, hi - k0);
                     if (RULES != kNoRules || mask) mrow = max_of<kBlockN>(s);
-                    if constexpr (RULES == kNoRules) {
-                        raise(mrow * p.rules.mult);
-                        test_pv();
-                        weigh([&](float2 x, float2 m, int) { return __ffma2_rn(x, two(p.rules.mult), m); });
-                    } else {
+                    if constexpr (RULES == kCap) {
                         raise(mrow);
                         test_pv();
-                        weigh([&](float2 x, float2 m, int) { return __fadd2_rn(x, m); });
+                        weigh([&](float2 x, float2 m) { return __fadd2_rn(x, m); });
+                    } else {
+                        raise(mrow * p.rules.mult);
+                        test_pv();
+                        weigh([&](float2 x, float2 m) { return __ffma2_rn(x, two(p.rules.mult), m); });
                     }
                 }
                 // O_i and the P_i columns are free once P_i(j-1) V_{j-1} has completed.  With P aliased into S_i this is

@@ -975,7 +975,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
         const uint32_t t_s = tmem + lane_base + C::col_s(wg);
         const uint32_t t_o = tmem + lane_base + C::col_o(wg);
         const uint32_t t_p = tmem + lane_base + C::col_p(wg);
-        const float sl2 = kWithCap || kWithBias ? 1.f : p.scale_log2;  // of what the exponentials take
+        const float sl2 = kWithCap && !kWithBias ? 1.f : p.scale_log2;  // of what the exponentials take
         int tiles = 0;                 // key tiles processed by this warpgroup
         int ready[2] = {0, 0};         // segments with tiles of warpgroup 0, 1 (ALT); this warpgroup's (else, [0])
         int segs = 0, k = 0;
@@ -991,7 +991,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             ok = __all_sync(0xffffffffu, ok);
             if (!ok || w.n == 0) break;
             int row0, rows;  // rows of this warpgroup's tile (<= 0: none), its first row
-            float slope2 = 0.f;
+            float slope = 0.f;
             int qpos = 0;  // SHARED: the row's position less that of the unit's first key
             if constexpr (SHARED) {
                 const int seq0 = w.b < 0 ? w.qp * p.seqs : w.b;  // the tile's first sequence
@@ -1000,7 +1000,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 if (kWithBias && r < rows) {
                     const int j = r / p.R;
                     const int kvh = w.b < 0 ? w.group : w.group - w.b * p.Hkv;
-                    slope2 = p.rules.slopes[kvh * p.R + (r - j * p.R)] * kLog2e;
+                    slope = p.rules.slopes[kvh * p.R + (r - j * p.R)] * p.rules.bias_in;
                     qpos = (w.b < 0 ? w.prefix + shared_own(p, seq0 + j).prefix : w.prefix) - 1;
                 }
             } else {
@@ -1024,14 +1024,14 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 tree_ancestors(p.parents != nullptr ? p.parents + static_cast<size_t>(w.b) * p.T : nullptr, p.T,
                                r < rows && node < w.nodes ? node : -1, lane, p.status, vis);
             }
-            // What the rules make of the scores x of keys from k0 on, in base 2, and their largest (mx: the largest absolute
+            // What the rules make of the scores x of keys from k0 on, over sl2, and their largest (mx: the largest absolute
             // one, as loaded; rows that are not there take no part in what the warp decides).
             auto apply = [&](auto& x, float mx, int k0) -> float {
                 constexpr int N = sizeof(x) / sizeof(float);
                 if constexpr (SHARED) {
                     const int range = kWithCap ? cap_range(p.rules, mx, r < rows) : 0;
                     if constexpr (kWithBias) {
-                        biased_scores<N, kWithCap>(x, p.rules, range, slope2, static_cast<float>(qpos - k0), 1);
+                        biased_scores<N, kWithCap>(x, p.rules, range, slope, static_cast<float>(qpos - k0), 1);
                     } else {
                         capped_scores<N>(x, p.rules, range);
                     }

@@ -46,9 +46,9 @@
  *   - q, k, v and the caches are bf16.  Arithmetic is fp32 (tensor-core accumulation in
  *     fp32; softmax statistics in fp32), but what a first product gives a second one on the
  *     tensor core is rounded to bf16 between them, by at most 2^-8 of each number: the softmax
- *     weights for the product with V (fa_fwd, fa_fwd_splitkv, fa_decode_tree, and
- *     fa_decode_splitkv_gqa but for groups of 1, 2 and, below d = 128, 4 heads), and P and
- *     scale * dS in fa_bwd, whatever the output's type.  O is written as bf16 (FA_BF16) or fp32 (FA_F32);
+ *     weights for the product with V (fa_fwd, fa_fwd_splitkv, fa_fwd_rules, fa_decode_tree,
+ *     fa_decode_prefix, and fa_decode_splitkv_gqa but for groups of 1, 2 and, below d = 128, 4
+ *     heads), and P and scale * dS in fa_bwd and fa_bwd_rules, whatever the output's type.  O is written as bf16 (FA_BF16) or fp32 (FA_F32);
  *     LSE is always fp32, natural log, scale included:
  *       LSE[i] = log sum_{visible j} exp(scale * q_i . k_j).
  *   - Causal masking places query i at position Nk - N + i and key j at position j
@@ -75,8 +75,8 @@
  *     of range) are recorded in a device status word read by fa_get_device_error.
  *   - Supported head sizes: d = dv, d in {32, 64, 128}.  Other sizes return
  *     FA_ERR_UNSUPPORTED.  Heads are independent; the number of key/value heads equals
- *     the number of query heads except in fa_decode_splitkv_gqa, fa_decode_tree and the
- *     fa_qk_norm_rope calls.
+ *     the number of query heads except in fa_decode_splitkv_gqa, fa_decode_tree, fa_decode_prefix,
+ *     fa_fwd_rules, fa_bwd_rules and the fa_qk_norm_rope calls.
  */
 #ifndef FA_H
 #define FA_H
@@ -507,7 +507,10 @@ fa_status fa_cache_compact(void* k_cache, void* v_cache, const int* seqlens, con
  *            query there, or before position 0, sees nothing.  Two runs of the same number are two
  *            documents.
  *
- *   slopes       fp32 [Hq]      (device; finite; NULL: no bias.  Distances are exact up to 2^24.)
+ *   scale > 0 and softcap >= 0, both finite; scale, 1 / scale, softcap, 1 / softcap and scale / softcap must be
+ *   within fp32's normal numbers where they come in (else FA_ERR_INVALID_ARG).
+ *   slopes       fp32 [Hq]      (device; slopes and slopes / scale, with a cap slopes / softcap, finite; NULL: no
+ *                bias.  Distances are exact up to 2^24.)
  *   documents    int32 [B, Nk]  (device; NULL: one document)
  *   prefix_lens  int32 [B]      (device; NULL: 0.  Without causal it has no effect.  Values outside
  *                [0, Nk] are clamped and recorded as FA_ERR_INVALID_ARG in the device status word.)
@@ -533,7 +536,7 @@ size_t fa_fwd_rules_workspace_size(int B, int N);
  *   workspace  with documents: ws_bytes >= fa_fwd_rules_workspace_size(B, N), 256-byte aligned; its
  *              contents on entry do not matter.  Calls sharing a workspace must not overlap on the GPU.
  *              Without documents it may be NULL.
- *   Hkv dividing Hq; d = dv in {32, 64, 128}; scale > 0, softcap >= 0, both finite.
+ *   Hkv dividing Hq; d = dv in {32, 64, 128}.
  * The result is the same from run to run.
  */
 fa_status fa_fwd_rules(const void* q, const void* k, const void* v, const float* slopes,

@@ -166,6 +166,52 @@ def test_capped_scores_in_both_forms_of_tanh():
         check_forward(o, lse, reference(q, kp, vp, k, v, lens, 300, rules), f"cap {cap}")
 
 
+def test_rows_past_32_bit_offsets():
+    """Caches of more than 2^31 elements: the last sequence's last head, against the same rows in a small cache."""
+    B, Hq, Hkv, P, Nk, d = 3, 16, 8, 300, 1 << 20, 128
+    if torch.cuda.mem_get_info()[0] < 30 << 30:
+        pytest.skip("needs 30 GB")
+    lens = i32(5, Nk, 333)
+    kc, vc = (torch.zeros((B, Hkv, Nk, d), dtype=BF16, device=DEV) for _ in range(2))
+    g = torch.Generator().manual_seed(8)
+    r = lambda *s: torch.randn(s, generator=g).to(BF16)  # noqa: E731
+    q, kp, vp, k, v = r(B, Hq, 1, d), r(Hkv, P, d), r(Hkv, P, d), r(B, Hkv, 400, d), r(B, Hkv, 400, d)
+    kc[:, :, :400], vc[:, :, :400] = k.to(DEV), v.to(DEV)
+    o, lse = call(q, kp, vp, kc, vc, lens, out_dtype=F32)
+    assert kc.numel() > 1 << 31 and fa().get_device_error() == 0
+    short = i32(5, 333, 333)
+    ref = reference(q, kp, vp, k, v, short, P, Rules())
+    for b in (0, 2):
+        check_forward(o[b:b + 1], lse[b:b + 1], {n: t[b:b + 1] for n, t in ref.items()}, f"{b}")
+    # sequence 1: 400 keys, and zeros' weights e^0 behind them
+    s = torch.einsum("hd,hkd->hk", q[1, :, 0].double(), torch.cat((kp, k[1]), 1).repeat_interleave(2, 0).double()) / d ** 0.5
+    want = torch.logsumexp(torch.cat((s, torch.full((Hq, 1), math.log(Nk - 400.0))), 1).double(), 1)
+    assert float((lse[1, :, 0].double().cpu() - want).abs().max()) < 1e-4
+
+
+@pytest.mark.parametrize("B,R,P,Nk,d", [(3, 4, 1000, 300, 32), (3, 4, 1000, 300, 64), (80, 4, 600, 300, 64), (3, 4, 1000, 300, 128),
+                                        (40, 8, 500, 300, 128)])
+def test_wait_limit_is_reported_and_the_next_call_is_right(B, R, P, Nk, d):
+    """With a limit of 1 ns waits run out in each form of the kernel: the status says so, every role ends, the merge
+    follows no record that was not written, and the next call is right."""
+    lens = torch.arange(B, dtype=torch.int32) % (Nk + 1)
+    Hq, Hkv = 4 * R, 4
+    x = inputs(B, Hq, Hkv, P, Nk, d, lens, seed=9)
+    ws = torch.full((fa().decode_prefix_workspace_size(B, Hq, Hkv, d, fa().num_sms()),), 0x7F, dtype=torch.uint8, device=DEV)
+    for junk in (0x7F, 0xFF, 0x01):
+        ws.fill_(junk)
+        fa().set_wait_timeout_ns(1)
+        try:
+            call(*x, lens, workspace=ws)
+            status = fa().get_device_error()
+        finally:
+            fa().set_wait_timeout_ns(0)
+        assert status == fa().FA_ERR_TIMEOUT
+    o, lse = call(*x, lens, out_dtype=F32, workspace=ws)
+    assert fa().get_device_error() == 0
+    check_forward(o, lse, reference(*x, lens, P, Rules()), "after")
+
+
 def test_outputs_and_workspace_given():
     B, Hq, Hkv, P, Nk, d = 50, 16, 4, 333, 90, 128
     lens = torch.arange(B, dtype=torch.int32) % 91

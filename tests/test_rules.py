@@ -146,6 +146,19 @@ def test_cap_over_its_whole_range(d):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("cap", [1e5, 1e7, 1e30])
+def test_cap_far_above_the_scores(cap):
+    """A cap that none of the scores comes near leaves them as they are.  The bounds are those without a cap: they take
+    the products' 2^-24 d |q| |k| four times over, and the cap's 1.2e-6 of a score is less than one of these times."""
+    q, k, v, do = inputs(2, 4, 2, 200, 260, 64, seed=21)
+    for sl in (None, slopes(4)):
+        ref = attention(q, k, v, Rules(causal=True, slopes=sl), do)
+        o, lse, grads = run(q, k, v, do, Rules(causal=True, softcap=cap, slopes=sl))
+        check_forward(o, lse, ref, f"cap {cap}")
+        check_gradients(grads, ref, f"cap {cap}")
+
+
+@pytest.mark.gpu
 def test_capped_scores_that_overflow():
     """q . k beyond fp32's range: the cap makes it +-cap."""
     q, k, v, _ = inputs(1, 1, 1, 130, 140, 64, seed=4)
@@ -248,7 +261,111 @@ def test_without_rules_as_the_plain_forward(d, causal):
     assert float((o - o2).abs().max()) < 2e-6 and float((lse - lse2).abs().max()) < 2e-6
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_slopes_of_every_kind(d, causal):
+    """Slopes of none, below zero, so steep that a tile's nearest and furthest key differ by more than 2^64, and just not."""
+    sl = torch.tensor([0.0, -0.01, 5.0, 0.34, 0.36, 1e-4])
+    pre = i32(0, 200)
+    for rules in (Rules(causal=causal, slopes=sl), Rules(causal=causal, slopes=sl, prefix_lens=pre), Rules(causal=causal, slopes=sl, softcap=5.0)):
+        check_all((2, 6, 3, 300, 420, d), rules, seed=d, what=f"slopes {d} {causal}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("causal", [False, True])
+def test_many_heads_at_once(causal):
+    """More heads than go out at once: several chunks of them, the last tiles ragged.  Against fwd and bwd."""
+    B, H, N, d = 21, 10, 2000, 128
+    q, k, v, do = (t.to(DEV) for t in inputs(B, H, H, N, N, d, seed=15))
+    o, lse = fa().fwd(q, k, v, causal=causal, out_dtype=F32)
+    o2, lse2 = fa().fwd_rules(q, k, v, causal=causal, out_dtype=F32)
+    assert float((o - o2).abs().max()) < 2e-6 and float((lse - lse2).abs().max()) < 2e-6
+    want = fa().bwd(q, k, v, o, lse, do, causal=causal, out_dtype=F32)
+    got = fa().bwd_rules(q, k, v, o, lse, do, causal=causal, out_dtype=F32)
+    # dq's sums come in any order; dk and dv in another one, of up to 16 tiles of fp32 sums
+    for a, b in zip(got, want):
+        assert float((a - b).abs().max()) < 2.0 ** -16 * float(b.abs().max())
+    # shared heads: a group's gradients are the sums of its heads'
+    o3, lse3 = fa().fwd_rules(q, k[:, ::5].contiguous(), v[:, ::5].contiguous(), causal=causal, out_dtype=F32)
+    kk, vv = (t[:, ::5].repeat_interleave(5, 1).contiguous() for t in (k, v))
+    o4, lse4 = fa().fwd(q, kk, vv, causal=causal, out_dtype=F32)
+    assert float((o3 - o4).abs().max()) < 2e-6
+    got = fa().bwd_rules(q, k[:, ::5].contiguous(), v[:, ::5].contiguous(), o3, lse3, do, causal=causal, out_dtype=F32)
+    want = fa().bwd(q, kk, vv, o4, lse4, do, causal=causal, out_dtype=F32)
+    for a, b in zip(got[1:], want[1:]):
+        b = b.view(B, 2, 5, N, d).sum(2)
+        assert float((a - b).abs().max()) < 2.0 ** -16 * float(b.abs().max())
+
+
+@pytest.mark.gpu
+def test_rows_past_32_bit_offsets():
+    """More than 2^31 elements of q, k and v, in short documents: the last sequence's last heads."""
+    B, Hq, Hkv, N, d = 33, 64, 64, 16384, 64
+    if torch.cuda.mem_get_info()[0] < 70 << 30:
+        pytest.skip("needs 70 GB")
+    g = torch.Generator(device=DEV).manual_seed(16)
+    q, k, v, do = (torch.randn((B, h, N, d), generator=g, device=DEV, dtype=BF16) for h in (Hq, Hkv, Hkv, Hq))
+    ids = (torch.arange(N, device=DEV) // 100).to(torch.int32).expand(B, N).contiguous()
+    o, lse = fa().fwd_rules(q, k, v, causal=True, documents=ids)
+    dq, dk, dv = fa().bwd_rules(q, k, v, o, lse, do, causal=True, documents=ids)
+    assert q.numel() > 1 << 31 and fa().get_device_error() == 0
+    last = [t[-1:, -2:].clone() for t in (q, k, v, do)]
+    o1, lse1 = fa().fwd_rules(*last[:3], causal=True, documents=ids[:1].contiguous())
+    assert torch.equal(o[-1:, -2:], o1) and torch.equal(lse[-1:, -2:], lse1)
+    g1 = fa().bwd_rules(*last[:3], o1, lse1, last[3], causal=True, documents=ids[:1].contiguous())
+    assert torch.equal(dk[-1:, -2:], g1[1]) and torch.equal(dv[-1:, -2:], g1[2])
+    assert float((dq[-1:, -2:].float() - g1[0].float()).abs().max()) < 2.0 ** -6
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_wait_limit_is_reported_and_the_next_call_is_right(d):
+    """With a limit of 1 ns waits run out: the status says so, every role ends, and the next call is right."""
+    B, Hq, Hkv, N = 3, 6, 2, 700
+    rules = Rules(causal=True, softcap=9.0, documents=documents(B, N, [300, 200]))
+    x = inputs(B, Hq, Hkv, N, N, d, seed=17)
+    ref = attention(*x[:3], rules, x[3])
+    o, lse, _ = run(*x, rules)
+    fa().set_wait_timeout_ns(1)
+    try:
+        fa().fwd_rules(*(t.to(DEV) for t in x[:3]), **rules.kwargs(DEV))
+        first = fa().get_device_error()
+        fa().bwd_rules(*(t.to(DEV) for t in x[:3]), o, lse, x[3].to(DEV), **rules.kwargs(DEV))
+        second = fa().get_device_error()
+    finally:
+        fa().set_wait_timeout_ns(0)
+    assert first == second == fa().FA_ERR_TIMEOUT
+    o, lse, grads = run(*x, rules)
+    assert fa().get_device_error() == 0
+    check_forward(o, lse, ref, "after")
+    check_gradients(grads, ref, "after")
+
+
 # ------------------------------------------------------------------------------------ streams, graphs, buffers
+@pytest.mark.gpu
+def test_two_streams_at_once():
+    """Calls on two streams with workspaces of their own."""
+    B, Hq, Hkv, N, d = 4, 8, 4, 900, 64
+    rules = Rules(causal=True, documents=documents(B, N, [350, 20, 400]))
+    xs = [inputs(B, Hq, Hkv, N, N, d, seed=s) for s in (18, 19)]
+    dev = [[t.to(DEV) for t in x] for x in xs]
+    a = rules.kwargs(DEV)
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in xs], [[], []]
+    for _ in range(3):
+        for i, (x, st) in enumerate(zip(dev, streams)):
+            with torch.cuda.stream(st):
+                o, lse = fa().fwd_rules(*x[:3], out_dtype=F32, **a)
+                got[i] = (o, lse, fa().bwd_rules(*x[:3], o, lse, x[3], out_dtype=F32, **a))
+    torch.cuda.synchronize()
+    assert fa().get_device_error() == 0
+    for x, (o, lse, grads) in zip(xs, got):
+        ref = attention(*x[:3], rules, x[3])
+        check_forward(o, lse, ref, "streams")
+        check_gradients(grads, ref, "streams")
+
+
 @pytest.mark.gpu
 def test_outputs_and_workspaces_given():
     B, Hq, Hkv, N, d = 2, 4, 2, 333, 64
