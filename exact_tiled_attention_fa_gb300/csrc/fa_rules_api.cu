@@ -94,8 +94,8 @@ fa_status check_rules(const void* q, const void* k, const void* v, const float* 
     if (!make_rules(&r, scale, softcap, slopes, true)) return FA_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(slopes, 4) || !aligned(documents, 4) || !aligned(prefix_lens, 4))
         return FA_ERR_INVALID_ARG;
-    // positions and tile indices are 32-bit, with room for a tile past the end
-    if (N > 0x7fffff00 || Nk > 0x7fffff00) return FA_ERR_INVALID_ARG;
+    // positions and tile indices are 32-bit, with room for a tile and for a look ahead (fa_rules_ranges.cuh) past the end
+    if (N > 0x7fff0000 || Nk > 0x7fff0000) return FA_ERR_INVALID_ARG;
     const long long tiles = static_cast<long long>(B) * Hq * (tiles_of(N) > tiles_of(Nk) ? tiles_of(N) : tiles_of(Nk));
     if (static_cast<long long>(B) * Hq > 0x3fffffffLL || tiles > 0x3fffffffLL) return FA_ERR_INVALID_ARG;
     return FA_OK;
@@ -270,7 +270,7 @@ fa_status fa_bwd_rules(const void* q, const void* k, const void* v, const void* 
     p.Hkv = Hkv;
     p.causal = causal;
     p.parts = parts;
-    p.part_heads = (R + parts - 1) / parts;  // (the heads that this number of parts was made from)
+    p.part_heads = (R + parts - 1) / parts;  // (at most the heads that this number of parts was made from)
     p.n_items = B * Hkv * parts * Tc;
     p.chunk = causal != 0 || documents != nullptr ? chunk_of(B * Hkv * parts, 8LL * N * d * p.part_heads) : 1;
     const cudaError_t e = by_kind(d, p.rules, [&](auto D, auto kind) { return fa::launch_bwd_rules<D(), kind()>(p, kv_type, st); });

@@ -52,7 +52,7 @@ def test_shared_refusals(lib, make):
                dict(Hq=0), dict(Hkv=0), dict(Hkv=3), dict(N=0), dict(Nk=-1), dict(d=0), dict(dv=0), dict(causal=2), dict(scale=0.0),
                dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(cap=-1.0), dict(cap=float("nan")),
                dict(cap=float("inf")), dict(scale=1e-30, cap=1e30), dict(scale=1e30, cap=1e-30), dict(cap=3.4e38), dict(odt=2),
-               dict(B=1 << 15, Hq=1 << 15, Hkv=1), dict(N=0x7fffff80), dict(Nk=0x7fffff80), dict(B=1 << 12, Hq=1 << 12, N=1 << 14)):
+               dict(B=1 << 15, Hq=1 << 15, Hkv=1), dict(N=0x7fffff80), dict(Nk=0x7fffff80), dict(Nk=0x7fff8000), dict(B=1 << 12, Hq=1 << 12, N=1 << 14)):
         assert call(**kw) == INVALID, kw
     for kw in (dict(d=96, dv=96), dict(d=48, dv=48), dict(dv=128)):
         assert call(**kw) == UNSUPPORTED, kw
