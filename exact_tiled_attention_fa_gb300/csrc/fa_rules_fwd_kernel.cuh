@@ -21,12 +21,12 @@
 //    is the largest, so the row's maximum is taken after them (without them the loads from tensor memory bring it, and
 //    under a cap whose tile lies in the near range the largest raw score gives it).  What was chosen for tanh, and why,
 //    stands in fa_rules_common.cuh.
+//  - A correction warpgroup (kRulesCorr).
 //
 // What bounds it: the softmax's chain between two products, as in fa_fwd_kernel.cuh, lengthened by the FMA units' work on
 // the rules: at the shape above d = 64 153 us, with a bias 200, a cap of 50 216, both 301; d = 128 286, 315, 348, 391.
 // In documents (64 sequences of 1024 tokens, 16 heads of 64) 144 us: 3.7 TB/s of the 541 MB that have to move;
-// by the counters tensor cores 21 % busy, the ALUs (masks by bits, packing) 37 %, issue slots 42 %.  A correction warpgroup (fa_fwd at d = 128) was not taken
-// over: without masks fa_fwd is the faster one there (64 x 1024 tokens 458 us against 568), with causal masks it is not.
+// by the counters tensor cores 21 % busy, the ALUs (masks by bits, packing) 37 %, issue slots 42 %.
 #pragma once
 
 #include "fa_fwd_kernel.cuh"
@@ -45,12 +45,21 @@ struct RulesItem {
 };
 enum : int { kBarItemFull = kBarCount, kBarItemEmpty = kBarItemFull + kRulesItems, kRulesBarCount = kBarItemEmpty + kRulesItems };
 
+// Whether calls without a causal mask take a kernel with a correction warpgroup (16 warps).  us, d = 128, without / with it:
+// 64 sequences of 1024 tokens, 16 heads 571 / 465, biased 639 / 551, both rules 787 / 740; 4 of 4097, 32/8 heads 1080 /
+// 1021; 16 of 1024 in documents of 100 - 300 94.5 / 88.2.  With a cap alone its softmax warps spill: 638 / 612, but in
+// documents 132 / 139.  With a causal mask (4 x 4097, 16 heads) 286 / 288, capped 348 / 365.  d = 64, whose softmax warps are
+// short of registers: 64 x 1024 277 / 279, in documents, causal 144 / 155.
+template <int D, int RULES>
+constexpr bool kRulesCorr = D == 128 && RULES != kCap;
+
 template <int D, int OutBytes>
 struct RulesCfg : FwdCfg<D, OutBytes> {
     using Base = FwdCfg<D, OutBytes>;
     static_assert(kRulesBarCount <= Base::kNumBars, "barrier slots");
     static constexpr int kOffItems = Base::kOffBar + Base::kNumBars * 8 + 16;
-    static constexpr int kUsed = kOffItems + kRulesItems * static_cast<int>(sizeof(RulesItem)) + 1024;  // 1 KB to align
+    static constexpr int kOffInv = kOffItems + kRulesItems * static_cast<int>(sizeof(RulesItem));  // 1 / l of both tiles' rows
+    static constexpr int kUsed = kOffInv + 2 * kBlockM * 4 + 1024;  // 1 KB to align
     static_assert(kUsed <= 227 * 1024, "shared memory per CTA");
     static constexpr int kSmem = kUsed > 120 * 1024 ? kUsed : 120 * 1024;  // one CTA on an SM, as FwdCfg
     static constexpr int kSoftRegs = 216;
@@ -114,8 +123,110 @@ __device__ __forceinline__ void rules_mask(float* s, int lo, int hi)
     }
 }
 
-template <int D, int RULES, typename OutT>
-__global__ void __launch_bounds__(kFwdThreads, 1) fa_rules_fwd_kernel(const __grid_constant__ FwdRulesParams p)
+// Correction warpgroup: the epilogue of both query tiles, so that the softmax warpgroups go on to the next item's
+// scores at once.  The tile that ends first goes first (in documents, d = 64, 168 us in fixed order, 155 so).  Warp w takes rows 32 (w mod 4) .. + 31 of each.  Once an item's last P V has completed (OReady) and
+// the softmax has written the rows' 1 / l (LFull; 0 for a row that saw no key) it writes the rows out; when it has read
+// them it releases O_i and 1 / l (OFree).
+template <int D, typename OutT>
+__device__ __forceinline__ void rules_correction(const FwdRulesParams& p, const uint8_t* smem, uint32_t bar0, uint32_t tmem,
+                                                 volatile int* abort_flag)
+{
+    using C = RulesCfg<D, static_cast<int>(sizeof(OutT))>;
+    using OS = OStage<OutT, D>;
+    auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
+    const FwdParams& f = p.f;
+    const int wq = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+    const int r = 32 * wq + lane;  // row within a query tile == TMEM lane
+    const uint32_t lane_base = static_cast<uint32_t>(32 * wq) << 16;
+    const float* inv_l = reinterpret_cast<const float*>(smem + C::kOffInv);
+    const unsigned long long limit = f.wait_limit_ns;
+    int done[2] = {0, 0};  // items whose O_i has been read, of each query tile
+    int last = 0;          // tile of the lane's last bulk store
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+        const int at = k % kRulesItems;
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarItemFull + at), static_cast<uint32_t>(k / kRulesItems) & 1, limit, abort_flag));
+        if (!ok) break;
+        const RulesItem it = reinterpret_cast<const RulesItem*>(smem + C::kOffItems)[at];
+        if (it.n_kv < 0) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarItemEmpty + at));
+        const int order = it.n[1] < it.n[0] ? 1 : 0;
+#pragma unroll 1
+        for (int ii = 0; ii < 2; ++ii) {
+            const int i = ii ^ order;
+            const int rows = i ? it.rows[1] : it.rows[0], n = i ? it.n[1] : it.n[0], r0 = i ? it.r0[1] : it.r0[0];
+            int& dn = i ? done[1] : done[0];
+            if (rows == 0) continue;  // tile lies past N
+            const bool any = n > 0;
+            float inv = 0.f;
+            if (any) {
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarOReady + i), dn & 1, limit, abort_flag) &&
+                                                 mbar_wait(bar(kBarLFull + i), dn & 1, limit, abort_flag));
+                if (!ok) break;
+                tc_fence_after_sync();
+                inv = inv_l[i * kBlockM + r];
+            }
+            const uint32_t t_o = tmem + lane_base + C::col_o(i);
+            auto read = [&](int c, uint32_t (&o)[32]) {  // columns c .. c + 31
+                if (any) {
+                    tmem_ld32(t_o + static_cast<uint32_t>(c), o);
+                    tmem_ld_wait();
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = inv == 0.f ? 0u : o[e];
+            };
+            auto read_out = [&] {
+                if (!any) return;
+                tc_fence_before_sync();
+                mbar_arrive(bar(kBarOFree + i));
+                ++dn;
+            };
+            if constexpr (C::kStoreO) {
+                const uint32_t stg = smem_u32(smem) + C::kOffStage + static_cast<uint32_t>(i) * C::kStageTileBytes;
+                if (lane == 0) {  // the rows staged here before have been read
+                    if (last == i) bulk_wait_read_all();
+                    else bulk_wait_read<1>();
+                }
+                __syncwarp();
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    read(c, o);
+                    if (c + 32 == D) read_out();
+                    stage_cols<OutT, D>(stg, r, c, o, inv);
+                }
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0 && r0 + 32 * wq < f.N) {  // rows past N lie outside the map and are skipped
+#pragma unroll
+                    for (int cb = 0; cb < OS::kNumCB; ++cb)
+                        tma_store_3d(&f.tm_o, stg + cb * OS::kBlkBytes + wq * 32 * OS::kRowBytes, cb * OS::kElems,
+                                     r0 + 32 * wq, it.bh);
+                    bulk_commit_group();
+                    last = i;
+                }
+            } else {
+                OutT* orow = reinterpret_cast<OutT*>(f.o) + (static_cast<size_t>(it.bh) * f.N + static_cast<size_t>(r0 + r)) * D;
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    float v[32];
+                    read(c, o);
+                    if (c + 32 == D) read_out();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[e]) * inv;
+                    if (r < rows) store_row32<OutT>(orow + c, v);
+                }
+            }
+        }
+    }
+    if (C::kStoreO && lane == 0) bulk_wait_all();  // before the CTA's shared memory goes away
+    if (!ok && !*abort_flag) record_failure(f.status, abort_flag, FA_ERR_TIMEOUT);
+}
+
+template <int D, int RULES, bool CORR, typename OutT>
+__global__ void __launch_bounds__(CORR ? 512 : kFwdThreads, 1) fa_rules_fwd_kernel(const __grid_constant__ FwdRulesParams p)
 {
     using C = RulesCfg<D, static_cast<int>(sizeof(OutT))>;
     constexpr int S = C::kStages;
@@ -147,6 +258,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_rules_fwd_kernel(const __gr
             mbar_init(bar(kBarOReady + i), 1);
             mbar_init(bar(kBarDrain + i), 1);
             mbar_init(bar(kBarSFree + i), kBlockM);
+            mbar_init(bar(kBarLFull + i), kBlockM);
+            mbar_init(bar(kBarOFree + i), kBlockM);
         }
         for (int s = 0; s < S; ++s) {
             mbar_init(bar(kBarKVFull + s), 1);
@@ -154,7 +267,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_rules_fwd_kernel(const __gr
         }
         for (int i = 0; i < kRulesItems; ++i) {
             mbar_init(bar(kBarItemFull + i), 1);
-            mbar_init(bar(kBarItemEmpty + i), 10);  // the issuers and the softmax warps
+            mbar_init(bar(kBarItemEmpty + i), CORR ? 14 : 10);  // the issuers, the softmax and the correction warps
         }
         *abort_flag = 0;
         fence_barrier_init();
@@ -178,8 +291,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_rules_fwd_kernel(const __gr
         return true;
     };
 
-    if (warp >= kWarpProducer) {
-        regs_decrease<C::kCtrlRegs>();
+    if (CORR && warp >= kWarpCorr) {
+        regs_decrease<kCorrRegs>();
+        rules_correction<D, OutT>(p, smem, bar0, tmem, abort_flag);
+    } else if (warp >= kWarpProducer) {
+        regs_decrease<CORR ? kCorrControlRegs : C::kCtrlRegs>();
         if (warp == kWarpProducer) {
             // ======================================================== producer
             if (lane == 0) {
@@ -344,6 +460,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_rules_fwd_kernel(const __gr
                             ok = false;
                             break;
                         }
+                        // the columns of O_i have been read
+                        if (CORR && j == a && q_uses > 0 && !mbar_wait(bar(kBarOFree + i), (q_uses - 1) & 1, limit, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
                         tc_fence_after_sync();
                         issue_pv(sj, j > a);
                         umma_commit(bar(kBarPVDone + i));
@@ -362,7 +483,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_rules_fwd_kernel(const __gr
             }
         }
     } else {
-        regs_increase<C::kSoftRegs>();
+        regs_increase<CORR ? kCorrSoftmaxRegs : C::kSoftRegs>();
         // ============================================================ softmax + epilogue
         const int wg = warp >> 2;         // query tile of this warpgroup
         const int r = threadIdx.x & 127;  // row within the tile == TMEM lane
@@ -476,7 +597,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_rules_fwd_kernel(const __gr
                 // Test whether P_i(j-1) V_{j-1} has completed before the exponentials; the answer is needed after them.
                 bool pv_ready = true;
                 auto test_pv = [&] {
-                    if (!C::kAliasP && j > a) pv_ready = mbar_test(bar(kBarPVDone + wg), (tiles - 1) & 1);
+                    if (!C::kAliasP && (CORR ? tiles > 0 : j > a)) pv_ready = mbar_test(bar(kBarPVDone + wg), (tiles - 1) & 1);
                 };
                 const int range = kWithCap ? cap_range(p.rules, mrow) : 0;
                 bool done = false;
@@ -514,7 +635,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_rules_fwd_kernel(const __gr
                 }
                 // O_i and the P_i columns are free once P_i(j-1) V_{j-1} has completed.  With P aliased into S_i this is
                 // implied by the arrival of S_i(j); otherwise wait for it.
-                if (!C::kAliasP && j > a) {
+                if (!C::kAliasP && (CORR ? tiles > 0 : j > a)) {
                     ok = __all_sync(0xffffffffu, pv_ready || mbar_wait(bar(kBarPVDone + wg), (tiles - 1) & 1, limit, abort_flag));
                     if (!ok) break;
                     tc_fence_after_sync();
@@ -549,13 +670,29 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_rules_fwd_kernel(const __gr
                 ++tiles;
             }
             if (!ok) break;
+            const bool none = l == 0.f;  // a row that sees no key: O = 0, LSE = -inf
+            if constexpr (CORR) {
+                if (n > 0) {  // 1 / l to the correction warpgroup, once it has read the last item's
+                    if (uses > 0) {
+                        ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarOFree + wg), (uses - 1) & 1, limit, abort_flag));
+                        if (!ok) break;
+                    }
+                    reinterpret_cast<float*>(smem + C::kOffInv)[wg * kBlockM + r] = none ? 0.f : 1.f / l;
+                    mbar_arrive(bar(kBarLFull + wg));
+                    ++uses;
+                }
+                const size_t row = static_cast<size_t>(it.bh) * f.N + static_cast<size_t>(it.r0[wg] + r);
+                const bool valid = r < it.rows[wg];
+                release();
+                if (valid && f.lse != nullptr) f.lse[row] = none ? -INFINITY : (m_run + lg2_approx(l)) * kLn2;
+                continue;
+            }
             if (n > 0) {
                 ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarOReady + wg), uses & 1, limit, abort_flag));
                 if (!ok) break;
                 ++uses;
                 tc_fence_after_sync();
             }
-            const bool none = l == 0.f;  // a row that sees no key: O = 0, LSE = -inf
             const bool hide = __any_sync(0xffffffffu, none);
             const float inv = none ? 0.f : 1.f / l;
             const int bh = it.bh, row0 = it.r0[wg];
@@ -610,7 +747,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_rules_fwd_kernel(const __gr
             if (valid && f.lse != nullptr) f.lse[row] = none ? -INFINITY : (m_run + lg2_approx(l)) * kLn2;
         }
         // Bulk stores must finish before the CTA's shared memory goes away.
-        if (C::kStoreO && lane == 0) bulk_wait_all();
+        if (!CORR && C::kStoreO && lane == 0) bulk_wait_all();
         if (!ok && !*abort_flag) record_failure(f.status, abort_flag, FA_ERR_TIMEOUT);
     }
 
@@ -623,11 +760,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_rules_fwd_kernel(const __gr
     }
 }
 
-template <int D, int RULES, typename OutT>
+template <int D, int RULES, bool CORR, typename OutT>
 cudaError_t launch_fwd_rules_t(const FwdRulesParams& p, cudaStream_t st)
 {
     using C = RulesCfg<D, static_cast<int>(sizeof(OutT))>;
-    auto kern = fa_rules_fwd_kernel<D, RULES, OutT>;
+    constexpr int kThreads = CORR ? 512 : kFwdThreads;
+    auto kern = fa_rules_fwd_kernel<D, RULES, CORR, OutT>;
     static bool configured[64] = {};  // attributes set and registers checked, per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -640,17 +778,25 @@ cudaError_t launch_fwd_rules_t(const FwdRulesParams& p, cudaStream_t st)
         e = cudaFuncGetAttributes(&attr, kern);
         if (e != cudaSuccess) return e;
         // a register increase that the launch's pool cannot satisfy would wait forever
-        if (attr.numRegs * kFwdThreads < 256 * C::kSoftRegs + 128 * C::kCtrlRegs) return cudaErrorLaunchOutOfResources;
+        constexpr int kNeed = CORR ? 256 * kCorrSoftmaxRegs + 128 * (kCorrRegs + kCorrControlRegs)
+                                                   : 256 * C::kSoftRegs + 128 * C::kCtrlRegs;
+        if (attr.numRegs * kThreads < kNeed) return cudaErrorLaunchOutOfResources;
         configured[dev] = true;
     }
     const int grid = p.f.n_items < p.f.num_ctas ? p.f.n_items : p.f.num_ctas;
-    return launch_pdl(kern, static_cast<unsigned>(grid), kFwdThreads, C::kSmem, st, p);
+    return launch_pdl(kern, static_cast<unsigned>(grid), kThreads, C::kSmem, st, p);
 }
 
 template <int D, int RULES>
 cudaError_t launch_fwd_rules_d(const FwdRulesParams& p, fa_dtype o_dtype, cudaStream_t st)
 {
-    return o_dtype == FA_F32 ? launch_fwd_rules_t<D, RULES, float>(p, st) : launch_fwd_rules_t<D, RULES, __nv_bfloat16>(p, st);
+    if constexpr (kRulesCorr<D, RULES>) {
+        if (p.causal == 0)
+            return o_dtype == FA_F32 ? launch_fwd_rules_t<D, RULES, true, float>(p, st)
+                                     : launch_fwd_rules_t<D, RULES, true, __nv_bfloat16>(p, st);
+    }
+    return o_dtype == FA_F32 ? launch_fwd_rules_t<D, RULES, false, float>(p, st)
+                             : launch_fwd_rules_t<D, RULES, false, __nv_bfloat16>(p, st);
 }
 
 }  // namespace fa

@@ -319,11 +319,11 @@ def test_rows_past_32_bit_offsets():
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("d", [32, 64, 128])
-def test_wait_limit_is_reported_and_the_next_call_is_right(d):
+@pytest.mark.parametrize("d,causal", [(32, True), (64, True), (128, True), (128, False)])
+def test_wait_limit_is_reported_and_the_next_call_is_right(d, causal):
     """With a limit of 1 ns waits run out: the status says so, every role ends, and the next call is right."""
     B, Hq, Hkv, N = 3, 6, 2, 700
-    rules = Rules(causal=True, softcap=9.0, documents=documents(B, N, [300, 200]))
+    rules = Rules(causal=causal, softcap=9.0 if causal else 0.0, documents=documents(B, N, [300, 200]))
     x = inputs(B, Hq, Hkv, N, N, d, seed=17)
     ref = attention(*x[:3], rules, x[3])
     o, lse, _ = run(*x, rules)
