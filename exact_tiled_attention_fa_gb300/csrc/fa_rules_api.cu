@@ -371,7 +371,7 @@ fa_status fa_decode_prefix(const void* q, const void* k_prefix, const void* v_pr
     const int n_pre = pre ? plan.units_pre : 0;
     const long long units = static_cast<long long>(n_pre) + plan.units_own;
     // Which form (ALT / SOLO, us).  d = 128, where SOLO's K and V come in halves: 2 sequences behind 512 tokens 12.8 / 11.1,
-    // 16 behind 8192 38.6 / 31.8, 64 behind 32K 114 / 103, 64 without a prefix 63.8 / 50.9.  d = 64, 5 heads, 37 sequences
+    // 16 behind 8192 38.6 / 31.8, 64 behind 32K 114 / 103 (SharedWalk: 88), 64 without a prefix 63.8 / 50.9.  d = 64, 5 heads, 37 sequences
     // behind 3000 tokens 19.7 / 21.7, without a prefix 19.0 / 15.5; 8 heads, 64 sequences behind 32K 68 / 53.
     const bool solo = d == 128 || (pre ? units >= 2LL * plan.ctas : 4 * units >= 3LL * plan.ctas);
     const int box = solo && d == 128 ? fa::kBlockN / 2 : fa::kBlockN;  // TrCfg::kHalves

@@ -94,7 +94,7 @@ enum : int {
 struct TreeSeg {
     int n;              // tiles; 0: the share is done
     int tile;           // the first one
-    int prefix, nodes;  // of the sequence
+    int prefix, nodes;  // of the sequence  (SHARED: nodes is the unit's tiles, one that many further the first again)
     int b, group, qp;   // (SHARED: b < 0 a prefix unit, group its key/value head)
     int slot;           // of its part; -1: the unit is whole
 };
@@ -121,6 +121,7 @@ struct TrCfg {
     // a stream took 3.5 us a tile whatever it read (64 sequences of up to 2000 tokens, 32/8 heads: 56 us,
     // so 51, with a cap 68 and 53; behind a prefix of 8K 16 such sequences 36 and 32).
     static constexpr bool kHalves = SHARED && FORM == kSolo && D == 128;
+    static constexpr bool kTurns = SHARED && D == 128;
     static constexpr int kSteps = D == 128 && (FORM == kPair || kHalves) ? 2 : 1;
     static constexpr int kStep = kBlockN / kSteps;  // keys
     // Registers after the split: 256 * softmax + 128 * control = 64512 = 384 * 168, checked by the launcher.
@@ -313,6 +314,8 @@ struct TreeWalk {
         next_nodes = p.n_nodes != nullptr ? p.n_nodes[i] : p.T;
     }
     __device__ __forceinline__ int group(const TreeParams& p) const { return b * p.Hkv + kvh; }
+    // first key of the segment's load i, of `keys` each
+    __device__ __forceinline__ int first_key(int i, int keys) const { return tile * kBlockN + i * keys; }
     // Slot of a part: of the units that a share holds without finishing them alone, one was begun in the
     // share before (it is the share's first) and one is begun here (its last).
     __device__ __forceinline__ int slot(int share) const { return n == tiles ? -1 : 2 * share + (tile == 0 ? 1 : 0); }
@@ -379,13 +382,33 @@ __device__ __forceinline__ TreeStart shared_locate(const PrefixParams& p, int c,
     return s;
 }
 
+// TURNS: a prefix that several query tiles meet (n_qp) and that the L2 does not hold is read once from DRAM if they meet
+// each tile at about the same time.  All shares start together, a share's length apart, so query tile qp, which begins qp
+// units later, walks its keys from the tile on that the first one has come to by then, and round: 64 sequences behind
+// 32K tokens, 32/8 heads of 128, 527 MB, so 415, and 100 us, so 88.  (At d <= 64, where prefixes are half as large, the
+// same batch stays at 49 us, and smaller ones pay 2 % for it.)
+template <bool TURNS>
 struct SharedWalk : TreeWalk {
+    int rot;          // the tile the unit begins with
+    float of_shares;  // shares a place
+    __device__ __forceinline__ void turn(const PrefixParams& p)
+    {
+        if constexpr (!TURNS) return;
+        const float x = static_cast<float>(qp * (tiles + p.unit_cost)) * of_shares;  // shares that the unit begins later
+        rot = min(__float2int_rz(__fdividef(x - floorf(x), of_shares)), tiles - 1);
+    }
+    __device__ __forceinline__ int first_key(int i, int keys) const
+    {
+        const int at = (tile + (TURNS ? rot : 0)) * kBlockN + i * keys, all = tiles * kBlockN;
+        return TURNS && at >= all ? at - all : at;
+    }
     __device__ __forceinline__ void begin(const PrefixParams& p, const TreeStart& s)
     {
         left = static_cast<int>(s.w1 - s.w0);
         b = kvh = qp = tile = tiles = n = 0;
         len = TreeLen{0, 0};
-        next_len = 0;
+        next_len = rot = 0;
+        of_shares = __fdividef(static_cast<float>(s.shares), static_cast<float>(s.total));
         if (left == 0) return;
         b = s.b;
         kvh = b < 0 ? s.unit / p.n_qp : s.unit;
@@ -393,6 +416,7 @@ struct SharedWalk : TreeWalk {
         len = TreeLen{s.prefix, 0};
         tiles = len.tiles();
         ahead(p);
+        if (b < 0) turn(p);
         take(p, s.at);
     }
     __device__ __forceinline__ void next(const PrefixParams& p)
@@ -404,8 +428,11 @@ struct SharedWalk : TreeWalk {
     }
     __device__ __forceinline__ void step(const PrefixParams& p)
     {
-        if (b < 0 && ++qp < p.n_qp) return;
-        qp = 0;
+        if (b < 0 && ++qp < p.n_qp) {
+            turn(p);
+            return;
+        }
+        qp = rot = 0;
         if (++kvh < p.Hkv) return;
         kvh = 0;
         ++b;
@@ -584,7 +611,8 @@ __device__ __forceinline__ void tree_scale(uint32_t (&o)[N], float alpha)
 // (fa_decode_prefix).  The prefix is read once for a query tile of many sequences' rows, instead of once for each; rows
 // of a sequence's own keys are the R query heads of a group.  Both kinds of units are in one launch, so that the
 // streams that have products to wait for share their SM with streams that have bytes to wait for: 64 sequences behind
-// 32K tokens with up to 2000 of their own, 32/8 heads of 128, 103 us; the prefix in PAIR form in a launch of its own 107.
+// 32K tokens with up to 2000 of their own, 32/8 heads of 128, 103 us (88 since the prefix's second reading is the L2's, SharedWalk); the prefix in PAIR form, read
+// once for 256 rows, in a launch of its own 107.
 // Every unit has its parts recorded, and whole ones go to buffers of their own, for the merge to join a row's two sides.
 // RULES: kNoRules, or kCap and kBias.  (Decided at run time they cost calls without them, by the registers that spilled:
 // 64 sequences of up to 2000 tokens of their own alone 82 us, so 63.)
@@ -701,7 +729,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 const TreeStart start = *reinterpret_cast<TreeStart*>(reinterpret_cast<uint8_t*>(start_slot) + 64 * stream);
                 const int share = stream * static_cast<int>(gridDim.x) + blockIdx.x;
                 const int stage0 = stream * S;
-                std::conditional_t<SHARED, SharedWalk, TreeWalk> kw, vw;  // K runs one tile ahead of V
+                std::conditional_t<SHARED, SharedWalk<C::kTurns>, TreeWalk> kw, vw;  // K runs one tile ahead of V
                 kw.begin(p, start);
                 vw.begin(p, start);
                 int kj = 0, vj = 0;  // load within the segment
@@ -719,6 +747,8 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                     x.qp = kw.qp;
                     x.slot = kw.slot(share);
                     if constexpr (SHARED) {
+                        if (C::kTurns) x.tile += kw.rot;
+                        x.nodes = kw.tiles;
                         if (n > 0 && kw.tile == 0) {  // begun here: the merge is told where to find it
                             const long long last = start.w1 + (kw.tiles - kw.n);
                             const int unit = kw.b < 0 ? kw.kvh * p.n_qp + kw.qp : p.n_pre + x.group;
@@ -773,7 +803,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                     if constexpr (SHARED) map = kw.b < 0 ? &p.tm_kp : map;
                     for (int cb = 0; cb < C::kNumCB; ++cb)
                         tma_load_3d(sbase + C::kOffK + s * C::kStageBytes + cb * C::kKVBlkBytes, map, bar(kTbKFull + s),
-                                    cb * C::kCB, kw.tile * kBlockN + kj * (kBlockN / HL), g, kw.b < 0 ? pol_kv : pol_own);
+                                    cb * C::kCB, kw.first_key(kj, kBlockN / HL), g, kw.b < 0 ? pol_kv : pol_own);
                     ++k_issued;
                     if (++kj == kw.n * HL) {
                         kj = 0;
@@ -791,7 +821,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                     if constexpr (SHARED) map = vw.b < 0 ? &p.tm_vp : map;
                     for (int cb = 0; cb < C::kNumCB; ++cb)
                         tma_load_3d(sbase + C::kOffV + s * C::kStageBytes + cb * C::kKVBlkBytes, map, bar(kTbVFull + s),
-                                    cb * C::kCB, vw.tile * kBlockN + vj * (kBlockN / HL), vw.group(p), vw.b < 0 ? pol_kv : pol_own);
+                                    cb * C::kCB, vw.first_key(vj, kBlockN / HL), vw.group(p), vw.b < 0 ? pol_kv : pol_own);
                     ++v_issued;
                     if (++vj == vw.n * HL) {
                         vj = 0;
@@ -1015,7 +1045,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             const int rows_warp = rows - 32 * (warp & 3);  // of this warp (<= 0: none)
             const bool warp_live = rows_warp > 0;
             const int j0 = ALT ? (k + wg) & 1 : 0;  // first tile of the segment for this warpgroup
-            const int end = w.prefix + w.nodes;     // keys of the sequence
+            const int end = w.prefix + (SHARED ? 0 : w.nodes);  // keys of the sequence
             // the row's ancestors, kept while the sequence and the row stay the same
             if (!SHARED && (w.tile + w.n) * kBlockN > w.prefix && (w.b != vis_b || (PAIR && w.qp != vis_qp))) {
                 vis_b = w.b;
@@ -1058,7 +1088,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 fence_proxy_async_shared();
             };
             for (int j = j0; ok && j < w.n; j += step) {
-                const int k0 = (w.tile + j) * kBlockN;
+                const int k0 = (w.tile + j - (C::kTurns && w.tile + j >= w.nodes ? w.nodes : 0)) * kBlockN;
                 if constexpr (H == 1) {
                     ok = __all_sync(0xffffffffu, mbar_wait(bar(kTbSFull + 2 * wg), tiles & 1, limit, abort_flag));
                     if (!ok) break;

@@ -104,6 +104,13 @@ def test_more_rows_than_a_tile(d, B, R):
     check(B, R, 1, 700, 200, d, lens, rules=rules, seed=R, what=f"{d} {B} {R}")
 
 
+@pytest.mark.parametrize("name,P", [("none", 20011), ("both", 20011), ("bias", 9000)])
+def test_long_prefix_for_several_query_tiles(name, P):
+    """Query tiles that come to the same prefix later begin further on in it and go round; its last tile is cut."""
+    lens = torch.arange(34, dtype=torch.int32) * 7 % 60
+    check(34, 16, 2, P + 30, 60, 128, lens, P=P, rules=RULES[name](16), seed=P, what=f"{name} {P}")
+
+
 @pytest.mark.parametrize("P,P_max", [(0, 64), (1, 64), (127, 300), (128, 128), (129, 300), (4000, 4001)])
 @pytest.mark.parametrize("B", [3, 60])
 def test_prefix_lengths(P, P_max, B):
