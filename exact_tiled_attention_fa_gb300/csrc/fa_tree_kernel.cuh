@@ -611,8 +611,8 @@ __device__ __forceinline__ void tree_scale(uint32_t (&o)[N], float alpha)
 // (fa_decode_prefix).  The prefix is read once for a query tile of many sequences' rows, instead of once for each; rows
 // of a sequence's own keys are the R query heads of a group.  Both kinds of units are in one launch, so that the
 // streams that have products to wait for share their SM with streams that have bytes to wait for: 64 sequences behind
-// 32K tokens with up to 2000 of their own, 32/8 heads of 128, 103 us (88 since the prefix's second reading is the L2's, SharedWalk); the prefix in PAIR form, read
-// once for 256 rows, in a launch of its own 107.
+// 32K tokens with up to 2000 of their own, 32/8 heads of 128, 103 us (88 since the prefix's second reading is the L2's,
+// SharedWalk); the prefix in PAIR form, read once for 256 rows, in a launch of its own 107.
 // Every unit has its parts recorded, and whole ones go to buffers of their own, for the merge to join a row's two sides.
 // RULES: kNoRules, or kCap and kBias.  (Decided at run time they cost calls without them, by the registers that spilled:
 // 64 sequences of up to 2000 tokens of their own alone 82 us, so 63.)
@@ -970,8 +970,12 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                                     tc_fence_after_sync();
                                     issue_pv(sv, h, j > j0 || h > 0);
                                     umma_commit(bar(kTbPVDone + 2 * i + h));
-                                    if (h == 1 && j == j_last) umma_commit(bar(kTbOReady + i));
-                                    if (h == 1 || HL == 2) umma_commit(bar(kTbVEmpty + sv));
+                                    if (h == 1) {
+                                        if (j == j_last) umma_commit(bar(kTbOReady + i));
+                                        umma_commit(bar(kTbVEmpty + sv));
+                                    } else if (HL == 2) {
+                                        umma_commit(bar(kTbVEmpty + sv));
+                                    }
                                     // The next tile's scores in the columns that this product frees; its first step's
                                     // now only if its keys are there already: the second step's product must not wait
                                     // for them (V's stage, and with it the next V, would wait too).
