@@ -48,8 +48,9 @@ enum : int { kBarItemFull = kBarCount, kBarItemEmpty = kBarItemFull + kRulesItem
 // Whether calls without a causal mask take a kernel with a correction warpgroup (16 warps).  us, d = 128, without / with it:
 // 64 sequences of 1024 tokens, 16 heads 571 / 465, biased 639 / 551, both rules 787 / 740; 4 of 4097, 32/8 heads 1080 /
 // 1021; 16 of 1024 in documents of 100 - 300 94.5 / 88.2.  With a cap alone its softmax warps spill: 638 / 612, but in
-// documents 132 / 139.  With a causal mask (4 x 4097, 16 heads) 286 / 288, capped 348 / 365.  d = 64, whose softmax warps are
-// short of registers: 64 x 1024 277 / 279, in documents, causal 144 / 155.
+// documents 132 / 139.  With a causal mask (4 x 4097, 16 heads) 286 / 288, capped 348 / 365.  At d = 64, where the softmax
+// warps need the registers, 64 x 1024 took 279 against 278, in documents, causal 155 (with O read whole and released
+// at once 164) against 144.
 template <int D, int RULES>
 constexpr bool kRulesCorr = D == 128 && RULES != kCap;
 
@@ -124,15 +125,15 @@ __device__ __forceinline__ void rules_mask(float* s, int lo, int hi)
 }
 
 // Correction warpgroup: the epilogue of both query tiles, so that the softmax warpgroups go on to the next item's
-// scores at once.  The tile that ends first goes first (in documents, d = 64, 168 us in fixed order, 155 so).  Warp w takes rows 32 (w mod 4) .. + 31 of each.  Once an item's last P V has completed (OReady) and
-// the softmax has written the rows' 1 / l (LFull; 0 for a row that saw no key) it writes the rows out; when it has read
-// them it releases O_i and 1 / l (OFree).
+// scores at once.  The tile that ends first goes first (16384 tokens in documents of 1800 and 2500, 32/8 heads 624 us in
+// fixed order, 606 - 618 so).  Warp w takes rows 32 (w mod 4) .. + 31 of each.  Once an item's last P V has completed (OReady)
+// and the softmax has written the rows' 1 / l (LFull; 0 for a row that saw no key) it writes the rows out; when it has
+// read them it releases O_i and 1 / l (OFree).
 template <int D, typename OutT>
 __device__ __forceinline__ void rules_correction(const FwdRulesParams& p, const uint8_t* smem, uint32_t bar0, uint32_t tmem,
                                                  volatile int* abort_flag)
 {
     using C = RulesCfg<D, static_cast<int>(sizeof(OutT))>;
-    using OS = OStage<OutT, D>;
     auto bar = [&](int i) -> uint32_t { return bar0 + 8u * static_cast<uint32_t>(i); };
     const FwdParams& f = p.f;
     const int wq = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
@@ -141,7 +142,6 @@ __device__ __forceinline__ void rules_correction(const FwdRulesParams& p, const 
     const float* inv_l = reinterpret_cast<const float*>(smem + C::kOffInv);
     const unsigned long long limit = f.wait_limit_ns;
     int done[2] = {0, 0};  // items whose O_i has been read, of each query tile
-    int last = 0;          // tile of the lane's last bulk store
     bool ok = true;
     for (int k = 0; ok; ++k) {
         const int at = k % kRulesItems;
@@ -168,60 +168,26 @@ __device__ __forceinline__ void rules_correction(const FwdRulesParams& p, const 
                 inv = inv_l[i * kBlockM + r];
             }
             const uint32_t t_o = tmem + lane_base + C::col_o(i);
-            auto read = [&](int c, uint32_t (&o)[32]) {  // columns c .. c + 31
+            OutT* orow = reinterpret_cast<OutT*>(f.o) + (static_cast<size_t>(it.bh) * f.N + static_cast<size_t>(r0 + r)) * D;
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
                 if (any) {
                     tmem_ld32(t_o + static_cast<uint32_t>(c), o);
                     tmem_ld_wait();
                 }
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = inv == 0.f ? 0u : o[e];
-            };
-            auto read_out = [&] {
-                if (!any) return;
-                tc_fence_before_sync();
-                mbar_arrive(bar(kBarOFree + i));
-                ++dn;
-            };
-            if constexpr (C::kStoreO) {
-                const uint32_t stg = smem_u32(smem) + C::kOffStage + static_cast<uint32_t>(i) * C::kStageTileBytes;
-                if (lane == 0) {  // the rows staged here before have been read
-                    if (last == i) bulk_wait_read_all();
-                    else bulk_wait_read<1>();
+                if (any && c + 32 == D) {
+                    tc_fence_before_sync();
+                    mbar_arrive(bar(kBarOFree + i));
+                    ++dn;
                 }
-                __syncwarp();
+                float v[32];
 #pragma unroll
-                for (int c = 0; c < D; c += 32) {
-                    uint32_t o[32];
-                    read(c, o);
-                    if (c + 32 == D) read_out();
-                    stage_cols<OutT, D>(stg, r, c, o, inv);
-                }
-                fence_proxy_async_shared();
-                __syncwarp();
-                if (lane == 0 && r0 + 32 * wq < f.N) {  // rows past N lie outside the map and are skipped
-#pragma unroll
-                    for (int cb = 0; cb < OS::kNumCB; ++cb)
-                        tma_store_3d(&f.tm_o, stg + cb * OS::kBlkBytes + wq * 32 * OS::kRowBytes, cb * OS::kElems,
-                                     r0 + 32 * wq, it.bh);
-                    bulk_commit_group();
-                    last = i;
-                }
-            } else {
-                OutT* orow = reinterpret_cast<OutT*>(f.o) + (static_cast<size_t>(it.bh) * f.N + static_cast<size_t>(r0 + r)) * D;
-#pragma unroll
-                for (int c = 0; c < D; c += 32) {
-                    uint32_t o[32];
-                    float v[32];
-                    read(c, o);
-                    if (c + 32 == D) read_out();
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[e]) * inv;
-                    if (r < rows) store_row32<OutT>(orow + c, v);
-                }
+                for (int e = 0; e < 32; ++e) v[e] = inv == 0.f ? 0.f : __uint_as_float(o[e]) * inv;
+                if (r < rows) store_row32<OutT>(orow + c, v);
             }
         }
     }
-    if (C::kStoreO && lane == 0) bulk_wait_all();  // before the CTA's shared memory goes away
     if (!ok && !*abort_flag) record_failure(f.status, abort_flag, FA_ERR_TIMEOUT);
 }
 
@@ -231,6 +197,7 @@ __global__ void __launch_bounds__(CORR ? 512 : kFwdThreads, 1) fa_rules_fwd_kern
     using C = RulesCfg<D, static_cast<int>(sizeof(OutT))>;
     constexpr int S = C::kStages;
     constexpr bool kWithCap = (RULES & kCap) != 0, kWithBias = (RULES & kBias) != 0;
+    static_assert(!CORR || C::kAliasP, "an item's first P goes where the last item's P V may still read");
     extern __shared__ uint8_t rules_smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(rules_smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
@@ -258,8 +225,10 @@ __global__ void __launch_bounds__(CORR ? 512 : kFwdThreads, 1) fa_rules_fwd_kern
             mbar_init(bar(kBarOReady + i), 1);
             mbar_init(bar(kBarDrain + i), 1);
             mbar_init(bar(kBarSFree + i), kBlockM);
-            mbar_init(bar(kBarLFull + i), kBlockM);
-            mbar_init(bar(kBarOFree + i), kBlockM);
+            if constexpr (CORR) {
+                mbar_init(bar(kBarLFull + i), kBlockM);
+                mbar_init(bar(kBarOFree + i), kBlockM);
+            }
         }
         for (int s = 0; s < S; ++s) {
             mbar_init(bar(kBarKVFull + s), 1);
@@ -291,10 +260,13 @@ __global__ void __launch_bounds__(CORR ? 512 : kFwdThreads, 1) fa_rules_fwd_kern
         return true;
     };
 
-    if (CORR && warp >= kWarpCorr) {
-        regs_decrease<kCorrRegs>();
-        rules_correction<D, OutT>(p, smem, bar0, tmem, abort_flag);
-    } else if (warp >= kWarpProducer) {
+    if constexpr (CORR) {
+        if (warp >= kWarpCorr) {
+            regs_decrease<kCorrRegs>();
+            rules_correction<D, OutT>(p, smem, bar0, tmem, abort_flag);
+        }
+    }
+    if (warp >= kWarpProducer && !(CORR && warp >= kWarpCorr)) {
         regs_decrease<CORR ? kCorrControlRegs : C::kCtrlRegs>();
         if (warp == kWarpProducer) {
             // ======================================================== producer
@@ -461,9 +433,9 @@ __global__ void __launch_bounds__(CORR ? 512 : kFwdThreads, 1) fa_rules_fwd_kern
                             break;
                         }
                         // the columns of O_i have been read
-                        if (CORR && j == a && q_uses > 0 && !mbar_wait(bar(kBarOFree + i), (q_uses - 1) & 1, limit, abort_flag)) {
-                            ok = false;
-                            break;
+                        if constexpr (CORR) {
+                            ok = j != a || q_uses == 0 || mbar_wait(bar(kBarOFree + i), (q_uses - 1) & 1, limit, abort_flag);
+                            if (!ok) break;
                         }
                         tc_fence_after_sync();
                         issue_pv(sj, j > a);
@@ -482,7 +454,7 @@ __global__ void __launch_bounds__(CORR ? 512 : kFwdThreads, 1) fa_rules_fwd_kern
                 mbar_wait(bar(kBarDrain + i), 0, kDrainLimitNs, nullptr);
             }
         }
-    } else {
+    } else if (!CORR || warp < kWarpProducer) {
         regs_increase<CORR ? kCorrSoftmaxRegs : C::kSoftRegs>();
         // ============================================================ softmax + epilogue
         const int wg = warp >> 2;         // query tile of this warpgroup
@@ -597,7 +569,7 @@ __global__ void __launch_bounds__(CORR ? 512 : kFwdThreads, 1) fa_rules_fwd_kern
                 // Test whether P_i(j-1) V_{j-1} has completed before the exponentials; the answer is needed after them.
                 bool pv_ready = true;
                 auto test_pv = [&] {
-                    if (!C::kAliasP && (CORR ? tiles > 0 : j > a)) pv_ready = mbar_test(bar(kBarPVDone + wg), (tiles - 1) & 1);
+                    if (!C::kAliasP && j > a) pv_ready = mbar_test(bar(kBarPVDone + wg), (tiles - 1) & 1);
                 };
                 const int range = kWithCap ? cap_range(p.rules, mrow) : 0;
                 bool done = false;
@@ -635,7 +607,7 @@ __global__ void __launch_bounds__(CORR ? 512 : kFwdThreads, 1) fa_rules_fwd_kern
                 }
                 // O_i and the P_i columns are free once P_i(j-1) V_{j-1} has completed.  With P aliased into S_i this is
                 // implied by the arrival of S_i(j); otherwise wait for it.
-                if (!C::kAliasP && (CORR ? tiles > 0 : j > a)) {
+                if (!C::kAliasP && j > a) {
                     ok = __all_sync(0xffffffffu, pv_ready || mbar_wait(bar(kBarPVDone + wg), (tiles - 1) & 1, limit, abort_flag));
                     if (!ok) break;
                     tc_fence_after_sync();
@@ -670,8 +642,8 @@ __global__ void __launch_bounds__(CORR ? 512 : kFwdThreads, 1) fa_rules_fwd_kern
                 ++tiles;
             }
             if (!ok) break;
-            const bool none = l == 0.f;  // a row that sees no key: O = 0, LSE = -inf
             if constexpr (CORR) {
+                const bool none = l == 0.f;
                 if (n > 0) {  // 1 / l to the correction warpgroup, once it has read the last item's
                     if (uses > 0) {
                         ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarOFree + wg), (uses - 1) & 1, limit, abort_flag));
@@ -693,6 +665,7 @@ __global__ void __launch_bounds__(CORR ? 512 : kFwdThreads, 1) fa_rules_fwd_kern
                 ++uses;
                 tc_fence_after_sync();
             }
+            const bool none = l == 0.f;  // a row that sees no key: O = 0, LSE = -inf
             const bool hide = __any_sync(0xffffffffu, none);
             const float inv = none ? 0.f : 1.f / l;
             const int bh = it.bh, row0 = it.r0[wg];
@@ -747,7 +720,7 @@ __global__ void __launch_bounds__(CORR ? 512 : kFwdThreads, 1) fa_rules_fwd_kern
             if (valid && f.lse != nullptr) f.lse[row] = none ? -INFINITY : (m_run + lg2_approx(l)) * kLn2;
         }
         // Bulk stores must finish before the CTA's shared memory goes away.
-        if (!CORR && C::kStoreO && lane == 0) bulk_wait_all();
+        if (C::kStoreO && lane == 0) bulk_wait_all();
         if (!ok && !*abort_flag) record_failure(f.status, abort_flag, FA_ERR_TIMEOUT);
     }
 
