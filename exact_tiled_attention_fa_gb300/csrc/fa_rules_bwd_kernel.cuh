@@ -21,8 +21,12 @@
 //    records in shared memory.
 //  - P's recomputation has the cap and the bias, and dS the cap's slope, made beside P from the same tanh.
 //
-// What bounds it: as in fa_bwd_kernel.cuh the chain S -> P -> dV and dP -> dS -> dK, dQ between the roles, lengthened by
-// the rules' instructions.
+// What bounds it, by the times of a CTA's steps (cycles, no rules).  d = 64: 2700 a step, of which the compute warps are
+// busy 2350 (P 1200, about 500 more where pairs are hidden, dS 1150), and some 4500 more an item from its last dS to its
+// successor's first P (last products, dK and dV on their way out).  d = 128: 5180 a step, 2900 of them products; P and dS
+// take 1800, but dQ lies in dP's columns: dP 870, dS 880, dK 650, dQ 710, its reductions 1390 (64 KB at 64 bytes a cycle
+// to the L2), the next dP 580 later.  4 sequences of 4097 tokens, 16 heads, causal, none / bias / cap of 50 / both: d = 64
+// 412 / 456 / 493 / 609 us, d = 128 789 / 821 / 837 / 960.
 #pragma once
 
 #include "fa_bwd_kernel.cuh"
@@ -596,10 +600,23 @@ __global__ void __launch_bounds__(kBwdThreads, 1) fa_rules_bwd_kernel(const __gr
                     tc_fence_before_sync();
                     mbar_arrive(bar(kBbSFree));
                 }
+                // Hidden pairs: P = 0.  Without a cap by their scores, one selection each, with one, which makes a number of
+                // any score, by P in both its forms: 16 sequences of 1024 tokens in documents, 16 heads of 64, forward and
+                // backward, 182 us by P, 169 by the scores.  (Masked inside rules_weights under a cap too: registers spill,
+                // d = 128 840 -> 885 us.)
+                const int q0 = i0 + 64 * h;  // this thread's first query
+                const bool hides = !__all_sync(0xffffffffu, qa <= q0 && qe >= q0 + 64);
+                if (!kWithCap && hides) {
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        const uint32_t see = low_bits(qe - q0 - 32 * w) & ~low_bits(qa - q0 - 32 * w);
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) u[32 * w + c] = (see >> c) & 1u ? u[32 * w + c] : 0xff800000u;  // -inf
+                    }
+                }
                 // P = exp2(s - L log2(e)), s the score in base 2; L = +inf gives 0 (row past N or with no key).  pf
                 // is P times the cap's slope, pk P in bf16 (rounded for the product with dO, half a step of 2^-8).
                 const uint32_t l_addr = sbase + C::kOffL + s * 512 + h * 256;
-                const int q0 = i0 + 64 * h;  // this thread's first query
                 float pf[64];
                 uint32_t pk[32];
                 int sign = 0;
@@ -611,7 +628,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) fa_rules_bwd_kernel(const __gr
                 if (kWithCap && range == 3) rules_weights<3, kWithBias>(u, pf, pk, l_addr, rp.rules, slope2, dist, sign);
                 else if (kWithCap && range == 2) rules_weights<2, kWithBias>(u, pf, pk, l_addr, rp.rules, slope2, dist, sign);
                 else rules_weights<kWithCap ? 0 : -1, kWithBias>(u, pf, pk, l_addr, rp.rules, slope2, dist, sign);
-                if (!__all_sync(0xffffffffu, qa <= q0 && qe >= q0 + 64)) {  // hidden pairs: P = 0
+                if (kWithCap && hides) {
 #pragma unroll
                     for (int w = 0; w < 2; ++w) {
                         const uint32_t see = low_bits(qe - q0 - 32 * w) & ~low_bits(qa - q0 - 32 * w);
