@@ -277,6 +277,7 @@ struct ScoreRules {
     float bias_in;        // log2(e) / mult: slopes[h] * bias_in * distance is taken off what mult multiplies
     // tanh(cap_in * S), times mult in forward kernels without a bias, as S P(S^2) (fa_rules_common.cuh, cap_factor)
     float2 near[3], mid[4], wide[6];  // (each twice, as the two-wide operations take them)
+    bool far;  // the cap is above kFarCap
     float near_in, mid_in, wide_in;  // cap_in over the polynomials' ranges: |S| times it is at most 1 where they hold; +inf: nowhere
 };
 

@@ -47,6 +47,7 @@ bool make_rules(fa::ScoreRules* r, float scale, float softcap, const float* slop
     r->bias_in = fa::kLog2e / r->mult;
     auto normal = [](float x) { return std::isfinite(x) && x >= std::numeric_limits<float>::min(); };
     if (!normal(r->mult) || (softcap > 0.f && !normal(r->cap_in)) || (slopes != nullptr && !normal(r->bias_in))) return false;
+    r->far = softcap > fa::kFarCap;
     r->near_in = r->mid_in = r->wide_in = INFINITY;
     const double near[] = {FA_TANH_NEAR}, mid[] = {FA_TANH_MID}, wide[] = {FA_TANH_WIDE}, k = r->cap_in;
     if (softcap == 0.f || k > 1e2) return true;  // (above, powers of cap_in up to the eleventh leave fp32)

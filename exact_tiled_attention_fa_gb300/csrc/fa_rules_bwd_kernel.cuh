@@ -109,7 +109,7 @@ __device__ __forceinline__ void rules_weights(const uint32_t (&u)[64], float (&p
         float t[32];
 #pragma unroll
         for (int c = 0; c < 32; ++c) t[c] = __uint_as_float(u[c0 + c]);
-        if constexpr (CAP == 0) tanh_any<32>(t, r.cap_in);
+        if constexpr (CAP == 0) tanh_any<32>(t, r.cap_in, r.far);
 #pragma unroll
         for (int c = 0; c < 32; c += 8) {
 #pragma unroll

@@ -33,10 +33,14 @@ __device__ __forceinline__ float rcp_approx(float x)
 // tokens, 16 heads of 128, a cap of 50 that leaves most tiles in the near range: a polynomial of degree 5 for every
 // argument, scaled before it, 487 us, the three 348, without a cap 286.)
 // Other arguments take 1 - 2 / (1 + e^2u): two operations of the special function unit that the exponentials also need
-// (586 us for all tiles); its absolute error of 2e-7 is one of 1e-5 of a weight at a cap of 50.  +-infinity gives +-1, NaN
-// NaN.  (The device's own tanh instruction is off by 2^-11 of its result: at a score of 20 by 0.01, and the weight by as
-// much.)
+// (586 us for all tiles); its absolute error of 2e-7 is one of 1e-5 of a weight at a cap of 50.  A warp takes one form for all
+// of a tile's scores, and a score beyond the cap is no reason for one far below it to be off by 2e-7 caps, 0.01 of a
+// score of 5 at a cap of 1e5: above kFarCap, where that error is a hundredth of a weight's rounding to bf16, scores up to
+// kNearRange take their polynomial beside it too.  (For every cap that costs 1.0 - 1.4 times the time of the tiles it is for.)
+// +-infinity gives +-1, NaN NaN.  (The device's own tanh instruction is off by 2^-11 of its result: at a score of 20
+// by 0.01, and the weight by as much.)
 constexpr float kNearRange = 0.3f, kMidRange = 0.55f, kWideRange = 1.f;
+constexpr float kFarCap = 128.f;
 #define FA_TANH_NEAR 0.999998838848, -0.333100215997, 0.126339459894
 #define FA_TANH_MID 0.999998880298, -0.333213872584, 0.131312313762, -0.0426959989808
 #define FA_TANH_WIDE 0.999999413602, -0.333290423701, 0.132814338124, -0.051605672318, 0.0167431133877, -0.00306705973621
@@ -54,17 +58,38 @@ __device__ __forceinline__ float2 cap_factor(float2 s, const float2 (&c)[N])
     return q;
 }
 
-// tanh of N numbers k * s, in place.
-template <int N>
-__device__ __forceinline__ void tanh_any(float* s, float k)
+// tanh of k * s, of any size.
+__device__ __forceinline__ float tanh_each(float s, float k)
 {
-    const float k2 = k * (2.f * kLog2e);
+    constexpr float c[] = {FA_TANH_NEAR};
+    const float y = fmaf(-2.f, rcp_approx(1.f + ex2(s * (k * (2.f * kLog2e)))), 1.f);
+    const float u = s * k, w = u * u;
+    return fabsf(u) <= kNearRange ? u * fmaf(w, fmaf(w, c[2], c[1]), c[0]) : y;  // (NaN: y, which is NaN)
+}
+
+// tanh of N numbers k * s, in place, beyond the polynomials' ranges or, with `far`, of any size.
+template <int N>
+__device__ __forceinline__ void tanh_any(float* s, float k, bool far)
+{
+    if (!far) {
+        const float2 k2 = two(k * (2.f * kLog2e));
 #pragma unroll
-    for (int c = 0; c < N; ++c) s[c] = fmaf(-2.f, rcp_approx(1.f + ex2(s[c] * k2)), 1.f);
+        for (int i = 0; i < N; i += 2) {
+            const float2 z = __fmul2_rn(make_float2(s[i], s[i + 1]), k2);
+            const float2 e = __fadd2_rn(make_float2(ex2(z.x), ex2(z.y)), two(1.f));
+            const float2 y = __ffma2_rn(two(-2.f), make_float2(rcp_approx(e.x), rcp_approx(e.y)), two(1.f));
+            s[i] = y.x;
+            s[i + 1] = y.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) s[i] = tanh_each(s[i], k);
+    }
 }
 
 // Whether every lane's |S| (its largest, mx) lies in the polynomials' ranges: 3 the near one, 2 the middle one, 1 the wide
-// one, 0 none.
+// one, 0 none.  kSettled stands for scores that are tanh already (tree_settle).
+constexpr int kSettled = -1;
 __device__ __forceinline__ int cap_range(const ScoreRules& r, float mx, bool counts = true)
 {
     if (__all_sync(0xffffffffu, !counts || mx * r.near_in <= 1.f)) return 3;
@@ -74,7 +99,7 @@ __device__ __forceinline__ int cap_range(const ScoreRules& r, float mx, bool cou
 
 // Scores s of N keys under a cap, in base 2, in place.
 template <int N>
-__device__ __forceinline__ void capped_scores(float* s, const ScoreRules& r, int range)
+__device__ __forceinline__ void capped_scores(float* s, const ScoreRules& r, int range, bool far)
 {
     auto poly = [&](const auto& c) {
 #pragma unroll
@@ -88,7 +113,7 @@ __device__ __forceinline__ void capped_scores(float* s, const ScoreRules& r, int
     if (range >= 2) poly(r.mid);
     else if (range == 1) poly(r.wide);
     else {
-        tanh_any<N>(s, r.cap_in);
+        if (range != kSettled) tanh_any<N>(s, r.cap_in, far);
 #pragma unroll
         for (int i = 0; i < N; ++i) s[i] *= r.mult;
     }
@@ -129,12 +154,12 @@ __device__ __forceinline__ void add_bias(float* s, float slope, float dist, int 
 
 // Scores s of N keys under a bias, and a cap if CAP, in place, over mult (as S and tanh are).
 template <int N, bool CAP>
-__device__ __forceinline__ void biased_scores(float* s, const ScoreRules& r, int range, float slope, float dist, int sign)
+__device__ __forceinline__ void biased_scores(float* s, const ScoreRules& r, int range, bool far, float slope, float dist, int sign)
 {
     if (CAP && range >= 2) {
         add_bias<N>(s, slope, dist, sign, [&](float2 x) { return __fmul2_rn(x, cap_factor(x, r.mid)); });
     } else {
-        if (CAP) tanh_any<N>(s, r.cap_in);
+        if (CAP && range != kSettled) tanh_any<N>(s, r.cap_in, far);
         add_bias<N>(s, slope, dist, sign, [&](float2 x) { return x; });
     }
 }

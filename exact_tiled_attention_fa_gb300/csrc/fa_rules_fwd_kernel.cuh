@@ -589,9 +589,9 @@ __global__ void __launch_bounds__(CORR ? 512 : kFwdThreads, 1) fa_rules_fwd_kern
                 }
                 if (!done) {
                     if constexpr (kWithBias) {
-                        biased_scores<kBlockN, kWithCap>(s, p.rules, range, slope, static_cast<float>(qpos - k0), before ? 1 : behind ? -1 : 0);
+                        biased_scores<kBlockN, kWithCap>(s, p.rules, range, p.rules.far, slope, static_cast<float>(qpos - k0), before ? 1 : behind ? -1 : 0);
                     } else if constexpr (kWithCap) {
-                        capped_scores<kBlockN>(s, p.rules, range);
+                        capped_scores<kBlockN>(s, p.rules, range, p.rules.far);
                     }
                     if (mask) rules_mask(s, lo - k0, hi - k0);
                     if (RULES != kNoRules || mask) mrow = max_of<kBlockN>(s);

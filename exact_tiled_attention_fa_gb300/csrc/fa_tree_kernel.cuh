@@ -607,6 +607,22 @@ __device__ __forceinline__ void tree_scale(uint32_t (&o)[N], float alpha)
     }
 }
 
+// The first n (a multiple of 8) scores in tensor memory, which are the warp's own until it says that it has them, become
+// their tanh, each by its own size.
+__device__ __forceinline__ void tree_settle(const ScoreRules& rules, uint32_t t_s, int n)
+{
+#pragma unroll 1
+    for (int c = 0; c < n; c += 8) {
+        uint32_t x[8];
+        tmem_ld8(t_s + static_cast<uint32_t>(c), x);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = __float_as_uint(tanh_each(__uint_as_float(x[e]), rules.cap_in));
+        tmem_st8(t_s + static_cast<uint32_t>(c), x);
+    }
+    tmem_st_wait();
+}
+
 // SHARED: decode of one query a sequence behind a prefix that all sequences have in common, under score rules
 // (fa_decode_prefix).  The prefix is read once for a query tile of many sequences' rows, instead of once for each; rows
 // of a sequence's own keys are the R query heads of a group.  Both kinds of units are in one launch, so that the
@@ -1058,19 +1074,39 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                 tree_ancestors(p.parents != nullptr ? p.parents + static_cast<size_t>(w.b) * p.T : nullptr, p.T,
                                r < rows && node < w.nodes ? node : -1, lane, p.status, vis);
             }
-            // What the rules make of the scores x of keys from k0 on, over sl2, and their largest (mx: the largest absolute
-            // one, as loaded; rows that are not there take no part in what the warp decides).
-            auto apply = [&](auto& x, float mx, int k0) -> float {
+            // What the rules make of the scores x of keys from k0 on, over sl2, and their largest.
+            auto apply = [&](auto& x, int range, int k0) -> float {
                 constexpr int N = sizeof(x) / sizeof(float);
                 if constexpr (SHARED) {
-                    const int range = kWithCap ? cap_range(p.rules, mx, r < rows) : 0;
                     if constexpr (kWithBias) {
-                        biased_scores<N, kWithCap>(x, p.rules, range, slope, static_cast<float>(qpos - k0), 1);
+                        biased_scores<N, kWithCap>(x, p.rules, range, false, slope, static_cast<float>(qpos - k0), 1);
                     } else {
-                        capped_scores<N>(x, p.rules, range);
+                        capped_scores<N>(x, p.rules, range, false);
                     }
                 }
                 return max_of<N>(x);
+            };
+            // Loads n scores of keys from `first` on by load(), which returns the largest absolute one, and returns the range of
+            // their cap (rows that are not there take no part in it).
+            // Above kFarCap the exponential form is taken score by score, in tensor memory, where it is a loop: unrolled beside
+            // the others it costs instruction fetches (64 sequences behind 32K tokens 97 -> 106 us).
+            auto load_scores = [&](uint32_t t, int first, int n, auto load) -> int {
+                if constexpr (kWithCap) {
+                    bool settled = false;
+#pragma unroll 1
+                    while (true) {
+                        const float mx = load();
+                        if (settled) return kSettled;
+                        const int range = cap_range(p.rules, mx, r < rows);
+                        if (range >= 2) return range;
+                        if (range == 1 && !kWithBias) return range;
+                        if (!p.rules.far) return 0;
+                        tree_settle(p.rules, t, n);
+                        settled = true;
+                    }
+                }
+                load();
+                return 0;
             };
             TreeRow row;
             // V rows past the tree may hold anything: zero them before the product reads them.  (The stage's
@@ -1100,32 +1136,35 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                     if (warp_live) {
                         uint32_t u[kBlockN];
                         float mrow;
-                        if constexpr (D == 128) {
-                            float mh[2];
-                            if constexpr (kWithCap) {
-                                tmem_ld64_absmax(t_s + 0, *reinterpret_cast<uint32_t(*)[64]>(&u[0]), mh[0]);
-                                tmem_ld64_absmax(t_s + 64, *reinterpret_cast<uint32_t(*)[64]>(&u[64]), mh[1]);
+                        const int range = load_scores(t_s, k0, kBlockN, [&]() -> float {
+                            if constexpr (D == 128) {
+                                float mh[2];
+                                if constexpr (kWithCap) {
+                                    tmem_ld64_absmax(t_s + 0, *reinterpret_cast<uint32_t(*)[64]>(&u[0]), mh[0]);
+                                    tmem_ld64_absmax(t_s + 64, *reinterpret_cast<uint32_t(*)[64]>(&u[64]), mh[1]);
+                                } else {
+                                    tmem_ld64_max(t_s + 0, *reinterpret_cast<uint32_t(*)[64]>(&u[0]), mh[0]);
+                                    tmem_ld64_max(t_s + 64, *reinterpret_cast<uint32_t(*)[64]>(&u[64]), mh[1]);
+                                }
+                                tmem_ld_wait();
+                                mrow = fmaxf(mh[0], mh[1]);
                             } else {
-                                tmem_ld64_max(t_s + 0, *reinterpret_cast<uint32_t(*)[64]>(&u[0]), mh[0]);
-                                tmem_ld64_max(t_s + 64, *reinterpret_cast<uint32_t(*)[64]>(&u[64]), mh[1]);
-                            }
-                            tmem_ld_wait();
-                            mrow = fmaxf(mh[0], mh[1]);
-                        } else {
-                            float mq[4];
-                            if constexpr (kWithCap) {
+                                float mq[4];
+                                if constexpr (kWithCap) {
 #pragma unroll
-                                for (int q = 0; q < 4; ++q)
-                                    tmem_ld32_absmax(t_s + 32u * q, *reinterpret_cast<uint32_t(*)[32]>(&u[32 * q]), mq[q]);
-                            } else {
-                                tmem_ld32_max(t_s + 0, *reinterpret_cast<uint32_t(*)[32]>(&u[0]), mq[0]);
-                                tmem_ld32_max(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(&u[32]), mq[1]);
-                                tmem_ld32_max(t_s + 64, *reinterpret_cast<uint32_t(*)[32]>(&u[64]), mq[2]);
-                                tmem_ld32_max(t_s + 96, *reinterpret_cast<uint32_t(*)[32]>(&u[96]), mq[3]);
+                                    for (int q = 0; q < 4; ++q)
+                                        tmem_ld32_absmax(t_s + 32u * q, *reinterpret_cast<uint32_t(*)[32]>(&u[32 * q]), mq[q]);
+                                } else {
+                                    tmem_ld32_max(t_s + 0, *reinterpret_cast<uint32_t(*)[32]>(&u[0]), mq[0]);
+                                    tmem_ld32_max(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(&u[32]), mq[1]);
+                                    tmem_ld32_max(t_s + 64, *reinterpret_cast<uint32_t(*)[32]>(&u[64]), mq[2]);
+                                    tmem_ld32_max(t_s + 96, *reinterpret_cast<uint32_t(*)[32]>(&u[96]), mq[3]);
+                                }
+                                tmem_ld_wait();
+                                mrow = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
                             }
-                            tmem_ld_wait();
-                            mrow = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
-                        }
+                            return mrow;
+                        });
                         if constexpr (!C::kAliasP) {
                             tc_fence_before_sync();
                             mbar_arrive(bar(kTbSFree + wg));
@@ -1133,7 +1172,7 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                         float s[kBlockN];
 #pragma unroll
                         for (int c = 0; c < kBlockN; ++c) s[c] = __uint_as_float(u[c]);
-                        if constexpr (kWithCap || kWithBias) mrow = apply(s, mrow, k0);
+                        if constexpr (kWithCap || kWithBias) mrow = apply(s, range, k0);
                         if (k0 + kBlockN > w.prefix) mrow = tree_mask(s, k0 - w.prefix, vis);  // drafted rows, or rows past them
                         if (SHARED && r >= rows) mrow = -INFINITY;  // not a row: no reason to rescale
                         const bool rescale = __any_sync(0xffffffffu, row.grow(mrow, sl2)) && j > j0;
@@ -1202,13 +1241,16 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                         if (warp_live) {
                             uint32_t u[KS];
                             float mrow;
-                            if constexpr (kWithCap) tmem_ld64_absmax(t_s + KS * h, u, mrow);
-                            else tmem_ld64_max(t_s + KS * h, u, mrow);
-                            tmem_ld_wait();
+                            const int range = load_scores(t_s + KS * h, k0 + KS * h, KS, [&]() -> float {
+                                if constexpr (kWithCap) tmem_ld64_absmax(t_s + KS * h, u, mrow);
+                                else tmem_ld64_max(t_s + KS * h, u, mrow);
+                                tmem_ld_wait();
+                                return mrow;
+                            });
                             float s[KS];
 #pragma unroll
                             for (int c = 0; c < KS; ++c) s[c] = __uint_as_float(u[c]);
-                            if constexpr (kWithCap || kWithBias) mrow = apply(s, mrow, k0 + KS * h);
+                            if constexpr (kWithCap || kWithBias) mrow = apply(s, range, k0 + KS * h);
                             const int shift = k0 + KS * h - w.prefix;
                             if (shift > -KS) mrow = tree_mask(s, shift, vis);  // drafted rows, or rows past them
                             if (SHARED && r >= rows) mrow = -INFINITY;  // not a row: no reason to rescale
