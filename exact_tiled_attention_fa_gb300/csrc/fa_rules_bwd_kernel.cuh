@@ -584,13 +584,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) fa_rules_bwd_kernel(const __gr
                 if (!ok) break;
                 tc_fence_after_sync();
                 uint32_t u[64];
-                int range = 0;
+                float mx[2];  // under a cap the largest absolute scores of both halves
                 if constexpr (kWithCap) {
-                    float mx[2];
                     tmem_ld32_absmax(t_s, *reinterpret_cast<uint32_t(*)[32]>(&u[0]), mx[0]);
                     tmem_ld32_absmax(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(&u[32]), mx[1]);
                     tmem_ld_wait();
-                    range = cap_range(rp.rules, fmaxf(mx[0], mx[1]));
                 } else {
                     tmem_ld32(t_s, *reinterpret_cast<uint32_t(*)[32]>(&u[0]));
                     tmem_ld32(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(&u[32]));
@@ -606,6 +604,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1) fa_rules_bwd_kernel(const __gr
                 // d = 128 840 -> 885 us.)
                 const int q0 = i0 + 64 * h;  // this thread's first query
                 const bool hides = !__all_sync(0xffffffffu, qa <= q0 && qe >= q0 + 64);
+                int range = 0;
+                if constexpr (kWithCap) {
+                    float t[64];
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) t[c] = __uint_as_float(u[c]);
+                    const float m = fmaxf(mx[0], mx[1]);
+                    range = hides ? cap_range_cut<64>(rp.rules, t, m, qa - q0, qe - q0) : cap_range(rp.rules, m);
+                }
                 if (!kWithCap && hides) {
 #pragma unroll
                     for (int w = 0; w < 2; ++w) {

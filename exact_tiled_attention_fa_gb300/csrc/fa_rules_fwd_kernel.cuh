@@ -571,7 +571,8 @@ __global__ void __launch_bounds__(CORR ? 512 : kFwdThreads, 1) fa_rules_fwd_kern
                 auto test_pv = [&] {
                     if (!C::kAliasP && j > a) pv_ready = mbar_test(bar(kBarPVDone + wg), (tiles - 1) & 1);
                 };
-                const int range = kWithCap ? cap_range(p.rules, mrow) : 0;
+                int range = 0;
+                if constexpr (kWithCap) range = mask ? cap_range_cut<kBlockN>(p.rules, s, mrow, lo - k0, hi - k0) : cap_range(p.rules, mrow);
                 bool done = false;
                 if (kWithCap && !kWithBias && range == 3 && !mask) {
                     // tanh rises with its argument: the largest raw score is the largest capped one

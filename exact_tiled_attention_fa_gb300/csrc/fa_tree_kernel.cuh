@@ -607,17 +607,21 @@ __device__ __forceinline__ void tree_scale(uint32_t (&o)[N], float alpha)
     }
 }
 
-// The first n (a multiple of 8) scores in tensor memory, which are the warp's own until it says that it has them, become
-// their tanh, each by its own size.
-__device__ __forceinline__ void tree_settle(const ScoreRules& rules, uint32_t t_s, int n)
+// Columns from `first` (a multiple of 8) to n - 1 of the scores in tensor memory, which are the warp's own until it says
+// that it has them: with CAP their tanh, each by its own size, otherwise 0 from `shown` on.
+template <bool CAP>
+__device__ __forceinline__ void tree_settle(const ScoreRules& rules, uint32_t t_s, int first, int n, int shown)
 {
 #pragma unroll 1
-    for (int c = 0; c < n; c += 8) {
+    for (int c = first; c < n; c += 8) {
         uint32_t x[8];
         tmem_ld8(t_s + static_cast<uint32_t>(c), x);
         tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = __float_as_uint(tanh_each(__uint_as_float(x[e]), rules.cap_in));
+        for (int e = 0; e < 8; ++e) {
+            if constexpr (CAP) x[e] = __float_as_uint(tanh_each(__uint_as_float(x[e]), rules.cap_in));
+            else x[e] = c + e < shown ? x[e] : 0u;
+        }
         tmem_st8(t_s + static_cast<uint32_t>(c), x);
     }
     tmem_st_wait();
@@ -1088,10 +1092,14 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             };
             // Loads n scores of keys from `first` on by load(), which returns the largest absolute one, and returns the range of
             // their cap (rows that are not there take no part in it).
+            // Rows behind the unit's keys may hold anything: where the polynomials do not do for the last tile as it stands, their
+            // scores are set to 0 first.
             // Above kFarCap the exponential form is taken score by score, in tensor memory, where it is a loop: unrolled beside
             // the others it costs instruction fetches (64 sequences behind 32K tokens 97 -> 106 us).
             auto load_scores = [&](uint32_t t, int first, int n, auto load) -> int {
                 if constexpr (kWithCap) {
+                    const int shown = max(w.prefix - first, 0);
+                    bool hidden = false;
                     bool settled = false;
 #pragma unroll 1
                     while (true) {
@@ -1099,9 +1107,14 @@ __global__ void __launch_bounds__(kTrThreads, 1)
                         if (settled) return kSettled;
                         const int range = cap_range(p.rules, mx, r < rows);
                         if (range >= 2) return range;
+                        if (!hidden && shown < n) {
+                            tree_settle<false>(p.rules, t, shown & ~7, n, shown);
+                            hidden = true;
+                            continue;
+                        }
                         if (range == 1 && !kWithBias) return range;
                         if (!p.rules.far) return 0;
-                        tree_settle(p.rules, t, n);
+                        tree_settle<true>(p.rules, t, 0, n, n);
                         settled = true;
                     }
                 }

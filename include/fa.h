@@ -518,9 +518,9 @@ fa_status fa_cache_compact(void* k_cache, void* v_cache, const int* seqlens, con
  * The cap's tanh is off by up to 1.2e-6 of its value; with a cap of up to 128 it may instead be off by 2e-7, so that a score
  * is off by 2e-7 caps (1e-5 at a cap of 50).
  *
- * A non-finite score of a hidden pair reaches nothing; a non-finite q, v or grad_o, or k in the gradient, may
- * reach every row whose 128-row tile meets its own (its weight there is 0, and 0 times NaN is NaN), so rows of
- * padding must be finite too.
+ * A non-finite score of a hidden pair reaches nothing; a finite one of up to 10 caps may decide in which form a cap is taken,
+ * within the errors above.  A non-finite q, v or grad_o, or k in the gradient, may reach every row whose 128-row tile
+ * meets its own (its weight there is 0, and 0 times NaN is NaN), so rows of padding must be finite too.
  */
 
 /* Bytes of workspace fa_fwd_rules needs with documents, 0 on invalid arguments.  Without documents it needs none. */

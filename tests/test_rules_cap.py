@@ -1,4 +1,5 @@
-"""A capped score is its own matter: its accuracy goes by its own size, not by scores beyond the cap that its tile holds too.
+"""A capped score is its own matter: its accuracy goes by its own size, not by scores beyond the cap that its tile holds too,
+and what hidden keys and rows hold does not reach it in any bit.
 
 Bounds.  A cap of 1e5 and more leaves scores up to 30 as they are to within s^3 / (3 cap^2) < 1e-6, so the references
 have none, and with them no error that is counted in caps.  The kernels' tanh is off by 1.2e-6 of its value, which the
@@ -46,6 +47,7 @@ def run(q, k, v, do, rules):
     return o, lse, grads
 
 
+# ------------------------------------------------------------------------------------ accuracy
 @pytest.mark.parametrize("d", [32, 64, 128])
 @pytest.mark.parametrize("cap", [1e5, 1e7, 1e30])
 @pytest.mark.parametrize("bias", [False, True])
@@ -110,3 +112,67 @@ def test_decode_beside_scores_far_beyond_the_cap(d, cap, B, R, bias):
     ref = decode_reference(q[~far], kp[:, 1:], vp[:, 1:], k[~far], v[~far], lens[~far], P - 1, Rules(slopes=sl))
     near = ~far.to(DEV)
     check_forward(o[near], lse[near], ref, f"d={d} cap={cap} B={B}")
+
+
+# ------------------------------------------------------------------------------------ what is hidden
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("cap", [50.0, 1e5, 1e7])
+@pytest.mark.parametrize("bias", [False, True])
+def test_hidden_keys_do_not_choose_the_form_of_the_cap(d, cap, bias):
+    """Whatever keys of another document and keys behind a causal position hold, other rows' results are bit by bit those
+    with zeros there.  (The borders are between 32 rows: a row that sees such a key may share its own form of the cap with
+    the rows beside it.)"""
+    q, k, v, _ = inputs(2, 2, 1, 330, 330, d, seed=4)
+    ids = torch.zeros((2, 330), dtype=torch.int32)
+    ids[:, 160:] = 1
+    sl = slopes(2) if bias else None
+    cases = [(Rules(causal=c, softcap=cap, slopes=sl, documents=ids), slice(0, 160), slice(160, 330)) for c in (False, True)]
+    cases.append((Rules(causal=True, softcap=cap, slopes=sl), slice(288, 330), slice(0, 288)))
+    for rules, keys, rows in cases:
+        got = []
+        for x in (0.0, math.inf, -math.inf, math.nan, 1e38, -1e38):
+            kk = k.clone()
+            kk[:, :, keys] = x
+            o, lse = fa().fwd_rules(q.to(DEV), kk.to(DEV), v.to(DEV), out_dtype=F32, **rules.kwargs(DEV))
+            got.append((x, o[:, :, rows], lse[:, :, rows]))
+        for x, o, lse in got[1:]:
+            assert torch.equal(o, got[0][1]) and torch.equal(lse, got[0][2]), (x, rules.causal, rules.docs is not None)
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("cap", [50.0, 1e5, 1e7])
+@pytest.mark.parametrize("bias", [False, True])
+def test_hidden_queries_do_not_choose_the_form_of_the_cap(d, cap, bias):
+    """The gradients of a document do not depend on the queries of another one in the same tile.  (One key tile: a query's
+    gradient is then one term, and no order of sums plays in.)"""
+    q, k, v, do = inputs(2, 2, 1, 128, 128, d, seed=5)
+    ids = torch.zeros((2, 128), dtype=torch.int32)
+    ids[:, 64:] = 1
+    rules = Rules(softcap=cap, slopes=slopes(2) if bias else None, documents=ids)
+    got = []
+    for x in (0.0, 2.0 ** 100):
+        qq = q.clone()
+        qq[:, :, :64] = (qq[:, :, :64].float().sign() * x).to(BF16)
+        o, lse, grads = run(qq, k, v, do, rules)
+        got.append([t[:, :, 64:] for t in (o, lse, *grads)])
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("cap", [50.0, 1e5, 1e7])
+@pytest.mark.parametrize("B,R,bias", [(3, 4, False), (3, 4, True), (70, 3, False), (70, 3, True)])
+def test_rows_behind_the_lengths_do_not_choose_the_form_of_the_cap(d, cap, B, R, bias):
+    """Decode: whatever rows behind the prefix and behind the sequences' own keys hold, the result is bit by bit the same."""
+    Hq, Hkv, P, P_max, Nk = 2 * R, 2, 333, 400, 200
+    lens = ((torch.arange(B, dtype=torch.int32) * 29) % (Nk + 1)).to(torch.int32)
+    sl = slopes(Hq).to(DEV) if bias else None
+    first = None
+    for x in (0.0, math.inf, -math.inf, math.nan, 1e38):
+        t = [a.to(DEV) for a in decode_inputs(B, Hq, Hkv, P_max, Nk, d, lens, P=P, seed=6, fill=x)]
+        n, plen = lens.to(DEV), torch.tensor([P], dtype=torch.int32, device=DEV)
+        o, lse = fa().decode_prefix(*t, n, prefix_len=plen, softcap=cap, slopes=sl, out_dtype=F32)
+        assert bool(torch.isfinite(o).all())
+        first = first or (o, lse)
+        assert torch.equal(o, first[0]) and torch.equal(lse, first[1]), x
+    assert fa().get_device_error() == 0
