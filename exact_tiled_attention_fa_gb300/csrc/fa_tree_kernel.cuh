@@ -389,13 +389,15 @@ __device__ __forceinline__ TreeStart shared_locate(const PrefixParams& p, int c,
 // same batch stays at 49 us, and smaller ones pay 2 % for it.)
 template <bool TURNS>
 struct SharedWalk : TreeWalk {
-    int rot;          // the tile the unit begins with
-    float of_shares;  // shares a place
+    int rot;            // the tile the unit begins with
+    int total, shares;  // places, and shares of them
+    // (In whole numbers: the walks of K and of V and all shares of a unit have to come to the same tile.)
     __device__ __forceinline__ void turn(const PrefixParams& p)
     {
         if constexpr (!TURNS) return;
-        const float x = static_cast<float>(qp * (tiles + p.unit_cost)) * of_shares;  // shares that the unit begins later
-        rot = min(__float2int_rz(__fdividef(x - floorf(x), of_shares)), tiles - 1);
+        // places that the unit begins later, times shares, past whole shares (below 2^30 times at most kTreeMaxShares)
+        const long long later = static_cast<long long>(qp * (tiles + p.unit_cost)) * shares % total;
+        rot = min(static_cast<int>(static_cast<unsigned>(later) / static_cast<unsigned>(shares)), tiles - 1);
     }
     __device__ __forceinline__ int first_key(int i, int keys) const
     {
@@ -408,7 +410,8 @@ struct SharedWalk : TreeWalk {
         b = kvh = qp = tile = tiles = n = 0;
         len = TreeLen{0, 0};
         next_len = rot = 0;
-        of_shares = __fdividef(static_cast<float>(s.shares), static_cast<float>(s.total));
+        total = static_cast<int>(s.total);
+        shares = static_cast<int>(s.shares);
         if (left == 0) return;
         b = s.b;
         kvh = b < 0 ? s.unit / p.n_qp : s.unit;
