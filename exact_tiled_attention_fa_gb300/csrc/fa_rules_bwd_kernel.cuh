@@ -610,7 +610,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) fa_rules_bwd_kernel(const __gr
 #pragma unroll
                     for (int c = 0; c < 64; ++c) t[c] = __uint_as_float(u[c]);
                     const float m = fmaxf(mx[0], mx[1]);
-                    range = hides ? cap_range_cut<64>(rp.rules, t, m, qa - q0, qe - q0) : cap_range(rp.rules, m);
+                    range = cap_range(rp.rules, m);
+                    if (range == 0 && hides) range = cap_range_seen<64>(rp.rules, t, m, qa - q0, qe - q0);
                 }
                 if (!kWithCap && hides) {
 #pragma unroll

@@ -103,17 +103,16 @@ __device__ __forceinline__ uint32_t low_bits(int n)
     return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
 }
 
-// The same for a tile that is cut, where mx has hidden columns in it, outside [lo, hi).  What they hold does not count if a
-// score lies beyond kNoScore caps, where tanh is 1 and none has a reason to be, or a lane has nothing but NaN: the choice is
-// then the one with zeros there.  (Short of that they may choose another polynomial, 1.2e-6 of a score.  Without them in
+// The range of a tile that is cut and that with its hidden columns, outside [lo, hi), is none's.  What they hold does not
+// count if a score lies beyond kNoScore caps, where tanh is 1 and none has a reason to be, or a lane has nothing but NaN:
+// the range is then the one with zeros there.  (Short of that they may choose another form, within its error.  Without them in
 // every case where the near range does not do: 64 sequences of 1024 tokens in documents of 200, 16 heads of 64, scores of
 // deviation 3 under a cap of 30, 213 -> 270 us.)
 constexpr float kNoScore = 10.f;
 template <int N>
-__device__ __forceinline__ int cap_range_cut(const ScoreRules& r, const float* s, float mx, int lo, int hi)
+__device__ __forceinline__ int cap_range_seen(const ScoreRules& r, const float* s, float mx, int lo, int hi)
 {
-    const int range = cap_range(r, mx);
-    if (range != 0 || __all_sync(0xffffffffu, mx * r.cap_in <= kNoScore)) return range;
+    if (__all_sync(0xffffffffu, mx * r.cap_in <= kNoScore)) return 0;
     float m = 0.f;
 #pragma unroll
     for (int q = 0; q < N / 32; ++q) {

@@ -571,8 +571,7 @@ __global__ void __launch_bounds__(CORR ? 512 : kFwdThreads, 1) fa_rules_fwd_kern
                 auto test_pv = [&] {
                     if (!C::kAliasP && j > a) pv_ready = mbar_test(bar(kBarPVDone + wg), (tiles - 1) & 1);
                 };
-                int range = 0;
-                if constexpr (kWithCap) range = mask ? cap_range_cut<kBlockN>(p.rules, s, mrow, lo - k0, hi - k0) : cap_range(p.rules, mrow);
+                int range = kWithCap ? cap_range(p.rules, mrow) : 0;
                 bool done = false;
                 if (kWithCap && !kWithBias && range == 3 && !mask) {
                     // tanh rises with its argument: the largest raw score is the largest capped one
@@ -589,6 +588,7 @@ __global__ void __launch_bounds__(CORR ? 512 : kFwdThreads, 1) fa_rules_fwd_kern
                     behind = __all_sync(0xffffffffu, k0 >= qpos);
                 }
                 if (!done) {
+                    if (kWithCap && range == 0 && mask) range = cap_range_seen<kBlockN>(p.rules, s, mrow, lo - k0, hi - k0);
                     if constexpr (kWithBias) {
                         biased_scores<kBlockN, kWithCap>(s, p.rules, range, p.rules.far, slope, static_cast<float>(qpos - k0), before ? 1 : behind ? -1 : 0);
                     } else if constexpr (kWithCap) {
