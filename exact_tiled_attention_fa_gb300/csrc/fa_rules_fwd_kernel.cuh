@@ -571,7 +571,21 @@ __global__ void __launch_bounds__(CORR ? 512 : kFwdThreads, 1) fa_rules_fwd_kern
                 auto test_pv = [&] {
                     if (!C::kAliasP && j > a) pv_ready = mbar_test(bar(kBarPVDone + wg), (tiles - 1) & 1);
                 };
-                int range = kWithCap ? cap_range(p.rules, mrow) : 0;
+                int range = 0;
+                // What hidden scores hold is looked at here, the range asked for on both sides, or, for a cap alone at d = 128, under
+                // the scores that are not in the near range.  (Whichever spills less: d = 128 64 x 1024 tokens cap and bias 746
+                // and 810 us, 4 x 4097 cap 368 and 360; d = 64 64 x 1024 in documents, cap 30 220 and 225.)
+                constexpr bool kCutHere = kWithBias || D < 128;
+                if constexpr (kWithCap && kCutHere) {
+                    if (mask) {
+                        range = cap_range(p.rules, mrow);
+                        if (range == 0) range = cap_range_seen<kBlockN>(p.rules, s, mrow, lo - k0, hi - k0);
+                    } else {
+                        range = cap_range(p.rules, mrow);
+                    }
+                } else if constexpr (kWithCap) {
+                    range = cap_range(p.rules, mrow);
+                }
                 bool done = false;
                 if (kWithCap && !kWithBias && range == 3 && !mask) {
                     // tanh rises with its argument: the largest raw score is the largest capped one
@@ -588,7 +602,7 @@ __global__ void __launch_bounds__(CORR ? 512 : kFwdThreads, 1) fa_rules_fwd_kern
                     behind = __all_sync(0xffffffffu, k0 >= qpos);
                 }
                 if (!done) {
-                    if (kWithCap && range == 0 && mask) range = cap_range_seen<kBlockN>(p.rules, s, mrow, lo - k0, hi - k0);
+                    if (kWithCap && !kCutHere && range == 0 && mask) range = cap_range_seen<kBlockN>(p.rules, s, mrow, lo - k0, hi - k0);
                     if constexpr (kWithBias) {
                         biased_scores<kBlockN, kWithCap>(s, p.rules, range, p.rules.far, slope, static_cast<float>(qpos - k0), before ? 1 : behind ? -1 : 0);
                     } else if constexpr (kWithCap) {
