@@ -4,8 +4,10 @@
 //   lse = log sum_s exp(lse_s),  o = sum_s exp(lse_s - lse) o_s
 // over all of them ("flash_lab.py", section 4).  A warp a row.  The time is that of three loads one behind the other
 // (the units' records, the log-sum-exps, the outputs) and of the launch; up to FEW results are loaded beside their
-// log-sum-exps.  More of them take registers, which counts where there are many rows: 16 sequences behind 8192 tokens
-// with 13 parts a row 31.5 us at 8 or 12, 28.2 at 16; 64 behind 32K with 10 parts 102, 100 and 103; 256 97.7, 99.9 and 104.
+// log-sum-exps.  More of them take registers, which counts where there are many rows.  Whole calls at FEW = 8, 12 and 16, us,
+// 32/8 heads of 128: 16 sequences behind 8192 tokens, 13 parts a row 32.2, 32.1 and 28.6; 64 behind 32K, 10 parts 89.9, 87.1 and
+// 89.7; 256 behind 8192 86.5, 88.5 and 92.  By rows, as the lengths are known on the device alone; few rows that also have
+// few parts would do with 8: 2 behind 512 11.6, 11.8 and 13.0, 37 behind 3001, 15/5 heads of 64, 19.3, 20.3 and 21.3.
 #include <cuda_bf16.h>
 
 #include <type_traits>

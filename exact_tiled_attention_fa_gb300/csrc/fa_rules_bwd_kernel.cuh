@@ -26,7 +26,10 @@
 // successor's first P (last products, dK and dV on their way out).  d = 128: 5180 a step, 2900 of them products; P and dS
 // take 1800, but dQ lies in dP's columns: dP 870, dS 880, dK 650, dQ 710, its reductions 1390 (64 KB at 64 bytes a cycle
 // to the L2), the next dP 580 later.  4 sequences of 4097 tokens, 16 heads, causal, none / bias / cap of 50 / both: d = 64
-// 412 / 456 / 493 / 609 us, d = 128 789 / 821 / 837 / 960.
+// 410 / 454 / 519 / 639 us, d = 128 788 / 820 / 834 / 954.  Capped so for scores of deviation 3; deviation 10, beyond the middle
+// range (the wide polynomial is not used here): d = 64 660, both rules 751, d = 128 935 and 1048.
+// Bytes stored and loaded that spill: d = 128 48/48 (no rules), 56/52 (bias, cap), 32/32 - 52/68 (both); d <= 64 up to 8/32 with a
+// cap, 36/44 with both rules.
 #pragma once
 
 #include "fa_bwd_kernel.cuh"
@@ -668,7 +671,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) fa_rules_bwd_kernel(const __gr
                     tc_fence_before_sync();
                     mbar_arrive(bar(kBbDPFree));
                 }
-                // dS' = scale dS = pf o (dP scale - scale D)
+                // dS' = scale dS = pf o (dP scale - scale D), rounded to bf16 for the products with K and Q (half a step, 2^-8 of
+                // each, as P for dV: one type for both operands of a tensor-core product)
                 const uint32_t d_addr = sbase + C::kOffDsc + s * 512 + h * 256;
 #pragma unroll
                 for (int c = 0; c < 64; c += 4) {

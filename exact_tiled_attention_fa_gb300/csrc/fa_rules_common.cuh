@@ -25,18 +25,20 @@ __device__ __forceinline__ float rcp_approx(float x)
     return y;
 }
 
-// The cap.  tanh(u) for |u| <= kWideRange, where the scores that a cap is meant for almost always are, is u P(u^2) with
-// P the minimax polynomial for tanh(u) / u (Remez exchange on u^2): degree n = 2 up to kNearRange (relative error
-// 1.2e-6), 3 up to kMidRange (1.1e-6), 5 up to kWideRange (5.9e-7).  With cap_in and mult in its coefficients a capped
-// score is S Q(S^2): n + 1 operations and the one that takes the maximum off it anyway.  (What bounds them is the FMA
-// units, 128 lanes an SM, whether two operations go in one instruction or not.  Causal prefill of 4 sequences of 4097
-// tokens, 16 heads of 128, a cap of 50 that leaves most tiles in the near range: a polynomial of degree 5 for every
-// argument, scaled before it, 487 us, the three 348, without a cap 286.)
+// The cap.  tanh(u) for |u| <= kWideRange is u P(u^2) with P the minimax polynomial for tanh(u) / u (Remez exchange on
+// u^2): degree n = 2 up to kNearRange (relative error 1.2e-6), 3 up to kMidRange (1.1e-6), 5 up to kWideRange (5.9e-7).  With
+// cap_in and mult in its coefficients a capped score is S Q(S^2): n + 1 operations and the one that takes the maximum
+// off it anyway.  (What bounds them is the FMA units, 128 lanes an SM, whether two operations go in one instruction or not.
+// Causal prefill of 4 sequences of 4097 tokens, 16 heads of 128, a cap of 50 that leaves most tiles in the near range: a
+// polynomial of degree 5 for every argument, scaled before it, 487 us, the three 348 when they were chosen, 360 with what
+// cap_range_seen adds, without a cap 286.)
 // Other arguments take 1 - 2 / (1 + e^2u): two operations of the special function unit that the exponentials also need
-// (586 us for all tiles); its absolute error of 2e-7 is one of 1e-5 of a weight at a cap of 50.  A warp takes one form for all
-// of a tile's scores, and a score beyond the cap is no reason for one far below it to be off by 2e-7 caps, 0.01 of a
-// score of 5 at a cap of 1e5: above kFarCap, where that error is a hundredth of a weight's rounding to bf16, scores up to
-// kNearRange take their polynomial beside it too.  (For every cap that costs 1.0 - 1.4 times the time of the tiles it is for.)
+// (586 us for all tiles one by one, 562 by pairs).  The form goes by the largest of a warp's scores in a tile, 32 x 128 of
+// them (backward 32 x 64), so one score near the cap is dear: scores of deviation 10 at the same shape 456 us.
+// The exponential form's absolute error of 2e-7 is one of 1e-5 of a weight at a cap of 50.  And a score beyond the cap is no
+// reason for one far below it to be off by 2e-7 caps, 0.01 of a score of 5 at a cap of 1e5: above kFarCap, where that error
+// is a hundredth of a weight's rounding to bf16, scores up to kNearRange take their polynomial beside it too.  (For every cap
+// that costs 1.0 - 1.4 times the time of the tiles it is for.)
 // +-infinity gives +-1, NaN NaN.  (The device's own tanh instruction is off by 2^-11 of its result: at a score of 20
 // by 0.01, and the weight by as much.)
 constexpr float kNearRange = 0.3f, kMidRange = 0.55f, kWideRange = 1.f;

@@ -24,9 +24,11 @@
 //  - A correction warpgroup (kRulesCorr).
 //
 // What bounds it: the softmax's chain between two products, as in fa_fwd_kernel.cuh, lengthened by the FMA units' work on
-// the rules: at the shape above d = 64 153 us, with a bias 200, a cap of 50 216, both 301; d = 128 286, 315, 348, 391.
-// In documents (64 sequences of 1024 tokens, 16 heads of 64) 144 us: 3.7 TB/s of the 541 MB that have to move;
-// by the counters tensor cores 21 % busy, the ALUs (masks by bits, packing) 37 %, issue slots 42 %.
+// the rules: at the shape above d = 64 152 us, with a bias 199, a cap of 50 220, both 296; d = 128 285, 314, 360, 393.  The
+// capped times are those of scores of deviation 3, nearly all in the cheapest range; deviation 10 / 30: d = 64 331 / 398, both
+// rules 410; d = 128 456 / 562, both 528.  In documents (64 sequences of 1024 tokens, 16 heads of 64) 144 us: 3.7 TB/s of the
+// 541 MB that have to move; by the counters tensor cores 22 % busy, the ALUs (masks by bits, packing) 47 %, issue slots 49 %.
+// Bytes stored and loaded that spill: cap d = 32 80/136, d = 128 84/104; bias d = 32 24/56, d = 64 12/32; both d <= 64 20/44.
 #pragma once
 
 #include "fa_fwd_kernel.cuh"
@@ -46,9 +48,10 @@ struct RulesItem {
 enum : int { kBarItemFull = kBarCount, kBarItemEmpty = kBarItemFull + kRulesItems, kRulesBarCount = kBarItemEmpty + kRulesItems };
 
 // Whether calls without a causal mask take a kernel with a correction warpgroup (16 warps).  us, d = 128, without / with it:
-// 64 sequences of 1024 tokens, 16 heads 571 / 465, biased 639 / 551, both rules 787 / 740; 4 of 4097, 32/8 heads 1080 /
-// 1021; 16 of 1024 in documents of 100 - 300 94.5 / 88.2.  With a cap alone its softmax warps spill: 638 / 612, but in
-// documents 132 / 139.  With a causal mask (4 x 4097, 16 heads) 286 / 288, capped 348 / 365.  At d = 64, where the softmax
+// 64 sequences of 1024 tokens, 16 heads 571 / 465, biased 639 / 551, both rules 787 / 747; 4 of 4097, 32/8 heads 1080 /
+// 1021; 16 of 1024 in documents of 100 - 300 94.5 / 88.2.  With a cap alone its softmax warps spill: 632 / 634, scores of
+// deviation 10 under a cap of 50 903 / 864, but in documents 138 / 141, 16384 tokens 802 / 818.  With a causal mask (4 x 4097,
+// 16 heads) 286 / 288, capped (before hidden scores were looked at) 348 / 365.  At d = 64, where the softmax
 // warps need the registers, 64 x 1024 took 279 against 278, in documents, causal 155 (with O read whole and released
 // at once 164) against 144.
 template <int D, int RULES>

@@ -40,7 +40,7 @@
 //
 // What bounds it, and what it takes with the merge (16 sequences of 1 - 32K tokens, 32/8 heads, d = 128):
 // with 16 nodes K and V, 168-173 us, 6.5 TB/s; with 64 nodes the softmax's chain between two products (scores
-// out of tensor memory, exponentials, weights back, two barriers), 258 us, 1100 TFLOP/s in a short series and
+// out of tensor memory, exponentials, weights back, two barriers), 259 - 263 us, 1080 TFLOP/s in a short series and
 // 275 us, 1030 TFLOP/s in a long one at the power limit's clock, tensor cores 47 % busy.  One sequence of 2000
 // tokens, 8 nodes: 12.1 us, latency: two launches, lengths, the first tiles, one tile's softmax, its rows out
 // and in again.  Many short caches (256 sequences of 150 - 300 tokens, 4 nodes) 73 us, half the copy's rate: a
@@ -127,7 +127,8 @@ struct TrCfg {
     // Registers after the split: 256 * softmax + 128 * control = 64512 = 384 * 168, checked by the launcher.
     // A softmax thread holds the scores of a step.  (With 224 and 56 at d = 128 the producers and issuers
     // spilled more: 256 sequences of 300 tokens 77.7 us, with 216 and 72 they take 72.9.  Bytes stored and
-    // loaded that still spill: d = 128 ALT 136/164, SOLO 56/72, PAIR 24/128; d <= 64 ALT 60/80, others none.)
+    // loaded that still spill: d = 128 ALT 136/160, SOLO 56/68, PAIR 24/128; d <= 64 ALT 60/76, others none.  Behind a shared
+    // prefix: d = 128 12/24; d <= 64 ALT 64/124 - 112/168 by the kind of rules, SOLO 12/268 without a cap, up to 20/48 with one.)
     static constexpr int kSoftmaxRegs = kSteps == 2 ? 192 : D == 128 ? 216 : 208;
     static constexpr int kControlRegs = kSteps == 2 ? 120 : D == 128 ? 72 : 88;
     static constexpr int kCB = D < 64 ? D : 64;
@@ -1097,8 +1098,8 @@ __global__ void __launch_bounds__(kTrThreads, 1)
             // their cap (rows that are not there take no part in it).
             // Rows behind the unit's keys may hold anything: where the polynomials do not do for the last tile as it stands, their
             // scores are set to 0 first.
-            // Above kFarCap the exponential form is taken score by score, in tensor memory, where it is a loop: unrolled beside
-            // the others it costs instruction fetches (64 sequences behind 32K tokens 97 -> 106 us).
+            // Above kFarCap the exponential form is taken score by score, in tensor memory, where it is a loop: unrolled beside the
+            // other forms and this one it costs instruction fetches (64 sequences behind 32K tokens 97 -> 107 us).
             auto load_scores = [&](uint32_t t, int first, int n, auto load) -> int {
                 if constexpr (kWithCap) {
                     const int shown = max(w.prefix - first, 0);
