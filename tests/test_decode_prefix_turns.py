@@ -54,7 +54,7 @@ def check(B, R, Hkv, P, P_max, Nk, seed):
 def test_every_tile_of_a_prefix_once(R):
     """Groups that fill a query tile and such that leave some of it, 2 to 10 query tiles, prefixes that end at a tile's end
     and beside it, from units a few tiles long to such of several shares."""
-    rng = random.Random(R)
+    rng = random.Random(500 + R)
     seqs = 128 // R
     for i in range(120):
         n_qp = rng.randint(2, 10)
